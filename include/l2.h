@@ -332,6 +332,131 @@ int l2_sample(const float *logits, int B, int vocab_size, float temperature, flo
               unsigned long long *rng_state, int *tokens_out, void *cuda_stream);
 
 /*
+ * Paged KV cache: pages of rows that sequences take as they grow and share
+ * after a fork, and the decode attention over them.  The pages this library
+ * follows keep one contiguous cache per sequence and have no counterpart.
+ *
+ * A pool keeps K (after RoPE) and V rows of head_size elements at
+ *   k + layer * layer_stride + page * page_stride + kv_head * head_stride + row * row_stride
+ * (v alike; strides in elements, multiples of 16 bytes, last dimension
+ * contiguous).  Position p of sequence s is row p % page_size of page
+ * table[s][p / page_size].  refs[page] counts the sequences that hold a page;
+ * 0 is free.  Full pages may be shared; a partly filled last page belongs to
+ * one sequence.  All arrays are DEVICE memory of the caller, 16-byte aligned
+ * k and v.  A new pool has refs, lens, status and scratch zero; table entries
+ * at or past ceil(lens[s] / page_size) are never read and may hold anything.
+ *
+ * Every call takes a stream (NULL: the legacy default stream), enqueues its
+ * kernels and returns; nothing is allocated or kept, so calls can be captured
+ * into graphs.  Calls that change a pool must be ordered by their streams,
+ * with each other and with calls that read it; attention calls with workspaces
+ * of their own may run at once.  Arguments the host can see are checked there
+ * (L2_EINVAL, l2_last_error(NULL) says what; nothing enqueued).  What only the
+ * device sees (indices, lengths, free pages) is checked by the kernels: a call
+ * that cannot be done whole changes nothing and sets bits of *status, which
+ * stay until the caller clears them: L2_PAGES_BAD_PAGE a table entry outside
+ * the pool (in an attention call its rows count as zero rows), L2_PAGES_BAD_CALL
+ * bad index arrays or inconsistent bookkeeping, L2_PAGES_FULL too few free pages.
+ */
+#define L2_F32 0
+#define L2_BF16 1
+#define L2_F16 2
+#define L2_PAGES_BAD_PAGE 2
+#define L2_PAGES_BAD_CALL 4
+#define L2_PAGES_FULL 8
+
+typedef struct {
+    void *k, *v;
+    int *refs;     /* [n_pages] */
+    int *lens;     /* [n_seqs] rows held */
+    int *table;    /* [n_seqs][max_pages] */
+    int *status;   /* one int */
+    int *scratch;  /* l2_pages_scratch_ints(n_pages) ints, used by calls that change the pool */
+    long long layer_stride, page_stride, head_stride, row_stride;
+    int dtype;     /* L2_F32, L2_BF16, L2_F16 */
+    int n_layers, n_pages, n_kv_heads, page_size;
+    int head_size; /* a multiple of 16 bytes, at most 128 elements */
+    int n_seqs, max_pages;
+} L2Pages;
+
+/* Ints a pool's scratch holds. */
+long long l2_pages_scratch_ints(int n_pages);
+
+/* New rows: rows starts[i] .. starts[i + 1] - 1 (row i, without starts) go to sequence seqs[i]. */
+typedef struct {
+    int n;               /* sequences, 1..1024, each named once */
+    int rows;            /* all rows; n without starts */
+    const int *seqs;     /* DEVICE [n] */
+    const int *starts;   /* DEVICE [n + 1], 0 .. rows, or NULL: one row each */
+    int layer;           /* -1: every layer */
+    int extend;          /* 1: first lengthen the sequences by their rows */
+    const void *k, *v;   /* DEVICE [layers][rows][kv heads][head_size], strides in elements */
+    long long layer_stride, row_stride, head_stride;
+} L2PagesRows;
+
+/*
+ * Appends rows of K and V.  With extend, each sequence first grows by its
+ * rows and takes the pages that needs, the lowest free ones in the order of
+ * the call; the rows are then written as the sequences' last ones.  A step
+ * extends with its first layer (or all layers at once) and writes its other
+ * layers with extend 0 and the same seqs and starts.  If the last extension
+ * was refused, rows are not written until one succeeds.
+ */
+int l2_pages_append(const L2Pages *pool, const L2PagesRows *rows, void *cuda_stream);
+
+/*
+ * Forks: for i < n (1..1024) the empty sequence dst[i] becomes a copy of the
+ * first rows[i] rows of src[i] (all its rows with rows NULL).  Whole pages
+ * are shared (refs rises); a last part of a page is copied into a new one, the
+ * lowest free in the order of the call, in every layer.  dst are distinct and
+ * none of src.
+ */
+int l2_pages_fork(const L2Pages *pool, int n, const int *src, const int *dst, const int *rows, void *cuda_stream);
+
+/*
+ * Frees the pages of n (0..1024) sequences and empties them (one named twice
+ * is freed once).  With compact the pool is then closed up: with L pages
+ * held, the k-th free page below L takes the rows of the k-th held page at or
+ * above L in every layer, and the tables follow.
+ */
+int l2_pages_free(const L2Pages *pool, int n, const int *seqs, int compact, void *cuda_stream);
+
+/*
+ * Attention of one query row per sequence over all its cached rows: for row b,
+ * sequence s = seqs[b] and query head h with KV head g(h) = floor(h * n_kv_heads
+ * / n_heads): out[b][h] = sum_t softmax_t(scale * q[b][h] . K[t][g(h)]) V[t][g(h)],
+ * t = 0 .. lens[s] - 1 (zeros when the sequence is empty).
+ * Rows come in G groups (group g: rows group_starts[g] .. group_starts[g + 1] - 1,
+ * all rows covered).  The first prefix_lens[g] positions of a group (at most
+ * its shortest member's length) are taken from its first row's sequence and
+ * read once for the whole group: the caller names groups whose sequences begin
+ * with the same rows, as forks do.  G = 0: no sharing.  q, out and the cache
+ * have the pool's type; scores, softmax and sums are fp32.
+ */
+typedef struct {
+    int layer;
+    int B;                   /* rows, 1..1024 */
+    int G;                   /* groups, 0..B */
+    int n_heads;             /* query heads, n_kv_heads..1024 */
+    const void *q;           /* DEVICE [B][n_heads][head_size], strides in elements */
+    void *out;               /* DEVICE, alike */
+    float *lse;              /* DEVICE [B][n_heads], or NULL: log of the sum of exp(scores), -inf without rows */
+    const int *seqs;         /* DEVICE [B], or NULL: sequence b */
+    const int *group_starts; /* DEVICE [G + 1] */
+    const int *prefix_lens;  /* DEVICE [G] */
+    long long q_row_stride, q_head_stride, out_row_stride, out_head_stride;
+    double scale;            /* usually 1 / sqrt(head_size) */
+} L2PagesAttention;
+
+/* Bytes of workspace an attention call of these sizes needs, or a negative status. */
+long long l2_pages_attention_ws(const L2Pages *pool, int B, int G, int n_heads);
+
+/* workspace: DEVICE memory of at least l2_pages_attention_ws bytes, 256-byte aligned, contents
+ * of no matter, not used by another call at the same time. */
+int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *args, void *workspace, long long workspace_bytes,
+                       void *cuda_stream);
+
+/*
  * Fault injection for tests: makes the n-th device allocation from now on
  * (n >= 1) fail as if out of memory; 0 disables.  Process-wide.
  */

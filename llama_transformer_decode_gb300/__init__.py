@@ -13,6 +13,7 @@ import numpy as np
 
 from . import _native
 from ._native import EXPORTS, WEIGHT_FIELDS, L2Config, L2Weights, build  # noqa: F401
+from .pages import PagePool  # noqa: F401
 
 L2_OK, L2_EINVAL, L2_ESTATE, L2_ENOMEM, L2_ECUDA, L2_EDEVICE, L2_ETIMEOUT = 0, -1, -2, -3, -4, -5, -6
 L2_FLAG_DEBUG, L2_FLAG_NO_GRAPH, L2_FLAG_NO_PDL, L2_FLAG_PERSIST, L2_FLAG_NO_TC = 0x1, 0x2, 0x4, 0x8, 0x10

@@ -16,8 +16,8 @@ LIB = os.path.join(BUILD, "libl2decode.so")
 BUILD_CHECKED = os.path.join(BUILD, "checked")
 LIB_CHECKED = os.path.join(BUILD, "libl2decode_checked.so")
 SOURCES = ("gemv.cu", "gemv_batched.cu", "gemv_tc.cu", "attention.cu", "attn_prefill.cu", "step_kernel.cu", "step_cta.cu",
-           "sample.cu", "l2_api.cu")
-HEADERS = ("l2_device.cuh", "l2_params.h", "l2_kernels.h")
+           "sample.cu", "pages.cu", "attn_pages.cu", "pages_api.cu", "l2_api.cu")
+HEADERS = ("l2_device.cuh", "l2_params.h", "l2_kernels.h", "l2_pages.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3"]
 
@@ -86,12 +86,33 @@ class L2Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in WEIGHT_FIELDS]
 
 
+class L2Pages(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "refs", "lens", "table", "status", "scratch")]
+                + [(n, ctypes.c_longlong) for n in ("layer_stride", "page_stride", "head_stride", "row_stride")]
+                + [(n, ctypes.c_int) for n in ("dtype", "n_layers", "n_pages", "n_kv_heads", "page_size", "head_size",
+                                               "n_seqs", "max_pages")])
+
+
+class L2PagesRows(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("rows", ctypes.c_int), ("seqs", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("layer", ctypes.c_int), ("extend", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("layer_stride", ctypes.c_longlong), ("row_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class L2PagesAttention(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("layer", "B", "G", "n_heads")]
+                + [(n, ctypes.c_void_p) for n in ("q", "out", "lse", "seqs", "group_starts", "prefix_lens")]
+                + [(n, ctypes.c_longlong) for n in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride")]
+                + [("scale", ctypes.c_double)])
+
+
 EXPORTS = ("l2_create", "l2_reset", "l2_forward", "l2_forward_batch", "l2_forward_host", "l2_logits",
            "l2_position", "l2_debug_attention", "l2_kv_export", "l2_kv_import", "l2_sync",
            "l2_last_error", "l2_destroy", "l2_launch_op", "l2_kernels_per_step",
            "l2_step_input_bytes", "l2_forward_static", "l2_debug_fail_alloc_at", "l2_sample",
            "l2_forward_dev_tokens", "l2_prefill", "l2_debug_fail_graph_at", "l2_debug_wait_timeout",
-           "l2_debug_bounds_checked", "l2_debug_limit_cache", "l2_launch_op_batch")
+           "l2_debug_bounds_checked", "l2_debug_limit_cache", "l2_launch_op_batch", "l2_pages_scratch_ints",
+           "l2_pages_append", "l2_pages_fork", "l2_pages_free", "l2_pages_attention_ws", "l2_pages_attention")
 
 _lib = None
 
@@ -138,6 +159,17 @@ def declare(lib):
     lib.l2_debug_bounds_checked.restype = i
     lib.l2_debug_limit_cache.argtypes = [vp, ctypes.c_ulonglong]
     lib.l2_debug_limit_cache.restype = i
+    pp = ctypes.POINTER(L2Pages)
+    lib.l2_pages_scratch_ints.argtypes = [i]
+    lib.l2_pages_scratch_ints.restype = ctypes.c_longlong
+    lib.l2_pages_append.argtypes = [pp, ctypes.POINTER(L2PagesRows), vp]
+    lib.l2_pages_fork.argtypes = [pp, i, vp, vp, vp, vp]
+    lib.l2_pages_free.argtypes = [pp, i, vp, i, vp]
+    lib.l2_pages_attention_ws.argtypes = [pp, i, i, i]
+    lib.l2_pages_attention_ws.restype = ctypes.c_longlong
+    lib.l2_pages_attention.argtypes = [pp, ctypes.POINTER(L2PagesAttention), vp, ctypes.c_longlong, vp]
+    for name in ("l2_pages_append", "l2_pages_fork", "l2_pages_free", "l2_pages_attention"):
+        getattr(lib, name).restype = i
     for name in ("l2_create", "l2_reset", "l2_forward", "l2_forward_batch", "l2_forward_host",
                  "l2_position", "l2_debug_attention", "l2_kv_export", "l2_kv_import", "l2_sync",
                  "l2_launch_op", "l2_launch_op_batch", "l2_kernels_per_step", "l2_forward_static"):

@@ -1,0 +1,790 @@
+// Decode attention of a batch over a paged cache whose sequences share prefixes.
+//
+// What it computes.  For row b (the newest token of sequence s_b, lens[s_b] = n rows cached),
+// query head h and its KV head g(h) = floor(h * n_kv_heads / n_heads):
+//     x_t = scale * q_bh . K[t, g(h)],  o_bh = sum_t softmax(x)_t V[t, g(h)],  t = 0 .. n - 1.
+// The batch comes in groups; the first P_g positions of a group (the group's prefix length, at
+// most the shortest member's length) are read through its first sequence's table, once for all
+// its rows, and the rest through each sequence's own.
+//
+// How.  A softmax over keys splits over any partition of them: each part keeps (m, l, acc) = (max
+// of x, sum of 2^(x - m), sum of 2^(x - m) V) in base 2, and parts merge by rescaling to the common max.
+// "Sources" are the groups' prefixes and then the sequences' own rows; a source has items, one
+// per KV head and tile of 16 (row, head) pairs, and an item's keys are cut into tiles.  All tiles,
+// numbered source by source, are split evenly over the warps of the grid; a warp walks its range
+// and writes one part per item it meets (item number + warp number is a distinct slot, because
+// each step from part to part raises one of the two).  A second kernel merges each row's
+// parts in key order, so results do not depend on timing.
+//
+// What bounds it.  16 rows against a tile give 16 products per word read, so the reading of K and V bounds
+// the kernel until a prefix serves many tiles of rows.  Each warp keeps its own ring of tiles
+// (cp.async, 16-byte words, rows gathered by the page table one by one, so pages may end anywhere
+// in a tile) and needs no block-wide barrier.  Rows are the M of mma.sync m16n8: the tensor pipe
+// has ample room at this ratio, and a warp works alone.
+// fp32 caches: products as hi*hi + hi*lo + lo*hi of tf32 halves (about 2^-21 relative), each tile's
+// sum added to the running one in fp32; 16-bit caches: q, K, V as stored, and the weights
+// 2^(x - m) as a sum of two 16-bit values, so nothing is rounded but the fp32 sums and the output.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "../../include/l2.h"
+#include "l2_device.cuh"
+#include "l2_pages.h"
+
+namespace l2 {
+
+namespace {
+
+constexpr int kWarps = 8;      // warps of a block, one block per SM
+constexpr int kStages = 3;     // tiles of a warp's ring
+constexpr int kM = 16;         // (row, head) pairs of an item
+// Fewest tiles a warp takes: below that the parts cost more to write and merge than the
+// parallel reading gains.
+constexpr int kMinTiles = 4;
+
+// Plan, in the workspace: header, then per source (S = G + B, at most 2 kPagesMaxCall)
+// the first tile, first item, tiles per item, first key, end key, first row, rows.
+enum { kHdrTiles = 0, kHdrItems = 1, kHdrWarps = 2, kHdrOk = 3, kHdrInts = 16 };
+struct Plan {
+    int *hdr, *t0, *i0, *kt, *key0, *key1, *row0, *rows;
+};
+__host__ __device__ inline Plan plan_of(int *base, int S) {
+    Plan p;
+    p.hdr = base;
+    p.t0 = base + kHdrInts;
+    p.i0 = p.t0 + S + 1;
+    p.kt = p.i0 + S + 1;
+    p.key0 = p.kt + S;
+    p.key1 = p.key0 + S;
+    p.row0 = p.key1 + S;
+    p.rows = p.row0 + S;
+    return p;
+}
+__host__ __device__ inline size_t plan_ints(int S) { return (kHdrInts + 2 * (size_t)(S + 1) + 5 * (size_t)S + 63) / 64 * 64; }
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// Most query heads of a KV head; head j of KV head g is first_head(g) + j.
+__host__ __device__ __forceinline__ int heads_per_kv(int H, int KV) { return (H + KV - 1) / KV; }
+__device__ __forceinline__ int first_head(int g, int H, int KV) { return (g * H + KV - 1) / KV; }
+
+// Tiles are cut evenly: warp w takes tiles [first_of(w), first_of(w + 1)).
+__device__ __forceinline__ int first_of(int w, int T, int W) { return (int)((long long)w * T / W); }
+__device__ __forceinline__ int warp_of(int tile, int T, int W) { return (int)((((long long)tile + 1) * W + T - 1) / T - 1); }
+
+}  // namespace
+
+// One block: lengths of the sources and the numbering of their tiles and items.
+__global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p, int tile_keys, int max_warps) {
+    __shared__ int part[2][32], minlen[kPagesMaxCall], gstart[kPagesMaxCall + 1], len_s[kPagesMaxCall];
+    const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+    const int S = p.G + p.B;
+    const Plan pl = plan_of(p.plan, S);
+    const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
+    pdl_launch_dependents();
+    bool bad = false;
+    int len = 0;
+    if (i < p.B) {
+        const int s = p.seqs ? p.seqs[i] : i;
+        bad = s < 0 || s >= p.n_seqs;
+        if (!bad) len = p.lens[s];
+        bad |= len < 0 || len > (long long)p.max_pages * p.page_size;
+    }
+    len_s[i] = len;
+    if (i <= p.G) {
+        const int a = p.G ? p.group_starts[i] : 0;
+        bad |= p.G && ((i == 0 && a != 0) || (i == p.G && a != p.B) || a < 0 || a > p.B);
+        gstart[i] = a;
+    }
+    if (i == 0 && p.G == kPagesMaxCall) {  // one entry more than threads
+        gstart[p.G] = p.group_starts[p.G];
+        bad |= gstart[p.G] != p.B;
+    }
+    __syncthreads();
+    int P = 0, r0 = 0, rows = 0;
+    if (i < p.G) {
+        r0 = gstart[i];
+        rows = gstart[i + 1] - r0;
+        P = p.prefix_lens[i];
+        bad |= rows < 0 || P < 0;
+    }
+    if (__syncthreads_or(bad)) {
+        if (i == 0) {
+            atomicOr(p.err, L2_PAGES_ERR_ARGS);
+            pl.hdr[kHdrTiles] = pl.hdr[kHdrItems] = 0;
+            pl.hdr[kHdrWarps] = 1;
+            pl.hdr[kHdrOk] = 0;
+        }
+        return;
+    }
+    // a row alone has nothing to share: all its keys are its own
+    if (i < p.G) minlen[i] = rows < 2 ? 0 : P;
+    __syncthreads();
+    if (p.G && i < p.B) {
+        int lo = 0, hi = p.G;  // the group of the row: the last that starts at or before it
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            gstart[m] <= i ? lo = m : hi = m;
+        }
+        atomicMin(&minlen[lo], len);
+    }
+    __syncthreads();
+    // sources in blocks of 1024: G prefixes, then B sequences
+    int tiles_before = 0, items_before = 0;
+    for (int s0 = 0; s0 < S; s0 += 1024) {
+        const int s = s0 + i;
+        int key0 = 0, key1 = 0, row0 = 0, n = 0;
+        if (s < p.G) {
+            key1 = minlen[s];
+            row0 = gstart[s];
+            n = gstart[s + 1] - row0;
+        } else if (s < S) {
+            row0 = s - p.G;
+            n = 1;
+            key1 = len_s[row0];
+            int lo = 0, hi = p.G;
+            while (hi - lo > 1) {
+                const int m = (lo + hi) >> 1;
+                gstart[m] <= row0 ? lo = m : hi = m;
+            }
+            key0 = p.G ? minlen[lo] : 0;
+        }
+        const int kt = s < S ? cdiv(key1 - key0, tile_keys) : 0;
+        const int items = kt > 0 ? cdiv(n * gq, kM) * p.n_kv_heads : 0;
+        int a = items * kt, b = items;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+            if (lane >= o) {
+                a += x;
+                b += y;
+            }
+        }
+        if (lane == 31) {
+            part[0][warp] = a;
+            part[1][warp] = b;
+        }
+        __syncthreads();
+        int ta = 0, tb = 0, wa = 0, wb = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w == warp) {
+                wa = ta;
+                wb = tb;
+            }
+            ta += part[0][w];
+            tb += part[1][w];
+        }
+        if (s < S) {
+            pl.t0[s] = tiles_before + wa + a - items * kt;
+            pl.i0[s] = items_before + wb + b - items;
+            pl.kt[s] = kt;
+            pl.key0[s] = key0;
+            pl.key1[s] = key1;
+            pl.row0[s] = row0;
+            pl.rows[s] = n;
+        }
+        tiles_before += ta;
+        items_before += tb;
+        __syncthreads();
+    }
+    if (i == 0) {
+        pl.t0[S] = tiles_before;
+        pl.i0[S] = items_before;
+        pl.hdr[kHdrTiles] = tiles_before;
+        pl.hdr[kHdrItems] = items_before;
+        pl.hdr[kHdrWarps] = max(1, min(max_warps, cdiv(tiles_before, kMinTiles)));
+        pl.hdr[kHdrOk] = 1;
+    }
+}
+
+namespace {
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
+    const int n = on ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+
+struct TBf16 {
+    static constexpr int kBytes = 2;
+    static __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ uint32_t pack(float x, float y) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t v) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v)); }
+};
+struct TF16 {
+    static constexpr int kBytes = 2;
+    static __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static __device__ __forceinline__ uint32_t pack(float x, float y) {
+        const __half2 v = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+};
+struct TF32 {
+    static constexpr int kBytes = 4;
+};
+
+__device__ __forceinline__ void mma_tf32_16x8x8(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo in tf32, to 2^-22 of x
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+
+// Tile shape: HS the head size padded to 32 (fp32 only), 64 or 128; keys per tile such that K and V of
+// one take 8 KB at most.
+template <typename T, int HS>
+struct Shape {
+    static constexpr int KT = T::kBytes == 4 ? (HS == 128 ? 8 : HS == 64 ? 16 : 32) : (HS == 128 ? 16 : 32);
+    static constexpr int C = HS * T::kBytes / 16;             // 16-byte words a row
+    static constexpr int kRow = HS * T::kBytes;
+    static constexpr int kStage = 2 * KT * kRow;              // K then V
+    static constexpr int kSmem = kWarps * kStages * kStage;
+};
+// Word c of row r sits at word c ^ swz(r): the eight rows (16-bit) or the two rows and four words
+// (fp32) that one shared-memory phase reads fall into different banks.
+template <typename T>
+__device__ __forceinline__ int swz(int r) {
+    return T::kBytes == 4 ? ((r & 1) << 2) | ((r >> 1) & 3) : r & 7;
+}
+
+}  // namespace
+
+// The warps' walk (see the head of the file).
+template <typename T, int HS>
+__global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesAttn p) {
+    using Sh = Shape<T, HS>;
+    constexpr int KT = Sh::KT, C = Sh::C, NT = KT / 8;  // NT: n8 tiles of keys
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
+    const int wid = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * (kStages * Sh::kStage);
+    const int S = p.G + p.B;
+    const Plan pl = plan_of(p.plan, S);
+    const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
+    pdl_launch_dependents();
+    pdl_wait();
+    const int T_all = pl.hdr[kHdrTiles], W = pl.hdr[kHdrWarps];
+    if (wid >= W) return;
+    int tile = first_of(wid, T_all, W);
+    const int tile_end = first_of(wid + 1, T_all, W);
+    if (tile >= tile_end) return;
+    // the source of the first tile: the last with t0 <= tile (32-way search)
+    int src = 0;
+    for (int lo = 0, hi = S + 1; hi - lo > 1;) {  // t0[lo] <= tile < t0[hi]
+        const int step = cdiv(hi - lo, 32);
+        const int at = lo + lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, at < hi && pl.t0[min(at, S)] <= tile);
+        lo += (31 - __clz(m)) * step;
+        hi = min(hi, lo + step);
+        src = lo;
+    }
+    const int words = p.head_size * T::kBytes / 16;  // 16-byte words of a row that exist
+
+    while (tile < tile_end) {
+        const int kt = pl.kt[src];
+        if (kt == 0 || tile >= pl.t0[src + 1]) {  // an empty source, or past this one
+            ++src;
+            continue;
+        }
+        const int local = tile - pl.t0[src], item = local / kt, k_first = local - item * kt;
+        const int k_end = min(kt, k_first + (tile_end - tile));
+        const int rows = pl.rows[src], row0 = pl.row0[src], key0 = pl.key0[src], key1 = pl.key1[src];
+        const int tiles_m = cdiv(rows * gq, kM), kvh = item / tiles_m, m0 = (item - kvh * tiles_m) * kM;
+        const int head0 = first_head(kvh, p.n_heads, p.n_kv_heads);
+        const int nh = first_head(kvh + 1, p.n_heads, p.n_kv_heads) - head0;
+        const int sq = p.seqs ? p.seqs[row0] : row0;
+        const int *table = p.table + (size_t)sq * p.max_pages;
+        const char *kb = p.k + kvh * p.head_stride, *vb = p.v + kvh * p.head_stride;
+
+        // place of this lane's key of a tile (lane < KT), -1 past the end
+        auto place = [&](int ktile) -> long long {
+            const int key = key0 + ktile * KT + lane;
+            if (lane >= KT || key >= key1) return -1;
+            const int pg = key / p.page_size, page = table[pg];
+            if (page < 0 || page >= p.n_pages) {
+                atomicOr(p.err, L2_DEV_ERR_BOUNDS);
+                return -1;
+            }
+            return page * p.page_stride + (key - pg * p.page_size) * p.row_stride;
+        };
+        auto fetch = [&](int stage, long long off) {
+            const uint32_t ks = ring + stage * Sh::kStage, vs = ks + KT * Sh::kRow;
+            constexpr int RP = C >= 32 ? 1 : 32 / C;  // rows one instruction covers
+            const int c = lane % C, rr = C >= 32 ? 0 : lane / C;
+#pragma unroll
+            for (int r0 = 0; r0 < KT; r0 += RP) {
+                const int r = r0 + rr;
+                const long long o = __shfl_sync(0xffffffffu, off, r);
+                const bool on = o >= 0 && c < words;
+                const uint32_t d = r * Sh::kRow + ((c ^ swz<T>(r)) << 4);
+                const long long so = on ? o + (c << 4) : 0;
+                cp_async16(ks + d, kb + so, on);
+                cp_async16(vs + d, vb + so, on);
+            }
+            cp_commit();
+        };
+
+        // queries of the item: pair m = (row r, head j), m = r * gq + j
+        auto q_ptr = [&](int m) -> const char * {
+            const int r = m / gq, j = m - r * gq;
+            return r < rows && j < nh ? p.q + (row0 + r) * p.q_row + (head0 + j) * p.q_head : nullptr;
+        };
+        long long off = place(k_first);
+        int n_tiles = k_end - k_first;
+        // fill the ring
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            if (s < n_tiles) {
+                const long long nx = s + 1 < n_tiles ? place(k_first + s + 1) : -1;
+                fetch(s, off);
+                off = nx;
+            } else {
+                cp_commit();
+            }
+        }
+
+        const char *qa = q_ptr(m0 + g4), *qb = q_ptr(m0 + g4 + 8);
+        float m_run[2] = {-CUDART_INF_F, -CUDART_INF_F}, l_run[2] = {0.f, 0.f};
+        float o[HS / 8][4];
+#pragma unroll
+        for (int i = 0; i < HS / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        // 16-bit: the A fragments of all K steps; fp32: the lane's query values
+        constexpr int QR = T::kBytes == 2 ? HS / 16 * 4 : HS / 2;
+        uint32_t qf[QR];
+        if constexpr (T::kBytes == 2) {
+#pragma unroll
+            for (int ks = 0; ks < HS / 16; ++ks) {
+                const int d0 = ks * 16 + 2 * t4, d1 = d0 + 8;
+                qf[4 * ks] = qa && d0 < p.head_size ? *reinterpret_cast<const uint32_t *>(qa + 2 * d0) : 0u;
+                qf[4 * ks + 1] = qb && d0 < p.head_size ? *reinterpret_cast<const uint32_t *>(qb + 2 * d0) : 0u;
+                qf[4 * ks + 2] = qa && d1 < p.head_size ? *reinterpret_cast<const uint32_t *>(qa + 2 * d1) : 0u;
+                qf[4 * ks + 3] = qb && d1 < p.head_size ? *reinterpret_cast<const uint32_t *>(qb + 2 * d1) : 0u;
+            }
+        } else {
+            // steps 2i, 2i + 1 of 8 take dimensions 16 i + 4 t4 + {0, 1} and {2, 3}: one 16-byte read
+#pragma unroll
+            for (int i = 0; i < HS / 16; ++i) {
+                const int d = 16 * i + 4 * t4;
+                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 a = qa && d < p.head_size ? *reinterpret_cast<const float4 *>(qa + 4 * d) : z;
+                const float4 b = qb && d < p.head_size ? *reinterpret_cast<const float4 *>(qb + 4 * d) : z;
+                qf[8 * i] = __float_as_uint(a.x);
+                qf[8 * i + 1] = __float_as_uint(b.x);
+                qf[8 * i + 2] = __float_as_uint(a.y);
+                qf[8 * i + 3] = __float_as_uint(b.y);
+                qf[8 * i + 4] = __float_as_uint(a.z);
+                qf[8 * i + 5] = __float_as_uint(b.z);
+                qf[8 * i + 6] = __float_as_uint(a.w);
+                qf[8 * i + 7] = __float_as_uint(b.w);
+            }
+        }
+
+#pragma unroll 1
+        for (int it = 0; it < n_tiles; ++it) {
+            cp_wait<kStages - 2>();
+            __syncwarp();
+            // the next tile goes into the stage read one step ago
+            if (it + kStages - 1 < n_tiles) {
+                const long long nx = it + kStages < n_tiles ? place(k_first + it + kStages) : -1;
+                fetch((it + kStages - 1) % kStages, off);
+                off = nx;
+            } else {
+                cp_commit();
+            }
+            const uint32_t ks_base = ring + (it % kStages) * Sh::kStage, vs_base = ks_base + KT * Sh::kRow;
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+            if constexpr (T::kBytes == 2) {
+                // lane's ldmatrix row: key (lane & 7) of the n8 tile, word 2 kpair + lane / 8
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int key = 8 * n + (lane & 7);
+#pragma unroll
+                    for (int c = 0; c < C; c += 4) {
+                        uint32_t b[4];
+                        ldsm4(ks_base + key * Sh::kRow + (((c + (lane >> 3)) ^ swz<T>(key)) << 4), b);
+                        T::mma(s[n], qf + 2 * c, b[0], b[1]);
+                        T::mma(s[n], qf + 2 * c + 4, b[2], b[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < HS / 16; ++i) {
+                    uint32_t qh[8], ql[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) split_tf32(__uint_as_float(qf[8 * i + j]), qh[j], ql[j]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int key = 8 * n + g4;
+                        uint32_t x[4], h[4], l[4];
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                     : "r"(ks_base + key * Sh::kRow + (((4 * i + t4) ^ swz<T>(key)) << 4)));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) split_tf32(__uint_as_float(x[j]), h[j], l[j]);
+#pragma unroll
+                        for (int st = 0; st < 2; ++st) {
+                            mma_tf32_16x8x8(s[n], ql + 4 * st, h[2 * st], h[2 * st + 1]);
+                            mma_tf32_16x8x8(s[n], qh + 4 * st, l[2 * st], l[2 * st + 1]);
+                            mma_tf32_16x8x8(s[n], qh + 4 * st, h[2 * st], h[2 * st + 1]);
+                        }
+                    }
+                }
+            }
+            // scale, mask keys past the end, running max
+            const int left = key1 - key0 - (k_first + it) * KT;
+            float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int key = 8 * n + 2 * t4 + (j & 1);
+                    s[n][j] = key < left ? s[n][j] * p.scale_log2 : -CUDART_INF_F;
+                    mx[j >> 1] = fmaxf(mx[j >> 1], s[n][j]);
+                }
+            float corr[2], base[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                const float mn = fmaxf(m_run[r], mx[r]);
+                base[r] = mn == -CUDART_INF_F ? 0.f : mn;  // only -inf so far: weights 0, not NaN
+                corr[r] = exp2f(m_run[r] - base[r]);
+                m_run[r] = mn;
+            }
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[n][j] = exp2f(s[n][j] - base[j >> 1]);
+                    sum[j >> 1] += s[n][j];
+                }
+            l_run[0] = l_run[0] * corr[0] + sum[0];
+            l_run[1] = l_run[1] * corr[1] + sum[1];
+            if constexpr (T::kBytes == 2) {
+#pragma unroll
+                for (int i = 0; i < HS / 8; ++i) {
+                    o[i][0] *= corr[0];
+                    o[i][1] *= corr[0];
+                    o[i][2] *= corr[1];
+                    o[i][3] *= corr[1];
+                }
+#pragma unroll
+                for (int kk = 0; kk < KT / 16; ++kk) {
+                    // weights as A fragments: hi and what it leaves
+                    uint32_t ph[4], plo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = s[2 * kk + (j >> 1)][2 * (j & 1)], y = s[2 * kk + (j >> 1)][2 * (j & 1) + 1];
+                        ph[j] = T::pack(x, y);
+                        const float2 back = T::unpack(ph[j]);
+                        plo[j] = T::pack(x - back.x, y - back.y);
+                    }
+                    const int key = 16 * kk + (lane & 15);
+#pragma unroll
+                    for (int c = 0; c < C; c += 2) {
+                        uint32_t b[4];
+                        ldsm4t(vs_base + key * Sh::kRow + (((c + (lane >> 4)) ^ swz<T>(key)) << 4), b);
+                        T::mma(o[c], ph, b[0], b[1]);
+                        T::mma(o[c], plo, b[0], b[1]);
+                        T::mma(o[c + 1], ph, b[2], b[3]);
+                        T::mma(o[c + 1], plo, b[2], b[3]);
+                    }
+                }
+            } else {
+                // n8 tile 4 i + j holds dimensions 32 i + 4 c(g4) + j, c(g) = the word that keeps a phase's
+                // eight reads in different banks
+                const int cg = ((g4 & 1) << 2) | (g4 >> 1);
+                uint32_t ph[NT][4], plo[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    split_tf32(s[n][0], ph[n][0], plo[n][0]);
+                    split_tf32(s[n][2], ph[n][1], plo[n][1]);
+                    split_tf32(s[n][1], ph[n][2], plo[n][2]);
+                    split_tf32(s[n][3], ph[n][3], plo[n][3]);
+                }
+#pragma unroll
+                for (int i = 0; i < HS / 32; ++i) {
+                    float acc[4][4] = {};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        uint32_t x[2][4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = 8 * n + 2 * t4 + e;
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(x[e][0]), "=r"(x[e][1]), "=r"(x[e][2]), "=r"(x[e][3])
+                                         : "r"(vs_base + key * Sh::kRow + (((8 * i + cg) ^ swz<T>(key)) << 4)));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t h0, l0, h1, l1;
+                            split_tf32(__uint_as_float(x[0][j]), h0, l0);
+                            split_tf32(__uint_as_float(x[1][j]), h1, l1);
+                            mma_tf32_16x8x8(acc[j], plo[n], h0, h1);
+                            mma_tf32_16x8x8(acc[j], ph[n], l0, l1);
+                            mma_tf32_16x8x8(acc[j], ph[n], h0, h1);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        o[4 * i + j][0] = fmaf(o[4 * i + j][0], corr[0], acc[j][0]);
+                        o[4 * i + j][1] = fmaf(o[4 * i + j][1], corr[0], acc[j][1]);
+                        o[4 * i + j][2] = fmaf(o[4 * i + j][2], corr[1], acc[j][2]);
+                        o[4 * i + j][3] = fmaf(o[4 * i + j][3], corr[1], acc[j][3]);
+                    }
+                }
+            }
+            __syncwarp();  // the stage is read before the next fetch into it
+        }
+        cp_wait<0>();
+        __syncwarp();
+        // the part: (m, l) and the sums of the item's pairs
+        const int slot = pl.i0[src] + item + wid;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float l = l_run[r];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int mi = g4 + 8 * r;
+            if (!(r ? qb : qa) || slot >= p.max_parts) continue;
+            if (t4 == 0) reinterpret_cast<float2 *>(p.ws_ml)[(size_t)slot * kM + mi] = make_float2(m_run[r], l);
+            float *dst = p.ws_acc + ((size_t)slot * kM + mi) * p.head_size;
+            if constexpr (T::kBytes == 2) {
+#pragma unroll
+                for (int i = 0; i < HS / 8; ++i) {
+                    const int d = 8 * i + 2 * t4;
+                    if (d < p.head_size) *reinterpret_cast<float2 *>(dst + d) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                }
+            } else {
+                // columns 2 t4, 2 t4 + 1 of n8 tile 4 i + j are dimensions 32 i + 4 c(2 t4 + e) + j
+#pragma unroll
+                for (int i = 0; i < HS / 32; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int gg = 2 * t4 + e, d = 32 * i + 4 * (((gg & 1) << 2) | (gg >> 1));
+                        if (d < p.head_size)
+                            *reinterpret_cast<float4 *>(dst + d) =
+                                make_float4(o[4 * i][2 * r + e], o[4 * i + 1][2 * r + e], o[4 * i + 2][2 * r + e], o[4 * i + 3][2 * r + e]);
+                    }
+            }
+        }
+        tile += n_tiles;
+    }
+}
+
+namespace {
+constexpr int kMergeThreads = 128;
+
+template <typename T>
+__device__ __forceinline__ void store_out(char *o, int d, float4 v);
+template <>
+__device__ __forceinline__ void store_out<TF32>(char *o, int d, float4 v) {
+    *reinterpret_cast<float4 *>(o + 4 * d) = v;
+}
+template <>
+__device__ __forceinline__ void store_out<TBf16>(char *o, int d, float4 v) {
+    *reinterpret_cast<uint2 *>(o + 2 * d) = make_uint2(TBf16::pack(v.x, v.y), TBf16::pack(v.z, v.w));
+}
+template <>
+__device__ __forceinline__ void store_out<TF16>(char *o, int d, float4 v) {
+    *reinterpret_cast<uint2 *>(o + 2 * d) = make_uint2(TF16::pack(v.x, v.y), TF16::pack(v.z, v.w));
+}
+}  // namespace
+
+// One block per (row, query head): its prefix's parts, then its own, merged in key order by four warps
+// (part i goes to warp i % 4) and then over the warps in order.
+template <typename T>
+__global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const PagesAttn p) {
+    __shared__ float sm[4], sl[4];
+    __shared__ float4 sa[4][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.x / p.n_heads, h = blockIdx.x - b * p.n_heads;
+    const int S = p.G + p.B;
+    const Plan pl = plan_of(p.plan, S);
+    const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
+    const int kvh = (int)((long long)h * p.n_kv_heads / p.n_heads), j = h - first_head(kvh, p.n_heads, p.n_kv_heads);
+    const int d = 4 * lane;
+    const bool on = d < p.head_size;
+    pdl_wait();
+    if (!pl.hdr[kHdrOk]) return;
+    const int T_all = pl.hdr[kHdrTiles], W = pl.hdr[kHdrWarps];
+    int grp = -1;
+    if (p.G) {
+        int lo = 0, hi = p.G;
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            p.group_starts[m] <= b ? lo = m : hi = m;
+        }
+        grp = lo;
+    }
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool any = false;
+    int seen = 0;
+    for (int which = 0; which < 2; ++which) {
+        const int s = which ? p.G + b : grp;
+        if (s < 0) continue;
+        const int kt = pl.kt[s];
+        if (kt == 0) continue;
+        any = true;
+        const int mi = (b - pl.row0[s]) * gq + j, tiles_m = cdiv(pl.rows[s] * gq, kM);
+        const int item = kvh * tiles_m + mi / kM;
+        const int u0 = pl.t0[s] + item * kt;
+        const int w0 = warp_of(u0, T_all, W), w1 = warp_of(u0 + kt - 1, T_all, W);
+        const int slot0 = pl.i0[s] + item;
+        for (int w = w0 + ((warp - seen) & 3); w <= w1; w += 4) {
+            const size_t at = (size_t)(slot0 + w) * kM + (mi % kM);
+            const float2 ml = reinterpret_cast<const float2 *>(p.ws_ml)[at];
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on) v = *reinterpret_cast<const float4 *>(p.ws_acc + at * p.head_size + d);
+            const float mn = fmaxf(m, ml.x), base = mn == -CUDART_INF_F ? 0.f : mn;
+            const float c0 = exp2f(m - base), c1 = exp2f(ml.x - base);
+            a.x = a.x * c0 + v.x * c1;
+            a.y = a.y * c0 + v.y * c1;
+            a.z = a.z * c0 + v.z * c1;
+            a.w = a.w * c0 + v.w * c1;
+            l = l * c0 + ml.y * c1;
+            m = mn;
+        }
+        seen = (seen + (w1 - w0 + 1)) & 3;
+    }
+    if (lane == 0) {
+        sm[warp] = m;
+        sl[warp] = l;
+    }
+    sa[warp][lane] = a;
+    __syncthreads();
+    if (warp) return;
+    for (int w = 1; w < 4; ++w) {
+        const float mn = fmaxf(m, sm[w]), base = mn == -CUDART_INF_F ? 0.f : mn;
+        const float c0 = exp2f(m - base), c1 = exp2f(sm[w] - base);
+        const float4 v = sa[w][lane];
+        a.x = a.x * c0 + v.x * c1;
+        a.y = a.y * c0 + v.y * c1;
+        a.z = a.z * c0 + v.z * c1;
+        a.w = a.w * c0 + v.w * c1;
+        l = l * c0 + sl[w] * c1;
+        m = mn;
+    }
+    // no keys at all: zeros, and a sum of nothing; all scores -inf: 0 / 0, as the formula has it
+    const float inv = any ? 1.0f / l : 0.f;
+    if (on)
+        store_out<T>(p.out + (long long)b * p.o_row + (long long)h * p.o_head, d,
+                     any ? make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
+    if (p.lse && lane == 0) p.lse[(size_t)b * p.n_heads + h] = any ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+}
+
+namespace {
+
+template <typename T, int HS>
+cudaError_t launch_walk(const PagesAttn &p, int grid, cudaLaunchConfig_t cfg) {
+    using Sh = Shape<T, HS>;
+    auto fn = attn_pages_kernel<T, HS>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = Sh::kSmem;
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+int tile_keys(int dtype, int hs) {
+    if (dtype == L2_F32) return hs <= 32 ? 32 : hs <= 64 ? 16 : 8;
+    return hs <= 64 ? 32 : 16;
+}
+
+int max_items(int B, int G, int n_heads, int n_kv_heads) {
+    // prefix tiles: sum over groups of ceil(rows gq / 16) <= (B gq) / 16 + G
+    const long long gq = heads_per_kv(n_heads, n_kv_heads);
+    const long long pre = G ? (B * gq) / kM + G : 0, own = B * ((gq + kM - 1) / kM);
+    return (int)((pre + own) * n_kv_heads);
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms) {
+    const size_t parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * kWarps;
+    return align256(plan_ints(B + G) * 4) + align256(parts * kM * 8) + align256(parts * kM * head_size * 4);
+}
+
+cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s) {
+    const size_t parts = (size_t)max_items(p.B, p.G, p.n_heads, p.n_kv_heads) + (size_t)num_sms * kWarps;
+    char *w = static_cast<char *>(ws);
+    p.plan = reinterpret_cast<int *>(w);
+    w += align256(plan_ints(p.B + p.G) * 4);
+    p.ws_ml = reinterpret_cast<float *>(w);
+    w += align256(parts * kM * 8);
+    p.ws_acc = reinterpret_cast<float *>(w);
+    p.max_parts = (int)parts;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(1024);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_pages_plan_kernel, p, tile_keys(p.dtype, p.head_size), num_sms * kWarps);
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 1;
+    const int hs = p.head_size;
+    if (p.dtype == L2_F32)
+        e = hs <= 32   ? launch_walk<TF32, 32>(p, num_sms, cfg)
+            : hs <= 64 ? launch_walk<TF32, 64>(p, num_sms, cfg)
+                       : launch_walk<TF32, 128>(p, num_sms, cfg);
+    else if (p.dtype == L2_BF16)
+        e = hs <= 64 ? launch_walk<TBf16, 64>(p, num_sms, cfg) : launch_walk<TBf16, 128>(p, num_sms, cfg);
+    else
+        e = hs <= 64 ? launch_walk<TF16, 64>(p, num_sms, cfg) : launch_walk<TF16, 128>(p, num_sms, cfg);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(p.B * p.n_heads);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.dynamicSmemBytes = 0;
+    if (p.dtype == L2_F32) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<TF32>, p);
+    if (p.dtype == L2_BF16) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<TBf16>, p);
+    return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<TF16>, p);
+}
+
+}  // namespace l2

@@ -1075,6 +1075,10 @@ int submit(l2_ctx *c, int B, const int *tokens, const int *pos, float *logits_ou
 
 }  // namespace
 
+namespace l2 {
+int set_call_error(int code, const char *text) { return fail(nullptr, code, "%s", text); }
+}  // namespace l2
+
 // Attention scratch of l2_forward_static: accumulators, (max, sum) pairs and
 // tickets, 512 KiB.  Every GPU that loads the library holds it until exit.  In
 // host code this name is only a stand-in: kernels get the address that

@@ -68,6 +68,9 @@ cudaError_t gemv_tc_init();
 cudaError_t launch_tc_embed(const TcParams &tp, int batch, cudaStream_t stream, bool pdl);
 cudaError_t launch_gemv_tc(int mode, const TcParams &tp, int grid, cudaStream_t stream, bool pdl);
 
+// Records `text` as the calling thread's last failure (l2_last_error(NULL)); returns code.
+int set_call_error(int code, const char *text);
+
 // Flash-decoding attention (attention.cu).
 struct AttnLaunch {
     int lp;       // lanes per cache row (power of two; a lane takes 4 / 2 / 1 of its 16-byte words

@@ -1,0 +1,72 @@
+// Paged KV cache: kernel parameter blocks and launch entry points (host side).
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "l2_params.h"
+
+namespace l2 {
+
+// Bits of a pool's status word (beside L2_DEV_ERR_BOUNDS): a call's index arrays or
+// the bookkeeping they meet are not valid; the pool has too few free pages.
+enum : int { L2_PAGES_ERR_ARGS = 4, L2_PAGES_ERR_FULL = 8 };
+
+constexpr int kPagesMaxCall = 1024;  // sequences one call names
+constexpr int kPagesThreads = 1024;  // threads of the one-block bookkeeping kernels
+
+// Integers at the head of a pool's scratch: whether the last bookkeeping kernel
+// refused its call (the row kernels that follow it then do nothing), and the pages a
+// compaction moves.  Then three lists of n_pages entries.
+enum : int { kScrRefused = 0, kScrMoved = 1, kScrLive = 2, kScrHead = 8 };
+
+// A page pool.  Rows of head_size elements; strides in bytes.  Position p of sequence s is
+// row p % page_size of page table[s * max_pages + p / page_size].
+struct PagesView {
+    char *k, *v;
+    int *refs, *lens, *table, *err, *scratch;
+    long long layer_stride, page_stride, head_stride, row_stride;  // bytes
+    int n_layers, n_pages, n_kv_heads, page_size, n_seqs, max_pages;
+    int row_bytes;  // head_size * element size, a multiple of 16
+};
+
+struct PagesAppend {
+    const char *k, *v;                                  // new rows
+    long long layer_stride, row_stride, head_stride;    // bytes
+    const int *seqs, *starts;                           // [n], [n + 1] or nullptr (one row each)
+    int n, rows, layer0, n_layers;
+};
+
+cudaError_t launch_pages_extend(const PagesView &p, int n, const int *seqs, const int *starts, int rows, cudaStream_t s);
+cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, bool pdl, cudaStream_t s);
+cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s);
+cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, cudaStream_t s);
+
+// Attention of one query row per sequence over its pages (attn_pages.cu).
+struct PagesAttn {
+    const char *k, *v;        // this layer's pages
+    const int *lens, *table;
+    int *err;
+    long long page_stride, head_stride, row_stride;     // bytes
+    const char *q;
+    char *out;
+    float *lse;               // [B][n_heads] natural-log sums, or nullptr
+    long long q_row, q_head, o_row, o_head;             // bytes
+    const int *seqs;          // [B] or nullptr (sequence b)
+    const int *group_starts;  // [G + 1] or nullptr
+    const int *prefix_lens;   // [G]
+    int B, G, n_heads, n_kv_heads, head_size, page_size, max_pages, n_seqs, n_pages;
+    int dtype;
+    float scale_log2;         // scale * log2(e)
+    // workspace
+    int *plan;
+    float *ws_ml, *ws_acc;
+    int max_parts;            // pieces the workspace holds
+};
+
+size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms);
+// Lays `p`'s workspace out in ws and launches the kernels.
+cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s);
+
+}  // namespace l2

@@ -1,0 +1,429 @@
+"""The paged cache on the GPU: bookkeeping and row movement equal to the plain
+statement of tests/pages_ref.py, and attention against 64 bits.
+
+Tolerance of attention, element by element (u = 2^-24, n keys, head size d):
+a score is a sum of d products, each within 2^-21 of its value (fp32 caches:
+tf32 halves; 16-bit caches: exact), added in fp32 by steps that may truncate
+(2u each), so it is off by at most e = (2^-21 + 2 d u) * scale * sum|q k| plus
+8u of its size for the scaling; a weight is then off by 2 (e + 8 u |x|) relative
+(numerator and denominator), plus 2^-16 where weights are split into two 16-bit
+values; the sum over keys takes at most one add per 8 keys and three chained
+products each, every one at most 2u of the sum of w |v|.  The output adds half
+a step of its type.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from tests import pages_ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import llama_transformer_decode_gb300 as pkg  # noqa: E402
+
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+U = 2.0 ** -24
+
+
+def dev(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def make_pool(dtype, n_layers, n_pages, kv, ps, hs, n_seqs, max_pages, order="head", fill=None):
+    """Pool tensors in one of two memory orders, filled with `fill` (default: seeded noise)."""
+    shape = (n_layers, n_pages, kv, ps, hs) if order == "head" else (n_layers, n_pages, ps, kv, hs)
+    g = torch.Generator(device="cuda").manual_seed(n_pages * 31 + ps)
+    kv_t = []
+    for _ in range(2):
+        t = torch.randn(shape, generator=g, device="cuda").to(dtype) if fill is None else torch.full(shape, fill, dtype=dtype, device="cuda")
+        kv_t.append(t if order == "head" else t.transpose(2, 3))
+    return pkg.PagePool.from_tensors(kv_t[0], kv_t[1], dev(np.zeros(n_pages)), dev(np.zeros(n_seqs)),
+                                     dev(np.zeros((n_seqs, max_pages))))
+
+
+def same_books(pool, ref):
+    assert pool.lens.cpu().numpy().tolist() == ref.lens.tolist()
+    assert pool.refs.cpu().numpy().tolist() == ref.refs.tolist()
+    t = pool.table.cpu().numpy()
+    for s in range(len(ref.lens)):
+        h = ref.held(s)
+        assert t[s, :h].tolist() == ref.table[s, :h].tolist(), s
+
+
+@pytest.mark.parametrize("dtype,ps,kv,hs,order", [("fp32", 16, 4, 8, "head"), ("bf16", 7, 3, 48, "row"),
+                                                  ("fp16", 1, 2, 64, "head"), ("fp32", 32, 1, 128, "row"),
+                                                  ("bf16", 128, 2, 8, "head")])
+def test_random_histories_match_the_plain_statement(dtype, ps, kv, hs, order):
+    rng = np.random.default_rng(ps * 100 + hs)
+    L, n_pages, n_seqs, max_pages = 3, 90, 24, 12
+    pool = make_pool(DT[dtype], L, n_pages, kv, ps, hs, n_seqs, max_pages, order)
+    ref = pages_ref.RefPool(n_pages, ps, n_seqs, max_pages)
+    k, v = pool.k.clone(), pool.v.clone()  # the expected rows, page by page
+    refused = 0
+    for step in range(60):
+        op = rng.choice(["append", "append", "fork", "free", "compact"])
+        if op == "append":
+            seqs = rng.permutation(n_seqs)[:rng.integers(1, n_seqs)]
+            counts = rng.integers(0, 2 * ps + 2, len(seqs)) if step % 3 else np.ones(len(seqs), int)
+            counts = [int(c) for c in counts]
+            before = [a.copy() for a in (ref.refs, ref.lens, ref.table)]
+            places = ref.append(seqs, counts)
+            rows = sum(counts)
+            # new rows as part of a wider tensor (a fused projection's output)
+            wide = torch.randn((L, rows, 3 * kv, hs), device="cuda").to(DT[dtype])
+            nk, nv = wide[:, :, kv:2 * kv], wide[:, :, 2 * kv:]
+            starts = None if all(c == 1 for c in counts) else dev(np.concatenate([[0], np.cumsum(counts)]))
+            if step % 2:
+                pool.append(nk, nv, dev(seqs), starts)
+            else:  # one layer after the other
+                for layer in range(L):
+                    pool.append(nk[layer], nv[layer], dev(seqs), starts, layer=layer)
+            if places is None:
+                refused += 1
+                ref.refs, ref.lens, ref.table = before
+                with pytest.raises(pkg.L2Error):
+                    pool.check()
+            elif rows:
+                pages, at = torch.tensor([p[0] for p in places]).cuda(), torch.tensor([p[1] for p in places]).cuda()
+                k.permute(1, 3, 0, 2, 4)[pages, at] = nk.transpose(0, 1)
+                v.permute(1, 3, 0, 2, 4)[pages, at] = nv.transpose(0, 1)
+        elif op == "fork":
+            empty = [s for s in range(n_seqs) if ref.lens[s] == 0]
+            full = [s for s in range(n_seqs) if ref.lens[s] > 0]
+            if not empty or not full:
+                continue
+            n = int(rng.integers(1, min(len(empty), 9) + 1))
+            dst = rng.permutation(empty)[:n]
+            src = rng.choice(full, n)
+            rows = None if step % 2 else [int(rng.integers(0, ref.lens[s] + 1)) for s in src]
+            copies = ref.fork(src, dst, rows)
+            pool.fork(dev(src), dev(dst), None if rows is None else dev(rows))
+            if copies is None:
+                refused += 1
+                with pytest.raises(pkg.L2Error):
+                    pool.check()
+            else:
+                for a, b, t in copies:
+                    k[:, b, :, :t], v[:, b, :, :t] = k[:, a, :, :t], v[:, a, :, :t]
+        else:
+            seqs = rng.permutation(n_seqs)[:rng.integers(0, 6)]
+            seqs = np.concatenate([seqs, seqs[:1]])  # one named twice
+            moves = ref.free(seqs, op == "compact")
+            pool.free(dev(seqs), compact=op == "compact")
+            for a, b in moves:
+                k[:, b], v[:, b] = k[:, a].clone(), v[:, a].clone()
+        same_books(pool, ref)
+        assert torch.equal(pool.k, k) and torch.equal(pool.v, v), (step, op)
+    pool.check()
+    assert refused < 40
+
+
+def test_refused_calls_change_nothing_and_say_why():
+    pool = make_pool(torch.float32, 2, 6, 2, 4, 8, 5, 4)
+    rows = lambda n: torch.randn((2, n, 2, 8), device="cuda")  # noqa: E731
+    x = rows(13)
+    pool.append(x, x, dev([0, 2]), dev([0, 6, 13]))
+    pool.check()
+    books = [t.clone() for t in (pool.refs, pool.lens, pool.table, pool.k, pool.v)]
+
+    def refused(call, text):
+        call()
+        with pytest.raises(pkg.L2Error, match=text):
+            pool.check()
+        for a, b in zip(books, (pool.refs, pool.lens, pool.table, pool.k, pool.v)):
+            assert torch.equal(a, b)
+
+    one, two, nine = rows(1), rows(2), rows(9)
+    refused(lambda: pool.append(two, two, dev([0, 0])), "index")                       # a sequence twice
+    refused(lambda: pool.append(one, one, dev([5])), "index")                          # no such sequence
+    refused(lambda: pool.append(one, one, dev([-1])), "index")
+    refused(lambda: pool.append(two, two, dev([0]), dev([0, 1])), "index")             # starts do not cover the rows
+    refused(lambda: pool.append(two, two, dev([0, 1]), dev([0, 3, 2])), "index")       # starts descend
+    refused(lambda: pool.append(rows(11), rows(11), dev([0]), dev([0, 11])), "index")  # longer than a table
+    refused(lambda: pool.append(nine, nine, dev([1]), dev([0, 9])), "free pages")
+    # ... and the other layers of a refused step are not written either
+    refused(lambda: (pool.append(nine[0], nine[0], dev([1]), dev([0, 9]), layer=0),
+                     pool.append(nine[1], nine[1], dev([1]), dev([0, 9]), layer=1)), "free pages")
+    refused(lambda: pool.fork(dev([0]), dev([2])), "index")                            # not empty
+    refused(lambda: pool.fork(dev([0, 0]), dev([1, 1])), "index")
+    refused(lambda: pool.fork(dev([1]), dev([1])), "index")
+    refused(lambda: pool.fork(dev([0]), dev([1]), dev([7])), "index")                  # more rows than there are
+    refused(lambda: pool.fork(dev([0, 0, 0]), dev([1, 3, 4])), "free pages")
+    refused(lambda: pool.free(dev([0, 9])), "index")
+    q = torch.randn((2, 4, 8), device="cuda")
+    out = torch.full((2, 4, 8), 7.0, device="cuda")
+    for bad in (dict(seqs=dev([0, 5])), dict(seqs=dev([0, 2]), group_starts=dev([0, 1]), prefix_lens=dev([2])),
+                dict(seqs=dev([0, 2]), group_starts=dev([0, 2]), prefix_lens=dev([-1])),
+                dict(seqs=dev([0, 2]), group_starts=dev([1, 2]), prefix_lens=dev([1]))):
+        refused(lambda: pool.attention(q, 0, out=out, **bad), "index")
+        assert bool((out == 7.0).all())
+    pool.append(one, one, dev([1]))   # the pool still works
+    pool.check()
+
+
+def test_appending_into_a_page_another_sequence_holds_is_refused():
+    pool = make_pool(torch.float32, 1, 8, 1, 4, 8, 3, 4)
+    x = torch.randn((1, 6, 1, 8), device="cuda")
+    pool.append(x, x, dev([0]), dev([0, 6]))
+    pool.table[1] = pool.table[0]      # a caller's own sharing of a partly filled page
+    pool.lens[1] = 6
+    pool.refs[pool.table[0, :2].long()] += 1
+    before = pool.k.clone()
+    pool.append(x[:, :1], x[:, :1], dev([1]))
+    with pytest.raises(pkg.L2Error, match="inconsistent"):
+        pool.check()
+    assert torch.equal(pool.k, before)
+
+
+# -- attention --------------------------------------------------------------
+
+def build(dtype, H, kv, hs, ps, groups, order="head", seed=0, layers=1, poison=float("nan"), slack=3):
+    """A pool whose sequences (in groups of (prefix, [own rows, ...])) hold shuffled pages; everything no sequence
+    holds is `poison`.  Returns pool, per-sequence rows in 64 bits, starts, prefixes."""
+    rng = np.random.default_rng(seed)
+    lens = [p + n for p, own in groups for n in own]
+    up = lambda n: -(-n // ps)  # noqa: E731
+    need = sum(up(n) for n in lens) + slack
+    n_seqs, max_pages = len(lens), max(up(max(lens)), 1) + 1
+    pool = make_pool(DT[dtype], layers, need, kv, ps, hs, n_seqs, max_pages, order, fill=poison)
+    ids = list(rng.permutation(need))
+    table = rng.integers(0, need, (n_seqs, max_pages)).astype(np.int32)  # entries past a sequence's end: anything
+    k_rows, v_rows, b = [], [], 0
+    layer = layers - 1
+    for prefix, own in groups:
+        first = b
+        for n in own:
+            total = prefix + n
+            k = torch.from_numpy(rng.standard_normal((total, kv, hs)).astype(np.float32)).to(DT[dtype])
+            v = torch.from_numpy(rng.standard_normal((total, kv, hs)).astype(np.float32)).to(DT[dtype])
+            if b != first:
+                k[:prefix], v[:prefix] = k_rows[first][:prefix], v_rows[first][:prefix]
+            for j in range(up(total)):
+                if b != first and (j + 1) * ps <= prefix:
+                    table[b, j] = table[first, j]
+                    continue
+                table[b, j] = ids.pop()
+                m = min(ps, total - j * ps)
+                pool.k[layer, int(table[b, j]), :, :m] = k[j * ps:j * ps + m].transpose(0, 1).cuda()
+                pool.v[layer, int(table[b, j]), :, :m] = v[j * ps:j * ps + m].transpose(0, 1).cuda()
+            k_rows.append(k)
+            v_rows.append(v)
+            b += 1
+    pool.table.copy_(dev(table))
+    pool.lens.copy_(dev(lens))
+    starts = np.concatenate([[0], np.cumsum([len(own) for _, own in groups])])
+    return pool, [(k.double().numpy(), v.double().numpy()) for k, v in zip(k_rows, v_rows)], starts, [p for p, _ in groups]
+
+
+def check_attention(got, lse, q, rows, dtype, scale, seqs=None):
+    hs = q.shape[2]
+    half = torch.finfo(DT[dtype]).eps / 2
+    qd = q.double().cpu().numpy()
+    got = got.double().cpu().numpy()
+    worst = 0.0
+    for b in range(q.shape[0]):
+        k, v = rows[b if seqs is None else seqs[b]]
+        want, want_lse, mag, spread = pages_ref.attention(qd[b], k, v, scale)
+        n = len(k)
+        e = (2.0 ** -21 + 2 * hs * U) * spread + 8 * U * spread
+        rel = 2 * e + (0 if dtype == "fp32" else 2.0 ** -16) + (3 * (n / 8 + 1) + 64) * 2 * U
+        tol = rel * mag + half * (np.abs(want) + rel * mag) + 1e-38 + (2.0 ** -25 if dtype == "fp16" else 0)
+        err = np.abs(got[b] - want)
+        assert (err <= tol).all(), (b, n, float((err / tol).max()))
+        worst = max(worst, float((err / tol).max()) if n else 0.0)
+        if n:
+            assert np.abs(lse[b].cpu().numpy() - want_lse).max() <= 2 * e + (3 * n / 8 + 64) * 2 * U + 2.0 ** -22 * (np.abs(want_lse).max() + 1)
+        else:
+            assert (got[b] == 0).all() and bool((lse[b] == -math.inf).all())
+    return worst
+
+
+CASES = [
+    # heads, kv, hs, page size, groups (prefix, own rows)
+    (8, 4, 8, 16, [(100, [1, 20, 7, 3])]),
+    (6, 4, 48, 24, [(65, [1, 2, 0, 40])]),                     # heads not a multiple of KV heads
+    (12, 12, 64, 7, [(33, [5] * 5), (0, [1, 0, 64, 65]), (129, [1])]),
+    (32, 4, 64, 32, [(257, [3, 100, 31, 32, 33, 0] * 3)]),
+    (32, 32, 128, 64, [(130, [1, 17]), (64, [64, 128, 1])]),
+    (8, 1, 128, 16, [(200, [9] * 9)]),
+    (16, 16, 16, 1, [(5, [3, 0])]),                            # pages of one row
+    (40, 1, 32, 128, [(300, [11, 0, 5, 128])]),                # more heads on a KV head than one tile of rows
+    (4, 2, 128, 1000, [(1500, [700, 1]), (0, [0])]),           # pages longer than a tile; an empty sequence
+    (3, 3, 24, 5, [(0, [1])]),
+    (2, 2, 64, 16, [(4000, [500] * 20)]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention_matches_64_bits(case, dtype):
+    H, kv, hs, ps, groups = CASES[case]
+    pool, rows, starts, prefix = build(dtype, H, kv, hs, ps, groups, order="head" if case % 2 else "row", seed=case, layers=1 + case % 2)
+    B = len(rows)
+    g = torch.Generator(device="cuda").manual_seed(case)
+    wide = torch.randn((B, H + 2 * kv, hs), generator=g, device="cuda").to(DT[dtype])  # q inside a fused projection
+    q = wide[:, :H] * 2
+    scale = 1 / math.sqrt(hs)
+    lse = torch.empty((B, H), device="cuda")
+    layer = pool.n_layers - 1
+    out = pool.attention(q, layer, group_starts=dev(starts), prefix_lens=dev(prefix), lse=lse)
+    pool.check()
+    check_attention(out, lse, q, rows, dtype, scale)
+    # the same rows without sharing, in another order, into a strided output
+    order = np.random.default_rng(case).permutation(B)
+    big = torch.full((B, H + 1, hs), 5.0, device="cuda").to(DT[dtype])
+    out2 = pool.attention(q[torch.from_numpy(order).cuda()], layer, seqs=dev(order), out=big[:, :H], lse=lse)
+    check_attention(out2, lse, q[torch.from_numpy(order).cuda()], rows, dtype, scale, seqs=order)
+    assert bool((big[:, H] == 5.0).all())
+    # twice the same call: the same bits
+    again = pool.attention(q, layer, group_starts=dev(starts), prefix_lens=dev(prefix))
+    assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
+    pool.check()
+
+
+def test_a_prefix_longer_than_a_member_is_cut_and_rows_may_repeat():
+    pool, rows, starts, prefix = build("bf16", 8, 2, 64, 16, [(50, [30, 4, 10])], seed=3)
+    q = torch.randn((4, 8, 64), device="cuda").to(torch.bfloat16)
+    lse = torch.empty((4, 8), device="cuda")
+    seqs = [0, 1, 2, 1]
+    out = pool.attention(q, 0, seqs=dev(seqs), group_starts=dev([0, 4]), prefix_lens=dev([50]), lse=lse)
+    check_attention(out, lse, q, rows, "bf16", 1 / 8, seqs=seqs)
+    # a prefix length past the shortest member: its rows end where the sequence does
+    same, rows2, _, _ = build("bf16", 8, 2, 64, 16, [(50, [0, 0, 0, 0])], seed=4)
+    out = same.attention(q, 0, group_starts=dev([0, 4]), prefix_lens=dev([10 ** 6]), lse=lse)
+    check_attention(out, lse, q, rows2, "bf16", 1 / 8)
+    # groups without rows
+    out = same.attention(q, 0, group_starts=dev([0, 0, 4, 4]), prefix_lens=dev([9, 20, 7]), lse=lse)
+    check_attention(out, lse, q, rows2, "bf16", 1 / 8)
+    same.check()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_infinities_and_nan_of_visible_rows_show_as_in_the_formula(dtype):
+    pool, rows, starts, prefix = build(dtype, 2, 2, 64, 16, [(40, [5, 9])], seed=5)
+    page = int(pool.table[1, 2])            # sequence 1's own page (positions 32..47)
+    pool.v[0, page, 0, 12] = float("nan")   # position 44: only sequence 1, KV head 0
+    pool.k[0, page, 1, 12] = float("nan")
+    q = torch.randn((2, 2, 64), device="cuda").to(DT[dtype])
+    out = pool.attention(q, 0, group_starts=dev(starts), prefix_lens=dev(prefix))
+    assert bool(out[0].isfinite().all()) and bool(out[1].isnan().all())
+    pool.check()
+
+
+def test_a_bad_page_is_reported_and_reads_nothing():
+    pool, rows, starts, prefix = build("fp32", 4, 2, 32, 8, [(16, [20, 3])], seed=6)
+    q = torch.randn((2, 4, 32), device="cuda")
+    good = pool.attention(q, 0)
+    for bad in (-1, pool.n_pages, 2 ** 31 - 1):
+        pool.table[0, 4] = bad
+        out = pool.attention(q, 0)
+        with pytest.raises(pkg.L2Error, match="outside the pool"):
+            pool.check()
+        assert torch.equal(out[1], good[1]) and bool(out[0].isfinite().all())
+
+
+def test_offsets_past_32_bits():
+    # 2 x 5.4 GB: pages past 2^32 bytes
+    ps, kv, hs, n_pages = 16, 4, 128, 330_000
+    pool = pkg.PagePool.from_tensors(torch.zeros((1, n_pages, kv, ps, hs), dtype=torch.bfloat16, device="cuda"),
+                                     torch.zeros((1, n_pages, kv, ps, hs), dtype=torch.bfloat16, device="cuda"),
+                                     dev(np.zeros(n_pages)), dev(np.zeros(3)), dev(np.zeros((3, 8))))
+    pool.refs[:n_pages - 12] = 1             # the free pages are the last ones
+    x = torch.randn((2, 1, 50, kv, hs), device="cuda").to(torch.bfloat16)
+    pool.append(x[0], x[1], dev([0]), dev([0, 50]))
+    pool.fork(dev([0]), dev([1]))
+    q = torch.randn((2, 8, hs), device="cuda").to(torch.bfloat16)
+    lse = torch.empty((2, 8), device="cuda")
+    out = pool.attention(q, 0, seqs=dev([0, 1]), group_starts=dev([0, 2]), prefix_lens=dev([48]), lse=lse)
+    pool.check()
+    assert int(pool.table[0, 0]) == n_pages - 12
+    rows = [(x[0, 0].double().cpu().numpy(), x[1, 0].double().cpu().numpy())] * 2
+    check_attention(out, lse, q, rows, "bf16", 1 / math.sqrt(hs))
+    pool.refs[:n_pages - 12] = 0
+    pool.free(compact=True)                  # and back to the lowest pages
+    out2 = pool.attention(q, 0, seqs=dev([0, 1]), group_starts=dev([0, 2]), prefix_lens=dev([48]))
+    pool.check()
+    assert torch.equal(out, out2) and int(pool.table[:2, :4].max()) == 4
+
+
+def test_a_step_captured_into_a_graph_follows_the_lengths():
+    """Append, attention and fork of a decode step in one graph, replayed while sequences grow."""
+    pool, rows, starts, prefix = build("fp32", 8, 4, 64, 16, [(70, [1, 5, 9])], seed=7, poison=0.0, slack=40)
+    pool.refs.copy_(dev(np.bincount(np.concatenate([pool.table.cpu().numpy()[s, :-(-int(n) // 16)] for s, n in enumerate(pool.lens.tolist())]),
+                                    minlength=pool.n_pages)))
+    seqs = dev([0, 1, 2])
+    k, v, q = (torch.zeros((3, n, 64), device="cuda") for n in (4, 4, 8))
+    gs, pl = dev(starts), dev(prefix)
+    lse = torch.zeros((3, 8), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pool.append(k, v, seqs, layer=0)
+        out = pool.attention(q, 0, group_starts=gs, prefix_lens=pl, lse=lse)
+    rows = [list(r) for r in rows]
+    for step in range(9):
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for s in range(3):
+            rows[s][0] = np.concatenate([rows[s][0], k[s:s + 1].double().cpu().numpy()])
+            rows[s][1] = np.concatenate([rows[s][1], v[s:s + 1].double().cpu().numpy()])
+        check_attention(out, lse, q, rows, "fp32", 1 / 8)
+    pool.check()
+
+
+def test_two_streams_at_once_and_a_chosen_stream():
+    pool, rows, starts, prefix = build("fp16", 16, 2, 64, 32, [(700, [50] * 12)], seed=8)
+    q = [torch.randn((12, 16, 64), device="cuda").to(torch.float16) for _ in range(2)]
+    gs, pl = dev(starts), dev(prefix)
+    want = [pool.attention(x, 0, group_starts=gs, prefix_lens=pl) for x in q]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(pool.attention(q[i], 0, group_starts=gs, prefix_lens=pl, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_a_serving_loop_of_all_operators(dtype):
+    """A prompt appended, forked to children, grown and attended step by step, children freed, the pool closed
+    up and the rest attended again: rows as kept on the host, attention in 64 bits."""
+    rng = np.random.default_rng(11)
+    L, H, kv, hs, ps = 2, 8, 2, 64, 16
+    pool = pkg.PagePool(L, 64, kv, ps, hs, 8, 12, dtype=DT[dtype])
+    new = lambda n: (torch.randn((L, n, kv, hs), device="cuda").to(DT[dtype]), torch.randn((L, n, kv, hs), device="cuda").to(DT[dtype]))  # noqa: E731
+    k, v = new(75)
+    pool.append(k, v, dev([0]), dev([0, 75]))
+    pool.fork(dev([0] * 5), dev([1, 2, 3, 4, 5]))
+    hist = {s: [k, v] for s in range(6)}
+    live = [0, 1, 2, 3, 4, 5]
+    for step in range(40):
+        if step == 20:
+            pool.free(dev([0, 2, 3]), compact=True)   # the parent among them: its pages live on in the children
+            live = [1, 4, 5]
+        order = [int(s) for s in rng.permutation(live)]
+        k, v = new(len(order))
+        for layer in range(L):
+            pool.append(k[layer], v[layer], dev(order), layer=layer)
+        for i, s in enumerate(order):
+            hist[s] = [torch.cat([hist[s][0], k[:, i:i + 1]], 1), torch.cat([hist[s][1], v[:, i:i + 1]], 1)]
+        if step % 10 in (0, 9):
+            layer = step % L
+            q = torch.randn((len(order), H, hs), device="cuda").to(DT[dtype])
+            lse = torch.empty((len(order), H), device="cuda")
+            out = pool.attention(q, layer, seqs=dev(order), group_starts=dev([0, len(order)]), prefix_lens=dev([75]), lse=lse)
+            rows = [(hist[s][0][layer].double().cpu().numpy(), hist[s][1][layer].double().cpu().numpy()) for s in order]
+            check_attention(out, lse, q, rows, dtype, 1 / 8)
+    pool.check()
+    assert int((pool.refs > 0).sum()) == int(pool.refs.nonzero().max()) + 1 or step > 20
+    pool.free(dev(live))
+    assert int(pool.refs.abs().sum()) == 0
