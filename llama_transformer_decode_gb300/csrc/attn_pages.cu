@@ -30,6 +30,7 @@
 #include <math_constants.h>
 
 #include "../../include/l2.h"
+#include "attn_pages.cuh"
 #include "l2_device.cuh"
 #include "l2_pages.h"
 
@@ -39,49 +40,49 @@ namespace {
 
 constexpr int kWarps = 8;      // warps of a block, one block per SM
 constexpr int kStages = 3;     // tiles of a warp's ring
-constexpr int kM = 16;         // (row, head) pairs of an item
 // Fewest tiles a warp takes: below that the parts cost more to write and merge than the
 // parallel reading gains.
 constexpr int kMinTiles = 4;
-
-// Plan, in the workspace: header, then per source (S = G + B, at most 2 kPagesMaxCall)
-// the first tile, first item, tiles per item, first key, end key, first row, rows.
-enum { kHdrTiles = 0, kHdrItems = 1, kHdrWarps = 2, kHdrOk = 3, kHdrInts = 16 };
-struct Plan {
-    int *hdr, *t0, *i0, *kt, *key0, *key1, *row0, *rows;
-};
-__host__ __device__ inline Plan plan_of(int *base, int S) {
-    Plan p;
-    p.hdr = base;
-    p.t0 = base + kHdrInts;
-    p.i0 = p.t0 + S + 1;
-    p.kt = p.i0 + S + 1;
-    p.key0 = p.kt + S;
-    p.key1 = p.key0 + S;
-    p.row0 = p.key1 + S;
-    p.rows = p.row0 + S;
-    return p;
-}
-__host__ __device__ inline size_t plan_ints(int S) { return (kHdrInts + 2 * (size_t)(S + 1) + 5 * (size_t)S + 63) / 64 * 64; }
-
-__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
-
-// Most query heads of a KV head; head j of KV head g is first_head(g) + j.
-__host__ __device__ __forceinline__ int heads_per_kv(int H, int KV) { return (H + KV - 1) / KV; }
-__device__ __forceinline__ int first_head(int g, int H, int KV) { return (g * H + KV - 1) / KV; }
-
-// Tiles are cut evenly: warp w takes tiles [first_of(w), first_of(w + 1)).
-__device__ __forceinline__ int first_of(int w, int T, int W) { return (int)((long long)w * T / W); }
-__device__ __forceinline__ int warp_of(int tile, int T, int W) { return (int)((((long long)tile + 1) * W + T - 1) / T - 1); }
+constexpr int kTcMinTiles = 4;  // the same for the tensor-core kernel's blocks (tiles of 128 keys)
 
 }  // namespace
 
+namespace {
+// Exclusive prefix sum over a block of 1024 threads; buf: 64 ints.
+__device__ __forceinline__ int block_scan_1024(int v, int *total, int *buf) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) buf[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = buf[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        buf[32 + lane] = w;
+    }
+    __syncthreads();
+    const int before = warp ? buf[32 + warp - 1] : 0;
+    *total = buf[63];
+    __syncthreads();
+    return before + x - v;
+}
+}  // namespace
+
 // One block: lengths of the sources and the numbering of their tiles and items.
-__global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p, int tile_keys, int max_warps) {
-    __shared__ int part[2][32], minlen[kPagesMaxCall], gstart[kPagesMaxCall + 1], len_s[kPagesMaxCall];
-    const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+// With p.tc the whole tiles of a prefix that serves more than 16 pairs go to the tensor-core kernel.
+__global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p, int tile_keys, int num_sms) {
+    __shared__ int part[1][64], minlen[kPagesMaxCall], mintc[kPagesMaxCall], gstart[kPagesMaxCall + 1], len_s[kPagesMaxCall];
+    const int i = threadIdx.x;
     const int S = p.G + p.B;
-    const Plan pl = plan_of(p.plan, S);
+    const Plan pl = plan_of(p.plan, S, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     pdl_launch_dependents();
     bool bad = false;
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p
     if (__syncthreads_or(bad)) {
         if (i == 0) {
             atomicOr(p.err, L2_PAGES_ERR_ARGS);
-            pl.hdr[kHdrTiles] = pl.hdr[kHdrItems] = 0;
-            pl.hdr[kHdrWarps] = 1;
+            pl.hdr[kHdrTiles] = pl.hdr[kHdrTcTiles] = 0;
+            pl.hdr[kHdrWarps] = pl.hdr[kHdrTcCtas] = 1;
             pl.hdr[kHdrOk] = 0;
         }
         return;
@@ -131,12 +132,27 @@ __global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p
         atomicMin(&minlen[lo], len);
     }
     __syncthreads();
+    // prefixes worth it go to the tensor cores in whole tiles of 128 keys; what is left of them stays here
+    int tc_tiles = 0, tc_rows = 0;
+    if (p.G) {
+        const int n = rows * gq, full = i < p.G && p.tc && n > kM ? minlen[i] / kTcKeys : 0;
+        const int tiles = full * tc_runs(n) * p.n_kv_heads, prows = full ? tc_head_rows(n) * p.n_kv_heads : 0;
+        const int tb = block_scan_1024(tiles, &tc_tiles, part[0]), rb = block_scan_1024(prows, &tc_rows, part[0]);
+        if (i < p.G) {
+            pl.tc_t0[i] = tb;
+            pl.tc_kt[i] = full;
+            pl.tc_r0[i] = rb;
+            mintc[i] = full * kTcKeys;
+        }
+        __syncthreads();
+    }
     // sources in blocks of 1024: G prefixes, then B sequences
     int tiles_before = 0, items_before = 0;
     for (int s0 = 0; s0 < S; s0 += 1024) {
         const int s = s0 + i;
         int key0 = 0, key1 = 0, row0 = 0, n = 0;
         if (s < p.G) {
+            key0 = mintc[s];
             key1 = minlen[s];
             row0 = gstart[s];
             n = gstart[s + 1] - row0;
@@ -153,48 +169,28 @@ __global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p
         }
         const int kt = s < S ? cdiv(key1 - key0, tile_keys) : 0;
         const int items = kt > 0 ? cdiv(n * gq, kM) * p.n_kv_heads : 0;
-        int a = items * kt, b = items;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-            if (lane >= o) {
-                a += x;
-                b += y;
-            }
-        }
-        if (lane == 31) {
-            part[0][warp] = a;
-            part[1][warp] = b;
-        }
-        __syncthreads();
-        int ta = 0, tb = 0, wa = 0, wb = 0;
-        for (int w = 0; w < 32; ++w) {
-            if (w == warp) {
-                wa = ta;
-                wb = tb;
-            }
-            ta += part[0][w];
-            tb += part[1][w];
-        }
+        int tiles_here, items_here;
+        const int a = block_scan_1024(items * kt, &tiles_here, part[0]), b = block_scan_1024(items, &items_here, part[0]);
         if (s < S) {
-            pl.t0[s] = tiles_before + wa + a - items * kt;
-            pl.i0[s] = items_before + wb + b - items;
+            pl.t0[s] = tiles_before + a;
+            pl.i0[s] = items_before + b;
             pl.kt[s] = kt;
             pl.key0[s] = key0;
             pl.key1[s] = key1;
             pl.row0[s] = row0;
             pl.rows[s] = n;
         }
-        tiles_before += ta;
-        items_before += tb;
-        __syncthreads();
+        tiles_before += tiles_here;
+        items_before += items_here;
     }
     if (i == 0) {
         pl.t0[S] = tiles_before;
         pl.i0[S] = items_before;
         pl.hdr[kHdrTiles] = tiles_before;
-        pl.hdr[kHdrItems] = items_before;
-        pl.hdr[kHdrWarps] = max(1, min(max_warps, cdiv(tiles_before, kMinTiles)));
+        pl.hdr[kHdrTcTiles] = tc_tiles;
+        pl.hdr[kHdrTcCtas] = max(1, min(num_sms, cdiv(tc_tiles, kTcMinTiles)));
+        if (p.G) pl.tc_t0[p.G] = tc_tiles;
+        pl.hdr[kHdrWarps] = max(1, min(num_sms * kWarps, cdiv(tiles_before, kMinTiles)));
         pl.hdr[kHdrOk] = 1;
     }
 }
@@ -292,7 +288,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
     const int wid = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * (kStages * Sh::kStage);
     const int S = p.G + p.B;
-    const Plan pl = plan_of(p.plan, S);
+    const Plan pl = plan_of(p.plan, S, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     pdl_launch_dependents();
     pdl_wait();
@@ -301,16 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
     int tile = first_of(wid, T_all, W);
     const int tile_end = first_of(wid + 1, T_all, W);
     if (tile >= tile_end) return;
-    // the source of the first tile: the last with t0 <= tile (32-way search)
-    int src = 0;
-    for (int lo = 0, hi = S + 1; hi - lo > 1;) {  // t0[lo] <= tile < t0[hi]
-        const int step = cdiv(hi - lo, 32);
-        const int at = lo + lane * step;
-        const unsigned m = __ballot_sync(0xffffffffu, at < hi && pl.t0[min(at, S)] <= tile);
-        lo += (31 - __clz(m)) * step;
-        hi = min(hi, lo + step);
-        src = lo;
-    }
+    int src = warp_find(pl.t0, S + 1, tile);
     const int words = p.head_size * T::kBytes / 16;  // 16-byte words of a row that exist
 
     while (tile < tile_end) {
@@ -640,7 +627,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / p.n_heads, h = blockIdx.x - b * p.n_heads;
     const int S = p.G + p.B;
-    const Plan pl = plan_of(p.plan, S);
+    const Plan pl = plan_of(p.plan, S, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const int kvh = (int)((long long)h * p.n_kv_heads / p.n_heads), j = h - first_head(kvh, p.n_heads, p.n_kv_heads);
     const int d = 4 * lane;
@@ -661,6 +648,36 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     bool any = false;
     int seen = 0;
+    // one part into the warp's running (m, l, a); a part without keys has m = -inf
+    auto take = [&](float2 ml, const float *acc) {
+        if (ml.x == -CUDART_INF_F && ml.y == 0.f) return;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) v = *reinterpret_cast<const float4 *>(acc + d);
+        const float mn = fmaxf(m, ml.x), base = mn == -CUDART_INF_F ? 0.f : mn;
+        const float c0 = exp2f(m - base), c1 = exp2f(ml.x - base);
+        a.x = a.x * c0 + v.x * c1;
+        a.y = a.y * c0 + v.y * c1;
+        a.z = a.z * c0 + v.z * c1;
+        a.w = a.w * c0 + v.w * c1;
+        l = l * c0 + ml.y * c1;
+        m = mn;
+    };
+    if (grp >= 0 && pl.tc_kt[grp]) {
+        const int kt = pl.tc_kt[grp], n = pl.rows[grp] * gq, mi = (b - pl.row0[grp]) * gq + j;
+        const int run = mi / (2 * kTcRows), r = mi - run * 2 * kTcRows, rows = min(2 * kTcRows, n - run * 2 * kTcRows);
+        const int u0 = pl.tc_t0[grp] + (kvh * tc_runs(n) + run) * kt;
+        const int Tt = pl.hdr[kHdrTcTiles], Wt = pl.hdr[kHdrTcCtas];
+        const int w0 = walker_of(u0, Tt, Wt), w1 = walker_of(u0 + kt - 1, Tt, Wt);
+        const int base = pl.tc_r0[grp] + kvh * tc_head_rows(n) + run * 2 * kTcRows + r;
+        const int per = rows > kTcRows ? 1 : 2;  // parts a walker leaves of this row
+        any = true;
+        for (int e = warp; e < (w1 - w0 + 1) * per; e += 4) {
+            const int w = w0 + e / per, sl2 = e - (w - w0) * per;
+            const size_t at = (size_t)(base + 2 * kTcRows * w + sl2 * rows);
+            take(reinterpret_cast<const float2 *>(p.tc_ml)[at], p.tc_acc + at * p.head_size);
+        }
+        seen = ((w1 - w0 + 1) * per) & 3;
+    }
     for (int which = 0; which < 2; ++which) {
         const int s = which ? p.G + b : grp;
         if (s < 0) continue;
@@ -670,21 +687,11 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
         const int mi = (b - pl.row0[s]) * gq + j, tiles_m = cdiv(pl.rows[s] * gq, kM);
         const int item = kvh * tiles_m + mi / kM;
         const int u0 = pl.t0[s] + item * kt;
-        const int w0 = warp_of(u0, T_all, W), w1 = warp_of(u0 + kt - 1, T_all, W);
+        const int w0 = walker_of(u0, T_all, W), w1 = walker_of(u0 + kt - 1, T_all, W);
         const int slot0 = pl.i0[s] + item;
         for (int w = w0 + ((warp - seen) & 3); w <= w1; w += 4) {
             const size_t at = (size_t)(slot0 + w) * kM + (mi % kM);
-            const float2 ml = reinterpret_cast<const float2 *>(p.ws_ml)[at];
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (on) v = *reinterpret_cast<const float4 *>(p.ws_acc + at * p.head_size + d);
-            const float mn = fmaxf(m, ml.x), base = mn == -CUDART_INF_F ? 0.f : mn;
-            const float c0 = exp2f(m - base), c1 = exp2f(ml.x - base);
-            a.x = a.x * c0 + v.x * c1;
-            a.y = a.y * c0 + v.y * c1;
-            a.z = a.z * c0 + v.z * c1;
-            a.w = a.w * c0 + v.w * c1;
-            l = l * c0 + ml.y * c1;
-            m = mn;
+            take(reinterpret_cast<const float2 *>(p.ws_ml)[at], p.ws_acc + at * p.head_size);
         }
         seen = (seen + (w1 - w0 + 1)) & 3;
     }
@@ -742,22 +749,45 @@ int max_items(int B, int G, int n_heads, int n_kv_heads) {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// Rows of the tensor-core kernel's parts: each run at most twice its pairs, and 256 a block.
+size_t tc_part_rows(int B, int n_heads, int n_kv_heads, int num_sms) {
+    return 2 * (size_t)B * heads_per_kv(n_heads, n_kv_heads) * n_kv_heads + 2 * kTcRows * (size_t)(num_sms + 1);
+}
+
+// The workspace's parts, in order.
+struct WsLayout {
+    size_t plan, ml, acc, tc_ml, tc_acc, bytes, parts;
+};
+WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms) {
+    WsLayout w;
+    w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * kWarps;
+    const size_t tc = G ? tc_part_rows(B, n_heads, n_kv_heads, num_sms) : 0;
+    w.plan = 0;
+    w.ml = w.plan + align256(plan_ints(B + G, G) * 4);
+    w.acc = w.ml + align256(w.parts * kM * 8);
+    w.tc_ml = w.acc + align256(w.parts * kM * head_size * 4);
+    w.tc_acc = w.tc_ml + align256(tc * 8);
+    w.bytes = w.tc_acc + align256(tc * head_size * 4);
+    return w;
+}
+
 }  // namespace
 
 size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms) {
-    const size_t parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * kWarps;
-    return align256(plan_ints(B + G) * 4) + align256(parts * kM * 8) + align256(parts * kM * head_size * 4);
+    return ws_layout(B, G, n_heads, n_kv_heads, head_size, num_sms).bytes;
 }
 
 cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s) {
-    const size_t parts = (size_t)max_items(p.B, p.G, p.n_heads, p.n_kv_heads) + (size_t)num_sms * kWarps;
-    char *w = static_cast<char *>(ws);
-    p.plan = reinterpret_cast<int *>(w);
-    w += align256(plan_ints(p.B + p.G) * 4);
-    p.ws_ml = reinterpret_cast<float *>(w);
-    w += align256(parts * kM * 8);
-    p.ws_acc = reinterpret_cast<float *>(w);
-    p.max_parts = (int)parts;
+    const WsLayout w = ws_layout(p.B, p.G, p.n_heads, p.n_kv_heads, p.head_size, num_sms);
+    char *base = static_cast<char *>(ws);
+    p.plan = reinterpret_cast<int *>(base + w.plan);
+    p.ws_ml = reinterpret_cast<float *>(base + w.ml);
+    p.ws_acc = reinterpret_cast<float *>(base + w.acc);
+    p.tc_ml = reinterpret_cast<float *>(base + w.tc_ml);
+    p.tc_acc = reinterpret_cast<float *>(base + w.tc_acc);
+    p.max_parts = (int)w.parts;
+    // a prefix that serves at most 16 pairs or is shorter than a tile gains nothing there
+    p.tc = p.G && p.B * heads_per_kv(p.n_heads, p.n_kv_heads) > kM && attn_pages_tc_supported(p);
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -766,9 +796,10 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     cfg.attrs = attr;
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(1024);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_pages_plan_kernel, p, tile_keys(p.dtype, p.head_size), num_sms * kWarps);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_pages_plan_kernel, p, tile_keys(p.dtype, p.head_size), num_sms);
     if (e != cudaSuccess) return e;
     cfg.numAttrs = 1;
+    if (p.tc && (e = launch_attn_pages_tc(p, num_sms, cfg)) != cudaSuccess) return e;
     const int hs = p.head_size;
     if (p.dtype == L2_F32)
         e = hs <= 32   ? launch_walk<TF32, 32>(p, num_sms, cfg)

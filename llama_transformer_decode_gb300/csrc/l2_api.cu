@@ -24,6 +24,7 @@
 #include "../../include/l2.h"
 #include "l2_device.cuh"
 #include "l2_kernels.h"
+#include "l2_pages.h"
 #include "l2_params.h"
 
 using namespace l2;
@@ -1077,6 +1078,7 @@ int submit(l2_ctx *c, int B, const int *tokens, const int *pos, float *logits_ou
 
 namespace l2 {
 int set_call_error(int code, const char *text) { return fail(nullptr, code, "%s", text); }
+void *tensor_map_encoder() { return reinterpret_cast<void *>(encode_tiled()); }
 }  // namespace l2
 
 // Attention scratch of l2_forward_static: accumulators, (max, sum) pairs and

@@ -62,8 +62,17 @@ struct PagesAttn {
     // workspace
     int *plan;
     float *ws_ml, *ws_acc;
-    int max_parts;            // pieces the workspace holds
+    int max_parts;            // parts the workspace holds
+    bool tc;                  // prefixes may go to the tensor-core kernel
+    float *tc_ml, *tc_acc;    // its parts, by row
 };
+
+// Tensor-core part of it (attn_pages_tc.cu): whether pages and type allow tiled copies of 128 keys, and the launch.
+bool attn_pages_tc_supported(const PagesAttn &p);
+cudaError_t launch_attn_pages_tc(const PagesAttn &p, int num_sms, cudaLaunchConfig_t cfg);
+
+// cuTensorMapEncodeTiled, looked up once (l2_api.cu).
+void *tensor_map_encoder();
 
 size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms);
 // Lays `p`'s workspace out in ws and launches the kernels.

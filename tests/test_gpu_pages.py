@@ -6,8 +6,9 @@ a score is a sum of d products, each within 2^-21 of its value (fp32 caches:
 tf32 halves; 16-bit caches: exact), added in fp32 by steps that may truncate
 (2u each), so it is off by at most e = (2^-21 + 2 d u) * scale * sum|q k| plus
 8u of its size for the scaling; a weight is then off by 2 (e + 8 u |x|) relative
-(numerator and denominator), plus 2^-16 where weights are split into two 16-bit
-values; the sum over keys takes at most one add per 8 keys and three chained
+(numerator and denominator), plus, in 16-bit caches, at most half a step of the
+type where the tensor cores take it as a 16-bit value (the sum l is of the
+unrounded weights, so the numerator alone is off); the sum over keys takes at most one add per 8 keys and three chained
 products each, every one at most 2u of the sum of w |v|.  The output adds half
 a step of its type.
 """
@@ -231,7 +232,7 @@ def check_attention(got, lse, q, rows, dtype, scale, seqs=None):
         want, want_lse, mag, spread = pages_ref.attention(qd[b], k, v, scale)
         n = len(k)
         e = (2.0 ** -21 + 2 * hs * U) * spread + 8 * U * spread
-        rel = 2 * e + (0 if dtype == "fp32" else 2.0 ** -16) + (3 * (n / 8 + 1) + 64) * 2 * U
+        rel = 2 * e + (0 if dtype == "fp32" else half) + (3 * (n / 8 + 1) + 64) * 2 * U
         tol = rel * mag + half * (np.abs(want) + rel * mag) + 1e-38 + (2.0 ** -25 if dtype == "fp16" else 0)
         err = np.abs(got[b] - want)
         assert (err <= tol).all(), (b, n, float((err / tol).max()))
@@ -256,6 +257,14 @@ CASES = [
     (4, 2, 128, 1000, [(1500, [700, 1]), (0, [0])]),           # pages longer than a tile; an empty sequence
     (3, 3, 24, 5, [(0, [1])]),
     (2, 2, 64, 16, [(4000, [500] * 20)]),
+    # prefixes that serve many rows: runs of 320 pairs, of 17 to 64, several groups, odd heads, every kind of page
+    (32, 4, 64, 16, [(1000, [5] * 40)]),
+    (32, 8, 128, 256, [(700, [3] * 33), (129, [1] * 5), (128, [0, 0, 0, 0, 0, 0, 1])]),
+    (6, 4, 48, 8, [(515, [2] * 20)]),
+    (12, 12, 128, 32, [(2048, [1] * 17)]),
+    (8, 1, 64, 128, [(256, [0] * 32), (4000, [7] * 33)]),
+    (4, 4, 96, 64, [(900, [70] * 129)]),
+    (16, 2, 8, 64, [(1300, [1] * 16)]),
 ]
 
 
@@ -284,6 +293,17 @@ def test_attention_matches_64_bits(case, dtype):
     again = pool.attention(q, layer, group_starts=dev(starts), prefix_lens=dev(prefix))
     assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
     pool.check()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 4.0])
+def test_any_scale(scale, dtype):
+    pool, rows, starts, prefix = build(dtype, 4, 2, 64, 16, [(300, [9] * 20)], seed=12)
+    q = torch.randn((20, 4, 64), device="cuda").to(DT[dtype])
+    lse = torch.empty((20, 4), device="cuda")
+    out = pool.attention(q, 0, group_starts=dev(starts), prefix_lens=dev(prefix), scale=scale, lse=lse)
+    pool.check()
+    check_attention(out, lse, q, rows, dtype, scale)
 
 
 def test_a_prefix_longer_than_a_member_is_cut_and_rows_may_repeat():
