@@ -38,7 +38,6 @@ namespace l2 {
 
 namespace {
 
-constexpr int kWarps = 8;      // warps of a block, one block per SM
 constexpr int kStages = 3;     // tiles of a warp's ring
 // Fewest tiles a warp takes: below that the parts cost more to write and merge than the
 // parallel reading gains.
@@ -114,7 +113,7 @@ __global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p
     if (__syncthreads_or(bad)) {
         if (i == 0) {
             atomicOr(p.err, L2_PAGES_ERR_ARGS);
-            pl.hdr[kHdrTiles] = pl.hdr[kHdrTcTiles] = 0;
+            pl.hdr[kHdrCost] = pl.hdr[kHdrTcTiles] = 0;
             pl.hdr[kHdrWarps] = pl.hdr[kHdrTcCtas] = 1;
             pl.hdr[kHdrOk] = 0;
         }
@@ -169,10 +168,12 @@ __global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p
         }
         const int kt = s < S ? cdiv(key1 - key0, tile_keys) : 0;
         const int items = kt > 0 ? cdiv(n * gq, kM) * p.n_kv_heads : 0;
+        const int cost = tile_cost(p.dtype, min(n * gq, kM));
         int tiles_here, items_here;
-        const int a = block_scan_1024(items * kt, &tiles_here, part[0]), b = block_scan_1024(items, &items_here, part[0]);
+        const int a = block_scan_1024(items * kt * cost, &tiles_here, part[0]), b = block_scan_1024(items, &items_here, part[0]);
         if (s < S) {
             pl.t0[s] = tiles_before + a;
+            pl.cost[s] = cost;
             pl.i0[s] = items_before + b;
             pl.kt[s] = kt;
             pl.key0[s] = key0;
@@ -186,26 +187,16 @@ __global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p
     if (i == 0) {
         pl.t0[S] = tiles_before;
         pl.i0[S] = items_before;
-        pl.hdr[kHdrTiles] = tiles_before;
+        pl.hdr[kHdrCost] = tiles_before;
         pl.hdr[kHdrTcTiles] = tc_tiles;
         pl.hdr[kHdrTcCtas] = max(1, min(num_sms, cdiv(tc_tiles, kTcMinTiles)));
         if (p.G) pl.tc_t0[p.G] = tc_tiles;
-        pl.hdr[kHdrWarps] = max(1, min(num_sms * kWarps, cdiv(tiles_before, kMinTiles)));
+        pl.hdr[kHdrWarps] = max(1, min(num_sms * kWalkWarps, cdiv(tiles_before, kMinTiles * kCostUnit)));
         pl.hdr[kHdrOk] = 1;
     }
 }
 
 namespace {
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
-    const int n = on ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t *r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -219,7 +210,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t *r) {
 }
 
 struct TBf16 {
-    static constexpr int kBytes = 2;
     static __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -232,7 +222,6 @@ struct TBf16 {
     static __device__ __forceinline__ float2 unpack(uint32_t v) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v)); }
 };
 struct TF16 {
-    static constexpr int kBytes = 2;
     static __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -244,90 +233,51 @@ struct TF16 {
     }
     static __device__ __forceinline__ float2 unpack(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
 };
-struct TF32 {
-    static constexpr int kBytes = 4;
-};
 
-__device__ __forceinline__ void mma_tf32_16x8x8(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// x = hi + lo in tf32, to 2^-22 of x
-__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
-}
-
-// Tile shape: HS the head size padded to 32 (fp32 only), 64 or 128; keys per tile such that K and V of
-// one take 8 KB at most.
-template <typename T, int HS>
+// Tile shape: HS the head size padded to 64 or 128; K and V of a tile's keys take 8 KB.
+template <int HS>
 struct Shape {
-    static constexpr int KT = T::kBytes == 4 ? (HS == 128 ? 8 : HS == 64 ? 16 : 32) : (HS == 128 ? 16 : 32);
-    static constexpr int C = HS * T::kBytes / 16;             // 16-byte words a row
-    static constexpr int kRow = HS * T::kBytes;
-    static constexpr int kStage = 2 * KT * kRow;              // K then V
-    static constexpr int kSmem = kWarps * kStages * kStage;
+    static constexpr int KT = HS == 128 ? 16 : 32;
+    static constexpr int C = HS * 2 / 16;         // 16-byte words a row
+    static constexpr int kRow = HS * 2;
+    static constexpr int kStage = 2 * KT * kRow;  // K then V
+    static constexpr int kSmem = kWalkWarps * kStages * kStage;
 };
-// Word c of row r sits at word c ^ swz(r): the eight rows (16-bit) or the two rows and four words
-// (fp32) that one shared-memory phase reads fall into different banks.
-template <typename T>
-__device__ __forceinline__ int swz(int r) {
-    return T::kBytes == 4 ? ((r & 1) << 2) | ((r >> 1) & 3) : r & 7;
-}
+// Word c of row r sits at word c ^ swz(r): the eight rows that one ldmatrix phase reads fall into
+// different banks.
+__device__ __forceinline__ int swz(int r) { return r & 7; }
 
 }  // namespace
 
 // The warps' walk (see the head of the file).
 template <typename T, int HS>
-__global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesAttn p) {
-    using Sh = Shape<T, HS>;
+__global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_kernel(const PagesAttn p) {
+    using Sh = Shape<HS>;
     constexpr int KT = Sh::KT, C = Sh::C, NT = KT / 8;  // NT: n8 tiles of keys
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
-    const int wid = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int wid = walker_id();
     const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * (kStages * Sh::kStage);
     const int S = p.G + p.B;
     const Plan pl = plan_of(p.plan, S, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     pdl_launch_dependents();
     pdl_wait();
-    const int T_all = pl.hdr[kHdrTiles], W = pl.hdr[kHdrWarps];
+    const int T_all = pl.hdr[kHdrCost], W = pl.hdr[kHdrWarps];
     if (wid >= W) return;
-    int tile = first_of(wid, T_all, W);
-    const int tile_end = first_of(wid + 1, T_all, W);
-    if (tile >= tile_end) return;
-    int src = warp_find(pl.t0, S + 1, tile);
-    const int words = p.head_size * T::kBytes / 16;  // 16-byte words of a row that exist
+    const int x0 = first_of(wid, T_all, W), x1 = first_of(wid + 1, T_all, W);
+    if (x0 >= x1) return;
+    int src = warp_find(pl.t0, S + 1, x0), x = x0;
+    const int words = p.head_size / 8;  // 16-byte words of a row that exist
 
-    while (tile < tile_end) {
-        const int kt = pl.kt[src];
-        if (kt == 0 || tile >= pl.t0[src + 1]) {  // an empty source, or past this one
-            ++src;
-            continue;
-        }
-        const int local = tile - pl.t0[src], item = local / kt, k_first = local - item * kt;
-        const int k_end = min(kt, k_first + (tile_end - tile));
-        const int rows = pl.rows[src], row0 = pl.row0[src], key0 = pl.key0[src], key1 = pl.key1[src];
-        const int tiles_m = cdiv(rows * gq, kM), kvh = item / tiles_m, m0 = (item - kvh * tiles_m) * kM;
-        const int head0 = first_head(kvh, p.n_heads, p.n_kv_heads);
-        const int nh = first_head(kvh + 1, p.n_heads, p.n_kv_heads) - head0;
-        const int sq = p.seqs ? p.seqs[row0] : row0;
-        const int *table = p.table + (size_t)sq * p.max_pages;
-        const char *kb = p.k + kvh * p.head_stride, *vb = p.v + kvh * p.head_stride;
-
-        // place of this lane's key of a tile (lane < KT), -1 past the end
-        auto place = [&](int ktile) -> long long {
-            const int key = key0 + ktile * KT + lane;
-            if (lane >= KT || key >= key1) return -1;
-            const int pg = key / p.page_size, page = table[pg];
-            if (page < 0 || page >= p.n_pages) {
-                atomicOr(p.err, L2_DEV_ERR_BOUNDS);
-                return -1;
-            }
-            return page * p.page_stride + (key - pg * p.page_size) * p.row_stride;
-        };
-        auto fetch = [&](int stage, long long off) {
+    WalkItem w;
+    while (walk_item(p, pl, src, x, x1, gq, w)) {
+        const char *kb = p.k + w.kvh * p.head_stride, *vb = p.v + w.kvh * p.head_stride;
+        // this lane's key of tile i of the item's share
+        auto key_of = [&](int i) { return lane < KT && i < w.n_tiles ? w.key0 + (w.k_first + i) * KT + lane : w.key1; };
+        auto fetch = [&](int i, int page) {
+            const int stage = i % kStages;
+            const long long off = walk_place(p, w, key_of(i), page);
             const uint32_t ks = ring + stage * Sh::kStage, vs = ks + KT * Sh::kRow;
             constexpr int RP = C >= 32 ? 1 : 32 / C;  // rows one instruction covers
             const int c = lane % C, rr = C >= 32 ? 0 : lane / C;
@@ -336,7 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
                 const int r = r0 + rr;
                 const long long o = __shfl_sync(0xffffffffu, off, r);
                 const bool on = o >= 0 && c < words;
-                const uint32_t d = r * Sh::kRow + ((c ^ swz<T>(r)) << 4);
+                const uint32_t d = r * Sh::kRow + ((c ^ swz(r)) << 4);
                 const long long so = on ? o + (c << 4) : 0;
                 cp_async16(ks + d, kb + so, on);
                 cp_async16(vs + d, vb + so, on);
@@ -344,26 +294,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
             cp_commit();
         };
 
-        // queries of the item: pair m = (row r, head j), m = r * gq + j
-        auto q_ptr = [&](int m) -> const char * {
-            const int r = m / gq, j = m - r * gq;
-            return r < rows && j < nh ? p.q + (row0 + r) * p.q_row + (head0 + j) * p.q_head : nullptr;
-        };
-        long long off = place(k_first);
-        int n_tiles = k_end - k_first;
+        const int n_tiles = w.n_tiles, k_first = w.k_first;
+        int page = walk_page(p, w, key_of(0)), next = walk_page(p, w, key_of(1));
         // fill the ring
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
-            if (s < n_tiles) {
-                const long long nx = s + 1 < n_tiles ? place(k_first + s + 1) : -1;
-                fetch(s, off);
-                off = nx;
-            } else {
-                cp_commit();
-            }
+            fetch(s, page);
+            page = next;
+            next = walk_page(p, w, key_of(s + 2));
         }
 
-        const char *qa = q_ptr(m0 + g4), *qb = q_ptr(m0 + g4 + 8);
+        const char *qa = walk_query(p, w, g4, gq), *qb = walk_query(p, w, g4 + 8, gq);
         float m_run[2] = {-CUDART_INF_F, -CUDART_INF_F}, l_run[2] = {0.f, 0.f};
         float o[HS / 8][4];
 #pragma unroll
@@ -371,35 +312,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
         // 16-bit: the A fragments of all K steps; fp32: the lane's query values
-        constexpr int QR = T::kBytes == 2 ? HS / 16 * 4 : HS / 2;
+        constexpr int QR = HS / 16 * 4;
         uint32_t qf[QR];
-        if constexpr (T::kBytes == 2) {
 #pragma unroll
-            for (int ks = 0; ks < HS / 16; ++ks) {
-                const int d0 = ks * 16 + 2 * t4, d1 = d0 + 8;
-                qf[4 * ks] = qa && d0 < p.head_size ? *reinterpret_cast<const uint32_t *>(qa + 2 * d0) : 0u;
-                qf[4 * ks + 1] = qb && d0 < p.head_size ? *reinterpret_cast<const uint32_t *>(qb + 2 * d0) : 0u;
-                qf[4 * ks + 2] = qa && d1 < p.head_size ? *reinterpret_cast<const uint32_t *>(qa + 2 * d1) : 0u;
-                qf[4 * ks + 3] = qb && d1 < p.head_size ? *reinterpret_cast<const uint32_t *>(qb + 2 * d1) : 0u;
-            }
-        } else {
-            // steps 2i, 2i + 1 of 8 take dimensions 16 i + 4 t4 + {0, 1} and {2, 3}: one 16-byte read
-#pragma unroll
-            for (int i = 0; i < HS / 16; ++i) {
-                const int d = 16 * i + 4 * t4;
-                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                const float4 a = qa && d < p.head_size ? *reinterpret_cast<const float4 *>(qa + 4 * d) : z;
-                const float4 b = qb && d < p.head_size ? *reinterpret_cast<const float4 *>(qb + 4 * d) : z;
-                qf[8 * i] = __float_as_uint(a.x);
-                qf[8 * i + 1] = __float_as_uint(b.x);
-                qf[8 * i + 2] = __float_as_uint(a.y);
-                qf[8 * i + 3] = __float_as_uint(b.y);
-                qf[8 * i + 4] = __float_as_uint(a.z);
-                qf[8 * i + 5] = __float_as_uint(b.z);
-                qf[8 * i + 6] = __float_as_uint(a.w);
-                qf[8 * i + 7] = __float_as_uint(b.w);
-            }
+        for (int ks = 0; ks < HS / 16; ++ks) {
+            const int d0 = ks * 16 + 2 * t4, d1 = d0 + 8;
+            qf[4 * ks] = qa && d0 < p.head_size ? *reinterpret_cast<const uint32_t *>(qa + 2 * d0) : 0u;
+            qf[4 * ks + 1] = qb && d0 < p.head_size ? *reinterpret_cast<const uint32_t *>(qb + 2 * d0) : 0u;
+            qf[4 * ks + 2] = qa && d1 < p.head_size ? *reinterpret_cast<const uint32_t *>(qa + 2 * d1) : 0u;
+            qf[4 * ks + 3] = qb && d1 < p.head_size ? *reinterpret_cast<const uint32_t *>(qb + 2 * d1) : 0u;
         }
+    
 
 #pragma unroll 1
         for (int it = 0; it < n_tiles; ++it) {
@@ -407,9 +330,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
             __syncwarp();
             // the next tile goes into the stage read one step ago
             if (it + kStages - 1 < n_tiles) {
-                const long long nx = it + kStages < n_tiles ? place(k_first + it + kStages) : -1;
-                fetch((it + kStages - 1) % kStages, off);
-                off = nx;
+                fetch(it + kStages - 1, page);
+                page = next;
+                next = walk_page(p, w, key_of(it + kStages + 1));
             } else {
                 cp_commit();
             }
@@ -419,45 +342,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
-            if constexpr (T::kBytes == 2) {
-                // lane's ldmatrix row: key (lane & 7) of the n8 tile, word 2 kpair + lane / 8
+            // lane's ldmatrix row: key (lane & 7) of the n8 tile, word 2 kpair + lane / 8
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int key = 8 * n + (lane & 7);
+            for (int n = 0; n < NT; ++n) {
+                const int key = 8 * n + (lane & 7);
 #pragma unroll
-                    for (int c = 0; c < C; c += 4) {
-                        uint32_t b[4];
-                        ldsm4(ks_base + key * Sh::kRow + (((c + (lane >> 3)) ^ swz<T>(key)) << 4), b);
-                        T::mma(s[n], qf + 2 * c, b[0], b[1]);
-                        T::mma(s[n], qf + 2 * c + 4, b[2], b[3]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < HS / 16; ++i) {
-                    uint32_t qh[8], ql[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) split_tf32(__uint_as_float(qf[8 * i + j]), qh[j], ql[j]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const int key = 8 * n + g4;
-                        uint32_t x[4], h[4], l[4];
-                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(ks_base + key * Sh::kRow + (((4 * i + t4) ^ swz<T>(key)) << 4)));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) split_tf32(__uint_as_float(x[j]), h[j], l[j]);
-#pragma unroll
-                        for (int st = 0; st < 2; ++st) {
-                            mma_tf32_16x8x8(s[n], ql + 4 * st, h[2 * st], h[2 * st + 1]);
-                            mma_tf32_16x8x8(s[n], qh + 4 * st, l[2 * st], l[2 * st + 1]);
-                            mma_tf32_16x8x8(s[n], qh + 4 * st, h[2 * st], h[2 * st + 1]);
-                        }
-                    }
+                for (int c = 0; c < C; c += 4) {
+                    uint32_t b[4];
+                    ldsm4(ks_base + key * Sh::kRow + (((c + (lane >> 3)) ^ swz(key)) << 4), b);
+                    T::mma(s[n], qf + 2 * c, b[0], b[1]);
+                    T::mma(s[n], qf + 2 * c + 4, b[2], b[3]);
                 }
             }
+        
             // scale, mask keys past the end, running max
-            const int left = key1 - key0 - (k_first + it) * KT;
+            const int left = w.key1 - w.key0 - (k_first + it) * KT;
             float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -487,86 +386,42 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
                 }
             l_run[0] = l_run[0] * corr[0] + sum[0];
             l_run[1] = l_run[1] * corr[1] + sum[1];
-            if constexpr (T::kBytes == 2) {
 #pragma unroll
-                for (int i = 0; i < HS / 8; ++i) {
-                    o[i][0] *= corr[0];
-                    o[i][1] *= corr[0];
-                    o[i][2] *= corr[1];
-                    o[i][3] *= corr[1];
+            for (int i = 0; i < HS / 8; ++i) {
+                o[i][0] *= corr[0];
+                o[i][1] *= corr[0];
+                o[i][2] *= corr[1];
+                o[i][3] *= corr[1];
+            }
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk) {
+                // weights as A fragments: hi and what it leaves
+                uint32_t ph[4], plo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = s[2 * kk + (j >> 1)][2 * (j & 1)], y = s[2 * kk + (j >> 1)][2 * (j & 1) + 1];
+                    ph[j] = T::pack(x, y);
+                    const float2 back = T::unpack(ph[j]);
+                    plo[j] = T::pack(x - back.x, y - back.y);
                 }
+                const int key = 16 * kk + (lane & 15);
 #pragma unroll
-                for (int kk = 0; kk < KT / 16; ++kk) {
-                    // weights as A fragments: hi and what it leaves
-                    uint32_t ph[4], plo[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = s[2 * kk + (j >> 1)][2 * (j & 1)], y = s[2 * kk + (j >> 1)][2 * (j & 1) + 1];
-                        ph[j] = T::pack(x, y);
-                        const float2 back = T::unpack(ph[j]);
-                        plo[j] = T::pack(x - back.x, y - back.y);
-                    }
-                    const int key = 16 * kk + (lane & 15);
-#pragma unroll
-                    for (int c = 0; c < C; c += 2) {
-                        uint32_t b[4];
-                        ldsm4t(vs_base + key * Sh::kRow + (((c + (lane >> 4)) ^ swz<T>(key)) << 4), b);
-                        T::mma(o[c], ph, b[0], b[1]);
-                        T::mma(o[c], plo, b[0], b[1]);
-                        T::mma(o[c + 1], ph, b[2], b[3]);
-                        T::mma(o[c + 1], plo, b[2], b[3]);
-                    }
-                }
-            } else {
-                // n8 tile 4 i + j holds dimensions 32 i + 4 c(g4) + j, c(g) = the word that keeps a phase's
-                // eight reads in different banks
-                const int cg = ((g4 & 1) << 2) | (g4 >> 1);
-                uint32_t ph[NT][4], plo[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    split_tf32(s[n][0], ph[n][0], plo[n][0]);
-                    split_tf32(s[n][2], ph[n][1], plo[n][1]);
-                    split_tf32(s[n][1], ph[n][2], plo[n][2]);
-                    split_tf32(s[n][3], ph[n][3], plo[n][3]);
-                }
-#pragma unroll
-                for (int i = 0; i < HS / 32; ++i) {
-                    float acc[4][4] = {};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        uint32_t x[2][4];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = 8 * n + 2 * t4 + e;
-                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                         : "=r"(x[e][0]), "=r"(x[e][1]), "=r"(x[e][2]), "=r"(x[e][3])
-                                         : "r"(vs_base + key * Sh::kRow + (((8 * i + cg) ^ swz<T>(key)) << 4)));
-                        }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t h0, l0, h1, l1;
-                            split_tf32(__uint_as_float(x[0][j]), h0, l0);
-                            split_tf32(__uint_as_float(x[1][j]), h1, l1);
-                            mma_tf32_16x8x8(acc[j], plo[n], h0, h1);
-                            mma_tf32_16x8x8(acc[j], ph[n], l0, l1);
-                            mma_tf32_16x8x8(acc[j], ph[n], h0, h1);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        o[4 * i + j][0] = fmaf(o[4 * i + j][0], corr[0], acc[j][0]);
-                        o[4 * i + j][1] = fmaf(o[4 * i + j][1], corr[0], acc[j][1]);
-                        o[4 * i + j][2] = fmaf(o[4 * i + j][2], corr[1], acc[j][2]);
-                        o[4 * i + j][3] = fmaf(o[4 * i + j][3], corr[1], acc[j][3]);
-                    }
+                for (int c = 0; c < C; c += 2) {
+                    uint32_t b[4];
+                    ldsm4t(vs_base + key * Sh::kRow + (((c + (lane >> 4)) ^ swz(key)) << 4), b);
+                    T::mma(o[c], ph, b[0], b[1]);
+                    T::mma(o[c], plo, b[0], b[1]);
+                    T::mma(o[c + 1], ph, b[2], b[3]);
+                    T::mma(o[c + 1], plo, b[2], b[3]);
                 }
             }
+        
             __syncwarp();  // the stage is read before the next fetch into it
         }
         cp_wait<0>();
         __syncwarp();
         // the part: (m, l) and the sums of the item's pairs
-        const int slot = pl.i0[src] + item + wid;
+        const int slot = pl.i0[w.src] + w.item + wid;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float l = l_run[r];
@@ -576,26 +431,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_pages_kernel(const PagesA
             if (!(r ? qb : qa) || slot >= p.max_parts) continue;
             if (t4 == 0) reinterpret_cast<float2 *>(p.ws_ml)[(size_t)slot * kM + mi] = make_float2(m_run[r], l);
             float *dst = p.ws_acc + ((size_t)slot * kM + mi) * p.head_size;
-            if constexpr (T::kBytes == 2) {
 #pragma unroll
-                for (int i = 0; i < HS / 8; ++i) {
-                    const int d = 8 * i + 2 * t4;
-                    if (d < p.head_size) *reinterpret_cast<float2 *>(dst + d) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-                }
-            } else {
-                // columns 2 t4, 2 t4 + 1 of n8 tile 4 i + j are dimensions 32 i + 4 c(2 t4 + e) + j
-#pragma unroll
-                for (int i = 0; i < HS / 32; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int gg = 2 * t4 + e, d = 32 * i + 4 * (((gg & 1) << 2) | (gg >> 1));
-                        if (d < p.head_size)
-                            *reinterpret_cast<float4 *>(dst + d) =
-                                make_float4(o[4 * i][2 * r + e], o[4 * i + 1][2 * r + e], o[4 * i + 2][2 * r + e], o[4 * i + 3][2 * r + e]);
-                    }
+            for (int i = 0; i < HS / 8; ++i) {
+                const int d = 8 * i + 2 * t4;
+                if (d < p.head_size) *reinterpret_cast<float2 *>(dst + d) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
             }
+        
         }
-        tile += n_tiles;
     }
 }
 
@@ -605,7 +447,7 @@ constexpr int kMergeThreads = 128;
 template <typename T>
 __device__ __forceinline__ void store_out(char *o, int d, float4 v);
 template <>
-__device__ __forceinline__ void store_out<TF32>(char *o, int d, float4 v) {
+__device__ __forceinline__ void store_out<float>(char *o, int d, float4 v) {
     *reinterpret_cast<float4 *>(o + 4 * d) = v;
 }
 template <>
@@ -634,7 +476,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
     const bool on = d < p.head_size;
     pdl_wait();
     if (!pl.hdr[kHdrOk]) return;
-    const int T_all = pl.hdr[kHdrTiles], W = pl.hdr[kHdrWarps];
+    const int T_all = pl.hdr[kHdrCost], W = pl.hdr[kHdrWarps];
     int grp = -1;
     if (p.G) {
         int lo = 0, hi = p.G;
@@ -686,10 +528,13 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
         any = true;
         const int mi = (b - pl.row0[s]) * gq + j, tiles_m = cdiv(pl.rows[s] * gq, kM);
         const int item = kvh * tiles_m + mi / kM;
-        const int u0 = pl.t0[s] + item * kt;
-        const int w0 = walker_of(u0, T_all, W), w1 = walker_of(u0 + kt - 1, T_all, W);
+        const int cost = pl.cost[s], u0 = pl.t0[s] + item * kt * cost;
+        const int w0 = walker_of(u0, T_all, W), w1 = walker_of(u0 + (kt - 1) * cost, T_all, W);
         const int slot0 = pl.i0[s] + item;
         for (int w = w0 + ((warp - seen) & 3); w <= w1; w += 4) {
+            // a walker whose range is narrower than a tile may hold none of it
+            const int lo = max(u0, first_of(w, T_all, W)), hi = min(u0 + kt * cost, first_of(w + 1, T_all, W));
+            if (cdiv(lo - u0, cost) >= cdiv(hi - u0, cost)) continue;
             const size_t at = (size_t)(slot0 + w) * kM + (mi % kM);
             take(reinterpret_cast<const float2 *>(p.ws_ml)[at], p.ws_acc + at * p.head_size);
         }
@@ -725,19 +570,18 @@ namespace {
 
 template <typename T, int HS>
 cudaError_t launch_walk(const PagesAttn &p, int grid, cudaLaunchConfig_t cfg) {
-    using Sh = Shape<T, HS>;
+    using Sh = Shape<HS>;
     auto fn = attn_pages_kernel<T, HS>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(kWalkWarps * 32);
     cfg.dynamicSmemBytes = Sh::kSmem;
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 int tile_keys(int dtype, int hs) {
-    if (dtype == L2_F32) return hs <= 32 ? 32 : hs <= 64 ? 16 : 8;
-    return hs <= 64 ? 32 : 16;
+    return dtype == L2_F32 ? attn_pages_f32_tile(hs) : hs <= 64 ? Shape<64>::KT : Shape<128>::KT;
 }
 
 int max_items(int B, int G, int n_heads, int n_kv_heads) {
@@ -760,7 +604,7 @@ struct WsLayout {
 };
 WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms) {
     WsLayout w;
-    w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * kWarps;
+    w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * kWalkWarps;
     const size_t tc = G ? tc_part_rows(B, n_heads, n_kv_heads, num_sms) : 0;
     w.plan = 0;
     w.ml = w.plan + align256(plan_ints(B + G, G) * 4);
@@ -802,9 +646,7 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     if (p.tc && (e = launch_attn_pages_tc(p, num_sms, cfg)) != cudaSuccess) return e;
     const int hs = p.head_size;
     if (p.dtype == L2_F32)
-        e = hs <= 32   ? launch_walk<TF32, 32>(p, num_sms, cfg)
-            : hs <= 64 ? launch_walk<TF32, 64>(p, num_sms, cfg)
-                       : launch_walk<TF32, 128>(p, num_sms, cfg);
+        e = launch_attn_pages_f32(p, num_sms, cfg);
     else if (p.dtype == L2_BF16)
         e = hs <= 64 ? launch_walk<TBf16, 64>(p, num_sms, cfg) : launch_walk<TBf16, 128>(p, num_sms, cfg);
     else
@@ -813,7 +655,7 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     cfg.gridDim = dim3(p.B * p.n_heads);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    if (p.dtype == L2_F32) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<TF32>, p);
+    if (p.dtype == L2_F32) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<float>, p);
     if (p.dtype == L2_BF16) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<TBf16>, p);
     return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<TF16>, p);
 }

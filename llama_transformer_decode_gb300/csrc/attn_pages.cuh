@@ -8,15 +8,16 @@
 
 namespace l2 {
 
-constexpr int kM = 16;      // (row, head) pairs of a warp's item
+constexpr int kWalkWarps = 8;  // warps of a block of the walking kernels, one block per SM
+constexpr int kM = 16;         // (row, head) pairs of a warp's item
 constexpr int kTcKeys = 128;  // keys of a tensor-core tile
 constexpr int kTcRows = 128;  // pairs of a tensor-core slot; an item has up to two slots' worth
 
-// Plan: a header; per source of the warps (S = G + B) its first tile, first item, tiles per item, key range and
-// rows; per group, for the tensor-core kernel, its first tile, tiles per item and first row of its parts.
-enum { kHdrTiles = 0, kHdrWarps = 1, kHdrOk = 2, kHdrTcTiles = 3, kHdrTcCtas = 4, kHdrInts = 16 };
+// Plan: a header; per source of the warps (S = G + B) the cost before it, its first item, tiles per item, cost of a
+// tile, key range and rows; per group, for the tensor-core kernel, its first tile, tiles per item and first row of its parts.
+enum { kHdrCost = 0, kHdrWarps = 1, kHdrOk = 2, kHdrTcTiles = 3, kHdrTcCtas = 4, kHdrInts = 16 };
 struct Plan {
-    int *hdr, *t0, *i0, *kt, *key0, *key1, *row0, *rows;
+    int *hdr, *t0, *i0, *kt, *cost, *key0, *key1, *row0, *rows;
     int *tc_t0, *tc_kt, *tc_r0;
 };
 __host__ __device__ inline Plan plan_of(int *base, int S, int G) {
@@ -25,7 +26,8 @@ __host__ __device__ inline Plan plan_of(int *base, int S, int G) {
     p.t0 = base + kHdrInts;
     p.i0 = p.t0 + S + 1;
     p.kt = p.i0 + S + 1;
-    p.key0 = p.kt + S;
+    p.cost = p.kt + S;
+    p.key0 = p.cost + S;
     p.key1 = p.key0 + S;
     p.row0 = p.key1 + S;
     p.rows = p.row0 + S;
@@ -35,7 +37,7 @@ __host__ __device__ inline Plan plan_of(int *base, int S, int G) {
     return p;
 }
 __host__ __device__ inline size_t plan_ints(int S, int G) {
-    return (kHdrInts + 2 * (size_t)(S + 1) + 5 * (size_t)S + 3 * (size_t)G + 1 + 63) / 64 * 64;
+    return (kHdrInts + 2 * (size_t)(S + 1) + 6 * (size_t)S + 3 * (size_t)G + 1 + 63) / 64 * 64;
 }
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -44,7 +46,7 @@ __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) 
 __host__ __device__ __forceinline__ int heads_per_kv(int H, int KV) { return (H + KV - 1) / KV; }
 __device__ __forceinline__ int first_head(int g, int H, int KV) { return (g * H + KV - 1) / KV; }
 
-// T tiles are cut evenly over W walkers: walker w takes tiles [first_of(w), first_of(w + 1)).
+// T tiles (or units of cost) are cut evenly over W walkers: walker w takes [first_of(w), first_of(w + 1)).
 __device__ __forceinline__ int first_of(int w, int T, int W) { return (int)((long long)w * T / W); }
 __device__ __forceinline__ int walker_of(int tile, int T, int W) { return (int)((((long long)tile + 1) * W + T - 1) / T - 1); }
 
@@ -60,6 +62,10 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n) {  // of all runs of
     return 2 * kTcRows * full + tc_run_rows(n - 2 * kTcRows * full);
 }
 
+// Walkers that are warps: neighbours in the numbering sit in different blocks, so that a stretch of costlier tiles
+// does not fall on one SM.
+__device__ __forceinline__ int walker_id() { return (threadIdx.x >> 5) * gridDim.x + blockIdx.x; }
+
 // The last entry i of an ascending list a[0 .. n) (a[0] <= x) with a[i] <= x, found by a whole warp.
 __device__ __forceinline__ int warp_find(const int *a, int n, int x) {
     int lo = 0, hi = n;
@@ -70,6 +76,86 @@ __device__ __forceinline__ int warp_find(const int *a, int n, int x) {
         hi = hi < lo + step ? hi : lo + step;
     }
     return lo;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool on) {
+    const int n = on ? 16 : 0;  // 0: the 16 bytes are filled with zeros, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Cost of a tile of an item of n pairs, in quarters of reading it.  16-bit: reading bounds every size.  fp32 FMAs take
+// over from 8 pairs on; measured on GB300, 1 GB of suffixes of head size 128 / 64: 166 / 167 us at 1 pair, 174 / 167 at
+// 4, 198 / 198 at 8, 271 / 279 at 16.
+constexpr int kCostUnit = 4;
+__host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : 7; }
+
+// key / page_size; page_shift is its logarithm where it is a power of two, else -1.
+__device__ __forceinline__ int page_of(const PagesAttn &p, int key) {
+    return p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+}
+
+// One item's share of a walker's range, for the kernels whose walkers are warps.
+struct WalkItem {
+    int src, item, k_first, n_tiles;          // source, item within it, tiles k_first .. k_first + n_tiles - 1
+    int row0, key0, key1, head0, nh, kvh, m0;  // rows, keys, query heads head0 .. head0 + nh - 1, first pair
+    int pairs;                                 // pairs of the item
+    const int *table;                          // page table its keys are found through
+};
+// The item whose tile starts at cost x or next after it (a tile belongs to the walker in whose range it starts),
+// and the tiles of it that start before x1; x moves behind them, src past finished sources.  False: no more.
+__device__ __forceinline__ bool walk_item(const PagesAttn &p, const Plan &pl, int &src, int &x, int x1, int gq, WalkItem &w) {
+    int kt, cost, i;  // i: tile of the source
+    for (;; ++src) {
+        if (x >= x1) return false;
+        kt = pl.kt[src];
+        if (kt == 0) continue;
+        cost = pl.cost[src];
+        i = cdiv(x - pl.t0[src], cost);
+        x = pl.t0[src] + i * cost;
+        if (x < pl.t0[src + 1]) break;
+    }
+    if (x >= x1) return false;
+    const int n = pl.rows[src] * gq, tiles_m = cdiv(n, kM);
+    w.src = src;
+    w.item = i / kt;
+    w.k_first = i - w.item * kt;
+    w.n_tiles = min(kt - w.k_first, cdiv(x1 - x, cost));
+    x += w.n_tiles * cost;
+    w.row0 = pl.row0[src];
+    w.key0 = pl.key0[src];
+    w.key1 = pl.key1[src];
+    w.kvh = w.item / tiles_m;
+    w.m0 = (w.item - w.kvh * tiles_m) * kM;
+    w.pairs = min(kM, n - w.m0);
+    w.head0 = first_head(w.kvh, p.n_heads, p.n_kv_heads);
+    w.nh = first_head(w.kvh + 1, p.n_heads, p.n_kv_heads) - w.head0;
+    const int sq = p.seqs ? p.seqs[w.row0] : w.row0;
+    w.table = p.table + (size_t)sq * p.max_pages;
+    return true;
+}
+// The query of pair m (row m / gq of the source, head m % gq of the KV head), or nullptr.
+__device__ __forceinline__ const char *walk_query(const PagesAttn &p, const WalkItem &w, int i, int gq) {
+    const int m = w.m0 + i, r = m / gq, j = m - r * gq;
+    return i < w.pairs && j < w.nh ? p.q + (w.row0 + r) * p.q_row + (w.head0 + j) * p.q_head : nullptr;
+}
+// A key's row is found in two steps, so that the load of the table entry is a tile old when its value is first
+// looked at: the page of `key` (0 past the item's end), and then the byte offset of the row in its KV head's pages, or
+// -1 past the end or where the table is bad.
+__device__ __forceinline__ int walk_page(const PagesAttn &p, const WalkItem &w, int key) {
+    return key < w.key1 ? w.table[page_of(p, key)] : 0;
+}
+__device__ __forceinline__ long long walk_place(const PagesAttn &p, const WalkItem &w, int key, int page) {
+    if (key >= w.key1) return -1;
+    if (page < 0 || page >= p.n_pages) {
+        atomicOr(p.err, L2_DEV_ERR_BOUNDS);
+        return -1;
+    }
+    return page * p.page_stride + (key - page_of(p, key) * p.page_size) * p.row_stride;
 }
 
 }  // namespace l2

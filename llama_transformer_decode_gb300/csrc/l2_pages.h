@@ -57,7 +57,7 @@ struct PagesAttn {
     const int *group_starts;  // [G + 1] or nullptr
     const int *prefix_lens;   // [G]
     int B, G, n_heads, n_kv_heads, head_size, page_size, max_pages, n_seqs, n_pages;
-    int dtype;
+    int dtype, page_shift;    // log2(page_size), -1 where it is no power of two
     float scale_log2;         // scale * log2(e)
     // workspace
     int *plan;
@@ -70,6 +70,10 @@ struct PagesAttn {
 // Tensor-core part of it (attn_pages_tc.cu): whether pages and type allow tiled copies of 128 keys, and the launch.
 bool attn_pages_tc_supported(const PagesAttn &p);
 cudaError_t launch_attn_pages_tc(const PagesAttn &p, int num_sms, cudaLaunchConfig_t cfg);
+
+// Its walk over fp32 caches (attn_pages_f32.cu) and the keys of one tile there.
+int attn_pages_f32_tile(int head_size);
+cudaError_t launch_attn_pages_f32(const PagesAttn &p, int num_sms, cudaLaunchConfig_t cfg);
 
 // cuTensorMapEncodeTiled, looked up once (l2_api.cu).
 void *tensor_map_encoder();
