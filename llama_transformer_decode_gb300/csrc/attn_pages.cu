@@ -31,6 +31,7 @@
 
 #include "../../include/l2.h"
 #include "attn_pages.cuh"
+#include "attn_plan.cuh"
 #include "l2_device.cuh"
 #include "l2_pages.h"
 
@@ -39,161 +40,14 @@ namespace l2 {
 namespace {
 
 constexpr int kStages = 3;     // tiles of a warp's ring
-// Fewest tiles a warp takes: below that the parts cost more to write and merge than the
-// parallel reading gains.
-constexpr int kMinTiles = 4;
-constexpr int kTcMinTiles = 4;  // the same for the tensor-core kernel's blocks (tiles of 128 keys)
 
 }  // namespace
 
-namespace {
-// Exclusive prefix sum over a block of 1024 threads; buf: 64 ints.
-__device__ __forceinline__ int block_scan_1024(int v, int *total, int *buf) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) buf[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int w = buf[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        buf[32 + lane] = w;
-    }
-    __syncthreads();
-    const int before = warp ? buf[32 + warp - 1] : 0;
-    *total = buf[63];
-    __syncthreads();
-    return before + x - v;
-}
-}  // namespace
-
-// One block: lengths of the sources and the numbering of their tiles and items.
-// With p.tc the whole tiles of a prefix that serves more than 16 pairs go to the tensor-core kernel.
-__global__ void __launch_bounds__(1024) attn_pages_plan_kernel(const PagesAttn p, int tile_keys, int num_sms) {
-    __shared__ int part[1][64], minlen[kPagesMaxCall], mintc[kPagesMaxCall], gstart[kPagesMaxCall + 1], len_s[kPagesMaxCall];
-    const int i = threadIdx.x;
-    const int S = p.G + p.B;
-    const Plan pl = plan_of(p.plan, S, p.G);
-    const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
+// The plan as a kernel of its own, for calls of more sources than a block plans for itself.
+__global__ void __launch_bounds__(kPagesMaxCall) attn_pages_plan_kernel(const PagesAttn p) {
+    __shared__ PlanScratch<kPagesMaxCall, kPagesMaxCall> sc;
     pdl_launch_dependents();
-    bool bad = false;
-    int len = 0;
-    if (i < p.B) {
-        const int s = p.seqs ? p.seqs[i] : i;
-        bad = s < 0 || s >= p.n_seqs;
-        if (!bad) len = p.lens[s];
-        bad |= len < 0 || len > (long long)p.max_pages * p.page_size;
-    }
-    len_s[i] = len;
-    if (i <= p.G) {
-        const int a = p.G ? p.group_starts[i] : 0;
-        bad |= p.G && ((i == 0 && a != 0) || (i == p.G && a != p.B) || a < 0 || a > p.B);
-        gstart[i] = a;
-    }
-    if (i == 0 && p.G == kPagesMaxCall) {  // one entry more than threads
-        gstart[p.G] = p.group_starts[p.G];
-        bad |= gstart[p.G] != p.B;
-    }
-    __syncthreads();
-    int P = 0, r0 = 0, rows = 0;
-    if (i < p.G) {
-        r0 = gstart[i];
-        rows = gstart[i + 1] - r0;
-        P = p.prefix_lens[i];
-        bad |= rows < 0 || P < 0;
-    }
-    if (__syncthreads_or(bad)) {
-        if (i == 0) {
-            atomicOr(p.err, L2_PAGES_ERR_ARGS);
-            pl.hdr[kHdrCost] = pl.hdr[kHdrTcTiles] = 0;
-            pl.hdr[kHdrWarps] = pl.hdr[kHdrTcCtas] = 1;
-            pl.hdr[kHdrOk] = 0;
-        }
-        return;
-    }
-    // a row alone has nothing to share: all its keys are its own
-    if (i < p.G) minlen[i] = rows < 2 ? 0 : P;
-    __syncthreads();
-    if (p.G && i < p.B) {
-        int lo = 0, hi = p.G;  // the group of the row: the last that starts at or before it
-        while (hi - lo > 1) {
-            const int m = (lo + hi) >> 1;
-            gstart[m] <= i ? lo = m : hi = m;
-        }
-        atomicMin(&minlen[lo], len);
-    }
-    __syncthreads();
-    // prefixes worth it go to the tensor cores in whole tiles of 128 keys; what is left of them stays here
-    int tc_tiles = 0, tc_rows = 0;
-    if (p.G) {
-        const int n = rows * gq, full = i < p.G && p.tc && n > kM ? minlen[i] / kTcKeys : 0;
-        const int tiles = full * tc_runs(n) * p.n_kv_heads, prows = full ? tc_head_rows(n) * p.n_kv_heads : 0;
-        const int tb = block_scan_1024(tiles, &tc_tiles, part[0]), rb = block_scan_1024(prows, &tc_rows, part[0]);
-        if (i < p.G) {
-            pl.tc_t0[i] = tb;
-            pl.tc_kt[i] = full;
-            pl.tc_r0[i] = rb;
-            mintc[i] = full * kTcKeys;
-        }
-        __syncthreads();
-    }
-    // sources in blocks of 1024: G prefixes, then B sequences
-    int tiles_before = 0, items_before = 0;
-    for (int s0 = 0; s0 < S; s0 += 1024) {
-        const int s = s0 + i;
-        int key0 = 0, key1 = 0, row0 = 0, n = 0;
-        if (s < p.G) {
-            key0 = mintc[s];
-            key1 = minlen[s];
-            row0 = gstart[s];
-            n = gstart[s + 1] - row0;
-        } else if (s < S) {
-            row0 = s - p.G;
-            n = 1;
-            key1 = len_s[row0];
-            int lo = 0, hi = p.G;
-            while (hi - lo > 1) {
-                const int m = (lo + hi) >> 1;
-                gstart[m] <= row0 ? lo = m : hi = m;
-            }
-            key0 = p.G ? minlen[lo] : 0;
-        }
-        const int kt = s < S ? cdiv(key1 - key0, tile_keys) : 0;
-        const int items = kt > 0 ? cdiv(n * gq, kM) * p.n_kv_heads : 0;
-        const int cost = tile_cost(p.dtype, min(n * gq, kM));
-        int tiles_here, items_here;
-        const int a = block_scan_1024(items * kt * cost, &tiles_here, part[0]), b = block_scan_1024(items, &items_here, part[0]);
-        if (s < S) {
-            pl.t0[s] = tiles_before + a;
-            pl.cost[s] = cost;
-            pl.i0[s] = items_before + b;
-            pl.kt[s] = kt;
-            pl.key0[s] = key0;
-            pl.key1[s] = key1;
-            pl.row0[s] = row0;
-            pl.rows[s] = n;
-        }
-        tiles_before += tiles_here;
-        items_before += items_here;
-    }
-    if (i == 0) {
-        pl.t0[S] = tiles_before;
-        pl.i0[S] = items_before;
-        pl.hdr[kHdrCost] = tiles_before;
-        pl.hdr[kHdrTcTiles] = tc_tiles;
-        pl.hdr[kHdrTcCtas] = max(1, min(num_sms, cdiv(tc_tiles, kTcMinTiles)));
-        if (p.G) pl.tc_t0[p.G] = tc_tiles;
-        pl.hdr[kHdrWarps] = max(1, min(num_sms * kWalkWarps, cdiv(tiles_before, kMinTiles * kCostUnit)));
-        pl.hdr[kHdrOk] = 1;
-    }
+    plan_build<kPagesMaxCall, kPagesMaxCall>(p, plan_of(p.plan, p.B, p.G), sc, true);
 }
 
 namespace {
@@ -241,7 +95,8 @@ struct Shape {
     static constexpr int C = HS * 2 / 16;         // 16-byte words a row
     static constexpr int kRow = HS * 2;
     static constexpr int kStage = 2 * KT * kRow;  // K then V
-    static constexpr int kSmem = kWalkWarps * kStages * kStage;
+    static constexpr int kRings = kWalkWarps * kStages * kStage;
+    static constexpr int kSmem = kRings + (int)kPlanSmem;
 };
 // Word c of row r sits at word c ^ swz(r): the eight rows that one ldmatrix phase reads fall into
 // different banks.
@@ -258,52 +113,27 @@ __global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_kernel(const Pa
     const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
     const int wid = walker_id();
     const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * (kStages * Sh::kStage);
-    const int S = p.G + p.B;
-    const Plan pl = plan_of(p.plan, S, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     pdl_launch_dependents();
-    pdl_wait();
+    if (p.wait_first) pdl_wait();
+    const Plan pl = plan_here<kWalkWarps * 32>(p, smem + Sh::kRings, smem, blockIdx.x == 0);
     const int T_all = pl.hdr[kHdrCost], W = pl.hdr[kHdrWarps];
-    if (wid >= W) return;
-    const int x0 = first_of(wid, T_all, W), x1 = first_of(wid + 1, T_all, W);
-    if (x0 >= x1) return;
-    int src = warp_find(pl.t0, S + 1, x0), x = x0;
+    const int x0 = wid < W ? first_of(wid, T_all, W) : 0, x1 = wid < W ? first_of(wid + 1, T_all, W) : 0;
     const int words = p.head_size / 8;  // 16-byte words of a row that exist
+    int src = 0, x = x0, done = 0;
+    WalkAhead<KT> ahead;
+    if (x0 < x1) {
+        src = warp_find(&pl.src[0].t0, sizeof(Source) / 4, p.G + p.B + 1, x0);
+        ahead.start(p, pl, src, x0, x1, gq);
+        for (int s = 0; s < kStages - 1; ++s) {
+            const uint32_t ks = ring + s * Sh::kStage;
+            walk_copy<KT, Sh::kRow>(p, pl, ahead, x1, gq, words, ks, ks + KT * Sh::kRow, swz);
+        }
+    }
 
     WalkItem w;
     while (walk_item(p, pl, src, x, x1, gq, w)) {
-        const char *kb = p.k + w.kvh * p.head_stride, *vb = p.v + w.kvh * p.head_stride;
-        // this lane's key of tile i of the item's share
-        auto key_of = [&](int i) { return lane < KT && i < w.n_tiles ? w.key0 + (w.k_first + i) * KT + lane : w.key1; };
-        auto fetch = [&](int i, int page) {
-            const int stage = i % kStages;
-            const long long off = walk_place(p, w, key_of(i), page);
-            const uint32_t ks = ring + stage * Sh::kStage, vs = ks + KT * Sh::kRow;
-            constexpr int RP = C >= 32 ? 1 : 32 / C;  // rows one instruction covers
-            const int c = lane % C, rr = C >= 32 ? 0 : lane / C;
-#pragma unroll
-            for (int r0 = 0; r0 < KT; r0 += RP) {
-                const int r = r0 + rr;
-                const long long o = __shfl_sync(0xffffffffu, off, r);
-                const bool on = o >= 0 && c < words;
-                const uint32_t d = r * Sh::kRow + ((c ^ swz(r)) << 4);
-                const long long so = on ? o + (c << 4) : 0;
-                cp_async16(ks + d, kb + so, on);
-                cp_async16(vs + d, vb + so, on);
-            }
-            cp_commit();
-        };
-
         const int n_tiles = w.n_tiles, k_first = w.k_first;
-        int page = walk_page(p, w, key_of(0)), next = walk_page(p, w, key_of(1));
-        // fill the ring
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            fetch(s, page);
-            page = next;
-            next = walk_page(p, w, key_of(s + 2));
-        }
-
         const char *qa = walk_query(p, w, g4, gq), *qb = walk_query(p, w, g4 + 8, gq);
         float m_run[2] = {-CUDART_INF_F, -CUDART_INF_F}, l_run[2] = {0.f, 0.f};
         float o[HS / 8][4];
@@ -325,18 +155,13 @@ __global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_kernel(const Pa
     
 
 #pragma unroll 1
-        for (int it = 0; it < n_tiles; ++it) {
+        for (int it = 0; it < n_tiles; ++it, ++done) {
             cp_wait<kStages - 2>();
             __syncwarp();
             // the next tile goes into the stage read one step ago
-            if (it + kStages - 1 < n_tiles) {
-                fetch(it + kStages - 1, page);
-                page = next;
-                next = walk_page(p, w, key_of(it + kStages + 1));
-            } else {
-                cp_commit();
-            }
-            const uint32_t ks_base = ring + (it % kStages) * Sh::kStage, vs_base = ks_base + KT * Sh::kRow;
+            const uint32_t nx = ring + ((done + kStages - 1) % kStages) * Sh::kStage;
+            walk_copy<KT, Sh::kRow>(p, pl, ahead, x1, gq, words, nx, nx + KT * Sh::kRow, swz);
+            const uint32_t ks_base = ring + (done % kStages) * Sh::kStage, vs_base = ks_base + KT * Sh::kRow;
             float s[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -418,10 +243,8 @@ __global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_kernel(const Pa
         
             __syncwarp();  // the stage is read before the next fetch into it
         }
-        cp_wait<0>();
-        __syncwarp();
         // the part: (m, l) and the sums of the item's pairs
-        const int slot = pl.i0[w.src] + w.item + wid;
+        const int slot = w.slot + wid;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float l = l_run[r];
@@ -439,6 +262,9 @@ __global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_kernel(const Pa
         
         }
     }
+    cp_wait<0>();
+    // the merge waits for this kernel alone: it ends after the tensor-core kernel before it
+    if (p.tc && threadIdx.x == 0) pdl_wait();
 }
 
 namespace {
@@ -458,125 +284,142 @@ template <>
 __device__ __forceinline__ void store_out<TF16>(char *o, int d, float4 v) {
     *reinterpret_cast<uint2 *>(o + 2 * d) = make_uint2(TF16::pack(v.x, v.y), TF16::pack(v.z, v.w));
 }
+
+// Parts of one (row, head) that a source's walkers left.
+struct PartRange {
+    int u0, kt, cost, w0, n, slot, pair;
+};
 }  // namespace
 
-// One block per (row, query head): its prefix's parts, then its own, merged in key order by four warps
-// (part i goes to warp i % 4) and then over the warps in order.
+// One warp per (row, query head): the parts of its prefix and of its own keys, in key order.  Lanes take a part each
+// for (m, l), so all weights are known after one round of loads; then the warp adds the parts' sums, LP
+// lanes to a part.
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const PagesAttn p) {
-    __shared__ float sm[4], sl[4];
-    __shared__ float4 sa[4][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = blockIdx.x / p.n_heads, h = blockIdx.x - b * p.n_heads;
-    const int S = p.G + p.B;
-    const Plan pl = plan_of(p.plan, S, p.G);
+    const int lane = threadIdx.x & 31;
+    const int bh = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    const int b = bh / p.n_heads, h = bh - b * p.n_heads;
+    const Plan pl = plan_of(p.plan, p.B, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const int kvh = (int)((long long)h * p.n_kv_heads / p.n_heads), j = h - first_head(kvh, p.n_heads, p.n_kv_heads);
-    const int d = 4 * lane;
-    const bool on = d < p.head_size;
     pdl_wait();
-    if (!pl.hdr[kHdrOk]) return;
+    if (b >= p.B || !pl.hdr[kHdrOk]) return;
     const int T_all = pl.hdr[kHdrCost], W = pl.hdr[kHdrWarps];
-    int grp = -1;
-    if (p.G) {
-        int lo = 0, hi = p.G;
-        while (hi - lo > 1) {
-            const int m = (lo + hi) >> 1;
-            p.group_starts[m] <= b ? lo = m : hi = m;
+    const int grp = p.G ? pl.group[b] : 0;
+    auto range = [&](int s) {
+        PartRange r = {};
+        const int4 a = *reinterpret_cast<const int4 *>(&pl.src[s].t0), c = *reinterpret_cast<const int4 *>(&pl.src[s].key0);
+        if (a.z) {
+            const int mi = (b - c.z) * gq + j, item = kvh * cdiv(c.w * gq, kM) + mi / kM;
+            r.kt = a.z;
+            r.cost = a.w;
+            r.u0 = a.x + item * a.z * a.w;
+            r.w0 = walker_of(r.u0, T_all, W);
+            r.n = walker_of(r.u0 + (a.z - 1) * a.w, T_all, W) - r.w0 + 1;
+            r.slot = a.y + item;
+            r.pair = mi % kM;
         }
-        grp = lo;
+        return r;
+    };
+    const PartRange own = range(p.G + b);
+    PartRange rest = {};
+    int tc_n = 0, tc_w0 = 0, tc_base = 0, tc_rows = 0, tc_per = 1;
+    if (p.G) {
+        rest = range(grp);
+        const int kt = pl.tc_kt[grp];
+        if (kt) {
+            const int row0 = pl.src[grp].row0, n = pl.src[grp].rows * gq, mi = (b - row0) * gq + j;
+            const int run = mi / (2 * kTcRows), r = mi - run * 2 * kTcRows;
+            const int u0 = pl.tc_t0[grp] + (kvh * tc_runs(n) + run) * kt, Tt = pl.hdr[kHdrTcTiles], Wt = pl.hdr[kHdrTcCtas];
+            tc_rows = min(2 * kTcRows, n - run * 2 * kTcRows);
+            tc_per = tc_rows > kTcRows ? 1 : 2;  // parts a block leaves of this row
+            tc_w0 = walker_of(u0, Tt, Wt);
+            tc_n = (walker_of(u0 + kt - 1, Tt, Wt) - tc_w0 + 1) * tc_per;
+            tc_base = pl.tc_r0[grp] + kvh * tc_head_rows(n) + run * 2 * kTcRows + r;
+        }
     }
+    const int n = tc_n + rest.n + own.n;
+    const int LP = p.head_size > 64 ? 32 : p.head_size > 32 ? 16 : 8;  // lanes of a part's sums
+    const int sub = lane / LP, d = 4 * (lane % LP), per = 32 / LP;
+    const bool on = d < p.head_size;
     float m = -CUDART_INF_F, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool any = false;
-    int seen = 0;
-    // one part into the warp's running (m, l, a); a part without keys has m = -inf
-    auto take = [&](float2 ml, const float *acc) {
-        if (ml.x == -CUDART_INF_F && ml.y == 0.f) return;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) v = *reinterpret_cast<const float4 *>(acc + d);
-        const float mn = fmaxf(m, ml.x), base = mn == -CUDART_INF_F ? 0.f : mn;
-        const float c0 = exp2f(m - base), c1 = exp2f(ml.x - base);
-        a.x = a.x * c0 + v.x * c1;
-        a.y = a.y * c0 + v.y * c1;
-        a.z = a.z * c0 + v.z * c1;
-        a.w = a.w * c0 + v.w * c1;
-        l = l * c0 + ml.y * c1;
-        m = mn;
-    };
-    if (grp >= 0 && pl.tc_kt[grp]) {
-        const int kt = pl.tc_kt[grp], n = pl.rows[grp] * gq, mi = (b - pl.row0[grp]) * gq + j;
-        const int run = mi / (2 * kTcRows), r = mi - run * 2 * kTcRows, rows = min(2 * kTcRows, n - run * 2 * kTcRows);
-        const int u0 = pl.tc_t0[grp] + (kvh * tc_runs(n) + run) * kt;
-        const int Tt = pl.hdr[kHdrTcTiles], Wt = pl.hdr[kHdrTcCtas];
-        const int w0 = walker_of(u0, Tt, Wt), w1 = walker_of(u0 + kt - 1, Tt, Wt);
-        const int base = pl.tc_r0[grp] + kvh * tc_head_rows(n) + run * 2 * kTcRows + r;
-        const int per = rows > kTcRows ? 1 : 2;  // parts a walker leaves of this row
-        any = true;
-        for (int e = warp; e < (w1 - w0 + 1) * per; e += 4) {
-            const int w = w0 + e / per, sl2 = e - (w - w0) * per;
-            const size_t at = (size_t)(base + 2 * kTcRows * w + sl2 * rows);
-            take(reinterpret_cast<const float2 *>(p.tc_ml)[at], p.tc_acc + at * p.head_size);
-        }
-        seen = ((w1 - w0 + 1) * per) & 3;
-    }
-    for (int which = 0; which < 2; ++which) {
-        const int s = which ? p.G + b : grp;
-        if (s < 0) continue;
-        const int kt = pl.kt[s];
-        if (kt == 0) continue;
-        any = true;
-        const int mi = (b - pl.row0[s]) * gq + j, tiles_m = cdiv(pl.rows[s] * gq, kM);
-        const int item = kvh * tiles_m + mi / kM;
-        const int cost = pl.cost[s], u0 = pl.t0[s] + item * kt * cost;
-        const int w0 = walker_of(u0, T_all, W), w1 = walker_of(u0 + (kt - 1) * cost, T_all, W);
-        const int slot0 = pl.i0[s] + item;
-        for (int w = w0 + ((warp - seen) & 3); w <= w1; w += 4) {
+    for (int e0 = 0; e0 < n; e0 += 32) {
+        const int e = e0 + lane;
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        const float *acc = nullptr;
+        if (e < tc_n) {
+            const int wi = e / tc_per;
+            const size_t at = (size_t)(tc_base + 2 * kTcRows * (tc_w0 + wi) + (e - wi * tc_per) * tc_rows);
+            ml = reinterpret_cast<const float2 *>(p.tc_ml)[at];
+            acc = p.tc_acc + at * p.head_size;
+        } else if (e < n) {
+            const bool first = e < tc_n + rest.n;
+            const PartRange &r = first ? rest : own;
+            const int w = r.w0 + e - tc_n - (first ? 0 : rest.n);
             // a walker whose range is narrower than a tile may hold none of it
-            const int lo = max(u0, first_of(w, T_all, W)), hi = min(u0 + kt * cost, first_of(w + 1, T_all, W));
-            if (cdiv(lo - u0, cost) >= cdiv(hi - u0, cost)) continue;
-            const size_t at = (size_t)(slot0 + w) * kM + (mi % kM);
-            take(reinterpret_cast<const float2 *>(p.ws_ml)[at], p.ws_acc + at * p.head_size);
+            const int lo = max(r.u0, first_of(w, T_all, W)), hi = min(r.u0 + r.kt * r.cost, first_of(w + 1, T_all, W));
+            if (cdiv(lo - r.u0, r.cost) < cdiv(hi - r.u0, r.cost)) {
+                const size_t at = (size_t)(r.slot + w) * kM + r.pair;
+                ml = reinterpret_cast<const float2 *>(p.ws_ml)[at];
+                acc = p.ws_acc + at * p.head_size;
+            }
         }
-        seen = (seen + (w1 - w0 + 1)) & 3;
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    sa[warp][lane] = a;
-    __syncthreads();
-    if (warp) return;
-    for (int w = 1; w < 4; ++w) {
-        const float mn = fmaxf(m, sm[w]), base = mn == -CUDART_INF_F ? 0.f : mn;
-        const float c0 = exp2f(m - base), c1 = exp2f(sm[w] - base);
-        const float4 v = sa[w][lane];
-        a.x = a.x * c0 + v.x * c1;
-        a.y = a.y * c0 + v.y * c1;
-        a.z = a.z * c0 + v.z * c1;
-        a.w = a.w * c0 + v.w * c1;
-        l = l * c0 + sl[w] * c1;
+        if (ml.x == -CUDART_INF_F && ml.y == 0.f) acc = nullptr;  // a part without keys
+        float mn = fmaxf(m, ml.x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        const float base = mn == -CUDART_INF_F ? 0.f : mn;
+        const float c0 = exp2f(m - base), wt = exp2f(ml.x - base);
+        float ls = acc ? ml.y * wt : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+        l = l * c0 + ls;
         m = mn;
+        a.x *= c0;
+        a.y *= c0;
+        a.z *= c0;
+        a.w *= c0;
+        const int cnt = min(32, n - e0);
+#pragma unroll 4
+        for (int q = 0; q < cnt; q += per) {
+            const int from = min(q + sub, 31);
+            const float c1 = __shfl_sync(0xffffffffu, wt, from);
+            const float *src = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(acc), from));
+            if (q + sub < cnt && src && on) {
+                const float4 v = *reinterpret_cast<const float4 *>(src + d);
+                a.x = fmaf(v.x, c1, a.x);
+                a.y = fmaf(v.y, c1, a.y);
+                a.z = fmaf(v.z, c1, a.z);
+                a.w = fmaf(v.w, c1, a.w);
+            }
+        }
+    }
+    for (int o = 16; o >= LP; o >>= 1) {
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+        a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
     }
     // no keys at all: zeros, and a sum of nothing; all scores -inf: 0 / 0, as the formula has it
-    const float inv = any ? 1.0f / l : 0.f;
-    if (on)
+    const float inv = n ? 1.0f / l : 0.f;
+    if (on && sub == 0)
         store_out<T>(p.out + (long long)b * p.o_row + (long long)h * p.o_head, d,
-                     any ? make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
-    if (p.lse && lane == 0) p.lse[(size_t)b * p.n_heads + h] = any ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                     n ? make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
+    if (p.lse && lane == 0) p.lse[(size_t)b * p.n_heads + h] = n ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
 }
 
 namespace {
 
 template <typename T, int HS>
-cudaError_t launch_walk(const PagesAttn &p, int grid, cudaLaunchConfig_t cfg) {
-    using Sh = Shape<HS>;
+cudaError_t launch_walk(const PagesAttn &p, cudaLaunchConfig_t cfg) {
     auto fn = attn_pages_kernel<T, HS>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    static DeviceOnce once;
+    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), Shape<HS>::kSmem);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(p.num_sms);
     cfg.blockDim = dim3(kWalkWarps * 32);
-    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.dynamicSmemBytes = Shape<HS>::kSmem;
     return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
@@ -607,7 +450,7 @@ WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int
     w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * kWalkWarps;
     const size_t tc = G ? tc_part_rows(B, n_heads, n_kv_heads, num_sms) : 0;
     w.plan = 0;
-    w.ml = w.plan + align256(plan_ints(B + G, G) * 4);
+    w.ml = w.plan + align256(plan_bytes(B, G));
     w.acc = w.ml + align256(w.parts * kM * 8);
     w.tc_ml = w.acc + align256(w.parts * kM * head_size * 4);
     w.tc_acc = w.tc_ml + align256(tc * 8);
@@ -621,6 +464,7 @@ size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_s
     return ws_layout(B, G, n_heads, n_kv_heads, head_size, num_sms).bytes;
 }
 
+// Kernels of a call, each after the first launched as its predecessor's dependent: [plan] [tensor cores] warps, merge.
 cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s) {
     const WsLayout w = ws_layout(p.B, p.G, p.n_heads, p.n_kv_heads, p.head_size, num_sms);
     char *base = static_cast<char *>(ws);
@@ -630,29 +474,39 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     p.tc_ml = reinterpret_cast<float *>(base + w.tc_ml);
     p.tc_acc = reinterpret_cast<float *>(base + w.tc_acc);
     p.max_parts = (int)w.parts;
+    p.num_sms = num_sms;
+    p.tile_keys = tile_keys(p.dtype, p.head_size);
     // a prefix that serves at most 16 pairs or is shorter than a tile gains nothing there
     p.tc = p.G && p.B * heads_per_kv(p.n_heads, p.n_kv_heads) > kM && attn_pages_tc_supported(p);
+    p.plan_in_block = p.B + p.G <= kPlanInBlock;
+    p.wait_first = !p.plan_in_block && !p.tc;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(1024);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, attn_pages_plan_kernel, p, tile_keys(p.dtype, p.head_size), num_sms);
-    if (e != cudaSuccess) return e;
-    cfg.numAttrs = 1;
-    if (p.tc && (e = launch_attn_pages_tc(p, num_sms, cfg)) != cudaSuccess) return e;
+    cudaError_t e = cudaSuccess;
+    if (!p.plan_in_block) {
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(kPagesMaxCall);
+        if ((e = cudaLaunchKernelEx(&cfg, attn_pages_plan_kernel, p)) != cudaSuccess) return e;
+        cfg.numAttrs = 1;
+    }
+    if (p.tc) {
+        if ((e = launch_attn_pages_tc(p, cfg)) != cudaSuccess) return e;
+        cfg.numAttrs = 1;
+    }
     const int hs = p.head_size;
     if (p.dtype == L2_F32)
-        e = launch_attn_pages_f32(p, num_sms, cfg);
+        e = launch_attn_pages_f32(p, cfg);
     else if (p.dtype == L2_BF16)
-        e = hs <= 64 ? launch_walk<TBf16, 64>(p, num_sms, cfg) : launch_walk<TBf16, 128>(p, num_sms, cfg);
+        e = hs <= 64 ? launch_walk<TBf16, 64>(p, cfg) : launch_walk<TBf16, 128>(p, cfg);
     else
-        e = hs <= 64 ? launch_walk<TF16, 64>(p, num_sms, cfg) : launch_walk<TF16, 128>(p, num_sms, cfg);
+        e = hs <= 64 ? launch_walk<TF16, 64>(p, cfg) : launch_walk<TF16, 128>(p, cfg);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(p.B * p.n_heads);
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((p.B * p.n_heads + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
     if (p.dtype == L2_F32) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<float>, p);

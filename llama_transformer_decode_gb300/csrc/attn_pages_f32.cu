@@ -16,6 +16,7 @@
 
 #include "../../include/l2.h"
 #include "attn_pages.cuh"
+#include "attn_plan.cuh"
 #include "l2_device.cuh"
 #include "l2_pages.h"
 
@@ -34,7 +35,7 @@ struct ShapeF {
     static constexpr int kQ = kM * kRow;          // queries
     static constexpr int kS = KT * kM * 4;        // scores, then weights [key][pair]
     static constexpr int kWarp = kStagesF * kStage + kQ + kS + kM * 4;
-    static constexpr int kSmem = kWalkWarps * kWarp;
+    static constexpr int kSmem = kWalkWarps * kWarp + (int)kPlanSmem;
 };
 
 // Word c of row r sits at word c ^ swzf(r): two rows by four words, or one row by eight, fall into different banks.
@@ -75,9 +76,10 @@ __device__ __forceinline__ void lane_sums(float *v, int lane, int &first) {
 template <int N, int D>
 constexpr int kKept = N >= D ? N / D : 1;
 
-// One item of at most R pairs.
+// One item of at most R pairs, its first two tiles already under way; done: tiles the warp has computed before.
 template <int HS, int R>
-__device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, const WalkItem &w, int wid, int gq, unsigned char *ring) {
+__device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, const WalkItem &w, WalkAhead<ShapeF<HS>::KT> &ahead, int x1,
+                                         int wid, int gq, unsigned char *ring, int done) {
     using Sh = ShapeF<HS>;
     constexpr int KT = Sh::KT, C = Sh::C;
     using Sp = Split<KT, R>;
@@ -87,32 +89,6 @@ __device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, con
     float *ss = reinterpret_cast<float *>(qs + Sh::kQ), *cs = ss + Sh::kS / 4;
     auto word = [](const unsigned char *a) { return *reinterpret_cast<const float4 *>(a); };
     const int words = p.head_size / 4;
-    const char *kb = p.k + w.kvh * p.head_stride, *vb = p.v + w.kvh * p.head_stride;
-    // this lane's key of tile i of the item's share
-    auto key_of = [&](int i) { return lane < KT && i < w.n_tiles ? w.key0 + (w.k_first + i) * KT + lane : w.key1; };
-    auto fetch = [&](int i, int page) {
-        const int stage = i & 1;
-        const long long off = walk_place(p, w, key_of(i), page);
-        const uint32_t ks = smem_u32(ring) + stage * Sh::kStage, vs = ks + KT * Sh::kRow;
-        constexpr int RP = 32 / C;  // rows one instruction covers
-        const int c = lane % C, rr = lane / C;
-#pragma unroll
-        for (int r0 = 0; r0 < KT; r0 += RP) {
-            const int r = r0 + rr;
-            const long long o = __shfl_sync(0xffffffffu, off, r);
-            const bool on = o >= 0 && c < words;
-            const uint32_t d = r * Sh::kRow + ((c ^ swzf(r)) << 4);
-            const long long so = on ? o + (c << 4) : 0;
-            cp_async16(ks + d, kb + so, on);
-            cp_async16(vs + d, vb + so, on);
-        }
-        cp_commit();
-    };
-    int page = walk_page(p, w, key_of(0));
-    const int page1 = walk_page(p, w, key_of(1));
-    fetch(0, page);
-    page = walk_page(p, w, key_of(2));
-    fetch(1, page1);
     // queries
     for (int e = lane; e < R * C; e += 32) {
         const int i = e / C, c = e - i * C;
@@ -138,7 +114,7 @@ __device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, con
     for (int it = 0; it < w.n_tiles; ++it) {
         cp_wait<1>();
         __syncwarp();
-        const unsigned char *ks = ring + (it & 1) * Sh::kStage, *vs = ks + KT * Sh::kRow;
+        unsigned char *ks = ring + ((done + it) & 1) * Sh::kStage, *vs = ks + KT * Sh::kRow;
         {
             float2 s2[A][Q];
 #pragma unroll
@@ -240,18 +216,12 @@ __device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, con
             }
         }
         __syncwarp();  // the stage, scores and factors are read
-        if (it + 2 < w.n_tiles) {
-            fetch(it + 2, page);
-            page = walk_page(p, w, key_of(it + 3));
-        } else {
-            cp_commit();
-        }
+        walk_copy<KT, Sh::kRow>(p, pl, ahead, x1, gq, words, smem_u32(ks), smem_u32(vs), swzf);
     }
-    cp_wait<0>();
     // the part
 #pragma unroll
     for (int o = LP / 2; o > 0; o >>= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, o);
-    const int slot = pl.i0[w.src] + w.item + wid;
+    const int slot = w.slot + wid;
     if (slot >= p.max_parts) return;
     if (sk == 0 && sr < w.pairs) reinterpret_cast<float2 *>(p.ws_ml)[(size_t)slot * kM + sr] = make_float2(m_run, l_run);
 #pragma unroll
@@ -277,38 +247,47 @@ __global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_f32_kernel(cons
     extern __shared__ __align__(128) unsigned char smem[];
     const int wid = walker_id();
     unsigned char *ring = smem + (threadIdx.x >> 5) * ShapeF<HS>::kWarp;
-    const int S = p.G + p.B;
-    const Plan pl = plan_of(p.plan, S, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     pdl_launch_dependents();
-    pdl_wait();
+    if (p.wait_first) pdl_wait();
+    const Plan pl = plan_here<kWalkWarps * 32>(p, smem + kWalkWarps * ShapeF<HS>::kWarp, smem, blockIdx.x == 0);
     const int T_all = pl.hdr[kHdrCost], W = pl.hdr[kHdrWarps];
-    if (wid >= W) return;
-    const int x0 = first_of(wid, T_all, W), x1 = first_of(wid + 1, T_all, W);
-    if (x0 >= x1) return;
-    int src = warp_find(pl.t0, S + 1, x0), x = x0;
-    WalkItem w;
-    while (walk_item(p, pl, src, x, x1, gq, w)) {
-        if (w.pairs <= 1)
-            walk_f32<HS, 1>(p, pl, w, wid, gq, ring);
-        else if (w.pairs <= 2)
-            walk_f32<HS, 2>(p, pl, w, wid, gq, ring);
-        else if (w.pairs <= 4)
-            walk_f32<HS, 4>(p, pl, w, wid, gq, ring);
-        else if (w.pairs <= 8)
-            walk_f32<HS, 8>(p, pl, w, wid, gq, ring);
-        else
-            walk_f32<HS, 16>(p, pl, w, wid, gq, ring);
+    const int x0 = wid < W ? first_of(wid, T_all, W) : 0, x1 = wid < W ? first_of(wid + 1, T_all, W) : 0;
+    if (x0 < x1) {
+        constexpr int KT = ShapeF<HS>::KT;
+        int src = warp_find(&pl.src[0].t0, sizeof(Source) / 4, p.G + p.B + 1, x0), x = x0, done = 0;
+        WalkAhead<KT> ahead;
+        ahead.start(p, pl, src, x0, x1, gq);
+        for (int s = 0; s < kStagesF; ++s) {
+            const uint32_t ks = smem_u32(ring) + s * ShapeF<HS>::kStage;
+            walk_copy<KT, ShapeF<HS>::kRow>(p, pl, ahead, x1, gq, p.head_size / 4, ks, ks + KT * ShapeF<HS>::kRow, swzf);
+        }
+        WalkItem w;
+        while (walk_item(p, pl, src, x, x1, gq, w)) {
+            if (w.pairs <= 1)
+                walk_f32<HS, 1>(p, pl, w, ahead, x1, wid, gq, ring, done);
+            else if (w.pairs <= 2)
+                walk_f32<HS, 2>(p, pl, w, ahead, x1, wid, gq, ring, done);
+            else if (w.pairs <= 4)
+                walk_f32<HS, 4>(p, pl, w, ahead, x1, wid, gq, ring, done);
+            else if (w.pairs <= 8)
+                walk_f32<HS, 8>(p, pl, w, ahead, x1, wid, gq, ring, done);
+            else
+                walk_f32<HS, 16>(p, pl, w, ahead, x1, wid, gq, ring, done);
+            done += w.n_tiles;
+        }
     }
+    cp_wait<0>();
 }
 
 namespace {
 template <int HS>
-cudaError_t launch(const PagesAttn &p, int grid, cudaLaunchConfig_t cfg) {
+cudaError_t launch(const PagesAttn &p, cudaLaunchConfig_t cfg) {
     auto fn = attn_pages_f32_kernel<HS>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ShapeF<HS>::kSmem);
+    static DeviceOnce once;
+    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), ShapeF<HS>::kSmem);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = dim3(p.num_sms);
     cfg.blockDim = dim3(kWalkWarps * 32);
     cfg.dynamicSmemBytes = ShapeF<HS>::kSmem;
     return cudaLaunchKernelEx(&cfg, fn, p);
@@ -317,9 +296,9 @@ cudaError_t launch(const PagesAttn &p, int grid, cudaLaunchConfig_t cfg) {
 
 int attn_pages_f32_tile(int hs) { return hs <= 32 ? ShapeF<32>::KT : hs <= 64 ? ShapeF<64>::KT : ShapeF<128>::KT; }
 
-cudaError_t launch_attn_pages_f32(const PagesAttn &p, int num_sms, cudaLaunchConfig_t cfg) {
+cudaError_t launch_attn_pages_f32(const PagesAttn &p, cudaLaunchConfig_t cfg) {
     const int hs = p.head_size;
-    return hs <= 32 ? launch<32>(p, num_sms, cfg) : hs <= 64 ? launch<64>(p, num_sms, cfg) : launch<128>(p, num_sms, cfg);
+    return hs <= 32 ? launch<32>(p, cfg) : hs <= 64 ? launch<64>(p, cfg) : launch<128>(p, cfg);
 }
 
 }  // namespace l2

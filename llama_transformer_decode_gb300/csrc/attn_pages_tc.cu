@@ -32,6 +32,7 @@
 
 #include "../../include/l2.h"
 #include "attn_pages.cuh"
+#include "attn_plan.cuh"
 #include "l2_device.cuh"
 #include "l2_pages.h"
 #include "l2_tc.cuh"
@@ -59,7 +60,8 @@ struct TcShape {
     static constexpr int kBlocks = HS / 64;                  // 64-value blocks of a row
     static constexpr uint32_t kTile = kBlocks * kBlock;      // a tile of K, V or queries
     static constexpr int kStagesK = HS == 64 ? 5 : 2, kStagesV = HS == 64 ? 5 : 2;
-    static constexpr uint32_t kSmem = 1024 + 1024 + (2 + kStagesK + kStagesV) * kTile;
+    static constexpr uint32_t kTiles = (2 + kStagesK + kStagesV) * kTile;
+    static constexpr uint32_t kSmem = 1024 + 1024 + kTiles + (uint32_t)kPlanSmem;
 };
 
 struct TcFx {
@@ -169,9 +171,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
     // slot s: scores at columns 256 s (the weights over their first half), acc at 256 s + 128
     auto s_col = [&](int s) { return tmem + 256 * s; };
     auto o_col = [&](int s) { return tmem + 256 * s + 128; };
-    pdl_wait();
+    if (!p.plan_in_block) pdl_wait();
     pdl_launch_dependents();  // after the wait: the warps' kernel reads the plan without one
-    const Plan pl = plan_of(p.plan, p.G + p.B, p.G);
+    // planned over the queries' tiles, which only these threads' own writes reach before the first product
+    const Plan pl = plan_here<kTcThreads>(p, smem + 1024 + Sh::kTiles, qs, false);
     const int T = pl.hdr[kHdrTcTiles], W = pl.hdr[kHdrTcCtas];
     const int u_begin = (int)blockIdx.x < W ? first_of(blockIdx.x, T, W) : 0;
     const int u_end = (int)blockIdx.x < W ? first_of(blockIdx.x + 1, T, W) : 0;
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
     auto segment = [&](int u, int &grp, Seg &g) {
         while (u >= pl.tc_t0[grp + 1]) ++grp;
         const int kt = pl.tc_kt[grp], local = u - pl.tc_t0[grp], item = local / kt;
-        const int n = pl.rows[grp] * gq, runs = tc_runs(n);
+        const int n = pl.src[grp].rows * gq, runs = tc_runs(n);
         g.group = grp;
         g.kvh = item / runs;
         const int run = item - g.kvh * runs;
@@ -194,7 +197,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
     auto slot_tiles = [&](const Seg &g, int s) { return g.rows > kTcRows ? g.n : (g.n + 1 - s) >> 1; };
     auto slot_tile = [&](const Seg &g, int s, int i) { return g.rows > kTcRows ? i : 2 * i + s; };
     int grp0 = 0;
-    if (u_begin < u_end) grp0 = warp_find(pl.tc_t0, p.G + 1, u_begin);
+    if (u_begin < u_end) grp0 = warp_find(pl.tc_t0, 1, p.G + 1, u_begin);
 
     if (warp == 0) {
         // ---------------- copies: lane j issues box j of a tile ----------------
@@ -205,8 +208,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
             Seg g;
             segment(u, grp, g);
             u += g.n;
-            const int r0 = pl.row0[g.group], sq = p.seqs ? p.seqs[r0] : r0;
-            const int *table = p.table + (size_t)sq * p.max_pages;
+            const int r0 = pl.src[g.group].row0;
+            const int *table = p.table + (size_t)(p.seqs ? p.seqs[r0] : r0) * p.max_pages;
             auto lookup = [&](int tile, int &page, int &row) {
                 const int pos = (g.k0 + tile) * kTcKeys + lane * ta.box_rows, pg = pos / p.page_size;
                 row = pos - pg * p.page_size;
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
             const int mine = both ? (s ? g.rows - kTcRows : kTcRows) : g.rows;  // pairs of the slot
             const int n = slot_tiles(g, s);
             // the pair's query, a row of the A operand: 16-byte word c of block b at word c ^ (r & 7)
-            const int row0 = pl.row0[g.group], head0 = first_head(g.kvh, p.n_heads, p.n_kv_heads);
+            const int row0 = pl.src[g.group].row0, head0 = first_head(g.kvh, p.n_heads, p.n_kv_heads);
             const int nh = first_head(g.kvh + 1, p.n_heads, p.n_kv_heads) - head0;
             const int m = g.m0 + (both ? s * kTcRows : 0) + r, br = m / gq, hj = m - br * gq;
             const bool real = r < mine && hj < nh;
@@ -465,11 +468,12 @@ bool encode_pages(CUtensorMap *m, const char *base, const PagesAttn &p, int rows
 }
 
 template <int HS, bool BF>
-cudaError_t launch_tc(const TcAttn &ta, int num_sms, cudaLaunchConfig_t cfg) {
+cudaError_t launch_tc(const TcAttn &ta, cudaLaunchConfig_t cfg) {
     auto fn = attn_pages_tc_kernel<HS, BF>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TcShape<HS>::kSmem);
+    static DeviceOnce once;
+    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), (int)TcShape<HS>::kSmem);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(num_sms);
+    cfg.gridDim = dim3(ta.p.num_sms);
     cfg.blockDim = dim3(kTcThreads);
     cfg.dynamicSmemBytes = TcShape<HS>::kSmem;
     return cudaLaunchKernelEx(&cfg, fn, ta);
@@ -486,15 +490,15 @@ bool attn_pages_tc_supported(const PagesAttn &p) {
     return (whole || part) && p.row_stride < lim && p.head_stride < lim && p.page_stride < lim && tensor_map_encoder();
 }
 
-cudaError_t launch_attn_pages_tc(const PagesAttn &p, int num_sms, cudaLaunchConfig_t cfg) {
+cudaError_t launch_attn_pages_tc(const PagesAttn &p, cudaLaunchConfig_t cfg) {
     TcAttn ta{};
     ta.p = p;
     ta.box_rows = box_rows(p.page_size);
     ta.scale_log2 = p.scale_log2 < 0.f ? -p.scale_log2 : p.scale_log2;
     ta.flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     if (!encode_pages(&ta.kmap, p.k, p, ta.box_rows) || !encode_pages(&ta.vmap, p.v, p, ta.box_rows)) return cudaErrorInvalidValue;
-    if (p.head_size <= 64) return p.dtype == L2_BF16 ? launch_tc<64, true>(ta, num_sms, cfg) : launch_tc<64, false>(ta, num_sms, cfg);
-    return p.dtype == L2_BF16 ? launch_tc<128, true>(ta, num_sms, cfg) : launch_tc<128, false>(ta, num_sms, cfg);
+    if (p.head_size <= 64) return p.dtype == L2_BF16 ? launch_tc<64, true>(ta, cfg) : launch_tc<64, false>(ta, cfg);
+    return p.dtype == L2_BF16 ? launch_tc<128, true>(ta, cfg) : launch_tc<128, false>(ta, cfg);
 }
 
 }  // namespace l2

@@ -1,5 +1,6 @@
 // Paged KV cache: kernel parameter blocks and launch entry points (host side).
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -43,6 +44,20 @@ cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, bool pd
 cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s);
 cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, cudaStream_t s);
 
+// Raises a kernel's shared-memory limit once per device (the attribute outlives the call).
+struct DeviceOnce {
+    std::atomic<unsigned long long> done{0};
+    cudaError_t smem(const void *fn, int bytes) {
+        int d = 0;
+        cudaError_t e = cudaGetDevice(&d);
+        if (e != cudaSuccess) return e;
+        if (d < 64 && (done.load(std::memory_order_relaxed) >> d & 1)) return cudaSuccess;
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && d < 64) done.fetch_or(1ull << d, std::memory_order_relaxed);
+        return e;
+    }
+};
+
 // Attention of one query row per sequence over its pages (attn_pages.cu).
 struct PagesAttn {
     const char *k, *v;        // this layer's pages
@@ -63,17 +78,20 @@ struct PagesAttn {
     int *plan;
     float *ws_ml, *ws_acc;
     int max_parts;            // parts the workspace holds
+    int num_sms, tile_keys;   // keys of a warp's tile
     bool tc;                  // prefixes may go to the tensor-core kernel
+    bool plan_in_block;       // every block plans for itself (no plan kernel before)
+    bool wait_first;          // the warps' kernel follows the plan kernel directly
     float *tc_ml, *tc_acc;    // its parts, by row
 };
 
 // Tensor-core part of it (attn_pages_tc.cu): whether pages and type allow tiled copies of 128 keys, and the launch.
 bool attn_pages_tc_supported(const PagesAttn &p);
-cudaError_t launch_attn_pages_tc(const PagesAttn &p, int num_sms, cudaLaunchConfig_t cfg);
+cudaError_t launch_attn_pages_tc(const PagesAttn &p, cudaLaunchConfig_t cfg);
 
 // Its walk over fp32 caches (attn_pages_f32.cu) and the keys of one tile there.
 int attn_pages_f32_tile(int head_size);
-cudaError_t launch_attn_pages_f32(const PagesAttn &p, int num_sms, cudaLaunchConfig_t cfg);
+cudaError_t launch_attn_pages_f32(const PagesAttn &p, cudaLaunchConfig_t cfg);
 
 // cuTensorMapEncodeTiled, looked up once (l2_api.cu).
 void *tensor_map_encoder();
