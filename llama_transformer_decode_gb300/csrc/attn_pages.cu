@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
         a.z *= c0;
         a.w *= c0;
         const int cnt = min(32, n - e0);
-#pragma unroll 4
+#pragma unroll 8
         for (int q = 0; q < cnt; q += per) {
             const int from = min(q + sub, 31);
             const float c1 = __shfl_sync(0xffffffffu, wt, from);

@@ -113,6 +113,13 @@ __device__ __forceinline__ uint32_t idesc_f16(bool bf, int M, int N, bool b_mn) 
     return (1u << 4) | (bf ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// 2^x, at most 2 units in the last place off; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // One item's part of a block's range of steps.
 struct Seg {
     int group, kvh, m0, rows, k0, n;  // m0: first pair, rows: pairs (up to 256), tiles k0 .. k0 + n - 1
@@ -210,36 +217,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
             u += g.n;
             const int r0 = pl.src[g.group].row0;
             const int *table = p.table + (size_t)(p.seqs ? p.seqs[r0] : r0) * p.max_pages;
-            auto lookup = [&](int tile, int &page, int &row) {
-                const int pos = (g.k0 + tile) * kTcKeys + lane * ta.box_rows, pg = pos / p.page_size;
-                row = pos - pg * p.page_size;
-                page = lane < boxes ? table[pg] : 0;
+            auto lookup = [&](int tile) {
+                const int pos = (g.k0 + tile) * kTcKeys + lane * ta.box_rows;
+                return lane < boxes && tile < g.n ? table[page_of(p, pos)] : 0;
             };
-            int page, row;
-            lookup(0, page, row);
-            for (int i = 0; i < g.n && ok; ++i, ++t) {
-                const int cp = page >= 0 && page < p.n_pages ? page : p.n_pages;  // out of range: TMA fills zeros
-                const int cr = row;
-                if (lane < boxes && cp == p.n_pages) atomicOr(p.err, L2_DEV_ERR_BOUNDS);
-                if (i + 1 < g.n) lookup(i + 1, page, row);
+            // one tile of K or V; its page ids were loaded a step before
+            auto copy = [&](int kv, int tile, int tt, int page) {
+                const int ns = kv ? Sh::kStagesV : Sh::kStagesK, st = tt % ns;
+                uint64_t *full = kv ? &fx.full_v[st] : &fx.full_k[st], *empty = kv ? &fx.empty_v[st] : &fx.empty_k[st];
+                if (tt >= ns) ok = wait_or_stop(fx, empty, (uint32_t)((tt / ns - 1) & 1), p.err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                if (lane == 0) mbar_arrive_expect_tx(full, Sh::kTile);
+                __syncwarp();
+                if (lane < boxes) {
+                    const int pos = (g.k0 + tile) * kTcKeys + lane * ta.box_rows, row = pos - page_of(p, pos) * p.page_size;
+                    const int cp = page >= 0 && page < p.n_pages ? page : p.n_pages;  // out of range: TMA fills zeros
+                    if (cp == p.n_pages) atomicOr(p.err, L2_DEV_ERR_BOUNDS);
+                    const uint32_t dst = (kv ? v_at : k_at) + st * Sh::kTile + lane * ta.box_rows * 128;
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int ns = kv ? Sh::kStagesV : Sh::kStagesK, st = t % ns;
-                    uint64_t *full = kv ? &fx.full_v[st] : &fx.full_k[st], *empty = kv ? &fx.empty_v[st] : &fx.empty_k[st];
-                    if (t >= ns) ok = wait_or_stop(fx, empty, (uint32_t)((t / ns - 1) & 1), p.err);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(full, Sh::kTile);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        const uint32_t dst = (kv ? v_at : k_at) + st * Sh::kTile + lane * ta.box_rows * 128;
-#pragma unroll
-                        for (int b = 0; b < Sh::kBlocks; ++b)
-                            tensor4d(dst + b * kBlock, kv ? &ta.vmap : &ta.kmap, 64 * b, cr, g.kvh, cp, full);
-                    }
-                    __syncwarp();
+                    for (int b = 0; b < Sh::kBlocks; ++b) tensor4d(dst + b * kBlock, kv ? &ta.vmap : &ta.kmap, 64 * b, row, g.kvh, cp, full);
                 }
+                __syncwarp();
+            };
+            // K runs a tile ahead of V: its stage is free first, and a tile's scores are the first thing needed
+            int pk = lookup(0), pn = lookup(1), pv = pk;
+            for (int i = 0; i <= g.n && ok; ++i) {
+                if (i < g.n) copy(0, i, t + i, pk);
+                if (ok && i > 0) copy(1, i - 1, t + i - 1, pv);
+                pv = pk;
+                pk = pn;
+                pn = lookup(i + 2);
             }
+            t += g.n;
         }
         // copies in flight land before the block's memory goes (all have, when the others finished)
         if (!ok) {
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
         __syncwarp();
     } else if (warp >= 4) {
         // ---------------- softmax warps ----------------
-        const int s = (warp - 4) >> 2, r = (tid - 128) & (kSlotThreads - 1);  // slot, pair within it
+        const int s = (warp - 4) >> 2, rl = (tid - 128) & (kSlotThreads - 1);  // slot, lane within it
         const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t sc = s_col(s) + lane_at, oc = o_col(s) + lane_at;
         unsigned char *qt = qs + s * Sh::kTile;
@@ -339,12 +349,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
             u += g.n;
             const bool both = g.rows > kTcRows;
             const int mine = both ? (s ? g.rows - kTcRows : kTcRows) : g.rows;  // pairs of the slot
+            // two slots of at most 64 pairs: the second takes the other two warps' lanes, so each scheduler has one busy warp
+            const int r = rl - (s && g.rows <= kTcRows / 2 ? kTcRows / 2 : 0);
             const int n = slot_tiles(g, s);
             // the pair's query, a row of the A operand: 16-byte word c of block b at word c ^ (r & 7)
             const int row0 = pl.src[g.group].row0, head0 = first_head(g.kvh, p.n_heads, p.n_kv_heads);
             const int nh = first_head(g.kvh + 1, p.n_heads, p.n_kv_heads) - head0;
-            const int m = g.m0 + (both ? s * kTcRows : 0) + r, br = m / gq, hj = m - br * gq;
-            const bool real = r < mine && hj < nh;
+            const int m = g.m0 + (both ? s * kTcRows : 0) + r, br = max(m, 0) / gq, hj = m - br * gq;
+            const bool real = r >= 0 && r < mine && hj < nh;
             const uint4 *q4 = reinterpret_cast<const uint4 *>(p.q + (real ? (row0 + br) * p.q_row + (head0 + hj) * p.q_head : 0));
 #pragma unroll
             for (int c = 0; c < HS / 8; ++c) {
@@ -356,12 +368,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
                     v.z ^= ta.flip;
                     v.w ^= ta.flip;
                 }
-                *reinterpret_cast<uint4 *>(qt + (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+                *reinterpret_cast<uint4 *>(qt + (c >> 3) * kBlock + rl * 128 + (((c & 7) ^ (rl & 7)) << 4)) = v;
             }
             fence_proxy_async_smem();
             tc_fence_before();  // acc of the segment before has been read
             mbar_arrive(&fx.q_full[s]);
-            const bool busy = (warp & 3) * 32 < mine;  // a warp without pairs only keeps the barriers going
+            const bool busy = __any_sync(0xffffffffu, r >= 0 && r < mine);  // a warp without pairs only keeps the barriers going
             float base = -CUDART_INF_F, sum = 0.f;
             for (int i = 0; i < n; ++i, ++done) {
                 ok = wait_or_stop(fx, &fx.s_full[s], (uint32_t)(done & 1), p.err);
@@ -369,45 +381,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
                 if (!ok) break;
                 tc_fence_after();
                 if (busy) {
-                    float v[32], mx = -CUDART_INF_F;
+                    float v[64], m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld32_wait(sc + 32 * c, v);
+                    for (int c = 0; c < 2; ++c) {
+                        tmem_ld64_wait(sc + 64 * c, v);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, v[j]);
+                        for (int j = 0; j < 64; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[j]);
                     }
-                    mx *= ta.scale_log2;
+                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * ta.scale_log2;
                     const bool grow = mx > base + kGrow || (base == -CUDART_INF_F && mx > base);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to = grow ? mx : base;
                         const float f = to == -CUDART_INF_F ? 1.f : exp2f(base - to);
                         if (i) {
 #pragma unroll
-                            for (int c = 0; c < HS / 32; ++c) {
-                                tmem_ld32_wait(oc + 32 * c, v);
-                                uint32_t w[32];
+                            for (int c = 0; c < HS / 64; ++c) {
+                                tmem_ld64_wait(oc + 64 * c, v);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j] * f);
-                                tmem_st32(oc + 32 * c, w);
+                                for (int k = 0; k < 2; ++k) {
+                                    uint32_t w[32];
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[32 * k + j] * f);
+                                    tmem_st32(oc + 64 * c + 32 * k, w);
+                                }
                             }
                         }
                         sum *= f;
                         base = to;
                     }
                     const float b0 = base == -CUDART_INF_F ? 0.f : base;
-                    // columns 16 c .. of the weights lie over scores read in this chunk or before
+                    // weights of scores 64 c .. go over columns 32 c .., read by then
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld32_wait(sc + 32 * c, v);
-                        uint32_t w[16];
+                    for (int c = 0; c < 2; ++c) {
+                        tmem_ld64_wait(sc + 64 * c, v);
+                        uint32_t w[32];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float x = exp2f(fmaf(v[2 * j], ta.scale_log2, -b0)), y = exp2f(fmaf(v[2 * j + 1], ta.scale_log2, -b0));
-                            sum += x + y;
+                        for (int j = 0; j < 32; ++j) {
+                            const float x = ex2(fmaf(v[2 * j], ta.scale_log2, -b0)), y = ex2(fmaf(v[2 * j + 1], ta.scale_log2, -b0));
+                            s4[j & 3] += x + y;
                             w[j] = pack16<BF>(x, y);
                         }
-                        tmem_st16(sc + 16 * c, w);
+                        tmem_st32(sc + 32 * c, w);
                     }
+                    sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                     tmem_wait_st();
                 }
                 tc_fence_before();
@@ -427,13 +444,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_pages_tc_kernel(const __gr
                 if (n) {
                     float4 *dst = reinterpret_cast<float4 *>(p.tc_acc + at * p.head_size);
 #pragma unroll
-                    for (int c = 0; c < HS / 32; ++c) {
-                        float v[32];
-                        tmem_ld32_wait(oc + 32 * c, v);
+                    for (int c = 0; c < HS / 64; ++c) {
+                        float v[64];
+                        tmem_ld64_wait(oc + 64 * c, v);
                         if (real) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (32 * c + 4 * j < p.head_size) dst[8 * c + j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                            for (int j = 0; j < 16; ++j)
+                                if (64 * c + 4 * j < p.head_size) dst[16 * c + j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                         }
                     }
                 }

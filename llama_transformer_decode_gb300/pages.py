@@ -8,6 +8,7 @@ into a CUDA graph.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -80,24 +81,28 @@ class PagePool:
                           *table.shape)
         self._ref = ctypes.byref(self._c)
         self._ws = {}  # workspace bytes per (rows, groups, heads)
+        self._torch, self._int32, self._index = torch, torch.int32, k.get_device()
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._scale = 1.0 / math.sqrt(self.head_size)
 
     # -- helpers -------------------------------------------------------------
     def _stream(self, stream):
-        import torch
-        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+        return self._raw_stream(self._index) if stream is None else stream.cuda_stream
 
     def _ints(self, name, t, n=None):
-        import torch
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != self.device or t.dim() != 1 \
+        """Address of an index array; n: its length, where the call fixes it."""
+        if not isinstance(t, self._torch.Tensor) or t.dtype is not self._int32 or t.get_device() != self._index or t.dim() != 1 \
                 or not t.is_contiguous() or (n is not None and t.numel() != n):
             raise ValueError(f"{name} must be a contiguous int32 tensor [{'n' if n is None else n}] on {self.device}")
         return t.data_ptr()
 
     def _rows(self, name, t, dims):
-        if t.dtype != self.dtype or t.device != self.device or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1) \
-                or t.shape[-1] != self.head_size:
+        """Address, shape and strides of a tensor of rows of head_size."""
+        shape, st = t.shape, t.stride()
+        if t.dtype is not self.dtype or t.get_device() != self._index or len(shape) != dims or shape[-1] != self.head_size \
+                or (st[-1] != 1 and shape[-1] > 1):
             raise ValueError(f"{name} must have {dims} dimensions, the pool's type, device and head size, its last one contiguous")
-        return t.data_ptr()
+        return t.data_ptr(), shape, st
 
     def check(self):
         """Waits for the pool's device and raises L2Error if a call could not be done (and clears the status)."""
@@ -113,15 +118,15 @@ class PagePool:
         dimension of all layers) at the ends of sequences ``seqs``: rows
         starts[i]..starts[i + 1] - 1 go to seqs[i] (row i, without ``starts``).  ``extend``
         (default: with all layers, or layer 0) first lengthens the sequences."""
-        dims = 4 if layer is None else 3
-        kp, vp = self._rows("k", k, dims), self._rows("v", v, dims)
-        if k.shape != v.shape or k.stride() != v.stride() or k.shape[-2] != self.n_kv_heads \
-                or (layer is None and k.shape[0] != self.n_layers):
+        whole = layer is None
+        kp, shape, st = self._rows("k", k, 4 if whole else 3)
+        vp, v_shape, v_st = self._rows("v", v, 4 if whole else 3)
+        if shape != v_shape or st != v_st or shape[-2] != self.n_kv_heads or (whole and shape[0] != self.n_layers):
             raise ValueError("k and v must be alike, with the pool's layers and heads")
         n = seqs.numel()
-        a = L2PagesRows(n, k.shape[-3], self._ints("seqs", seqs), None if starts is None else self._ints("starts", starts, n + 1),
-                        -1 if layer is None else int(layer), int(layer in (None, 0) if extend is None else bool(extend)), kp, vp,
-                        k.stride(0) if layer is None else 0, k.stride(-3), k.stride(-2))
+        a = L2PagesRows(n, shape[-3], self._ints("seqs", seqs), None if starts is None else self._ints("starts", starts, n + 1),
+                        -1 if whole else int(layer), int((whole or layer == 0) if extend is None else bool(extend)), kp, vp,
+                        st[0] if whole else 0, st[-3], st[-2])
         rc = self._lib.l2_pages_append(self._ref, ctypes.byref(a), self._stream(stream))
         if rc:
             _raise(rc)
@@ -148,15 +153,13 @@ class PagePool:
         sequence seqs[b] (b, without ``seqs``), with prefixes shared by groups of rows read
         once (``l2_pages_attention``).  ``lse``: a float32 [rows][heads] tensor for the log
         sums, or None.  Returns ``out``."""
-        import torch
-        qp = self._rows("q", q, 3)
-        B, H = q.shape[0], q.shape[1]
-        G = 0
+        qp, (B, H, _), q_st = self._rows("q", q, 3)
+        G = gs = pl = 0
         if group_starts is not None:
             G = group_starts.numel() - 1
             if G < 1 or prefix_lens is None:
                 raise ValueError("group_starts needs at least one group, and prefix_lens")
-            self._ints("prefix_lens", prefix_lens, G)
+            gs, pl = self._ints("group_starts", group_starts), self._ints("prefix_lens", prefix_lens, G)
         elif prefix_lens is not None:
             raise ValueError("prefix_lens needs group_starts")
         need = self._ws.get((B, G, H))
@@ -165,26 +168,21 @@ class PagePool:
             if need < 0:
                 _raise(int(need))
             self._ws[(B, G, H)] = need
-        if stream is None:
+        torch = self._torch
+        # the workspace belongs to the stream that uses it
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             if out is None:
                 out = torch.empty((B, H, self.head_size), dtype=self.dtype, device=self.device)
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        else:  # the workspace belongs to the stream that uses it
-            with torch.cuda.stream(stream):
-                if out is None:
-                    out = torch.empty((B, H, self.head_size), dtype=self.dtype, device=self.device)
-                ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        op = self._rows("out", out, 3)
-        if out.shape != q.shape:
+        op, o_shape, o_st = self._rows("out", out, 3)
+        if o_shape != q.shape:
             raise ValueError("out must have q's shape")
-        if lse is not None and (lse.dtype != torch.float32 or lse.device != self.device or not lse.is_contiguous()
+        if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != self._index or not lse.is_contiguous()
                                 or tuple(lse.shape) != (B, H)):
             raise ValueError("lse must be a contiguous float32 tensor [rows][heads] of the pool's device")
         a = L2PagesAttention(int(layer), B, G, H, qp, op, None if lse is None else lse.data_ptr(),
-                             None if seqs is None else self._ints("seqs", seqs, B),
-                             self._ints("group_starts", group_starts) if G else None,
-                             prefix_lens.data_ptr() if G else None, q.stride(0), q.stride(1), out.stride(0), out.stride(1),
-                             1.0 / math.sqrt(self.head_size) if scale is None else float(scale))
+                             None if seqs is None else self._ints("seqs", seqs, B), gs, pl, q_st[0], q_st[1], o_st[0], o_st[1],
+                             self._scale if scale is None else float(scale))
         rc = self._lib.l2_pages_attention(self._ref, ctypes.byref(a), ws.data_ptr(), need, self._stream(stream))
         if rc:
             _raise(rc)
