@@ -8,15 +8,13 @@
 
 namespace l2 {
 
-constexpr int kWalkWarps = 8;  // warps of a block of the walking kernels, one block per SM
 constexpr int kM = 16;         // (row, head) pairs of a warp's item
-constexpr int kTcKeys = 128;  // keys of a tensor-core tile
 constexpr int kTcRows = 128;  // pairs of a tensor-core slot; an item has up to two slots' worth
 
 // Plan: a header; the sources of the warps (the groups' prefixes, then the rows' own keys: S = G + B, and an end);
-// per group, for the tensor-core kernel, its first tile, tiles per item and first row of its parts; the group of
+// per group, for the tensor-core role, the cost before it, tiles per item and first row of its parts; the group of
 // each row.
-enum { kHdrCost = 0, kHdrWarps = 1, kHdrOk = 2, kHdrTcTiles = 3, kHdrTcCtas = 4, kHdrInts = 16 };
+enum { kHdrCost = 0, kHdrWarps = 1, kHdrOk = 2, kHdrTcCost = 3, kHdrTcBlocks = 4, kHdrInts = 16 };
 struct alignas(16) Source {
     int t0, i0, kt, cost;          // cost and items of the sources before it, tiles per item, cost of a tile
     int key0, key1, row0, rows;    // keys, rows
@@ -69,7 +67,7 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n) {  // of all runs of
 
 // Walkers that are warps: neighbours in the numbering sit in different blocks, so that a stretch of costlier tiles
 // does not fall on one SM.
-__device__ __forceinline__ int walker_id() { return (threadIdx.x >> 5) * gridDim.x + blockIdx.x; }
+__device__ __forceinline__ int walker_id(int warp, int block0) { return warp * (gridDim.x - block0) + blockIdx.x - block0; }
 
 // The last entry i of an ascending list of n (every `stride`-th int of a, the first at most x) that is at most x,
 // found by a whole warp.
@@ -99,6 +97,10 @@ __device__ __forceinline__ void cp_wait() {
 // 4, 198 / 198 at 8, 271 / 279 at 16.
 constexpr int kCostUnit = 4;
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : 7; }
+
+// Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of 8 KB): reading its 32 KB while the
+// slots take turns, the slots' time when both work on every tile.
+__host__ __device__ __forceinline__ int tc_cost(int n, int hs) { return n > kTcRows ? 28 : 16; }
 
 // key / page_size; page_shift is its logarithm where it is a power of two, else -1.
 __device__ __forceinline__ int page_of(const PagesAttn &p, int key) {

@@ -245,11 +245,11 @@ __device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, con
 template <int HS>
 __global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_f32_kernel(const PagesAttn p) {
     extern __shared__ __align__(128) unsigned char smem[];
-    const int wid = walker_id();
+    const int wid = walker_id(threadIdx.x / 32, 0);
     unsigned char *ring = smem + (threadIdx.x >> 5) * ShapeF<HS>::kWarp;
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     pdl_launch_dependents();
-    if (p.wait_first) pdl_wait();
+    if (!p.plan_in_block) pdl_wait();
     const Plan pl = plan_here<kWalkWarps * 32>(p, smem + kWalkWarps * ShapeF<HS>::kWarp, smem, blockIdx.x == 0);
     const int T_all = pl.hdr[kHdrCost], W = pl.hdr[kHdrWarps];
     const int x0 = wid < W ? first_of(wid, T_all, W) : 0, x1 = wid < W ? first_of(wid + 1, T_all, W) : 0;

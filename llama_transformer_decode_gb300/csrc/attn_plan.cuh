@@ -7,11 +7,11 @@ namespace l2 {
 
 // Fewest tiles a warp takes: below that the parts cost more to write and merge than the parallel reading gains.
 constexpr int kMinTiles = 4;
-constexpr int kTcMinTiles = 4;  // the same for the tensor-core kernel's blocks (tiles of 128 keys)
+constexpr int kTcMinTiles = 2;  // the same for the blocks of the tensor-core role
 
 template <int NT, int MAX>
 struct PlanScratch {
-    int minlen[MAX], mintc[MAX], gstart[MAX + 1], len[MAX], group[MAX];
+    int minlen[MAX], mintc[MAX], gstart[MAX + 1], len[MAX], group[MAX], seq[MAX];
     long long sums[2][NT / 32];
 };
 
@@ -43,25 +43,25 @@ template <int NT, int MAX>
 __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, PlanScratch<NT, MAX> &sc, bool report) {
     const int i = threadIdx.x, S = p.G + p.B, gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     bool bad = false;
-    int len = 0, seq = 0;
+    int len = 0, seq = 0, P = 0, a0 = 0;
+    // what depends on nothing is loaded before the lengths, which depend on seqs
+    if (i < p.G) P = p.prefix_lens[i];
+    if (p.G && i <= p.G) a0 = p.group_starts[i];
     if (i < p.B) {
         seq = p.seqs ? p.seqs[i] : i;
         bad = seq < 0 || seq >= p.n_seqs;
         if (!bad) len = p.lens[seq];
         bad |= len < 0 || len > (long long)p.max_pages * p.page_size;
         sc.len[i] = len;
+        sc.seq[i] = seq;
     }
-    int P = 0;
     if (p.G) {
         for (int g = i; g <= p.G; g += NT) {
-            const int a = p.group_starts[g];
+            const int a = g == i ? a0 : p.group_starts[g];
             bad |= (g == 0 && a != 0) || (g == p.G && a != p.B) || a < 0 || a > p.B;
             sc.gstart[g] = a;
         }
-        if (i < p.G) {
-            P = p.prefix_lens[i];
-            bad |= P < 0;
-        }
+        bad |= P < 0;
         __syncthreads();
         if (i < p.G) {
             const int rows = sc.gstart[i + 1] - sc.gstart[i];
@@ -72,8 +72,8 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     if (__syncthreads_or(bad)) {
         if (i == 0) {
             if (report) atomicOr(p.err, L2_PAGES_ERR_ARGS);
-            pl.hdr[kHdrCost] = pl.hdr[kHdrTcTiles] = 0;
-            pl.hdr[kHdrWarps] = pl.hdr[kHdrTcCtas] = 1;
+            pl.hdr[kHdrCost] = pl.hdr[kHdrTcCost] = pl.hdr[kHdrTcBlocks] = 0;
+            pl.hdr[kHdrWarps] = 1;
             pl.hdr[kHdrOk] = 0;
         }
         __syncthreads();
@@ -92,14 +92,14 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         }
         __syncthreads();
         // prefixes worth it go to the tensor cores in whole tiles of 128 keys; what is left of them stays with the warps
-        const int n = i < p.G ? (sc.gstart[i + 1] - sc.gstart[i]) * gq : 0, full = i < p.G && p.tc && n > kM ? sc.minlen[i] / kTcKeys : 0;
-        const int tiles = full * tc_runs(n) * p.n_kv_heads, prows = full ? tc_head_rows(n) * p.n_kv_heads : 0;
+        const int n = i < p.G ? (sc.gstart[i + 1] - sc.gstart[i]) * gq : 0, full = i < p.G && p.tc && n > kM ? sc.minlen[i] / p.tc_keys : 0;
+        const int tiles = full * tc_runs(n) * p.n_kv_heads * tc_cost(n, p.head_size), prows = full ? tc_head_rows(n) * p.n_kv_heads : 0;
         const long long before = plan_scan<NT>((long long)tiles << 32 | prows, &tc_all, sc.sums[0]);
         if (i < p.G) {
             pl.tc_t0[i] = (int)(before >> 32);
             pl.tc_kt[i] = full;
             pl.tc_r0[i] = (int)before;
-            sc.mintc[i] = full * kTcKeys;
+            sc.mintc[i] = full * p.tc_keys;
         }
         __syncthreads();
     }
@@ -119,7 +119,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
             e.key1 = sc.len[e.row0];
         }
         e.kt = s < S ? cdiv(e.key1 - e.key0, p.tile_keys) : 0;
-        if (e.kt) e.seq = p.seqs ? p.seqs[e.row0] : e.row0;
+        if (s < p.G ? e.rows > 0 : s < S) e.seq = sc.seq[e.row0];
         e.cost = tile_cost(p.dtype, min(e.rows * gq, kM));
         const int items = e.kt ? cdiv(e.rows * gq, kM) * p.n_kv_heads : 0;
         long long here;
@@ -132,11 +132,17 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     }
     if (i == 0) {
         const int cost = (int)(all >> 32), tc = (int)(tc_all >> 32);
+        // blocks of the two roles by cost, at least one of each that has work
+        int n_tc = 0;
+        if (tc) {
+            n_tc = (int)(((long long)tc * p.num_sms + (tc + (long long)cost) / 2) / (tc + (long long)cost));
+            n_tc = max(1, min(min(n_tc, cdiv(tc, kTcMinTiles * tc_cost(1, p.head_size))), p.num_sms - (cost ? 1 : 0)));
+        }
         pl.src[S].t0 = cost;
         pl.hdr[kHdrCost] = cost;
-        pl.hdr[kHdrWarps] = max(1, min(p.num_sms * kWalkWarps, cdiv(cost, kMinTiles * kCostUnit)));
-        pl.hdr[kHdrTcTiles] = tc;
-        pl.hdr[kHdrTcCtas] = max(1, min(p.num_sms, cdiv(tc, kTcMinTiles)));
+        pl.hdr[kHdrWarps] = max(1, min((p.num_sms - n_tc) * p.walk_warps, cdiv(cost, kMinTiles * kCostUnit)));
+        pl.hdr[kHdrTcCost] = tc;
+        pl.hdr[kHdrTcBlocks] = n_tc;
         if (p.G) pl.tc_t0[p.G] = tc;
         pl.hdr[kHdrOk] = 1;
     }

@@ -78,20 +78,23 @@ struct PagesAttn {
     int *plan;
     float *ws_ml, *ws_acc;
     int max_parts;            // parts the workspace holds
-    int num_sms, tile_keys;   // keys of a warp's tile
-    bool tc;                  // prefixes may go to the tensor-core kernel
+    int num_sms, walk_warps;  // blocks, warps of one that walk
+    int tile_keys, tc_keys;   // keys of a warp's tile, of a tensor-core tile
+    bool tc;                  // prefixes may go to the tensor cores
     bool plan_in_block;       // every block plans for itself (no plan kernel before)
-    bool wait_first;          // the warps' kernel follows the plan kernel directly
     float *tc_ml, *tc_acc;    // its parts, by row
 };
 
-// Tensor-core part of it (attn_pages_tc.cu): whether pages and type allow tiled copies of 128 keys, and the launch.
+// Its kernels over 16-bit caches (attn_pages_16.cu) and fp32 caches (attn_pages_f32.cu): keys of a warp's tile, walking
+// warps of a block; keys of a tensor-core tile, and whether its pages allow such tiles.
+int attn_pages_16_tile(int head_size);
+int attn_pages_16_warps();
+int attn_pages_tc_tile(int head_size);
 bool attn_pages_tc_supported(const PagesAttn &p);
-cudaError_t launch_attn_pages_tc(const PagesAttn &p, cudaLaunchConfig_t cfg);
-
-// Its walk over fp32 caches (attn_pages_f32.cu) and the keys of one tile there.
+cudaError_t launch_attn_pages_16(const PagesAttn &p, cudaLaunchConfig_t cfg);
 int attn_pages_f32_tile(int head_size);
 cudaError_t launch_attn_pages_f32(const PagesAttn &p, cudaLaunchConfig_t cfg);
+constexpr int kWalkWarps = 8;  // of a block of the fp32 kernel
 
 // cuTensorMapEncodeTiled, looked up once (l2_api.cu).
 void *tensor_map_encoder();
