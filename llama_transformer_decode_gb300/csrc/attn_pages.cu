@@ -39,6 +39,7 @@ namespace l2 {
 __global__ void __launch_bounds__(kPagesMaxCall) attn_pages_plan_kernel(const PagesAttn p) {
     __shared__ PlanScratch<kPagesMaxCall, kPagesMaxCall> sc;
     pdl_launch_dependents();
+    pdl_wait();
     plan_build<kPagesMaxCall, kPagesMaxCall>(p, plan_of(p.plan, p.B, p.G), sc, true);
 }
 
@@ -64,7 +65,7 @@ __device__ __forceinline__ void store_out<__half>(char *o, int d, float4 v) {
 
 // Parts of one (row, head) that a source's walkers left.
 struct PartRange {
-    int u0, kt, cost, w0, n, slot, pair;
+    int w0, n, slot, pair;
 };
 }  // namespace
 
@@ -79,53 +80,49 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
     const Plan pl = plan_of(p.plan, p.B, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const int kvh = (int)((long long)h * p.n_kv_heads / p.n_heads), j = h - first_head(kvh, p.n_heads, p.n_kv_heads);
+    pdl_launch_dependents();
     pdl_wait();
-    if (b >= p.B || !pl.hdr[kHdrOk]) return;
-    const int T_all = pl.hdr[kHdrCost], W = pl.hdr[kHdrWarps];
+    if (b >= p.B) return;
+    // one round of loads: the header, the row's group and its own source
+    const int4 h0 = *reinterpret_cast<const int4 *>(pl.hdr);
     const int grp = p.G ? pl.group[b] : 0;
-    auto range = [&](int s) {
+    const int4 own_a = *reinterpret_cast<const int4 *>(&pl.src[p.G + b].t0), own_c = *reinterpret_cast<const int4 *>(&pl.src[p.G + b].key0);
+    const int per = h0.y, per_tc = pl.hdr[kHdrTcPer];
+    if (!h0.z) return;
+    auto range = [&](const int4 &a, const int4 &c) {
         PartRange r = {};
-        const int4 a = *reinterpret_cast<const int4 *>(&pl.src[s].t0), c = *reinterpret_cast<const int4 *>(&pl.src[s].key0);
         if (a.z) {
-            const int mi = (b - c.z) * gq + j, item = kvh * cdiv(c.w * gq, kM) + mi / kM;
-            r.kt = a.z;
-            r.cost = a.w;
-            r.u0 = a.x + item * a.z * a.w;
-            r.w0 = walker_of(r.u0, T_all, W);
-            r.n = walker_of(r.u0 + (a.z - 1) * a.w, T_all, W) - r.w0 + 1;
+            const int mi = (b - c.z) * gq + j, item = kvh * ((c.w * gq + kM - 1) / kM) + mi / kM;
+            const int u0 = a.x + item * a.z * a.w;
+            r.w0 = walker_of(u0, per);
+            r.n = walker_of(u0 + (a.z - 1) * a.w, per) - r.w0 + 1;
             r.slot = a.y + item;
             r.pair = mi % kM;
         }
         return r;
     };
-    // whether walker w holds a tile of the item at u0 (len long, cost a tile): a range narrower than a tile may not
-    auto holds = [](int w, int u0, int len, int cost, int total, int W) {
-        return cdiv(max(u0, first_of(w, total, W)) - u0, cost) < cdiv(min(u0 + len, first_of(w + 1, total, W)) - u0, cost);
-    };
-    const PartRange own = range(p.G + b);
+    const PartRange own = range(own_a, own_c);
     PartRange rest = {};
-    int tc_n = 0, tc_w0 = 0, tc_base = 0, tc_rows = 0, tc_per = 1, tc_u0 = 0, tc_len = 0, tc_c = 1;
+    int tc_n = 0, tc_w0 = 0, tc_base = 0, tc_rows = 0, tc_per = 1;
     if (p.G) {
-        rest = range(grp);
-        const int kt = pl.tc_kt[grp];
+        const int4 ga = *reinterpret_cast<const int4 *>(&pl.src[grp].t0), gc = *reinterpret_cast<const int4 *>(&pl.src[grp].key0);
+        const int kt = pl.tc_kt[grp], t0 = pl.tc_t0[grp], r0 = pl.tc_r0[grp];
+        rest = range(ga, gc);
         if (kt) {
-            const int row0 = pl.src[grp].row0, n = pl.src[grp].rows * gq, mi = (b - row0) * gq + j;
+            const int row0 = gc.z, n = gc.w * gq, mi = (b - row0) * gq + j;
             const int run = mi / (2 * kTcRows), r = mi - run * 2 * kTcRows;
-            const int cost = tc_cost(n, p.head_size), Tt = pl.hdr[kHdrTcCost], Wt = pl.hdr[kHdrTcBlocks];
-            const int u0 = pl.tc_t0[grp] + (kvh * tc_runs(n) + run) * kt * cost;
+            const int cost = tc_cost(n);
+            const int u0 = t0 + (kvh * tc_runs(n) + run) * kt * cost;
             tc_rows = min(2 * kTcRows, n - run * 2 * kTcRows);
             tc_per = tc_rows > kTcRows ? 1 : 2;  // parts a block leaves of this row
-            tc_w0 = walker_of(u0, Tt, Wt);
-            tc_n = (walker_of(u0 + (kt - 1) * cost, Tt, Wt) - tc_w0 + 1) * tc_per;
-            tc_u0 = u0;
-            tc_len = kt * cost;
-            tc_c = cost;
-            tc_base = pl.tc_r0[grp] + kvh * tc_head_rows(n) + run * 2 * kTcRows + r;
+            tc_w0 = walker_of(u0, per_tc);
+            tc_n = (walker_of(u0 + (kt - 1) * cost, per_tc) - tc_w0 + 1) * tc_per;
+            tc_base = r0 + kvh * tc_head_rows(n) + run * 2 * kTcRows + r;
         }
     }
     const int n = tc_n + rest.n + own.n;
     const int LP = p.head_size > 64 ? 32 : p.head_size > 32 ? 16 : 8;  // lanes of a part's sums
-    const int sub = lane / LP, d = 4 * (lane % LP), per = 32 / LP;
+    const int sub = lane / LP, d = 4 * (lane % LP), at_once = 32 / LP;
     const bool on = d < p.head_size;
     float m = -CUDART_INF_F, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -134,21 +131,16 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
         float2 ml = make_float2(-CUDART_INF_F, 0.f);
         const float *acc = nullptr;
         if (e < tc_n) {
-            const int wi = e / tc_per;
-            if (holds(tc_w0 + wi, tc_u0, tc_len, tc_c, pl.hdr[kHdrTcCost], pl.hdr[kHdrTcBlocks])) {
-                const size_t at = (size_t)(tc_base + 2 * kTcRows * (tc_w0 + wi) + (e - wi * tc_per) * tc_rows);
-                ml = reinterpret_cast<const float2 *>(p.tc_ml)[at];
-                acc = p.tc_acc + at * p.head_size;
-            }
+            const int wi = tc_per == 2 ? e >> 1 : e;
+            const size_t at = (size_t)(tc_base + 2 * kTcRows * (tc_w0 + wi) + (e - wi * tc_per) * tc_rows);
+            ml = reinterpret_cast<const float2 *>(p.tc_ml)[at];
+            acc = p.tc_acc + at * p.head_size;
         } else if (e < n) {
             const bool first = e < tc_n + rest.n;
-            const PartRange &r = first ? rest : own;
-            const int w = r.w0 + e - tc_n - (first ? 0 : rest.n);
-            if (holds(w, r.u0, r.kt * r.cost, r.cost, T_all, W)) {
-                const size_t at = (size_t)(r.slot + w) * kM + r.pair;
-                ml = reinterpret_cast<const float2 *>(p.ws_ml)[at];
-                acc = p.ws_acc + at * p.head_size;
-            }
+            const int w = e - tc_n + (first ? rest.w0 : own.w0 - rest.n);
+            const size_t at = (size_t)((first ? rest.slot : own.slot) + w) * kM + (first ? rest.pair : own.pair);
+            ml = reinterpret_cast<const float2 *>(p.ws_ml)[at];
+            acc = p.ws_acc + at * p.head_size;
         }
         if (ml.x == -CUDART_INF_F && ml.y == 0.f) acc = nullptr;  // a part without keys
         float mn = fmaxf(m, ml.x);
@@ -167,7 +159,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
         a.w *= c0;
         const int cnt = min(32, n - e0);
 #pragma unroll 8
-        for (int q = 0; q < cnt; q += per) {
+        for (int q = 0; q < cnt; q += at_once) {
             const int from = min(q + sub, 31);
             const float c1 = __shfl_sync(0xffffffffu, wt, from);
             const float *src = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(acc), from));
@@ -233,7 +225,8 @@ size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_s
     return ws_layout(B, G, n_heads, n_kv_heads, head_size, num_sms).bytes;
 }
 
-// Kernels of a call, each after the first launched as its predecessor's dependent: [plan] parts, merge.
+// Kernels of a call: [plan] parts, merge.  Each is launched as a dependent of what is before it in the stream (the first too: its blocks
+// come up while that ends, and wait for its end before they read anything).
 cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s) {
     const WsLayout w = ws_layout(p.B, p.G, p.n_heads, p.n_kv_heads, p.head_size, num_sms);
     char *base = static_cast<char *>(ws);
@@ -245,9 +238,8 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     p.max_parts = (int)w.parts;
     p.num_sms = num_sms;
     const bool f32 = p.dtype == L2_F32;
-    p.tile_keys = f32 ? attn_pages_f32_tile(p.head_size) : attn_pages_16_tile(p.head_size);
+    p.tile_shift = f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size);
     p.walk_warps = f32 ? kWalkWarps : attn_pages_16_warps();
-    p.tc_keys = attn_pages_tc_tile(p.head_size);
     // a prefix that serves at most 16 pairs gains nothing on the tensor cores
     p.tc = !f32 && p.G && p.B * heads_per_kv(p.n_heads, p.n_kv_heads) > kM && attn_pages_tc_supported(p);
     p.plan_in_block = p.B + p.G <= kPlanInBlock;
@@ -257,15 +249,14 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = 1;
     cudaError_t e = cudaSuccess;
     if (!p.plan_in_block) {
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(kPagesMaxCall);
         if ((e = cudaLaunchKernelEx(&cfg, attn_pages_plan_kernel, p)) != cudaSuccess) return e;
-        cfg.numAttrs = 1;
     }
     if ((e = f32 ? launch_attn_pages_f32(p, cfg) : launch_attn_pages_16(p, cfg)) != cudaSuccess) return e;
-    cfg.numAttrs = 1;
     cfg.gridDim = dim3((p.B * p.n_heads + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;

@@ -69,7 +69,8 @@ struct Shape {
     static constexpr int C = HS * 2 / 16;         // 16-byte words a row
     static constexpr int kRow = HS * 2;
     static constexpr int kStage = 2 * KT * kRow;  // K then V
-    static constexpr int kSmem = kWarps16 * kStages * kStage;
+    static constexpr int kRings = kWarps16 * kStages * kStage;
+    static constexpr int kSmem = kRings + kWarps16 * kItems * (int)sizeof(WalkItem);
 };
 // Shared memory of either role, before the plan.
 template <int HS>
@@ -86,150 +87,163 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
     constexpr int KT = Sh::KT, C = Sh::C, NT = KT / 8;  // NT: n8 tiles of keys
     const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
     const uint32_t ring = smem_u32(smem) + (threadIdx.x / 32 - 4) * (kStages * Sh::kStage);
+    WalkItem *queue = reinterpret_cast<WalkItem *>(smem + Sh::kRings) + (threadIdx.x / 32 - 4) * kItems;
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
-    const int T_all = pl.hdr[kHdrCost], W = pl.hdr[kHdrWarps];
-    const int x0 = wid < W ? first_of(wid, T_all, W) : 0, x1 = wid < W ? first_of(wid + 1, T_all, W) : 0;
     const int words = p.head_size / 8;  // 16-byte words of a row that exist
-    int src = 0, x = x0, done = 0;
-    WalkAhead<KT> ahead;
-    if (x0 < x1) {
-        src = warp_find(&pl.src[0].t0, sizeof(Source) / 4, p.G + p.B + 1, x0);
-        ahead.start(p, pl, src, x0, x1, gq);
-        for (int s = 0; s < kStages - 1; ++s) {
-            const uint32_t ks = ring + s * Sh::kStage;
-            walk_copy<KT, Sh::kRow>(p, pl, ahead, x1, gq, words, ks, ks + KT * Sh::kRow, swz);
-        }
-    }
-
-    WalkItem w;
-    while (walk_item(p, pl, src, x, x1, gq, w)) {
-        const int n_tiles = w.n_tiles, k_first = w.k_first;
-        const char *qa = walk_query(p, w, g4, gq), *qb = walk_query(p, w, g4 + 8, gq);
-        float m_run[2] = {-CUDART_INF_F, -CUDART_INF_F}, l_run[2] = {0.f, 0.f};
-        float o[HS / 8][4];
-#pragma unroll
-        for (int i = 0; i < HS / 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-        // the A fragments of all K steps
-        constexpr int QR = HS / 16 * 4;
-        uint32_t qf[QR];
-#pragma unroll
-        for (int ks = 0; ks < HS / 16; ++ks) {
-            const int d0 = ks * 16 + 2 * t4, d1 = d0 + 8;
-            qf[4 * ks] = qa && d0 < p.head_size ? *reinterpret_cast<const uint32_t *>(qa + 2 * d0) : 0u;
-            qf[4 * ks + 1] = qb && d0 < p.head_size ? *reinterpret_cast<const uint32_t *>(qb + 2 * d0) : 0u;
-            qf[4 * ks + 2] = qa && d1 < p.head_size ? *reinterpret_cast<const uint32_t *>(qa + 2 * d1) : 0u;
-            qf[4 * ks + 3] = qb && d1 < p.head_size ? *reinterpret_cast<const uint32_t *>(qb + 2 * d1) : 0u;
-        }
-
+    Walk<KT, Sh::kRow> walk;
+    walk.start(pl, wid, p.G + p.B);
+    float m_run[2], l_run[2], o[HS / 8][4];
+    constexpr int QR = HS / 16 * 4;
+    uint32_t qf[QR];
+    WalkItem w = {};
+    int it = 0, items = 0;  // tile within the item, items taken
+    // step s copies tile s - 1 and computes tile s - kStages
 #pragma unroll 1
-        for (int it = 0; it < n_tiles; ++it, ++done) {
-            cp_wait<kStages - 2>();
-            __syncwarp();
-            // the next tile goes into the stage read one step ago
-            const uint32_t nx = ring + ((done + kStages - 1) % kStages) * Sh::kStage;
-            walk_copy<KT, Sh::kRow>(p, pl, ahead, x1, gq, words, nx, nx + KT * Sh::kRow, swz);
-            const uint32_t ks_base = ring + (done % kStages) * Sh::kStage, vs_base = ks_base + KT * Sh::kRow;
-            float s[NT][4];
+    for (int step = 0;; ++step) {
+        {
+            const uint32_t st = ring + ((step + kStages - 1) % kStages) * Sh::kStage;
+            walk.step(p, pl, gq, words, queue, st, st + KT * Sh::kRow, swz);
+        }
+        if (step < kStages) continue;
+        if (step - kStages >= walk.issued) break;
+        if (it == 0) {
+            __syncwarp();  // the item was written by lane 0
+            w = queue[items++ % kItems];
+            const char *qa = walk_query(p, w, g4, gq), *qb = walk_query(p, w, g4 + 8, gq);
+            m_run[0] = m_run[1] = -CUDART_INF_F;
+            l_run[0] = l_run[1] = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < HS / 8; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
-            // lane's ldmatrix row: key (lane & 7) of the n8 tile, word 2 kpair + lane / 8
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int key = 8 * n + (lane & 7);
-#pragma unroll
-                for (int c = 0; c < C; c += 4) {
-                    uint32_t b[4];
-                    ldsm4(ks_base + key * Sh::kRow + (((c + (lane >> 3)) ^ swz(key)) << 4), b);
-                    T::mma(s[n], qf + 2 * c, b[0], b[1]);
-                    T::mma(s[n], qf + 2 * c + 4, b[2], b[3]);
-                }
-            }
-
-            // scale, mask keys past the end, running max
-            const int left = w.key1 - w.key0 - (k_first + it) * KT;
-            float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int key = 8 * n + 2 * t4 + (j & 1);
-                    s[n][j] = key < left ? s[n][j] * p.scale_log2 : -CUDART_INF_F;
-                    mx[j >> 1] = fmaxf(mx[j >> 1], s[n][j]);
-                }
-            float corr[2], base[2];
+                for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+            // The A fragments of all K steps: word t4 of every 16-byte chunk of rows g4 and g4 + 8.  Each lane loads every fourth
+            // chunk whole (few loads, all in flight) and the four lanes of a row exchange words.
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-                const float mn = fmaxf(m_run[r], mx[r]);
-                base[r] = mn == -CUDART_INF_F ? 0.f : mn;  // only -inf so far: weights 0, not NaN
-                corr[r] = exp2f(m_run[r] - base[r]);
-                m_run[r] = mn;
-            }
-            float sum[2] = {0.f, 0.f};
+                const uint4 *q4 = reinterpret_cast<const uint4 *>(r ? qb : qa);
+                uint4 v[HS / 32];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < HS / 32; ++i) v[i] = q4 && 4 * i + t4 < words ? q4[4 * i + t4] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[n][j] = exp2f(s[n][j] - base[j >> 1]);
-                    sum[j >> 1] += s[n][j];
-                }
-            l_run[0] = l_run[0] * corr[0] + sum[0];
-            l_run[1] = l_run[1] * corr[1] + sum[1];
-#pragma unroll
-            for (int i = 0; i < HS / 8; ++i) {
-                o[i][0] *= corr[0];
-                o[i][1] *= corr[0];
-                o[i][2] *= corr[1];
-                o[i][3] *= corr[1];
-            }
-#pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk) {
-                // weights as A fragments: hi and what it leaves
-                uint32_t ph[4], plo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x = s[2 * kk + (j >> 1)][2 * (j & 1)], y = s[2 * kk + (j >> 1)][2 * (j & 1) + 1];
-                    ph[j] = T::pack(x, y);
-                    const float2 back = T::unpack(ph[j]);
-                    plo[j] = T::pack(x - back.x, y - back.y);
-                }
-                const int key = 16 * kk + (lane & 15);
-#pragma unroll
-                for (int c = 0; c < C; c += 2) {
-                    uint32_t b[4];
-                    ldsm4t(vs_base + key * Sh::kRow + (((c + (lane >> 4)) ^ swz(key)) << 4), b);
-                    T::mma(o[c], ph, b[0], b[1]);
-                    T::mma(o[c], plo, b[0], b[1]);
-                    T::mma(o[c + 1], ph, b[2], b[3]);
-                    T::mma(o[c + 1], plo, b[2], b[3]);
+                for (int i = 0; i < HS / 32; ++i) {
+                    // 4 x 4 transpose: lane t4 ends with word t4 of chunks 4 i .. 4 i + 3
+                    const bool o1 = t4 & 1, o2 = t4 & 2;
+                    uint32_t a0 = __shfl_xor_sync(0xffffffffu, o1 ? v[i].x : v[i].y, 1), a1 = __shfl_xor_sync(0xffffffffu, o1 ? v[i].z : v[i].w, 1);
+                    const uint32_t x0 = o1 ? a0 : v[i].x, x1 = o1 ? v[i].y : a0, x2 = o1 ? a1 : v[i].z, x3 = o1 ? v[i].w : a1;
+                    a0 = __shfl_xor_sync(0xffffffffu, o2 ? x0 : x2, 2);
+                    a1 = __shfl_xor_sync(0xffffffffu, o2 ? x1 : x3, 2);
+                    // chunk 4 i + c is half c & 1 of K step 2 i + c / 2
+                    qf[8 * i + r] = o2 ? a0 : x0;
+                    qf[8 * i + 2 + r] = o2 ? a1 : x1;
+                    qf[8 * i + 4 + r] = o2 ? x2 : a0;
+                    qf[8 * i + 6 + r] = o2 ? x3 : a1;
                 }
             }
-        
-            __syncwarp();  // the stage is read before the next copy into it
         }
-        // the part: (m, l) and the sums of the item's pairs
-        const int slot = w.slot + wid;
+        cp_wait<kStages - 1>();
+        __syncwarp();
+        const uint32_t ks_base = ring + (step % kStages) * Sh::kStage, vs_base = ks_base + KT * Sh::kRow;
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+        // lane's ldmatrix row: key (lane & 7) of the n8 tile, word 2 kpair + lane / 8
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int key = 8 * n + (lane & 7);
+#pragma unroll
+            for (int c = 0; c < C; c += 4) {
+                uint32_t b[4];
+                ldsm4(ks_base + key * Sh::kRow + (((c + (lane >> 3)) ^ swz(key)) << 4), b);
+                T::mma(s[n], qf + 2 * c, b[0], b[1]);
+                T::mma(s[n], qf + 2 * c + 4, b[2], b[3]);
+            }
+        }
+
+        // scale, mask keys past the end, running max
+        const int left = w.left - it * KT;
+        float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = 8 * n + 2 * t4 + (j & 1);
+                s[n][j] = key < left ? s[n][j] * p.scale_log2 : -CUDART_INF_F;
+                mx[j >> 1] = fmaxf(mx[j >> 1], s[n][j]);
+            }
+        float corr[2], base[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            float l = l_run[r];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            const int mi = g4 + 8 * r;
-            if (!(r ? qb : qa) || slot >= p.max_parts) continue;
-            if (t4 == 0) reinterpret_cast<float2 *>(p.ws_ml)[(size_t)slot * kM + mi] = make_float2(m_run[r], l);
-            float *dst = p.ws_acc + ((size_t)slot * kM + mi) * p.head_size;
-#pragma unroll
-            for (int i = 0; i < HS / 8; ++i) {
-                const int d = 8 * i + 2 * t4;
-                if (d < p.head_size) *reinterpret_cast<float2 *>(dst + d) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
-            }
-        
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+            const float mn = fmaxf(m_run[r], mx[r]);
+            base[r] = mn == -CUDART_INF_F ? 0.f : mn;  // only -inf so far: weights 0, not NaN
+            corr[r] = exp2f(m_run[r] - base[r]);
+            m_run[r] = mn;
         }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[n][j] = exp2f(s[n][j] - base[j >> 1]);
+                sum[j >> 1] += s[n][j];
+            }
+        l_run[0] = l_run[0] * corr[0] + sum[0];
+        l_run[1] = l_run[1] * corr[1] + sum[1];
+#pragma unroll
+        for (int i = 0; i < HS / 8; ++i) {
+            o[i][0] *= corr[0];
+            o[i][1] *= corr[0];
+            o[i][2] *= corr[1];
+            o[i][3] *= corr[1];
+        }
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk) {
+            // weights as A fragments: hi and what it leaves
+            uint32_t ph[4], plo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = s[2 * kk + (j >> 1)][2 * (j & 1)], y = s[2 * kk + (j >> 1)][2 * (j & 1) + 1];
+                ph[j] = T::pack(x, y);
+                const float2 back = T::unpack(ph[j]);
+                plo[j] = T::pack(x - back.x, y - back.y);
+            }
+            const int key = 16 * kk + (lane & 15);
+#pragma unroll
+            for (int c = 0; c < C; c += 2) {
+                uint32_t b[4];
+                ldsm4t(vs_base + key * Sh::kRow + (((c + (lane >> 4)) ^ swz(key)) << 4), b);
+                T::mma(o[c], ph, b[0], b[1]);
+                T::mma(o[c], plo, b[0], b[1]);
+                T::mma(o[c + 1], ph, b[2], b[3]);
+                T::mma(o[c + 1], plo, b[2], b[3]);
+            }
+        }
+    
+        if (++it == w.n_tiles) {
+            it = 0;
+            // the part: (m, l) and the sums of the item's pairs
+            const int slot = w.slot + wid;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float l = l_run[r];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int mi = g4 + 8 * r;
+                if (mi >= w.pairs || slot >= p.max_parts) continue;
+                if (t4 == 0) reinterpret_cast<float2 *>(p.ws_ml)[(size_t)slot * kM + mi] = make_float2(m_run[r], l);
+                float *dst = p.ws_acc + ((size_t)slot * kM + mi) * p.head_size;
+#pragma unroll
+                for (int i = 0; i < HS / 8; ++i) {
+                    const int d = 8 * i + 2 * t4;
+                    if (d < p.head_size) *reinterpret_cast<float2 *>(dst + d) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                }
+        
+            }
+        }
+        __syncwarp();  // the stage is read before the next copy into it
     }
     cp_wait<0>();
 }
@@ -242,11 +256,11 @@ __global__ void __launch_bounds__(kThreads16, 1) attn_pages_16_kernel(const __gr
     extern __shared__ __align__(1024) unsigned char smem[];
     const PagesAttn &p = ta.p;
     pdl_launch_dependents();
-    if (!p.plan_in_block) pdl_wait();
+    pdl_wait();
     const Plan pl = plan_here<kThreads16>(p, smem + kWork<HS>, smem, blockIdx.x == 0);
     const int n_tc = pl.hdr[kHdrTcBlocks];
     if ((int)blockIdx.x < n_tc)
-        tc_role<HS, BF>(ta, pl, smem, blockIdx.x, n_tc);
+        tc_role<HS, BF>(ta, pl, smem, blockIdx.x);
     else if (threadIdx.x >= 128)
         walk_role<T, HS>(p, pl, smem, walker_id(threadIdx.x / 32 - 4, n_tc));
 }
@@ -288,18 +302,18 @@ cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
 // tile or are a multiple of one; a tensor's strides are below 2^40 bytes.
 bool attn_pages_tc_supported(const PagesAttn &p) {
     const long long lim = 1ll << 40;
-    return p.page_size >= 8 && (p.page_size % p.tc_keys == 0 || p.tc_keys % p.page_size == 0) && p.row_stride < lim &&
-           p.head_stride < lim && p.page_stride < lim && tensor_map_encoder();
+    return p.page_size >= 8 && (p.page_size % kTcKeys == 0 || kTcKeys % p.page_size == 0) && p.row_stride < lim && p.head_stride < lim &&
+           p.page_stride < lim && tensor_map_encoder();
 }
 
-int attn_pages_16_tile(int hs) { return hs <= 64 ? Shape<64>::KT : Shape<128>::KT; }
+int attn_pages_16_shift(int hs) { return hs <= 64 ? 5 : 4; }
+static_assert(Shape<64>::KT == 1 << 5 && Shape<128>::KT == 1 << 4, "the plan counts tiles by shifts");
 int attn_pages_16_warps() { return kWarps16; }
-int attn_pages_tc_tile(int hs) { return hs <= 64 ? TcShape<64>::KT : TcShape<128>::KT; }
 
 cudaError_t launch_attn_pages_16(const PagesAttn &p, cudaLaunchConfig_t cfg) {
     TcAttn ta{};
     ta.p = p;
-    ta.box_rows = p.page_size < p.tc_keys ? p.page_size : p.tc_keys;
+    ta.box_rows = p.page_size < kTcKeys ? p.page_size : kTcKeys;
     ta.scale_log2 = p.scale_log2 < 0.f ? -p.scale_log2 : p.scale_log2;
     ta.flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     if (p.tc && (!encode_pages(&ta.kmap, p.k, p, ta.box_rows) || !encode_pages(&ta.vmap, p.v, p, ta.box_rows))) return cudaErrorInvalidValue;

@@ -60,7 +60,7 @@ struct alignas(128) TcAttn {
 // 215 us against 152 for 65408 keys, 8 KV heads and 512 pairs each.)
 template <int HS>
 struct TcShape {
-    static constexpr int KT = 128;                           // keys of a tile
+    static constexpr int KT = kTcKeys;
     static constexpr bool kOwnP = HS == 64;
     static constexpr int kBlocks = HS / 64;                  // 64-value blocks of a row
     static constexpr uint32_t kBlock = KT * 128, kQBlock = kTcRows * 128;
@@ -145,9 +145,9 @@ __device__ __forceinline__ uint32_t pack16(float x, float y) {
     }
 }
 
-// One block's work, all of its threads.  smem: kSmem bytes; pl: the plan; bid of W blocks.
+// One block's work, all of its threads.  smem: kSmem bytes; pl: the plan; bid: the block among those of the role.
 template <int HS, bool BF>
-__device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsigned char *smem_raw, int bid, int W) {
+__device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsigned char *smem_raw, int bid) {
     using Sh = TcShape<HS>;
     const PagesAttn &p = ta.p;
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -183,20 +183,21 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
     auto s_col = [&](int s) { return tmem + 256 * s; };
     auto p_col = [&](int s) { return tmem + 256 * s + Sh::kP; };
     auto o_col = [&](int s) { return tmem + 256 * s + Sh::kO; };
-    const int x_begin = first_of(bid, pl.hdr[kHdrTcCost], W), x_end = first_of(bid + 1, pl.hdr[kHdrTcCost], W);
+    const int x_begin = bid * pl.hdr[kHdrTcPer], x_end = min(x_begin + pl.hdr[kHdrTcPer], pl.hdr[kHdrTcCost]);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     // every role walks the same segments: the tiles that start in the block's range of cost, item by item
     auto segment = [&](int &x, int &grp, Seg &g) {
+#pragma unroll 1
         for (;; ++grp) {
             if (x >= x_end) return false;
             const int kt = pl.tc_kt[grp], t0 = pl.tc_t0[grp];
             if (kt == 0) continue;
-            const int n = pl.src[grp].rows * gq, runs = tc_runs(n), cost = tc_cost(n, HS), i = cdiv(x - t0, cost), item = i / kt;
+            const int n = pl.src[grp].rows * gq, runs = tc_runs(n), cost = tc_cost(n), i = cdiv(x - t0, cost), item = (int)((unsigned)i / (unsigned)kt);
             x = t0 + i * cost;
             if (item >= runs * p.n_kv_heads) continue;
             if (x >= x_end) return false;
             g.group = grp;
-            g.kvh = item / runs;
+            g.kvh = (int)((unsigned)item / (unsigned)runs);
             const int run = item - g.kvh * runs;
             g.m0 = run * 2 * kTcRows;
             g.rows = min(2 * kTcRows, n - g.m0);

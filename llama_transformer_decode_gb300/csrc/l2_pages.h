@@ -40,7 +40,7 @@ struct PagesAppend {
 };
 
 cudaError_t launch_pages_extend(const PagesView &p, int n, const int *seqs, const int *starts, int rows, cudaStream_t s);
-cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, bool pdl, cudaStream_t s);
+cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, cudaStream_t s);
 cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s);
 cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, cudaStream_t s);
 
@@ -79,20 +79,19 @@ struct PagesAttn {
     float *ws_ml, *ws_acc;
     int max_parts;            // parts the workspace holds
     int num_sms, walk_warps;  // blocks, warps of one that walk
-    int tile_keys, tc_keys;   // keys of a warp's tile, of a tensor-core tile
+    int tile_shift;           // log2 of the keys of a warp's tile
     bool tc;                  // prefixes may go to the tensor cores
     bool plan_in_block;       // every block plans for itself (no plan kernel before)
     float *tc_ml, *tc_acc;    // its parts, by row
 };
 
-// Its kernels over 16-bit caches (attn_pages_16.cu) and fp32 caches (attn_pages_f32.cu): keys of a warp's tile, walking
-// warps of a block; keys of a tensor-core tile, and whether its pages allow such tiles.
-int attn_pages_16_tile(int head_size);
+// Its kernels over 16-bit caches (attn_pages_16.cu) and fp32 caches (attn_pages_f32.cu): the logarithm of the keys of a
+// warp's tile, walking warps of a block; whether the pages allow tensor-core tiles.
+int attn_pages_16_shift(int head_size);
 int attn_pages_16_warps();
-int attn_pages_tc_tile(int head_size);
 bool attn_pages_tc_supported(const PagesAttn &p);
 cudaError_t launch_attn_pages_16(const PagesAttn &p, cudaLaunchConfig_t cfg);
-int attn_pages_f32_tile(int head_size);
+int attn_pages_f32_shift(int head_size);
 cudaError_t launch_attn_pages_f32(const PagesAttn &p, cudaLaunchConfig_t cfg);
 constexpr int kWalkWarps = 8;  // of a block of the fp32 kernel
 

@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kT) pages_extend_kernel(const PagesView p, int
     __shared__ int buf[64], sq[kPagesMaxCall], base_s[kPagesMaxCall + 1];
     const int i = threadIdx.x;
     pdl_launch_dependents();
+    pdl_wait();
     const int s = i < n ? seqs[i] : -1;
     sq[i] = s;
     __syncthreads();
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(kT) pages_fork_kernel(const PagesView p, int n
     __shared__ int buf[64], ss[kPagesMaxCall], sd[kPagesMaxCall], full_s[kPagesMaxCall];
     const int i = threadIdx.x;
     pdl_launch_dependents();
+    pdl_wait();
     const int s = i < n ? src[i] : -1, d = i < n ? dst[i] : -2;
     ss[i] = s;
     sd[i] = d;
@@ -288,6 +290,7 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
     __shared__ int buf[64], sq[kPagesMaxCall], len_s[kPagesMaxCall];
     const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
     pdl_launch_dependents();
+    pdl_wait();
     const int s = i < n ? seqs[i] : -1;
     sq[i] = s;
     __syncthreads();
@@ -399,14 +402,16 @@ __global__ void __launch_bounds__(256) pages_compact_kernel(const PagesView p, i
 
 namespace {
 
-cudaError_t launch(void *fn, dim3 grid, int threads, void **args, bool pdl, cudaStream_t s) {
+// Every kernel here is launched as a dependent of what is before it in the stream: its blocks come up while that
+// ends, and wait for its end before they read anything.
+cudaError_t launch(void *fn, dim3 grid, int threads, void **args, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelExC(&cfg, fn, args);
@@ -416,32 +421,32 @@ cudaError_t launch(void *fn, dim3 grid, int threads, void **args, bool pdl, cuda
 
 cudaError_t launch_pages_extend(const PagesView &p, int n, const int *seqs, const int *starts, int rows, cudaStream_t s) {
     void *args[] = {const_cast<PagesView *>(&p), &n, &seqs, &starts, &rows};
-    return launch(reinterpret_cast<void *>(pages_extend_kernel), dim3(1), kT, args, false, s);
+    return launch(reinterpret_cast<void *>(pages_extend_kernel), dim3(1), kT, args, s);
 }
 
-cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, bool pdl, cudaStream_t s) {
+cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, cudaStream_t s) {
     if (a.rows == 0) return cudaSuccess;
     int per = 4;
     void *args[] = {const_cast<PagesView *>(&p), const_cast<PagesAppend *>(&a), &per};
     const long long warps = (long long)a.rows * ((a.n_layers + per - 1) / per);
-    return launch(reinterpret_cast<void *>(pages_write_kernel), dim3((unsigned)((warps + 7) / 8)), 256, args, pdl, s);
+    return launch(reinterpret_cast<void *>(pages_write_kernel), dim3((unsigned)((warps + 7) / 8)), 256, args, s);
 }
 
 cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s) {
     void *args[] = {const_cast<PagesView *>(&p), &n, &src, &dst, &rows};
-    cudaError_t e = launch(reinterpret_cast<void *>(pages_fork_kernel), dim3(1), kT, args, false, s);
+    cudaError_t e = launch(reinterpret_cast<void *>(pages_fork_kernel), dim3(1), kT, args, s);
     if (e != cudaSuccess) return e;
     const long long runs = 2ll * p.n_layers * p.n_kv_heads;
     long long gx = (runs + 31) / 32;  // about four runs a warp
     if (gx > 256) gx = 256;
     void *args2[] = {const_cast<PagesView *>(&p), &src, &dst};
-    return launch(reinterpret_cast<void *>(pages_fork_copy_kernel), dim3((unsigned)gx, n), 256, args2, true, s);
+    return launch(reinterpret_cast<void *>(pages_fork_copy_kernel), dim3((unsigned)gx, n), 256, args2, s);
 }
 
 cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, cudaStream_t s) {
     int c = compact ? 1 : 0;
     void *args[] = {const_cast<PagesView *>(&p), &n, &seqs, &c};
-    cudaError_t e = launch(reinterpret_cast<void *>(pages_free_kernel), dim3(1), kT, args, false, s);
+    cudaError_t e = launch(reinterpret_cast<void *>(pages_free_kernel), dim3(1), kT, args, s);
     if (e != cudaSuccess || !compact) return e;
     // heads and rows that lie side by side are one run
     int heads = p.n_kv_heads, rows = p.page_size, bytes = p.row_bytes;
@@ -456,7 +461,7 @@ cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool c
         rows = 1;
     }
     void *args2[] = {const_cast<PagesView *>(&p), &heads, &rows, &bytes};
-    return launch(reinterpret_cast<void *>(pages_compact_kernel), dim3(152 * 8), 256, args2, true, s);
+    return launch(reinterpret_cast<void *>(pages_compact_kernel), dim3(152 * 8), 256, args2, s);
 }
 
 }  // namespace l2

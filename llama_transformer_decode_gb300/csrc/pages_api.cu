@@ -186,7 +186,7 @@ int l2_pages_append(const L2Pages *pool, const L2PagesRows *a, void *cuda_stream
         cudaError_t e = launch_pages_extend(v, a->n, a->seqs, a->starts, a->rows, s);
         if (e != cudaSuccess) return finish(who, e);
     }
-    return finish(who, launch_pages_write(v, w, a->extend != 0, s));
+    return finish(who, launch_pages_write(v, w, s));
 }
 
 int l2_pages_fork(const L2Pages *pool, int n, const int *src, const int *dst, const int *rows, void *cuda_stream) {
