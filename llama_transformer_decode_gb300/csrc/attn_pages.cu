@@ -40,7 +40,9 @@ __global__ void __launch_bounds__(kPagesMaxCall) attn_pages_plan_kernel(const Pa
     __shared__ PlanScratch<kPagesMaxCall, kPagesMaxCall> sc;
     pdl_launch_dependents();
     pdl_wait();
-    plan_build<kPagesMaxCall, kPagesMaxCall>(p, plan_of(p.plan, p.B, p.G), sc, true);
+    const Plan pl = plan_of(p.plan, p.B, p.G);
+    plan_build<kPagesMaxCall, kPagesMaxCall>(p, pl, sc, true);
+    plan_rows<kPagesMaxCall>(p, pl, pl.row);
 }
 
 namespace {
@@ -63,92 +65,104 @@ __device__ __forceinline__ void store_out<__half>(char *o, int d, float4 v) {
     reinterpret_cast<__half2 *>(o + 2 * d)[1] = __floats2half2_rn(v.z, v.w);
 }
 
-// Parts of one (row, head) that a source's walkers left.
-struct PartRange {
-    int w0, n, slot, pair;
-};
+constexpr int kEarly = 8;  // rounds of parts' sums loaded before their weights are known
 }  // namespace
 
 // One warp per (row, query head): the parts of its prefix and of its own keys, in key order.  Lanes take a part each
-// for (m, l), so all weights are known after one round of loads; then the warp adds the parts' sums, LP
-// lanes to a part.
+// for (m, l), so all weights are known after one round of loads; LP lanes take a part's sums, the first kEarly
+// rounds of which are loaded beside (m, l).
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const PagesAttn p) {
     const int lane = threadIdx.x & 31;
     const int bh = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
-    const int b = bh / p.n_heads, h = bh - b * p.n_heads;
+    const int b = (int)((unsigned)bh / (unsigned)p.n_heads), h = bh - b * p.n_heads;
     const Plan pl = plan_of(p.plan, p.B, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
-    const int kvh = (int)((long long)h * p.n_kv_heads / p.n_heads), j = h - first_head(kvh, p.n_heads, p.n_kv_heads);
-    pdl_launch_dependents();
-    pdl_wait();
-    if (b >= p.B) return;
-    // one round of loads: the header, the row's group and its own source
-    const int4 h0 = *reinterpret_cast<const int4 *>(pl.hdr);
-    const int grp = p.G ? pl.group[b] : 0;
-    const int4 own_a = *reinterpret_cast<const int4 *>(&pl.src[p.G + b].t0), own_c = *reinterpret_cast<const int4 *>(&pl.src[p.G + b].key0);
-    const int per = h0.y, per_tc = pl.hdr[kHdrTcPer];
-    if (!h0.z) return;
-    auto range = [&](const int4 &a, const int4 &c) {
-        PartRange r = {};
-        if (a.z) {
-            const int mi = (b - c.z) * gq + j, item = kvh * ((c.w * gq + kM - 1) / kM) + mi / kM;
-            const int u0 = a.x + item * a.z * a.w;
-            r.w0 = walker_of(u0, per);
-            r.n = walker_of(u0 + (a.z - 1) * a.w, per) - r.w0 + 1;
-            r.slot = a.y + item;
-            r.pair = mi % kM;
-        }
-        return r;
-    };
-    const PartRange own = range(own_a, own_c);
-    PartRange rest = {};
-    int tc_n = 0, tc_w0 = 0, tc_base = 0, tc_rows = 0, tc_per = 1;
-    if (p.G) {
-        const int4 ga = *reinterpret_cast<const int4 *>(&pl.src[grp].t0), gc = *reinterpret_cast<const int4 *>(&pl.src[grp].key0);
-        const int kt = pl.tc_kt[grp], t0 = pl.tc_t0[grp], r0 = pl.tc_r0[grp];
-        rest = range(ga, gc);
-        if (kt) {
-            const int row0 = gc.z, n = gc.w * gq, mi = (b - row0) * gq + j;
-            const int run = mi / (2 * kTcRows), r = mi - run * 2 * kTcRows;
-            const int cost = tc_cost(n);
-            const int u0 = t0 + (kvh * tc_runs(n) + run) * kt * cost;
-            tc_rows = min(2 * kTcRows, n - run * 2 * kTcRows);
-            tc_per = tc_rows > kTcRows ? 1 : 2;  // parts a block leaves of this row
-            tc_w0 = walker_of(u0, per_tc);
-            tc_n = (walker_of(u0 + (kt - 1) * cost, per_tc) - tc_w0 + 1) * tc_per;
-            tc_base = r0 + kvh * tc_head_rows(n) + run * 2 * kTcRows + r;
-        }
-    }
-    const int n = tc_n + rest.n + own.n;
+    const int kvh = (int)((unsigned)(h * p.n_kv_heads) / (unsigned)p.n_heads), j = h - first_head(kvh, p.n_heads, p.n_kv_heads);
     const int LP = p.head_size > 64 ? 32 : p.head_size > 32 ? 16 : 8;  // lanes of a part's sums
     const int sub = lane / LP, d = 4 * (lane % LP), at_once = 32 / LP;
     const bool on = d < p.head_size;
-    float m = -CUDART_INF_F, l = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int e0 = 0; e0 < n; e0 += 32) {
-        const int e = e0 + lane;
-        float2 ml = make_float2(-CUDART_INF_F, 0.f);
-        const float *acc = nullptr;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (b >= p.B) return;
+    const int4 h0 = *reinterpret_cast<const int4 *>(pl.hdr);
+    const int per_tc = pl.hdr[kHdrTcPer];
+    const int4 *rp = reinterpret_cast<const int4 *>(pl.row + b);
+    const int4 ow = rp[0], re = rp[1], tc = rp[2];
+    const int gr = rp[3].x, per = h0.y;
+    if (!h0.z) return;
+    // first walker, parts and first row of the parts of the item that holds pair mi of a source of n pairs
+    struct Range {
+        int w0, n, row;
+    };
+    auto range = [&](const int4 &s, int mi, int n) {
+        Range r = {};
+        if (s.z) {
+            const int item = kvh * ((n + kM - 1) / kM) + mi / kM, u0 = s.x + item * (kItemCost + s.z * s.w);
+            r.w0 = walker_of(u0, per);
+            r.n = walker_of(u0 + tile_place(s.z - 1, kItemCost, s.w), per) - r.w0 + 1;
+            r.row = (s.y + item + r.w0) * kM + mi % kM;
+        }
+        return r;
+    };
+    const Range own = range(ow, j, gq);
+    Range rest = {};
+    int tc_n = 0, tc_row = 0, tc_rows = 0, tc_two = 0;
+    if (p.G) {
+        const int n = tc.w * gq, mi = gr * gq + j;
+        rest = range(re, mi, n);
+        if (tc.y) {
+            const int run = mi / (2 * kTcRows), cost = tc_cost(n, p.head_size);
+            const int u0 = tc.x + (kvh * tc_runs(n) + run) * (kTcItemCost + tc.y * cost), w0 = walker_of(u0, per_tc);
+            tc_rows = min(2 * kTcRows, n - run * 2 * kTcRows);
+            tc_two = tc_rows <= kTcRows;  // two parts of this row a block, tc_rows apart
+            tc_n = (walker_of(u0 + tile_place(tc.y - 1, kTcItemCost, cost), per_tc) - w0 + 1) << tc_two;
+            tc_row = tc.z + kvh * tc_head_rows(n) + mi + 2 * kTcRows * w0;
+        }
+    }
+    const int n = tc_n + rest.n + own.n;
+    // (m, l) and sums of part e
+    auto part = [&](int e, const float2 *&ml, const float *&acc) {
         if (e < tc_n) {
-            const int wi = tc_per == 2 ? e >> 1 : e;
-            const size_t at = (size_t)(tc_base + 2 * kTcRows * (tc_w0 + wi) + (e - wi * tc_per) * tc_rows);
-            ml = reinterpret_cast<const float2 *>(p.tc_ml)[at];
+            const size_t at = (size_t)(tc_row + 2 * kTcRows * (e >> tc_two) + (tc_two ? (e & 1) * tc_rows : 0));
+            ml = reinterpret_cast<const float2 *>(p.tc_ml) + at;
             acc = p.tc_acc + at * p.head_size;
-        } else if (e < n) {
-            const bool first = e < tc_n + rest.n;
-            const int w = e - tc_n + (first ? rest.w0 : own.w0 - rest.n);
-            const size_t at = (size_t)((first ? rest.slot : own.slot) + w) * kM + (first ? rest.pair : own.pair);
-            ml = reinterpret_cast<const float2 *>(p.ws_ml)[at];
+        } else {
+            e -= tc_n;
+            const size_t at = (size_t)(e < rest.n ? rest.row + e * kM : own.row + (e - rest.n) * kM);
+            ml = reinterpret_cast<const float2 *>(p.ws_ml) + at;
             acc = p.ws_acc + at * p.head_size;
         }
-        if (ml.x == -CUDART_INF_F && ml.y == 0.f) acc = nullptr;  // a part without keys
+    };
+    auto sums = [&](int e) {
+        const float2 *ml;
+        const float *acc;
+        part(e, ml, acc);
+        return *reinterpret_cast<const float4 *>(acc + d);
+    };
+    float m = -CUDART_INF_F, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int e0 = 0; e0 < n; e0 += 32) {
+        const int e = e0 + lane, cnt = min(32, n - e0);
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        if (e < n) {
+            const float2 *pm;
+            const float *acc;
+            part(e, pm, acc);
+            ml = *pm;
+        }
+        float4 v[kEarly];
+#pragma unroll
+        for (int q = 0; q < kEarly; ++q)
+            if (on && q * at_once + sub < cnt) v[q] = sums(e0 + q * at_once + sub);
+        const bool some = !(ml.x == -CUDART_INF_F && ml.y == 0.f);  // a part without keys has sums of no matter
         float mn = fmaxf(m, ml.x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
         const float base = mn == -CUDART_INF_F ? 0.f : mn;
         const float c0 = exp2f(m - base), wt = exp2f(ml.x - base);
-        float ls = acc ? ml.y * wt : 0.f;
+        float ls = some ? ml.y * wt : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
         l = l * c0 + ls;
@@ -157,27 +171,35 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
         a.y *= c0;
         a.z *= c0;
         a.w *= c0;
-        const int cnt = min(32, n - e0);
-#pragma unroll 8
-        for (int q = 0; q < cnt; q += at_once) {
-            const int from = min(q + sub, 31);
-            const float c1 = __shfl_sync(0xffffffffu, wt, from);
-            const float *src = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(acc), from));
-            if (q + sub < cnt && src && on) {
-                const float4 v = *reinterpret_cast<const float4 *>(src + d);
-                a.x = fmaf(v.x, c1, a.x);
-                a.y = fmaf(v.y, c1, a.y);
-                a.z = fmaf(v.z, c1, a.z);
-                a.w = fmaf(v.w, c1, a.w);
+        const unsigned have = __ballot_sync(0xffffffffu, some);
+        auto add = [&](int q, const float4 &x, float w) {
+            if (on && q < cnt && (have >> q & 1)) {
+                a.x = fmaf(x.x, w, a.x);
+                a.y = fmaf(x.y, w, a.y);
+                a.z = fmaf(x.z, w, a.z);
+                a.w = fmaf(x.w, w, a.w);
             }
+        };
+#pragma unroll
+        for (int q = 0; q < kEarly; ++q) {
+            const int i = q * at_once + sub;
+            add(i, v[q], __shfl_sync(0xffffffffu, wt, i & 31));
+        }
+#pragma unroll 4
+        for (int q = kEarly * at_once; q < cnt; q += at_once) {
+            const int i = q + sub;
+            const float w = __shfl_sync(0xffffffffu, wt, i & 31);
+            if (on && i < cnt) add(i, sums(e0 + i), w);
         }
     }
-    for (int o = 16; o >= LP; o >>= 1) {
-        a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
-        a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
-        a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
-        a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
-    }
+#pragma unroll
+    for (int o = 16; o >= 8; o >>= 1)
+        if (o >= LP) {
+            a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+            a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+            a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+            a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+        }
     // no keys at all: zeros, and a sum of nothing; all scores -inf: 0 / 0, as the formula has it
     const float inv = n ? 1.0f / l : 0.f;
     if (on && sub == 0)
@@ -211,7 +233,7 @@ WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int
     w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * attn_pages_16_warps();  // the most warps
     const size_t tc = G ? tc_part_rows(B, n_heads, n_kv_heads, num_sms) : 0;
     w.plan = 0;
-    w.ml = w.plan + align256(plan_bytes(B, G));
+    w.ml = w.plan + align256(plan_bytes(B, G) + (size_t)B * sizeof(RowPlan));
     w.acc = w.ml + align256(w.parts * kM * 8);
     w.tc_ml = w.acc + align256(w.parts * kM * head_size * 4);
     w.tc_acc = w.tc_ml + align256(tc * 8);

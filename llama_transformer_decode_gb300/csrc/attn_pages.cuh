@@ -13,20 +13,34 @@ constexpr int kM = 16;        // (row, head) pairs of a warp's item
 constexpr int kTcRows = 128;  // pairs of a tensor-core slot; an item has up to two slots' worth
 constexpr int kTcKeys = 128;  // keys of a tensor-core tile
 
+// A walker takes the tiles whose place in the numbering of costs falls into its range.  An item of kt tiles is
+// first + kt * cost long: `first` is what starting an item costs.  Tile 0 stands at its beginning, tile k at first + k * cost.
+__host__ __device__ __forceinline__ int tile_place(int k, int first, int cost) { return k ? first + k * cost : 0; }
+
 // Plan: a header; the sources of the warps (the groups' prefixes, then the rows' own keys: S = G + B, and an end);
 // per group, for the tensor-core role, the cost before it, tiles per item and first row of its parts; the group of
-// each row.
+// each row; and, for the merge, what it needs of a row's three sources.
 enum { kHdrCost = 0, kHdrPer = 1, kHdrOk = 2, kHdrTcCost = 3, kHdrTcPer = 4, kHdrTcBlocks = 5, kHdrInts = 16 };
 struct alignas(16) Source {
     int t0, i0, kt, cost;          // cost and items of the sources before it, tiles per item, cost of a tile
     int key0, key1, row0, rows;    // keys, rows
     int seq, pad[3];               // sequence whose table finds the keys
 };
+struct alignas(16) RowPlan {
+    int own_t0, own_i0, own_kt, own_cost;          // its own keys
+    int rest_t0, rest_i0, rest_kt, rest_cost;      // what is left of its group's prefix
+    int tc_t0, tc_kt, tc_r0, group_rows;           // the prefix's whole tiles
+    int row_in_group, pad[3];
+};
 struct Plan {
     int *hdr;
     Source *src;
     int *tc_t0, *tc_kt, *tc_r0, *group;
+    RowPlan *row;  // in the workspace only
 };
+__host__ __device__ constexpr size_t plan_bytes(int B, int G) {
+    return (kHdrInts * 4 + (size_t)(G + B + 1) * sizeof(Source) + (3 * (size_t)G + 1 + B) * 4 + 127) / 128 * 128;
+}
 __host__ __device__ inline Plan plan_of(void *base, int B, int G) {
     Plan p;
     p.hdr = static_cast<int *>(base);
@@ -35,10 +49,8 @@ __host__ __device__ inline Plan plan_of(void *base, int B, int G) {
     p.tc_kt = p.tc_t0 + G + 1;
     p.tc_r0 = p.tc_kt + G;
     p.group = p.tc_r0 + G;
+    p.row = reinterpret_cast<RowPlan *>(static_cast<char *>(base) + plan_bytes(B, G));
     return p;
-}
-__host__ __device__ constexpr size_t plan_bytes(int B, int G) {
-    return (kHdrInts * 4 + (size_t)(G + B + 1) * sizeof(Source) + (3 * (size_t)G + 1 + B) * 4 + 127) / 128 * 128;
 }
 // A call of at most this many sources is planned by every block of its kernel for itself, in shared memory: about
 // 2 us of latency where a kernel of its own before it costs 6.  Larger calls have such a kernel.
@@ -51,9 +63,8 @@ __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (int)((unsig
 __host__ __device__ __forceinline__ int heads_per_kv(int H, int KV) { return cdiv(H, KV); }
 __device__ __forceinline__ int first_head(int g, int H, int KV) { return cdiv(g * H, KV); }
 
-// A total cost T is cut into ranges of `per`: walker w takes the tiles that start in [w per, (w + 1) per), and a cost x
-// falls to walker x / per.  per is at least the cost of a tile, so every walker between those of an
-// item's first and last tile holds one of its tiles.
+// A total cost T is cut into ranges of `per`: a cost x falls to walker x / per.  per is at least the distance of two tiles, so
+// every walker between those of an item's first and last tile holds one of its tiles.
 __device__ __forceinline__ int walker_of(int x, int per) { return (int)((unsigned)x / (unsigned)per); }
 
 // Tensor-core items of a group: n pairs (row, head) of one KV head in runs of up to 256.  A run of up to 128
@@ -71,11 +82,14 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n) {  // of all runs of
 // Cost of a tile of an item of n pairs, in quarters of reading it.  16-bit: reading bounds every size.  fp32 FMAs take
 // over from 8 pairs on; measured on GB300, 1 GB of suffixes of head size 128 / 64: 166 / 167 us at 1 pair, 174 / 167 at
 // 4, 198 / 198 at 8, 271 / 279 at 16.
-constexpr int kCostUnit = 4;
-__host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : 7; }
-// Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of 8 KB): reading its 32 KB while the
-// slots take turns, the slots' time when both work on every tile.
-__host__ __device__ __forceinline__ int tc_cost(int n) { return n > kTcRows ? 28 : 16; }
+// Starting an item (its queries, its part) takes a warp 1.25 us where a tile takes 1.55.
+constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
+__host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }
+// Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of reading 8 KB, 0.049 us an SM).  Measured
+// at prefixes of 131072: head size 64, 0.84 to 0.95 us up to 128 pairs, 1.67 at 136, 1.86 at 256; head size 128, 1.40
+// (reading), 1.66, 2.10.  Starting an item: its queries, its part, and the pipeline's filling.
+constexpr int kTcItemCost = 60, kTcMaxTileCost = 42;
+__host__ __device__ __forceinline__ int tc_cost(int n, int hs) { return n > kTcRows ? (hs > 64 ? 42 : 38) : (hs > 64 ? 30 : 18); }
 
 // The last entry i of an ascending list of n (every `stride`-th int of a, the first at most x) that is at most x,
 // found by a whole warp.
@@ -142,13 +156,22 @@ struct Walk {
             const int4 a = *reinterpret_cast<const int4 *>(&pl.src[src].t0), b = *reinterpret_cast<const int4 *>(&pl.src[src].key0);
             const int kt = a.z, cost = a.w, n = b.w * gq, tiles_m = (n + kM - 1) / kM;
             if (kt == 0) continue;
-            const int i = cdiv(x - a.x, cost), item = (int)((unsigned)i / (unsigned)kt);  // tile, item of the source
-            x = a.x + i * cost;
+            x = max(x, a.x);
+            const int len = kItemCost + kt * cost;
+            int item = (int)((unsigned)(x - a.x) / (unsigned)len), at = a.x + item * len;  // item of the source, its place
+            int k_first = x == at ? 0 : max(1, cdiv(max(x - at - kItemCost, 0), cost));
+            if (k_first >= kt) {
+                ++item;
+                at += len;
+                k_first = 0;
+            }
+            x = at + tile_place(k_first, kItemCost, cost);
             if (item >= tiles_m * p.n_kv_heads) continue;
             if (x >= x1) break;
-            const int k_first = i - item * kt, kvh = (int)((unsigned)item / (unsigned)tiles_m), m0 = (item - kvh * tiles_m) * kM;
-            rem = min(kt - k_first, cdiv(x1 - x, cost));
-            x += rem * cost;
+            const int kvh = (int)((unsigned)item / (unsigned)tiles_m), m0 = (item - kvh * tiles_m) * kM;
+            const int end = min(kt, max(k_first + 1, cdiv(max(x1 - at - kItemCost, 0), cost)));
+            rem = end - k_first;
+            x = end == kt ? at + len : at + tile_place(end, kItemCost, cost);
             key = b.x + k_first * KT;
             key1 = b.y;
             head = kvh * p.head_stride;

@@ -192,19 +192,28 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
             if (x >= x_end) return false;
             const int kt = pl.tc_kt[grp], t0 = pl.tc_t0[grp];
             if (kt == 0) continue;
-            const int n = pl.src[grp].rows * gq, runs = tc_runs(n), cost = tc_cost(n), i = cdiv(x - t0, cost), item = (int)((unsigned)i / (unsigned)kt);
-            x = t0 + i * cost;
+            const int n = pl.src[grp].rows * gq, runs = tc_runs(n), cost = tc_cost(n, HS), len = kTcItemCost + kt * cost;
+            x = max(x, t0);
+            int item = (int)((unsigned)(x - t0) / (unsigned)len), at = t0 + item * len;
+            int k0 = x == at ? 0 : max(1, cdiv(max(x - at - kTcItemCost, 0), cost));
+            if (k0 >= kt) {
+                ++item;
+                at += len;
+                k0 = 0;
+            }
+            x = at + tile_place(k0, kTcItemCost, cost);
             if (item >= runs * p.n_kv_heads) continue;
             if (x >= x_end) return false;
+            const int end = min(kt, max(k0 + 1, cdiv(max(x_end - at - kTcItemCost, 0), cost)));
+            x = end == kt ? at + len : at + tile_place(end, kTcItemCost, cost);
             g.group = grp;
             g.kvh = (int)((unsigned)item / (unsigned)runs);
             const int run = item - g.kvh * runs;
             g.m0 = run * 2 * kTcRows;
             g.rows = min(2 * kTcRows, n - g.m0);
-            g.k0 = i - item * kt;
-            g.n = min(kt - g.k0, cdiv(x_end - x, cost));
+            g.k0 = k0;
+            g.n = end - k0;
             g.out = pl.tc_r0[grp] + g.kvh * tc_head_rows(n) + g.m0 + 2 * kTcRows * bid;
-            x += g.n * cost;
             return true;
         }
     };

@@ -5,10 +5,10 @@
 
 namespace l2 {
 
-// Fewest tiles a warp takes: below that the parts cost more to write and merge than the parallel reading gains.  (Their cost
-// is also at least that of one tile of any kind, see walker_of.)
-constexpr int kMinTiles = 2;
-constexpr int kTcMinCost = 32;  // least cost of a block in the tensor-core role
+// Least cost of a range: fewer than two tiles a warp cost more to write and merge as parts than the parallel reading gains.  (And
+// at least the distance of two tiles of any kind, see walker_of.)
+constexpr int kMinPer = kItemCost + 2 * kCostUnit, kTcMinPer = kTcItemCost + kTcMaxTileCost;
+static_assert(kMinPer >= kItemCost + kMaxTileCost, "every walker between an item's first and last must hold a tile of it");
 
 template <int NT, int MAX>
 struct PlanScratch {
@@ -94,7 +94,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         __syncthreads();
         // prefixes worth it go to the tensor cores in whole tiles; what is left of them stays with the warps
         const int n = i < p.G ? (sc.gstart[i + 1] - sc.gstart[i]) * gq : 0, full = i < p.G && p.tc && n > kM ? sc.minlen[i] / kTcKeys : 0;
-        const int2 before = plan_scan<NT>(full ? make_int2(full * tc_runs(n) * p.n_kv_heads * tc_cost(n), tc_head_rows(n) * p.n_kv_heads)
+        const int2 before = plan_scan<NT>(full ? make_int2((kTcItemCost + full * tc_cost(n, p.head_size)) * tc_runs(n) * p.n_kv_heads, tc_head_rows(n) * p.n_kv_heads)
                                                : make_int2(0, 0), &tc_all, sc.sums[0]);
         if (i < p.G) {
             pl.tc_t0[i] = before.x;
@@ -125,7 +125,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         e.cost = tile_cost(p.dtype, min(e.rows * gq, kM));
         const int items = e.kt ? (e.rows * gq + kM - 1) / kM * p.n_kv_heads : 0;
         int2 here;
-        const int2 before = plan_scan<NT>(make_int2(items * e.kt * e.cost, items), &here, sc.sums[1]);
+        const int2 before = plan_scan<NT>(make_int2(items * (kItemCost + e.kt * e.cost), items), &here, sc.sums[1]);
         e.t0 = all.x + before.x;
         e.i0 = all.y + before.y;
         if (s < S) pl.src[s] = e;
@@ -136,16 +136,16 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     if (i == 0) {
         const int cost = all.x, tc = tc_all.x;
         // blocks of the two roles by cost, at least one of each that has work
-        int n_tc = 0, per_tc = kTcMinCost;
+        int n_tc = 0, per_tc = kTcMinPer;
         if (tc) {
             n_tc = (int)((float)p.num_sms * ((float)tc / ((float)tc + (float)cost)) + 0.5f);
             n_tc = max(1, min(n_tc, p.num_sms - (cost ? 1 : 0)));
-            per_tc = max(kTcMinCost, cdiv(tc, n_tc));
+            per_tc = max(kTcMinPer, cdiv(tc, n_tc));
             n_tc = cdiv(tc, per_tc);
         }
         pl.src[S].t0 = cost;
         pl.hdr[kHdrCost] = cost;
-        pl.hdr[kHdrPer] = max(kMinTiles * kCostUnit, cdiv(cost, (p.num_sms - n_tc) * p.walk_warps));
+        pl.hdr[kHdrPer] = max(kMinPer, cdiv(cost, (p.num_sms - n_tc) * p.walk_warps));
         pl.hdr[kHdrTcCost] = tc;
         pl.hdr[kHdrTcPer] = per_tc;
         pl.hdr[kHdrTcBlocks] = n_tc;
@@ -153,6 +153,34 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         pl.hdr[kHdrOk] = 1;
     }
     __syncthreads();
+}
+
+// What the merge needs of each row, from a plan that is complete.
+template <int NT>
+__device__ __forceinline__ void plan_rows(const PagesAttn &p, const Plan &pl, RowPlan *rows) {
+#pragma unroll 1
+    for (int b = threadIdx.x; b < p.B; b += NT) {
+        RowPlan r = {};
+        const Source &o = pl.src[p.G + b];
+        r.own_t0 = o.t0;
+        r.own_i0 = o.i0;
+        r.own_kt = o.kt;
+        r.own_cost = o.cost;
+        if (p.G && pl.hdr[kHdrOk]) {
+            const int g = pl.group[b];
+            const Source &e = pl.src[g];
+            r.rest_t0 = e.t0;
+            r.rest_i0 = e.i0;
+            r.rest_kt = e.kt;
+            r.rest_cost = e.cost;
+            r.tc_t0 = pl.tc_t0[g];
+            r.tc_kt = pl.tc_kt[g];
+            r.tc_r0 = pl.tc_r0[g];
+            r.group_rows = e.rows;
+            r.row_in_group = b - e.row0;
+        }
+        rows[b] = r;
+    }
 }
 
 // The plan as a kernel's block uses it: built here (mem: kPlanSmem bytes, scratch: free until the caller's first
@@ -163,9 +191,9 @@ __device__ __forceinline__ Plan plan_here(const PagesAttn &p, void *mem, void *s
     const Plan pl = plan_of(mem, p.B, p.G);
     plan_build<NT, kPlanInBlock>(p, pl, *static_cast<PlanScratch<NT, kPlanInBlock> *>(scratch), keep);
     if (keep) {
-        const int n = (int)(plan_bytes(p.B, p.G) / 4);
-#pragma unroll 1
-        for (int i = threadIdx.x; i < n; i += NT) p.plan[i] = static_cast<const int *>(mem)[i];
+        const Plan out = plan_of(p.plan, p.B, p.G);
+        if (threadIdx.x < kHdrInts) out.hdr[threadIdx.x] = pl.hdr[threadIdx.x];
+        plan_rows<NT>(p, pl, out.row);
     }
     return pl;
 }

@@ -139,7 +139,7 @@ int check_attn_shape(const char *who, const L2Pages *p, int B, int G, int n_head
         return refuse(L2_EINVAL, "%s: n_heads = %d outside n_kv_heads..1024", who, n_heads);
     // tiles are numbered in 32 bits
     const long long gq = (n_heads + p->n_kv_heads - 1) / p->n_kv_heads, items = 2ll * B * ((gq + 15) / 16 + 1) * p->n_kv_heads;
-    if (items * (((long long)p->max_pages * p->page_size + 7) / 8) * 7 > 0x7fffffffll)
+    if (items * ((((long long)p->max_pages * p->page_size + 7) / 8) * 7 + 64) > 0x7fffffffll)
         return refuse(L2_EINVAL, "%s: B, heads and max_pages * page_size are too large together", who);
     return L2_OK;
 }
