@@ -14,7 +14,7 @@
 //   warp 0     tiles of K and V by TMA into two rings (128-byte swizzle; a box is a page's rows
 //              that fall into the tile, so pages of 8, 16, 32, 64 rows or a multiple of 128 are gathered
 //              without a copy); rows past the prefix are never loaded, so nothing is masked
-//   warp 1     one thread polls the barriers and issues whichever product is ready
+//   warp 1     polls the barriers and issues whichever product is ready
 //   warps 4-7, 8-11  slots 0 and 1: queries to shared memory, softmax, parts out
 // A thread owns one pair: its row of scores is a lane of tensor memory, so max and sum need no
 // exchange.  The weights go back over the scores as 16-bit values (half a step of the type, 2^-9 in bf16
@@ -65,7 +65,11 @@ struct TcShape {
     static constexpr int kBlocks = HS / 64;                  // 64-value blocks of a row
     static constexpr uint32_t kBlock = KT * 128, kQBlock = kTcRows * 128;
     static constexpr uint32_t kTile = kBlocks * kBlock, kQ = kBlocks * kQBlock;
-    static constexpr int kStages = HS == 64 ? 5 : 2;         // of each ring
+    // Stages of each ring, an even number: tiles alternate between the slots, so the tile before in a stage was the same
+    // slot's, and whoever waits for a tile has seen that one arrive.  (A slot that waited two phases of a barrier ahead would
+    // take the phase before for its own.)
+    static constexpr int kStages = HS == 64 ? 4 : 2;
+    static_assert(kStages % 2 == 0, "see above");
     static constexpr uint32_t kTiles = 2 * kQ + 2 * kStages * kTile;
     static constexpr uint32_t kSmem = 1024 + 1024 + kTiles;  // alignment, barriers
     static constexpr int kP = kOwnP ? KT : 0, kO = HS == 64 ? 192 : 128;
@@ -74,7 +78,7 @@ struct TcShape {
 
 struct TcFx {
     uint64_t full_k[kRing], empty_k[kRing], full_v[kRing], empty_v[kRing];
-    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2];
+    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], fin;
     uint32_t tmem;
     int abort;
 };
@@ -168,6 +172,7 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
             mbar_init(&fx.p_full[i], kSlotThreads);
             mbar_init(&fx.pv_done[i], 1);
         }
+        mbar_init(&fx.fin, 1);
         fence_barrier_init();
         fx.abort = 0;
     }
@@ -265,7 +270,12 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
             }
             t += g.n;
         }
-        // copies in flight land before the block's memory goes (all have, when the others finished)
+        // the last stages' releases land before the block's memory goes; copies in flight do where something gave up
+        for (int tt = max(0, t - Sh::kStages); tt < t && ok; ++tt) {
+            const int st = tt % Sh::kStages;
+            ok = wait_or_stop(fx, &fx.empty_k[st], (uint32_t)((tt / Sh::kStages) & 1), p.err) &&
+                 wait_or_stop(fx, &fx.empty_v[st], (uint32_t)((tt / Sh::kStages) & 1), p.err);
+        }
         if (!ok) {
             for (int st = 0; st < Sh::kStages; ++st)
                 for (int ph = 0; ph < 2; ++ph) {
@@ -274,81 +284,98 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
                 }
         }
     } else if (warp == 1) {
-        // ---------------- products: one thread, whichever is ready ----------------
-        if (lane == 0) {
-            int grp = grp0, t_base = 0, x = x_begin;
-            int np[2] = {0, 0}, nd[2] = {0, 0}, nseg = 0;  // weights taken, second products awaited per slot; segments begun
-            const uint32_t id_qk = idesc_f16(BF, kTcRows, Sh::KT, false), id_pv = idesc_f16(BF, kTcRows, HS, true);
-            bool ok = true;
-            for (Seg g; ok && segment(x, grp, g); ++nseg) {
-                const bool both = g.rows > kTcRows;
-                int qk[2] = {0, 0}, pv[2] = {0, 0};  // products issued
-                const int cnt[2] = {slot_tiles(g, 0), slot_tiles(g, 1)};
-                bool in[2] = {false, false};         // the slot's queries, then its current weights, are in
-                uint32_t idle = 0;
-                uint64_t t_idle = 0;
-                while (pv[0] < cnt[0] || pv[1] < cnt[1]) {
-                    bool moved = false;
+        // ---------------- products: whichever is ready ----------------
+        // The whole warp keeps the books, with values every lane shares (a shuffle from lane 0 tells the compiler so), and one
+        // lane issues: descriptors then stay in uniform registers.  Issued from inside a one-lane branch instead, a tile's
+        // twelve products took 0.74 us.
+        auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+        auto ready = [](uint64_t *bar, int parity) { return __any_sync(0xffffffffu, mbar_test(bar, (uint32_t)parity)); };
+        const uint32_t tm = (uint32_t)uniform((int)tmem);
+        int grp = grp0, t_base = 0, x = x_begin;
+        int np[2] = {0, 0}, nd[2] = {0, 0}, nseg = 0;  // weights taken, second products awaited per slot; segments begun
+        const uint32_t id_qk = idesc_f16(BF, kTcRows, Sh::KT, false), id_pv = idesc_f16(BF, kTcRows, HS, true);
+        bool ok = true;
+        for (Seg g; ok && segment(x, grp, g); ++nseg) {
+            const bool both = g.rows > kTcRows;
+            int qk[2] = {0, 0}, pv[2] = {0, 0};  // products issued
+            const int cnt[2] = {uniform(slot_tiles(g, 0)), uniform(slot_tiles(g, 1))};
+            bool in[2] = {false, false};   // the slot's current weights are in
+            bool q_in[2] = {false, false};  // the slot's queries are (awaited of a slot without tiles too: every phase is seen)
+            uint32_t idle = 0;
+            uint64_t t_idle = 0;
+            while (pv[0] < cnt[0] || pv[1] < cnt[1] || !q_in[0] || !q_in[1]) {
+                bool moved = false;
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (pv[s] < qk[s]) {
-                            // the second product, once the weights of the slot's last scores are in
-                            if (!in[s]) in[s] = mbar_test(&fx.p_full[s], (uint32_t)(np[s] & 1));
-                            const int t = t_base + slot_tile(g, s, pv[s]), st = t % Sh::kStages;
-                            if (in[s] && mbar_test(&fx.full_v[st], (uint32_t)((t / Sh::kStages) & 1))) {
-                                tc_fence_after();
-                                const uint64_t dv = desc_sw128_mn(v_at + st * Sh::kTile, Sh::kBlock);
+                for (int s = 0; s < 2; ++s) {
+                    if (!q_in[s] && !(q_in[s] = ready(&fx.q_full[s], nseg & 1))) continue;
+                    if (pv[s] < qk[s]) {
+                        // the second product, once the weights of the slot's last scores are in
+                        if (!in[s] && !(in[s] = ready(&fx.p_full[s], np[s] & 1))) continue;
+                        const int t = uniform(t_base + slot_tile(g, s, pv[s])), st = t % Sh::kStages;
+                        if (ready(&fx.full_v[st], (t / Sh::kStages) & 1)) {
+                            tc_fence_after();
+                            const uint64_t dv = desc_sw128_mn(v_at + st * Sh::kTile, Sh::kBlock);
+                            const uint32_t first = pv[s] ? 1u : 0u;
+                            ++pv[s];
+                            ++np[s];
+                            in[s] = false;
+                            const bool free_v = !both || pv[s ^ 1] >= pv[s], tell = !Sh::kOwnP || pv[s] == cnt[s];
+                            if (tell) ++nd[s];
+                            if (elect_one()) {
 #pragma unroll
                                 for (int k = 0; k < Sh::KT / 16; ++k)  // 16 keys: 8 columns of weights, 16 lines of V
-                                    mma_f16_ta(o_col(s), p_col(s) + 8 * k, dv + (uint64_t)(k * (16 * 128 >> 4)), id_pv, pv[s] || k ? 1u : 0u);
-                                ++pv[s];
-                                ++np[s];
-                                in[s] = false;
-                                if (!both || pv[s ^ 1] >= pv[s]) mma_commit(&fx.empty_v[st]);
-                                if (!Sh::kOwnP || pv[s] == cnt[s]) {
-                                    mma_commit(&fx.pv_done[s]);
-                                    ++nd[s];
-                                }
-                                moved = true;
+                                    mma_f16_ta(tm + 256 * s + Sh::kO, tm + 256 * s + Sh::kP + 8 * k, dv + (uint64_t)(k * (16 * 128 >> 4)),
+                                               id_pv, k ? 1u : first);
+                                if (free_v) mma_commit(&fx.empty_v[st]);
+                                if (tell) mma_commit(&fx.pv_done[s]);
                             }
-                        }
-                        if (qk[s] < cnt[s] && pv[s] == qk[s]) {
-                            // the next scores: the last ones were read before their weights came (and the weights over
-                            // them by the second product, where they share columns)
-                            const int t = t_base + slot_tile(g, s, qk[s]), st = t % Sh::kStages;
-                            const bool q_in = qk[s] ? Sh::kOwnP || mbar_test(&fx.pv_done[s], (uint32_t)((nd[s] - 1) & 1))
-                                                    : mbar_test(&fx.q_full[s], (uint32_t)(nseg & 1));
-                            if (q_in && mbar_test(&fx.full_k[st], (uint32_t)((t / Sh::kStages) & 1))) {
-                                tc_fence_after();
-                                const uint64_t dq = desc_sw128(q_at + s * Sh::kQ), dk = desc_sw128(k_at + st * Sh::kTile);
-#pragma unroll
-                                for (int k = 0; k < HS / 16; ++k)  // 32 bytes a step, blocks of 4 steps
-                                    mma_bf16(s_col(s), dq + (uint64_t)(((k >> 2) * Sh::kQBlock + (k & 3) * 32) >> 4),
-                                             dk + (uint64_t)(((k >> 2) * Sh::kBlock + (k & 3) * 32) >> 4), id_qk, k ? 1u : 0u);
-                                ++qk[s];
-                                mma_commit(&fx.s_full[s]);  // and the second product before it
-                                if (!both || qk[s ^ 1] >= qk[s]) mma_commit(&fx.empty_k[st]);
-                                moved = true;
-                            }
+                            __syncwarp();
+                            moved = true;
                         }
                     }
-                    if (moved) {
-                        idle = 0;
-                    } else if ((++idle & 255u) == 0) {
-                        const uint64_t now = globaltimer_ns();
-                        if (idle == 256u) t_idle = now;
-                        if (stopped(fx) || now - t_idle > kWaitLimitNs) {
-                            if (!stopped(fx)) atomicOr(p.err, L2_DEV_ERR_TIMEOUT);
-                            stop(fx);
-                            ok = false;
-                            break;
+                    if (qk[s] < cnt[s] && pv[s] == qk[s]) {
+                        // the next scores: the last ones were read before their weights came (and the weights over
+                        // them by the second product, where they share columns)
+                        if (!Sh::kOwnP && qk[s] && !ready(&fx.pv_done[s], (nd[s] - 1) & 1)) continue;
+                        const int t = uniform(t_base + slot_tile(g, s, qk[s])), st = t % Sh::kStages;
+                        if (ready(&fx.full_k[st], (t / Sh::kStages) & 1)) {
+                            tc_fence_after();
+                            const uint64_t dq = desc_sw128(q_at + s * Sh::kQ), dk = desc_sw128(k_at + st * Sh::kTile);
+                            ++qk[s];
+                            const bool free_k = !both || qk[s ^ 1] >= qk[s];
+                            if (elect_one()) {
+#pragma unroll
+                                for (int k = 0; k < HS / 16; ++k)  // 32 bytes a step, blocks of 4 steps
+                                    mma_bf16(tm + 256 * s, dq + (uint64_t)(((k >> 2) * Sh::kQBlock + (k & 3) * 32) >> 4),
+                                             dk + (uint64_t)(((k >> 2) * Sh::kBlock + (k & 3) * 32) >> 4), id_qk, k ? 1u : 0u);
+                                mma_commit(&fx.s_full[s]);  // and the second product before it
+                                if (free_k) mma_commit(&fx.empty_k[st]);
+                            }
+                            __syncwarp();
+                            moved = true;
                         }
                     }
                 }
-                t_base += g.n;
+                if (moved) {
+                    idle = 0;
+                } else if ((++idle & 255u) == 0) {
+                    const uint64_t now = globaltimer_ns();
+                    if (idle == 256u) t_idle = now;
+                    if (__any_sync(0xffffffffu, stopped(fx) || now - t_idle > kWaitLimitNs)) {
+                        if (lane == 0 && !stopped(fx)) atomicOr(p.err, L2_DEV_ERR_TIMEOUT);
+                        stop(fx);
+                        ok = false;
+                        break;
+                    }
+                }
             }
+            t_base += g.n;
         }
-        __syncwarp();
+        if (!ok) {  // products in flight end before their memory goes
+            if (elect_one()) mma_commit(&fx.fin);
+            __syncwarp();
+            (void)mbar_wait_limit(&fx.fin, 0, p.err, 1000000ull);
+        }
     } else if (warp >= 4) {
         // ---------------- softmax warps ----------------
         const int s = (warp - 4) >> 2, rl = (tid - 128) & (kSlotThreads - 1);  // slot, lane within it
