@@ -14,7 +14,7 @@
 //   warp 0     tiles of K and V by TMA into two rings (128-byte swizzle; a box is a page's rows
 //              that fall into the tile, so pages of 8, 16, 32, 64 rows or a multiple of 128 are gathered
 //              without a copy); rows past the prefix are never loaded, so nothing is masked
-//   warp 1     polls the barriers and issues whichever product is ready
+//   warps 1-2  the products of slots 0 and 1
 //   warps 4-7, 8-11  slots 0 and 1: queries to shared memory, softmax, parts out
 // A thread owns one pair: its row of scores is a lane of tensor memory, so max and sum need no
 // exchange.  The weights go back over the scores as 16-bit values (half a step of the type, 2^-9 in bf16
@@ -78,22 +78,11 @@ struct TcShape {
 
 struct TcFx {
     uint64_t full_k[kRing], empty_k[kRing], full_v[kRing], empty_v[kRing];
-    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], fin;
+    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], fin[2];
     uint32_t tmem;
     int abort;
 };
 static_assert(sizeof(TcFx) <= 1024, "the fixed block must fit before the tiles");
-
-// Whether a phase of `bar` is over, without suspending the thread.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
 
 __device__ __forceinline__ void tensor4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
     asm volatile(
@@ -162,9 +151,9 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
     if (tid == 0) {
         for (int i = 0; i < Sh::kStages; ++i) {
             mbar_init(&fx.full_k[i], 1);
-            mbar_init(&fx.empty_k[i], 1);
+            mbar_init(&fx.empty_k[i], 2);  // a release by each slot
             mbar_init(&fx.full_v[i], 1);
-            mbar_init(&fx.empty_v[i], 1);
+            mbar_init(&fx.empty_v[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&fx.q_full[i], kSlotThreads);
@@ -172,7 +161,8 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
             mbar_init(&fx.p_full[i], kSlotThreads);
             mbar_init(&fx.pv_done[i], 1);
         }
-        mbar_init(&fx.fin, 1);
+        mbar_init(&fx.fin[0], 1);
+        mbar_init(&fx.fin[1], 1);
         fence_barrier_init();
         fx.abort = 0;
     }
@@ -283,98 +273,73 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
                     (void)mbar_wait_limit(&fx.full_v[st], ph, p.err, 1000000ull);
                 }
         }
-    } else if (warp == 1) {
-        // ---------------- products: whichever is ready ----------------
+    } else if (warp <= 2) {
+        // ---------------- products: a warp per slot ----------------
         // The whole warp keeps the books, with values every lane shares (a shuffle from lane 0 tells the compiler so), and one
-        // lane issues: descriptors then stay in uniform registers.  Issued from inside a one-lane branch instead, a tile's
-        // twelve products took 0.74 us.
+        // lane issues: descriptors then stay in uniform registers.  (Issued from inside a one-lane branch, a tile's twelve products
+        // took 0.74 us; one warp for both slots let each slot wait behind the other's issue: 2.6 us a tile at head size 128.)
+        const int s = warp - 1;
         auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-        auto ready = [](uint64_t *bar, int parity) { return __any_sync(0xffffffffu, mbar_test(bar, (uint32_t)parity)); };
-        const uint32_t tm = (uint32_t)uniform((int)tmem);
-        int grp = grp0, t_base = 0, x = x_begin;
-        int np[2] = {0, 0}, nd[2] = {0, 0}, nseg = 0;  // weights taken, second products awaited per slot; segments begun
-        const uint32_t id_qk = idesc_f16(BF, kTcRows, Sh::KT, false), id_pv = idesc_f16(BF, kTcRows, HS, true);
         bool ok = true;
+        auto await = [&](uint64_t *bar, int parity) {
+            ok = __all_sync(0xffffffffu, wait_or_stop(fx, bar, (uint32_t)parity & 1u, p.err));
+            return ok;
+        };
+        const uint32_t tm = (uint32_t)uniform((int)tmem) + 256 * s;
+        const uint32_t id_qk = idesc_f16(BF, kTcRows, Sh::KT, false), id_pv = idesc_f16(BF, kTcRows, HS, true);
+        int grp = grp0, t_base = 0, x = x_begin, n_p = 0, n_pv = 0, nseg = 0;  // weights taken, second products told of, items begun
         for (Seg g; ok && segment(x, grp, g); ++nseg) {
             const bool both = g.rows > kTcRows;
-            int qk[2] = {0, 0}, pv[2] = {0, 0};  // products issued
-            const int cnt[2] = {uniform(slot_tiles(g, 0)), uniform(slot_tiles(g, 1))};
-            bool in[2] = {false, false};   // the slot's current weights are in
-            bool q_in[2] = {false, false};  // the slot's queries are (awaited of a slot without tiles too: every phase is seen)
-            uint32_t idle = 0;
-            uint64_t t_idle = 0;
-            while (pv[0] < cnt[0] || pv[1] < cnt[1] || !q_in[0] || !q_in[1]) {
-                bool moved = false;
+            const int cnt = uniform(slot_tiles(g, s));
+            // the scores of tile i, once its K is there
+            auto scores = [&](int i) {
+                const int t = uniform(t_base + slot_tile(g, s, i)), st = t % Sh::kStages;
+                if (!await(&fx.full_k[st], t / Sh::kStages)) return;
+                tc_fence_after();
+                const uint64_t dq = desc_sw128(q_at + s * Sh::kQ), dk = desc_sw128(k_at + st * Sh::kTile);
+                if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (!q_in[s] && !(q_in[s] = ready(&fx.q_full[s], nseg & 1))) continue;
-                    if (pv[s] < qk[s]) {
-                        // the second product, once the weights of the slot's last scores are in
-                        if (!in[s] && !(in[s] = ready(&fx.p_full[s], np[s] & 1))) continue;
-                        const int t = uniform(t_base + slot_tile(g, s, pv[s])), st = t % Sh::kStages;
-                        if (ready(&fx.full_v[st], (t / Sh::kStages) & 1)) {
-                            tc_fence_after();
-                            const uint64_t dv = desc_sw128_mn(v_at + st * Sh::kTile, Sh::kBlock);
-                            const uint32_t first = pv[s] ? 1u : 0u;
-                            ++pv[s];
-                            ++np[s];
-                            in[s] = false;
-                            const bool free_v = !both || pv[s ^ 1] >= pv[s], tell = !Sh::kOwnP || pv[s] == cnt[s];
-                            if (tell) ++nd[s];
-                            if (elect_one()) {
-#pragma unroll
-                                for (int k = 0; k < Sh::KT / 16; ++k)  // 16 keys: 8 columns of weights, 16 lines of V
-                                    mma_f16_ta(tm + 256 * s + Sh::kO, tm + 256 * s + Sh::kP + 8 * k, dv + (uint64_t)(k * (16 * 128 >> 4)),
-                                               id_pv, k ? 1u : first);
-                                if (free_v) mma_commit(&fx.empty_v[st]);
-                                if (tell) mma_commit(&fx.pv_done[s]);
-                            }
-                            __syncwarp();
-                            moved = true;
-                        }
-                    }
-                    if (qk[s] < cnt[s] && pv[s] == qk[s]) {
-                        // the next scores: the last ones were read before their weights came (and the weights over
-                        // them by the second product, where they share columns)
-                        if (!Sh::kOwnP && qk[s] && !ready(&fx.pv_done[s], (nd[s] - 1) & 1)) continue;
-                        const int t = uniform(t_base + slot_tile(g, s, qk[s])), st = t % Sh::kStages;
-                        if (ready(&fx.full_k[st], (t / Sh::kStages) & 1)) {
-                            tc_fence_after();
-                            const uint64_t dq = desc_sw128(q_at + s * Sh::kQ), dk = desc_sw128(k_at + st * Sh::kTile);
-                            ++qk[s];
-                            const bool free_k = !both || qk[s ^ 1] >= qk[s];
-                            if (elect_one()) {
-#pragma unroll
-                                for (int k = 0; k < HS / 16; ++k)  // 32 bytes a step, blocks of 4 steps
-                                    mma_bf16(tm + 256 * s, dq + (uint64_t)(((k >> 2) * Sh::kQBlock + (k & 3) * 32) >> 4),
-                                             dk + (uint64_t)(((k >> 2) * Sh::kBlock + (k & 3) * 32) >> 4), id_qk, k ? 1u : 0u);
-                                mma_commit(&fx.s_full[s]);  // and the second product before it
-                                if (free_k) mma_commit(&fx.empty_k[st]);
-                            }
-                            __syncwarp();
-                            moved = true;
-                        }
-                    }
+                    for (int k = 0; k < HS / 16; ++k)  // 32 bytes a step, blocks of 4 steps
+                        mma_bf16(tm, dq + (uint64_t)(((k >> 2) * Sh::kQBlock + (k & 3) * 32) >> 4),
+                                 dk + (uint64_t)(((k >> 2) * Sh::kBlock + (k & 3) * 32) >> 4), id_qk, k ? 1u : 0u);
+                    mma_commit(&fx.s_full[s]);  // and the second product before it
+                    mma_commit(&fx.empty_k[st]);
+                    if (!both) mma_commit(&fx.empty_k[st]);  // for the slot that does not use it
                 }
-                if (moved) {
-                    idle = 0;
-                } else if ((++idle & 255u) == 0) {
-                    const uint64_t now = globaltimer_ns();
-                    if (idle == 256u) t_idle = now;
-                    if (__any_sync(0xffffffffu, stopped(fx) || now - t_idle > kWaitLimitNs)) {
-                        if (lane == 0 && !stopped(fx)) atomicOr(p.err, L2_DEV_ERR_TIMEOUT);
-                        stop(fx);
-                        ok = false;
-                        break;
-                    }
+                __syncwarp();
+            };
+            if (!await(&fx.q_full[s], nseg)) break;  // seen for every item, of a slot without tiles too
+            if (cnt) scores(0);
+            for (int i = 0; i < cnt && ok; ++i) {
+                // the second product, once the weights of the last scores are in (those scores have been read by then)
+                const int t = uniform(t_base + slot_tile(g, s, i)), st = t % Sh::kStages;
+                if (!await(&fx.p_full[s], n_p) || !await(&fx.full_v[st], t / Sh::kStages)) break;
+                ++n_p;
+                tc_fence_after();
+                const uint64_t dv = desc_sw128_mn(v_at + st * Sh::kTile, Sh::kBlock);
+                const bool tell = !Sh::kOwnP || i + 1 == cnt;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < Sh::KT / 16; ++k)  // 16 keys: 8 columns of weights, 16 lines of V
+                        mma_f16_ta(tm + Sh::kO, tm + Sh::kP + 8 * k, dv + (uint64_t)(k * (16 * 128 >> 4)), id_pv, i || k ? 1u : 0u);
+                    if (tell) mma_commit(&fx.pv_done[s]);
+                    mma_commit(&fx.empty_v[st]);
+                    if (!both) mma_commit(&fx.empty_v[st]);
+                }
+                __syncwarp();
+                if (tell) ++n_pv;
+                if (i + 1 < cnt) {
+                    // where the weights lie over the scores, the next scores wait for the product that reads them
+                    if (!Sh::kOwnP && !await(&fx.pv_done[s], n_pv - 1)) break;
+                    scores(i + 1);
                 }
             }
             t_base += g.n;
         }
         if (!ok) {  // products in flight end before their memory goes
-            if (elect_one()) mma_commit(&fx.fin);
+            if (elect_one()) mma_commit(&fx.fin[s]);
             __syncwarp();
-            (void)mbar_wait_limit(&fx.fin, 0, p.err, 1000000ull);
+            (void)mbar_wait_limit(&fx.fin[s], 0, p.err, 1000000ull);
         }
     } else if (warp >= 4) {
         // ---------------- softmax warps ----------------
