@@ -287,7 +287,7 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
         };
         const uint32_t tm = (uint32_t)uniform((int)tmem) + 256 * s;
         const uint32_t id_qk = idesc_f16(BF, kTcRows, Sh::KT, false), id_pv = idesc_f16(BF, kTcRows, HS, true);
-        int grp = grp0, t_base = 0, x = x_begin, n_p = 0, n_pv = 0, nseg = 0;  // weights taken, second products told of, items begun
+        int grp = grp0, t_base = 0, x = x_begin, n_p = 0, nseg = 0;  // second products, items begun
         for (Seg g; ok && segment(x, grp, g); ++nseg) {
             const bool both = g.rows > kTcRows;
             const int cnt = uniform(slot_tiles(g, s));
@@ -302,7 +302,7 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
                     for (int k = 0; k < HS / 16; ++k)  // 32 bytes a step, blocks of 4 steps
                         mma_bf16(tm, dq + (uint64_t)(((k >> 2) * Sh::kQBlock + (k & 3) * 32) >> 4),
                                  dk + (uint64_t)(((k >> 2) * Sh::kBlock + (k & 3) * 32) >> 4), id_qk, k ? 1u : 0u);
-                    mma_commit(&fx.s_full[s]);  // and the second product before it
+                    mma_commit(&fx.s_full[s]);
                     mma_commit(&fx.empty_k[st]);
                     if (!both) mma_commit(&fx.empty_k[st]);  // for the slot that does not use it
                 }
@@ -311,26 +311,27 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
             if (!await(&fx.q_full[s], nseg)) break;  // seen for every item, of a slot without tiles too
             if (cnt) scores(0);
             for (int i = 0; i < cnt && ok; ++i) {
-                // the second product, once the weights of the last scores are in (those scores have been read by then)
+                // the second product, once the weights of the last scores are in (those scores have been read by then: with
+                // weights of their own columns the next scores go first, and the softmax need not wait for this one)
                 const int t = uniform(t_base + slot_tile(g, s, i)), st = t % Sh::kStages;
-                if (!await(&fx.p_full[s], n_p) || !await(&fx.full_v[st], t / Sh::kStages)) break;
+                if (!await(&fx.p_full[s], n_p)) break;
                 ++n_p;
+                if (Sh::kOwnP && i + 1 < cnt) scores(i + 1);
+                if (!ok || !await(&fx.full_v[st], t / Sh::kStages)) break;
                 tc_fence_after();
                 const uint64_t dv = desc_sw128_mn(v_at + st * Sh::kTile, Sh::kBlock);
-                const bool tell = !Sh::kOwnP || i + 1 == cnt;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < Sh::KT / 16; ++k)  // 16 keys: 8 columns of weights, 16 lines of V
                         mma_f16_ta(tm + Sh::kO, tm + Sh::kP + 8 * k, dv + (uint64_t)(k * (16 * 128 >> 4)), id_pv, i || k ? 1u : 0u);
-                    if (tell) mma_commit(&fx.pv_done[s]);
+                    mma_commit(&fx.pv_done[s]);
                     mma_commit(&fx.empty_v[st]);
                     if (!both) mma_commit(&fx.empty_v[st]);
                 }
                 __syncwarp();
-                if (tell) ++n_pv;
-                if (i + 1 < cnt) {
-                    // where the weights lie over the scores, the next scores wait for the product that reads them
-                    if (!Sh::kOwnP && !await(&fx.pv_done[s], n_pv - 1)) break;
+                if (!Sh::kOwnP && i + 1 < cnt) {
+                    // the weights lie over the scores: the next ones wait for the product that reads them
+                    if (!await(&fx.pv_done[s], n_p - 1)) break;
                     scores(i + 1);
                 }
             }
@@ -386,16 +387,26 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
+                constexpr int NC = Sh::KT / 64;
+                float v[64], mx = -CUDART_INF_F;
                 if (busy) {
-                    constexpr int NC = Sh::KT / 64;
-                    float v[64], m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                    float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         tmem_ld64_wait(sc + 64 * c, v);
 #pragma unroll
                         for (int j = 0; j < 64; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[j]);
                     }
-                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * ta.scale_log2;
+                    mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * ta.scale_log2;
+                }
+                // the second product of the tile before reads the weights' columns and adds to acc
+                if (Sh::kOwnP && i) {
+                    ok = wait_or_stop(fx, &fx.pv_done[s], (uint32_t)(ended++ & 1), p.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (busy) {
                     const bool grow = mx > base + kGrow || (base == -CUDART_INF_F && mx > base);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to = grow ? mx : base;
