@@ -377,7 +377,13 @@ typedef struct {
     int n_layers, n_pages, n_kv_heads, page_size;
     int head_size; /* a multiple of 16 bytes, at most 128 elements */
     int n_seqs, max_pages;
+    unsigned ready; /* set by l2_pages_init */
 } L2Pages;
+
+/* Checks everything about a pool that the host can see and marks it usable; its
+ * fields stay as they are from then on (another pool, or a changed one, is
+ * initialised anew).  Every other call refuses a pool without it (L2_EINVAL). */
+int l2_pages_init(L2Pages *pool);
 
 /* Ints a pool's scratch holds. */
 long long l2_pages_scratch_ints(int n_pages);

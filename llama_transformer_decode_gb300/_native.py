@@ -90,7 +90,8 @@ class L2Pages(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "refs", "lens", "table", "status", "scratch")]
                 + [(n, ctypes.c_longlong) for n in ("layer_stride", "page_stride", "head_stride", "row_stride")]
                 + [(n, ctypes.c_int) for n in ("dtype", "n_layers", "n_pages", "n_kv_heads", "page_size", "head_size",
-                                               "n_seqs", "max_pages")])
+                                               "n_seqs", "max_pages")]
+                + [("ready", ctypes.c_uint)])
 
 
 class L2PagesRows(ctypes.Structure):
@@ -112,7 +113,7 @@ EXPORTS = ("l2_create", "l2_reset", "l2_forward", "l2_forward_batch", "l2_forwar
            "l2_step_input_bytes", "l2_forward_static", "l2_debug_fail_alloc_at", "l2_sample",
            "l2_forward_dev_tokens", "l2_prefill", "l2_debug_fail_graph_at", "l2_debug_wait_timeout",
            "l2_debug_bounds_checked", "l2_debug_limit_cache", "l2_launch_op_batch", "l2_pages_scratch_ints",
-           "l2_pages_append", "l2_pages_fork", "l2_pages_free", "l2_pages_attention_ws", "l2_pages_attention")
+           "l2_pages_init", "l2_pages_append", "l2_pages_fork", "l2_pages_free", "l2_pages_attention_ws", "l2_pages_attention")
 
 _lib = None
 
@@ -162,6 +163,8 @@ def declare(lib):
     pp = ctypes.POINTER(L2Pages)
     lib.l2_pages_scratch_ints.argtypes = [i]
     lib.l2_pages_scratch_ints.restype = ctypes.c_longlong
+    lib.l2_pages_init.argtypes = [pp]
+    lib.l2_pages_init.restype = i
     lib.l2_pages_append.argtypes = [pp, ctypes.POINTER(L2PagesRows), vp]
     lib.l2_pages_fork.argtypes = [pp, i, vp, vp, vp, vp]
     lib.l2_pages_free.argtypes = [pp, i, vp, i, vp]

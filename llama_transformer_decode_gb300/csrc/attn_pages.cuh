@@ -86,10 +86,10 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n) {  // of all runs of
 constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }
 // Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of reading 8 KB, 0.049 us an SM).  Measured
-// at prefixes of 131072: head size 64, 0.84 to 0.95 us up to 128 pairs, 1.67 at 136, 1.86 at 256; head size 128, 1.40
-// (reading), 1.66, 2.10.  Starting an item: its queries, its part, and the pipeline's filling.
-constexpr int kTcItemCost = 60, kTcMaxTileCost = 42;
-__host__ __device__ __forceinline__ int tc_cost(int n, int hs) { return n > kTcRows ? (hs > 64 ? 42 : 38) : (hs > 64 ? 30 : 18); }
+// at prefixes of 131072: head size 64, 0.84 to 0.89 us up to 128 pairs (reading), 1.34 at 136, 1.58 at 256; head size 128, 1.3
+// (reading), 1.56, 1.92.  Starting an item: its queries, its part, and the pipeline's filling.
+constexpr int kTcItemCost = 80, kTcMaxTileCost = 39;
+__host__ __device__ __forceinline__ int tc_cost(int n, int hs) { return n > kTcRows ? (hs > 64 ? 39 : 32) : (hs > 64 ? 30 : 18); }
 
 // The last entry i of an ascending list of n (every `stride`-th int of a, the first at most x) that is at most x,
 // found by a whole warp.

@@ -55,8 +55,10 @@ int check_ptr(const char *who, const char *name, const void *p, unsigned align, 
     return L2_OK;
 }
 
-// Everything about a pool that the host can see; *v is the kernels' view of it.
-int check_pool(const char *who, const L2Pages *p, PagesView *v, int *device) {
+constexpr unsigned kReady = 0x50a6e500u;  // with the pool's device below
+
+// Everything about a pool that the host can see.
+int check_pool(const char *who, const L2Pages *p, int *device) {
     if (!p) return refuse(L2_EINVAL, "%s: NULL pool", who);
     if (p->dtype != L2_F32 && p->dtype != L2_BF16 && p->dtype != L2_F16)
         return refuse(L2_EINVAL, "%s: dtype %d is not L2_F32, L2_BF16 or L2_F16", who, p->dtype);
@@ -79,12 +81,22 @@ int check_pool(const char *who, const L2Pages *p, PagesView *v, int *device) {
             return refuse(L2_EINVAL, "%s: %s %lld must be at least head_size and a multiple of 16 bytes", who, names[i], st[i]);
         if (st[i] > (1ll << 40)) return refuse(L2_EINVAL, "%s: %s %lld too large", who, names[i], st[i]);
     }
-    int rc;
-    if ((rc = check_ptr(who, "k", p->k, 16, device)) || (rc = check_ptr(who, "v", p->v, 16, device)) ||
-        (rc = check_ptr(who, "refs", p->refs, 4, device)) || (rc = check_ptr(who, "lens", p->lens, 4, device)) ||
-        (rc = check_ptr(who, "table", p->table, 4, device)) || (rc = check_ptr(who, "status", p->status, 4, device)) ||
-        (rc = check_ptr(who, "scratch", p->scratch, 4, device)))
-        return rc;
+    const void *const ptrs[7] = {p->k, p->v, p->refs, p->lens, p->table, p->status, p->scratch};
+    static const char *const ptr_names[7] = {"k", "v", "refs", "lens", "table", "status", "scratch"};
+    for (int i = 0; i < 7; ++i)
+        if (!ptrs[i]) return refuse(L2_EINVAL, "%s: %s is NULL", who, ptr_names[i]);
+    for (int i = 0; i < 7; ++i)
+        if (int rc = check_ptr(who, ptr_names[i], ptrs[i], i < 2 ? 16 : 4, device)) return rc;
+    if (*device > 0xff) return refuse(L2_EINVAL, "%s: device %d", who, *device);
+    return L2_OK;
+}
+
+// A pool that l2_pages_init has checked: its device and the kernels' view of it.
+int view_pool(const char *who, const L2Pages *p, PagesView *v, int *device) {
+    if (!p) return refuse(L2_EINVAL, "%s: NULL pool", who);
+    if ((p->ready & ~0xffu) != kReady) return refuse(L2_EINVAL, "%s: the pool needs l2_pages_init", who);
+    *device = (int)(p->ready & 0xffu);
+    const long long es = elt_size(p->dtype), rb = p->head_size * es;
     v->k = static_cast<char *>(p->k);
     v->v = static_cast<char *>(p->v);
     v->refs = p->refs;
@@ -92,10 +104,10 @@ int check_pool(const char *who, const L2Pages *p, PagesView *v, int *device) {
     v->table = p->table;
     v->err = p->status;
     v->scratch = p->scratch;
-    v->layer_stride = p->n_layers > 1 ? st[0] * es : 0;
-    v->page_stride = p->n_pages > 1 ? st[1] * es : 0;
-    v->head_stride = p->n_kv_heads > 1 ? st[2] * es : rb;
-    v->row_stride = p->page_size > 1 ? st[3] * es : rb;
+    v->layer_stride = p->n_layers > 1 ? p->layer_stride * es : 0;
+    v->page_stride = p->n_pages > 1 ? p->page_stride * es : rb;
+    v->head_stride = p->n_kv_heads > 1 ? p->head_stride * es : rb;
+    v->row_stride = p->page_size > 1 ? p->row_stride * es : rb;
     v->n_layers = p->n_layers;
     v->n_pages = p->n_pages;
     v->n_kv_heads = p->n_kv_heads;
@@ -148,10 +160,17 @@ int check_attn_shape(const char *who, const L2Pages *p, int B, int G, int n_head
 
 long long l2_pages_scratch_ints(int n_pages) { return n_pages < 1 ? L2_EINVAL : kScrHead + 3ll * n_pages; }
 
+int l2_pages_init(L2Pages *pool) {
+    int device = -1;
+    const int rc = check_pool("l2_pages_init", pool, &device);
+    if (rc == L2_OK) pool->ready = kReady | (unsigned)device;
+    return rc;
+}
+
 int l2_pages_append(const L2Pages *pool, const L2PagesRows *a, void *cuda_stream) {
     const char *who = "l2_pages_append";
     PagesView v;
-    int device = -1, rc = check_pool(who, pool, &v, &device);
+    int device = -1, rc = view_pool(who, pool, &v, &device);
     if (rc) return rc;
     if (!a) return refuse(L2_EINVAL, "%s: NULL rows", who);
     if ((rc = check_count(who, a->n, 1))) return rc;
@@ -192,7 +211,7 @@ int l2_pages_append(const L2Pages *pool, const L2PagesRows *a, void *cuda_stream
 int l2_pages_fork(const L2Pages *pool, int n, const int *src, const int *dst, const int *rows, void *cuda_stream) {
     const char *who = "l2_pages_fork";
     PagesView v;
-    int device = -1, rc = check_pool(who, pool, &v, &device);
+    int device = -1, rc = view_pool(who, pool, &v, &device);
     if (rc || (rc = check_count(who, n, 1)) || (rc = check_ptr(who, "src", src, 4, &device)) ||
         (rc = check_ptr(who, "dst", dst, 4, &device)) || (rows && (rc = check_ptr(who, "rows", rows, 4, &device))))
         return rc;
@@ -204,7 +223,7 @@ int l2_pages_fork(const L2Pages *pool, int n, const int *src, const int *dst, co
 int l2_pages_free(const L2Pages *pool, int n, const int *seqs, int compact, void *cuda_stream) {
     const char *who = "l2_pages_free";
     PagesView v;
-    int device = -1, rc = check_pool(who, pool, &v, &device);
+    int device = -1, rc = view_pool(who, pool, &v, &device);
     if (rc || (rc = check_count(who, n, 0)) || (n && (rc = check_ptr(who, "seqs", seqs, 4, &device)))) return rc;
     DeviceGuard guard;
     if (!guard.enter(device)) return refuse(L2_ECUDA, "%s: cannot use device %d", who, device);
@@ -214,7 +233,7 @@ int l2_pages_free(const L2Pages *pool, int n, const int *seqs, int compact, void
 long long l2_pages_attention_ws(const L2Pages *pool, int B, int G, int n_heads) {
     const char *who = "l2_pages_attention_ws";
     PagesView v;
-    int device = -1, rc = check_pool(who, pool, &v, &device);
+    int device = -1, rc = view_pool(who, pool, &v, &device);
     if (rc || (rc = check_attn_shape(who, pool, B, G, n_heads))) return rc;
     const int sms = sm_count(device);
     if (!sms) return refuse(L2_ECUDA, "%s: cannot query device %d", who, device);
@@ -224,7 +243,7 @@ long long l2_pages_attention_ws(const L2Pages *pool, int B, int G, int n_heads) 
 int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws, long long ws_bytes, void *cuda_stream) {
     const char *who = "l2_pages_attention";
     PagesView v;
-    int device = -1, rc = check_pool(who, pool, &v, &device);
+    int device = -1, rc = view_pool(who, pool, &v, &device);
     if (rc) return rc;
     if (!a) return refuse(L2_EINVAL, "%s: NULL arguments", who);
     if ((rc = check_attn_shape(who, pool, a->B, a->G, a->n_heads))) return rc;

@@ -8,7 +8,6 @@ into a CUDA graph.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -80,10 +79,14 @@ class PagePool:
                           self.status.data_ptr(), self._scratch.data_ptr(), *k.stride()[:4], kinds[k.dtype], *k.shape,
                           *table.shape)
         self._ref = ctypes.byref(self._c)
+        rc = self._lib.l2_pages_init(self._ref)
+        if rc:
+            _raise(rc)
         self._ws = {}  # workspace bytes per (rows, groups, heads)
         self._torch, self._int32, self._index = torch, torch.int32, k.get_device()
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._scale = 1.0 / math.sqrt(self.head_size)
+        self._bytes = torch.empty(0, dtype=torch.uint8, device=k.device)  # workspaces are made like it
 
     # -- helpers -------------------------------------------------------------
     def _stream(self, stream):
@@ -169,19 +172,27 @@ class PagePool:
                 _raise(int(need))
             self._ws[(B, G, H)] = need
         torch = self._torch
-        # the workspace belongs to the stream that uses it
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-            if out is None:
+        fresh = out is None
+        if stream is None:
+            if fresh:
                 out = torch.empty((B, H, self.head_size), dtype=self.dtype, device=self.device)
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-        op, o_shape, o_st = self._rows("out", out, 3)
-        if o_shape != q.shape:
-            raise ValueError("out must have q's shape")
+            ws = self._bytes.new_empty(need)
+        else:  # the workspace belongs to the stream that uses it
+            with torch.cuda.stream(stream):
+                if fresh:
+                    out = torch.empty((B, H, self.head_size), dtype=self.dtype, device=self.device)
+                ws = self._bytes.new_empty(need)
+        if fresh:
+            op, o_row, o_head = out.data_ptr(), H * self.head_size, self.head_size
+        else:
+            op, o_shape, (o_row, o_head, _) = self._rows("out", out, 3)
+            if o_shape != q.shape:
+                raise ValueError("out must have q's shape")
         if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != self._index or not lse.is_contiguous()
                                 or tuple(lse.shape) != (B, H)):
             raise ValueError("lse must be a contiguous float32 tensor [rows][heads] of the pool's device")
         a = L2PagesAttention(int(layer), B, G, H, qp, op, None if lse is None else lse.data_ptr(),
-                             None if seqs is None else self._ints("seqs", seqs, B), gs, pl, q_st[0], q_st[1], o_st[0], o_st[1],
+                             None if seqs is None else self._ints("seqs", seqs, B), gs, pl, q_st[0], q_st[1], o_row, o_head,
                              self._scale if scale is None else float(scale))
         rc = self._lib.l2_pages_attention(self._ref, ctypes.byref(a), ws.data_ptr(), need, self._stream(stream))
         if rc:

@@ -43,6 +43,9 @@ def text(lib):
     (dict(table=0), "NULL"), (dict(), "device memory")])
 def test_pools_the_host_can_refuse(lib, bad, word):
     p = pool_struct(**bad)
+    assert lib.l2_pages_init(ctypes.byref(p)) == pkg.L2_EINVAL
+    assert word in text(lib), text(lib)
+    # and a pool that was not initialised is refused by every call
     idx = ctypes.c_void_p(p.refs or p.k)
     for call in (lambda: lib.l2_pages_fork(ctypes.byref(p), 1, idx, idx, None, None),
                  lambda: lib.l2_pages_free(ctypes.byref(p), 1, idx, 0, None),
@@ -50,11 +53,11 @@ def test_pools_the_host_can_refuse(lib, bad, word):
                  lambda: lib.l2_pages_attention_ws(ctypes.byref(p), 1, 0, 2),
                  lambda: lib.l2_pages_attention(ctypes.byref(p), ctypes.byref(_native.L2PagesAttention()), None, 0, None)):
         assert call() == pkg.L2_EINVAL
-        if word != "NULL" and word != "device memory":
-            assert word in text(lib), text(lib)
+        assert "l2_pages_init" in text(lib), text(lib)
 
 
 def test_null_pools_and_sizes(lib):
+    assert lib.l2_pages_init(None) == pkg.L2_EINVAL
     assert lib.l2_pages_fork(None, 1, None, None, None, None) == pkg.L2_EINVAL
     assert lib.l2_pages_free(None, 1, None, 0, None) == pkg.L2_EINVAL
     assert lib.l2_pages_append(None, None, None) == pkg.L2_EINVAL
@@ -64,7 +67,7 @@ def test_null_pools_and_sizes(lib):
 
 
 def test_struct_layouts_match_the_header():
-    assert ctypes.sizeof(_native.L2Pages) == 7 * 8 + 4 * 8 + 8 * 4
+    assert ctypes.sizeof(_native.L2Pages) == 7 * 8 + 4 * 8 + 8 * 4 + 8  # ready, padded
     assert ctypes.sizeof(_native.L2PagesRows) == 8 + 2 * 8 + 8 + 2 * 8 + 3 * 8
     assert ctypes.sizeof(_native.L2PagesAttention) == 16 + 6 * 8 + 4 * 8 + 8
 
