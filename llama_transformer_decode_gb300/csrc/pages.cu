@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
 
 // Compaction: the moved pages' rows in every layer, and the tables' entries.  A run is one page's
 // rows of one (layer, K or V, head), or all its heads where they lie side by side (`heads` 1).
-__global__ void __launch_bounds__(256) pages_compact_kernel(const PagesView p, int heads, int rows, int row_bytes) {
+__global__ void __launch_bounds__(512) pages_compact_kernel(const PagesView p, int heads, int rows, int row_bytes) {
     pdl_launch_dependents();
     pdl_wait();
     if (p.scratch[kScrRefused]) return;
@@ -391,11 +391,11 @@ __global__ void __launch_bounds__(256) pages_compact_kernel(const PagesView p, i
         char *pool = (lv & 1 ? p.v : p.k) + l * p.layer_stride + h * p.head_stride;
         const char *a = pool + mover[e] * p.page_stride;
         char *b = pool + hole[e] * p.page_stride;
-#pragma unroll 4
+#pragma unroll 8
         for (int c = threadIdx.x; c < words; c += blockDim.x) {
             const int r = c / vr;
             const long long o = r * p.row_stride + ((long long)(c - r * vr) << 4);
-            __stcs(reinterpret_cast<uint4 *>(b + o), __ldcs(reinterpret_cast<const uint4 *>(a + o)));
+            *reinterpret_cast<uint4 *>(b + o) = __ldcs(reinterpret_cast<const uint4 *>(a + o));
         }
     }
 }
@@ -461,7 +461,7 @@ cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool c
         rows = 1;
     }
     void *args2[] = {const_cast<PagesView *>(&p), &heads, &rows, &bytes};
-    return launch(reinterpret_cast<void *>(pages_compact_kernel), dim3(152 * 8), 256, args2, s);
+    return launch(reinterpret_cast<void *>(pages_compact_kernel), dim3(152 * 4), 512, args2, s);
 }
 
 }  // namespace l2
