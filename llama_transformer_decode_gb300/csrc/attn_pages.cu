@@ -68,13 +68,16 @@ __device__ __forceinline__ void store_out<__half>(char *o, int d, float4 v) {
 constexpr int kEarly = 8;  // rounds of parts' sums loaded before their weights are known
 }  // namespace
 
-// One warp per (row, query head): the parts of its prefix and of its own keys, in key order.  Lanes take a part each
-// for (m, l), so all weights are known after one round of loads; LP lanes take a part's sums, the first kEarly
-// rounds of which are loaded beside (m, l).
-template <typename T>
+// NW warps per (row, query head) take the parts of its prefix and of its own keys in turn.  Lanes take a part each
+// for (m, l), so a warp's weights are known after one round of loads; LP lanes take a part's sums, the first kEarly
+// rounds of which are loaded beside (m, l).  Then the warps' results are joined in order.
+template <typename T, int NW>
 __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const PagesAttn p) {
-    const int lane = threadIdx.x & 31;
-    const int bh = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    constexpr int kRows = kMergeThreads / 32 / NW;  // (row, head) pairs a block
+    __shared__ float sm[NW], sl[NW];
+    __shared__ float4 sa[NW][32];
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW;
+    const int bh = blockIdx.x * kRows + (threadIdx.x >> 5) / NW;
     const int b = (int)((unsigned)bh / (unsigned)p.n_heads), h = bh - b * p.n_heads;
     const Plan pl = plan_of(p.plan, p.B, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
@@ -120,9 +123,10 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
             tc_row = tc.z + kvh * tc_head_rows(n) + mi + 2 * kTcRows * w0;
         }
     }
-    const int n = tc_n + rest.n + own.n;
-    // (m, l) and sums of part e
-    auto part = [&](int e, const float2 *&ml, const float *&acc) {
+    const int total = tc_n + rest.n + own.n, n = (total + NW - 1 - warp) / NW;  // parts of the row, of this warp
+    // (m, l) and sums of the warp's i-th part
+    auto part = [&](int i, const float2 *&ml, const float *&acc) {
+        int e = i * NW + warp;
         if (e < tc_n) {
             const size_t at = (size_t)(tc_row + 2 * kTcRows * (e >> tc_two) + (tc_two ? (e & 1) * tc_rows : 0));
             ml = reinterpret_cast<const float2 *>(p.tc_ml) + at;
@@ -200,12 +204,37 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
             a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
             a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
         }
+    if constexpr (NW > 1) {
+        if (sub == 0) sa[warp][lane] = a;
+        if (lane == 0) {
+            sm[warp] = m;
+            sl[warp] = l;
+        }
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int w = 1; w < NW; ++w) m = fmaxf(m, sm[w]);
+        const float base = m == -CUDART_INF_F ? 0.f : m;
+        l = 0.f;
+        a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w >= total) break;  // a warp without parts
+            const float c = exp2f(sm[w] - base);
+            const float4 v = sa[w][lane % LP];
+            l = fmaf(sl[w], c, l);
+            a.x = fmaf(v.x, c, a.x);
+            a.y = fmaf(v.y, c, a.y);
+            a.z = fmaf(v.z, c, a.z);
+            a.w = fmaf(v.w, c, a.w);
+        }
+    }
     // no keys at all: zeros, and a sum of nothing; all scores -inf: 0 / 0, as the formula has it
-    const float inv = n ? 1.0f / l : 0.f;
+    const float inv = total ? 1.0f / l : 0.f;
     if (on && sub == 0)
         store_out<T>(p.out + (long long)b * p.o_row + (long long)h * p.o_head, d,
-                     n ? make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
-    if (p.lse && lane == 0) p.lse[(size_t)b * p.n_heads + h] = n ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                     total ? make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
+    if (p.lse && lane == 0) p.lse[(size_t)b * p.n_heads + h] = total ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
 }
 
 namespace {
@@ -279,12 +308,17 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
         if ((e = cudaLaunchKernelEx(&cfg, attn_pages_plan_kernel, p)) != cudaSuccess) return e;
     }
     if ((e = f32 ? launch_attn_pages_f32(p, cfg) : launch_attn_pages_16(p, cfg)) != cudaSuccess) return e;
-    cfg.gridDim = dim3((p.B * p.n_heads + kMergeThreads / 32 - 1) / (kMergeThreads / 32));
+    // few (row, head) pairs: four warps to each, since prefixes then come in many parts (a row of 112 parts: 57 -> 31 us a call);
+    // many: one warp to each (2048 pairs of 7 parts: 41 us a call against 46)
+    const int pairs = p.B * p.n_heads;
+    const bool few = pairs <= 1024;
+    cfg.gridDim = dim3(few ? pairs : (pairs + 3) / 4);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    if (f32) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<float>, p);
-    if (p.dtype == L2_BF16) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<__nv_bfloat16>, p);
-    return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<__half>, p);
+    if (f32) return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<float, 4> : attn_pages_merge_kernel<float, 1>, p);
+    if (p.dtype == L2_BF16)
+        return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<__nv_bfloat16, 4> : attn_pages_merge_kernel<__nv_bfloat16, 1>, p);
+    return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<__half, 4> : attn_pages_merge_kernel<__half, 1>, p);
 }
 
 }  // namespace l2

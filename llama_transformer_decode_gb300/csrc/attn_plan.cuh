@@ -8,12 +8,16 @@ namespace l2 {
 // Least cost of a range: fewer than two tiles a warp cost more to write and merge as parts than the parallel reading gains.  (And
 // at least the distance of two tiles of any kind, see walker_of.)
 constexpr int kMinPer = kItemCost + 2 * kCostUnit, kTcMinPer = kTcItemCost + kTcMaxTileCost;
+// An item of k tiles goes to sqrt(13 k) warps at most (48 for 180 tiles, 285 for 6250): with P warps they take k / P tiles each and
+// the merge P parts, a part a thirteenth of a tile's time, and that many make the sum least.
+constexpr float kSpread = 1.0f / 13.0f;
 static_assert(kMinPer >= kItemCost + kMaxTileCost, "every walker between an item's first and last must hold a tile of it");
 
 template <int NT, int MAX>
 struct PlanScratch {
     int minlen[MAX], mintc[MAX], gstart[MAX + 1], len[MAX], group[MAX], seq[MAX];
     int2 sums[2][32];
+    int spread;
 };
 
 // Exclusive prefix sums of both components over the block, and the totals; buf: one int2 a warp, not used by another scan.
@@ -58,6 +62,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         sc.len[i] = len;
         sc.seq[i] = seq;
     }
+    if (i == 0) sc.spread = 0;
     if (p.G) {
 #pragma unroll 1
         for (int g = i; g <= p.G; g += NT) {
@@ -124,6 +129,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         e.kt = (e.key1 - e.key0 + (1 << p.tile_shift) - 1) >> p.tile_shift;
         e.cost = tile_cost(p.dtype, min(e.rows * gq, kM));
         const int items = e.kt ? (e.rows * gq + kM - 1) / kM * p.n_kv_heads : 0;
+        if (items) atomicMax(&sc.spread, (int)((float)e.cost * sqrtf((float)e.kt * kSpread)));
         int2 here;
         const int2 before = plan_scan<NT>(make_int2(items * (kItemCost + e.kt * e.cost), items), &here, sc.sums[1]);
         e.t0 = all.x + before.x;
@@ -145,7 +151,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         }
         pl.src[S].t0 = cost;
         pl.hdr[kHdrCost] = cost;
-        pl.hdr[kHdrPer] = max(kMinPer, cdiv(cost, (p.num_sms - n_tc) * p.walk_warps));
+        pl.hdr[kHdrPer] = max(max(kMinPer, sc.spread), cdiv(cost, (p.num_sms - n_tc) * p.walk_warps));
         pl.hdr[kHdrTcCost] = tc;
         pl.hdr[kHdrTcPer] = per_tc;
         pl.hdr[kHdrTcBlocks] = n_tc;
