@@ -37,7 +37,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t *r) {
                  : "r"(a));
 }
 
+// kLift: the weights of a tile are 2^(x - max + kLift).  In fp16, whose least step is 2^-24, weights far below the
+// largest would otherwise be lost, and there may be 10^5 of them; in bf16 the exponent is that of fp32.
 struct TBf16 {
+    static constexpr float kLift = 0.f;
     static __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -50,6 +53,7 @@ struct TBf16 {
     static __device__ __forceinline__ float2 unpack(uint32_t v) { return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v)); }
 };
 struct TF16 {
+    static constexpr float kLift = 15.f;
     static __device__ __forceinline__ void mma(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -181,6 +185,7 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
             base[r] = mn == -CUDART_INF_F ? 0.f : mn;  // only -inf so far: weights 0, not NaN
             corr[r] = exp2f(m_run[r] - base[r]);
             m_run[r] = mn;
+            base[r] -= T::kLift;
         }
         float sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -221,7 +226,6 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
                 T::mma(o[c + 1], plo, b[2], b[3]);
             }
         }
-    
         if (++it == w.n_tiles) {
             it = 0;
             // the part: (m, l) and the sums of the item's pairs
@@ -233,14 +237,13 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
                 const int mi = g4 + 8 * r;
                 if (mi >= w.pairs || slot >= p.max_parts) continue;
-                if (t4 == 0) reinterpret_cast<float2 *>(p.ws_ml)[(size_t)slot * kM + mi] = make_float2(m_run[r], l);
+                if (t4 == 0) reinterpret_cast<float2 *>(p.ws_ml)[(size_t)slot * kM + mi] = make_float2(m_run[r] - T::kLift, l);
                 float *dst = p.ws_acc + ((size_t)slot * kM + mi) * p.head_size;
 #pragma unroll
                 for (int i = 0; i < HS / 8; ++i) {
                     const int d = 8 * i + 2 * t4;
                     if (d < p.head_size) *reinterpret_cast<float2 *>(dst + d) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
                 }
-        
             }
         }
         __syncwarp();  // the stage is read before the next copy into it

@@ -268,13 +268,36 @@ __device__ __forceinline__ void tile_mma(StateF<HS> &st, float *m2, float *l2, c
             for (int j = 0; j < 4; ++j) s[n][j] += c[j];
         }
     }
+    bool odd = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s[n][j] += sl[n][j];
+            odd |= s[n][j] != s[n][j];
+        }
+    // the halves of an infinity make NaN of a score that may be infinite: such tiles are summed again as they are
+    if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = 8 * n + 2 * t4 + (j & 1), row = g4 + 8 * (j >> 1);
+                s[n][j] = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < Sh::C; ++c) {
+                    const float4 x = word(ks + key * Sh::kRow + ((c ^ swzf(key)) << 4)), y = word(qs + row * Sh::kRow + (c << 4));
+                    s[n][j] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[n][j]))));
+                }
+            }
+    }
     float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int key = 8 * n + 2 * t4 + (j & 1);
-            s[n][j] = key < left ? (s[n][j] + sl[n][j]) * scale_log2 : -CUDART_INF_F;
+            s[n][j] = key < left ? s[n][j] * scale_log2 : -CUDART_INF_F;
             mx[j >> 1] = fmaxf(mx[j >> 1], s[n][j]);
         }
     float corr[2], base[2];

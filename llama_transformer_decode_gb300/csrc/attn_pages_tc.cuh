@@ -17,11 +17,12 @@
 //   warps 1-2  the products of slots 0 and 1
 //   warps 4-7, 8-11  slots 0 and 1: queries to shared memory, softmax, parts out
 // A thread owns one pair: its row of scores is a lane of tensor memory, so max and sum need no
-// exchange.  The weights go back over the scores as 16-bit values (half a step of the type, 2^-9 in bf16
-// and 2^-12 in fp16 of each weight, below the output's own rounding of the sum) and are
-// the A operand of the second product from there; the sums l are of the unrounded weights.  acc is
-// rescaled only when a row's maximum has grown by more than 2^8 since the last time: weights
-// stay below 2^8, far from either type's limits, and the result is the same.
+// exchange.  The weights go back over the scores as 16-bit values (at most half a step of the type off, as
+// the output is anyway: 2^-8 in bf16, 2^-11 in fp16) and are the A operand of the second product from there; the sums l are
+// of the unrounded weights.  acc is rescaled only when a row's maximum has grown by more than a factor of 2^kGrow since the
+// last time.  In bf16 weights then stay below 2^8.  fp16 ends at 2^16 and its least step is 2^-24, so its weights are
+// 2^(x - m + 13), at most 2^15: rounding then loses at most 2^-38 of the largest weight on each, where without the 13
+// a prefix of 131072 keys whose weights are 2^-26 of one other key's lost a 512th of the sum.
 //
 // What bounds it: up to 128 pairs, reading K and V; above, the products and the exponentials in about
 // equal measure.
@@ -44,7 +45,11 @@ namespace {
 
 constexpr int kSlotThreads = 128;
 constexpr int kRing = 6;                    // most stages of a ring
-constexpr float kGrow = 8.0f;               // see above
+// See above: a row's weights are at most 2^(lift + grow) of its type.
+template <bool BF>
+constexpr float kLiftTc = BF ? 0.f : 13.f;
+template <bool BF>
+constexpr float kGrow = BF ? 8.f : 2.f;
 
 struct alignas(128) TcAttn {
     CUtensorMap kmap, vmap;
@@ -407,9 +412,9 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
                     tc_fence_after();
                 }
                 if (busy) {
-                    const bool grow = mx > base + kGrow || (base == -CUDART_INF_F && mx > base);
+                    const bool grow = mx > base + (kLiftTc<BF> + kGrow<BF>) || (base == -CUDART_INF_F && mx > base);
                     if (__any_sync(0xffffffffu, grow)) {
-                        const float to = grow ? mx : base;
+                        const float to = grow ? mx - kLiftTc<BF> : base;
                         const float f = to == -CUDART_INF_F ? 1.f : exp2f(base - to);
                         if (i) {
 #pragma unroll

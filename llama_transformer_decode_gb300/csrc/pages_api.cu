@@ -137,11 +137,12 @@ int check_stride(const char *who, const char *name, long long stride, int steps,
 }
 
 int sm_count(int device) {
-    static int counts[64] = {};
+    static std::atomic<int> counts[64];
     if (device < 0 || device >= 64) return 0;
-    if (!counts[device] && cudaDeviceGetAttribute(&counts[device], cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
-        return 0;
-    return counts[device];
+    int n = counts[device].load(std::memory_order_relaxed);
+    if (!n && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) == cudaSuccess)
+        counts[device].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 int check_attn_shape(const char *who, const L2Pages *p, int B, int G, int n_heads) {
@@ -189,6 +190,8 @@ int l2_pages_append(const L2Pages *pool, const L2PagesRows *a, void *cuda_stream
     if ((rc = check_ptr(who, "seqs", a->seqs, 4, &device)) || (a->starts && (rc = check_ptr(who, "starts", a->starts, 4, &device))) ||
         (a->rows && ((rc = check_ptr(who, "k", a->k, 16, &device)) || (rc = check_ptr(who, "v", a->v, 16, &device)))))
         return rc;
+    if ((long long)a->rows * w.n_layers > 0x3fffffffll)  // warps of the copy are counted in 32 bits
+        return refuse(L2_EINVAL, "%s: %d rows of %d layers in one call", who, a->rows, w.n_layers);
     DeviceGuard guard;
     if (!guard.enter(device)) return refuse(L2_ECUDA, "%s: cannot use device %d", who, device);
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
@@ -257,7 +260,10 @@ int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws,
         (rc = check_stride(who, "out_row_stride", a->out_row_stride, a->B, es)) ||
         (rc = check_stride(who, "out_head_stride", a->out_head_stride, a->n_heads, es)))
         return rc;
-    if ((a->n_heads > 1 && a->out_head_stride < pool->head_size) || (a->B > 1 && a->out_row_stride < pool->head_size))
+    // every row of the output has memory of its own: heads within rows, or rows within heads
+    const long long hs = pool->head_size, heads = (a->n_heads - 1) * a->out_head_stride + hs, rows = (a->B - 1) * a->out_row_stride + hs;
+    if ((a->n_heads > 1 && a->out_head_stride < hs) || (a->B > 1 && a->out_row_stride < hs) ||
+        (a->n_heads > 1 && a->B > 1 && heads > a->out_row_stride && rows > a->out_head_stride))
         return refuse(L2_EINVAL, "%s: output rows overlap", who);
     if ((rc = check_ptr(who, "q", a->q, 16, &device)) || (rc = check_ptr(who, "out", a->out, 16, &device)) ||
         (a->lse && (rc = check_ptr(who, "lse", a->lse, 4, &device))) || (a->seqs && (rc = check_ptr(who, "seqs", a->seqs, 4, &device))) ||

@@ -126,7 +126,7 @@ class PagePool:
         vp, v_shape, v_st = self._rows("v", v, 4 if whole else 3)
         if shape != v_shape or st != v_st or shape[-2] != self.n_kv_heads or (whole and shape[0] != self.n_layers):
             raise ValueError("k and v must be alike, with the pool's layers and heads")
-        n = seqs.numel()
+        n = len(seqs)
         a = L2PagesRows(n, shape[-3], self._ints("seqs", seqs), None if starts is None else self._ints("starts", starts, n + 1),
                         -1 if whole else int(layer), int((whole or layer == 0) if extend is None else bool(extend)), kp, vp,
                         st[0] if whole else 0, st[-3], st[-2])
@@ -136,15 +136,15 @@ class PagePool:
 
     def fork(self, src, dst, rows=None, stream=None):
         """Empty sequence dst[i] becomes the first rows[i] rows of src[i] (all, without ``rows``)."""
-        n = src.numel()
-        rc = self._lib.l2_pages_fork(self._ref, n, self._ints("src", src), self._ints("dst", dst, n),
+        n = len(src)
+        rc = self._lib.l2_pages_fork(self._ref, n, self._ints("src", src, n), self._ints("dst", dst, n),
                                      None if rows is None else self._ints("rows", rows, n), self._stream(stream))
         if rc:
             _raise(rc)
 
     def free(self, seqs=None, compact=False, stream=None):
         """Empties sequences ``seqs`` and gives their pages back; ``compact`` then closes the pool up."""
-        n = 0 if seqs is None else seqs.numel()
+        n = 0 if seqs is None else len(seqs)
         rc = self._lib.l2_pages_free(self._ref, n, self._ints("seqs", seqs) if n else None, int(bool(compact)),
                                      self._stream(stream))
         if rc:
@@ -159,7 +159,7 @@ class PagePool:
         qp, (B, H, _), q_st = self._rows("q", q, 3)
         G = gs = pl = 0
         if group_starts is not None:
-            G = group_starts.numel() - 1
+            G = len(group_starts) - 1
             if G < 1 or prefix_lens is None:
                 raise ValueError("group_starts needs at least one group, and prefix_lens")
             gs, pl = self._ints("group_starts", group_starts), self._ints("prefix_lens", prefix_lens, G)

@@ -447,3 +447,254 @@ def test_a_serving_loop_of_all_operators(dtype):
     assert int((pool.refs > 0).sum()) == int(pool.refs.nonzero().max()) + 1 or step > 20
     pool.free(dev(live))
     assert int(pool.refs.abs().sum()) == 0
+
+
+# -- large calls ------------------------------------------------------------
+
+def wide_pool(dtype, n_seqs, kv, hs, ps, lens, prefix_of=None, seed=0, k=None):
+    """A pool filled in a few tensor operations: sequence s holds lens[s] rows in shuffled pages; with prefix_of[s] = (first, n)
+    its first n // ps pages are sequence `first`'s.  Returns the pool and a function that gathers a sequence's rows in 64 bits."""
+    rng = np.random.default_rng(seed)
+    held = [-(-int(n) // ps) for n in lens]
+    own_from = [0 if prefix_of is None or prefix_of[s][0] == s else prefix_of[s][1] // ps for s in range(n_seqs)]
+    need = sum(h - o for h, o in zip(held, own_from))
+    n_pages, max_pages = need + 5, max(held) + 1
+    ids = rng.permutation(n_pages).astype(np.int32)
+    table, at = np.full((n_seqs, max_pages), -7, np.int32), 0
+    for s in range(n_seqs):
+        table[s, own_from[s]:held[s]] = ids[at:at + held[s] - own_from[s]]
+        at += held[s] - own_from[s]
+    for s in range(n_seqs):
+        if own_from[s]:
+            table[s, :own_from[s]] = table[prefix_of[s][0], :own_from[s]]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = [torch.randn((1, n_pages, kv, ps, hs), generator=g, device="cuda").to(DT[dtype]) for _ in range(2)]
+    pool = pkg.PagePool.from_tensors(t[0], t[1], dev(np.bincount(np.concatenate([table[s, :held[s]] for s in range(n_seqs)]), minlength=n_pages)),
+                                     dev(lens), dev(table))
+
+    def rows(s):
+        pages = pool.table[s, :held[s]].long()
+        return [x[0, pages].transpose(1, 2).reshape(-1, kv, hs)[:int(lens[s])].double() for x in (pool.k, pool.v)]
+    return pool, rows
+
+
+def check_wide(out, lse, q, rows, dtype, scale, which):
+    """check_attention's bounds for the rows `which`, the 64-bit attention on the GPU."""
+    H, hs = q.shape[1:]
+    half = torch.finfo(DT[dtype]).eps / 2
+    for b in which:
+        k, v = rows(b)
+        n, kv = k.shape[:2]
+        if n == 0:
+            assert bool((out[b] == 0).all()) and bool((lse[b] == -math.inf).all())
+            continue
+        kvh = torch.arange(H, device="cuda") * kv // H
+        qd = q[b].double()
+        x = scale * torch.einsum("thd,hd->ht", k[:, kvh], qd)
+        spread = float((abs(scale) * torch.einsum("thd,hd->ht", k[:, kvh].abs(), qd.abs())).max())
+        w = torch.softmax(x, 1)
+        want, mag = torch.einsum("ht,thd->hd", w, v[:, kvh]), torch.einsum("ht,thd->hd", w, v[:, kvh].abs())
+        e = (2.0 ** -21 + 2 * hs * U) * spread + 8 * U * spread
+        rel = 2 * e + (0 if dtype == "fp32" else half) + (3 * (n / 8 + 1) + 64) * 2 * U
+        tol = rel * mag + half * (want.abs() + rel * mag) + 1e-38 + (2.0 ** -25 if dtype == "fp16" else 0)
+        err = (out[b].double() - want).abs()
+        assert bool((err <= tol).all()), (b, n, float((err / tol).max()))
+        want_lse = torch.logsumexp(x, 1)
+        assert float((lse[b].double() - want_lse).abs().max()) <= 2 * e + (3 * n / 8 + 64) * 2 * U + 2.0 ** -22 * (float(want_lse.abs().max()) + 1)
+
+
+# rows, group sizes, prefix, most own rows, heads, KV heads, head size, page size
+WIDE = [
+    (193, None, 0, 40, 4, 2, 64, 16),               # one source more than a block plans for itself
+    (97, [1] * 96 + [1], 30, 40, 2, 1, 64, 16),
+    (300, [20] * 10 + [1] * 100, 300, 30, 4, 2, 64, 16),
+    (1024, [1024], 700, 9, 8, 2, 128, 128),
+    (1024, [1] * 1024, 100, 50, 2, 2, 32, 8),
+    (1024, [512, 0, 0, 512], 257, 3, 1, 1, 64, 20),  # pages that fit no tensor-core box
+    (640, [64] * 10, 1000, 5, 5, 1, 96, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_calls_of_many_rows_and_groups(case, dtype):
+    B, groups, prefix, own, H, kv, hs, ps = WIDE[case]
+    rng = np.random.default_rng(case)
+    lens = (prefix if groups else 0) + rng.integers(0, own + 1, B)
+    firsts = None if groups is None else np.repeat(np.concatenate([[0], np.cumsum(groups)[:-1]]), groups)
+    pool, rows = wide_pool(dtype, B, kv, hs, ps, lens, None if groups is None else [(int(f), prefix // ps * ps) for f in firsts], seed=case)
+    if groups is not None:  # what of the prefix lies in a partly filled page is each sequence's own copy
+        for t in (pool.k, pool.v):
+            tail = prefix % ps
+            if tail:
+                col = pool.table[:, prefix // ps].long()
+                t[0, col, :, :tail] = t[0, col[torch.from_numpy(firsts).cuda()], :, :tail]
+    q = torch.randn((B, H, hs), device="cuda").to(DT[dtype])
+    lse = torch.empty((B, H), device="cuda")
+    args = {} if groups is None else dict(group_starts=dev(np.concatenate([[0], np.cumsum(groups)])), prefix_lens=dev([prefix] * len(groups)))
+    out = pool.attention(q, 0, lse=lse, **args)
+    pool.check()
+    check_wide(out, lse, q, rows, dtype, 1 / math.sqrt(hs), sorted({0, 1, B - 1, *rng.integers(0, B, 40).tolist()}))
+    # every row agrees with the call that shares nothing to the bounds of both, here the type's own step of |v| < 6
+    plain = pool.attention(q, 0)
+    assert float((out.float() - plain.float()).abs().max()) <= 6 * 4 * max(torch.finfo(DT[dtype]).eps, 1e-4)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("n,members,H,kv,hs", [(200_000, 1, 1, 1, 128), (70_001, 3, 4, 2, 64), (131_072, 20, 1, 1, 64),
+                                               (100_003, 150, 1, 1, 64), (40_000, 9, 32, 1, 128)])
+def test_long_prefixes_of_few_heads(dtype, n, members, H, kv, hs):
+    """One KV head over many keys: an item in as many parts as it may have, and merges of several rounds."""
+    lens = [n + 3 * s % 7 for s in range(members)]
+    pool, rows = wide_pool(dtype, members, kv, hs, 16, lens, [(0, n // 16 * 16)] * members, seed=n)
+    q = torch.randn((members, H, hs), device="cuda").to(DT[dtype])
+    lse = torch.empty((members, H), device="cuda")
+    out = pool.attention(q, 0, group_starts=dev([0, members]), prefix_lens=dev([n // 16 * 16]), lse=lse)
+    pool.check()
+    check_wide(out, lse, q, rows, dtype, 1 / math.sqrt(hs), {0, members // 2, members - 1})
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("members", [1, 20, 200])
+def test_many_small_weights_beside_a_large_one(dtype, members):
+    """2^17 keys of weight 2^-25.5 beside one of 1 whose V is 0: the output is what the small ones leave."""
+    n, hs = 1 << 17, 64
+    lens = [n + 1 if s == 0 else n for s in range(members)]
+    pool, rows = wide_pool(dtype, members, 1, hs, 128, lens, [(0, n)] * members, seed=1)
+    low = -25.5 * math.log(2)
+    pool.k.zero_()
+    pool.k[..., 0] = low          # rounded to the type, as the check's rows are
+    pool.v.fill_(1.0)
+    at = [(int(pool.table[0, 5]), 77), (int(pool.table[0, n // 128]), 0)]
+    for page, row in at:
+        pool.k[0, page, :, row, 0] = 0.0
+        pool.v[0, page, :, row] = 0.0
+    q = torch.zeros((members, 1, hs), device="cuda", dtype=DT[dtype])
+    q[..., 0] = 1.0
+    lse = torch.empty((members, 1), device="cuda")
+    out = pool.attention(q, 0, scale=1.0, group_starts=dev([0, members]), prefix_lens=dev([n]), lse=lse)
+    pool.check()
+    check_wide(out, lse, q, rows, dtype, 1.0, {0, members - 1})
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_scores_of_minus_infinity(dtype):
+    """Keys whose score is -inf have weight 0, in a prefix of its first tiles too; a row of nothing else is 0 / 0."""
+    members, n, hs = 24, 512, 64
+    pool, rows = wide_pool(dtype, members, 1, hs, 32, [n + 5] * members, [(0, n)] * members, seed=2)
+    q = torch.randn((members, 1, hs), device="cuda").to(DT[dtype])
+    q[..., 3] = 1.0
+    pages = pool.table[0, :10].long()
+    pool.k[0, pages, :, :, 3] = -math.inf        # keys 0 .. 319
+    own = pool.table[2, :n // 32 + 1].long()
+    lse = torch.empty((members, 1), device="cuda")
+    args = dict(group_starts=dev([0, members]), prefix_lens=dev([n]), lse=lse)
+    out = pool.attention(q, 0, **args)
+    pool.check()
+    assert bool(out.isfinite().all())
+    for b in (0, 2, members - 1):
+        k, v = rows(b)
+        check_wide(out, lse, q, lambda _: (k[320:], v[320:]), dtype, 1 / 8, [b])
+    pool.k[0, own, :, :, 3] = -math.inf          # all of sequence 2 (and the whole prefix, but not the others' own rows)
+    out = pool.attention(q, 0, **args)
+    assert bool(out[2].isnan().all()) and bool(out[[0, 1, 3]].isfinite().all())
+    pool.check()
+
+
+def test_bookkeeping_of_the_largest_calls():
+    """1024 sequences a call, pools of more pages than one round of the search takes."""
+    rng = np.random.default_rng(5)
+    n_seqs, n_pages, ps, max_pages = 2048, 20000, 2, 40
+    pool = make_pool(torch.bfloat16, 1, n_pages, 1, ps, 8, n_seqs, max_pages, fill=0.0)
+    ref = pages_ref.RefPool(n_pages, ps, n_seqs, max_pages)
+    k = pool.k.clone()
+
+    def append(seqs, counts):
+        rows = int(sum(counts))
+        x = torch.randn((1, rows, 1, 8), device="cuda").to(torch.bfloat16)
+        places = ref.append(seqs, [int(c) for c in counts])
+        pool.append(x, x, dev(seqs), dev(np.concatenate([[0], np.cumsum(counts)])))
+        k[0, torch.tensor([p[0] for p in places]).cuda(), 0, torch.tensor([p[1] for p in places]).cuda()] = x[0, :, 0]
+
+    append(rng.permutation(1024), rng.integers(0, 30, 1024))
+    same_books(pool, ref)
+    src = rng.choice(np.flatnonzero(ref.lens[:1024] > 0), 1024)
+    for a, b, t in ref.fork(src, np.arange(1024, 2048)):
+        k[:, b, :, :t] = k[:, a, :, :t]
+    pool.fork(dev(src), dev(np.arange(1024, 2048)))
+    same_books(pool, ref)
+    assert torch.equal(pool.k, k)
+    for compact in (False, True):
+        gone = rng.permutation(n_seqs)[:700]
+        for a, b in ref.free(gone, compact):
+            k[:, b] = k[:, a].clone()
+        pool.free(dev(gone), compact=compact)
+        same_books(pool, ref)
+        assert torch.equal(pool.k, k)
+    append(rng.permutation(n_seqs)[:1024], np.ones(1024, int))
+    same_books(pool, ref)
+    pool.check()
+    assert torch.equal(pool.k, k) and torch.equal(pool.v, k)
+
+
+def test_two_graphs_of_one_pool_and_calls_between():
+    pool, rows, starts, prefix = build("bf16", 8, 2, 64, 16, [(300, [5, 9, 30])], seed=9, poison=0.0, slack=30)
+    pool.refs.copy_(dev(np.bincount(np.concatenate([pool.table.cpu().numpy()[s, :-(-int(n) // 16)] for s, n in enumerate(pool.lens.tolist())]),
+                                    minlength=pool.n_pages)))
+    gs, pl, seqs = dev(starts), dev(prefix), dev([0, 1, 2])
+    q = [torch.randn((3, 8, 64), device="cuda").to(torch.bfloat16) for _ in range(3)]
+    k = torch.randn((3, 2, 64), device="cuda").to(torch.bfloat16)
+    lse = [torch.zeros((3, 8), device="cuda") for _ in range(3)]
+    step, look = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(step):
+        pool.append(k, k, seqs, layer=0)
+        out0 = pool.attention(q[0], 0, group_starts=gs, prefix_lens=pl, lse=lse[0])
+    with torch.cuda.graph(look):
+        out1 = pool.attention(q[1], 0, lse=lse[1])
+    rows = [list(r) for r in rows]
+    for _ in range(4):
+        step.replay()
+        look.replay()
+        out2 = pool.attention(q[2], 0, group_starts=gs, prefix_lens=pl, lse=lse[2])
+        torch.cuda.synchronize()
+        for s in range(3):
+            rows[s] = [np.concatenate([r, k[s:s + 1].double().cpu().numpy()]) for r in rows[s]]
+        for o, x, l in ((out0, q[0], lse[0]), (out1, q[1], lse[1]), (out2, q[2], lse[2])):
+            check_attention(o, l, x, rows, "bf16", 1 / 8)
+    pool.check()
+
+
+def test_arguments_the_host_refuses():
+    pool, rows, starts, prefix = build("bf16", 4, 2, 64, 16, [(30, [5, 9])], seed=10)
+    q = torch.randn((2, 4, 64), device="cuda").to(torch.bfloat16)
+    k = torch.randn((2, 2, 64), device="cuda").to(torch.bfloat16)
+    wide = torch.zeros(4096, device="cuda", dtype=torch.bfloat16)
+    i2 = dev([0, 1])
+    for call in (lambda: pool.attention(q.float(), 0), lambda: pool.attention(q[..., :56], 0), lambda: pool.attention(q[:, 0], 0),
+                 lambda: pool.attention(q, 1), lambda: pool.attention(q, -1), lambda: pool.attention(q[:, :1], 0),
+                 lambda: pool.attention(q, 0, scale=math.inf), lambda: pool.attention(q, 0, scale=math.nan),
+                 lambda: pool.attention(q, 0, seqs=i2.long()), lambda: pool.attention(q, 0, seqs=dev([0, 1, 0])),
+                 lambda: pool.attention(q, 0, group_starts=dev([0, 2])), lambda: pool.attention(q, 0, prefix_lens=dev([2])),
+                 lambda: pool.attention(q, 0, group_starts=dev([0, 1, 1, 2]), prefix_lens=dev([1, 1, 1])),   # more groups than rows
+                 lambda: pool.attention(q, 0, group_starts=dev([0]), prefix_lens=dev([])),
+                 lambda: pool.attention(q, 0, out=wide[:512].view(1, 8, 64)), lambda: pool.attention(q, 0, lse=wide[:8]),
+                 lambda: pool.attention(q, 0, out=wide.as_strided((2, 4, 64), (64, 64, 1))),                 # rows over one another
+                 lambda: pool.attention(q, 0, out=wide.as_strided((2, 4, 64), (128, 64, 1))),
+                 lambda: pool.attention(wide.as_strided((2, 4, 64), (300, 68, 1)), 0),                       # strides of no whole words
+                 lambda: pool.attention(wide[1:513].view(2, 4, 64), 0),                                      # a base of no whole word
+                 lambda: pool.attention(torch.zeros((3, 4, 64), device="cuda", dtype=torch.bfloat16), 0),    # more rows than sequences
+                 lambda: pool.attention(q[:0], 0),
+                 lambda: pool.append(k, k, i2[:1], layer=0), lambda: pool.append(k, k[:1], i2, layer=0),
+                 lambda: pool.append(k, k, [0, 1], layer=0), lambda: pool.append(k[:0], k[:0], i2[:0], layer=0),
+                 lambda: pool.append(k, k, i2, layer=1), lambda: pool.append(k, k, i2, starts=dev([0, 2]), layer=0),
+                 lambda: pool.append(k, k, i2), lambda: pool.append(k[:, :1], k[:, :1], i2, layer=0),
+                 lambda: pool.fork(i2, i2[:1]), lambda: pool.fork(i2[:0], i2[:0]), lambda: pool.fork(i2.cpu(), i2),
+                 lambda: pool.fork(dev(np.arange(1025)), dev(np.arange(1025))), lambda: pool.free(i2.float())):
+        with pytest.raises((ValueError, pkg.L2Error)):
+            call()
+    pool.check()
+    # rows within heads are as good as heads within rows
+    out = torch.empty((4, 2, 64), device="cuda", dtype=torch.bfloat16).transpose(0, 1)
+    lse = torch.empty((2, 4), device="cuda")
+    pool.attention(q, 0, out=out, lse=lse)
+    check_attention(out, lse, q, rows, "bf16", 1 / 8)
