@@ -16,8 +16,8 @@
 // each step from part to part raises one of the two).  A second kernel merges each row's
 // parts in key order, so results do not depend on timing.
 //
-// fp32 caches are walked by attn_pages_f32.cu; in 16-bit caches prefixes that serve many pairs go to the tensor
-// cores instead, as blocks of the same kernel (attn_pages_16.cu, attn_pages_tc.cuh).  A warp keeps its own ring of tiles (cp.async,
+// Caches of either kind are walked (attn_pages_f32.cu, attn_pages_16.cu); prefixes that serve many pairs go to the tensor
+// cores instead, as blocks of the same kernel (attn_pages_tc32.cuh, attn_pages_tc.cuh).  A walking warp keeps its own ring of tiles (cp.async,
 // 16-byte words, rows gathered by the page table one by one, so pages may end anywhere in a tile) and needs no
 // block-wide barrier; with all warps reading, HBM is the bound.
 //
@@ -26,6 +26,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "../../include/l2.h"
 #include "attn_pages.cuh"
@@ -73,6 +75,7 @@ constexpr int kEarly = 8;  // rounds of parts' sums loaded before their weights 
 // rounds of which are loaded beside (m, l).  Then the warps' results are joined in order.
 template <typename T, int NW>
 __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const PagesAttn p) {
+    constexpr bool f32 = std::is_same<T, float>::value;
     constexpr int kRows = kMergeThreads / 32 / NW;  // (row, head) pairs a block
     __shared__ float sm[NW], sl[NW];
     __shared__ float4 sa[NW][32];
@@ -115,12 +118,12 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
         const int n = tc.w * gq, mi = gr * gq + j;
         rest = range(re, mi, n);
         if (tc.y) {
-            const int run = mi / (2 * kTcRows), cost = tc_cost(n, p.head_size);
-            const int u0 = tc.x + (kvh * tc_runs(n) + run) * (kTcItemCost + tc.y * cost), w0 = walker_of(u0, per_tc);
-            tc_rows = min(2 * kTcRows, n - run * 2 * kTcRows);
-            tc_two = tc_rows <= kTcRows;  // two parts of this row a block, tc_rows apart
+            const int run = mi / tc_run(f32), cost = tc_cost(n, p.head_size, f32);
+            const int u0 = tc.x + (kvh * tc_runs(n, f32) + run) * (kTcItemCost + tc.y * cost), w0 = walker_of(u0, per_tc);
+            tc_rows = min(tc_run(f32), n - run * tc_run(f32));
+            tc_two = !f32 && tc_rows <= kTcRows;  // two parts of this row a block, tc_rows apart
             tc_n = (walker_of(u0 + tile_place(tc.y - 1, kTcItemCost, cost), per_tc) - w0 + 1) << tc_two;
-            tc_row = tc.z + kvh * tc_head_rows(n) + mi + 2 * kTcRows * w0;
+            tc_row = tc.z + kvh * tc_head_rows(n, f32) + mi + tc_run(f32) * w0;
         }
     }
     const int total = tc_n + rest.n + own.n, n = (total + NW - 1 - warp) / NW;  // parts of the row, of this warp
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
     auto part = [&](int i, const float2 *&ml, const float *&acc) {
         int e = i * NW + warp;
         if (e < tc_n) {
-            const size_t at = (size_t)(tc_row + 2 * kTcRows * (e >> tc_two) + (tc_two ? (e & 1) * tc_rows : 0));
+            const size_t at = (size_t)(tc_row + tc_run(f32) * (e >> tc_two) + (tc_two ? (e & 1) * tc_rows : 0));
             ml = reinterpret_cast<const float2 *>(p.tc_ml) + at;
             acc = p.tc_acc + at * p.head_size;
         } else {
@@ -259,7 +262,7 @@ struct WsLayout {
 };
 WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms) {
     WsLayout w;
-    w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * attn_pages_16_warps();  // the most warps
+    w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * kWalkWarps;
     const size_t tc = G ? tc_part_rows(B, n_heads, n_kv_heads, num_sms) : 0;
     w.plan = 0;
     w.ml = w.plan + align256(plan_bytes(B, G) + (size_t)B * sizeof(RowPlan));
@@ -290,9 +293,8 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     p.num_sms = num_sms;
     const bool f32 = p.dtype == L2_F32;
     p.tile_shift = f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size);
-    p.walk_warps = f32 ? kWalkWarps : attn_pages_16_warps();
-    // a prefix that serves at most 16 pairs gains nothing on the tensor cores
-    p.tc = !f32 && p.G && p.B * heads_per_kv(p.n_heads, p.n_kv_heads) > kM && attn_pages_tc_supported(p);
+    // whether any prefix of such a call could be one for the tensor cores; the plan decides for each
+    p.tc = p.G && tc_worth(p, p.B * heads_per_kv(p.n_heads, p.n_kv_heads), p.max_pages * p.page_size) && (f32 || attn_pages_tc_supported(p));
     p.plan_in_block = p.B + p.G <= kPlanInBlock;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;

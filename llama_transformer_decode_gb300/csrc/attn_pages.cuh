@@ -10,8 +10,10 @@
 namespace l2 {
 
 constexpr int kM = 16;        // (row, head) pairs of a warp's item
-constexpr int kTcRows = 128;  // pairs of a tensor-core slot; an item has up to two slots' worth
-constexpr int kTcKeys = 128;  // keys of a tensor-core tile
+constexpr int kTcRows = 128;  // pairs of a tensor-core slot
+// Keys of a tensor-core tile and most pairs of an item: 16-bit caches have two slots, fp32 caches one.
+__host__ __device__ constexpr int tc_keys(bool f32) { return f32 ? 64 : 128; }
+__host__ __device__ constexpr int tc_run(bool f32) { return f32 ? kTcRows : 2 * kTcRows; }
 
 // A walker takes the tiles whose place in the numbering of costs falls into its range.  An item of kt tiles is
 // first + kt * cost long: `first` is what starting an item costs.  Tile 0 stands at its beginning, tile k at first + k * cost.
@@ -67,16 +69,16 @@ __device__ __forceinline__ int first_head(int g, int H, int KV) { return cdiv(g 
 // every walker between those of an item's first and last tile holds one of its tiles.
 __device__ __forceinline__ int walker_of(int x, int per) { return (int)((unsigned)x / (unsigned)per); }
 
-// Tensor-core items of a group: n pairs (row, head) of one KV head in runs of up to 256.  A run of up to 128
-// pairs is served by both slots, which take alternate tiles and leave a part of n rows each; of a
+// Tensor-core items of a group: n pairs (row, head) of one KV head in runs of up to tc_run.  In 16-bit caches a run of up
+// to 128 pairs is served by both slots, which take alternate tiles and leave a part of n rows each; of a
 // longer one slot 0 takes the first 128.  Parts of walker w and a run: rows
-// tc_r0 + (rows of the group's runs before) + 256 w of the parts' arrays, which keeps
-// them apart: from walker to walker by 256 rows, from run to run by the run's own.
-__host__ __device__ __forceinline__ int tc_runs(int n) { return cdiv(n, 2 * kTcRows); }
-__host__ __device__ __forceinline__ int tc_run_rows(int n) { return n > kTcRows ? n : 2 * n; }
-__host__ __device__ __forceinline__ int tc_head_rows(int n) {  // of all runs of one KV head
-    const int full = tc_runs(n) - 1;
-    return 2 * kTcRows * full + tc_run_rows(n - 2 * kTcRows * full);
+// tc_r0 + (rows of the group's runs before) + tc_run * w of the parts' arrays, which keeps
+// them apart: from walker to walker by tc_run rows, from run to run by the run's own.
+__host__ __device__ __forceinline__ int tc_runs(int n, bool f32) { return cdiv(n, tc_run(f32)); }
+__host__ __device__ __forceinline__ int tc_head_rows(int n, bool f32) {  // of all runs of one KV head
+    if (f32) return n;
+    const int full = tc_runs(n, false) - 1, last = n - tc_run(false) * full;
+    return tc_run(false) * full + (last > kTcRows ? last : 2 * last);
 }
 
 // Cost of a tile of an item of n pairs, in quarters of reading it.  16-bit: reading bounds every size.  fp32: the FMAs cost
@@ -86,10 +88,24 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n) {  // of all runs of
 constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }
 // Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of reading 8 KB, 0.049 us an SM).  Measured
-// at prefixes of 131072: head size 64, 0.84 to 0.89 us up to 128 pairs (reading), 1.34 at 136, 1.58 at 256; head size 128, 1.3
-// (reading), 1.56, 1.92.  Starting an item: its queries, its part, and the pipeline's filling.
-constexpr int kTcItemCost = 80, kTcMaxTileCost = 39;
-__host__ __device__ __forceinline__ int tc_cost(int n, int hs) { return n > kTcRows ? (hs > 64 ? 39 : 32) : (hs > 64 ? 30 : 18); }
+// at prefixes of 131072: 16-bit, head size 64, 0.84 to 0.89 us up to 128 pairs (reading), 1.34 at 136, 1.58 at 256; head size
+// 128, 1.3 (reading), 1.56, 1.92.  Starting an item: its queries, its part, and the pipeline's filling.
+constexpr int kTcItemCost = 80, kTcMaxTileCost = 90;
+__host__ __device__ __forceinline__ int tc_cost(int n, int hs, bool f32) {
+    if (f32) return hs > 64 ? kTcMaxTileCost : 50;
+    return n > kTcRows ? (hs > 64 ? 39 : 32) : (hs > 64 ? 30 : 18);
+}
+
+// Whether the tensor-core role takes a prefix of so many keys that serves n pairs of a KV head.  Its blocks start slower (8 us to
+// the first parts where a walk has them after 4), so it takes what would keep the walkers for a while if all groups were alike:
+// in 16-bit caches 10 us of them all, in fp32 ones 1 us, since their split products walk slower.  Over 60 calls of 1 to 64
+// rows with prefixes of 16 to 12000, geometric means with no such limit and with this one: bf16 15.4 and 13.1 us, fp16 17.5 and 14.3;
+// with a limit eight times higher, one of 64 rows and five prefixes of up to 16390 took 40 us instead of 32.
+constexpr int kTcLeast16 = 40000, kTcLeast32 = 4000;
+__host__ __device__ __forceinline__ bool tc_worth(const PagesAttn &p, int n, int keys) {
+    return n > kM && (long long)cdiv(n, kM) * p.n_kv_heads * p.G * tile_cost(p.dtype, kM) * (keys >> p.tile_shift) >=
+                         (p.dtype == 0 ? kTcLeast32 : kTcLeast16);
+}
 
 // The last entry i of an ascending list of n (every `stride`-th int of a, the first at most x) that is at most x,
 // found by a whole warp.

@@ -23,7 +23,6 @@ namespace l2 {
 
 namespace {
 
-constexpr int kWarps16 = 8, kThreads16 = 384;  // warps that walk (4 .. 11), threads of a block
 constexpr int kStages = 3;                      // tiles of a warp's ring
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t *r) {
@@ -73,25 +72,25 @@ struct Shape {
     static constexpr int C = HS * 2 / 16;         // 16-byte words a row
     static constexpr int kRow = HS * 2;
     static constexpr int kStage = 2 * KT * kRow;  // K then V
-    static constexpr int kRings = kWarps16 * kStages * kStage;
-    static constexpr int kSmem = kRings + kWarps16 * kItems * (int)sizeof(WalkItem);
+    static constexpr int kRings = kWalkWarps * kStages * kStage;
+    static constexpr int kSmem = kRings + kWalkWarps * kItems * (int)sizeof(WalkItem);
 };
 // Shared memory of either role, before the plan.
-template <int HS>
-constexpr int kWork = Shape<HS>::kSmem > (int)TcShape<HS>::kSmem ? Shape<HS>::kSmem : (int)TcShape<HS>::kSmem;
+template <int HS, bool TC>
+constexpr int kWork = TC && (int)TcShape<HS>::kSmem > Shape<HS>::kSmem ? (int)TcShape<HS>::kSmem : Shape<HS>::kSmem;
 
 // Word c of row r sits at word c ^ swz(r): the eight rows that one ldmatrix phase reads fall into
 // different banks.
 __device__ __forceinline__ int swz(int r) { return r & 7; }
 
-// The walk of one warp (see the head of attn_pages.cu): warp wid of the walking ones.
+// The walk of one warp (see the head of attn_pages.cu): number `warp` of its block's, whose first walking one is block0.
 template <typename T, int HS>
-__device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, unsigned char *smem, int wid) {
+__device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, unsigned char *smem, int warp, int block0) {
     using Sh = Shape<HS>;
     constexpr int KT = Sh::KT, C = Sh::C, NT = KT / 8;  // NT: n8 tiles of keys
-    const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
-    const uint32_t ring = smem_u32(smem) + (threadIdx.x / 32 - 4) * (kStages * Sh::kStage);
-    WalkItem *queue = reinterpret_cast<WalkItem *>(smem + Sh::kRings) + (threadIdx.x / 32 - 4) * kItems;
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3, wid = walker_id(warp, block0);
+    const uint32_t ring = smem_u32(smem) + warp * (kStages * Sh::kStage);
+    WalkItem *queue = reinterpret_cast<WalkItem *>(smem + Sh::kRings) + warp * kItems;
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const int words = p.head_size / 8;  // 16-byte words of a row that exist
     Walk<KT, Sh::kRow> walk;
@@ -253,19 +252,20 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
 
 }  // namespace
 
-// Blocks below the plan's share take the tensor-core role, the others walk.
-template <typename T, int HS, bool BF>
-__global__ void __launch_bounds__(kThreads16, 1) attn_pages_16_kernel(const __grid_constant__ TcAttn ta) {
+// TC: blocks below the plan's share take the tensor-core role, the others walk.  Calls that have no use for it have a kernel of
+// the walk alone, of fewer threads, which is up sooner.
+template <typename T, int HS, bool BF, bool TC>
+__global__ void __launch_bounds__(attn_threads(TC), 1) attn_pages_16_kernel(const __grid_constant__ TcAttn ta) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const PagesAttn &p = ta.p;
     pdl_launch_dependents();
     pdl_wait();
-    const Plan pl = plan_here<kThreads16>(p, smem + kWork<HS>, smem, blockIdx.x == 0);
-    const int n_tc = pl.hdr[kHdrTcBlocks];
-    if ((int)blockIdx.x < n_tc)
+    const Plan pl = plan_here<attn_threads(TC)>(p, smem + kWork<HS, TC>, smem, blockIdx.x == 0);
+    const int n_tc = TC ? pl.hdr[kHdrTcBlocks] : 0, warp = threadIdx.x / 32 - walk_first(TC);
+    if (TC && (int)blockIdx.x < n_tc)
         tc_role<HS, BF>(ta, pl, smem, blockIdx.x);
-    else if (threadIdx.x >= 128)
-        walk_role<T, HS>(p, pl, smem, walker_id(threadIdx.x / 32 - 4, n_tc));
+    else if (warp >= 0)
+        walk_role<T, HS>(p, pl, smem, warp, n_tc);
 }
 
 namespace {
@@ -286,17 +286,21 @@ bool encode_pages(CUtensorMap *m, const char *base, const PagesAttn &p, int rows
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int HS, bool BF>
+template <typename T, int HS, bool BF, bool TC>
 cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
-    constexpr int bytes = kWork<HS> + (int)kPlanSmem;
-    auto fn = attn_pages_16_kernel<T, HS, BF>;
+    constexpr int bytes = kWork<HS, TC> + (int)kPlanSmem;
+    auto fn = attn_pages_16_kernel<T, HS, BF, TC>;
     static DeviceOnce once;
     cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(ta.p.num_sms);
-    cfg.blockDim = dim3(kThreads16);
+    cfg.blockDim = dim3(attn_threads(TC));
     cfg.dynamicSmemBytes = bytes;
     return cudaLaunchKernelEx(&cfg, fn, ta);
+}
+template <typename T, int HS, bool BF>
+cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
+    return ta.p.tc ? launch<T, HS, BF, true>(ta, cfg) : launch<T, HS, BF, false>(ta, cfg);
 }
 
 }  // namespace
@@ -305,18 +309,17 @@ cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
 // tile or are a multiple of one; a tensor's strides are below 2^40 bytes.
 bool attn_pages_tc_supported(const PagesAttn &p) {
     const long long lim = 1ll << 40;
-    return p.page_size >= 8 && (p.page_size % kTcKeys == 0 || kTcKeys % p.page_size == 0) && p.row_stride < lim && p.head_stride < lim &&
+    return p.page_size >= 8 && (p.page_size % tc_keys(false) == 0 || tc_keys(false) % p.page_size == 0) && p.row_stride < lim && p.head_stride < lim &&
            p.page_stride < lim && tensor_map_encoder();
 }
 
 int attn_pages_16_shift(int hs) { return hs <= 64 ? 5 : 4; }
 static_assert(Shape<64>::KT == 1 << 5 && Shape<128>::KT == 1 << 4, "the plan counts tiles by shifts");
-int attn_pages_16_warps() { return kWarps16; }
 
 cudaError_t launch_attn_pages_16(const PagesAttn &p, cudaLaunchConfig_t cfg) {
     TcAttn ta{};
     ta.p = p;
-    ta.box_rows = p.page_size < kTcKeys ? p.page_size : kTcKeys;
+    ta.box_rows = p.page_size < tc_keys(false) ? p.page_size : tc_keys(false);
     ta.scale_log2 = p.scale_log2 < 0.f ? -p.scale_log2 : p.scale_log2;
     ta.flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     if (p.tc && (!encode_pages(&ta.kmap, p.k, p, ta.box_rows) || !encode_pages(&ta.vmap, p.v, p, ta.box_rows))) return cudaErrorInvalidValue;

@@ -1,6 +1,7 @@
-// The walk of the paged attention over fp32 caches (see attn_pages.cu for the split into items, tiles and parts).
+// The paged attention over fp32 caches: one kernel whose blocks take one of two roles, the tensor-core role for shared prefixes
+// (attn_pages_tc32.cuh) or the walk for everything else (see attn_pages.cu for the split into items, tiles and parts).
 //
-// An item has 1 to 16 (row, head) pairs.  Up to 8, products are fp32 FMAs on the CUDA cores: a word of K or V read serves
+// The walk.  // An item has 1 to 16 (row, head) pairs.  Up to 8, products are fp32 FMAs on the CUDA cores: a word of K or V read serves
 // at most 8, 2 FMAs a byte, a third of an SM's rate when HBM feeds it.  From 9 pairs on they are mma.sync of tf32 halves,
 // hi * hi + hi * lo + lo * hi (2^-21 of a product is left out); the tensor core cuts the sums it adds into, so only
 // two steps of hi * hi go into one accumulator before an fp32 addition takes over, and the lo products, 2^-11 as
@@ -16,6 +17,7 @@
 
 #include "../../include/l2.h"
 #include "attn_pages.cuh"
+#include "attn_pages_tc32.cuh"
 #include "attn_plan.cuh"
 #include "l2_device.cuh"
 #include "l2_pages.h"
@@ -35,8 +37,13 @@ struct ShapeF {
     static constexpr int kQ = kM * kRow;          // queries
     static constexpr int kS = KT * 8 * 4;         // scores, then weights [key][pair]
     static constexpr int kWarp = kStagesF * kStage + kQ + kS + kM * 4 + kItems * (int)sizeof(WalkItem);
-    static constexpr int kSmem = kWalkWarps * kWarp + (int)kPlanSmem;
+    static constexpr int kSmem = kWalkWarps * kWarp;
 };
+// Head size of the tensor-core role, and the shared memory of either role, before the plan.
+template <int HS>
+constexpr int kTcHead = HS > 64 ? 128 : 64;
+template <int HS, bool TC>
+constexpr int kWorkF = TC && (int)Tc32Shape<kTcHead<HS>>::kSmem > ShapeF<HS>::kSmem ? (int)Tc32Shape<kTcHead<HS>>::kSmem : ShapeF<HS>::kSmem;
 
 // Word c of row r sits at word c ^ swzf(r): two rows by four words, or one row by eight, fall into different banks.
 __device__ __forceinline__ int swzf(int r) { return ((r & 1) << 2) | ((r >> 1) & 3); }
@@ -354,21 +361,16 @@ __device__ __forceinline__ void tile_mma(StateF<HS> &st, float *m2, float *l2, c
     }
 }
 
-}  // namespace
-
+// The walk of one warp: number `warp` of its block's, whose first walking one is block0.
 template <int HS>
-__global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_f32_kernel(const PagesAttn p) {
+__device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, unsigned char *smem, int warp, int block0) {
     using Sh = ShapeF<HS>;
     constexpr int KT = Sh::KT, C = Sh::C;
-    extern __shared__ __align__(128) unsigned char smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wid = walker_id(warp, 0);
+    const int lane = threadIdx.x & 31, wid = walker_id(warp, block0);
     unsigned char *ring = smem + warp * Sh::kWarp, *qs = ring + kStagesF * Sh::kStage;
     float *ss = reinterpret_cast<float *>(qs + Sh::kQ), *cs = ss + Sh::kS / 4;
     WalkItem *queue = reinterpret_cast<WalkItem *>(cs + kM);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads), words = p.head_size / 4;
-    pdl_launch_dependents();
-    pdl_wait();
-    const Plan pl = plan_here<kWalkWarps * 32>(p, smem + kWalkWarps * Sh::kWarp, smem, blockIdx.x == 0);
     Walk<KT, Sh::kRow> walk;
     walk.start(pl, wid, p.G + p.B);
     StateF<HS> st;
@@ -467,17 +469,45 @@ __global__ void __launch_bounds__(kWalkWarps * 32, 1) attn_pages_f32_kernel(cons
     cp_wait<0>();
 }
 
+}  // namespace
+
+// TC: blocks below the plan's share take the tensor-core role, the others walk.  Calls that have no use for it have a kernel of
+// the walk alone, of fewer threads, which is up sooner.
+template <int HS, bool TC>
+__global__ void __launch_bounds__(attn_threads(TC), 1) attn_pages_f32_kernel(const __grid_constant__ PagesAttn p) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    const Plan pl = plan_here<attn_threads(TC)>(p, smem + kWorkF<HS, TC>, smem, blockIdx.x == 0);
+    const int n_tc = TC ? pl.hdr[kHdrTcBlocks] : 0, warp = threadIdx.x / 32 - walk_first(TC);
+    if constexpr (TC) {
+        if ((int)blockIdx.x < n_tc) return tc32_role<kTcHead<HS>>(p, pl, smem, blockIdx.x);
+        // the four warps that do not walk leave their registers to the eight that do: 24 + 2 * 240 = 3 * 168
+        if (warp < 0) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+            return;
+        }
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    }
+    walk_f32<HS>(p, pl, smem, warp, n_tc);
+}
+
 namespace {
-template <int HS>
+template <int HS, bool TC>
 cudaError_t launch(const PagesAttn &p, cudaLaunchConfig_t cfg) {
-    auto fn = attn_pages_f32_kernel<HS>;
+    constexpr int bytes = kWorkF<HS, TC> + (int)kPlanSmem;
+    auto fn = attn_pages_f32_kernel<HS, TC>;
     static DeviceOnce once;
-    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), ShapeF<HS>::kSmem);
+    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(p.num_sms);
-    cfg.blockDim = dim3(kWalkWarps * 32);
-    cfg.dynamicSmemBytes = ShapeF<HS>::kSmem;
+    cfg.blockDim = dim3(attn_threads(TC));
+    cfg.dynamicSmemBytes = bytes;
     return cudaLaunchKernelEx(&cfg, fn, p);
+}
+template <int HS>
+cudaError_t launch(const PagesAttn &p, cudaLaunchConfig_t cfg) {
+    return p.tc ? launch<HS, true>(p, cfg) : launch<HS, false>(p, cfg);
 }
 }  // namespace
 

@@ -65,7 +65,7 @@ struct alignas(128) TcAttn {
 // 215 us against 152 for 65408 keys, 8 KV heads and 512 pairs each.)
 template <int HS>
 struct TcShape {
-    static constexpr int KT = kTcKeys;
+    static constexpr int KT = tc_keys(false);
     static constexpr bool kOwnP = HS == 64;
     static constexpr int kBlocks = HS / 64;                  // 64-value blocks of a row
     static constexpr uint32_t kBlock = KT * 128, kQBlock = kTcRows * 128;
@@ -96,20 +96,27 @@ __device__ __forceinline__ void tensor4d(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
-__device__ __forceinline__ bool stopped(const TcFx &fx) { return *reinterpret_cast<const volatile int *>(&fx.abort) != 0; }
-__device__ __forceinline__ void stop(TcFx &fx) { *reinterpret_cast<volatile int *>(&fx.abort) = 1; }
+template <class Fx>
+__device__ __forceinline__ bool stopped(const Fx &fx) { return *reinterpret_cast<const volatile int *>(&fx.abort) != 0; }
+template <class Fx>
+__device__ __forceinline__ void stop(Fx &fx) { *reinterpret_cast<volatile int *>(&fx.abort) = 1; }
 
 // A bounded wait that also ends when another warp gave up; false: leave.
-__device__ __forceinline__ bool wait_or_stop(TcFx &fx, uint64_t *bar, uint32_t parity, int *err) {
+template <class Fx>
+__device__ __forceinline__ bool wait_or_stop(Fx &fx, uint64_t *bar, uint32_t parity, int *err) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = 0;  // the timer is read once the wait is long
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if (stopped(fx)) return false;
-        if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
-            atomicOr(err, L2_DEV_ERR_TIMEOUT);
-            stop(fx);
-            return false;
+        if ((i & 255u) == 0) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+                atomicOr(err, L2_DEV_ERR_TIMEOUT);
+                stop(fx);
+                return false;
+            }
         }
     }
 }
@@ -131,6 +138,41 @@ struct Seg {
     int group, kvh, m0, rows, k0, n;  // m0: first pair, rows: pairs (up to 256), tiles k0 .. k0 + n - 1
     int out;                          // first row of its parts
 };
+
+// The next segment of block bid's range of cost, which ends at x_end: the tiles of one item that start in it, from x
+// and group grp on.  Every warp of a block walks the same segments.
+template <bool F32>
+__device__ __forceinline__ bool tc_segment(const PagesAttn &p, const Plan &pl, int gq, int bid, int x_end, int &x, int &grp, Seg &g) {
+#pragma unroll 1
+    for (;; ++grp) {
+        if (x >= x_end) return false;
+        const int kt = pl.tc_kt[grp], t0 = pl.tc_t0[grp];
+        if (kt == 0) continue;
+        const int n = pl.src[grp].rows * gq, runs = tc_runs(n, F32), cost = tc_cost(n, p.head_size, F32), len = kTcItemCost + kt * cost;
+        x = max(x, t0);
+        int item = (int)((unsigned)(x - t0) / (unsigned)len), at = t0 + item * len;
+        int k0 = x == at ? 0 : max(1, cdiv(max(x - at - kTcItemCost, 0), cost));
+        if (k0 >= kt) {
+            ++item;
+            at += len;
+            k0 = 0;
+        }
+        x = at + tile_place(k0, kTcItemCost, cost);
+        if (item >= runs * p.n_kv_heads) continue;
+        if (x >= x_end) return false;
+        const int end = min(kt, max(k0 + 1, cdiv(max(x_end - at - kTcItemCost, 0), cost)));
+        x = end == kt ? at + len : at + tile_place(end, kTcItemCost, cost);
+        g.group = grp;
+        g.kvh = (int)((unsigned)item / (unsigned)runs);
+        const int run = item - g.kvh * runs;
+        g.m0 = run * tc_run(F32);
+        g.rows = min(tc_run(F32), n - g.m0);
+        g.k0 = k0;
+        g.n = end - k0;
+        g.out = pl.tc_r0[grp] + g.kvh * tc_head_rows(n, F32) + g.m0 + tc_run(F32) * bid;
+        return true;
+    }
+}
 
 template <bool BF>
 __device__ __forceinline__ uint32_t pack16(float x, float y) {
@@ -185,38 +227,7 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
     auto o_col = [&](int s) { return tmem + 256 * s + Sh::kO; };
     const int x_begin = bid * pl.hdr[kHdrTcPer], x_end = min(x_begin + pl.hdr[kHdrTcPer], pl.hdr[kHdrTcCost]);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
-    // every role walks the same segments: the tiles that start in the block's range of cost, item by item
-    auto segment = [&](int &x, int &grp, Seg &g) {
-#pragma unroll 1
-        for (;; ++grp) {
-            if (x >= x_end) return false;
-            const int kt = pl.tc_kt[grp], t0 = pl.tc_t0[grp];
-            if (kt == 0) continue;
-            const int n = pl.src[grp].rows * gq, runs = tc_runs(n), cost = tc_cost(n, HS), len = kTcItemCost + kt * cost;
-            x = max(x, t0);
-            int item = (int)((unsigned)(x - t0) / (unsigned)len), at = t0 + item * len;
-            int k0 = x == at ? 0 : max(1, cdiv(max(x - at - kTcItemCost, 0), cost));
-            if (k0 >= kt) {
-                ++item;
-                at += len;
-                k0 = 0;
-            }
-            x = at + tile_place(k0, kTcItemCost, cost);
-            if (item >= runs * p.n_kv_heads) continue;
-            if (x >= x_end) return false;
-            const int end = min(kt, max(k0 + 1, cdiv(max(x_end - at - kTcItemCost, 0), cost)));
-            x = end == kt ? at + len : at + tile_place(end, kTcItemCost, cost);
-            g.group = grp;
-            g.kvh = (int)((unsigned)item / (unsigned)runs);
-            const int run = item - g.kvh * runs;
-            g.m0 = run * 2 * kTcRows;
-            g.rows = min(2 * kTcRows, n - g.m0);
-            g.k0 = k0;
-            g.n = end - k0;
-            g.out = pl.tc_r0[grp] + g.kvh * tc_head_rows(n) + g.m0 + 2 * kTcRows * bid;
-            return true;
-        }
-    };
+    auto segment = [&](int &x, int &grp, Seg &g) { return tc_segment<false>(p, pl, gq, bid, x_end, x, grp, g); };
     // tiles slot s works on, and the tile of its i-th
     auto slot_tiles = [&](const Seg &g, int s) { return g.rows > kTcRows ? g.n : (g.n + 1 - s) >> 1; };
     auto slot_tile = [&](const Seg &g, int s, int i) { return g.rows > kTcRows ? i : 2 * i + s; };

@@ -1,6 +1,7 @@
 // The plan of a paged attention call: lengths of the sources and the numbering of their tiles and items.  Built by one
 // block of NT threads, either a kernel of its own or, for calls of few sources, every block of the kernel for itself.
 #pragma once
+#include "../../include/l2.h"
 #include "attn_pages.cuh"
 
 namespace l2 {
@@ -49,6 +50,7 @@ __device__ __forceinline__ int2 plan_scan(int2 v, int2 *total, int2 *buf) {
 template <int NT, int MAX>
 __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, PlanScratch<NT, MAX> &sc, bool report) {
     const int i = threadIdx.x, S = p.G + p.B, gq = heads_per_kv(p.n_heads, p.n_kv_heads);
+    const bool f32 = p.dtype == L2_F32;
     bool bad = false;
     int len = 0, seq = 0, P = 0, a0 = 0;
     // what depends on nothing is loaded before the lengths, which depend on seqs
@@ -98,14 +100,17 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         }
         __syncthreads();
         // prefixes worth it go to the tensor cores in whole tiles; what is left of them stays with the warps
-        const int n = i < p.G ? (sc.gstart[i + 1] - sc.gstart[i]) * gq : 0, full = i < p.G && p.tc && n > kM ? sc.minlen[i] / kTcKeys : 0;
-        const int2 before = plan_scan<NT>(full ? make_int2((kTcItemCost + full * tc_cost(n, p.head_size)) * tc_runs(n) * p.n_kv_heads, tc_head_rows(n) * p.n_kv_heads)
+        const int n = i < p.G ? (sc.gstart[i + 1] - sc.gstart[i]) * gq : 0;
+        int full = i < p.G && p.tc ? sc.minlen[i] / tc_keys(f32) : 0;
+        if (!tc_worth(p, n, full * tc_keys(f32))) full = 0;
+        const int2 before = plan_scan<NT>(full ? make_int2((kTcItemCost + full * tc_cost(n, p.head_size, f32)) * tc_runs(n, f32) * p.n_kv_heads,
+                                                               tc_head_rows(n, f32) * p.n_kv_heads)
                                                : make_int2(0, 0), &tc_all, sc.sums[0]);
         if (i < p.G) {
             pl.tc_t0[i] = before.x;
             pl.tc_kt[i] = full;
             pl.tc_r0[i] = before.y;
-            sc.mintc[i] = full * kTcKeys;
+            sc.mintc[i] = full * tc_keys(f32);
         }
         __syncthreads();
     }
@@ -144,14 +149,18 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         // blocks of the two roles by cost, at least one of each that has work
         int n_tc = 0, per_tc = kTcMinPer;
         if (tc) {
-            n_tc = (int)((float)p.num_sms * ((float)tc / ((float)tc + (float)cost)) + 0.5f);
-            n_tc = max(1, min(n_tc, p.num_sms - (cost ? 1 : 0)));
+            // n or n + 1 blocks, whichever leaves the slower role less
+            const float t = (float)tc, w = (float)cost;
+            const int most = p.num_sms - (cost ? 1 : 0);
+            n_tc = max(1, min((int)((float)p.num_sms * (t / (t + w))), most));
+            auto slower = [&](int n) { return fmaxf(t / (float)n, cost ? w / (float)(p.num_sms - n) : 0.f); };
+            if (n_tc < most && slower(n_tc + 1) < slower(n_tc)) ++n_tc;
             per_tc = max(kTcMinPer, cdiv(tc, n_tc));
             n_tc = cdiv(tc, per_tc);
         }
         pl.src[S].t0 = cost;
         pl.hdr[kHdrCost] = cost;
-        pl.hdr[kHdrPer] = max(max(kMinPer, sc.spread), cdiv(cost, (p.num_sms - n_tc) * p.walk_warps));
+        pl.hdr[kHdrPer] = max(max(kMinPer, sc.spread), cdiv(cost, (p.num_sms - n_tc) * kWalkWarps));
         pl.hdr[kHdrTcCost] = tc;
         pl.hdr[kHdrTcPer] = per_tc;
         pl.hdr[kHdrTcBlocks] = n_tc;

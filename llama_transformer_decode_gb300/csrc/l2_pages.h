@@ -58,6 +58,12 @@ struct DeviceOnce {
     }
 };
 
+// Warps of a block of its kernels that walk, the last ones; with the tensor-core role there are four more before them.  (Which
+// cost 0.7 us where nothing uses them: a call of 11.6 us took 12.3.)
+constexpr int kWalkWarps = 8;
+__host__ __device__ constexpr int walk_first(bool tc) { return tc ? 4 : 0; }
+__host__ __device__ constexpr int attn_threads(bool tc) { return 32 * (walk_first(tc) + kWalkWarps); }
+
 // Attention of one query row per sequence over its pages (attn_pages.cu).
 struct PagesAttn {
     const char *k, *v;        // this layer's pages
@@ -78,7 +84,7 @@ struct PagesAttn {
     int *plan;
     float *ws_ml, *ws_acc;
     int max_parts;            // parts the workspace holds
-    int num_sms, walk_warps;  // blocks, warps of one that walk
+    int num_sms;              // blocks
     int tile_shift;           // log2 of the keys of a warp's tile
     bool tc;                  // prefixes may go to the tensor cores
     bool plan_in_block;       // every block plans for itself (no plan kernel before)
@@ -86,14 +92,12 @@ struct PagesAttn {
 };
 
 // Its kernels over 16-bit caches (attn_pages_16.cu) and fp32 caches (attn_pages_f32.cu): the logarithm of the keys of a
-// warp's tile, walking warps of a block; whether the pages allow tensor-core tiles.
+// warp's tile; whether 16-bit pages allow tensor-core tiles (fp32 pages all do).
 int attn_pages_16_shift(int head_size);
-int attn_pages_16_warps();
 bool attn_pages_tc_supported(const PagesAttn &p);
 cudaError_t launch_attn_pages_16(const PagesAttn &p, cudaLaunchConfig_t cfg);
 int attn_pages_f32_shift(int head_size);
 cudaError_t launch_attn_pages_f32(const PagesAttn &p, cudaLaunchConfig_t cfg);
-constexpr int kWalkWarps = 8;  // of a block of the fp32 kernel
 
 // cuTensorMapEncodeTiled, looked up once (l2_api.cu).
 void *tensor_map_encoder();
