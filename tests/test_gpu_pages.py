@@ -451,7 +451,7 @@ def test_a_serving_loop_of_all_operators(dtype):
 
 # -- large calls ------------------------------------------------------------
 
-def wide_pool(dtype, n_seqs, kv, hs, ps, lens, prefix_of=None, seed=0, k=None):
+def wide_pool(dtype, n_seqs, kv, hs, ps, lens, prefix_of=None, seed=0, order="head"):
     """A pool filled in a few tensor operations: sequence s holds lens[s] rows in shuffled pages; with prefix_of[s] = (first, n)
     its first n // ps pages are sequence `first`'s.  Returns the pool and a function that gathers a sequence's rows in 64 bits."""
     rng = np.random.default_rng(seed)
@@ -468,7 +468,9 @@ def wide_pool(dtype, n_seqs, kv, hs, ps, lens, prefix_of=None, seed=0, k=None):
         if own_from[s]:
             table[s, :own_from[s]] = table[prefix_of[s][0], :own_from[s]]
     g = torch.Generator(device="cuda").manual_seed(seed)
-    t = [torch.randn((1, n_pages, kv, ps, hs), generator=g, device="cuda").to(DT[dtype]) for _ in range(2)]
+    t = [torch.randn((1, n_pages, kv, ps, hs) if order == "head" else (1, n_pages, ps, kv, hs), generator=g, device="cuda").to(DT[dtype])
+         for _ in range(2)]
+    t = t if order == "head" else [x.transpose(2, 3) for x in t]
     pool = pkg.PagePool.from_tensors(t[0], t[1], dev(np.bincount(np.concatenate([table[s, :held[s]] for s in range(n_seqs)]), minlength=n_pages)),
                                      dev(lens), dev(table))
 
@@ -698,3 +700,89 @@ def test_arguments_the_host_refuses():
     lse = torch.empty((2, 4), device="cuda")
     pool.attention(q, 0, out=out, lse=lse)
     check_attention(out, lse, q, rows, "bf16", 1 / 8)
+
+
+# -- prefixes long enough for the tensor cores ------------------------------
+
+# heads, KV heads, head size, page size, memory order, groups of (prefix, members), most own rows, scale
+LONG = [
+    (8, 1, 64, 16, "head", [(21000, 40)], 9, 0.125),                      # 320 pairs: a run of 256 and one of 64
+    (4, 4, 128, 64, "row", [(20011, 17)], 3, -0.1),                       # 17 pairs, a prefix that ends inside a page
+    (2, 1, 8, 8, "head", [(60000, 65), (30100, 9)], 5, 0.5),              # 130 pairs, 18 pairs
+    (3, 1, 32, 128, "row", [(50000, 43)], 40, 0.2),                       # 129 pairs
+    (12, 4, 48, 256, "head", [(9000, 43), (0, 3), (8999, 30), (7, 1)], 70, 0.15),
+    (5, 2, 96, 32, "row", [(16385, 48)], 2, 0.1),                         # heads not a multiple of KV heads
+    (16, 2, 128, 128, "head", [(12800, 16), (12800, 3), (25600, 2)], 300, 0.09),
+    (64, 1, 64, 32, "head", [(30000, 1), (4096, 9)], 0, 0.125),           # rows without rows of their own; a row alone
+    (6, 6, 64, 20, "head", [(5000, 90)], 4, 0.125),                       # pages that only fp32 can read by tensor core
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_long_prefixes_of_many_pairs(case, dtype):
+    H, kv, hs, ps, order, groups, own, scale = LONG[case]
+    rng = np.random.default_rng(case)
+    sizes = [m for _, m in groups]
+    B = sum(sizes)
+    starts = np.concatenate([[0], np.cumsum(sizes)])
+    firsts, prefix = np.repeat(starts[:-1], sizes), np.repeat([p for p, _ in groups], sizes)
+    lens = prefix + rng.integers(0, own + 1, B)
+    pool, rows = wide_pool(dtype, B, kv, hs, ps, lens, [(int(f), int(p) // ps * ps) for f, p in zip(firsts, prefix)], seed=case, order=order)
+    for t in (pool.k, pool.v):  # the rest of a prefix lies in each sequence's own page
+        for b in range(B):
+            tail, col = int(prefix[b]) % ps, int(prefix[b]) // ps
+            if tail and firsts[b] != b:
+                t[0, int(pool.table[b, col]), :, :tail] = t[0, int(pool.table[firsts[b], col]), :, :tail]
+    q = torch.randn((B, H, hs), device="cuda").to(DT[dtype])
+    lse = torch.empty((B, H), device="cuda")
+    args = dict(group_starts=dev(starts), prefix_lens=dev([p for p, _ in groups]), scale=scale)
+    out = pool.attention(q, 0, lse=lse, **args)
+    pool.check()
+    check_wide(out, lse, q, rows, dtype, scale, sorted({0, 1, B - 1, *rng.integers(0, B, 12).tolist()}))
+    again = pool.attention(q, 0, **args)
+    assert torch.equal(out, again)
+    # a table entry outside the pool: reported, and its rows count as zeros
+    page = int(lens[0] > ps) and int(pool.table[0, 1])
+    pool.table[pool.table == page] = pool.n_pages + 5
+    out = pool.attention(q, 0, **args)
+    with pytest.raises(pkg.L2Error, match="outside the pool"):
+        pool.check()
+    assert bool(out.isfinite().all())
+    pool.k[0, page], pool.v[0, page] = 0, 0
+    pool.table[pool.table == pool.n_pages + 5] = page
+    zeros = pool.attention(q, 0, **args)
+    assert torch.equal(out, zeros)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("hs", [64, 128])
+def test_infinite_scores_in_long_prefixes(dtype, hs):
+    """-inf in K: weight 0, in whole tiles and single keys; NaN in K and in a query: their own rows alone."""
+    members, n, H = 40, 20000, 4
+    pool, rows = wide_pool(dtype, members, 1, hs, 64, [n + s % 3 for s in range(members)], [(0, n // 64 * 64)] * members, seed=3)
+    q = torch.randn((members, H, hs), device="cuda").to(DT[dtype])
+    q[..., 3] = q[..., 3].abs() + 0.5
+    gone = torch.zeros(n + 3, dtype=torch.bool, device="cuda")
+    gone[:512] = True
+    gone[10_000:10_030:7] = True
+    for j in range(n // 64):  # the shared pages
+        hit = gone[64 * j:64 * j + 64]
+        if bool(hit.any()):
+            pool.k[0, int(pool.table[0, j]), 0, hit, 3] = -math.inf
+    q[7, 2] = math.nan
+    lse = torch.empty((members, H), device="cuda")
+    args = dict(group_starts=dev([0, members]), prefix_lens=dev([n // 64 * 64]))
+    out = pool.attention(q, 0, lse=lse, **args)
+    pool.check()
+    assert bool(out[7, 2].isnan().all()) and int(out.isnan().sum()) == hs
+
+    def visible(b):
+        k, v = rows(b)
+        keep = ~gone[:len(k)]
+        return k[keep], v[keep]
+    q[7, 2], out[7, 2], lse[7, 2] = q[7, 1], out[7, 1], lse[7, 1]
+    check_wide(out, lse, q, visible, dtype, 1 / math.sqrt(hs), [0, 7, 13, members - 1])
+    pool.k[0, int(pool.table[0, 100]), 0, 5, 1] = math.nan
+    out = pool.attention(q, 0, **args)
+    assert bool(out.isnan().all())
