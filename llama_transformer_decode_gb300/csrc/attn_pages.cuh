@@ -89,10 +89,12 @@ constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }
 // Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of reading 8 KB, 0.049 us an SM).  Measured
 // at prefixes of 131072: 16-bit, head size 64, 0.84 to 0.89 us up to 128 pairs (reading), 1.34 at 136, 1.58 at 256; head size
-// 128, 1.3 (reading), 1.56, 1.92.  Starting an item: its queries, its part, and the pipeline's filling.
-constexpr int kTcItemCost = 80, kTcMaxTileCost = 90;
+// // 128, 1.3 (reading), 1.56, 1.92; fp32, whatever the pairs, 2.4 and 3.4, and 4.4 for the planning, since the walkers beside it
+// need HBM rather than SMs (32 KV heads of 32 pairs, prefix 2048: 189 us with 3.0, 161 with 3.7, 153 with 4.4 or more).
+// Starting an item: its queries, its part, and the pipeline's filling.
+constexpr int kTcItemCost = 80;
 __host__ __device__ __forceinline__ int tc_cost(int n, int hs, bool f32) {
-    if (f32) return hs > 64 ? kTcMaxTileCost : 50;
+    if (f32) return hs > 64 ? 90 : 50;
     return n > kTcRows ? (hs > 64 ? 39 : 32) : (hs > 64 ? 30 : 18);
 }
 

@@ -8,7 +8,8 @@ namespace l2 {
 
 // Least cost of a range: fewer than two tiles a warp cost more to write and merge as parts than the parallel reading gains.  (And
 // at least the distance of two tiles of any kind, see walker_of.)
-constexpr int kMinPer = kItemCost + 2 * kCostUnit, kTcMinPer = kTcItemCost + kTcMaxTileCost;
+constexpr int kMinPer = kItemCost + 2 * kCostUnit;
+__device__ __forceinline__ int tc_min_per(int hs, bool f32) { return kTcItemCost + tc_cost(2 * kTcRows, hs, f32); }
 // An item of k tiles goes to sqrt(13 k) warps at most (48 for 180 tiles, 285 for 6250): with P warps they take k / P tiles each and
 // the merge P parts, a part a thirteenth of a tile's time, and that many make the sum least.
 constexpr float kSpread = 1.0f / 13.0f;
@@ -102,10 +103,14 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         // prefixes worth it go to the tensor cores in whole tiles; what is left of them stays with the warps
         const int n = i < p.G ? (sc.gstart[i + 1] - sc.gstart[i]) * gq : 0;
         int full = i < p.G && p.tc ? sc.minlen[i] / tc_keys(f32) : 0;
-        if (!tc_worth(p, n, full * tc_keys(f32))) full = 0;
-        const int2 before = plan_scan<NT>(full ? make_int2((kTcItemCost + full * tc_cost(n, p.head_size, f32)) * tc_runs(n, f32) * p.n_kv_heads,
-                                                               tc_head_rows(n, f32) * p.n_kv_heads)
-                                               : make_int2(0, 0), &tc_all, sc.sums[0]);
+        int2 before = make_int2(0, 0);
+        if (p.tc) {
+            if (!tc_worth(p, n, full * tc_keys(f32))) full = 0;
+            if (full)
+                before = make_int2((kTcItemCost + full * tc_cost(n, p.head_size, f32)) * tc_runs(n, f32) * p.n_kv_heads,
+                                   tc_head_rows(n, f32) * p.n_kv_heads);
+            before = plan_scan<NT>(before, &tc_all, sc.sums[0]);
+        }
         if (i < p.G) {
             pl.tc_t0[i] = before.x;
             pl.tc_kt[i] = full;
@@ -147,7 +152,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     if (i == 0) {
         const int cost = all.x, tc = tc_all.x;
         // blocks of the two roles by cost, at least one of each that has work
-        int n_tc = 0, per_tc = kTcMinPer;
+        int n_tc = 0, per_tc = 1;
         if (tc) {
             // n or n + 1 blocks, whichever leaves the slower role less
             const float t = (float)tc, w = (float)cost;
@@ -155,7 +160,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
             n_tc = max(1, min((int)((float)p.num_sms * (t / (t + w))), most));
             auto slower = [&](int n) { return fmaxf(t / (float)n, cost ? w / (float)(p.num_sms - n) : 0.f); };
             if (n_tc < most && slower(n_tc + 1) < slower(n_tc)) ++n_tc;
-            per_tc = max(kTcMinPer, cdiv(tc, n_tc));
+            per_tc = max(tc_min_per(p.head_size, f32), cdiv(tc, n_tc));
             n_tc = cdiv(tc, per_tc);
         }
         pl.src[S].t0 = cost;
