@@ -79,6 +79,32 @@ __device__ int lowest_free(const PagesView &p, int need, int *list, int *buf) {
     return found < need ? found : need;
 }
 
+// Copies `words` 16-byte words, vr to a row and rows row_stride bytes apart, with NT threads, of which this is number t: W
+// words in flight a thread (all loads before the stores, which might alias as far as the compiler knows).
+template <int NT, int W>
+__device__ __forceinline__ void copy_words(const char *a, char *b, int t, int words, int vr, long long row_stride) {
+    const bool flat = row_stride == (long long)vr * 16;
+#pragma unroll 1
+    for (int c0 = t; c0 < words; c0 += W * NT) {
+        uint4 x[W];
+        long long o[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const int c = c0 + j * NT;
+            if (flat)
+                o[j] = (long long)c << 4;
+            else {
+                const int r = (int)((unsigned)c / (unsigned)vr);
+                o[j] = r * row_stride + ((long long)(c - r * vr) << 4);
+            }
+            if (c < words) x[j] = *reinterpret_cast<const uint4 *>(a + o[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (c0 + j * NT < words) *reinterpret_cast<uint4 *>(b + o[j]) = x[j];
+    }
+}
+
 // Ends a refused call: nothing was changed, the row kernels that follow skip.
 __device__ __forceinline__ void refuse(const PagesView &p, int bit) {
     if (threadIdx.x == 0) {
@@ -180,17 +206,25 @@ __global__ void __launch_bounds__(256) pages_write_kernel(const PagesView p, con
     const long long at = page * p.page_stride + (pos % p.page_size) * p.row_stride;
     const int vh = p.row_bytes >> 4, nv = vh * p.n_kv_heads;  // 16-byte words a head, a row
     const int l0 = lg * layers_per, l1 = min(a.n_layers, l0 + layers_per);
-    // two layers of K and V in flight a lane: four loads before the stores
+    // four layers of K and V in flight a lane: their loads before the stores
     for (int c = lane; c < nv; c += 32) {
         const int h = c / vh, w = (c - h * vh) << 4;
         const long long so = (long long)r * a.row_stride + h * a.head_stride + w;
         const long long d = at + h * p.head_stride + w;
-#pragma unroll 4
-        for (int l = l0; l < l1; ++l) {
-            const uint4 kx = __ldcs(reinterpret_cast<const uint4 *>(a.k + so + l * a.layer_stride));
-            const uint4 vx = __ldcs(reinterpret_cast<const uint4 *>(a.v + so + l * a.layer_stride));
-            *reinterpret_cast<uint4 *>(p.k + d + (a.layer0 + l) * p.layer_stride) = kx;
-            *reinterpret_cast<uint4 *>(p.v + d + (a.layer0 + l) * p.layer_stride) = vx;
+        for (int l = l0; l < l1; l += 4) {
+            uint4 kx[4], vx[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (l + j < l1) {
+                    kx[j] = __ldcs(reinterpret_cast<const uint4 *>(a.k + so + (l + j) * a.layer_stride));
+                    vx[j] = __ldcs(reinterpret_cast<const uint4 *>(a.v + so + (l + j) * a.layer_stride));
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (l + j < l1) {
+                    *reinterpret_cast<uint4 *>(p.k + d + (a.layer0 + l + j) * p.layer_stride) = kx[j];
+                    *reinterpret_cast<uint4 *>(p.v + d + (a.layer0 + l + j) * p.layer_stride) = vx[j];
+                }
         }
     }
 }
@@ -274,12 +308,7 @@ __global__ void __launch_bounds__(256) pages_fork_copy_kernel(const PagesView p,
         char *pool = (lv & 1 ? p.v : p.k) + l * p.layer_stride + h * p.head_stride;
         const char *a = pool + from * p.page_stride;
         char *b = pool + to * p.page_stride;
-#pragma unroll 4
-        for (int c = lane; c < words; c += 32) {
-            const int r = c / vr;
-            const long long o = r * p.row_stride + ((c - r * vr) << 4);
-            *reinterpret_cast<uint4 *>(b + o) = *reinterpret_cast<const uint4 *>(a + o);
-        }
+        copy_words<32, 4>(a, b, lane, words, vr, p.row_stride);
     }
 }
 
@@ -363,8 +392,11 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
 }
 
 // Compaction: the moved pages' rows in every layer, and the tables' entries.  A run is one page's
-// rows of one (layer, K or V, head), or all its heads where they lie side by side (`heads` 1).
-__global__ void __launch_bounds__(512) pages_compact_kernel(const PagesView p, int heads, int rows, int row_bytes) {
+// rows of one (layer, K or V, head), or all its heads where they lie side by side (`heads` 1).  A word a thread at a time: more
+// loads before the stores were slower (335 MB moved: 125 us, 134 with two, 149 with four), while a fork's copies, from rows that
+// L2 holds, and an append's, whose rows come side by side, gain from four (63 children of 7B: 59 -> 57 us; 1.4 GB: 225 -> 219).
+constexpr int kCompactThreads = 512;
+__global__ void __launch_bounds__(kCompactThreads, 4) pages_compact_kernel(const PagesView p, int heads, int rows, int row_bytes) {
     pdl_launch_dependents();
     pdl_wait();
     if (p.scratch[kScrRefused]) return;
@@ -391,12 +423,7 @@ __global__ void __launch_bounds__(512) pages_compact_kernel(const PagesView p, i
         char *pool = (lv & 1 ? p.v : p.k) + l * p.layer_stride + h * p.head_stride;
         const char *a = pool + mover[e] * p.page_stride;
         char *b = pool + hole[e] * p.page_stride;
-#pragma unroll 8
-        for (int c = threadIdx.x; c < words; c += blockDim.x) {
-            const int r = c / vr;
-            const long long o = r * p.row_stride + ((long long)(c - r * vr) << 4);
-            *reinterpret_cast<uint4 *>(b + o) = __ldcs(reinterpret_cast<const uint4 *>(a + o));
-        }
+        copy_words<kCompactThreads, 1>(a, b, threadIdx.x, words, vr, p.row_stride);
     }
 }
 
@@ -461,7 +488,7 @@ cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool c
         rows = 1;
     }
     void *args2[] = {const_cast<PagesView *>(&p), &heads, &rows, &bytes};
-    return launch(reinterpret_cast<void *>(pages_compact_kernel), dim3(152 * 4), 512, args2, s);
+    return launch(reinterpret_cast<void *>(pages_compact_kernel), dim3(152 * 4), kCompactThreads, args2, s);
 }
 
 }  // namespace l2
