@@ -3,7 +3,7 @@
 // The plan divides the blocks by the roles' costs, so the two run side by side, with one launch and one start-up.
 //
 // The walk.  A warp's 16 pairs are the M of mma.sync m16n8k16 against its tile's keys (16 products per word read: reading
-// bounds it, at 6.2-6.3 TB/s of suffixes of 1000 rows, and a warp needs no other); q, K and V as
+// bounds it, at 5.8 to 6.2 TB/s of suffixes of 4000 rows, and a warp needs no other); q, K and V as
 // stored, and the weights 2^(x - m) as a sum of two 16-bit values, so nothing is rounded but the fp32 sums and the output.
 // Eight warps of a block walk, each with three tiles (24 KB) of its own.
 #include <cuda.h>

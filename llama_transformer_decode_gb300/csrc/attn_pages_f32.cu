@@ -1,7 +1,7 @@
 // The paged attention over fp32 caches: one kernel whose blocks take one of two roles, the tensor-core role for shared prefixes
 // (attn_pages_tc32.cuh) or the walk for everything else (see attn_pages.cu for the split into items, tiles and parts).
 //
-// The walk.  // An item has 1 to 16 (row, head) pairs.  Up to 8, products are fp32 FMAs on the CUDA cores: a word of K or V read serves
+// The walk.  An item has 1 to 16 (row, head) pairs.  Up to 8, products are fp32 FMAs on the CUDA cores: a word of K or V read serves
 // at most 8, 2 FMAs a byte, a third of an SM's rate when HBM feeds it.  From 9 pairs on they are mma.sync of tf32 halves,
 // hi * hi + hi * lo + lo * hi (2^-21 of a product is left out); the tensor core cuts the sums it adds into, so only
 // two steps of hi * hi go into one accumulator before an fp32 addition takes over, and the lo products, 2^-11 as

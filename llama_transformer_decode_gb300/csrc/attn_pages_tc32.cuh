@@ -18,7 +18,9 @@
 // Tensor memory: Q 3 HS / 2 columns, S 64, P 96, the tile's sums HS; head sizes up to 64 leave room for a second tile of
 // scores, which is then issued two tiles ahead, and otherwise as soon as S has been read.
 //
-// What bounds it: the products, 6 of bf16 for one of fp32, and the weights in turn; a tile of 64 keys by 128 pairs.
+// What bounds it: the warps that cut K and V.  A tile takes 2.4 us at head size 64 and 3.4 at 128, whatever its pairs, and as long
+// with one product of the six; an SM's walkers take 2.5 and 6 for 32 pairs, 10 and 24 for 128.  (Copies by cp.async from every
+// cutting warp: 2.5 and 3.4; plain loads: 6.4 and 13.)
 #pragma once
 #include "attn_pages_tc.cuh"
 

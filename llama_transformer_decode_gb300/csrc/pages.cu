@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
 
 // Compaction: the moved pages' rows in every layer, and the tables' entries.  A run is one page's
 // rows of one (layer, K or V, head), or all its heads where they lie side by side (`heads` 1).  A word a thread at a time: more
-// loads before the stores were slower (335 MB moved: 125 us, 134 with two, 149 with four), while a fork's copies, from rows that
+// loads before the stores were slower (356 MB moved: 125 us, 134 with two, 149 with four), while a fork's copies, from rows that
 // L2 holds, and an append's, whose rows come side by side, gain from four (63 children of 7B: 59 -> 57 us; 1.4 GB: 225 -> 219).
 constexpr int kCompactThreads = 512;
 __global__ void __launch_bounds__(kCompactThreads, 4) pages_compact_kernel(const PagesView p, int heads, int rows, int row_bytes) {
