@@ -448,7 +448,7 @@ typedef struct {
     int G;                   /* groups, 0..B */
     int n_heads;             /* query heads, n_kv_heads..1024 */
     const void *q;           /* DEVICE [B][n_heads][head_size], strides in elements */
-    void *out;               /* DEVICE, alike */
+    void *out;               /* DEVICE, alike; heads within rows or rows within heads */
     float *lse;              /* DEVICE [B][n_heads], or NULL: log of the sum of exp(scores), -inf without rows */
     const int *seqs;         /* DEVICE [B], or NULL: sequence b */
     const int *group_starts; /* DEVICE [G + 1] */

@@ -498,7 +498,7 @@ cudaError_t launch(const PagesAttn &p, cudaLaunchConfig_t cfg) {
     constexpr int bytes = kWorkF<HS, TC> + (int)kPlanSmem;
     auto fn = attn_pages_f32_kernel<HS, TC>;
     static DeviceOnce once;
-    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes);
+    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes, TC ? 168 : 0);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(p.num_sms);
     cfg.blockDim = dim3(attn_threads(TC));

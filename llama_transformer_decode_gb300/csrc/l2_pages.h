@@ -44,14 +44,18 @@ cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, cudaStr
 cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s);
 cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, cudaStream_t s);
 
-// Raises a kernel's shared-memory limit once per device (the attribute outlives the call).
+// Raises a kernel's shared-memory limit once per device (the attribute outlives the call).  least_regs: registers a thread it
+// must have been compiled to, where it hands them around between its warps.
 struct DeviceOnce {
     std::atomic<unsigned long long> done{0};
-    cudaError_t smem(const void *fn, int bytes) {
+    cudaError_t smem(const void *fn, int bytes, int least_regs = 0) {
         int d = 0;
         cudaError_t e = cudaGetDevice(&d);
         if (e != cudaSuccess) return e;
         if (d < 64 && (done.load(std::memory_order_relaxed) >> d & 1)) return cudaSuccess;
+        cudaFuncAttributes a{};
+        if (least_regs && ((e = cudaFuncGetAttributes(&a, fn)) != cudaSuccess || a.numRegs < least_regs))
+            return e != cudaSuccess ? e : cudaErrorInvalidDeviceFunction;
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e == cudaSuccess && d < 64) done.fetch_or(1ull << d, std::memory_order_relaxed);
         return e;

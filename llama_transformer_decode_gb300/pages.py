@@ -109,6 +109,7 @@ class PagePool:
 
     def check(self):
         """Waits for the pool's device and raises L2Error if a call could not be done (and clears the status)."""
+        self._torch.cuda.synchronize(self.device)
         bits = int(self.status.item())
         if bits:
             from . import L2Error

@@ -786,3 +786,31 @@ def test_infinite_scores_in_long_prefixes(dtype, hs):
     pool.k[0, int(pool.table[0, 100]), 0, 5, 1] = math.nan
     out = pool.attention(q, 0, **args)
     assert bool(out.isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_long_prefixes_captured_and_on_two_streams(dtype):
+    members, n, H, hs = 48, 16_384, 4, 128
+    pool, rows = wide_pool(dtype, members, 1, hs, 64, [n + s % 50 for s in range(members)], [(0, n)] * members, seed=4)
+    q = [torch.randn((members, H, hs), device="cuda").to(DT[dtype]) for _ in range(2)]
+    args = dict(group_starts=dev([0, members]), prefix_lens=dev([n]))
+    want = [pool.attention(x, 0, **args) for x in q]
+    lse = torch.empty((members, H), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = pool.attention(q[0], 0, lse=lse, **args)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        for i in range(2):
+            got[i].append(pool.attention(q[i], 0, stream=streams[i], **args))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0])
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i])
+    check_wide(out, lse, q[0], rows, dtype, 1 / math.sqrt(hs), [0, 1, members - 1])
+    pool.check()
