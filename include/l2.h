@@ -411,6 +411,14 @@ typedef struct {
 int l2_pages_append(const L2Pages *pool, const L2PagesRows *rows, void *cuda_stream);
 
 /*
+ * Reads rows back: k and v (written here) receive the first starts[i + 1] -
+ * starts[i] rows of sequence seqs[i], of one layer or all; extend is 0 and no two
+ * rows of k or v share memory.  Rows past a sequence's end are left as they were and
+ * reported (L2_PAGES_BAD_CALL).
+ */
+int l2_pages_read(const L2Pages *pool, const L2PagesRows *rows, void *cuda_stream);
+
+/*
  * Forks: for i < n (1..1024) the empty sequence dst[i] becomes a copy of the
  * first rows[i] rows of src[i] (all its rows with rows NULL).  Whole pages
  * are shared (refs rises); a last part of a page is copied into a new one, the
@@ -464,6 +472,19 @@ long long l2_pages_attention_ws(const L2Pages *pool, int B, int G, int n_heads);
  * of no matter, not used by another call at the same time. */
 int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *args, void *workspace, long long workspace_bytes,
                        void *cuda_stream);
+
+/*
+ * A handle's cache rows into and out of a page pool (fp32, of the handle's layers, KV
+ * heads and head size), without the host: a prompt prefilled once (l2_prefill) and
+ * kept in pages starts later sequences, in any slot, with a copy of its rows.
+ * l2_kv_to_pages appends the slot's rows 0 .. l2_position(slot) - 1 to one sequence;
+ * l2_kv_from_pages copies a sequence's first n_pos rows into the slot and sets its
+ * position to n_pos.  seq: DEVICE [1], the sequence; starts: DEVICE {0, rows}.  Both are
+ * enqueued on the handle's stream; what the device finds wrong (no such sequence, too
+ * few rows or free pages) is in the pool's status.
+ */
+int l2_kv_to_pages(l2_ctx *ctx, int slot, const L2Pages *pool, const int *seq, const int *starts);
+int l2_kv_from_pages(l2_ctx *ctx, int slot, int n_pos, const L2Pages *pool, const int *seq, const int *starts);
 
 /*
  * Fault injection for tests: makes the n-th device allocation from now on

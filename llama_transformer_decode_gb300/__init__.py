@@ -194,6 +194,21 @@ class Decoder:
         self._check(self._lib.l2_kv_import(self._h, int(slot), int(k.shape[1]), ctypes.c_void_p(k.ctypes.data),
                                            ctypes.c_void_p(v.ctypes.data)))
 
+    def _page_index(self, seq: int, n: int):
+        import torch
+        with torch.cuda.stream(self.stream):  # made by the stream that reads them
+            return torch.full((1,), int(seq), dtype=torch.int32, device="cuda"), torch.arange(0, n + 1, n, dtype=torch.int32, device="cuda")
+
+    def kv_to_pages(self, pool, seq: int, slot: int = 0):
+        """The slot's cache rows at the end of sequence ``seq`` of a float32 PagePool (l2_kv_to_pages, on this decoder's stream)."""
+        index, starts = self._page_index(seq, max(self.position(slot), 1))
+        self._check(self._lib.l2_kv_to_pages(self._h, int(slot), pool._ref, index.data_ptr(), starts.data_ptr()))
+
+    def kv_from_pages(self, pool, seq: int, n_pos: int, slot: int = 0):
+        """The first ``n_pos`` rows of sequence ``seq`` into the slot, which then stands at n_pos (l2_kv_from_pages)."""
+        index, starts = self._page_index(seq, max(int(n_pos), 1))
+        self._check(self._lib.l2_kv_from_pages(self._h, int(slot), int(n_pos), pool._ref, index.data_ptr(), starts.data_ptr()))
+
     def launch_op(self, op, layer: int = 0, count: int = 1, batch: int = 1):
         """``count`` launches of one kernel of the step (l2_launch_op, or
         l2_launch_op_batch for a step of ``batch`` rows, the last one run)."""

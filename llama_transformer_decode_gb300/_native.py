@@ -113,7 +113,8 @@ EXPORTS = ("l2_create", "l2_reset", "l2_forward", "l2_forward_batch", "l2_forwar
            "l2_step_input_bytes", "l2_forward_static", "l2_debug_fail_alloc_at", "l2_sample",
            "l2_forward_dev_tokens", "l2_prefill", "l2_debug_fail_graph_at", "l2_debug_wait_timeout",
            "l2_debug_bounds_checked", "l2_debug_limit_cache", "l2_launch_op_batch", "l2_pages_scratch_ints",
-           "l2_pages_init", "l2_pages_append", "l2_pages_fork", "l2_pages_free", "l2_pages_attention_ws", "l2_pages_attention")
+           "l2_pages_init", "l2_pages_append", "l2_pages_read", "l2_pages_fork", "l2_pages_free", "l2_pages_attention_ws",
+           "l2_pages_attention", "l2_kv_to_pages", "l2_kv_from_pages")
 
 _lib = None
 
@@ -166,12 +167,15 @@ def declare(lib):
     lib.l2_pages_init.argtypes = [pp]
     lib.l2_pages_init.restype = i
     lib.l2_pages_append.argtypes = [pp, ctypes.POINTER(L2PagesRows), vp]
+    lib.l2_pages_read.argtypes = [pp, ctypes.POINTER(L2PagesRows), vp]
+    lib.l2_kv_to_pages.argtypes = [vp, i, pp, vp, vp]
+    lib.l2_kv_from_pages.argtypes = [vp, i, i, pp, vp, vp]
     lib.l2_pages_fork.argtypes = [pp, i, vp, vp, vp, vp]
     lib.l2_pages_free.argtypes = [pp, i, vp, i, vp]
     lib.l2_pages_attention_ws.argtypes = [pp, i, i, i]
     lib.l2_pages_attention_ws.restype = ctypes.c_longlong
     lib.l2_pages_attention.argtypes = [pp, ctypes.POINTER(L2PagesAttention), vp, ctypes.c_longlong, vp]
-    for name in ("l2_pages_append", "l2_pages_fork", "l2_pages_free", "l2_pages_attention"):
+    for name in ("l2_pages_append", "l2_pages_read", "l2_kv_to_pages", "l2_kv_from_pages", "l2_pages_fork", "l2_pages_free", "l2_pages_attention"):
         getattr(lib, name).restype = i
     for name in ("l2_create", "l2_reset", "l2_forward", "l2_forward_batch", "l2_forward_host",
                  "l2_position", "l2_debug_attention", "l2_kv_export", "l2_kv_import", "l2_sync",

@@ -1476,6 +1476,47 @@ int l2_kv_import(l2_ctx *c, int slot, int n_pos, const float *k_in, const float 
     return L2_OK;
 }
 
+// Rows 0 .. n - 1 of a slot, as l2_pages_append and l2_pages_read take them.
+static int move_kv(l2_ctx *c, int slot, int n, const L2Pages *pool, const int *seq, const int *starts, bool out) {
+    const L2Config &p = c->cfg;
+    if (!pool) return fail(c, L2_EINVAL, "NULL pool");
+    if (pool->dtype != L2_F32 || pool->n_layers != p.n_layers || pool->n_kv_heads != p.n_kv_heads || pool->head_size != c->head_size)
+        return fail(c, L2_EINVAL, "the pool must hold float32 rows of %d layers, %d KV heads and head size %d", p.n_layers, p.n_kv_heads,
+                    c->head_size);
+    if (!starts) return fail(c, L2_EINVAL, "starts is NULL");
+    const size_t head = (size_t)p.seq_len * c->head_size, layer = head * p.n_kv_heads, at = (size_t)slot * p.n_layers * layer;
+    L2PagesRows r = {};
+    r.n = 1;
+    r.rows = n;
+    r.seqs = seq;
+    r.starts = starts;
+    r.layer = -1;
+    r.extend = out ? 1 : 0;
+    r.k = c->kcache + at;
+    r.v = c->vcache + at;
+    r.layer_stride = (long long)layer;
+    r.row_stride = c->head_size;
+    r.head_stride = (long long)head;
+    const int rc = out ? l2_pages_append(pool, &r, c->stream) : l2_pages_read(pool, &r, c->stream);
+    return rc == L2_OK ? rc : fail(c, rc, "%s", l2_last_error(nullptr));
+}
+
+int l2_kv_to_pages(l2_ctx *c, int slot, const L2Pages *pool, const int *seq, const int *starts) {
+    if (!c) return L2_EINVAL;
+    if (slot < 0 || slot >= c->max_batch) return fail(c, L2_EINVAL, "slot %d outside 0..%d", slot, c->max_batch - 1);
+    if (c->written[slot] == 0) return fail(c, L2_ESTATE, "slot %d has no rows yet", slot);
+    return move_kv(c, slot, c->written[slot], pool, seq, starts, true);
+}
+
+int l2_kv_from_pages(l2_ctx *c, int slot, int n_pos, const L2Pages *pool, const int *seq, const int *starts) {
+    if (!c) return L2_EINVAL;
+    if (slot < 0 || slot >= c->max_batch) return fail(c, L2_EINVAL, "slot %d outside 0..%d", slot, c->max_batch - 1);
+    if (n_pos < 1 || n_pos > c->cfg.seq_len) return fail(c, L2_EINVAL, "n_pos %d outside 1..seq_len", n_pos);
+    const int rc = move_kv(c, slot, n_pos, pool, seq, starts, false);
+    if (rc == L2_OK) c->written[slot] = n_pos;
+    return rc;
+}
+
 int l2_sync(l2_ctx *c) {
     if (!c) return L2_EINVAL;
     L2_CUDA(c, cudaStreamSynchronize(c->stream));

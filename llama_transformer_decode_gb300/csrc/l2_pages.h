@@ -33,14 +33,15 @@ struct PagesView {
 };
 
 struct PagesAppend {
-    const char *k, *v;                                  // new rows
+    char *k, *v;                                        // rows, read or written
     long long layer_stride, row_stride, head_stride;    // bytes
     const int *seqs, *starts;                           // [n], [n + 1] or nullptr (one row each)
     int n, rows, layer0, n_layers;
 };
 
 cudaError_t launch_pages_extend(const PagesView &p, int n, const int *seqs, const int *starts, int rows, cudaStream_t s);
-cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, cudaStream_t s);
+// read: rows from the pool instead of into it.
+cudaError_t launch_pages_rows(const PagesView &p, const PagesAppend &a, bool read, cudaStream_t s);
 cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s);
 cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, cudaStream_t s);
 

@@ -1,4 +1,4 @@
-// Bookkeeping and row movement of a paged KV cache: append, fork, free, compact.
+// Bookkeeping and row movement of a paged KV cache: append, read, fork, free, compact.
 //
 // A pool holds pages of page_size rows; a page belongs to refs[page] sequences, and
 // sequence s of lens[s] rows holds pages table[s][0 .. ceil(lens[s] / page_size)).
@@ -174,7 +174,9 @@ __global__ void __launch_bounds__(kT) pages_extend_kernel(const PagesView p, int
 
 // Append, second half: one warp per new row and layer range copies its heads' K and V.  A row's place
 // is found once (its sequence, length, page: dependent loads) and used for every layer of the warp.
-__global__ void __launch_bounds__(256) pages_write_kernel(const PagesView p, const PagesAppend a, int layers_per) {
+// READ: the other way, from the sequences' first rows.
+template <bool READ>
+__global__ void __launch_bounds__(256) pages_rows_kernel(const PagesView p, const PagesAppend a, int layers_per) {
     const int lane = threadIdx.x & 31;
     const int warp = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     pdl_launch_dependents();
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(256) pages_write_kernel(const PagesView p, con
     const int groups = ceil_div_d(a.n_layers, layers_per);
     if (warp >= a.rows * groups) return;
     const int r = warp / groups, lg = warp - r * groups;
-    if (p.scratch[kScrRefused]) return;
+    if (!READ && p.scratch[kScrRefused]) return;
     int i = r, start = r, end = r + 1;
     if (a.starts) {
         int lo = 0, hi = a.n;
@@ -195,7 +197,12 @@ __global__ void __launch_bounds__(256) pages_write_kernel(const PagesView p, con
         end = a.starts[i + 1];
     }
     const int s = a.seqs[i];
-    const int pos = s >= 0 && s < p.n_seqs ? p.lens[s] - (end - r) : -1;
+    const int n = s >= 0 && s < p.n_seqs ? p.lens[s] : -1;
+    const int pos = n < 0 ? -1 : READ ? r - start : n - (end - r);
+    if (READ && (r < start || r >= end || pos >= n)) {  // no such row
+        if (lane == 0) atomicOr(p.err, L2_PAGES_ERR_ARGS);
+        return;
+    }
     int page = -1;
     if (r >= start && r < end && pos >= 0 && pos / p.page_size < p.max_pages)
         page = p.table[(size_t)s * p.max_pages + pos / p.page_size];
@@ -216,14 +223,16 @@ __global__ void __launch_bounds__(256) pages_write_kernel(const PagesView p, con
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (l + j < l1) {
-                    kx[j] = __ldcs(reinterpret_cast<const uint4 *>(a.k + so + (l + j) * a.layer_stride));
-                    vx[j] = __ldcs(reinterpret_cast<const uint4 *>(a.v + so + (l + j) * a.layer_stride));
+                    const long long rows = so + (l + j) * a.layer_stride, pool = d + (a.layer0 + l + j) * p.layer_stride;
+                    kx[j] = __ldcs(reinterpret_cast<const uint4 *>(READ ? p.k + pool : a.k + rows));
+                    vx[j] = __ldcs(reinterpret_cast<const uint4 *>(READ ? p.v + pool : a.v + rows));
                 }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (l + j < l1) {
-                    *reinterpret_cast<uint4 *>(p.k + d + (a.layer0 + l + j) * p.layer_stride) = kx[j];
-                    *reinterpret_cast<uint4 *>(p.v + d + (a.layer0 + l + j) * p.layer_stride) = vx[j];
+                    const long long rows = so + (l + j) * a.layer_stride, pool = d + (a.layer0 + l + j) * p.layer_stride;
+                    *reinterpret_cast<uint4 *>(READ ? a.k + rows : p.k + pool) = kx[j];
+                    *reinterpret_cast<uint4 *>(READ ? a.v + rows : p.v + pool) = vx[j];
                 }
         }
     }
@@ -451,12 +460,12 @@ cudaError_t launch_pages_extend(const PagesView &p, int n, const int *seqs, cons
     return launch(reinterpret_cast<void *>(pages_extend_kernel), dim3(1), kT, args, s);
 }
 
-cudaError_t launch_pages_write(const PagesView &p, const PagesAppend &a, cudaStream_t s) {
+cudaError_t launch_pages_rows(const PagesView &p, const PagesAppend &a, bool read, cudaStream_t s) {
     if (a.rows == 0) return cudaSuccess;
     int per = 4;
     void *args[] = {const_cast<PagesView *>(&p), const_cast<PagesAppend *>(&a), &per};
     const long long warps = (long long)a.rows * ((a.n_layers + per - 1) / per);
-    return launch(reinterpret_cast<void *>(pages_write_kernel), dim3((unsigned)((warps + 7) / 8)), 256, args, s);
+    return launch(read ? reinterpret_cast<void *>(pages_rows_kernel<true>) : reinterpret_cast<void *>(pages_rows_kernel<false>), dim3((unsigned)((warps + 7) / 8)), 256, args, s);
 }
 
 cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s) {

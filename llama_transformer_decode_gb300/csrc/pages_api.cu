@@ -157,19 +157,8 @@ int check_attn_shape(const char *who, const L2Pages *p, int B, int G, int n_head
     return L2_OK;
 }
 
-}  // namespace
-
-long long l2_pages_scratch_ints(int n_pages) { return n_pages < 1 ? L2_EINVAL : kScrHead + 3ll * n_pages; }
-
-int l2_pages_init(L2Pages *pool) {
-    int device = -1;
-    const int rc = check_pool("l2_pages_init", pool, &device);
-    if (rc == L2_OK) pool->ready = kReady | (unsigned)device;
-    return rc;
-}
-
-int l2_pages_append(const L2Pages *pool, const L2PagesRows *a, void *cuda_stream) {
-    const char *who = "l2_pages_append";
+// Append, or the other way.
+int move_rows(const char *who, const L2Pages *pool, const L2PagesRows *a, bool read, void *cuda_stream) {
     PagesView v;
     int device = -1, rc = view_pool(who, pool, &v, &device);
     if (rc) return rc;
@@ -187,6 +176,10 @@ int l2_pages_append(const L2Pages *pool, const L2PagesRows *a, void *cuda_stream
         (rc = check_stride(who, "row_stride", a->row_stride, a->rows, es)) ||
         (rc = check_stride(who, "head_stride", a->head_stride, pool->n_kv_heads, es)))
         return rc;
+    if (read && a->extend) return refuse(L2_EINVAL, "%s: reading does not extend", who);
+    if (read && ((w.n_layers > 1 && a->layer_stride < pool->head_size) || (a->rows > 1 && a->row_stride < pool->head_size) ||
+                 (pool->n_kv_heads > 1 && a->head_stride < pool->head_size)))
+        return refuse(L2_EINVAL, "%s: the rows overlap", who);
     if ((rc = check_ptr(who, "seqs", a->seqs, 4, &device)) || (a->starts && (rc = check_ptr(who, "starts", a->starts, 4, &device))) ||
         (a->rows && ((rc = check_ptr(who, "k", a->k, 16, &device)) || (rc = check_ptr(who, "v", a->v, 16, &device)))))
         return rc;
@@ -195,8 +188,8 @@ int l2_pages_append(const L2Pages *pool, const L2PagesRows *a, void *cuda_stream
     DeviceGuard guard;
     if (!guard.enter(device)) return refuse(L2_ECUDA, "%s: cannot use device %d", who, device);
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    w.k = static_cast<const char *>(a->k);
-    w.v = static_cast<const char *>(a->v);
+    w.k = static_cast<char *>(const_cast<void *>(a->k));
+    w.v = static_cast<char *>(const_cast<void *>(a->v));
     w.layer_stride = a->layer_stride * es;
     w.row_stride = a->row_stride * es;
     w.head_stride = a->head_stride * es;
@@ -208,7 +201,26 @@ int l2_pages_append(const L2Pages *pool, const L2PagesRows *a, void *cuda_stream
         cudaError_t e = launch_pages_extend(v, a->n, a->seqs, a->starts, a->rows, s);
         if (e != cudaSuccess) return finish(who, e);
     }
-    return finish(who, launch_pages_write(v, w, s));
+    return finish(who, launch_pages_rows(v, w, read, s));
+}
+
+}  // namespace
+
+long long l2_pages_scratch_ints(int n_pages) { return n_pages < 1 ? L2_EINVAL : kScrHead + 3ll * n_pages; }
+
+int l2_pages_init(L2Pages *pool) {
+    int device = -1;
+    const int rc = check_pool("l2_pages_init", pool, &device);
+    if (rc == L2_OK) pool->ready = kReady | (unsigned)device;
+    return rc;
+}
+
+int l2_pages_append(const L2Pages *pool, const L2PagesRows *rows, void *cuda_stream) {
+    return move_rows("l2_pages_append", pool, rows, false, cuda_stream);
+}
+
+int l2_pages_read(const L2Pages *pool, const L2PagesRows *rows, void *cuda_stream) {
+    return move_rows("l2_pages_read", pool, rows, true, cuda_stream);
 }
 
 int l2_pages_fork(const L2Pages *pool, int n, const int *src, const int *dst, const int *rows, void *cuda_stream) {

@@ -122,18 +122,27 @@ class PagePool:
         dimension of all layers) at the ends of sequences ``seqs``: rows
         starts[i]..starts[i + 1] - 1 go to seqs[i] (row i, without ``starts``).  ``extend``
         (default: with all layers, or layer 0) first lengthens the sequences."""
+        a = self._moved(k, v, seqs, starts, layer, (layer is None or layer == 0) if extend is None else bool(extend))
+        rc = self._lib.l2_pages_append(self._ref, ctypes.byref(a), self._stream(stream))
+        if rc:
+            _raise(rc)
+
+    def read(self, k, v, seqs, starts=None, layer=None, stream=None):
+        """Into ``k``, ``v`` (shaped as for append): rows starts[i]..starts[i + 1]-1 receive the first rows of seqs[i]."""
+        a = self._moved(k, v, seqs, starts, layer, False)
+        rc = self._lib.l2_pages_read(self._ref, ctypes.byref(a), self._stream(stream))
+        if rc:
+            _raise(rc)
+
+    def _moved(self, k, v, seqs, starts, layer, extend):
         whole = layer is None
         kp, shape, st = self._rows("k", k, 4 if whole else 3)
         vp, v_shape, v_st = self._rows("v", v, 4 if whole else 3)
         if shape != v_shape or st != v_st or shape[-2] != self.n_kv_heads or (whole and shape[0] != self.n_layers):
             raise ValueError("k and v must be alike, with the pool's layers and heads")
         n = len(seqs)
-        a = L2PagesRows(n, shape[-3], self._ints("seqs", seqs), None if starts is None else self._ints("starts", starts, n + 1),
-                        -1 if whole else int(layer), int((whole or layer == 0) if extend is None else bool(extend)), kp, vp,
-                        st[0] if whole else 0, st[-3], st[-2])
-        rc = self._lib.l2_pages_append(self._ref, ctypes.byref(a), self._stream(stream))
-        if rc:
-            _raise(rc)
+        return L2PagesRows(n, shape[-3], self._ints("seqs", seqs), None if starts is None else self._ints("starts", starts, n + 1),
+                           -1 if whole else int(layer), int(extend), kp, vp, st[0] if whole else 0, st[-3], st[-2])
 
     def fork(self, src, dst, rows=None, stream=None):
         """Empty sequence dst[i] becomes the first rows[i] rows of src[i] (all, without ``rows``)."""

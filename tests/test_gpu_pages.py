@@ -814,3 +814,80 @@ def test_long_prefixes_captured_and_on_two_streams(dtype):
         assert all(torch.equal(x, want[i]) for x in got[i])
     check_wide(out, lse, q[0], rows, dtype, 1 / math.sqrt(hs), [0, 1, members - 1])
     pool.check()
+
+
+# -- reading back, and a decoder's cache in pages -----------------------------
+
+@pytest.mark.parametrize("dtype,ps,kv,hs,order", [("fp32", 16, 4, 8, "head"), ("bf16", 7, 3, 48, "row"), ("fp16", 32, 1, 128, "head")])
+def test_rows_read_back_are_the_rows_appended(dtype, ps, kv, hs, order):
+    L, lens = 5, [40, 1, 0, 77]
+    pool = make_pool(DT[dtype], L, 30, kv, ps, hs, 4, 12, order)
+    starts = dev(np.concatenate([[0], np.cumsum(lens)]))
+    x = torch.randn((2, L, sum(lens), kv, hs), device="cuda").to(DT[dtype])
+    pool.append(x[0], x[1], dev([3, 0, 2, 1]), starts)
+    wide = torch.full((2, L, sum(lens), kv + 2, hs), 3.0, device="cuda").to(DT[dtype])
+    pool.read(wide[0, :, :, 1:-1], wide[1, :, :, 1:-1], dev([3, 0, 2, 1]), starts)
+    assert torch.equal(wide[:, :, :, 1:-1], x) and bool((wide[:, :, :, [0, -1]] == 3).all())
+    # one layer, the first rows only, a sequence twice
+    part = torch.zeros((2, 8, kv, hs), device="cuda").to(DT[dtype])
+    pool.read(part[0], part[1], dev([1, 1]), dev([0, 5, 8]), layer=3)
+    pool.check()
+    assert torch.equal(part[:, :5], x[:, 3, 41:46]) and torch.equal(part[:, 5:], x[:, 3, 41:44])
+    # rows past the end stay and are reported; so are bad indices
+    part.fill_(7.0)
+    pool.read(part[0], part[1], dev([0, 9]), dev([0, 4, 8]), layer=0)
+    with pytest.raises(pkg.L2Error, match="index"):
+        pool.check()
+    assert torch.equal(part[:, :1], x[:, 0, 40:41]) and bool((part[:, 1:] == 7).all())
+    for bad in (lambda: pool.read(x[0, 0, :1].expand(2, kv, hs), x[1, 0, :1].expand(2, kv, hs), dev([3]), dev([0, 2]), layer=0),
+                lambda: pool.read(x[0], x[1], dev([3]), dev([0, 1, 2]))):
+        with pytest.raises((ValueError, pkg.L2Error)):
+            bad()
+
+
+def test_a_prompt_prefilled_once_starts_other_slots():
+    import synth
+    wl = synth.WORKLOADS["gqa_small"]
+    w = pkg.to_device(synth.make_weights(wl))
+    dec = pkg.Decoder(wl.config_tuple(), w, max_batch=3)
+    head = dec.dim // dec.n_heads
+    toks = synth.token_stream(wl, 0, 60)
+    pool = pkg.PagePool(dec.n_layers, 40, dec.n_kv_heads, 16, head, 4, 8)
+    torch.cuda.synchronize()
+    dec.prefill(toks[:50], slot=1)
+    dec.kv_to_pages(pool, 2, slot=1)
+    with torch.cuda.stream(dec.stream):
+        pool.fork(dev([2]), dev([0]))
+        pool.free(dev([2]), compact=True)
+    dec.kv_from_pages(pool, 0, 50, slot=0)
+    dec.kv_from_pages(pool, 0, 33, slot=2)
+    dec.sync()
+    pool.check()
+    assert [dec.position(s) for s in range(3)] == [50, 50, 33]
+    for layer in range(dec.n_layers):
+        want = dec.kv_export(layer, slot=1)
+        for got, n in ((dec.kv_export(layer, slot=0), 50), (dec.kv_export(layer, slot=2), 33)):
+            assert all(np.array_equal(a, b[:n]) for a, b in zip(got, want))
+    # the slots go on alike: a step from the copied rows, and the rest of the prompt from the shorter copy
+    out = torch.empty((3, wl.vocab_size), device="cuda")
+    dec.prefill(toks[33:50], pos0=33, slot=2)
+    dec.forward_batch([toks[50]] * 3, [50] * 3, out)
+    dec.sync()
+    assert torch.equal(out[0], out[1])
+    assert float((out[2] - out[1]).abs().max()) <= 1e-4 * float(out[1].abs().max())  # other chunks of the prompt: other sums
+    # attention over the pages agrees with the rows the decoder exports
+    q = torch.randn((1, dec.n_heads, head), device="cuda")
+    lse = torch.empty((1, dec.n_heads), device="cuda")
+    k, v = (a.reshape(50, dec.n_kv_heads, head).astype(np.float64) for a in [x[:50] for x in dec.kv_export(1, slot=1)])
+    check_attention(pool.attention(q, 1, seqs=dev([0]), lse=lse), lse, q, [(k, v)], "fp32", 1 / math.sqrt(head))
+    # refusals
+    other = pkg.PagePool(dec.n_layers, 4, dec.n_kv_heads, 16, head, 2, 2, dtype=torch.bfloat16)
+    fresh = pkg.Decoder(wl.config_tuple(), w)
+    for call in (lambda: dec.kv_to_pages(other, 0), lambda: dec.kv_from_pages(other, 0, 5), lambda: dec.kv_from_pages(pool, 0, 0),
+                 lambda: dec.kv_from_pages(pool, 0, wl.seq_len + 1), lambda: dec.kv_to_pages(pool, 0, slot=3), lambda: fresh.kv_to_pages(pool, 0)):
+        with pytest.raises(pkg.L2Error):
+            call()
+    dec.kv_from_pages(pool, 3, 1, slot=0)  # an empty sequence: the device's finding
+    dec.sync()
+    with pytest.raises(pkg.L2Error, match="index"):
+        pool.check()

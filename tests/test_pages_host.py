@@ -105,3 +105,11 @@ def test_the_plain_statement_keeps_counts_and_tables_in_step():
             if ref.lens[s] % 4:
                 assert ref.refs[ref.table[s, h - 1]] == 1
         assert count.tolist() == ref.refs.tolist()
+
+
+def test_reading_and_a_handles_rows_refuse_what_the_host_sees(lib):
+    assert lib.l2_pages_read(None, None, None) == pkg.L2_EINVAL
+    assert lib.l2_pages_read(ctypes.byref(pool_struct()), ctypes.byref(_native.L2PagesRows(n=1, rows=1)), None) == pkg.L2_EINVAL
+    assert "l2_pages_init" in text(lib), text(lib)
+    assert lib.l2_kv_to_pages(None, 0, None, None, None) == pkg.L2_EINVAL
+    assert lib.l2_kv_from_pages(None, 0, 1, None, None, None) == pkg.L2_EINVAL
