@@ -356,11 +356,13 @@ int l2_sample(const float *logits, int B, int vocab_size, float temperature, flo
  * that cannot be done whole changes nothing and sets bits of *status, which
  * stay until the caller clears them: L2_PAGES_BAD_PAGE a table entry outside
  * the pool (in an attention call its rows count as zero rows), L2_PAGES_BAD_CALL
- * bad index arrays or inconsistent bookkeeping, L2_PAGES_FULL too few free pages.
+ * bad index arrays or inconsistent bookkeeping, L2_PAGES_FULL too few free pages;
+ * L2_PAGES_TIMEOUT a bounded wait inside a kernel that ran out (its output is void).
  */
 #define L2_F32 0
 #define L2_BF16 1
 #define L2_F16 2
+#define L2_PAGES_TIMEOUT 1
 #define L2_PAGES_BAD_PAGE 2
 #define L2_PAGES_BAD_CALL 4
 #define L2_PAGES_FULL 8

@@ -44,7 +44,7 @@ namespace l2 {
 namespace {
 
 constexpr int kSlotThreads = 128;
-constexpr int kRing = 6;                    // most stages of a ring
+constexpr int kRing = 4;                    // most stages of a ring
 // See above: a row's weights are at most 2^(lift + grow) of its type.
 template <bool BF>
 constexpr float kLiftTc = BF ? 0.f : 13.f;

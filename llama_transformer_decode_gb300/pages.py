@@ -15,11 +15,12 @@ from . import _native
 from ._native import L2Pages, L2PagesAttention, L2PagesRows
 
 L2_F32, L2_BF16, L2_F16 = 0, 1, 2
-L2_PAGES_BAD_PAGE, L2_PAGES_BAD_CALL, L2_PAGES_FULL = 2, 4, 8
-_REASONS = ((L2_PAGES_BAD_PAGE, "a table entry outside the pool"),
+L2_PAGES_TIMEOUT, L2_PAGES_BAD_PAGE, L2_PAGES_BAD_CALL, L2_PAGES_FULL = 1, 2, 4, 8
+_REASONS = ((L2_PAGES_TIMEOUT, "a kernel's bounded wait ran out"),
+            (L2_PAGES_BAD_PAGE, "a table entry outside the pool"),
             (L2_PAGES_BAD_CALL, "bad index arrays or inconsistent bookkeeping"),
             (L2_PAGES_FULL, "too few free pages"))
-_L2_EINVAL, _L2_EDEVICE = -1, -5
+_L2_EDEVICE, _L2_ETIMEOUT = -5, -6
 
 
 def _raise(code: int):
@@ -114,7 +115,7 @@ class PagePool:
         if bits:
             from . import L2Error
             self.status.zero_()
-            raise L2Error(_L2_EDEVICE, "page pool: " + "; ".join(text for bit, text in _REASONS if bits & bit))
+            raise L2Error(_L2_ETIMEOUT if bits & L2_PAGES_TIMEOUT else _L2_EDEVICE, "page pool: " + "; ".join(text for bit, text in _REASONS if bits & bit))
 
     # -- API -----------------------------------------------------------------
     def append(self, k, v, seqs, starts=None, layer=None, extend=None, stream=None):

@@ -891,3 +891,14 @@ def test_a_prompt_prefilled_once_starts_other_slots():
     dec.sync()
     with pytest.raises(pkg.L2Error, match="index"):
         pool.check()
+
+
+@pytest.mark.parametrize("bits,code,words", [(1, pkg.L2_ETIMEOUT, ["wait ran out"]), (2, pkg.L2_EDEVICE, ["outside the pool"]),
+                                             (12, pkg.L2_EDEVICE, ["index arrays", "free pages"])])
+def test_every_status_bit_has_its_words(bits, code, words):
+    pool = make_pool(torch.float32, 1, 2, 1, 4, 8, 1, 2)
+    pool.status.fill_(bits)
+    with pytest.raises(pkg.L2Error) as e:
+        pool.check()
+    assert e.value.code == code and all(w in str(e.value) for w in words)
+    pool.check()  # cleared
