@@ -22,7 +22,9 @@
 // of the unrounded weights.  acc is rescaled only when a row's maximum has grown by more than a factor of 2^kGrow since the
 // last time.  In bf16 weights then stay below 2^8.  fp16 ends at 2^16 and its least step is 2^-24, so its weights are
 // 2^(x - m + 13), at most 2^15: rounding then loses at most 2^-38 of the largest weight on each, where without the 13
-// a prefix of 131072 keys whose weights are 2^-26 of one other key's lost a 512th of the sum.
+// a prefix of 131072 keys whose weights are 2^-26 of one other key's lost a 512th of the sum.  (Error of a 16384-key bf16 prefix
+// against 64 bits 0.0023, of its exact result rounded 0.0017; the weights as two bf16 values each reached that, at 117 us
+// instead of 101 for 32 KV heads of 64 pairs.)
 //
 // What bounds it: up to 128 pairs, reading K and V; above, the products and the exponentials in about
 // equal measure.

@@ -74,8 +74,8 @@ class PagePool:
         self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_size = k.shape
         self.n_seqs, self.max_pages = table.shape
         self._lib = _native.load()
-        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        self._scratch = torch.zeros(self._lib.l2_pages_scratch_ints(self.n_pages), dtype=torch.int32, device=k.device)
+        ints = torch.zeros(64 + self._lib.l2_pages_scratch_ints(self.n_pages), dtype=torch.int32, device=k.device)
+        self.status, self._scratch = ints[:1], ints[64:]
         self._c = L2Pages(k.data_ptr(), v.data_ptr(), refs.data_ptr(), lens.data_ptr(), table.data_ptr(),
                           self.status.data_ptr(), self._scratch.data_ptr(), *k.stride()[:4], kinds[k.dtype], *k.shape,
                           *table.shape)
