@@ -262,10 +262,16 @@ __global__ void __launch_bounds__(attn_threads(TC), 1) attn_pages_16_kernel(cons
     pdl_wait();
     const Plan pl = plan_here<attn_threads(TC)>(p, smem + kWork<HS, TC>, smem, blockIdx.x == 0);
     const int n_tc = TC ? pl.hdr[kHdrTcBlocks] : 0, warp = threadIdx.x / 32 - walk_first(TC);
-    if (TC && (int)blockIdx.x < n_tc)
-        tc_role<HS, BF>(ta, pl, smem, blockIdx.x);
-    else if (warp >= 0)
-        walk_role<T, HS>(p, pl, smem, warp, n_tc);
+    if constexpr (TC) {
+        if ((int)blockIdx.x < n_tc) return tc_role<HS, BF>(ta, pl, smem, blockIdx.x);
+        // the four warps that do not walk leave their registers to the eight that do: 24 + 2 * 240 = 3 * 168
+        if (warp < 0) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+            return;
+        }
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    }
+    walk_role<T, HS>(p, pl, smem, warp, n_tc);
 }
 
 namespace {
@@ -291,7 +297,7 @@ cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
     constexpr int bytes = kWork<HS, TC> + (int)kPlanSmem;
     auto fn = attn_pages_16_kernel<T, HS, BF, TC>;
     static DeviceOnce once;
-    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes);
+    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes, TC ? 168 : 0);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(ta.p.num_sms);
     cfg.blockDim = dim3(attn_threads(TC));
