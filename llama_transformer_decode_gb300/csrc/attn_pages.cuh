@@ -83,7 +83,7 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n, bool f32) {  // of a
 
 // Cost of a tile of an item of n pairs, in quarters of reading it.  16-bit: reading bounds every size.  fp32: the FMAs cost
 // what reading does from 5 pairs on, the split products of more than 8 pairs nearly twice that; measured on GB300,
-// 1 GB of suffixes of head size 128 / 64: 166 / 167 us at 1 pair, 174 / 167 at 4, 198 / 198 at 8, 313 / 273 at 16.
+// 1 GB of suffixes of head size 128 / 64: 168 / 167 us at 1 pair, 174 / 167 at 4, 210 / 220 at 8, 318 / 282 at 16.
 // Starting an item (its queries, its part) takes a warp 1.25 us where a tile takes 1.55.
 constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }

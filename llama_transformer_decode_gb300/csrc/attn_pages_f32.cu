@@ -157,7 +157,6 @@ __device__ __forceinline__ void tile_f32(StateF<HS> &st, const unsigned char *ks
     for (int o = LP / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float mn = fmaxf(st.m, mx), base = mn == -CUDART_INF_F ? 0.f : mn;
     const float corr = exp2f(st.m - base);
-    const bool any_corr = __any_sync(0xffffffffu, corr != 1.f);
     st.m = mn;
     float sum = 0.f;
 #pragma unroll
@@ -170,14 +169,11 @@ __device__ __forceinline__ void tile_f32(StateF<HS> &st, const unsigned char *ks
     st.l = st.l * corr + sum;  // the lane's own keys; joined at the end
     if (sk == 0) cs[sr] = corr;
     __syncwarp();
-    if (any_corr) {
+    // the tile's sums by themselves, so that a long walk is a chain of tiles and not of keys: 20000 keys a warp, error 5.7e-7 in
+    // place of 1.6e-6 (torch's fp32 products: 4.9e-7), for 3 % at 8 pairs
+    float2 t[R][2];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float c = cs[r];
-            st.acc[r][0] = make_float2(st.acc[r][0].x * c, st.acc[r][0].y * c);
-            st.acc[r][1] = make_float2(st.acc[r][1].x * c, st.acc[r][1].y * c);
-        }
-    }
+    for (int r = 0; r < R; ++r) t[r][0] = t[r][1] = make_float2(0.f, 0.f);
     constexpr int VK = 32 / C;
     const int vc = lane % C, vk = lane / C;
 #pragma unroll 2
@@ -200,9 +196,15 @@ __device__ __forceinline__ void tile_f32(StateF<HS> &st, const unsigned char *ks
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float2 w2 = make_float2(pe[r], pe[r]);
-            st.acc[r][0] = ffma2(w2, make_float2(v.x, v.y), st.acc[r][0]);
-            st.acc[r][1] = ffma2(w2, make_float2(v.z, v.w), st.acc[r][1]);
+            t[r][0] = ffma2(w2, make_float2(v.x, v.y), t[r][0]);
+            t[r][1] = ffma2(w2, make_float2(v.z, v.w), t[r][1]);
         }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float2 c = make_float2(cs[r], cs[r]);
+        st.acc[r][0] = ffma2(st.acc[r][0], c, t[r][0]);
+        st.acc[r][1] = ffma2(st.acc[r][1], c, t[r][1]);
     }
 }
 
