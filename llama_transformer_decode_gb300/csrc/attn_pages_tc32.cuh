@@ -159,8 +159,8 @@ __device__ __forceinline__ void tc32_role(const PagesAttn &p, const Plan &pl, un
         auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
         const uint32_t tm = (uint32_t)uniform((int)tmem);
         const uint32_t id_qk = idesc_f16(true, kTcRows, Sh::KT, false), id_pv = idesc_f16(true, kTcRows, HS, true);
-        // parts of A and B of product o, 0 the largest: the smallest products first.  (Loops over o stay loops: the three roles'
-        // code runs side by side, and unrolled they did not fit the instruction caches.)
+        // parts of A and B of product o, 0 the largest: the smallest products first.  (Loops over o stay loops:
+        // unrolled they were six times the code and no faster.)
         auto part_a = [](int o) { return 0x001102 >> 4 * o & 3; };
         auto part_b = [](int o) { return 0x010120 >> 4 * o & 3; };
         int t0 = 0, n_p = 0, nseg = 0;  // tiles before the item, second products, items begun
