@@ -37,6 +37,7 @@
 
 #include "attn_pages.cuh"
 #include "attn_plan.cuh"
+#include "attn_slots.h"
 #include "l2_device.cuh"
 #include "l2_pages.h"
 #include "l2_tc.cuh"
@@ -72,11 +73,7 @@ struct TcShape {
     static constexpr int kBlocks = HS / 64;                  // 64-value blocks of a row
     static constexpr uint32_t kBlock = KT * 128, kQBlock = kTcRows * 128;
     static constexpr uint32_t kTile = kBlocks * kBlock, kQ = kBlocks * kQBlock;
-    // Stages of each ring, an even number: tiles alternate between the slots, so the tile before in a stage was the same
-    // slot's, and whoever waits for a tile has seen that one arrive.  (A slot that waited two phases of a barrier ahead would
-    // take the phase before for its own.)
-    static constexpr int kStages = HS == 64 ? 4 : 2;
-    static_assert(kStages % 2 == 0, "see above");
+    static constexpr int kStages = HS == 64 ? 4 : 2;         // of each ring
     static constexpr uint32_t kTiles = 2 * kQ + 2 * kStages * kTile;
     static constexpr uint32_t kSmem = 1024 + 1024 + kTiles;  // alignment, barriers
     static constexpr int kP = kOwnP ? KT : 0, kO = HS == 64 ? 192 : 128;
@@ -84,7 +81,7 @@ struct TcShape {
 };
 
 struct TcFx {
-    uint64_t full_k[kRing], empty_k[kRing], full_v[kRing], empty_v[kRing];
+    uint64_t full_k[kTakers][kRing], empty_k[kRing], full_v[kTakers][kRing], empty_v[kRing];  // full: by who takes the tile
     uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], fin[2];
     uint32_t tmem;
     int abort;
@@ -199,9 +196,11 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < Sh::kStages; ++i) {
-            mbar_init(&fx.full_k[i], 1);
+            for (int taker = 0; taker < kTakers; ++taker) {
+                mbar_init(&fx.full_k[taker][i], 1);
+                mbar_init(&fx.full_v[taker][i], 1);
+            }
             mbar_init(&fx.empty_k[i], 2);  // a release by each slot
-            mbar_init(&fx.full_v[i], 1);
             mbar_init(&fx.empty_v[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
@@ -230,9 +229,8 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
     const int x_begin = bid * pl.hdr[kHdrTcPer], x_end = min(x_begin + pl.hdr[kHdrTcPer], pl.hdr[kHdrTcCost]);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     auto segment = [&](int &x, int &grp, Seg &g) { return tc_segment<false>(p, pl, gq, bid, x_end, x, grp, g); };
-    // tiles slot s works on, and the tile of its i-th
+    // tiles slot s works on
     auto slot_tiles = [&](const Seg &g, int s) { return g.rows > kTcRows ? g.n : (g.n + 1 - s) >> 1; };
-    auto slot_tile = [&](const Seg &g, int s, int i) { return g.rows > kTcRows ? i : 2 * i + s; };
     const int grp0 = x_begin < x_end ? warp_find(pl.tc_t0, 1, p.G + 1, x_begin) : 0;
 
     if (warp == 0) {
@@ -250,8 +248,8 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
             };
             // one tile of K or V; its page ids were loaded a step before
             auto copy = [&](int kv, int tile, int tt, int page) {
-                const int ns = Sh::kStages, st = tt % ns;
-                uint64_t *full = kv ? &fx.full_v[st] : &fx.full_k[st], *empty = kv ? &fx.empty_v[st] : &fx.empty_k[st];
+                const int ns = Sh::kStages, st = tt % ns, taker = taker_of(tile, g.rows > kTcRows);
+                uint64_t *full = kv ? &fx.full_v[taker][st] : &fx.full_k[taker][st], *empty = kv ? &fx.empty_v[st] : &fx.empty_k[st];
                 if (tt >= ns) ok = wait_or_stop(fx, empty, (uint32_t)((tt / ns - 1) & 1), p.err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) return;
@@ -286,9 +284,9 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
         }
         if (!ok) {
             for (int st = 0; st < Sh::kStages; ++st)
-                for (int ph = 0; ph < 2; ++ph) {
-                    (void)mbar_wait_limit(&fx.full_k[st], ph, p.err, 1000000ull);
-                    (void)mbar_wait_limit(&fx.full_v[st], ph, p.err, 1000000ull);
+                for (int w = 0; w < 2 * kTakers; ++w) {
+                    (void)mbar_wait_limit(&fx.full_k[w >> 1][st], w & 1, p.err, 1000000ull);
+                    (void)mbar_wait_limit(&fx.full_v[w >> 1][st], w & 1, p.err, 1000000ull);
                 }
         }
     } else if (warp <= 2) {
@@ -305,55 +303,54 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
         };
         const uint32_t tm = (uint32_t)uniform((int)tmem) + 256 * s;
         const uint32_t id_qk = idesc_f16(BF, kTcRows, Sh::KT, false), id_pv = idesc_f16(BF, kTcRows, HS, true);
-        int grp = grp0, t_base = 0, x = x_begin, n_p = 0, nseg = 0;  // second products, items begun
-        for (Seg g; ok && segment(x, grp, g); ++nseg) {
-            const bool both = g.rows > kTcRows;
-            const int cnt = uniform(slot_tiles(g, s));
-            // the scores of tile i, once its K is there
-            auto scores = [&](int i) {
-                const int t = uniform(t_base + slot_tile(g, s, i)), st = t % Sh::kStages;
-                if (!await(&fx.full_k[st], t / Sh::kStages)) return;
-                tc_fence_after();
-                const uint64_t dq = desc_sw128(q_at + s * Sh::kQ), dk = desc_sw128(k_at + st * Sh::kTile);
-                if (elect_one()) {
+        int grp = grp0, t_base = 0, x = x_begin, n_p = 0, nq = 0;  // tiles before the item, second products, items with tiles
+        bool both = false;                                         // this item's tiles go to both slots
+        Phases<Sh::kStages> k_phases, v_phases;
+        // a tile's stage, and whether it has landed there
+        auto see = [&](uint64_t (*full)[kRing], Phases<Sh::kStages> &phases, int tile) {
+            const int st = tile % Sh::kStages, taker = taker_of(tile - t_base, both);
+            return await(&full[taker][st], phases.next(taker, st));
+        };
+        auto see_k = [&](int tile) { return see(fx.full_k, k_phases, tile); };
+        auto see_v = [&](int tile) { return see(fx.full_v, v_phases, tile); };
+        auto queries = [&]() { return await(&fx.q_full[s], nq++); };
+        auto scores = [&](int tile) {
+            const int st = uniform(tile) % Sh::kStages;
+            tc_fence_after();
+            const uint64_t dq = desc_sw128(q_at + s * Sh::kQ), dk = desc_sw128(k_at + st * Sh::kTile);
+            if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < HS / 16; ++k)  // 32 bytes a step, blocks of 4 steps
-                        mma_bf16(tm, dq + (uint64_t)(((k >> 2) * Sh::kQBlock + (k & 3) * 32) >> 4),
-                                 dk + (uint64_t)(((k >> 2) * Sh::kBlock + (k & 3) * 32) >> 4), id_qk, k ? 1u : 0u);
-                    mma_commit(&fx.s_full[s]);
-                    mma_commit(&fx.empty_k[st]);
-                    if (!both) mma_commit(&fx.empty_k[st]);  // for the slot that does not use it
-                }
-                __syncwarp();
-            };
-            if (!await(&fx.q_full[s], nseg)) break;  // seen for every item, of a slot without tiles too
-            if (cnt) scores(0);
-            for (int i = 0; i < cnt && ok; ++i) {
-                // the second product, once the weights of the last scores are in (those scores have been read by then: with
-                // weights of their own columns the next scores go first, and the softmax need not wait for this one)
-                const int t = uniform(t_base + slot_tile(g, s, i)), st = t % Sh::kStages;
-                if (!await(&fx.p_full[s], n_p)) break;
-                ++n_p;
-                if (Sh::kOwnP && i + 1 < cnt) scores(i + 1);
-                if (!ok || !await(&fx.full_v[st], t / Sh::kStages)) break;
-                tc_fence_after();
-                const uint64_t dv = desc_sw128_mn(v_at + st * Sh::kTile, Sh::kBlock);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < Sh::KT / 16; ++k)  // 16 keys: 8 columns of weights, 16 lines of V
-                        mma_f16_ta(tm + Sh::kO, tm + Sh::kP + 8 * k, dv + (uint64_t)(k * (16 * 128 >> 4)), id_pv, i || k ? 1u : 0u);
-                    mma_commit(&fx.pv_done[s]);
-                    mma_commit(&fx.empty_v[st]);
-                    if (!both) mma_commit(&fx.empty_v[st]);
-                }
-                __syncwarp();
-                if (!Sh::kOwnP && i + 1 < cnt) {
-                    // the weights lie over the scores: the next ones wait for the product that reads them
-                    if (!await(&fx.pv_done[s], n_p - 1)) break;
-                    scores(i + 1);
-                }
+                for (int k = 0; k < HS / 16; ++k)  // 32 bytes a step, blocks of 4 steps
+                    mma_bf16(tm, dq + (uint64_t)(((k >> 2) * Sh::kQBlock + (k & 3) * 32) >> 4),
+                             dk + (uint64_t)(((k >> 2) * Sh::kBlock + (k & 3) * 32) >> 4), id_qk, k ? 1u : 0u);
+                mma_commit(&fx.s_full[s]);
+                mma_commit(&fx.empty_k[st]);
+                if (!both) mma_commit(&fx.empty_k[st]);  // for the slot that does not use it
             }
-            t_base += g.n;
+            __syncwarp();
+        };
+        // the weights of the last scores are in, and those scores have been read by then: with weights of their own columns the
+        // next scores go before the second product, and the softmax need not wait for it
+        auto weights = [&]() { return await(&fx.p_full[s], n_p++); };
+        auto products = [&](int tile, bool first) {
+            const int st = uniform(tile) % Sh::kStages, add = first ? 0 : 1;
+            tc_fence_after();
+            const uint64_t dv = desc_sw128_mn(v_at + st * Sh::kTile, Sh::kBlock);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < Sh::KT / 16; ++k)  // 16 keys: 8 columns of weights, 16 lines of V
+                    mma_f16_ta(tm + Sh::kO, tm + Sh::kP + 8 * k, dv + (uint64_t)(k * (16 * 128 >> 4)), id_pv, add || k ? 1u : 0u);
+                mma_commit(&fx.pv_done[s]);
+                mma_commit(&fx.empty_v[st]);
+                if (!both) mma_commit(&fx.empty_v[st]);
+            }
+            __syncwarp();
+        };
+        // weights that lie over the scores: the next ones wait for the product that reads them
+        auto drained = [&]() { return await(&fx.pv_done[s], n_p - 1); };
+        for (Seg g; segment(x, grp, g); t_base += g.n) {
+            both = g.rows > kTcRows;
+            if (!slot_item<Sh::kOwnP>(s, t_base, uniform(g.n), both, queries, see_k, see_v, scores, weights, products, drained)) break;
         }
         if (!ok) {  // products in flight end before their memory goes
             if (elect_one()) mma_commit(&fx.fin[s]);
@@ -397,7 +394,7 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
             }
             fence_proxy_async_smem();
             tc_fence_before();  // acc of the segment before has been read
-            mbar_arrive(&fx.q_full[s]);
+            if (n) mbar_arrive(&fx.q_full[s]);  // (nothing would hold this warp back until a slot without tiles had seen it)
             const bool busy = __any_sync(0xffffffffu, r >= 0 && r < mine);  // a warp without pairs only keeps the barriers going
             float base = -CUDART_INF_F, sum = 0.f;
             for (int i = 0; i < n; ++i, ++done) {
