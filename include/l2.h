@@ -447,7 +447,10 @@ int l2_pages_free(const L2Pages *pool, int n, const int *seqs, int compact, void
  * its shortest member's length) are taken from its first row's sequence and
  * read once for the whole group: the caller names groups whose sequences begin
  * with the same rows, as forks do.  G = 0: no sharing.  q, out and the cache
- * have the pool's type; scores, softmax and sums are fp32.  NaN and infinite
+ * have the pool's type; scores, softmax and sums are fp32, whatever else is in the
+ * call (products of fp32 caches within 2^-21 of their size; in 16-bit caches a weight
+ * enters its product as the sum of two values of the type, within 2^-16 of it in
+ * bf16, 2^-22 in fp16).  NaN and infinite
  * scores count as in the formula (-inf: weight 0); an infinity in a cached row
  * of V makes the outputs it reaches infinite or NaN.  Rows no sequence holds may
  * hold anything.

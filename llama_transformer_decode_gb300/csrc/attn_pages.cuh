@@ -87,15 +87,16 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n, bool f32) {  // of a
 // Starting an item (its queries, its part) takes a warp 1.25 us where a tile takes 1.55.
 constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }
-// Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of reading 8 KB, 0.049 us an SM).  Measured
-// at prefixes of 131072: 16-bit, head size 64, 0.84 to 0.89 us up to 128 pairs (reading), 1.34 at 136, 1.58 at 256; head size
-// // 128, 1.3 (reading), 1.56, 1.92; fp32, whatever the pairs, 2.4 and 3.4, and 4.4 for the planning, since the walkers beside it
-// need HBM rather than SMs (32 KV heads of 32 pairs, prefix 2048: 189 us with 3.0, 161 with 3.7, 153 with 4.4 or more).
-// Starting an item: its queries, its part, and the pipeline's filling.
+// Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of reading 8 KB, 0.049 us an SM).  A 16-bit tile
+// alone, prefix 131072: head size 64, 1.0 to 1.4 us up to 128 pairs, 2.0 to 2.4 above; head size 128, 1.65 (reading) to 1.9, and 2.7
+// to 3.3.  Beside walkers, which take HBM, it is longer; over eleven calls with both, prefixes of 4096 to 16384, these costs
+// were best or within 3 % of it (64 rows of 32 KV heads: 108 us, 115 with costs a third lower).  fp32, whatever the pairs, 2.4 and
+// 3.4, and 4.4 for the planning, for the same reason (32 KV heads of 32 pairs, prefix 2048: 189 us with 3.0, 161 with 3.7, 153
+// with 4.4 or more).  Starting an item: its queries, its part, and the pipeline's filling.
 constexpr int kTcItemCost = 80;
 __host__ __device__ __forceinline__ int tc_cost(int n, int hs, bool f32) {
     if (f32) return hs > 64 ? 90 : 50;
-    return n > kTcRows ? (hs > 64 ? 39 : 32) : (hs > 64 ? 30 : 18);
+    return n > kTcRows ? (hs > 64 ? 60 : 38) : (hs > 64 ? 44 : 24);
 }
 
 // Whether the tensor-core role takes a prefix of so many keys that serves n pairs of a KV head.  Its blocks start slower (8 us to

@@ -17,17 +17,18 @@
 //   warps 1-2  the products of slots 0 and 1
 //   warps 4-7, 8-11  slots 0 and 1: queries to shared memory, softmax, parts out
 // A thread owns one pair: its row of scores is a lane of tensor memory, so max and sum need no
-// exchange.  The weights go back over the scores as 16-bit values (at most half a step of the type off, as
-// the output is anyway: 2^-8 in bf16, 2^-11 in fp16) and are the A operand of the second product from there; the sums l are
-// of the unrounded weights.  acc is rescaled only when a row's maximum has grown by more than a factor of 2^kGrow since the
+// exchange.  The weights go back over the scores as sums of two 16-bit values, which is what the walk of attn_pages_16.cu takes (off by at
+// most 2^-16 of a weight in bf16, 2^-22 in fp16), and are the A operand of the second product from there, once for each; the sums l are
+// of the fp32 weights.  acc is rescaled only when a row's maximum has grown by more than a factor of 2^kGrow since the
 // last time.  In bf16 weights then stay below 2^8.  fp16 ends at 2^16 and its least step is 2^-24, so its weights are
 // 2^(x - m + 13), at most 2^15: rounding then loses at most 2^-38 of the largest weight on each, where without the 13
-// a prefix of 131072 keys whose weights are 2^-26 of one other key's lost a 512th of the sum.  (Error of a 16384-key bf16 prefix
-// against 64 bits 0.0023, of its exact result rounded 0.0017; the weights as two bf16 values each reached that, at 117 us
-// instead of 101 for 32 KV heads of 64 pairs.)
+// a prefix of 131072 keys whose weights are 2^-26 of one other key's lost a 512th of the sum.  (One value a weight took 101 us in
+// place of 108 for 32 KV heads of 64 pairs and 16384 bf16 keys, and left an error of 0.0023 in place of 0.0017 against 64 bits, the latter
+// what rounding the exact output leaves; how many bits a row got then hung on what else was in its call.)  The second product
+// of a tile's first 64 keys is issued while the weights of the others are made (256 pairs of head size 128: 4.1 -> 3.2 us a tile).
 //
-// What bounds it: up to 128 pairs, reading K and V; above, the products and the exponentials in about
-// equal measure.
+// What bounds it: up to 128 pairs, reading K and V; above, the products, the exponentials and the cutting of
+// the weights, one after the other for each slot.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -62,27 +63,26 @@ struct alignas(128) TcAttn {
     uint32_t flip;     // 0x8000 in both halves when the scale is negative
 };
 
-// Tensor memory of slot s, columns from 256 s on: scores, weights as 16-bit pairs, acc from kO on.  Head sizes up to 64
-// leave the weights columns of their own, so the next scores are issued right behind the second product, without waiting for
-// it; above, they lie over the scores and the next scores wait.  (Tiles of 64 keys, which would leave room there too, were slower:
-// 215 us against 152 for 65408 keys, 8 KV heads and 512 pairs each.)
+// Tensor memory of slot s, columns from 256 s on: scores, then, in their place, weights as 16-bit pairs (of 64 keys at a time the 32
+// columns of the larger values, then those of what they leave), and acc from kO on.  The next scores wait for the product that reads
+// the weights.  (Tiles of 64 keys, which would leave room for the scores beside them, were slower: 215 us against 152 for 65408
+// keys, 8 KV heads and 512 pairs each.)
 template <int HS>
 struct TcShape {
     static constexpr int KT = tc_keys(false);
-    static constexpr bool kOwnP = HS == 64;
     static constexpr int kBlocks = HS / 64;                  // 64-value blocks of a row
     static constexpr uint32_t kBlock = KT * 128, kQBlock = kTcRows * 128;
     static constexpr uint32_t kTile = kBlocks * kBlock, kQ = kBlocks * kQBlock;
     static constexpr int kStages = HS == 64 ? 4 : 2;         // of each ring
     static constexpr uint32_t kTiles = 2 * kQ + 2 * kStages * kTile;
     static constexpr uint32_t kSmem = 1024 + 1024 + kTiles;  // alignment, barriers
-    static constexpr int kP = kOwnP ? KT : 0, kO = HS == 64 ? 192 : 128;
-    static_assert(kP + KT / 2 <= kO && KT <= kO && kO + HS <= 256, "a slot has 256 columns");
+    static constexpr int kO = KT;
+    static_assert(kO + HS <= 256, "a slot has 256 columns");
 };
 
 struct TcFx {
     uint64_t full_k[kTakers][kRing], empty_k[kRing], full_v[kTakers][kRing], empty_v[kRing];  // full: by who takes the tile
-    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], fin[2];
+    uint64_t q_full[2], s_full[2], p_half[2], p_full[2], pv_done[2], fin[2];
     uint32_t tmem;
     int abort;
 };
@@ -184,6 +184,14 @@ __device__ __forceinline__ uint32_t pack16(float x, float y) {
     }
 }
 
+template <bool BF>
+__device__ __forceinline__ float2 unpack16(uint32_t v) {
+    if constexpr (BF)
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
+    else
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+
 // One block's work, all of its threads.  smem: kSmem bytes; pl: the plan; bid: the block among those of the role.
 template <int HS, bool BF>
 __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsigned char *smem_raw, int bid) {
@@ -206,6 +214,7 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
         for (int i = 0; i < 2; ++i) {
             mbar_init(&fx.q_full[i], kSlotThreads);
             mbar_init(&fx.s_full[i], 1);
+            mbar_init(&fx.p_half[i], kSlotThreads);
             mbar_init(&fx.p_full[i], kSlotThreads);
             mbar_init(&fx.pv_done[i], 1);
         }
@@ -223,9 +232,6 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = fx.tmem;
-    auto s_col = [&](int s) { return tmem + 256 * s; };
-    auto p_col = [&](int s) { return tmem + 256 * s + Sh::kP; };
-    auto o_col = [&](int s) { return tmem + 256 * s + Sh::kO; };
     const int x_begin = bid * pl.hdr[kHdrTcPer], x_end = min(x_begin + pl.hdr[kHdrTcPer], pl.hdr[kHdrTcCost]);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     auto segment = [&](int &x, int &grp, Seg &g) { return tc_segment<false>(p, pl, gq, bid, x_end, x, grp, g); };
@@ -329,28 +335,34 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
             }
             __syncwarp();
         };
-        // the weights of the last scores are in, and those scores have been read by then: with weights of their own columns the
-        // next scores go before the second product, and the softmax need not wait for it
-        auto weights = [&]() { return await(&fx.p_full[s], n_p++); };
+        auto weights = [&]() { return await(&fx.p_half[s], n_p++); };
         auto products = [&](int tile, bool first) {
             const int st = uniform(tile) % Sh::kStages, add = first ? 0 : 1;
-            tc_fence_after();
             const uint64_t dv = desc_sw128_mn(v_at + st * Sh::kTile, Sh::kBlock);
-            if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < Sh::KT / 16; ++k)  // 16 keys: 8 columns of weights, 16 lines of V
-                    mma_f16_ta(tm + Sh::kO, tm + Sh::kP + 8 * k, dv + (uint64_t)(k * (16 * 128 >> 4)), id_pv, add || k ? 1u : 0u);
-                mma_commit(&fx.pv_done[s]);
-                mma_commit(&fx.empty_v[st]);
-                if (!both) mma_commit(&fx.empty_v[st]);
+            for (int half = 0; half < 2; ++half) {
+                if (half && !await(&fx.p_full[s], n_p - 1)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = Sh::KT / 32 * half; k < Sh::KT / 32 * (half + 1); ++k)  // 16 keys: 8 columns of weights, twice, 16 lines of V
+#pragma unroll
+                        for (int lo = 0; lo < 2; ++lo)
+                            mma_f16_ta(tm + Sh::kO, tm + 64 * (k >> 2) + 32 * lo + 8 * (k & 3), dv + (uint64_t)(k * (16 * 128 >> 4)), id_pv, add || k || lo ? 1u : 0u);
+                    if (half) {
+                        mma_commit(&fx.pv_done[s]);
+                        mma_commit(&fx.empty_v[st]);
+                        if (!both) mma_commit(&fx.empty_v[st]);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            return true;
         };
-        // weights that lie over the scores: the next ones wait for the product that reads them
         auto drained = [&]() { return await(&fx.pv_done[s], n_p - 1); };
         for (Seg g; segment(x, grp, g); t_base += g.n) {
             both = g.rows > kTcRows;
-            if (!slot_item<Sh::kOwnP>(s, t_base, uniform(g.n), both, queries, see_k, see_v, scores, weights, products, drained)) break;
+            if (!slot_item(s, t_base, uniform(g.n), both, queries, see_k, see_v, scores, weights, products, drained)) break;
         }
         if (!ok) {  // products in flight end before their memory goes
             if (elect_one()) mma_commit(&fx.fin[s]);
@@ -361,10 +373,10 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
         // ---------------- softmax warps ----------------
         const int s = (warp - 4) >> 2, rl = (tid - 128) & (kSlotThreads - 1);  // slot, lane within it
         const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t sc = s_col(s) + lane_at, pc = p_col(s) + lane_at, oc = o_col(s) + lane_at;
+        const uint32_t sc = tmem + 256 * s + lane_at, oc = sc + Sh::kO;
         unsigned char *qt = qs + s * Sh::kQ;
         const int words = p.head_size / 8;
-        int grp = grp0, done = 0, ended = 0;
+        int grp = grp0, done = 0;
         bool ok = true;
         int x = x_begin;
         Seg g;
@@ -403,8 +415,8 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
                 if (!ok) break;
                 tc_fence_after();
                 constexpr int NC = Sh::KT / 64;
-                float v[64], mx = -CUDART_INF_F;
                 if (busy) {
+                    float v[64], mx;
                     float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
@@ -413,15 +425,6 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
                         for (int j = 0; j < 64; ++j) m4[j & 3] = fmaxf(m4[j & 3], v[j]);
                     }
                     mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * ta.scale_log2;
-                }
-                // the second product of the tile before reads the weights' columns and adds to acc
-                if (Sh::kOwnP && i) {
-                    ok = wait_or_stop(fx, &fx.pv_done[s], (uint32_t)(ended++ & 1), p.err);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                if (busy) {
                     const bool grow = mx > base + (kLiftTc<BF> + kGrow<BF>) || (base == -CUDART_INF_F && mx > base);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float to = grow ? mx - kLiftTc<BF> : base;
@@ -444,31 +447,42 @@ __device__ __forceinline__ void tc_role(const TcAttn &ta, const Plan &pl, unsign
                         base = to;
                     }
                     const float b0 = base == -CUDART_INF_F ? 0.f : base;
-                    // (weights of scores 64 c .. go to columns 32 c .., over scores read by then where they share columns)
                     float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         tmem_ld64_wait(sc + 64 * c, v);
-                        uint32_t w[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float x0 = ex2(fmaf(v[2 * j], ta.scale_log2, -b0)), x1 = ex2(fmaf(v[2 * j + 1], ta.scale_log2, -b0));
-                            s4[j & 3] += x0 + x1;
-                            w[j] = pack16<BF>(x0, x1);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t hi[16], lo[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float *at = v + 32 * h + 2 * j;
+                                const float x0 = ex2(fmaf(at[0], ta.scale_log2, -b0)), x1 = ex2(fmaf(at[1], ta.scale_log2, -b0));
+                                s4[j & 3] += x0 + x1;
+                                hi[j] = pack16<BF>(x0, x1);
+                                const float2 back = unpack16<BF>(hi[j]);
+                                lo[j] = pack16<BF>(x0 - back.x, x1 - back.y);
+                            }
+                            tmem_st16(sc + 64 * c + 16 * h, hi);
+                            tmem_st16(sc + 64 * c + 32 + 16 * h, lo);
                         }
-                        tmem_st32(pc + 32 * c, w);
+                        if (c == 0) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            mbar_arrive(&fx.p_half[s]);
+                        }
                     }
                     sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
                     tmem_wait_st();
-                }
+                } else
+                    mbar_arrive(&fx.p_half[s]);
                 tc_fence_before();
                 mbar_arrive(&fx.p_full[s]);
             }
             if (!ok) break;
             // the part: acc, complete once the slot's last second product is
             if (n) {
-                ended += Sh::kOwnP ? 1 : n;
-                ok = wait_or_stop(fx, &fx.pv_done[s], (uint32_t)((ended - 1) & 1), p.err);
+                ok = wait_or_stop(fx, &fx.pv_done[s], (uint32_t)((done - 1) & 1), p.err);  // (the issuing warp has seen those before)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();

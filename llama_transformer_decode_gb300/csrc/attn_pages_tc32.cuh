@@ -67,12 +67,6 @@ __device__ __forceinline__ void cut3(float x, float y, uint32_t *w) {
     w[2] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);  // at most 8 bits are left
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
-                 "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-                 : "memory");
-}
 __device__ __forceinline__ void tmem_st1(uint32_t addr, uint32_t v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
 }

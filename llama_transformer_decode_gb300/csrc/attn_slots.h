@@ -36,11 +36,11 @@ struct Phases {
 //   queries()            waits for the item's queries; a slot without tiles has none
 //   see_k(t), see_v(t)   waits until K or V of tile t is there
 //   scores(t)            issues the first product
-//   weights()            waits for the weights of the last scores
-//   products(t, first)   issues the second product
+//   weights()            waits for the weights of the first half of the last scores' keys
+//   products(t, first)   issues the second product, for those keys and, once their weights are there, for the others
 //   drained()            waits until it is complete
-// All but the issues return whether to go on.  OWN_P: the weights have columns of their own, so the next scores go before the second product.
-template <bool OWN_P, class Queries, class SeeK, class SeeV, class Scores, class Weights, class Products, class Drained>
+// All but scores return whether to go on.  The weights lie over their scores, so the next scores wait for the product that reads them.
+template <class Queries, class SeeK, class SeeV, class Scores, class Weights, class Products, class Drained>
 L2_SLOTS_FN bool slot_item(int s, int t0, int n, bool both, Queries &queries, SeeK &see_k, SeeV &see_v, Scores &scores, Weights &weights,
                            Products &products, Drained &drained) {
     const int step = both ? 1 : 2, end = t0 + n, begin = t0 + (both ? 0 : s);
@@ -51,12 +51,8 @@ L2_SLOTS_FN bool slot_item(int s, int t0, int n, bool both, Queries &queries, Se
     };
     if (begin < end && (!queries() || !score(begin))) return false;
     for (int t = begin; t < end; t += step) {
-        const bool more = t + step < end;
-        if (!weights()) return false;
-        if (OWN_P && more && !score(t + step)) return false;
-        if (!see_v(t)) return false;
-        products(t, t == begin);
-        if (!OWN_P && more && !(drained() && score(t + step))) return false;
+        if (!weights() || !see_v(t) || !products(t, t == begin)) return false;
+        if (t + step < end && !(drained() && score(t + step))) return false;
     }
     return true;
 }

@@ -129,7 +129,7 @@ struct Item {
 struct Block {
     int ns;
     std::vector<Bar> full[2], empty[2];  // K, V; a full barrier for each taker and stage
-    Bar q_full[2], s_full[2], p_full[2], pv_done[2];
+    Bar q_full[2], s_full[2], p_half[2], p_full[2], pv_done[2];
     std::vector<int> holds[2], readers[2];  // tile that has landed in a stage (-1: none), products reading it
     const char *fault = nullptr;
     void bad(const char *what) {
@@ -137,7 +137,7 @@ struct Block {
     }
 };
 
-template <int NS, bool OWN_P>
+template <int NS>
 const char *simulate(const std::vector<Item> &items, unsigned seed, int lazy) {
     constexpr int ns = NS;
     Sim sim(seed);
@@ -152,7 +152,7 @@ const char *simulate(const std::vector<Item> &items, unsigned seed, int lazy) {
         b.readers[kv].assign(ns, 0);
     }
     for (int s = 0; s < 2; ++s)
-        for (Bar *x : {&b.q_full[s], &b.s_full[s], &b.p_full[s], &b.pv_done[s]}) x->init(1);
+        for (Bar *x : {&b.q_full[s], &b.s_full[s], &b.p_half[s], &b.p_full[s], &b.pv_done[s]}) x->init(1);
 
     auto wait = [&](int me, Bar &bar, int parity) { return sim.yield(me, [&bar, parity] { return bar.passed(parity); }); };
     auto copier = [&](int me) {
@@ -196,10 +196,13 @@ const char *simulate(const std::vector<Item> &items, unsigned seed, int lazy) {
                     return true;
                 };
                 // queue s: this slot's products complete in order, and their commits arrive behind them
-                auto issue = [&](int kv, int t, Bar &after) {
+                auto start = [&](int kv, int t) {
                     const int st = t % ns;
                     if (b.holds[kv][st] != t) b.bad("a product reads a stage that does not hold its tile");
                     ++b.readers[kv][st];
+                };
+                auto commit = [&](int kv, int t, Bar &after) {
+                    const int st = t % ns;
                     sim.later.emplace_back(s, [&b, kv, st, &after, both = g.both] {
                         --b.readers[kv][st];
                         after.arrive();
@@ -209,29 +212,37 @@ const char *simulate(const std::vector<Item> &items, unsigned seed, int lazy) {
                 };
                 auto see_k = [&](int t) { return see(0, t); };
                 auto see_v = [&](int t) { return see(1, t); };
-                auto scores = [&](int t) { issue(0, t, b.s_full[s]); };
-                auto weights = [&]() { return wait(me, b.p_full[s], n_p++); };
-                auto products = [&](int t, bool) { issue(1, t, b.pv_done[s]); };
+                auto scores = [&](int t) {
+                    start(0, t);
+                    commit(0, t, b.s_full[s]);
+                };
+                auto weights = [&]() { return wait(me, b.p_half[s], n_p++); };
+                auto products = [&](int t, bool) {
+                    start(1, t);
+                    if (!wait(me, b.p_full[s], n_p - 1)) return false;
+                    commit(1, t, b.pv_done[s]);
+                    return true;
+                };
                 auto drained = [&]() { return wait(me, b.pv_done[s], n_p - 1); };
-                if (!l2::slot_item<OWN_P>(s, t0, g.n, g.both, queries, see_k, see_v, scores, weights, products, drained)) return;
+                if (!l2::slot_item(s, t0, g.n, g.both, queries, see_k, see_v, scores, weights, products, drained)) return;
                 t0 += g.n;
             }
         };
     };
     auto softmax = [&](int s) {
         return [&, s](int me) {
-            int done = 0, ended = 0;
+            int done = 0;
             for (const Item &g : items) {
                 const int n = g.both ? g.n : (g.n + 1 - s) >> 1;
                 if (n) b.q_full[s].arrive();
                 for (int i = 0; i < n; ++i, ++done) {
                     if (!wait(me, b.s_full[s], done)) return;
-                    if (OWN_P && i && !wait(me, b.pv_done[s], ended++)) return;
+                    b.p_half[s].arrive();
+                    if (!sim.yield(me, [] { return true; })) return;
                     b.p_full[s].arrive();
                 }
                 if (n) {
-                    ended += OWN_P ? 1 : n;
-                    if (!wait(me, b.pv_done[s], ended - 1)) return;
+                    if (!wait(me, b.pv_done[s], done - 1)) return;
                 }
             }
         };
@@ -243,12 +254,12 @@ const char *simulate(const std::vector<Item> &items, unsigned seed, int lazy) {
 
 }  // namespace
 
-// stages, own weights, seeds, then items as n or -n (both slots): prints the first fault, or "ok".  Several lists: separated by 0.
+// stages, seeds, then items as n or -n (both slots): prints the first fault, or "ok".  Several lists: separated by 0.
 int main(int argc, char **argv) {
-    if (argc < 5) return 2;
-    const int ns = atoi(argv[1]), own = atoi(argv[2]), seeds = atoi(argv[3]);
+    if (argc < 4) return 2;
+    const int ns = atoi(argv[1]), seeds = atoi(argv[2]);
     std::vector<std::vector<Item>> lists(1);
-    for (int i = 4; i < argc; ++i) {
+    for (int i = 3; i < argc; ++i) {
         const int n = atoi(argv[i]);
         if (n)
             lists.back().push_back({abs(n), n < 0});
@@ -260,9 +271,7 @@ int main(int argc, char **argv) {
         for (int seed = 0; seed < seeds; ++seed) {
             // events only when nothing else can go on, or now and then, or early
             const int lazy = seed % 3 == 0 ? 100 : seed % 3 == 1 ? 80 : 20;
-            const char *f = ns == 4 ? (own ? simulate<4, true>(items, seed, lazy) : simulate<4, false>(items, seed, lazy))
-                            : ns == 3 ? (own ? simulate<3, true>(items, seed, lazy) : simulate<3, false>(items, seed, lazy))
-                                      : (own ? simulate<2, true>(items, seed, lazy) : simulate<2, false>(items, seed, lazy));
+            const char *f = ns == 4 ? simulate<4>(items, seed, lazy) : ns == 3 ? simulate<3>(items, seed, lazy) : simulate<2>(items, seed, lazy);
             if (!f) continue;
             if (!faults++) {
                 printf("%s: seed %d, tiles", f, seed);

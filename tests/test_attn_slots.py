@@ -18,40 +18,40 @@ def simulate(tmp_path_factory):
     subprocess.run([os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-pthread", "-I", pages_plan.CSRC,
                     os.path.join(HERE, "slot_order.cpp"), "-o", exe], check=True)
 
-    def run(stages, own_weights, seeds, lists):
+    def run(stages, seeds, lists):
         """lists: items as numbers of tiles, negative where both slots take every tile."""
         words = []
         for items in lists:
             words += (["0"] if words else []) + [str(n) for n in items]
-        r = subprocess.run([exe, str(stages), str(int(own_weights)), str(seeds), *words], capture_output=True, text=True, timeout=300)
+        r = subprocess.run([exe, str(stages), str(seeds), *words], capture_output=True, text=True, timeout=300)
         assert r.returncode == 0, r.stdout
         assert r.stdout.strip() == "ok"
     return run
 
 
-# stages of a ring, weights in columns of their own: head sizes up to 64, and above; and what neither uses
-SHAPES = [(4, True), (2, False), (4, False), (3, True)]
+# stages of a ring: head sizes up to 64, and above; and what neither uses
+SHAPES = [4, 2, 3]
 
 
-@pytest.mark.parametrize("stages,own", SHAPES)
-def test_every_order_of_short_items(simulate, stages, own):
+@pytest.mark.parametrize("stages", SHAPES)
+def test_every_order_of_short_items(simulate, stages):
     kinds = [1, 2, 3, -1, -2]
-    simulate(stages, own, 3, [x for n in (1, 2, 3) for x in itertools.product(kinds, repeat=n)])
+    simulate(stages, 3, [x for n in (1, 2, 3) for x in itertools.product(kinds, repeat=n)])
 
 
-@pytest.mark.parametrize("stages,own", SHAPES)
-def test_items_of_many_tiles(simulate, stages, own):
-    simulate(stages, own, 12, [(1, 51), (52, 1, 9), (7, -8, 5), (-5, 1, 1, 1, 12), (1,) * 12 + (20,), (3, -1, 3, -1, 3, -1, 10)])
+@pytest.mark.parametrize("stages", SHAPES)
+def test_items_of_many_tiles(simulate, stages):
+    simulate(stages, 12, [(1, 51), (52, 1, 9), (7, -8, 5), (-5, 1, 1, 1, 12), (1,) * 12 + (20,), (3, -1, 3, -1, 3, -1, 10)])
 
 
 @pytest.mark.parametrize("case", range(len(pages_plan.CROSSED)))
 def test_blocks_of_planned_calls(simulate, case):
     groups, _, heads, kv, hs = pages_plan.CROSSED[case]
-    stages, own = (2, False) if hs > 64 else (4, True)
+    stages = 2 if hs > 64 else 4
     blocks = pages_plan.tc_blocks(groups, pages_plan.crossed_lens(case), heads, kv, hs)
     crossed = [b for b in blocks if pages_plan.slots_change(b, stages)]
     assert crossed, "a call whose blocks do not cross slots tests nothing"
-    simulate(stages, own, 4, [[-n if both else n for _, _, _, n, both in b] for b in crossed])
+    simulate(stages, 4, [[-n if both else n for _, _, _, n, both in b] for b in crossed])
 
 
 def test_the_replayed_plan_covers_every_tile_once():

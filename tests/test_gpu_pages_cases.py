@@ -49,3 +49,42 @@ def test_blocks_that_go_on_to_another_item(case, dtype):
     for _ in range(5):
         assert torch.equal(pool.attention(q, 0, **args), out)
     pool.check()
+
+
+# heads, KV heads, head size, members, prefix, whether the tensor-core role takes the prefix
+WEIGHTS = [(32, 4, 64, 40, 6400, True), (32, 32, 64, 40, 3456, True), (32, 32, 128, 40, 2048, True), (32, 4, 128, 40, 3200, True),
+           (8, 2, 64, 3, 700, False), (8, 8, 128, 1, 1000, False)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", range(len(WEIGHTS)))
+def test_weights_of_16_bit_caches_are_not_rounded_to_16_bits(case, dtype):
+    """Whichever way a tile goes, a weight is two values of the type: off by at most w = 2^-16 (bf16: a half step of a half step)
+    or 2^-22 (fp16), and in fp16 by 2^-38 of the largest.  Keys differ in one dimension, so a score is one exact product, off by
+    the scaling alone, e = 8u of its size; a sum takes two products per 16 keys, each add at most 2u of the sum of w |v|.
+    A single 16-bit value (half a step of the type on each weight) does not keep this where few keys matter."""
+    H, kv, hs, members, prefix, tc = WEIGHTS[case]
+    groups = [(prefix, members)]
+    lens = prefix + np.arange(members) % 5
+    assert bool(pages_plan.tc_blocks(groups, lens, H, kv, hs)) == tc
+    pool, rows, args = grouped(dtype, groups, lens, kv, hs, 32, seed=case)
+    pool.k[..., 1:] = 0
+    q = torch.zeros((members, H, hs), device="cuda").to(DT[dtype])
+    q[..., 0] = (torch.rand((members, H), device="cuda") * 2 + 3).to(DT[dtype])
+    out = pool.attention(q, 0, scale=1.0, **args)
+    pool.check()
+    u, half, w2 = 2.0 ** -24, torch.finfo(DT[dtype]).eps / 2, 2.0 ** -16 if dtype == "bf16" else 2.0 ** -22
+    heads = torch.arange(H, device="cuda") * kv // H
+    worst = 0.0
+    for b in range(0, members, 3):
+        k, v = rows(b)
+        n = len(k)
+        x = k[:, heads, 0].T * q[b, :, 0].double()[:, None]
+        w = torch.softmax(x, 1)
+        want, mag = torch.einsum("ht,thd->hd", w, v[:, heads]), torch.einsum("ht,thd->hd", w, v[:, heads].abs())
+        e = 8 * u * float(x.abs().max())
+        rel = 2 * (e + 8 * u * float(x.abs().max())) + w2 + (n / 8 + 66) * 2 * u
+        tiny = n * 2.0 ** -38 * float(v.abs().max()) + 2.0 ** -25 if dtype == "fp16" else 1e-38
+        tol = rel * mag + half * (want.abs() + rel * mag) + tiny
+        worst = max(worst, float(((out[b].double() - want).abs() / tol).max()))
+    assert worst <= 1, worst
