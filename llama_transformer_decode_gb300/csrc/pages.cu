@@ -105,11 +105,11 @@ __device__ __forceinline__ void copy_words(const char *a, char *b, int t, int wo
     }
 }
 
-// Ends a refused call: nothing was changed, the row kernels that follow skip.
-__device__ __forceinline__ void refuse(const PagesView &p, int bit) {
+// Ends a refused call: nothing was changed, the row kernels that go by `flag` skip.
+__device__ __forceinline__ void refuse(const PagesView &p, int bit, int flag = kScrRefused) {
     if (threadIdx.x == 0) {
         atomicOr(p.err, bit);
-        p.scratch[kScrRefused] = 1;
+        p.scratch[flag] = 1;
     }
 }
 
@@ -148,13 +148,13 @@ __global__ void __launch_bounds__(kT) pages_extend_kernel(const PagesView p, int
             }
         }
     }
-    if (__syncthreads_or(bad)) return refuse(p, L2_PAGES_ERR_ARGS);
+    if (__syncthreads_or(bad)) return refuse(p, L2_PAGES_ERR_ARGS, kScrExtension);
     int need;
     const int base = block_scan(want - have, &need, buf);
     base_s[i] = base;
     if (i == 0) base_s[kT] = need;
     int *list = p.scratch + kScrHead;
-    if (need > p.n_pages || lowest_free(p, need, list, buf) < need) return refuse(p, L2_PAGES_ERR_FULL);
+    if (need > p.n_pages || lowest_free(p, need, list, buf) < need) return refuse(p, L2_PAGES_ERR_FULL, kScrExtension);
     // page e of the list belongs to the last sequence whose base is at most e and that takes pages
     for (int e = i; e < need; e += kT) {
         int lo = 0, hi = n;  // base_s[lo] <= e < base_s[hi]
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kT) pages_extend_kernel(const PagesView p, int
     }
     __syncthreads();  // the lengths above are read
     if (i < n) p.lens[s] = old + cnt;
-    if (i == 0) p.scratch[kScrRefused] = 0;
+    if (i == 0) p.scratch[kScrExtension] = 0;
 }
 
 // Append, second half: one warp per new row and layer range copies its heads' K and V.  A row's place
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256) pages_rows_kernel(const PagesView p, cons
     const int groups = ceil_div_d(a.n_layers, layers_per);
     if (warp >= a.rows * groups) return;
     const int r = warp / groups, lg = warp - r * groups;
-    if (!READ && p.scratch[kScrRefused]) return;
+    if (!READ && p.scratch[kScrExtension]) return;
     int i = r, start = r, end = r + 1;
     if (a.starts) {
         int lo = 0, hi = a.n;

@@ -88,3 +88,64 @@ def test_weights_of_16_bit_caches_are_not_rounded_to_16_bits(case, dtype):
         tol = rel * mag + half * (want.abs() + rel * mag) + tiny
         worst = max(worst, float(((out[b].double() - want).abs() / tol).max()))
     assert worst <= 1, worst
+
+
+# -- a step's layers, with other calls between them ---------------------------
+
+def small_pool(n_pages=6, layers=2):
+    """Sequences 0 (6 rows) and 2 (7 rows) in pages of 4; 0 shares nothing."""
+    pool = pkg.PagePool(layers, n_pages, 2, 4, 8, 6, 4)
+    x = torch.randn((2, layers, 13, 2, 8), device="cuda")
+    pool.append(x[0], x[1], dev([0, 2]), dev([0, 6, 13]))
+    pool.check()
+    return pool
+
+
+def refused(pool, match):
+    with pytest.raises(pkg.L2Error, match=match):
+        pool.check()
+
+
+@pytest.mark.parametrize("between", ["free", "fork", "free_compact"])
+def test_a_refused_extension_holds_for_the_other_layers_whatever_succeeds_between(between):
+    pool = small_pool()
+    x = torch.randn((2, 9, 2, 8), device="cuda")
+    pool.append(x[0], x[0], dev([0]), dev([0, 9]), layer=0)     # 15 rows: 2 more pages, both free
+    pool.check()
+    pool.append(x[1], x[1], dev([1]), dev([0, 9]), layer=0)     # no page is left
+    refused(pool, "free pages")
+    if between == "fork":
+        pool.fork(dev([0]), dev([3]), dev([4]))                 # a whole page: no new one
+    else:
+        pool.free(dev([2]), compact=between == "free_compact")
+    pool.check()
+    k, v, lens = pool.k.clone(), pool.v.clone(), pool.lens.clone()
+    pool.append(x[1], x[1], dev([1]), dev([0, 9]), layer=1)     # the refused step's other layer
+    pool.append(x[1, :1], x[1, :1], dev([0]), layer=1, extend=False)
+    torch.cuda.synchronize()
+    assert torch.equal(pool.k, k) and torch.equal(pool.v, v) and torch.equal(pool.lens, lens)
+    pool.status.zero_()
+    # and one that succeeds ends it
+    pool.free(dev([2]))
+    pool.append(x[1, :3], x[1, :3], dev([1]), dev([0, 3]), layer=0)
+    pool.append(x[0, :3], x[0, :3], dev([1]), dev([0, 3]), layer=1)
+    pool.check()
+    page = int(pool.table[1, 0])
+    assert torch.equal(pool.k[0, page, :, :3], x[1, :3].transpose(0, 1)) and torch.equal(pool.k[1, page, :, :3], x[0, :3].transpose(0, 1))
+
+
+def test_refused_calls_between_a_steps_layers_leave_its_rows():
+    pool = small_pool(n_pages=8)
+    x = torch.randn((2, 2, 2, 8), device="cuda")
+    seqs, starts = dev([0, 2]), None
+    pool.append(x[0], x[0], seqs, starts, layer=0)
+    pool.fork(dev([0]), dev([2]))                               # not empty
+    refused(pool, "index")
+    pool.free(dev([0, 9]))                                      # no such sequence
+    refused(pool, "index")
+    pool.append(x[1], x[1], seqs, starts, layer=1)
+    pool.check()
+    for i, (s, pos) in enumerate(((0, 6), (2, 7))):
+        page = int(pool.table[s, pos // 4])
+        for layer in range(2):
+            assert torch.equal(pool.k[layer, page, :, pos % 4], x[layer, i]) and torch.equal(pool.v[layer, page, :, pos % 4], x[layer, i])
