@@ -433,7 +433,9 @@ int l2_pages_fork(const L2Pages *pool, int n, const int *src, const int *dst, co
  * Frees the pages of n (0..1024) sequences and empties them (one named twice
  * is freed once).  With compact the pool is then closed up: with L pages
  * held, the k-th free page below L takes the rows of the k-th held page at or
- * above L in every layer, and the tables follow.
+ * above L in every layer, and the tables follow.  (Sequences it does not name
+ * are not checked beforehand: an entry of theirs that is outside the pool, or whose
+ * page nobody holds by its count, is reported and left as it is.)
  */
 int l2_pages_free(const L2Pages *pool, int n, const int *seqs, int compact, void *cuda_stream);
 

@@ -20,7 +20,7 @@ constexpr int kPagesThreads = 1024;  // threads of the one-block bookkeeping ker
 // Integers at the head of a pool's scratch: whether the last fork or free was refused (the kernel that copies its rows then does
 // nothing), the pages a compaction moves, and whether the last extension was refused, which holds for the step's other
 // layers too, whatever is called between them.  Then three lists of n_pages entries.
-enum : int { kScrRefused = 0, kScrMoved = 1, kScrLive = 2, kScrExtension = 3, kScrHead = 8 };
+enum : int { kScrRefused = 0, kScrMoved = 1, kScrExtension = 2, kScrHead = 8 };
 
 // A page pool.  Rows of head_size elements; strides in bytes.  Position p of sequence s is
 // row p % page_size of page table[s * max_pages + p / page_size].

@@ -114,6 +114,7 @@ __device__ __forceinline__ void refuse(const PagesView &p, int bit, int flag = k
 }
 
 __device__ __forceinline__ bool page_ok(const PagesView &p, int page) { return page >= 0 && page < p.n_pages; }
+__device__ __forceinline__ bool page_held(const PagesView &p, int page) { return page_ok(p, page) && p.refs[page] > 0; }
 
 }  // namespace
 
@@ -266,14 +267,14 @@ __global__ void __launch_bounds__(kT) pages_fork_kernel(const PagesView p, int n
     if (__syncthreads_or(bad)) return refuse(p, L2_PAGES_ERR_ARGS);
     const int full = m / p.page_size, tail = m % p.page_size;
     full_s[i] = full;
-    // every page that would be shared or copied must exist
+    // every page that would be shared or copied must exist and be held (one that is not might be handed out below)
     const int warp = i >> 5, lane = i & 31;
     __syncthreads();
     for (int e = warp; e < n; e += kT / 32) {
         const int *ts = p.table + (size_t)ss[e] * p.max_pages;
-        for (int j = lane; j < full_s[e]; j += 32) bad |= !page_ok(p, ts[j]);
+        for (int j = lane; j < full_s[e]; j += 32) bad |= !page_held(p, ts[j]);
     }
-    if (i < n && tail) bad |= !page_ok(p, p.table[(size_t)s * p.max_pages + full]);
+    if (i < n && tail) bad |= !page_held(p, p.table[(size_t)s * p.max_pages + full]);
     if (__syncthreads_or(bad)) return refuse(p, L2_PAGES_ERR_ARGS);
     int need;
     const int base = block_scan(i < n && tail ? 1 : 0, &need, buf);
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(256) pages_fork_copy_kernel(const PagesView p,
 // the k-th free page below n_live takes the k-th held page at or above it, so no page is both read
 // and written and the moves can run in any order.
 __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n, const int *seqs, int compact) {
-    __shared__ int buf[64], sq[kPagesMaxCall], len_s[kPagesMaxCall];
+    __shared__ int buf[64], sq[kPagesMaxCall], len_s[kPagesMaxCall], why;
     const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
     pdl_launch_dependents();
     pdl_wait();
@@ -341,19 +342,26 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
         bad = m < 0 || m > (long long)p.max_pages * p.page_size;
     }
     len_s[i] = bad ? 0 : ceil_div_d(m, p.page_size);
+    if (i == 0) why = 0;
     if (__syncthreads_or(bad)) return refuse(p, L2_PAGES_ERR_ARGS);
-    for (int e = warp; e < n; e += kT / 32) {
-        const int *t = p.table + (size_t)sq[e] * p.max_pages;
-        for (int j = lane; j < len_s[e]; j += 32) {
-            const int page = t[j];
-            // a page out of range, or with no holder left, is reported and left alone
-            if (!page_ok(p, page))
-                atomicOr(p.err, L2_DEV_ERR_BOUNDS);
-            else if (atomicSub(p.refs + page, 1) <= 0) {
-                atomicAdd(p.refs + page, 1);
-                atomicOr(p.err, L2_PAGES_ERR_ARGS);
-            }
+    auto held = [&](auto take) {  // every page of the sequences
+        for (int e = warp; e < n; e += kT / 32) {
+            const int *t = p.table + (size_t)sq[e] * p.max_pages;
+            for (int j = lane; j < len_s[e]; j += 32) take(t[j]);
         }
+    };
+    held([&](int page) {
+        if (!page_ok(p, page))
+            atomicOr(&why, L2_DEV_ERR_BOUNDS);
+        else if (atomicSub(p.refs + page, 1) <= 0)  // no holder left
+            atomicOr(&why, L2_PAGES_ERR_ARGS);
+    });
+    __syncthreads();
+    if (why) {  // nothing changes: what was taken is put back
+        held([&](int page) {
+            if (page_ok(p, page)) atomicAdd(p.refs + page, 1);
+        });
+        return refuse(p, why);
     }
     if (i < n) p.lens[s] = 0;
     if (i == 0) p.scratch[kScrRefused] = 0;
@@ -365,7 +373,8 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
     block_scan(live, &n_live, buf);
     int *hole = p.scratch + kScrHead, *mover = hole + p.n_pages, *to = mover + p.n_pages;
     int moved = 0;
-    // holes below n_live ascending, then held pages from n_live on ascending: as many of one as of the other
+    // holes below n_live ascending, then held pages from n_live on ascending: as many of one as of the other.  to: where each
+    // page's rows will be, -1 for pages that nobody holds
     for (int pass = 0; pass < 2; ++pass) {
         int found = 0;
         const int lo = pass ? n_live : 0, hi = pass ? p.n_pages : n_live;
@@ -382,7 +391,10 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
             int at = found + block_scan(c, &total, buf);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (f[j]) (pass ? mover : hole)[at++] = i0 + j;
+                if (i0 + j < hi) {
+                    to[i0 + j] = f[j] == (pass == 1) ? i0 + j : -1;
+                    if (f[j]) (pass ? mover : hole)[at++] = i0 + j;
+                }
             found += total;
         }
         moved = found;
@@ -394,10 +406,7 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
         p.refs[b] = __ldcg(p.refs + a);
         p.refs[a] = 0;
     }
-    if (i == 0) {
-        p.scratch[kScrMoved] = moved;
-        p.scratch[kScrLive] = n_live;
-    }
+    if (i == 0) p.scratch[kScrMoved] = moved;
 }
 
 // Compaction: the moved pages' rows in every layer, and the tables' entries.  A run is one page's
@@ -409,7 +418,7 @@ __global__ void __launch_bounds__(kCompactThreads, 4) pages_compact_kernel(const
     pdl_launch_dependents();
     pdl_wait();
     if (p.scratch[kScrRefused]) return;
-    const int moved = p.scratch[kScrMoved], n_live = p.scratch[kScrLive];
+    const int moved = p.scratch[kScrMoved];
     const int *hole = p.scratch + kScrHead, *mover = hole + p.n_pages, *to = mover + p.n_pages;
     if (!moved) return;
     const int tid = blockIdx.x * blockDim.x + threadIdx.x, nt = gridDim.x * blockDim.x;
@@ -417,11 +426,11 @@ __global__ void __launch_bounds__(kCompactThreads, 4) pages_compact_kernel(const
         const int s = (int)(e / p.max_pages), j = (int)(e - (long long)s * p.max_pages);
         const int m = p.lens[s];
         if (m <= 0 || j >= ceil_div_d(m, p.page_size)) continue;
-        const int page = p.table[e];
-        if (!page_ok(p, page))
-            atomicOr(p.err, L2_DEV_ERR_BOUNDS);
-        else if (page >= n_live)
-            p.table[e] = to[page];
+        const int page = p.table[e], now = page_ok(p, page) ? to[page] : -1;
+        if (now < 0)  // left as it is
+            atomicOr(p.err, page_ok(p, page) ? L2_PAGES_ERR_ARGS : L2_DEV_ERR_BOUNDS);
+        else if (now != page)
+            p.table[e] = now;
     }
     const int vr = row_bytes >> 4, words = rows * vr;
     const long long units = (long long)moved * 2 * p.n_layers * heads;

@@ -149,3 +149,62 @@ def test_refused_calls_between_a_steps_layers_leave_its_rows():
         page = int(pool.table[s, pos // 4])
         for layer in range(2):
             assert torch.equal(pool.k[layer, page, :, pos % 4], x[layer, i]) and torch.equal(pool.v[layer, page, :, pos % 4], x[layer, i])
+
+
+# -- bookkeeping that does not agree with itself -------------------------------
+
+def books(pool):
+    return [t.clone() for t in (pool.refs, pool.lens, pool.table, pool.k, pool.v)]
+
+
+def unchanged(pool, before):
+    return all(torch.equal(a, b) for a, b in zip(before, books(pool)))
+
+
+@pytest.mark.parametrize("compact", [False, True])
+@pytest.mark.parametrize("wrong", ["page outside", "page below", "count of one page", "count of a shared page"])
+def test_a_free_that_cannot_be_done_whole_changes_nothing(wrong, compact):
+    pool = small_pool(n_pages=12)
+    pool.fork(dev([0, 2]), dev([3, 4]))
+    pool.free(dev([2]))                     # a hole before the last pages
+    pool.check()
+    if wrong == "page outside":
+        pool.table[4, 1] = pool.n_pages
+    elif wrong == "page below":
+        pool.table[0, 0] = -3
+    elif wrong == "count of one page":
+        pool.refs[int(pool.table[4, 1])] = 0
+    else:
+        pool.refs[int(pool.table[0, 0])] = 1    # two sequences hold it
+    before = books(pool)
+    pool.free(dev([0, 3, 4, 3]), compact=compact)
+    refused(pool, "outside the pool" if wrong.startswith("page") else "inconsistent")
+    assert unchanged(pool, before)
+
+
+def test_a_fork_of_pages_that_nobody_holds_is_refused():
+    for col, rows in ((0, 6), (1, 6), (0, 4)):
+        pool = small_pool(n_pages=12)
+        pool.refs[int(pool.table[0, col])] = 0
+        before = books(pool)
+        pool.fork(dev([0, 2]), dev([3, 4]), dev([rows, 7]))
+        refused(pool, "inconsistent")
+        assert unchanged(pool, before)
+
+
+def test_a_compaction_reports_and_leaves_entries_of_pages_that_nobody_holds():
+    pool = small_pool(n_pages=12)
+    x = torch.randn((2, 2, 8, 2, 8), device="cuda")
+    pool.append(x[0], x[1], dev([1, 3]), dev([0, 4, 8]))     # pages 4 and 5
+    pool.append(x[0, :, :4], x[1, :, :4], dev([4]), dev([0, 4]))  # page 6
+    pool.free(dev([0]))                                      # pages 0 and 1 are holes; 2 .. 6 held
+    pool.check()
+    assert pool.table[[1, 3, 4], 0].tolist() == [4, 5, 6]
+    pool.refs[5] = 0                                         # sequence 3's page counts as free: 4 are held, 4 and 6 move
+    pool.table[2, 1] = 0                                     # and sequence 2 names a hole
+    pool._scratch[8:].fill_(7)                               # what earlier calls may have left
+    pool.free(compact=True)
+    refused(pool, "inconsistent")
+    assert pool.table[[1, 3, 4], 0].tolist() == [0, 5, 1] and pool.table[2, :2].tolist() == [2, 0]
+    assert pool.refs.tolist() == [1, 1, 1, 1] + [0] * 8
+    assert torch.equal(pool.k[:, 0], x[0, :, :4].transpose(1, 2)) and torch.equal(pool.v[:, 1], x[1, :, :4].transpose(1, 2))
