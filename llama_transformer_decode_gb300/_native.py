@@ -17,7 +17,7 @@ BUILD_CHECKED = os.path.join(BUILD, "checked")
 LIB_CHECKED = os.path.join(BUILD, "libl2decode_checked.so")
 SOURCES = ("gemv.cu", "gemv_batched.cu", "gemv_tc.cu", "attention.cu", "attn_prefill.cu", "step_kernel.cu", "step_cta.cu",
            "sample.cu", "pages.cu", "attn_pages.cu", "attn_pages_f32.cu", "attn_pages_16.cu", "pages_api.cu", "l2_api.cu")
-HEADERS = ("l2_device.cuh", "l2_params.h", "l2_kernels.h", "l2_pages.h", "l2_tc.cuh", "attn_pages.cuh", "attn_plan.cuh", "attn_pages_tc.cuh", "attn_pages_tc32.cuh", "attn_slots.h")
+HEADERS = ("l2_device.cuh", "l2_params.h", "l2_kernels.h", "l2_pages.h", "l2_tc.cuh", "attn_pages.cuh", "attn_plan.cuh", "attn_pages_tc.cuh", "attn_pages_tc32.cuh", "attn_slots.h", "attn_split.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3"]
 

@@ -3,6 +3,7 @@
 #pragma once
 #include "../../include/l2.h"
 #include "attn_pages.cuh"
+#include "attn_split.h"
 
 namespace l2 {
 
@@ -151,24 +152,13 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     }
     if (i == 0) {
         const int cost = all.x, tc = tc_all.x;
-        // blocks of the two roles by cost, at least one of each that has work
-        int n_tc = 0, per_tc = 1;
-        if (tc) {
-            // n or n + 1 blocks, whichever leaves the slower role less
-            const float t = (float)tc, w = (float)cost;
-            const int most = p.num_sms - (cost ? 1 : 0);
-            n_tc = max(1, min((int)((float)p.num_sms * (t / (t + w))), most));
-            auto slower = [&](int n) { return fmaxf(t / (float)n, cost ? w / (float)(p.num_sms - n) : 0.f); };
-            if (n_tc < most && slower(n_tc + 1) < slower(n_tc)) ++n_tc;
-            per_tc = max(tc_min_per(p.head_size, f32), cdiv(tc, n_tc));
-            n_tc = cdiv(tc, per_tc);
-        }
+        const RoleSplit r = split_roles(cost, tc, p.num_sms, kWalkWarps, max(kMinPer, sc.spread), tc_min_per(p.head_size, f32));
         pl.src[S].t0 = cost;
         pl.hdr[kHdrCost] = cost;
-        pl.hdr[kHdrPer] = max(max(kMinPer, sc.spread), cdiv(cost, (p.num_sms - n_tc) * kWalkWarps));
+        pl.hdr[kHdrPer] = r.per;
         pl.hdr[kHdrTcCost] = tc;
-        pl.hdr[kHdrTcPer] = per_tc;
-        pl.hdr[kHdrTcBlocks] = n_tc;
+        pl.hdr[kHdrTcPer] = r.per_tc;
+        pl.hdr[kHdrTcBlocks] = r.n_tc;
         if (p.G) pl.tc_t0[p.G] = tc;
         pl.hdr[kHdrOk] = 1;
     }

@@ -208,3 +208,17 @@ def test_a_compaction_reports_and_leaves_entries_of_pages_that_nobody_holds():
     assert pool.table[[1, 3, 4], 0].tolist() == [0, 5, 1] and pool.table[2, :2].tolist() == [2, 0]
     assert pool.refs.tolist() == [1, 1, 1, 1] + [0] * 8
     assert torch.equal(pool.k[:, 0], x[0, :, :4].transpose(1, 2)) and torch.equal(pool.v[:, 1], x[1, :, :4].transpose(1, 2))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("H,kv,hs,members,n", [(32, 8, 64, 32, 16384), (16, 16, 128, 40, 8192)])
+def test_keys_that_all_lie_in_whole_tensor_core_tiles(dtype, H, kv, hs, members, n):
+    """Attention right after a fork of a long prompt: no key is left for the walk."""
+    groups = [(n, members)]
+    lens = np.full(members, n)
+    pool, rows, args = grouped(dtype, groups, lens, kv, hs, 64, seed=n)
+    q = torch.randn((members, H, hs), device="cuda").to(DT[dtype])
+    lse = torch.empty((members, H), device="cuda")
+    out = pool.attention(q, 0, lse=lse, **args)
+    pool.check()
+    check_wide(out, lse, q, rows, dtype, 1 / math.sqrt(hs), [0, members // 2, members - 1])
