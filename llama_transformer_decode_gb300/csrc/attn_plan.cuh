@@ -21,7 +21,11 @@ struct PlanScratch {
     int minlen[MAX], mintc[MAX], gstart[MAX + 1], len[MAX], group[MAX], seq[MAX];
     int2 sums[2][32];
     int spread;
+    unsigned long long cost[2];
 };
+
+// Places are numbered in 32 bits; a walker's range ends at most as far beyond the last as it is long.
+constexpr long long kMostCost = 1ll << 30;
 
 // Exclusive prefix sums of both components over the block, and the totals; buf: one int2 a warp, not used by another scan.
 template <int NT>
@@ -66,7 +70,10 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         sc.len[i] = len;
         sc.seq[i] = seq;
     }
-    if (i == 0) sc.spread = 0;
+    if (i == 0) {
+        sc.spread = 0;
+        sc.cost[0] = sc.cost[1] = 0;
+    }
     if (p.G) {
 #pragma unroll 1
         for (int g = i; g <= p.G; g += NT) {
@@ -82,12 +89,14 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
             sc.minlen[i] = rows < 2 ? 0 : P;  // a row alone has nothing to share: all its keys are its own
         }
     }
-    if (__syncthreads_or(bad)) {
+    auto refused = [&]() {
+        if (!__syncthreads_or(bad)) return false;
         if (i < kHdrInts) pl.hdr[i] = i == kHdrPer || i == kHdrTcPer ? 1 : 0;
         if (i == 0 && report) atomicOr(p.err, L2_PAGES_ERR_ARGS);
         __syncthreads();
-        return;
-    }
+        return true;
+    };
+    if (refused()) return;
     int2 tc_all = make_int2(0, 0);
     if (p.G) {
         if (i < p.B) {
@@ -101,6 +110,24 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
             sc.group[i] = pl.group[i] = lo;
         }
         __syncthreads();
+    }
+    if (p.wide) {
+        // sequences as long as their tables would not do: what these cost, with every prefix in both roles
+        auto tiles = [&](int keys) { return (long long)((keys + (1 << p.tile_shift) - 1) >> p.tile_shift); };
+        long long walk = 0, tc = 0;
+        if (i < p.B) walk = cdiv(gq, kM) * (kItemCost + kMaxTileCost * tiles(len - (p.G ? sc.minlen[sc.group[i]] : 0)));
+        if (i < p.G) {
+            const int n = (sc.gstart[i + 1] - sc.gstart[i]) * gq;
+            walk += cdiv(n, kM) * (kItemCost + kMaxTileCost * tiles(sc.minlen[i]));
+            tc = tc_runs(n, f32) * (kTcItemCost + tc_cost(n, p.head_size, f32) * (long long)(sc.minlen[i] / tc_keys(f32)));
+        }
+        if (walk) atomicAdd(&sc.cost[0], (unsigned long long)walk * p.n_kv_heads);
+        if (tc) atomicAdd(&sc.cost[1], (unsigned long long)tc * p.n_kv_heads);
+        __syncthreads();
+        bad = max(sc.cost[0], sc.cost[1]) > (unsigned long long)kMostCost;
+        if (refused()) return;
+    }
+    if (p.G) {
         // prefixes worth it go to the tensor cores in whole tiles; what is left of them stays with the warps
         const int n = i < p.G ? (sc.gstart[i + 1] - sc.gstart[i]) * gq : 0;
         int full = i < p.G && p.tc ? sc.minlen[i] / tc_keys(f32) : 0;

@@ -93,6 +93,7 @@ struct PagesAttn {
     int tile_shift;           // log2 of the keys of a warp's tile
     bool tc;                  // prefixes may go to the tensor cores
     bool plan_in_block;       // every block plans for itself (no plan kernel before)
+    bool wide;                // sequences as long as their tables would overflow the plan's 32 bits
     float *tc_ml, *tc_acc;    // its parts, by row
 };
 

@@ -150,10 +150,6 @@ int check_attn_shape(const char *who, const L2Pages *p, int B, int G, int n_head
     if (G < 0 || G > B) return refuse(L2_EINVAL, "%s: G = %d outside 0..B", who, G);
     if (n_heads < p->n_kv_heads || n_heads > 1024)
         return refuse(L2_EINVAL, "%s: n_heads = %d outside n_kv_heads..1024", who, n_heads);
-    // tiles are numbered in 32 bits
-    const long long gq = (n_heads + p->n_kv_heads - 1) / p->n_kv_heads, items = 2ll * B * ((gq + 15) / 16 + 1) * p->n_kv_heads;
-    if (items * ((((long long)p->max_pages * p->page_size + 7) / 8) * 7 + 64) > 0x7fffffffll)
-        return refuse(L2_EINVAL, "%s: B, heads and max_pages * page_size are too large together", who);
     return L2_OK;
 }
 
@@ -321,6 +317,9 @@ int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws,
     k.page_shift = -1;
     for (int i = 0; i < 31; ++i)
         if (v.page_size == 1 << i) k.page_shift = i;
+    // a bound of the plan's costs: own keys and prefixes, as long as the tables, in tiles of 8 keys that cost 7
+    const long long gq = (k.n_heads + k.n_kv_heads - 1) / k.n_kv_heads, items = 2ll * k.B * ((gq + 15) / 16 + 1) * k.n_kv_heads;
+    k.wide = items * ((((long long)v.max_pages * v.page_size + 7) / 8) * 7 + 128) > 1ll << 30;
     k.scale_log2 = (float)(a->scale * 1.4426950408889634);
     return finish(who, launch_pages_attn(k, ws, sms, static_cast<cudaStream_t>(cuda_stream)));
 }

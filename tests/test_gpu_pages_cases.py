@@ -222,3 +222,40 @@ def test_keys_that_all_lie_in_whole_tensor_core_tiles(dtype, H, kv, hs, members,
     out = pool.attention(q, 0, lse=lse, **args)
     pool.check()
     check_wide(out, lse, q, rows, dtype, 1 / math.sqrt(hs), [0, members // 2, members - 1])
+
+
+# -- pools with room for long sequences ----------------------------------------
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("B,shared", [(200, False), (160, True), (1024, False), (1024, True)])
+def test_many_rows_of_a_pool_with_room_for_long_sequences(dtype, B, shared):
+    """What a call may do hangs on what its sequences hold, not on what their tables could hold."""
+    H = kv = 32
+    ps, max_pages = 128, 1024
+    rng = np.random.default_rng(B)
+    prefix = 128 * 9 if shared else 0
+    lens = prefix + rng.integers(0, 200, B)
+    groups = [(prefix, B // 4), (prefix, B - B // 4)] if shared else [(0, 1)] * B
+    small, rows, args = grouped(dtype, groups, lens, kv, 8, ps, seed=B)
+    table = torch.zeros((B, max_pages), dtype=torch.int32, device="cuda")
+    table[:, :small.max_pages] = small.table
+    pool = pkg.PagePool.from_tensors(small.k, small.v, small.refs, small.lens, table)
+    q = torch.randn((B, H, 8), device="cuda").to(DT[dtype])
+    lse = torch.empty((B, H), device="cuda")
+    out = pool.attention(q, 0, lse=lse, **(args if shared else {}))
+    pool.check()
+    check_wide(out, lse, q, rows, dtype, 1 / math.sqrt(8), sorted({0, B // 4, B - 1, *rng.integers(0, B, 10).tolist()}))
+    assert torch.equal(out, small.attention(q, 0, **(args if shared else {})))
+    # sequences that hold too much together: refused, the output as it was
+    kept = out.clone()
+    pool.lens.fill_(ps * max_pages)
+    if B == 1024 and not shared:
+        wide = pkg.PagePool.from_tensors(small.k, small.v, small.refs, pool.lens, torch.zeros((B, 8 * max_pages), dtype=torch.int32, device="cuda"))
+        pool.lens.fill_(8 * ps * max_pages)
+        wide.attention(q, 0, out=out)
+        with pytest.raises(pkg.L2Error, match="index"):
+            wide.check()
+        wide.attention(q, 0, out=out, group_starts=dev([0, 1024]), prefix_lens=dev([7]))
+        with pytest.raises(pkg.L2Error, match="index"):
+            wide.check()
+        assert torch.equal(out, kept)
