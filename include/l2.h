@@ -339,7 +339,7 @@ int l2_sample(const float *logits, int B, int vocab_size, float temperature, flo
  * A pool keeps K (after RoPE) and V rows of head_size elements at
  *   k + layer * layer_stride + page * page_stride + kv_head * head_stride + row * row_stride
  * (v alike; strides in elements, multiples of 16 bytes, last dimension
- * contiguous).  Position p of sequence s is row p % page_size of page
+ * contiguous, each at least what the smaller ones span: no two rows share memory).  Position p of sequence s is row p % page_size of page
  * table[s][p / page_size].  refs[page] counts the sequences that hold a page;
  * 0 is free.  Full pages may be shared; a partly filled last page belongs to
  * one sequence.  All arrays are DEVICE memory of the caller, 16-byte aligned

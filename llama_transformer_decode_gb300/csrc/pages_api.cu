@@ -55,6 +55,24 @@ int check_ptr(const char *who, const char *name, const void *p, unsigned align, 
     return L2_OK;
 }
 
+// Whether rows of `width` elements at every combination of the strides have memory of their own: each stride, in ascending
+// order, is at least what the smaller ones span.
+bool rows_apart(const long long *strides, const int *counts, int dims, long long width) {
+    constexpr long long kFar = 1ll << 62;
+    long long span = width;
+    unsigned done = 0;
+    for (int k = 0; k < dims; ++k) {
+        int at = -1;  // the next stride; dimensions of one index are never stepped
+        for (int i = 0; i < dims; ++i)
+            if (counts[i] > 1 && !(done >> i & 1) && (at < 0 || strides[i] < strides[at])) at = i;
+        if (at < 0) return true;
+        done |= 1u << at;
+        if (strides[at] < span) return false;
+        span = strides[at] > kFar / counts[at] ? kFar : span + strides[at] * (counts[at] - 1);
+    }
+    return true;
+}
+
 constexpr unsigned kReady = 0x50a6e500u;  // with the pool's device below
 
 // Everything about a pool that the host can see.
@@ -81,6 +99,7 @@ int check_pool(const char *who, const L2Pages *p, int *device) {
             return refuse(L2_EINVAL, "%s: %s %lld must be at least head_size and a multiple of 16 bytes", who, names[i], st[i]);
         if (st[i] > (1ll << 40)) return refuse(L2_EINVAL, "%s: %s %lld too large", who, names[i], st[i]);
     }
+    if (!rows_apart(st, n, 4, p->head_size)) return refuse(L2_EINVAL, "%s: the strides give two rows the same memory", who);
     const void *const ptrs[7] = {p->k, p->v, p->refs, p->lens, p->table, p->status, p->scratch};
     static const char *const ptr_names[7] = {"k", "v", "refs", "lens", "table", "status", "scratch"};
     for (int i = 0; i < 7; ++i)
@@ -173,9 +192,9 @@ int move_rows(const char *who, const L2Pages *pool, const L2PagesRows *a, bool r
         (rc = check_stride(who, "head_stride", a->head_stride, pool->n_kv_heads, es)))
         return rc;
     if (read && a->extend) return refuse(L2_EINVAL, "%s: reading does not extend", who);
-    if (read && ((w.n_layers > 1 && a->layer_stride < pool->head_size) || (a->rows > 1 && a->row_stride < pool->head_size) ||
-                 (pool->n_kv_heads > 1 && a->head_stride < pool->head_size)))
-        return refuse(L2_EINVAL, "%s: the rows overlap", who);
+    const long long st[3] = {a->layer_stride, a->row_stride, a->head_stride};
+    const int counts[3] = {w.n_layers, a->rows, pool->n_kv_heads};
+    if (read && !rows_apart(st, counts, 3, pool->head_size)) return refuse(L2_EINVAL, "%s: the rows overlap", who);
     if ((rc = check_ptr(who, "seqs", a->seqs, 4, &device)) || (a->starts && (rc = check_ptr(who, "starts", a->starts, 4, &device))) ||
         (a->rows && ((rc = check_ptr(who, "k", a->k, 16, &device)) || (rc = check_ptr(who, "v", a->v, 16, &device)))))
         return rc;
@@ -268,11 +287,9 @@ int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws,
         (rc = check_stride(who, "out_row_stride", a->out_row_stride, a->B, es)) ||
         (rc = check_stride(who, "out_head_stride", a->out_head_stride, a->n_heads, es)))
         return rc;
-    // every row of the output has memory of its own: heads within rows, or rows within heads
-    const long long hs = pool->head_size, heads = (a->n_heads - 1) * a->out_head_stride + hs, rows = (a->B - 1) * a->out_row_stride + hs;
-    if ((a->n_heads > 1 && a->out_head_stride < hs) || (a->B > 1 && a->out_row_stride < hs) ||
-        (a->n_heads > 1 && a->B > 1 && heads > a->out_row_stride && rows > a->out_head_stride))
-        return refuse(L2_EINVAL, "%s: output rows overlap", who);
+    const long long out_st[2] = {a->out_row_stride, a->out_head_stride};
+    const int out_n[2] = {a->B, a->n_heads};
+    if (!rows_apart(out_st, out_n, 2, pool->head_size)) return refuse(L2_EINVAL, "%s: output rows overlap", who);
     if ((rc = check_ptr(who, "q", a->q, 16, &device)) || (rc = check_ptr(who, "out", a->out, 16, &device)) ||
         (a->lse && (rc = check_ptr(who, "lse", a->lse, 4, &device))) || (a->seqs && (rc = check_ptr(who, "seqs", a->seqs, 4, &device))) ||
         (a->G && ((rc = check_ptr(who, "group_starts", a->group_starts, 4, &device)) ||

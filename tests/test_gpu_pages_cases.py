@@ -259,3 +259,21 @@ def test_many_rows_of_a_pool_with_room_for_long_sequences(dtype, B, shared):
         with pytest.raises(pkg.L2Error, match="index"):
             wide.check()
         assert torch.equal(out, kept)
+
+
+def test_rows_read_into_shared_memory_are_refused():
+    pool = small_pool()
+    flat = torch.zeros(4096, device="cuda")
+    for strides in ((8, 8, 1), (16, 0, 1), (24, 32, 1)):   # rows over heads, heads over one another, half over one another
+        t = flat.as_strided((5, 2, 8), strides)
+        with pytest.raises(pkg.L2Error, match="overlap"):
+            pool.read(t, t, dev([0]), dev([0, 5]), layer=0)
+    with pytest.raises(pkg.L2Error, match="same memory"):
+        k = flat.as_strided((1, 4, 2, 4, 8), (0, 64, 8, 8, 1))
+        pkg.PagePool.from_tensors(k, k, dev(np.zeros(4)), dev(np.zeros(2)), dev(np.zeros((2, 4))))
+    for strides in ((16, 8, 1), (8, 40, 1), (24, 8, 1)):
+        k, v = (torch.zeros(4096, device="cuda").as_strided((5, 2, 8), strides) for _ in range(2))
+        pool.read(k, v, dev([0]), dev([0, 5]), layer=1)
+        page = pool.table[0, :2].long()
+        assert torch.equal(k, pool.k[1, page].transpose(1, 2).reshape(8, 2, 8)[:5]) and torch.equal(v, pool.v[1, page].transpose(1, 2).reshape(8, 2, 8)[:5])
+    pool.check()
