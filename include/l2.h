@@ -408,7 +408,9 @@ typedef struct {
  * the call; the rows are then written as the sequences' last ones.  A step
  * extends with its first layer (or all layers at once) and writes its other
  * layers with extend 0 and the same seqs and starts.  If the last extension
- * was refused, rows are not written until one succeeds.
+ * was refused, rows are not written until one succeeds.  Rows of an extend 0 call
+ * that would go into a page other sequences hold are left out and reported
+ * (L2_PAGES_BAD_CALL).
  */
 int l2_pages_append(const L2Pages *pool, const L2PagesRows *rows, void *cuda_stream);
 

@@ -37,6 +37,7 @@ struct PagesAppend {
     long long layer_stride, row_stride, head_stride;    // bytes
     const int *seqs, *starts;                           // [n], [n + 1] or nullptr (one row each)
     int n, rows, layer0, n_layers;
+    bool extended;                                      // the call has just lengthened the sequences: their last pages are theirs
 };
 
 cudaError_t launch_pages_extend(const PagesView &p, int n, const int *seqs, const int *starts, int rows, cudaStream_t s);

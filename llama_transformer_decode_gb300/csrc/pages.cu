@@ -211,6 +211,10 @@ __global__ void __launch_bounds__(256) pages_rows_kernel(const PagesView p, cons
         if (lane == 0) atomicOr(p.err, L2_DEV_ERR_BOUNDS);
         return;
     }
+    if (!READ && !a.extended && p.refs[page] != 1) {  // other sequences would see the row
+        if (lane == 0) atomicOr(p.err, L2_PAGES_ERR_ARGS);
+        return;
+    }
     const long long at = page * p.page_stride + (pos % p.page_size) * p.row_stride;
     const int vh = p.row_bytes >> 4, nv = vh * p.n_kv_heads;  // 16-byte words a head, a row
     const int l0 = lg * layers_per, l1 = min(a.n_layers, l0 + layers_per);

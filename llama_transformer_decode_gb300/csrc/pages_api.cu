@@ -212,6 +212,7 @@ int move_rows(const char *who, const L2Pages *pool, const L2PagesRows *a, bool r
     w.starts = a->starts;
     w.n = a->n;
     w.rows = a->rows;
+    w.extended = a->extend != 0;
     if (a->extend) {
         cudaError_t e = launch_pages_extend(v, a->n, a->seqs, a->starts, a->rows, s);
         if (e != cudaSuccess) return finish(who, e);

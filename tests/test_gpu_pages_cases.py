@@ -277,3 +277,26 @@ def test_rows_read_into_shared_memory_are_refused():
         page = pool.table[0, :2].long()
         assert torch.equal(k, pool.k[1, page].transpose(1, 2).reshape(8, 2, 8)[:5]) and torch.equal(v, pool.v[1, page].transpose(1, 2).reshape(8, 2, 8)[:5])
     pool.check()
+
+
+@pytest.mark.parametrize("starts", [None, [0, 3, 4]])
+def test_rows_without_an_extension_do_not_go_into_pages_that_others_hold(starts):
+    pool = pkg.PagePool(2, 12, 2, 4, 8, 6, 4)
+    x = torch.randn((2, 13, 2, 8), device="cuda")
+    pool.append(x, x, dev([0, 2]), dev([0, 8, 13]))      # two full pages; a full one and a row
+    pool.fork(dev([0]), dev([1]))                        # shares both
+    pool.check()
+    k, v = pool.k.clone(), pool.v.clone()
+    n = 2 if starts is None else starts[-1]
+    y = torch.randn((n, 2, 8), device="cuda")
+    pool.append(y, y, dev([1, 2]), None if starts is None else dev(starts), layer=1, extend=False)
+    refused(pool, "index")
+    page = int(pool.table[2, 1])
+    k[1, page, :, 0], v[1, page, :, 0] = y[-1], y[-1]    # sequence 2's own page takes its row
+    assert torch.equal(pool.k, k) and torch.equal(pool.v, v)
+    pool.free(dev([0]))                                  # now they are sequence 1's alone
+    pool.append(y, y, dev([1, 2]), None if starts is None else dev(starts), layer=1, extend=False)
+    pool.check()
+    at = n - 1
+    page = int(pool.table[1, 1])
+    assert torch.equal(pool.k[1, page, :, 4 - at:], y[:at].transpose(0, 1))
