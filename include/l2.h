@@ -456,7 +456,8 @@ int l2_pages_free(const L2Pages *pool, int n, const int *seqs, int compact, void
  * enters its product as the sum of two values of the type, within 2^-16 of it in
  * bf16, 2^-22 in fp16).  NaN and infinite
  * scores count as in the formula (-inf: weight 0); an infinity in a cached row
- * of V makes the outputs it reaches infinite or NaN.  Rows no sequence holds may
+ * of V makes the outputs it reaches infinite or NaN, and so do finite values whose
+ * sums over keys of weight up to 1 pass fp32's largest.  Rows no sequence holds may
  * hold anything.  A call whose rows hold so many keys that its work cannot be
  * numbered in 32 bits (150 million tiles of 8 to 32 keys by 16 query heads of a KV
  * head) is refused by the kernels (L2_PAGES_BAD_CALL).

@@ -225,6 +225,14 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) 
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
 }
+// The same for a value that stays in the output: hi is at most tf32's largest, so that a finite x does not round to infinity (but for the
+// two largest floats, whose halves add up to 2^128).  An infinite or NaN x is one in lo.
+__device__ __forceinline__ void split_tf32_finite(float x, uint32_t &hi, uint32_t &lo) {
+    float y;
+    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(__uint_as_float(0x7f7fe000u)));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(y));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
 // Columns 2 t4 + e of n8 tile 4 i + j of the sums are dimensions 32 i + 4 w(2 t4 + e) + j: the word of V a lane reads, chosen
 // so that a phase's eight reads fall into different banks.
 __device__ __forceinline__ int v_word(int g) { return ((g & 1) << 2) | (g >> 1); }
@@ -347,8 +355,8 @@ __device__ __forceinline__ void tile_mma(StateF<HS> &st, float *m2, float *l2, c
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t h0, l0, h1, l1;
-                split_tf32(a0[j], h0, l0);
-                split_tf32(a1[j], h1, l1);
+                split_tf32_finite(a0[j], h0, l0);
+                split_tf32_finite(a1[j], h1, l1);
                 mma_tf32_to(acc[j], plo[n], h0, h1, n > 0);
                 mma_tf32_to(acc[j], ph[n], l0, l1, true);
                 mma_tf32_to(acc[j], ph[n], h0, h1, true);

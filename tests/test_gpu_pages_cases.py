@@ -300,3 +300,29 @@ def test_rows_without_an_extension_do_not_go_into_pages_that_others_hold(starts)
     at = n - 1
     page = int(pool.table[1, 1])
     assert torch.equal(pool.k[1, page, :, 4 - at:], y[:at].transpose(0, 1))
+
+
+@pytest.mark.parametrize("H,members,prefix", [(1, 1, 0), (8, 1, 0), (12, 1, 0), (16, 1, 0), (1, 11, 60), (4, 40, 4096)])
+@pytest.mark.parametrize("hs", [32, 64, 128])
+def test_a_large_value_of_v_does_not_round_to_infinity(H, members, prefix, hs):
+    """fp32: one key has all the weight (the others' is below 2^-150, so 0) and a V up to 2^-20 below the largest float; the
+    other keys' V is of normal size, so that the sums, which are fp32, stay finite however many weights of 1 a part begins with.
+    The tensor-core role takes weights as 2^fma(score, c, -m) with m = round(score c), so the largest is not 1 but up to
+    2^(half a step of m) <= 1 + 2^-17 for m below 256: V has to be that much smaller for its product to be finite, 2^-16 here."""
+    groups = [(prefix, members)]
+    pool, rows, args = grouped("fp32", groups, np.full(members, prefix + 50), 1, hs, 16, seed=hs)
+    top = float(np.finfo(np.float32).max) * (1 - 2.0 ** (-16 if prefix >= 4096 else -20))
+    pool.k.zero_()
+    at = prefix // 2 if prefix else 17
+    for b in range(members):
+        pool.k[0, int(pool.table[b, at // 16]), 0, at % 16, 0] = 1.0
+    v = (torch.rand(hs, device="cuda") * 2 - 1) * top
+    v[::2], v[1::4] = top, -top
+    pool.v[0, int(pool.table[0, at // 16]), 0, at % 16] = v
+    q = torch.zeros((members, H, hs), device="cuda")
+    q[..., 0] = 120.0
+    out = pool.attention(q, 0, scale=1.0, **(args if members > 1 else {}))
+    pool.check()
+    want = rows(0)[1][at, 0]
+    # weight and sum of weights are one number: what is left are the halves, 2^-22 of the value, and a rounding or two
+    assert float(((out[0].double() - want) / want).abs().max()) <= 2.0 ** -21
