@@ -37,13 +37,13 @@
 
 namespace l2 {
 
-// The plan as a kernel of its own, for calls of more sources than a block plans for itself.
+// The plan as a kernel of its own, for calls of more sources than a block plans for itself and for wide ones.
 __global__ void __launch_bounds__(kPagesMaxCall) attn_pages_plan_kernel(const PagesAttn p) {
     __shared__ PlanScratch<kPagesMaxCall, kPagesMaxCall> sc;
     pdl_launch_dependents();
     pdl_wait();
     const Plan pl = plan_of(p.plan, p.B, p.G);
-    plan_build<kPagesMaxCall, kPagesMaxCall>(p, pl, sc, true);
+    plan_build<kPagesMaxCall, kPagesMaxCall, true>(p, pl, sc, true);
     plan_rows<kPagesMaxCall>(p, pl, pl.row);
 }
 
@@ -295,7 +295,7 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     p.tile_shift = f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size);
     // whether any prefix of such a call could be one for the tensor cores; the plan decides for each
     p.tc = p.G && tc_worth(p, p.B * heads_per_kv(p.n_heads, p.n_kv_heads), p.max_pages * p.page_size) && (f32 || attn_pages_tc_supported(p));
-    p.plan_in_block = p.B + p.G <= kPlanInBlock;
+    p.plan_in_block = p.B + p.G <= kPlanInBlock && !p.wide;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -52,8 +52,9 @@ __device__ __forceinline__ int2 plan_scan(int2 v, int2 *total, int2 *buf) {
     return make_int2((warp ? bx : 0) + x.x - v.x, (warp ? by : 0) + x.y - v.y);
 }
 
-// MAX: most groups or rows (MAX <= NT).  Ends with a barrier.  report: sets the status word when the call is bad.
-template <int NT, int MAX>
+// MAX: most groups or rows (MAX <= NT).  Ends with a barrier.  report: sets the status word when the call is bad.  WIDE: calls with p.wide
+// are among those planned; they have a plan kernel (in the attention kernels the sum would cost every call: 155.7 us against 154.4).
+template <int NT, int MAX, bool WIDE = false>
 __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, PlanScratch<NT, MAX> &sc, bool report) {
     const int i = threadIdx.x, S = p.G + p.B, gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const bool f32 = p.dtype == L2_F32;
@@ -111,7 +112,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         }
         __syncthreads();
     }
-    if (p.wide) {
+    if (WIDE && p.wide) {
         // sequences as long as their tables would not do: what these cost, with every prefix in both roles
         auto tiles = [&](int keys) { return (long long)((keys + (1 << p.tile_shift) - 1) >> p.tile_shift); };
         long long walk = 0, tc = 0;
