@@ -45,6 +45,7 @@ struct Tc32Shape {
 struct Tc32Fx {
     uint64_t full_k[2], empty_k[2], full_v[2], empty_v[2];
     uint64_t raw_full[6], raw_empty[6], s_full[2], q_full, p_full, pv_done, l_full, fin;
+    uint64_t seen[4];    // the two warps of a lane quarter have read the scores that they are about to write
     uint32_t tmem;
     int abort;
     unsigned bad[6][2];  // rows of a tile whose page is out of range
@@ -119,6 +120,7 @@ __device__ __forceinline__ void tc32_role(const PagesAttn &p, const Plan &pl, un
         mbar_init(&fx.pv_done, 1);
         mbar_init(&fx.l_full, kSlotThreads);
         mbar_init(&fx.fin, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&fx.seen[i], 2);
         fence_barrier_init();
         fx.abort = 0;
     }
@@ -331,7 +333,7 @@ __device__ __forceinline__ void tc32_role(const PagesAttn &p, const Plan &pl, un
         constexpr int HD = HS / 2;  // dimensions of the sums a warpgroup keeps
         // the queries carry the scale's sign, so the largest score is the largest product
         const float scale = fabsf(p.scale_log2), sign = p.scale_log2 < 0.f ? -1.f : 1.f;
-        int done = 0, ended = 0, nseg = 0;
+        int done = 0, ended = 0, nseg = 0, odd = 0;
         for (; ok && segment(g); ++nseg) {
             const int row0 = pl.src[g.group].row0, head0 = first_head(g.kvh, p.n_heads, p.n_kv_heads);
             const int nh = first_head(g.kvh + 1, p.n_heads, p.n_kv_heads) - head0;
@@ -391,7 +393,13 @@ __device__ __forceinline__ void tc32_role(const PagesAttn &p, const Plan &pl, un
                     }
                     mx = max_nan(max_nan(m4[0], m4[1]), max_nan(m4[2], m4[3]));
                     // the parts of an infinity make NaN of a score that may be infinite: such tiles are summed again as they are
+                    // (by both warps of the lanes, which read the same scores, so both come here; each then writes its own keys')
                     if (__any_sync(0xffffffffu, mx != mx && real)) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&fx.seen[warp & 3]);
+                        if (!await(&fx.seen[warp & 3], odd++)) break;
+                        tc_fence_after();
                         mx = -CUDART_INF_F;
                         const int *table = p.table + (size_t)pl.src[g.group].seq * p.max_pages;
 #pragma unroll 1
@@ -407,7 +415,7 @@ __device__ __forceinline__ void tc32_role(const PagesAttn &p, const Plan &pl, un
                                     d = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, d))));
                                 }
                             d *= sign;
-                            tmem_st1(sc + j, __float_as_uint(d));
+                            if (j / (Sh::KT / 2) == w) tmem_st1(sc + j, __float_as_uint(d));
                             mx = fmaxf(mx, d);
                         }
                         tmem_wait_st();

@@ -326,3 +326,29 @@ def test_a_large_value_of_v_does_not_round_to_infinity(H, members, prefix, hs):
     want = rows(0)[1][at, 0]
     # weight and sum of weights are one number: what is left are the halves, 2^-22 of the value, and a rounding or two
     assert float(((out[0].double() - want) / want).abs().max()) <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("hs", [64, 128])
+def test_infinite_keys_give_the_same_bits_every_time(hs):
+    """fp32 prefixes on the tensor cores: tiles with infinities are summed again, by two warps over the same scores."""
+    members, n, H = 40, 6400, 8
+    pool, rows, args = grouped("fp32", [(n, members)], np.full(members, n) + np.arange(members) % 3, 2, hs, 64, seed=hs)
+    q = torch.randn((members, H, hs), device="cuda")
+    q[..., 3] = q[..., 3].abs() + 0.5
+    gone = torch.zeros(n + 64, dtype=torch.bool, device="cuda")
+    for j in range(0, n // 64, 2):
+        page = int(pool.table[0, j])
+        pool.k[0, page, :, (j * 7) % 64, 3] = -math.inf
+        gone[64 * j + (j * 7) % 64] = True
+    lse = torch.empty((members, H), device="cuda")
+    out = pool.attention(q, 0, lse=lse, **args)
+    pool.check()
+
+    def visible(b):
+        k, v = rows(b)
+        return k[~gone[:len(k)]], v[~gone[:len(k)]]
+    check_wide(out, lse, q, visible, "fp32", 1 / math.sqrt(hs), [0, 1, members - 1])
+    again = torch.empty_like(lse)
+    for _ in range(30):
+        assert torch.equal(pool.attention(q, 0, lse=again, **args), out) and torch.equal(again, lse)
+    pool.check()
