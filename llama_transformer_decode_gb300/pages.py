@@ -141,6 +141,8 @@ class PagePool:
         vp, v_shape, v_st = self._rows("v", v, 4 if whole else 3)
         if shape != v_shape or st != v_st or shape[-2] != self.n_kv_heads or (whole and shape[0] != self.n_layers):
             raise ValueError("k and v must be alike, with the pool's layers and heads")
+        if not whole and not 0 <= layer < self.n_layers:  # the library's -1 means every layer, whose rows have a leading dimension
+            raise ValueError(f"layer {layer} outside 0..{self.n_layers - 1}")
         n = len(seqs)
         return L2PagesRows(n, shape[-3], self._ints("seqs", seqs), None if starts is None else self._ints("starts", starts, n + 1),
                            -1 if whole else int(layer), int(extend), kp, vp, st[0] if whole else 0, st[-3], st[-2])

@@ -352,3 +352,16 @@ def test_infinite_keys_give_the_same_bits_every_time(hs):
     for _ in range(30):
         assert torch.equal(pool.attention(q, 0, lse=again, **args), out) and torch.equal(again, lse)
     pool.check()
+
+
+def test_one_layers_rows_do_not_go_to_every_layer():
+    pool = small_pool()
+    x = torch.randn((2, 2, 8), device="cuda")
+    before = books(pool)
+    for layer in (-1, -2, 2):
+        for call in (lambda: pool.append(x, x, dev([0, 2]), layer=layer), lambda: pool.append(x, x, dev([0, 2]), layer=layer, extend=True),  # noqa: B023
+                     lambda: pool.read(x, x, dev([0, 2]), layer=layer)):  # noqa: B023
+            with pytest.raises((ValueError, pkg.L2Error)):
+                call()
+    pool.check()
+    assert unchanged(pool, before)
