@@ -474,7 +474,7 @@ typedef struct {
     const int *group_starts; /* DEVICE [G + 1] */
     const int *prefix_lens;  /* DEVICE [G] */
     long long q_row_stride, q_head_stride, out_row_stride, out_head_stride;
-    double scale;            /* usually 1 / sqrt(head_size) */
+    double scale;            /* usually 1 / sqrt(head_size); scale * log2(e) finite in fp32 */
 } L2PagesAttention;
 
 /* Bytes of workspace an attention call of these sizes needs, or a negative status. */

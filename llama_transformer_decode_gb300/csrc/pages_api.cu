@@ -280,7 +280,8 @@ int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws,
     if ((rc = check_attn_shape(who, pool, a->B, a->G, a->n_heads))) return rc;
     if (a->layer < 0 || a->layer >= pool->n_layers)
         return refuse(L2_EINVAL, "%s: layer %d outside 0..%d", who, a->layer, pool->n_layers - 1);
-    if (!std::isfinite(a->scale)) return refuse(L2_EINVAL, "%s: scale must be finite", who);
+    const float scale_log2 = (float)(a->scale * 1.4426950408889634);  // scores are fp32
+    if (!std::isfinite(a->scale) || !std::isfinite(scale_log2)) return refuse(L2_EINVAL, "%s: scale must be finite, in fp32 too", who);
     if (!a->seqs && a->B > pool->n_seqs) return refuse(L2_EINVAL, "%s: B = %d exceeds the pool's %d sequences", who, a->B, pool->n_seqs);
     const int es = elt_size(pool->dtype);
     if ((rc = check_stride(who, "q_row_stride", a->q_row_stride, a->B, es)) ||
@@ -338,6 +339,6 @@ int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws,
     // a bound of the plan's costs: own keys and prefixes, as long as the tables, in tiles of 8 keys that cost 7
     const long long gq = (k.n_heads + k.n_kv_heads - 1) / k.n_kv_heads, items = 2ll * k.B * ((gq + 15) / 16 + 1) * k.n_kv_heads;
     k.wide = items * ((((long long)v.max_pages * v.page_size + 7) / 8) * 7 + 128) > 1ll << 30;
-    k.scale_log2 = (float)(a->scale * 1.4426950408889634);
+    k.scale_log2 = scale_log2;
     return finish(who, launch_pages_attn(k, ws, sms, static_cast<cudaStream_t>(cuda_stream)));
 }

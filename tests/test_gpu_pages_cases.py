@@ -365,3 +365,18 @@ def test_one_layers_rows_do_not_go_to_every_layer():
                 call()
     pool.check()
     assert unchanged(pool, before)
+
+
+def test_scales_that_fp32_does_not_hold_are_refused():
+    pool = small_pool()
+    q = torch.zeros((1, 2, 8), device="cuda")
+    for scale in (2.4e38, -3e38, 1e39, -1e300):     # times log2(e): above 3.4e38
+        with pytest.raises(pkg.L2Error, match="finite"):
+            pool.attention(q, 0, scale=scale)
+    for scale in (2.3e38, -2.3e38, 1e-300, 0.0):    # all scores 0: the mean of the rows
+        out = pool.attention(q, 0, scale=scale)
+        pool.check()
+        page = pool.table[0, :2].long()
+        want = pool.v[0, page].double().transpose(1, 2).reshape(8, 2, 8)[:6]
+        # six weights of 1: five adds of a step each, the product with 1 / 6, the output
+        assert bool(((out[0].double() - want.mean(0)).abs() <= 8 * 2.0 ** -23 * want.abs().mean(0)).all())
