@@ -44,7 +44,7 @@ cudaError_t launch_pages_extend(const PagesView &p, int n, const int *seqs, cons
 // read: rows from the pool instead of into it.
 cudaError_t launch_pages_rows(const PagesView &p, const PagesAppend &a, bool read, cudaStream_t s);
 cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s);
-cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, cudaStream_t s);
+cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, int num_sms, cudaStream_t s);
 
 // Raises a kernel's shared-memory limit once per device (the attribute outlives the call).  least_regs: registers a thread it
 // must have been compiled to, where it hands them around between its warps.

@@ -492,7 +492,7 @@ cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const i
     return launch(reinterpret_cast<void *>(pages_fork_copy_kernel), dim3((unsigned)gx, n), 256, args2, s);
 }
 
-cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, cudaStream_t s) {
+cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, int num_sms, cudaStream_t s) {
     int c = compact ? 1 : 0;
     void *args[] = {const_cast<PagesView *>(&p), &n, &seqs, &c};
     cudaError_t e = launch(reinterpret_cast<void *>(pages_free_kernel), dim3(1), kT, args, s);
@@ -510,7 +510,7 @@ cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool c
         rows = 1;
     }
     void *args2[] = {const_cast<PagesView *>(&p), &heads, &rows, &bytes};
-    return launch(reinterpret_cast<void *>(pages_compact_kernel), dim3(152 * 4), kCompactThreads, args2, s);
+    return launch(reinterpret_cast<void *>(pages_compact_kernel), dim3(num_sms * 4), kCompactThreads, args2, s);
 }
 
 }  // namespace l2

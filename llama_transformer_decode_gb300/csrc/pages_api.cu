@@ -258,7 +258,9 @@ int l2_pages_free(const L2Pages *pool, int n, const int *seqs, int compact, void
     if (rc || (rc = check_count(who, n, 0)) || (n && (rc = check_ptr(who, "seqs", seqs, 4, &device)))) return rc;
     DeviceGuard guard;
     if (!guard.enter(device)) return refuse(L2_ECUDA, "%s: cannot use device %d", who, device);
-    return finish(who, launch_pages_free(v, n, seqs, compact != 0, static_cast<cudaStream_t>(cuda_stream)));
+    const int sms = sm_count(device);
+    if (!sms) return refuse(L2_ECUDA, "%s: cannot query device %d", who, device);
+    return finish(who, launch_pages_free(v, n, seqs, compact != 0, sms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 long long l2_pages_attention_ws(const L2Pages *pool, int B, int G, int n_heads) {
