@@ -108,6 +108,14 @@ class PagePool:
             raise ValueError(f"{name} must have {dims} dimensions, the pool's type, device and head size, its last one contiguous")
         return t.data_ptr(), shape, st
 
+    @staticmethod
+    def _used_on(stream, *tensors):
+        """A call on a stream of its own may run after its arguments are dropped: their memory is kept until it has."""
+        if stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+
     def check(self):
         """Waits for the pool's device and raises L2Error if a call could not be done (and clears the status)."""
         self._torch.cuda.synchronize(self.device)
@@ -127,6 +135,7 @@ class PagePool:
         rc = self._lib.l2_pages_append(self._ref, ctypes.byref(a), self._stream(stream))
         if rc:
             _raise(rc)
+        self._used_on(stream, k, v, seqs, starts)
 
     def read(self, k, v, seqs, starts=None, layer=None, stream=None):
         """Into ``k``, ``v`` (shaped as for append): rows starts[i]..starts[i + 1]-1 receive the first rows of seqs[i]."""
@@ -134,6 +143,7 @@ class PagePool:
         rc = self._lib.l2_pages_read(self._ref, ctypes.byref(a), self._stream(stream))
         if rc:
             _raise(rc)
+        self._used_on(stream, k, v, seqs, starts)
 
     def _moved(self, k, v, seqs, starts, layer, extend):
         whole = layer is None
@@ -154,6 +164,7 @@ class PagePool:
                                      None if rows is None else self._ints("rows", rows, n), self._stream(stream))
         if rc:
             _raise(rc)
+        self._used_on(stream, src, dst, rows)
 
     def free(self, seqs=None, compact=False, stream=None):
         """Empties sequences ``seqs`` and gives their pages back; ``compact`` then closes the pool up."""
@@ -162,6 +173,7 @@ class PagePool:
                                      self._stream(stream))
         if rc:
             _raise(rc)
+        self._used_on(stream, seqs)
 
     def attention(self, q, layer: int, seqs=None, group_starts=None, prefix_lens=None, scale=None, out=None, lse=None,
                   stream=None):
@@ -210,4 +222,5 @@ class PagePool:
         rc = self._lib.l2_pages_attention(self._ref, ctypes.byref(a), ws.data_ptr(), need, self._stream(stream))
         if rc:
             _raise(rc)
+        self._used_on(stream, q, seqs, group_starts, prefix_lens, None if fresh else out, lse)
         return out

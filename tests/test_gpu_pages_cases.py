@@ -380,3 +380,30 @@ def test_scales_that_fp32_does_not_hold_are_refused():
         want = pool.v[0, page].double().transpose(1, 2).reshape(8, 2, 8)[:6]
         # six weights of 1: five adds of a step each, the product with 1 / 6, the output
         assert bool(((out[0].double() - want.mean(0)).abs() <= 8 * 2.0 ** -23 * want.abs().mean(0)).all())
+
+
+def test_arguments_of_a_call_on_another_stream_may_be_dropped():
+    """The calls wait behind a long kernel of their stream while the memory of their arguments would be handed out again."""
+    pool = pkg.PagePool(1, 40, 2, 16, 64, 6, 8)
+    side = torch.cuda.Stream()
+    k, v = (torch.randn((1, 300, 2, 64), device="cuda") for _ in range(2))
+    q = torch.randn((3, 4, 64), device="cuda")
+    keep, lens = (k.clone(), v.clone(), q.clone()), [100, 93, 107]
+    index = dev([0, 1, 2]), dev([0, 100, 193, 300]), dev([0, 1, 2]), dev([3, 4, 5]), dev([64, 64, 64]), dev([0, 3]), dev([0])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(60_000_000)
+    pool.append(k, v, index[0], index[1], stream=side)
+    pool.fork(index[2], index[3], index[4], stream=side)
+    lse = torch.empty((3, 4), device="cuda")
+    out = pool.attention(q, 0, seqs=index[3], group_starts=index[5], prefix_lens=index[6], lse=lse, stream=side)
+    rows_k, rows_v = (torch.zeros((100, 2, 64), device="cuda") for _ in range(2))
+    del k, v, q, index
+    junk = [torch.full(n, -99, dtype=torch.int32, device="cuda") for n in ((1, 300, 2, 64),) * 4 + ((3, 4, 64),) * 4 + ((3,), (2,), (4,), (1,)) * 64]
+    torch.cuda.synchronize()
+    pool.check()
+    assert pool.lens.tolist() == lens + [64, 64, 64] and len(junk) == 264
+    pool.read(rows_k, rows_v, dev([0]), dev([0, 100]), layer=0)
+    assert torch.equal(rows_k, keep[0][0, :100]) and torch.equal(rows_v, keep[1][0, :100])
+    again = pool.attention(keep[2], 0, seqs=dev([3, 4, 5]), group_starts=dev([0, 3]), prefix_lens=dev([0]))
+    assert torch.equal(out, again) and bool(lse.isfinite().all())
