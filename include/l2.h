@@ -318,7 +318,8 @@ int l2_forward_static(l2_ctx *ctx, int token, int pos, float *logits_out);
  *     that order against floor(k * P / 2^24).
  * All sums are exact integer arithmetic, so the result is a function of the
  * inputs alone (bit-for-bit reproducible).  Tokens whose weight is below
- * 2^-48 of the largest are never drawn.
+ * 2^-48 of the largest are never drawn.  A row in which no token has a weight (all of
+ * them -inf, as a mask that allows nothing leaves it) gives the first maximum, whatever the temperature.
  * logits (fp32, row-major [B][vocab_size], 4-byte aligned), rng_state
  * ([B] 64-bit states, non-zero) and tokens_out ([B] ints) are DEVICE
  * pointers owned by the caller; rows of logits are not modified.  The work
@@ -484,6 +485,163 @@ long long l2_pages_attention_ws(const L2Pages *pool, int B, int G, int n_heads);
  * of no matter, not used by another call at the same time. */
 int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *args, void *workspace, long long workspace_bytes,
                        void *cuda_stream);
+
+/*
+ * Drafted tokens.  A sequence that drafts holds, behind its committed rows, one row for each token of a tree of at most
+ * L2_TREE_NODES: rows starts[i] .. starts[i + 1] - 1 of a call (starts[0] = 0, ascending; rows behind starts[n] are nobody's and left
+ * as they are, so that calls of a fixed size can be captured) are the last starts[i + 1] - starts[i] rows of sequence seqs[i], appended by
+ * l2_pages_append in the same order.  parents[r] is the place of the parent of row r's token within its own tree, before its own
+ * (-1: it follows the committed rows; there may be several such tokens); without parents every tree is a chain.
+ */
+#define L2_TREE_NODES 64
+
+/*
+ * Attention of trees: row r of sequence s attends to s's committed rows, its own and those of the tokens above it,
+ *   out[r][h] = sum_t softmax_t(scale * q[r][h] . K[t][g(h)]) V[t][g(h)],  t over those rows,
+ * as l2_pages_attention computes it (types, accuracy, NaN and infinities, what the status says).  Rows that a token does not see have
+ * no part in its result, whatever they hold.  Committed rows are read once for all tokens of a sequence, on the tensor cores where
+ * they are long and (token, head) pairs many.  Chains take a prompt's chunk of up to L2_TREE_NODES tokens, too; a tree of one
+ * token is a decode step.
+ */
+typedef struct {
+    int layer;
+    int n;                   /* sequences, 1..1024 */
+    int rows;                /* 1..1024 */
+    int n_heads;             /* query heads, n_kv_heads..1024 */
+    const void *q;           /* DEVICE [rows][n_heads][head_size], strides in elements */
+    void *out;               /* DEVICE, alike; heads within rows or rows within heads */
+    float *lse;              /* DEVICE [rows][n_heads], or NULL: log of the sum of exp(scores) */
+    const int *seqs;         /* DEVICE [n] */
+    const int *starts;       /* DEVICE [n + 1] */
+    const int *parents;      /* DEVICE [rows], or NULL: chains */
+    long long q_row_stride, q_head_stride, out_row_stride, out_head_stride;
+    double scale;            /* usually 1 / sqrt(head_size); scale * log2(e) finite in fp32 */
+} L2PagesTreeAttention;
+
+/* Bytes of workspace a call of these sizes needs, or a negative status. */
+long long l2_pages_tree_attention_ws(const L2Pages *pool, int n, int rows, int n_heads);
+
+/* workspace: as for l2_pages_attention. */
+int l2_pages_tree_attention(const L2Pages *pool, const L2PagesTreeAttention *args, void *workspace, long long workspace_bytes,
+                            void *cuda_stream);
+
+/*
+ * Acceptance.  l2_pages_accept finds the path of each tree that the model agrees with: token 0 (what was sampled after the
+ * committed rows), then from each accepted token u the first child whose token is targets[u], what was sampled from u's logits.
+ * path[starts[i] ..] receives the places of the accepted tokens, ascending, then -1; counts[i] how many they are (0 for a tree without
+ * tokens); next[i] the target of the last one (-1 without tokens), which is token 0 of the sequence's next tree.
+ * Their rows then become the sequence's last ones, side by side, in every layer; the other rows' places are
+ * given back, with the pages that become free.  l2_pages_keep does that with a path and counts that are given (0 <= counts[i]; the first
+ * counts[i] entries ascending places of the tree), for callers with a rule of their own; tokens, targets, parents and next are NULL.
+ * A page that rows move into, or that is left partly filled, must be held by its sequence alone.  A call that cannot be done
+ * whole changes nothing and writes nothing (L2_PAGES_BAD_CALL, L2_PAGES_BAD_PAGE).
+ */
+typedef struct {
+    int n;                        /* sequences, 1..1024, each named once */
+    int rows;                     /* drafted rows of all, 0..65536 */
+    const int *seqs, *starts;     /* DEVICE [n], [n + 1] */
+    const int *parents;           /* DEVICE [rows], or NULL: chains */
+    const int *tokens, *targets;  /* DEVICE [rows] */
+    int *path, *counts, *next;    /* DEVICE [rows], [n], [n] or NULL */
+} L2PagesAccept;
+int l2_pages_accept(const L2Pages *pool, const L2PagesAccept *args, void *cuda_stream);
+int l2_pages_keep(const L2Pages *pool, const L2PagesAccept *args, void *cuda_stream);
+
+/*
+ * Rotary positions, for callers with layer code of their own: the queries and keys of rows at any positions, before the keys go into
+ * a pool.  The first rot_dim elements of a head are rot_dim / 2 pairs, (2 i, 2 i + 1) or with L2_ROPE_HALF (i, i + rot_dim / 2), and
+ * pair i of a row at position p turns by p * freqs[i]:
+ *   (a, b) -> amplitude * (a cos - b sin, a sin + b cos);
+ * the elements behind them stay as they are.  L2_ROPE_INTERLEAVED with base 10000 is what the decoder's steps do.
+ * l2_rope_freqs fills freqs[i] = base^(-2 i / rot_dim) (radians a position), scaled for contexts longer than a model was trained on:
+ *   L2_ROPE_LINEAR   freqs / factor;
+ *   L2_ROPE_BASE     with base * factor^(rot_dim / (rot_dim - 2)) for base: the slowest pair is slowed by factor, the first not;
+ *   L2_ROPE_BANDS    by wavelength: with t = original_len * freq / (2 pi) turns over the trained length, freq * (s + (1 - s) / factor),
+ *                    s = (t - low) / (high - low) clamped to 0..1: fast pairs stay, slow ones are slowed by factor.
+ * l2_rope_plan takes such frequencies, or a caller's own (finite), once; angles are exact to 2^-52 of p * freq
+ * and rounded to fp32 within half a turn, so far positions lose nothing.  Positions are int32, of either sign.
+ */
+#define L2_ROPE_INTERLEAVED 0
+#define L2_ROPE_HALF 1
+#define L2_ROPE_PLAIN 0
+#define L2_ROPE_LINEAR 1
+#define L2_ROPE_BASE 2
+#define L2_ROPE_BANDS 3
+#define L2_ROPE_MAX 256 /* largest rot_dim and head_size */
+
+/* HOST only.  factor > 0; original_len, low < high: L2_ROPE_BANDS only.  freqs: HOST [rot_dim / 2]. */
+int l2_rope_freqs(int rot_dim, double base, int scaling, double factor, double original_len, double low, double high, double *freqs);
+
+typedef struct {
+    int rot_dim, layout;
+    float amplitude;
+    unsigned ready;                            /* set by l2_rope_plan */
+    unsigned long long turns[L2_ROPE_MAX / 2]; /* 2^64 * freqs / (2 pi), mod 2^64 */
+} L2RopePlan;
+int l2_rope_plan(L2RopePlan *plan, int rot_dim, int layout, const double *freqs, double amplitude);
+
+/* q and k (either may be NULL, with no heads) are turned in one launch, in place where q_out = q with q's strides; otherwise the
+ * outputs share no memory with the inputs. */
+typedef struct {
+    int rows;                /* 0..2^24 - 1 */
+    int dtype;               /* L2_F32, L2_BF16, L2_F16 */
+    int head_size;           /* rot_dim..256 */
+    int n_heads, n_kv_heads; /* of q and of k, 0..1024 */
+    const int *positions;    /* DEVICE [rows] */
+    const void *q, *k;       /* DEVICE [rows][heads][head_size], strides in elements */
+    void *q_out, *k_out;     /* DEVICE, alike */
+    long long q_row_stride, q_head_stride, k_row_stride, k_head_stride;
+    long long q_out_row_stride, q_out_head_stride, k_out_row_stride, k_out_head_stride;
+} L2RopeRows;
+int l2_rope(const L2RopePlan *plan, const L2RopeRows *rows, void *cuda_stream);
+
+/*
+ * Rules on logits before l2_sample: penalties for tokens that a sequence already holds, biases, grammar masks.  For logit l of
+ * token v in a row of sequence s, in fp32 and in this order:
+ *   v in the history of s or on the row's path:     l = l > 0 ? l / repetition[s] : l * repetition[s];
+ *   n times, counted from counted_from[s] on, n > 0: l = l - (frequency[s] * n + presence[s]);
+ *   v among the biases of s:                        l = l + its value (of the last entry that names it);
+ *   bit v of the row's mask clear:                  l = -inf (whatever it was).
+ * history[s][0 .. lens[s]) are the sequence's committed tokens; repetition looks at all of them, the others from counted_from[s] on (after a
+ * prompt, say).  A row's path is, where drafted is given, its own drafted token and those above it, so that each token of a tree
+ * is penalised for what comes before its logits.  Tokens outside 0..vocab_size - 1 count nothing.  NULL penalties are 1, 0 and 0; NULL
+ * counted_from is 0.  A row whose mask allows nothing is -inf throughout.
+ */
+typedef struct {
+    int n_seqs, vocab_size;          /* vocab_size 1..2^24 */
+    int max_len;                     /* tokens a history has room for */
+    int n_bias;                      /* bias entries of all sequences; 0: none */
+    long long history_stride;        /* ints, at least max_len */
+    const int *history;              /* DEVICE [n_seqs][max_len] */
+    const int *lens, *counted_from;  /* DEVICE [n_seqs], counted_from or NULL */
+    const float *repetition, *presence, *frequency; /* DEVICE [n_seqs], each or NULL; repetition above 0 */
+    const int *bias_starts;          /* DEVICE [n_seqs + 1]: entries of sequence s */
+    const int *bias_tokens;          /* DEVICE [n_bias] */
+    const float *bias_values;        /* DEVICE [n_bias] */
+    int *status;                     /* DEVICE, one int, or NULL: L2_PAGES_BAD_CALL for rows that could not be done */
+    unsigned ready;                  /* set by l2_token_rules_init */
+} L2TokenRules;
+/* Checks what the host can see of the rules, which stay as they are from then on (their arrays' contents may change). */
+int l2_token_rules_init(L2TokenRules *rules);
+
+/* Rows of logits.  A row whose sequence, tree, lengths or mask number is invalid is not written, and reported. */
+typedef struct {
+    int n;                       /* sequences, 1..65535; one may be named twice */
+    int rows;                    /* 0..65535; n without starts */
+    const int *seqs;             /* DEVICE [n], or NULL: sequence i */
+    const int *starts;           /* DEVICE [n + 1], or NULL: one row each; rows behind starts[n] are left as they are */
+    const int *parents;          /* DEVICE [rows], or NULL: chains */
+    const int *drafted;          /* DEVICE [rows] tokens, or NULL: no path counts (and trees may be of any size) */
+    const void *logits;          /* DEVICE [rows][vocab_size] */
+    void *out;                   /* DEVICE, alike: logits itself with its type and stride, or memory of its own */
+    int dtype, out_dtype;        /* out_dtype: L2_F32 or dtype */
+    long long row_stride, out_row_stride; /* elements */
+    const unsigned *masks;       /* DEVICE [n_masks][ceil(vocab_size / 32)], bit v % 32 of word v / 32 for token v; or NULL */
+    long long mask_stride;       /* words */
+    int n_masks;
+    const int *mask_rows;        /* DEVICE [rows]: the row's mask, -1 for none; or NULL: mask r */
+} L2TokenRows;
+int l2_token_rules(const L2TokenRules *rules, const L2TokenRows *rows, void *cuda_stream);
 
 /*
  * A handle's cache rows into and out of a page pool (fp32, of the handle's layers, KV

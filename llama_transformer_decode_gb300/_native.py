@@ -16,8 +16,10 @@ LIB = os.path.join(BUILD, "libl2decode.so")
 BUILD_CHECKED = os.path.join(BUILD, "checked")
 LIB_CHECKED = os.path.join(BUILD, "libl2decode_checked.so")
 SOURCES = ("gemv.cu", "gemv_batched.cu", "gemv_tc.cu", "attention.cu", "attn_prefill.cu", "step_kernel.cu", "step_cta.cu",
-           "sample.cu", "pages.cu", "attn_pages.cu", "attn_pages_f32.cu", "attn_pages_16.cu", "pages_api.cu", "l2_api.cu")
-HEADERS = ("l2_device.cuh", "l2_params.h", "l2_kernels.h", "l2_pages.h", "l2_tc.cuh", "attn_pages.cuh", "attn_plan.cuh", "attn_pages_tc.cuh", "attn_pages_tc32.cuh", "attn_slots.h", "attn_split.h")
+           "sample.cu", "pages.cu", "pages_tree.cu", "attn_pages.cu", "attn_pages_f32.cu", "attn_pages_16.cu", "attn_tree_f32.cu",
+           "attn_tree_16.cu", "pages_api.cu", "rope.cu", "rules.cu", "rows_api.cu", "l2_api.cu")
+HEADERS = ("l2_device.cuh", "l2_params.h", "l2_kernels.h", "l2_check.h", "l2_pages.h", "l2_rows.h", "l2_tree.cuh", "l2_tc.cuh", "attn_pages.cuh",
+           "attn_plan.cuh", "attn_walk_f32.cuh", "attn_walk_16.cuh", "attn_pages_tc.cuh", "attn_pages_tc32.cuh", "attn_slots.h", "attn_split.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3"]
 
@@ -107,6 +109,48 @@ class L2PagesAttention(ctypes.Structure):
                 + [("scale", ctypes.c_double)])
 
 
+class L2PagesTreeAttention(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("layer", "n", "rows", "n_heads")]
+                + [(n, ctypes.c_void_p) for n in ("q", "out", "lse", "seqs", "starts", "parents")]
+                + [(n, ctypes.c_longlong) for n in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride")]
+                + [("scale", ctypes.c_double)])
+
+
+class L2PagesAccept(ctypes.Structure):
+    _fields_ = ([("n", ctypes.c_int), ("rows", ctypes.c_int)]
+                + [(n, ctypes.c_void_p) for n in ("seqs", "starts", "parents", "tokens", "targets", "path", "counts", "next")])
+
+
+ROPE_MAX = 256
+
+
+class L2RopePlan(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("amplitude", ctypes.c_float), ("ready", ctypes.c_uint),
+                ("turns", ctypes.c_ulonglong * (ROPE_MAX // 2))]
+
+
+class L2RopeRows(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("rows", "dtype", "head_size", "n_heads", "n_kv_heads")]
+                + [(n, ctypes.c_void_p) for n in ("positions", "q", "k", "q_out", "k_out")]
+                + [(n, ctypes.c_longlong) for n in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                                                    "q_out_row_stride", "q_out_head_stride", "k_out_row_stride", "k_out_head_stride")])
+
+
+class L2TokenRules(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("n_seqs", "vocab_size", "max_len", "n_bias")] + [("history_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in ("history", "lens", "counted_from", "repetition", "presence", "frequency",
+                                                  "bias_starts", "bias_tokens", "bias_values", "status")]
+                + [("ready", ctypes.c_uint)])
+
+
+class L2TokenRows(ctypes.Structure):
+    _fields_ = ([("n", ctypes.c_int), ("rows", ctypes.c_int)]
+                + [(n, ctypes.c_void_p) for n in ("seqs", "starts", "parents", "drafted", "logits", "out")]
+                + [("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("row_stride", ctypes.c_longlong),
+                   ("out_row_stride", ctypes.c_longlong), ("masks", ctypes.c_void_p), ("mask_stride", ctypes.c_longlong),
+                   ("n_masks", ctypes.c_int), ("mask_rows", ctypes.c_void_p)])
+
+
 EXPORTS = ("l2_create", "l2_reset", "l2_forward", "l2_forward_batch", "l2_forward_host", "l2_logits",
            "l2_position", "l2_debug_attention", "l2_kv_export", "l2_kv_import", "l2_sync",
            "l2_last_error", "l2_destroy", "l2_launch_op", "l2_kernels_per_step",
@@ -114,7 +158,8 @@ EXPORTS = ("l2_create", "l2_reset", "l2_forward", "l2_forward_batch", "l2_forwar
            "l2_forward_dev_tokens", "l2_prefill", "l2_debug_fail_graph_at", "l2_debug_wait_timeout",
            "l2_debug_bounds_checked", "l2_debug_limit_cache", "l2_launch_op_batch", "l2_pages_scratch_ints",
            "l2_pages_init", "l2_pages_append", "l2_pages_read", "l2_pages_fork", "l2_pages_free", "l2_pages_attention_ws",
-           "l2_pages_attention", "l2_kv_to_pages", "l2_kv_from_pages")
+           "l2_pages_attention", "l2_pages_tree_attention_ws", "l2_pages_tree_attention", "l2_pages_accept", "l2_pages_keep",
+           "l2_kv_to_pages", "l2_kv_from_pages", "l2_rope_freqs", "l2_rope_plan", "l2_rope", "l2_token_rules_init", "l2_token_rules")
 
 _lib = None
 
@@ -175,6 +220,20 @@ def declare(lib):
     lib.l2_pages_attention_ws.argtypes = [pp, i, i, i]
     lib.l2_pages_attention_ws.restype = ctypes.c_longlong
     lib.l2_pages_attention.argtypes = [pp, ctypes.POINTER(L2PagesAttention), vp, ctypes.c_longlong, vp]
+    lib.l2_pages_tree_attention_ws.argtypes = [pp, i, i, i]
+    lib.l2_pages_tree_attention_ws.restype = ctypes.c_longlong
+    lib.l2_pages_tree_attention.argtypes = [pp, ctypes.POINTER(L2PagesTreeAttention), vp, ctypes.c_longlong, vp]
+    lib.l2_pages_accept.argtypes = [pp, ctypes.POINTER(L2PagesAccept), vp]
+    lib.l2_pages_keep.argtypes = [pp, ctypes.POINTER(L2PagesAccept), vp]
+    d, dp = ctypes.c_double, ctypes.POINTER(ctypes.c_double)
+    lib.l2_rope_freqs.argtypes = [i, d, i, d, d, d, d, dp]
+    lib.l2_rope_plan.argtypes = [ctypes.POINTER(L2RopePlan), i, i, dp, d]
+    lib.l2_rope.argtypes = [ctypes.POINTER(L2RopePlan), ctypes.POINTER(L2RopeRows), vp]
+    lib.l2_token_rules_init.argtypes = [ctypes.POINTER(L2TokenRules)]
+    lib.l2_token_rules.argtypes = [ctypes.POINTER(L2TokenRules), ctypes.POINTER(L2TokenRows), vp]
+    for name in ("l2_pages_tree_attention", "l2_pages_accept", "l2_pages_keep", "l2_rope_freqs", "l2_rope_plan", "l2_rope",
+                 "l2_token_rules_init", "l2_token_rules"):
+        getattr(lib, name).restype = i
     for name in ("l2_pages_append", "l2_pages_read", "l2_kv_to_pages", "l2_kv_from_pages", "l2_pages_fork", "l2_pages_free", "l2_pages_attention"):
         getattr(lib, name).restype = i
     for name in ("l2_create", "l2_reset", "l2_forward", "l2_forward_batch", "l2_forward_host",

@@ -43,8 +43,16 @@ __global__ void __launch_bounds__(kPagesMaxCall) attn_pages_plan_kernel(const Pa
     pdl_launch_dependents();
     pdl_wait();
     const Plan pl = plan_of(p.plan, p.B, p.G);
-    plan_build<kPagesMaxCall, kPagesMaxCall, true>(p, pl, sc, true);
-    plan_rows<kPagesMaxCall>(p, pl, pl.row);
+    plan_build<kPagesMaxCall, kPagesMaxCall, false, true>(p, pl, sc, true);
+    plan_rows<kPagesMaxCall, false>(p, pl, pl.row);
+}
+__global__ void __launch_bounds__(kPagesMaxCall) attn_tree_plan_kernel(const PagesAttn p) {
+    __shared__ PlanScratch<kPagesMaxCall, kPagesMaxCall> sc;
+    pdl_launch_dependents();
+    pdl_wait();
+    const Plan pl = plan_of(p.plan, p.B, p.G);
+    plan_build<kPagesMaxCall, kPagesMaxCall, true, true>(p, pl, sc, true);
+    plan_rows<kPagesMaxCall, true>(p, pl, pl.row);
 }
 
 namespace {
@@ -95,8 +103,9 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
     const int per_tc = pl.hdr[kHdrTcPer];
     const int4 *rp = reinterpret_cast<const int4 *>(pl.row + b);
     const int4 ow = rp[0], re = rp[1], tc = rp[2];
-    const int gr = rp[3].x, per = h0.y;
-    if (!h0.z) return;
+    const int4 in = rp[3];
+    const int gr = in.x, per = h0.y;
+    if (!h0.z || in.y) return;
     // first walker, parts and first row of the parts of the item that holds pair mi of a source of n pairs
     struct Range {
         int w0, n, row;
@@ -242,10 +251,10 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
 
 namespace {
 
-int max_items(int B, int G, int n_heads, int n_kv_heads) {
+int max_items(int B, int G, int n_heads, int n_kv_heads, bool tree) {
     // prefix tiles: sum over groups of ceil(rows gq / 16) <= (B gq) / 16 + G
     const long long gq = heads_per_kv(n_heads, n_kv_heads);
-    const long long pre = G ? (B * gq) / kM + G : 0, own = B * ((gq + kM - 1) / kM);
+    const long long pre = G ? (B * gq) / kM + G : 0, own = tree ? 0 : B * ((gq + kM - 1) / kM);
     return (int)((pre + own) * n_kv_heads);
 }
 
@@ -260,9 +269,9 @@ size_t tc_part_rows(int B, int n_heads, int n_kv_heads, int num_sms) {
 struct WsLayout {
     size_t plan, ml, acc, tc_ml, tc_acc, bytes, parts;
 };
-WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms) {
+WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms, bool tree) {
     WsLayout w;
-    w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads) + (size_t)num_sms * kWalkWarps;
+    w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads, tree) + (size_t)num_sms * kWalkWarps;
     const size_t tc = G ? tc_part_rows(B, n_heads, n_kv_heads, num_sms) : 0;
     w.plan = 0;
     w.ml = w.plan + align256(plan_bytes(B, G) + (size_t)B * sizeof(RowPlan));
@@ -275,14 +284,14 @@ WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int
 
 }  // namespace
 
-size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms) {
-    return ws_layout(B, G, n_heads, n_kv_heads, head_size, num_sms).bytes;
+size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms, bool tree) {
+    return ws_layout(B, G, n_heads, n_kv_heads, head_size, num_sms, tree).bytes;
 }
 
 // Kernels of a call: [plan] parts, merge.  Each is launched as a dependent of what is before it in the stream (the first too: its blocks
 // come up while that ends, and wait for its end before they read anything).
 cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s) {
-    const WsLayout w = ws_layout(p.B, p.G, p.n_heads, p.n_kv_heads, p.head_size, num_sms);
+    const WsLayout w = ws_layout(p.B, p.G, p.n_heads, p.n_kv_heads, p.head_size, num_sms, p.tree);
     char *base = static_cast<char *>(ws);
     p.plan = reinterpret_cast<int *>(base + w.plan);
     p.ws_ml = reinterpret_cast<float *>(base + w.ml);
@@ -295,7 +304,7 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     p.tile_shift = f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size);
     // whether any prefix of such a call could be one for the tensor cores; the plan decides for each
     p.tc = p.G && tc_worth(p, p.B * heads_per_kv(p.n_heads, p.n_kv_heads), p.max_pages * p.page_size) && (f32 || attn_pages_tc_supported(p));
-    p.plan_in_block = p.B + p.G <= kPlanInBlock && !p.wide;
+    p.plan_in_block = (p.tree ? p.G <= kTreePlanInBlock : p.B + p.G <= kPlanInBlock) && !p.wide;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -307,9 +316,13 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     if (!p.plan_in_block) {
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(kPagesMaxCall);
-        if ((e = cudaLaunchKernelEx(&cfg, attn_pages_plan_kernel, p)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, p.tree ? attn_tree_plan_kernel : attn_pages_plan_kernel, p)) != cudaSuccess) return e;
     }
-    if ((e = f32 ? launch_attn_pages_f32(p, cfg) : launch_attn_pages_16(p, cfg)) != cudaSuccess) return e;
+    if (p.tree)
+        e = f32 ? launch_attn_tree_f32(p, cfg) : launch_attn_tree_16(p, cfg);
+    else
+        e = f32 ? launch_attn_pages_f32(p, cfg) : launch_attn_pages_16(p, cfg);
+    if (e != cudaSuccess) return e;
     // few (row, head) pairs: four warps to each, since prefixes then come in many parts (a row of 112 parts: 57 -> 31 us a call);
     // many: one warp to each (2048 pairs of 7 parts: 41 us a call against 46)
     const int pairs = p.B * p.n_heads;

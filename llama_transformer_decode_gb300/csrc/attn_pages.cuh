@@ -6,6 +6,7 @@
 
 #include "l2_device.cuh"
 #include "l2_pages.h"
+#include "l2_tree.cuh"
 
 namespace l2 {
 
@@ -32,7 +33,7 @@ struct alignas(16) RowPlan {
     int own_t0, own_i0, own_kt, own_cost;          // its own keys
     int rest_t0, rest_i0, rest_kt, rest_cost;      // what is left of its group's prefix
     int tc_t0, tc_kt, tc_r0, group_rows;           // the prefix's whole tiles
-    int row_in_group, pad[3];
+    int row_in_group, behind, pad[2];              // behind: the last tree, a row that is left as it was
 };
 struct Plan {
     int *hdr;
@@ -58,6 +59,8 @@ __host__ __device__ inline Plan plan_of(void *base, int B, int G) {
 // 2 us of latency where a kernel of its own before it costs 6.  Larger calls have such a kernel.
 constexpr int kPlanInBlock = 192;
 constexpr size_t kPlanSmem = plan_bytes(kPlanInBlock / 2, kPlanInBlock / 2);  // the most for G + B sources, G <= B
+constexpr int kTreePlanInBlock = 128;  // sequences with trees, whose rows are no sources
+static_assert(plan_bytes(0, kTreePlanInBlock) <= kPlanSmem && kTreePlanInBlock <= kPlanInBlock, "the plan's room");
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (int)((unsigned)(a + b - 1) / (unsigned)b); }  // a >= 0, b > 0
 
@@ -142,13 +145,13 @@ __device__ __forceinline__ void cp_wait() {
 // One item's share of a walker's range, as the copying side hands it to the computing side (in shared memory).
 struct alignas(16) WalkItem {
     int slot, n_tiles, left;          // item number of all, tiles, keys from the first tile on
-    int row0, m0, pairs, head0, nh;   // rows, first pair, pairs, query heads head0 .. head0 + nh - 1
+    int row0, m0, pairs, head0, nh;   // rows, first pair, pairs, query heads head0 .. head0 + nh - 1 (trees: and 2^16 times the source's rows)
 };
 constexpr int kItems = 8;  // a ring of them a warp: the copies are at most four tiles, so four items, ahead
 
 // The copies of a walking warp run through the tiles of its range in order, item after item, without a break: step()
 // copies one tile and finds the next, whose page ids then have a tile's time to arrive.
-template <int KT, int ROW>
+template <int KT, int ROW, bool TREE>
 struct Walk {
     const int *table;
     long long head;       // byte offset of the KV head
@@ -158,7 +161,8 @@ struct Walk {
     int issued, items;    // tiles copied, items found
     bool on;
 
-    __device__ __forceinline__ void start(const Plan &pl, int wid, int S) {
+    __device__ __forceinline__ void start(const PagesAttn &p, const Plan &pl, int wid) {
+        const int S = TREE ? p.G : p.G + p.B;
         const int T = pl.hdr[kHdrCost], per = pl.hdr[kHdrPer];
         x = min(wid * per, T);
         x1 = min(x + per, T);
@@ -199,7 +203,8 @@ struct Walk {
                 const int h0 = first_head(kvh, p.n_heads, p.n_kv_heads);
                 int4 *q = reinterpret_cast<int4 *>(queue + items % kItems);
                 q[0] = make_int4(a.y + item, rem, key1 - key, b.z);
-                q[1] = make_int4(m0, min(kM, n - m0), h0, first_head(kvh + 1, p.n_heads, p.n_kv_heads) - h0);
+                const int nh = first_head(kvh + 1, p.n_heads, p.n_kv_heads) - h0;
+                q[1] = make_int4(m0, min(kM, n - m0), h0, TREE ? nh | b.w << 16 : nh);
             }
             key += threadIdx.x & 31;
             ++items;
@@ -251,6 +256,32 @@ struct Walk {
 __device__ __forceinline__ const char *walk_query(const PagesAttn &p, const WalkItem &w, int i, int gq) {
     const int m = w.m0 + i, r = (int)((unsigned)m / (unsigned)gq), j = m - r * gq;
     return i < w.pairs && j < w.nh ? p.q + (w.row0 + r) * p.q_row + (w.head0 + j) * p.q_head : nullptr;
+}
+
+// What a walker knows of its item where rows are drafted tokens: how many the source has, and, in lane i, for pair i & 15, which of
+// them its token sees, a bit each.  It sees all keys before theirs.
+struct TreeItem {
+    int n;
+    u64 sees;
+};
+// The words are made where the item's last tile reaches the drafted rows.
+template <int KT>
+__device__ __forceinline__ TreeItem tree_item(const PagesAttn &p, WalkItem &w, int gq) {
+    TreeItem t;
+    t.n = w.nh >> 16;
+    w.nh &= 0xffff;
+    t.sees = ~0ull;
+    if (w.left - w.n_tiles * KT < t.n) {
+        const TreeWords words = tree_words(tree_parents(p.parents ? p.parents + w.row0 : nullptr, t.n));
+        const int m = w.m0 + (int)(threadIdx.x & 15);
+        t.sees = tree_word(words, min((int)((unsigned)m / (unsigned)gq), kTreeNodes - 1));
+    }
+    return t;
+}
+// Keys of a tile that a token sees, bit k for key k: `left` keys from the tile's first to the end of the sequence, the last n of them drafted.
+__device__ __forceinline__ unsigned tree_bits(u64 sees, int n, int left) {
+    const int at = n - left;  // of the tile's first key among the drafted ones
+    return at >= 0 ? (unsigned)(sees >> at) : at <= -32 ? ~0u : (unsigned)(sees << -at) | ((1u << -at) - 1u);
 }
 
 // Walkers that are warps: neighbours in the numbering sit in different blocks, so that a stretch of costlier tiles

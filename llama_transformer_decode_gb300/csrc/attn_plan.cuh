@@ -54,40 +54,71 @@ __device__ __forceinline__ int2 plan_scan(int2 v, int2 *total, int2 *buf) {
 
 // MAX: most groups or rows (MAX <= NT).  Ends with a barrier.  report: sets the status word when the call is bad.  WIDE: calls with p.wide
 // are among those planned; they have a plan kernel (in the attention kernels the sum would cost every call: 155.7 us against 154.4).
-template <int NT, int MAX, bool WIDE = false>
+// TREE: groups are sequences with trees of drafted tokens.  A group's keys, but for whole tiles that go to the tensor cores, are one
+// source then: which of the last ones a row sees is the walk's matter.
+template <int NT, int MAX, bool TREE, bool WIDE = false>
 __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, PlanScratch<NT, MAX> &sc, bool report) {
-    const int i = threadIdx.x, S = p.G + p.B, gq = heads_per_kv(p.n_heads, p.n_kv_heads);
+    const int i = threadIdx.x, S = TREE ? p.G : p.G + p.B, gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const bool f32 = p.dtype == L2_F32;
     bool bad = false;
     int len = 0, seq = 0, P = 0, a0 = 0;
-    // what depends on nothing is loaded before the lengths, which depend on seqs
-    if (i < p.G) P = p.prefix_lens[i];
-    if (p.G && i <= p.G) a0 = p.group_starts[i];
-    if (i < p.B) {
-        seq = p.seqs ? p.seqs[i] : i;
-        bad = seq < 0 || seq >= p.n_seqs;
-        if (!bad) len = p.lens[seq];
-        bad |= len < 0 || len > p.max_pages * p.page_size;
-        sc.len[i] = len;
-        sc.seq[i] = seq;
-    }
-    if (i == 0) {
-        sc.spread = 0;
-        sc.cost[0] = sc.cost[1] = 0;
-    }
-    if (p.G) {
-#pragma unroll 1
-        for (int g = i; g <= p.G; g += NT) {
-            const int a = g == i ? a0 : p.group_starts[g];
-            bad |= (g == 0 && a != 0) || (g == p.G && a != p.B) || a < 0 || a > p.B;
-            sc.gstart[g] = a;
-        }
-        bad |= P < 0;
-        __syncthreads();
+    constexpr int kOwn = TREE ? (kPagesMaxCall + NT - 1) / NT : 1;  // parents that a thread looks at
+    int parent[kOwn];
+    if constexpr (TREE) {
+        int a1 = 0;
         if (i < p.G) {
-            const int rows = sc.gstart[i + 1] - sc.gstart[i];
-            bad |= rows < 0;
-            sc.minlen[i] = rows < 2 ? 0 : P;  // a row alone has nothing to share: all its keys are its own
+            seq = p.seqs[i];
+            a0 = p.group_starts[i];
+            a1 = p.group_starts[i + 1];
+        }
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k)
+            if (p.parents && k * NT + i < p.B) parent[k] = p.parents[k * NT + i];
+        if (i < p.G) {
+            bad = seq < 0 || seq >= p.n_seqs;
+            if (!bad) len = p.lens[seq];
+            bad |= a0 < 0 || a1 < a0 || a1 > p.B || a1 - a0 > kTreeNodes || (i == 0 && a0 != 0);
+            bad |= len < a1 - a0 || len > p.max_pages * p.page_size;
+            sc.gstart[i] = a0;
+            if (i == p.G - 1) sc.gstart[p.G] = a1;
+            sc.len[i] = len;
+            sc.seq[i] = seq;
+            sc.minlen[i] = len - (a1 - a0);  // committed rows
+        }
+        if (i == 0) {
+            sc.spread = 0;
+            sc.cost[0] = sc.cost[1] = 0;
+        }
+    } else {
+        // what depends on nothing is loaded before the lengths, which depend on seqs
+        if (i < p.G) P = p.prefix_lens[i];
+        if (p.G && i <= p.G) a0 = p.group_starts[i];
+        if (i < p.B) {
+            seq = p.seqs ? p.seqs[i] : i;
+            bad = seq < 0 || seq >= p.n_seqs;
+            if (!bad) len = p.lens[seq];
+            bad |= len < 0 || len > p.max_pages * p.page_size;
+            sc.len[i] = len;
+            sc.seq[i] = seq;
+        }
+        if (i == 0) {
+            sc.spread = 0;
+            sc.cost[0] = sc.cost[1] = 0;
+        }
+        if (p.G) {
+#pragma unroll 1
+            for (int g = i; g <= p.G; g += NT) {
+                const int a = g == i ? a0 : p.group_starts[g];
+                bad |= (g == 0 && a != 0) || (g == p.G && a != p.B) || a < 0 || a > p.B;
+                sc.gstart[g] = a;
+            }
+            bad |= P < 0;
+            __syncthreads();
+            if (i < p.G) {
+                const int rows = sc.gstart[i + 1] - sc.gstart[i];
+                bad |= rows < 0;
+                sc.minlen[i] = rows < 2 ? 0 : P;  // a row alone has nothing to share: all its keys are its own
+            }
         }
     }
     auto refused = [&]() {
@@ -99,7 +130,24 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     };
     if (refused()) return;
     int2 tc_all = make_int2(0, 0);
-    if (p.G) {
+    if constexpr (TREE) {
+        // every parent comes before its token, in the same tree
+        if (p.parents) {
+#pragma unroll
+            for (int k = 0; k < kOwn; ++k) {
+                const int r = k * NT + i;
+                if (r >= sc.gstart[p.G]) continue;
+                int lo = 0, hi = p.G;
+#pragma unroll 1
+                while (hi - lo > 1) {
+                    const int m = (lo + hi) >> 1;
+                    sc.gstart[m] <= r ? lo = m : hi = m;
+                }
+                bad |= parent[k] < -1 || parent[k] >= r - sc.gstart[lo];
+            }
+            if (refused()) return;
+        }
+    } else if (p.G) {
         if (i < p.B) {
             int lo = 0, hi = p.G;  // the group of the row: the last that starts at or before it
 #pragma unroll 1
@@ -116,10 +164,10 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         // sequences as long as their tables would not do: what these cost, with every prefix in both roles
         auto tiles = [&](int keys) { return (long long)((keys + (1 << p.tile_shift) - 1) >> p.tile_shift); };
         long long walk = 0, tc = 0;
-        if (i < p.B) walk = cdiv(gq, kM) * (kItemCost + kMaxTileCost * tiles(len - (p.G ? sc.minlen[sc.group[i]] : 0)));
+        if (!TREE && i < p.B) walk = cdiv(gq, kM) * (kItemCost + kMaxTileCost * tiles(len - (p.G ? sc.minlen[sc.group[i]] : 0)));
         if (i < p.G) {
             const int n = (sc.gstart[i + 1] - sc.gstart[i]) * gq;
-            walk += cdiv(n, kM) * (kItemCost + kMaxTileCost * tiles(sc.minlen[i]));
+            walk += cdiv(n, kM) * (kItemCost + kMaxTileCost * tiles(TREE ? sc.len[i] : sc.minlen[i]));
             tc = tc_runs(n, f32) * (kTcItemCost + tc_cost(n, p.head_size, f32) * (long long)(sc.minlen[i] / tc_keys(f32)));
         }
         if (walk) atomicAdd(&sc.cost[0], (unsigned long long)walk * p.n_kv_heads);
@@ -155,16 +203,20 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         Source e = {};
         if (s < p.G) {
             e.key0 = sc.mintc[s];
-            e.key1 = sc.minlen[s];
+            e.key1 = TREE ? sc.len[s] : sc.minlen[s];
             e.row0 = sc.gstart[s];
             e.rows = sc.gstart[s + 1] - e.row0;
+            if (TREE) {
+                e.seq = sc.seq[s];
+                if (!e.rows) e.key1 = e.key0;
+            }
         } else if (s < S) {
             e.row0 = s - p.G;
             e.rows = 1;
             e.key0 = p.G ? sc.minlen[sc.group[e.row0]] : 0;
             e.key1 = sc.len[e.row0];
         }
-        if (e.rows > 0) e.seq = sc.seq[e.row0];
+        if (!TREE && e.rows > 0) e.seq = sc.seq[e.row0];
         e.kt = (e.key1 - e.key0 + (1 << p.tile_shift) - 1) >> p.tile_shift;
         e.cost = tile_cost(p.dtype, min(e.rows * gq, kM));
         const int items = e.kt ? (e.rows * gq + kM - 1) / kM * p.n_kv_heads : 0;
@@ -194,18 +246,31 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
 }
 
 // What the merge needs of each row, from a plan that is complete.
-template <int NT>
+template <int NT, bool TREE>
 __device__ __forceinline__ void plan_rows(const PagesAttn &p, const Plan &pl, RowPlan *rows) {
 #pragma unroll 1
     for (int b = threadIdx.x; b < p.B; b += NT) {
         RowPlan r = {};
-        const Source &o = pl.src[p.G + b];
-        r.own_t0 = o.t0;
-        r.own_i0 = o.i0;
-        r.own_kt = o.kt;
-        r.own_cost = o.cost;
+        if constexpr (!TREE) {
+            const Source &o = pl.src[p.G + b];
+            r.own_t0 = o.t0;
+            r.own_i0 = o.i0;
+            r.own_kt = o.kt;
+            r.own_cost = o.cost;
+        }
         if (p.G && pl.hdr[kHdrOk]) {
-            const int g = pl.group[b];
+            int g = 0;
+            if constexpr (TREE) {
+                int hi = p.G;  // the last group that starts at or before the row
+#pragma unroll 1
+                while (hi - g > 1) {
+                    const int m = (g + hi) >> 1;
+                    pl.src[m].row0 <= b ? g = m : hi = m;
+                }
+                r.behind = b >= pl.src[g].row0 + pl.src[g].rows;
+            } else {
+                g = pl.group[b];
+            }
             const Source &e = pl.src[g];
             r.rest_t0 = e.t0;
             r.rest_i0 = e.i0;
@@ -223,15 +288,15 @@ __device__ __forceinline__ void plan_rows(const PagesAttn &p, const Plan &pl, Ro
 
 // The plan as a kernel's block uses it: built here (mem: kPlanSmem bytes, scratch: free until the caller's first
 // use of it; `keep`: also left in the workspace for the merge), or the workspace's.
-template <int NT>
+template <int NT, bool TREE>
 __device__ __forceinline__ Plan plan_here(const PagesAttn &p, void *mem, void *scratch, bool keep) {
     if (!p.plan_in_block) return plan_of(p.plan, p.B, p.G);
-    const Plan pl = plan_of(mem, p.B, p.G);
-    plan_build<NT, kPlanInBlock>(p, pl, *static_cast<PlanScratch<NT, kPlanInBlock> *>(scratch), keep);
+    const Plan pl = plan_of(mem, TREE ? 0 : p.B, p.G);  // a tree's rows have no sources of their own
+    plan_build<NT, kPlanInBlock, TREE>(p, pl, *static_cast<PlanScratch<NT, kPlanInBlock> *>(scratch), keep);
     if (keep) {
         const Plan out = plan_of(p.plan, p.B, p.G);
         if (threadIdx.x < kHdrInts) out.hdr[threadIdx.x] = pl.hdr[threadIdx.x];
-        plan_rows<NT>(p, pl, out.row);
+        plan_rows<NT, TREE>(p, pl, out.row);
     }
     return pl;
 }

@@ -46,6 +46,17 @@ cudaError_t launch_pages_rows(const PagesView &p, const PagesAppend &a, bool rea
 cudaError_t launch_pages_fork(const PagesView &p, int n, const int *src, const int *dst, const int *rows, cudaStream_t s);
 cudaError_t launch_pages_free(const PagesView &p, int n, const int *seqs, bool compact, int num_sms, cudaStream_t s);
 
+// Acceptance of drafted rows (pages_tree.cu): of the last starts[i + 1] - starts[i] rows of sequence seqs[i], those of its path stay, side by side.
+struct PagesAccept {
+    const int *seqs, *starts;        // [n], [n + 1]
+    int n, rows;
+    bool find;                       // path, counts and next are written; else path and counts are read
+    const int *parents;              // [rows] or nullptr (chains)
+    const int *tokens, *targets;     // [rows]
+    int *path, *counts, *next;       // [rows], [n], [n] or nullptr
+};
+cudaError_t launch_pages_accept(const PagesView &p, const PagesAccept &a, cudaStream_t s);
+
 // Raises a kernel's shared-memory limit once per device (the attribute outlives the call).  least_regs: registers a thread it
 // must have been compiled to, where it hands them around between its warps.
 struct DeviceOnce {
@@ -83,6 +94,9 @@ struct PagesAttn {
     const int *seqs;          // [B] or nullptr (sequence b)
     const int *group_starts;  // [G + 1] or nullptr
     const int *prefix_lens;   // [G]
+    // Trees of drafted tokens: group g is sequence seqs[g], its rows the sequence's last ones; the last group may end before row B.
+    bool tree;
+    const int *parents;       // [B] or nullptr (chains)
     int B, G, n_heads, n_kv_heads, head_size, page_size, max_pages, n_seqs, n_pages;
     int dtype, page_shift;    // log2(page_size), -1 where it is no power of two
     float scale_log2;         // scale * log2(e)
@@ -105,11 +119,14 @@ bool attn_pages_tc_supported(const PagesAttn &p);
 cudaError_t launch_attn_pages_16(const PagesAttn &p, cudaLaunchConfig_t cfg);
 int attn_pages_f32_shift(int head_size);
 cudaError_t launch_attn_pages_f32(const PagesAttn &p, cudaLaunchConfig_t cfg);
+// The same kernels compiled for trees (attn_tree_16.cu, attn_tree_f32.cu).
+cudaError_t launch_attn_tree_16(const PagesAttn &p, cudaLaunchConfig_t cfg);
+cudaError_t launch_attn_tree_f32(const PagesAttn &p, cudaLaunchConfig_t cfg);
 
 // cuTensorMapEncodeTiled, looked up once (l2_api.cu).
 void *tensor_map_encoder();
 
-size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms);
+size_t pages_attn_ws_bytes(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms, bool tree);
 // Lays `p`'s workspace out in ws and launches the kernels.
 cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s);
 

@@ -3,75 +3,15 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
 #include "../../include/l2.h"
+#include "l2_check.h"
 #include "l2_kernels.h"
 #include "l2_pages.h"
 
 using namespace l2;
 
 namespace {
-
-int refuse(int code, const char *fmt, ...) {
-    char buf[400];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    return set_call_error(code, buf);
-}
-
-int elt_size(int dtype) { return dtype == L2_F32 ? 4 : 2; }
-
-// Makes the pool's device current for the call and puts the caller's back.
-struct DeviceGuard {
-    int before = -1;
-    ~DeviceGuard() {
-        if (before >= 0) cudaSetDevice(before);
-    }
-    bool enter(int device) {
-        int cur = 0;
-        if (cudaGetDevice(&cur) != cudaSuccess) return false;
-        if (cur == device) return true;
-        if (cudaSetDevice(device) != cudaSuccess) return false;
-        before = cur;
-        return true;
-    }
-};
-
-// Device memory of one device (*device -1: any, and it is set), aligned to `align` bytes.
-int check_ptr(const char *who, const char *name, const void *p, unsigned align, int *device) {
-    if (!p) return refuse(L2_EINVAL, "%s: %s is NULL", who, name);
-    if (reinterpret_cast<uintptr_t>(p) & (align - 1)) return refuse(L2_EINVAL, "%s: %s must be %u-byte aligned", who, name, align);
-    cudaPointerAttributes a{};
-    if (cudaPointerGetAttributes(&a, p) != cudaSuccess || (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)) {
-        cudaGetLastError();
-        return refuse(L2_EINVAL, "%s: %s must be device memory", who, name);
-    }
-    if (*device < 0) *device = a.device;
-    if (a.device != *device) return refuse(L2_EINVAL, "%s: %s is on device %d, the pool on %d", who, name, a.device, *device);
-    return L2_OK;
-}
-
-// Whether rows of `width` elements at every combination of the strides have memory of their own: each stride, in ascending
-// order, is at least what the smaller ones span.
-bool rows_apart(const long long *strides, const int *counts, int dims, long long width) {
-    constexpr long long kFar = 1ll << 62;
-    long long span = width;
-    unsigned done = 0;
-    for (int k = 0; k < dims; ++k) {
-        int at = -1;  // the next stride; dimensions of one index are never stepped
-        for (int i = 0; i < dims; ++i)
-            if (counts[i] > 1 && !(done >> i & 1) && (at < 0 || strides[i] < strides[at])) at = i;
-        if (at < 0) return true;
-        done |= 1u << at;
-        if (strides[at] < span) return false;
-        span = strides[at] > kFar / counts[at] ? kFar : span + strides[at] * (counts[at] - 1);
-    }
-    return true;
-}
 
 constexpr unsigned kReady = 0x50a6e500u;  // with the pool's device below
 
@@ -142,28 +82,6 @@ int check_count(const char *who, int n, int least) {
     return L2_OK;
 }
 
-int finish(const char *who, cudaError_t e) {
-    if (e == cudaSuccess) return L2_OK;
-    cudaGetLastError();
-    return refuse(L2_ECUDA, "%s: %s (%s)", who, cudaGetErrorString(e), cudaGetErrorName(e));
-}
-
-// A row stride of the caller's tensors, in elements: whole 16-byte words.
-int check_stride(const char *who, const char *name, long long stride, int steps, int es) {
-    if (steps > 1 && (stride * es % 16 || stride < 0 || stride > (1ll << 40)))
-        return refuse(L2_EINVAL, "%s: %s %lld must not be negative and a multiple of 16 bytes", who, name, stride);
-    return L2_OK;
-}
-
-int sm_count(int device) {
-    static std::atomic<int> counts[64];
-    if (device < 0 || device >= 64) return 0;
-    int n = counts[device].load(std::memory_order_relaxed);
-    if (!n && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) == cudaSuccess)
-        counts[device].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 int check_attn_shape(const char *who, const L2Pages *p, int B, int G, int n_heads) {
     if (B < 1 || B > kPagesMaxCall) return refuse(L2_EINVAL, "%s: B = %d outside 1..%d", who, B, kPagesMaxCall);
     if (G < 0 || G > B) return refuse(L2_EINVAL, "%s: G = %d outside 0..B", who, G);
@@ -220,6 +138,64 @@ int move_rows(const char *who, const L2Pages *pool, const L2PagesRows *a, bool r
     return finish(who, launch_pages_rows(v, w, read, s));
 }
 
+// What attention of either kind takes: the layer, rows of queries and outputs, the scale.
+int attn_rows(const char *who, const L2Pages *pool, const PagesView &v, int layer, int B, int n_heads, double scale, const void *q, void *out,
+              float *lse, long long q_row, long long q_head, long long out_row, long long out_head, PagesAttn *k) {
+    int rc;
+    if (layer < 0 || layer >= pool->n_layers) return refuse(L2_EINVAL, "%s: layer %d outside 0..%d", who, layer, pool->n_layers - 1);
+    const float scale_log2 = (float)(scale * 1.4426950408889634);  // scores are fp32
+    if (!std::isfinite(scale) || !std::isfinite(scale_log2)) return refuse(L2_EINVAL, "%s: scale must be finite, in fp32 too", who);
+    const int es = elt_size(pool->dtype);
+    if ((rc = check_stride(who, "q_row_stride", q_row, B, es)) || (rc = check_stride(who, "q_head_stride", q_head, n_heads, es)) ||
+        (rc = check_stride(who, "out_row_stride", out_row, B, es)) || (rc = check_stride(who, "out_head_stride", out_head, n_heads, es)))
+        return rc;
+    const long long out_st[2] = {out_row, out_head};
+    const int out_n[2] = {B, n_heads};
+    if (!rows_apart(out_st, out_n, 2, pool->head_size)) return refuse(L2_EINVAL, "%s: output rows overlap", who);
+    k->k = v.k + layer * v.layer_stride;
+    k->v = v.v + layer * v.layer_stride;
+    k->lens = v.lens;
+    k->table = v.table;
+    k->err = v.err;
+    k->page_stride = v.page_stride;
+    k->head_stride = v.head_stride;
+    k->row_stride = v.row_stride;
+    k->q = static_cast<const char *>(q);
+    k->out = static_cast<char *>(out);
+    k->lse = lse;
+    k->q_row = q_row * es;
+    k->q_head = q_head * es;
+    k->o_row = out_row * es;
+    k->o_head = out_head * es;
+    k->B = B;
+    k->n_heads = n_heads;
+    k->n_kv_heads = v.n_kv_heads;
+    k->head_size = pool->head_size;
+    k->page_size = v.page_size;
+    k->max_pages = v.max_pages;
+    k->n_seqs = v.n_seqs;
+    k->n_pages = v.n_pages;
+    k->dtype = pool->dtype;
+    k->page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (v.page_size == 1 << i) k->page_shift = i;
+    k->scale_log2 = scale_log2;
+    return L2_OK;
+}
+
+// Most that an item costs in the plan: as many keys as a table has room for, in tiles of 8 that cost 7.
+long long longest_item(const PagesView &v) { return (((long long)v.max_pages * v.page_size + 7) / 8) * 7 + 128; }
+
+int attn_launch(const char *who, const PagesAttn &k, int device, void *ws, long long ws_bytes, void *cuda_stream) {
+    DeviceGuard guard;
+    if (!guard.enter(device)) return refuse(L2_ECUDA, "%s: cannot use device %d", who, device);
+    const int sms = sm_count(device);
+    if (!sms) return refuse(L2_ECUDA, "%s: cannot query device %d", who, device);
+    const long long need = (long long)pages_attn_ws_bytes(k.B, k.G, k.n_heads, k.n_kv_heads, k.head_size, sms, k.tree);
+    if (ws_bytes < need) return refuse(L2_EINVAL, "%s: workspace of %lld bytes, %lld needed", who, ws_bytes, need);
+    return finish(who, launch_pages_attn(k, ws, sms, static_cast<cudaStream_t>(cuda_stream)));
+}
+
 }  // namespace
 
 long long l2_pages_scratch_ints(int n_pages) { return n_pages < 1 ? L2_EINVAL : kScrHead + 3ll * n_pages; }
@@ -270,7 +246,7 @@ long long l2_pages_attention_ws(const L2Pages *pool, int B, int G, int n_heads) 
     if (rc || (rc = check_attn_shape(who, pool, B, G, n_heads))) return rc;
     const int sms = sm_count(device);
     if (!sms) return refuse(L2_ECUDA, "%s: cannot query device %d", who, device);
-    return (long long)pages_attn_ws_bytes(B, G, n_heads, pool->n_kv_heads, pool->head_size, sms);
+    return (long long)pages_attn_ws_bytes(B, G, n_heads, pool->n_kv_heads, pool->head_size, sms, false);
 }
 
 int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws, long long ws_bytes, void *cuda_stream) {
@@ -280,67 +256,106 @@ int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws,
     if (rc) return rc;
     if (!a) return refuse(L2_EINVAL, "%s: NULL arguments", who);
     if ((rc = check_attn_shape(who, pool, a->B, a->G, a->n_heads))) return rc;
-    if (a->layer < 0 || a->layer >= pool->n_layers)
-        return refuse(L2_EINVAL, "%s: layer %d outside 0..%d", who, a->layer, pool->n_layers - 1);
-    const float scale_log2 = (float)(a->scale * 1.4426950408889634);  // scores are fp32
-    if (!std::isfinite(a->scale) || !std::isfinite(scale_log2)) return refuse(L2_EINVAL, "%s: scale must be finite, in fp32 too", who);
-    if (!a->seqs && a->B > pool->n_seqs) return refuse(L2_EINVAL, "%s: B = %d exceeds the pool's %d sequences", who, a->B, pool->n_seqs);
-    const int es = elt_size(pool->dtype);
-    if ((rc = check_stride(who, "q_row_stride", a->q_row_stride, a->B, es)) ||
-        (rc = check_stride(who, "q_head_stride", a->q_head_stride, a->n_heads, es)) ||
-        (rc = check_stride(who, "out_row_stride", a->out_row_stride, a->B, es)) ||
-        (rc = check_stride(who, "out_head_stride", a->out_head_stride, a->n_heads, es)))
+    PagesAttn k{};
+    if ((rc = attn_rows(who, pool, v, a->layer, a->B, a->n_heads, a->scale, a->q, a->out, a->lse, a->q_row_stride, a->q_head_stride,
+                        a->out_row_stride, a->out_head_stride, &k)))
         return rc;
-    const long long out_st[2] = {a->out_row_stride, a->out_head_stride};
-    const int out_n[2] = {a->B, a->n_heads};
-    if (!rows_apart(out_st, out_n, 2, pool->head_size)) return refuse(L2_EINVAL, "%s: output rows overlap", who);
+    if (!a->seqs && a->B > pool->n_seqs) return refuse(L2_EINVAL, "%s: B = %d exceeds the pool's %d sequences", who, a->B, pool->n_seqs);
     if ((rc = check_ptr(who, "q", a->q, 16, &device)) || (rc = check_ptr(who, "out", a->out, 16, &device)) ||
         (a->lse && (rc = check_ptr(who, "lse", a->lse, 4, &device))) || (a->seqs && (rc = check_ptr(who, "seqs", a->seqs, 4, &device))) ||
         (a->G && ((rc = check_ptr(who, "group_starts", a->group_starts, 4, &device)) ||
                   (rc = check_ptr(who, "prefix_lens", a->prefix_lens, 4, &device)))) ||
         (rc = check_ptr(who, "workspace", ws, 256, &device)))
         return rc;
-    DeviceGuard guard;
-    if (!guard.enter(device)) return refuse(L2_ECUDA, "%s: cannot use device %d", who, device);
-    const int sms = sm_count(device);
-    if (!sms) return refuse(L2_ECUDA, "%s: cannot query device %d", who, device);
-    const long long need = (long long)pages_attn_ws_bytes(a->B, a->G, a->n_heads, pool->n_kv_heads, pool->head_size, sms);
-    if (ws_bytes < need) return refuse(L2_EINVAL, "%s: workspace of %lld bytes, %lld needed", who, ws_bytes, need);
-    PagesAttn k{};
-    k.k = v.k + a->layer * v.layer_stride;
-    k.v = v.v + a->layer * v.layer_stride;
-    k.lens = v.lens;
-    k.table = v.table;
-    k.err = v.err;
-    k.page_stride = v.page_stride;
-    k.head_stride = v.head_stride;
-    k.row_stride = v.row_stride;
-    k.q = static_cast<const char *>(a->q);
-    k.out = static_cast<char *>(a->out);
-    k.lse = a->lse;
-    k.q_row = a->q_row_stride * es;
-    k.q_head = a->q_head_stride * es;
-    k.o_row = a->out_row_stride * es;
-    k.o_head = a->out_head_stride * es;
     k.seqs = a->seqs;
     k.group_starts = a->group_starts;
     k.prefix_lens = a->prefix_lens;
-    k.B = a->B;
     k.G = a->G;
-    k.n_heads = a->n_heads;
-    k.n_kv_heads = v.n_kv_heads;
-    k.head_size = pool->head_size;
-    k.page_size = v.page_size;
-    k.max_pages = v.max_pages;
-    k.n_seqs = v.n_seqs;
-    k.n_pages = v.n_pages;
-    k.dtype = pool->dtype;
-    k.page_shift = -1;
-    for (int i = 0; i < 31; ++i)
-        if (v.page_size == 1 << i) k.page_shift = i;
-    // a bound of the plan's costs: own keys and prefixes, as long as the tables, in tiles of 8 keys that cost 7
+    // a bound of the plan's costs: own keys and prefixes
     const long long gq = (k.n_heads + k.n_kv_heads - 1) / k.n_kv_heads, items = 2ll * k.B * ((gq + 15) / 16 + 1) * k.n_kv_heads;
-    k.wide = items * ((((long long)v.max_pages * v.page_size + 7) / 8) * 7 + 128) > 1ll << 30;
-    k.scale_log2 = scale_log2;
-    return finish(who, launch_pages_attn(k, ws, sms, static_cast<cudaStream_t>(cuda_stream)));
+    k.wide = items * longest_item(v) > 1ll << 30;
+    return attn_launch(who, k, device, ws, ws_bytes, cuda_stream);
+}
+
+long long l2_pages_tree_attention_ws(const L2Pages *pool, int n, int rows, int n_heads) {
+    const char *who = "l2_pages_tree_attention_ws";
+    PagesView v;
+    int device = -1, rc = view_pool(who, pool, &v, &device);
+    if (rc || (rc = check_count(who, n, 1)) || (rc = check_attn_shape(who, pool, rows, 0, n_heads))) return rc;
+    const int sms = sm_count(device);
+    if (!sms) return refuse(L2_ECUDA, "%s: cannot query device %d", who, device);
+    return (long long)pages_attn_ws_bytes(rows, n, n_heads, pool->n_kv_heads, pool->head_size, sms, true);
+}
+
+int l2_pages_tree_attention(const L2Pages *pool, const L2PagesTreeAttention *a, void *ws, long long ws_bytes, void *cuda_stream) {
+    const char *who = "l2_pages_tree_attention";
+    PagesView v;
+    int device = -1, rc = view_pool(who, pool, &v, &device);
+    if (rc) return rc;
+    if (!a) return refuse(L2_EINVAL, "%s: NULL arguments", who);
+    if ((rc = check_count(who, a->n, 1)) || (rc = check_attn_shape(who, pool, a->rows, 0, a->n_heads))) return rc;
+    PagesAttn k{};
+    if ((rc = attn_rows(who, pool, v, a->layer, a->rows, a->n_heads, a->scale, a->q, a->out, a->lse, a->q_row_stride, a->q_head_stride,
+                        a->out_row_stride, a->out_head_stride, &k)))
+        return rc;
+    if ((rc = check_ptr(who, "q", a->q, 16, &device)) || (rc = check_ptr(who, "out", a->out, 16, &device)) ||
+        (a->lse && (rc = check_ptr(who, "lse", a->lse, 4, &device))) || (rc = check_ptr(who, "seqs", a->seqs, 4, &device)) ||
+        (rc = check_ptr(who, "starts", a->starts, 4, &device)) || (a->parents && (rc = check_ptr(who, "parents", a->parents, 4, &device))) ||
+        (rc = check_ptr(who, "workspace", ws, 256, &device)))
+        return rc;
+    k.tree = true;
+    k.seqs = a->seqs;
+    k.group_starts = a->starts;
+    k.parents = a->parents;
+    k.G = a->n;
+    // as above: all rows' pairs in items of 16, one more for each sequence
+    const long long gq = (k.n_heads + k.n_kv_heads - 1) / k.n_kv_heads, items = (k.B * gq / 16 + k.G) * k.n_kv_heads;
+    k.wide = items * longest_item(v) > 1ll << 30;
+    return attn_launch(who, k, device, ws, ws_bytes, cuda_stream);
+}
+
+namespace {
+
+int accept_rows(const char *who, const L2Pages *pool, const L2PagesAccept *a, bool find, void *cuda_stream) {
+    PagesView v;
+    int device = -1, rc = view_pool(who, pool, &v, &device);
+    if (rc) return rc;
+    if (!a) return refuse(L2_EINVAL, "%s: NULL arguments", who);
+    if ((rc = check_count(who, a->n, 1))) return rc;
+    if (a->rows < 0 || a->rows > L2_TREE_NODES * kPagesMaxCall)
+        return refuse(L2_EINVAL, "%s: rows = %d outside 0..%d", who, a->rows, L2_TREE_NODES * kPagesMaxCall);
+    if ((rc = check_ptr(who, "seqs", a->seqs, 4, &device)) || (rc = check_ptr(who, "starts", a->starts, 4, &device)) ||
+        (rc = check_ptr(who, "counts", a->counts, 4, &device)) || (a->rows && (rc = check_ptr(who, "path", a->path, 4, &device))))
+        return rc;
+    if (find && ((a->rows && ((rc = check_ptr(who, "tokens", a->tokens, 4, &device)) || (rc = check_ptr(who, "targets", a->targets, 4, &device)))) ||
+                 (a->parents && (rc = check_ptr(who, "parents", a->parents, 4, &device))) ||
+                 (a->next && (rc = check_ptr(who, "next", a->next, 4, &device)))))
+        return rc;
+    if (!find && (a->tokens || a->targets || a->parents || a->next))
+        return refuse(L2_EINVAL, "%s: tokens, targets, parents and next are NULL where the path is given", who);
+    DeviceGuard guard;
+    if (!guard.enter(device)) return refuse(L2_ECUDA, "%s: cannot use device %d", who, device);
+    PagesAccept k{};
+    k.seqs = a->seqs;
+    k.starts = a->starts;
+    k.n = a->n;
+    k.rows = a->rows;
+    k.find = find;
+    k.parents = a->parents;
+    k.tokens = a->tokens;
+    k.targets = a->targets;
+    k.path = a->path;
+    k.counts = a->counts;
+    k.next = a->next;
+    return finish(who, launch_pages_accept(v, k, static_cast<cudaStream_t>(cuda_stream)));
+}
+
+}  // namespace
+
+int l2_pages_accept(const L2Pages *pool, const L2PagesAccept *a, void *cuda_stream) {
+    return accept_rows("l2_pages_accept", pool, a, true, cuda_stream);
+}
+
+int l2_pages_keep(const L2Pages *pool, const L2PagesAccept *a, void *cuda_stream) {
+    return accept_rows("l2_pages_keep", pool, a, false, cuda_stream);
 }

@@ -3,7 +3,8 @@
 // What it computes ("run.c", argmax(), sample() and the main loop; "run.c
 // 逐行解讀" §6 Sampler: random_u32() and sample()), per sequence b of B:
 //   temperature == 0: the index of the first maximum of the logits; the
-//     generator is not advanced;
+//     generator is not advanced (the index of a row without any weight, all of
+//     it -inf, too, whatever the temperature);
 //   otherwise: one xorshift* draw from rng_state[b], whose top 24 bits k are
 //     the coin; the tempered softmax weights e_i = E(l_i / T - max_j l_j / T)
 //     held as the integers q_i = floor(e_i * 2^48); r = floor(k * S / 2^24)
@@ -161,6 +162,47 @@ __device__ u64 cta_exclusive_scan(u64 v, SampleScratch &sc) {
     return sc.part[warp] + incl - v;
 }
 
+// The index of the first maximum of a row, by its whole block.
+__device__ void first_maximum(const float *l, int V, SampleScratch &sc, int *out) {
+    const int tid = threadIdx.x;
+    // first maximum: larger value, or equal value at a lower index
+    float bv = -INFINITY;
+    int bi = 0x7fffffff;
+    for (int i = tid; i < V; i += kST) {
+        const float v = l[i];
+        if (v > bv || (v == bv && i < bi)) {
+            bv = v;
+            bi = i;
+        }
+    }
+    const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
+        const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
+        if (ov > bv || (ov == bv && oi < bi)) {
+            bv = ov;
+            bi = oi;
+        }
+    }
+    if (lane == 0) {
+        sc.fpart[warp] = bv;
+        sc.ipart[warp] = bi;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        float v = sc.fpart[0];
+        int i = sc.ipart[0];
+        for (int w = 1; w < kST / 32; ++w)
+            if (sc.fpart[w] > v || (sc.fpart[w] == v && sc.ipart[w] < i)) {
+                v = sc.fpart[w];
+                i = sc.ipart[w];
+            }
+        // all logits NaN: the pages' loop keeps index 0
+        *out = i == 0x7fffffff ? 0 : i;
+    }
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(kST, 1) sample_kernel(const SampleParams p) {
@@ -172,42 +214,7 @@ __global__ void __launch_bounds__(kST, 1) sample_kernel(const SampleParams p) {
     const float *l = p.logits + (size_t)b * V;
 
     if (p.temperature == 0.0f) {
-        // first maximum: larger value, or equal value at a lower index
-        float bv = -INFINITY;
-        int bi = 0x7fffffff;
-        for (int i = tid; i < V; i += kST) {
-            const float v = l[i];
-            if (v > bv || (v == bv && i < bi)) {
-                bv = v;
-                bi = i;
-            }
-        }
-        const int lane = tid & 31, warp = tid >> 5;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-            const int oi = __shfl_xor_sync(0xffffffffu, bi, o);
-            if (ov > bv || (ov == bv && oi < bi)) {
-                bv = ov;
-                bi = oi;
-            }
-        }
-        if (lane == 0) {
-            sc.fpart[warp] = bv;
-            sc.ipart[warp] = bi;
-        }
-        __syncthreads();
-        if (tid == 0) {
-            float v = sc.fpart[0];
-            int i = sc.ipart[0];
-            for (int w = 1; w < kST / 32; ++w)
-                if (sc.fpart[w] > v || (sc.fpart[w] == v && sc.ipart[w] < i)) {
-                    v = sc.fpart[w];
-                    i = sc.ipart[w];
-                }
-            // all logits NaN: the pages' loop keeps index 0
-            p.out[b] = i == 0x7fffffff ? 0 : i;
-        }
+        first_maximum(l, V, sc, p.out + b);
         return;
     }
 
@@ -236,6 +243,10 @@ __global__ void __launch_bounds__(kST, 1) sample_kernel(const SampleParams p) {
     u64 s_loc = 0;
     for (int i = i0; i < i1; ++i) s_loc += weight_of(ecache[slot(i)]);
     const u64 S = cta_sum(s_loc, sc);
+    if (S == 0) {  // every token is masked (-inf): there is nothing to draw from
+        first_maximum(l, V, sc, p.out + b);
+        return;
+    }
 
     const bool nucleus = p.topp > 0.0f && p.topp < 1.0f;
     if (!nucleus) {

@@ -12,7 +12,7 @@ import ctypes
 import math
 
 from . import _native
-from ._native import L2Pages, L2PagesAttention, L2PagesRows
+from ._native import L2Pages, L2PagesAccept, L2PagesAttention, L2PagesRows, L2PagesTreeAttention
 
 L2_F32, L2_BF16, L2_F16 = 0, 1, 2
 L2_PAGES_TIMEOUT, L2_PAGES_BAD_PAGE, L2_PAGES_BAD_CALL, L2_PAGES_FULL = 1, 2, 4, 8
@@ -83,7 +83,7 @@ class PagePool:
         rc = self._lib.l2_pages_init(self._ref)
         if rc:
             _raise(rc)
-        self._ws = {}  # workspace bytes per (rows, groups, heads)
+        self._ws = {}  # workspace bytes per call and its sizes
         self._torch, self._int32, self._index = torch, torch.int32, k.get_device()
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._scale = 1.0 / math.sqrt(self.head_size)
@@ -107,6 +107,37 @@ class PagePool:
                 or (st[-1] != 1 and shape[-1] > 1):
             raise ValueError(f"{name} must have {dims} dimensions, the pool's type, device and head size, its last one contiguous")
         return t.data_ptr(), shape, st
+
+    def _outputs(self, tree, sizes, q, out, lse, stream):
+        """Of an attention call (of trees): ``out`` (a new one, if None), whether it is new, its strides, workspace and its bytes."""
+        B, H, _ = q.shape
+        need = self._ws.get((tree, *sizes))
+        if need is None:
+            need = (self._lib.l2_pages_tree_attention_ws if tree else self._lib.l2_pages_attention_ws)(self._ref, *sizes)
+            if need < 0:
+                _raise(int(need))
+            self._ws[(tree, *sizes)] = need
+        torch = self._torch
+        fresh = out is None
+        if stream is None:
+            if fresh:
+                out = torch.empty((B, H, self.head_size), dtype=self.dtype, device=self.device)
+            ws = self._bytes.new_empty(need)
+        else:  # the workspace belongs to the stream that uses it
+            with torch.cuda.stream(stream):
+                if fresh:
+                    out = torch.empty((B, H, self.head_size), dtype=self.dtype, device=self.device)
+                ws = self._bytes.new_empty(need)
+        if fresh:
+            o_row, o_head = H * self.head_size, self.head_size
+        else:
+            _, o_shape, (o_row, o_head, _) = self._rows("out", out, 3)
+            if o_shape != q.shape:
+                raise ValueError("out must have q's shape")
+        if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != self._index or not lse.is_contiguous()
+                                or tuple(lse.shape) != (B, H)):
+            raise ValueError("lse must be a contiguous float32 tensor [rows][heads] of the pool's device")
+        return out, fresh, o_row, o_head, ws, need
 
     @staticmethod
     def _used_on(stream, *tensors):
@@ -190,32 +221,8 @@ class PagePool:
             gs, pl = self._ints("group_starts", group_starts), self._ints("prefix_lens", prefix_lens, G)
         elif prefix_lens is not None:
             raise ValueError("prefix_lens needs group_starts")
-        need = self._ws.get((B, G, H))
-        if need is None:
-            need = self._lib.l2_pages_attention_ws(self._ref, B, G, H)
-            if need < 0:
-                _raise(int(need))
-            self._ws[(B, G, H)] = need
-        torch = self._torch
-        fresh = out is None
-        if stream is None:
-            if fresh:
-                out = torch.empty((B, H, self.head_size), dtype=self.dtype, device=self.device)
-            ws = self._bytes.new_empty(need)
-        else:  # the workspace belongs to the stream that uses it
-            with torch.cuda.stream(stream):
-                if fresh:
-                    out = torch.empty((B, H, self.head_size), dtype=self.dtype, device=self.device)
-                ws = self._bytes.new_empty(need)
-        if fresh:
-            op, o_row, o_head = out.data_ptr(), H * self.head_size, self.head_size
-        else:
-            op, o_shape, (o_row, o_head, _) = self._rows("out", out, 3)
-            if o_shape != q.shape:
-                raise ValueError("out must have q's shape")
-        if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != self._index or not lse.is_contiguous()
-                                or tuple(lse.shape) != (B, H)):
-            raise ValueError("lse must be a contiguous float32 tensor [rows][heads] of the pool's device")
+        out, fresh, o_row, o_head, ws, need = self._outputs(False, (B, G, H), q, out, lse, stream)
+        op = out.data_ptr()
         a = L2PagesAttention(int(layer), B, G, H, qp, op, None if lse is None else lse.data_ptr(),
                              None if seqs is None else self._ints("seqs", seqs, B), gs, pl, q_st[0], q_st[1], o_row, o_head,
                              self._scale if scale is None else float(scale))
@@ -224,3 +231,56 @@ class PagePool:
             _raise(rc)
         self._used_on(stream, q, seqs, group_starts, prefix_lens, None if fresh else out, lse)
         return out
+
+    # -- drafted tokens --------------------------------------------------------
+    def tree_attention(self, q, layer: int, seqs, starts, parents=None, scale=None, out=None, lse=None, stream=None):
+        """Attention of drafted tokens: rows starts[i]..starts[i + 1] - 1 of ``q`` [rows][heads][head size] are the tree of
+        sequence seqs[i], whose last rows they are (appended in the same order); each attends to the committed rows
+        before them, to itself and to the tokens above it (``l2_pages_tree_attention``).  ``parents``: each row's parent
+        within its tree, -1 for none; without it the trees are chains.  ``lse`` and ``out`` as for attention."""
+        qp, (B, H, _), q_st = self._rows("q", q, 3)
+        n = len(seqs)
+        out, fresh, o_row, o_head, ws, need = self._outputs(True, (n, B, H), q, out, lse, stream)
+        a = L2PagesTreeAttention(int(layer), n, B, H, qp, out.data_ptr(), None if lse is None else lse.data_ptr(), self._ints("seqs", seqs),
+                                 self._ints("starts", starts, n + 1), None if parents is None else self._ints("parents", parents, B),
+                                 q_st[0], q_st[1], o_row, o_head, self._scale if scale is None else float(scale))
+        rc = self._lib.l2_pages_tree_attention(self._ref, ctypes.byref(a), ws.data_ptr(), need, self._stream(stream))
+        if rc:
+            _raise(rc)
+        self._used_on(stream, q, seqs, starts, parents, None if fresh else out, lse)
+        return out
+
+    def accept(self, tokens, targets, seqs, starts, parents=None, stream=None):
+        """Finds the path of each tree that the model agrees with and shortens the sequences to it (``l2_pages_accept``):
+        token 0, then the first child of each accepted token whose token is what was sampled from that one's logits
+        (``targets``).  Returns int32 tensors ``path`` (each tree's accepted places, then -1), ``counts`` and ``next`` (the target
+        of the last accepted token)."""
+        rows, n = len(tokens), len(seqs)
+        made = self._made(rows + 2 * n, stream)
+        path, counts, following = made[:rows], made[rows:rows + n], made[rows + n:]
+        a = L2PagesAccept(n, rows, self._ints("seqs", seqs), self._ints("starts", starts, n + 1),
+                          None if parents is None else self._ints("parents", parents, rows), self._ints("tokens", tokens),
+                          self._ints("targets", targets, rows), path.data_ptr(), counts.data_ptr(), following.data_ptr())
+        rc = self._lib.l2_pages_accept(self._ref, ctypes.byref(a), self._stream(stream))
+        if rc:
+            _raise(rc)
+        self._used_on(stream, tokens, targets, seqs, starts, parents)
+        return path, counts, following
+
+    def keep(self, path, counts, seqs, starts, stream=None):
+        """Shortens the sequences to given paths (``l2_pages_keep``): of the last starts[i + 1] - starts[i] rows of seqs[i],
+        those at places path[starts[i]] .. (counts[i] of them, ascending) stay, side by side."""
+        n = len(seqs)
+        a = L2PagesAccept(n, len(path), self._ints("seqs", seqs), self._ints("starts", starts, n + 1), None, None, None,
+                          self._ints("path", path), self._ints("counts", counts, n), None)
+        rc = self._lib.l2_pages_keep(self._ref, ctypes.byref(a), self._stream(stream))
+        if rc:
+            _raise(rc)
+        self._used_on(stream, path, counts, seqs, starts)
+
+    def _made(self, n, stream):
+        """n new integers, of the stream that writes them."""
+        if stream is None:
+            return self._torch.empty(n, dtype=self._int32, device=self.device)
+        with self._torch.cuda.stream(stream):
+            return self._torch.empty(n, dtype=self._int32, device=self.device)
