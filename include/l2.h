@@ -609,7 +609,7 @@ int l2_rope(const L2RopePlan *plan, const L2RopeRows *rows, void *cuda_stream);
  */
 typedef struct {
     int n_seqs, vocab_size;          /* vocab_size 1..2^24 */
-    int max_len;                     /* tokens a history has room for */
+    int max_len;                     /* tokens a history has room for, 0..2^24 - 256 */
     int n_bias;                      /* bias entries of all sequences; 0: none */
     long long history_stride;        /* ints, at least max_len */
     const int *history;              /* DEVICE [n_seqs][max_len] */

@@ -81,7 +81,7 @@ constexpr int kEarly = 8;  // rounds of parts' sums loaded before their weights 
 // NW warps per (row, query head) take the parts of its prefix and of its own keys in turn.  Lanes take a part each
 // for (m, l), so a warp's weights are known after one round of loads; LP lanes take a part's sums, the first kEarly
 // rounds of which are loaded beside (m, l).  Then the warps' results are joined in order.
-template <typename T, int NW>
+template <typename T, int NW, bool TREE>
 __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const PagesAttn p) {
     constexpr bool f32 = std::is_same<T, float>::value;
     constexpr int kRows = kMergeThreads / 32 / NW;  // (row, head) pairs a block
@@ -105,7 +105,9 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
     const int4 ow = rp[0], re = rp[1], tc = rp[2];
     const int4 in = rp[3];
     const int gr = in.x, per = h0.y;
-    if (!h0.z || in.y) return;
+    if (!h0.z || (TREE && in.y)) return;
+    const int shift = TREE ? p.pair_shift : 4, pairs = 1 << shift, start = TREE ? p.start : kItemCost;
+    static_assert(kM == 1 << 4, "pairs of an item");
     // first walker, parts and first row of the parts of the item that holds pair mi of a source of n pairs
     struct Range {
         int w0, n, row;
@@ -113,10 +115,10 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
     auto range = [&](const int4 &s, int mi, int n) {
         Range r = {};
         if (s.z) {
-            const int item = kvh * ((n + kM - 1) / kM) + mi / kM, u0 = s.x + item * (kItemCost + s.z * s.w);
+            const int item = kvh * ((n + pairs - 1) >> shift) + (mi >> shift), u0 = s.x + item * (start + s.z * s.w);
             r.w0 = walker_of(u0, per);
-            r.n = walker_of(u0 + tile_place(s.z - 1, kItemCost, s.w), per) - r.w0 + 1;
-            r.row = (s.y + item + r.w0) * kM + mi % kM;
+            r.n = walker_of(u0 + tile_place(s.z - 1, start, s.w), per) - r.w0 + 1;
+            r.row = ((s.y + item + r.w0) << shift) + (mi & (pairs - 1));
         }
         return r;
     };
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
             acc = p.tc_acc + at * p.head_size;
         } else {
             e -= tc_n;
-            const size_t at = (size_t)(e < rest.n ? rest.row + e * kM : own.row + (e - rest.n) * kM);
+            const size_t at = (size_t)(e < rest.n ? rest.row + (e << shift) : own.row + ((e - rest.n) << shift));
             ml = reinterpret_cast<const float2 *>(p.ws_ml) + at;
             acc = p.ws_acc + at * p.head_size;
         }
@@ -251,10 +253,11 @@ __global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const P
 
 namespace {
 
-int max_items(int B, int G, int n_heads, int n_kv_heads, bool tree) {
+// pairs: of an item
+int max_items(int B, int G, int n_heads, int n_kv_heads, bool tree, int pairs) {
     // prefix tiles: sum over groups of ceil(rows gq / 16) <= (B gq) / 16 + G
     const long long gq = heads_per_kv(n_heads, n_kv_heads);
-    const long long pre = G ? (B * gq) / kM + G : 0, own = tree ? 0 : B * ((gq + kM - 1) / kM);
+    const long long pre = G ? (B * gq) / pairs + G : 0, own = tree ? 0 : B * ((gq + kM - 1) / kM);
     return (int)((pre + own) * n_kv_heads);
 }
 
@@ -271,15 +274,21 @@ struct WsLayout {
 };
 WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms, bool tree) {
     WsLayout w;
-    w.parts = (size_t)max_items(B, G, n_heads, n_kv_heads, tree) + (size_t)num_sms * kWalkWarps;
+    const int team = tree ? team_of(B, G, n_heads, n_kv_heads) : 1;
+    w.parts = ((size_t)max_items(B, G, n_heads, n_kv_heads, tree, kM * team) + (size_t)num_sms * (kWalkWarps / team));
     const size_t tc = G ? tc_part_rows(B, n_heads, n_kv_heads, num_sms) : 0;
     w.plan = 0;
     w.ml = w.plan + align256(plan_bytes(B, G) + (size_t)B * sizeof(RowPlan));
-    w.acc = w.ml + align256(w.parts * kM * 8);
-    w.tc_ml = w.acc + align256(w.parts * kM * head_size * 4);
+    w.acc = w.ml + align256(w.parts * kM * team * 8);
+    w.tc_ml = w.acc + align256(w.parts * kM * team * head_size * 4);
     w.tc_acc = w.tc_ml + align256(tc * 8);
     w.bytes = w.tc_acc + align256(tc * head_size * 4);
     return w;
+}
+
+template <typename T, bool TREE>
+cudaError_t launch_merge(const PagesAttn &p, bool few, const cudaLaunchConfig_t &cfg) {
+    return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<T, 4, TREE> : attn_pages_merge_kernel<T, 1, TREE>, p);
 }
 
 }  // namespace
@@ -301,7 +310,14 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     p.max_parts = (int)w.parts;
     p.num_sms = num_sms;
     const bool f32 = p.dtype == L2_F32;
-    p.tile_shift = f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size);
+    p.team = p.tree ? team_of(p.B, p.G, p.n_heads, p.n_kv_heads) : 1;
+    if (p.tree)
+        p.tile_shift = f32 ? attn_tree_f32_shift(p.head_size, p.team) : attn_tree_16_shift(p.head_size, p.team);
+    else
+        p.tile_shift = f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size);
+    p.tile_units = 1 << (p.tile_shift - (f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size)));
+    p.pair_shift = p.team == 1 ? 4 : p.team == 2 ? 5 : 6;
+    p.start = item_cost(p.team);
     // whether any prefix of such a call could be one for the tensor cores; the plan decides for each
     p.tc = p.G && tc_worth(p, p.B * heads_per_kv(p.n_heads, p.n_kv_heads), p.max_pages * p.page_size) && (f32 || attn_pages_tc_supported(p));
     p.plan_in_block = (p.tree ? p.G <= kTreePlanInBlock : p.B + p.G <= kPlanInBlock) && !p.wide;
@@ -330,10 +346,8 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
     cfg.gridDim = dim3(few ? pairs : (pairs + 3) / 4);
     cfg.blockDim = dim3(kMergeThreads);
     cfg.dynamicSmemBytes = 0;
-    if (f32) return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<float, 4> : attn_pages_merge_kernel<float, 1>, p);
-    if (p.dtype == L2_BF16)
-        return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<__nv_bfloat16, 4> : attn_pages_merge_kernel<__nv_bfloat16, 1>, p);
-    return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<__half, 4> : attn_pages_merge_kernel<__half, 1>, p);
+    if (p.tree) return f32 ? launch_merge<float, true>(p, few, cfg) : p.dtype == L2_BF16 ? launch_merge<__nv_bfloat16, true>(p, few, cfg) : launch_merge<__half, true>(p, few, cfg);
+    return f32 ? launch_merge<float, false>(p, few, cfg) : p.dtype == L2_BF16 ? launch_merge<__nv_bfloat16, false>(p, few, cfg) : launch_merge<__half, false>(p, few, cfg);
 }
 
 }  // namespace l2

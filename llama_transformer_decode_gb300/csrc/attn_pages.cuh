@@ -89,7 +89,16 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n, bool f32) {  // of a
 // 1 GB of suffixes of head size 128 / 64: 168 / 167 us at 1 pair, 174 / 167 at 4, 210 / 220 at 8, 318 / 282 at 16.
 // Starting an item (its queries, its part) takes a warp 1.25 us where a tile takes 1.55.
 constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
+// A team of warps is one walker: while it starts an item, that many are idle.
+__host__ __device__ constexpr int item_cost(int team) { return kItemCost * team; }
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }
+// The same for teams, whose tiles keep their warps busier than HBM, since mma.sync then bounds them.  32 sequences of 8000 keys: bf16, 8 KV
+// heads of 128, 16 / 32 / 64 pairs with 1 / 2 / 4 warps 171 / 232 / 450 us; fp32, 8 of 3000 and 32 heads of 128: 246 / 369 / 720.
+__host__ __device__ __forceinline__ int tree_tile_cost(int dtype, int n, int team, int units) {
+    if (team == 1) return tile_cost(dtype, n);
+    return dtype == 0 ? (team == 2 ? 21 : 41) * units / 2 : (team == 2 ? 11 : 21) * units / 2;
+}
+constexpr int kMaxTreeTileCost = 41;
 // Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of reading 8 KB, 0.049 us an SM).  A 16-bit tile
 // alone, prefix 131072: head size 64, 1.0 to 1.4 us up to 128 pairs, 2.0 to 2.4 above; head size 128, 1.65 (reading) to 1.9, and 2.7
 // to 3.3.  Beside walkers, which take HBM, it is longer; over eleven calls with both, prefixes of 4096 to 16384, these costs
@@ -102,14 +111,23 @@ __host__ __device__ __forceinline__ int tc_cost(int n, int hs, bool f32) {
     return n > kTcRows ? (hs > 64 ? 60 : 38) : (hs > 64 ? 44 : 24);
 }
 
+// Warps of a walker's team where rows are drafted tokens: as many as 16 pairs each of a sequence's pairs ask for, on average (a call's host
+// side knows no more), up to 4.
+__host__ __device__ inline int team_of(int B, int G, int n_heads, int n_kv_heads) {
+    const long long pairs = (long long)B * cdiv(n_heads, n_kv_heads);
+    return pairs <= 16ll * G ? 1 : pairs <= 32ll * G ? 2 : 4;
+}
+
 // Whether the tensor-core role takes a prefix of so many keys that serves n pairs of a KV head.  Its blocks start slower (8 us to
 // the first parts where a walk has them after 4), so it takes what would keep the walkers for a while if all groups were alike:
 // in 16-bit caches 10 us of them all, in fp32 ones 1 us, since their split products walk slower.  Over 60 calls of 1 to 64
 // rows with prefixes of 16 to 12000, geometric means with no such limit and with this one: bf16 15.4 and 13.1 us, fp16 17.5 and 14.3;
 // with a limit eight times higher, one of 64 rows and five prefixes of up to 16390 took 40 us instead of 32.
 constexpr int kTcLeast16 = 40000, kTcLeast32 = 4000;
+// In a tree's call teams of warps take up to 32 pairs (fp32: 64) faster: 232 us against 278 in the calls above (32 pairs, bf16; 64 pairs: 450, 333),
+// in fp32 369 against 595 (64 pairs: 720, 706).
 __host__ __device__ __forceinline__ bool tc_worth(const PagesAttn &p, int n, int keys) {
-    return n > kM && (long long)cdiv(n, kM) * p.n_kv_heads * p.G * tile_cost(p.dtype, kM) * (keys >> p.tile_shift) >=
+    return n > (!p.tree ? kM : p.dtype == 0 ? 64 : 32) && (long long)cdiv(n, kM) * p.n_kv_heads * p.G * tile_cost(p.dtype, kM) * (keys >> p.tile_shift) >=
                          (p.dtype == 0 ? kTcLeast32 : kTcLeast16);
 }
 
@@ -147,12 +165,15 @@ struct alignas(16) WalkItem {
     int slot, n_tiles, left;          // item number of all, tiles, keys from the first tile on
     int row0, m0, pairs, head0, nh;   // rows, first pair, pairs, query heads head0 .. head0 + nh - 1 (trees: and 2^16 times the source's rows)
 };
-constexpr int kItems = 8;  // a ring of them a warp: the copies are at most four tiles, so four items, ahead
+constexpr int ring_items(int team) { return team > 1 ? 16 : 8; }  // a ring of them a warp: more than the tiles, so the items, that copies are ahead
 
 // The copies of a walking warp run through the tiles of its range in order, item after item, without a break: step()
 // copies one tile and finds the next, whose page ids then have a tile's time to arrive.
-template <int KT, int ROW, bool TREE>
+// TEAM (trees): so many warps share a tile, the `member`-th copying its part of the rows; an item has kM pairs for each.  Their walks
+// are the same.
+template <int KT, int ROW, bool TREE, int TEAM = 1>
 struct Walk {
+    static constexpr int kPairs = kM * TEAM, kStart = item_cost(TEAM), kItems = ring_items(TEAM);
     const int *table;
     long long head;       // byte offset of the KV head
     int src, x, x1;       // source, cost up to which tiles are found, end of the range
@@ -177,24 +198,24 @@ struct Walk {
         for (;; ++src) {
             if (x >= x1) break;
             const int4 a = *reinterpret_cast<const int4 *>(&pl.src[src].t0), b = *reinterpret_cast<const int4 *>(&pl.src[src].key0);
-            const int kt = a.z, cost = a.w, n = b.w * gq, tiles_m = (n + kM - 1) / kM;
+            const int kt = a.z, cost = a.w, n = b.w * gq, tiles_m = (n + kPairs - 1) / kPairs;
             if (kt == 0) continue;
             x = max(x, a.x);
-            const int len = kItemCost + kt * cost;
+            const int len = kStart + kt * cost;
             int item = (int)((unsigned)(x - a.x) / (unsigned)len), at = a.x + item * len;  // item of the source, its place
-            int k_first = x == at ? 0 : max(1, cdiv(max(x - at - kItemCost, 0), cost));
+            int k_first = x == at ? 0 : max(1, cdiv(max(x - at - kStart, 0), cost));
             if (k_first >= kt) {
                 ++item;
                 at += len;
                 k_first = 0;
             }
-            x = at + tile_place(k_first, kItemCost, cost);
+            x = at + tile_place(k_first, kStart, cost);
             if (item >= tiles_m * p.n_kv_heads) continue;
             if (x >= x1) break;
-            const int kvh = (int)((unsigned)item / (unsigned)tiles_m), m0 = (item - kvh * tiles_m) * kM;
-            const int end = min(kt, max(k_first + 1, cdiv(max(x1 - at - kItemCost, 0), cost)));
+            const int kvh = (int)((unsigned)item / (unsigned)tiles_m), m0 = (item - kvh * tiles_m) * kPairs;
+            const int end = min(kt, max(k_first + 1, cdiv(max(x1 - at - kStart, 0), cost)));
             rem = end - k_first;
-            x = end == kt ? at + len : at + tile_place(end, kItemCost, cost);
+            x = end == kt ? at + len : at + tile_place(end, kStart, cost);
             key = b.x + k_first * KT;
             key1 = b.y;
             head = kvh * p.head_stride;
@@ -204,7 +225,7 @@ struct Walk {
                 int4 *q = reinterpret_cast<int4 *>(queue + items % kItems);
                 q[0] = make_int4(a.y + item, rem, key1 - key, b.z);
                 const int nh = first_head(kvh + 1, p.n_heads, p.n_kv_heads) - h0;
-                q[1] = make_int4(m0, min(kM, n - m0), h0, TREE ? nh | b.w << 16 : nh);
+                q[1] = make_int4(m0, min(kPairs, n - m0), h0, TREE ? nh | b.w << 16 : nh);
             }
             key += threadIdx.x & 31;
             ++items;
@@ -218,7 +239,7 @@ struct Walk {
     // first call only finds the first.
     template <class Swz>
     __device__ __forceinline__ void step(const PagesAttn &p, const Plan &pl, int gq, int words, WalkItem *queue, uint32_t ks, uint32_t vs,
-                                         Swz swz) {
+                                         Swz swz, int member = 0) {
         if (on) {
             if (rem) {
                 constexpr int C = ROW / 16, RP = 32 / C;  // words a row, rows one instruction covers
@@ -232,8 +253,8 @@ struct Walk {
                         atomicOr(p.err, L2_DEV_ERR_BOUNDS);
                 }
 #pragma unroll
-                for (int r0 = 0; r0 < KT; r0 += RP) {
-                    const int r = r0 + rr;
+                for (int r0 = 0; r0 < KT / TEAM; r0 += RP) {
+                    const int r = (TEAM > 1 ? member * (KT / TEAM) : 0) + r0 + rr;
                     const long long o = __shfl_sync(0xffffffffu, off, r);
                     const bool in = o >= 0 && c < words;
                     const uint32_t d = r * ROW + ((c ^ swz(r)) << 4);
@@ -264,12 +285,14 @@ struct TreeItem {
     int n;
     u64 sees;
 };
-// The words are made where the item's last tile reaches the drafted rows.
+// The words are made where the item's last tile reaches the drafted rows.  w: the team's item, then its `member`-th warp's own pairs.
 template <int KT>
-__device__ __forceinline__ TreeItem tree_item(const PagesAttn &p, WalkItem &w, int gq) {
+__device__ __forceinline__ TreeItem tree_item(const PagesAttn &p, WalkItem &w, int gq, int member) {
     TreeItem t;
     t.n = w.nh >> 16;
     w.nh &= 0xffff;
+    w.m0 += kM * member;
+    w.pairs = max(0, min(kM, w.pairs - kM * member));
     t.sees = ~0ull;
     if (w.left - w.n_tiles * KT < t.n) {
         const TreeWords words = tree_words(tree_parents(p.parents ? p.parents + w.row0 : nullptr, t.n));
@@ -282,6 +305,15 @@ __device__ __forceinline__ TreeItem tree_item(const PagesAttn &p, WalkItem &w, i
 __device__ __forceinline__ unsigned tree_bits(u64 sees, int n, int left) {
     const int at = n - left;  // of the tile's first key among the drafted ones
     return at >= 0 ? (unsigned)(sees >> at) : at <= -32 ? ~0u : (unsigned)(sees << -at) | ((1u << -at) - 1u);
+}
+
+// Waits for the warps of a team (number `team` of its block's).
+template <int TEAM>
+__device__ __forceinline__ void team_sync(int team) {
+    if constexpr (TEAM == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");
 }
 
 // Walkers that are warps: neighbours in the numbering sit in different blocks, so that a stretch of costlier tiles

@@ -12,7 +12,7 @@ bool attn_pages_tc_supported(const PagesAttn &p) {
 }
 
 int attn_pages_16_shift(int hs) { return hs <= 64 ? 5 : 4; }
-static_assert(Shape<64>::KT == 1 << 5 && Shape<128>::KT == 1 << 4, "the plan counts tiles by shifts");
+static_assert(Shape<64, 1>::KT == 1 << 5 && Shape<128, 1>::KT == 1 << 4, "the plan counts tiles by shifts");
 
 cudaError_t launch_attn_pages_16(const PagesAttn &p, cudaLaunchConfig_t cfg) { return launch_16<false>(p, cfg); }
 

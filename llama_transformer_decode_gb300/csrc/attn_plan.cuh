@@ -7,14 +7,13 @@
 
 namespace l2 {
 
-// Least cost of a range: fewer than two tiles a warp cost more to write and merge as parts than the parallel reading gains.  (And
+// Least cost of a range, an item's start and two tiles: fewer cost more to write and merge as parts than the parallel reading gains.  (And
 // at least the distance of two tiles of any kind, see walker_of.)
-constexpr int kMinPer = kItemCost + 2 * kCostUnit;
 __device__ __forceinline__ int tc_min_per(int hs, bool f32) { return kTcItemCost + tc_cost(2 * kTcRows, hs, f32); }
 // An item of k tiles goes to sqrt(13 k) warps at most (48 for 180 tiles, 285 for 6250): with P warps they take k / P tiles each and
 // the merge P parts, a part a thirteenth of a tile's time, and that many make the sum least.
 constexpr float kSpread = 1.0f / 13.0f;
-static_assert(kMinPer >= kItemCost + kMaxTileCost, "every walker between an item's first and last must hold a tile of it");
+static_assert(2 * kCostUnit >= kMaxTileCost, "every walker between an item's first and last must hold a tile of it");
 
 template <int NT, int MAX>
 struct PlanScratch {
@@ -60,6 +59,8 @@ template <int NT, int MAX, bool TREE, bool WIDE = false>
 __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, PlanScratch<NT, MAX> &sc, bool report) {
     const int i = threadIdx.x, S = TREE ? p.G : p.G + p.B, gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const bool f32 = p.dtype == L2_F32;
+    // pairs and start of an item, tiles of 8 KB that one of its tiles is
+    const int pairs = TREE ? kM * p.team : kM, start = TREE ? item_cost(p.team) : kItemCost, units = TREE ? p.tile_units : 1;
     bool bad = false;
     int len = 0, seq = 0, P = 0, a0 = 0;
     constexpr int kOwn = TREE ? (kPagesMaxCall + NT - 1) / NT : 1;  // parents that a thread looks at
@@ -167,7 +168,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         if (!TREE && i < p.B) walk = cdiv(gq, kM) * (kItemCost + kMaxTileCost * tiles(len - (p.G ? sc.minlen[sc.group[i]] : 0)));
         if (i < p.G) {
             const int n = (sc.gstart[i + 1] - sc.gstart[i]) * gq;
-            walk += cdiv(n, kM) * (kItemCost + kMaxTileCost * tiles(TREE ? sc.len[i] : sc.minlen[i]));
+            walk += cdiv(n, pairs) * (start + (TREE ? kMaxTreeTileCost : kMaxTileCost) * tiles(TREE ? sc.len[i] : sc.minlen[i]));
             tc = tc_runs(n, f32) * (kTcItemCost + tc_cost(n, p.head_size, f32) * (long long)(sc.minlen[i] / tc_keys(f32)));
         }
         if (walk) atomicAdd(&sc.cost[0], (unsigned long long)walk * p.n_kv_heads);
@@ -218,11 +219,11 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
         }
         if (!TREE && e.rows > 0) e.seq = sc.seq[e.row0];
         e.kt = (e.key1 - e.key0 + (1 << p.tile_shift) - 1) >> p.tile_shift;
-        e.cost = tile_cost(p.dtype, min(e.rows * gq, kM));
-        const int items = e.kt ? (e.rows * gq + kM - 1) / kM * p.n_kv_heads : 0;
+        e.cost = TREE ? tree_tile_cost(p.dtype, min(e.rows * gq, kM), p.team, units) : tile_cost(p.dtype, min(e.rows * gq, kM));
+        const int items = e.kt ? (e.rows * gq + pairs - 1) / pairs * p.n_kv_heads : 0;
         if (items) atomicMax(&sc.spread, (int)((float)e.cost * sqrtf((float)e.kt * kSpread)));
         int2 here;
-        const int2 before = plan_scan<NT>(make_int2(items * (kItemCost + e.kt * e.cost), items), &here, sc.sums[1]);
+        const int2 before = plan_scan<NT>(make_int2(items * (start + e.kt * e.cost), items), &here, sc.sums[1]);
         e.t0 = all.x + before.x;
         e.i0 = all.y + before.y;
         if (s < S) pl.src[s] = e;
@@ -232,7 +233,9 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     }
     if (i == 0) {
         const int cost = all.x, tc = tc_all.x;
-        const RoleSplit r = split_roles(cost, tc, p.num_sms, kWalkWarps, max(kMinPer, sc.spread), tc_min_per(p.head_size, f32));
+        const int least = TREE ? max(2 * kCostUnit * units, tree_tile_cost(p.dtype, kM, p.team, units)) : 2 * kCostUnit;
+        const RoleSplit r = split_roles(cost, tc, p.num_sms, kWalkWarps / (TREE ? p.team : 1), max(start + least, sc.spread),
+                                        tc_min_per(p.head_size, f32));
         pl.src[S].t0 = cost;
         pl.hdr[kHdrCost] = cost;
         pl.hdr[kHdrPer] = r.per;

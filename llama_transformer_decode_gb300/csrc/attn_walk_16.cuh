@@ -73,19 +73,23 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
     return __vcmpeq2(v & T::kExponent, T::kExponent);
 }
 
-// Tile shape: HS the head size padded to 64 or 128; K and V of a tile's keys take 8 KB.
-template <int HS>
+// Tile shape: HS the head size padded to 64 or 128; K and V of a tile's keys take 8 KB, or of a team's 16 KB where heads are 128.  A team
+// has its warps' shared memory together, so more stages.
+template <int HS, int TEAM>
 struct Shape {
-    static constexpr int KT = HS == 128 ? 16 : 32;
+    static constexpr int KT = HS == 128 && TEAM == 1 ? 16 : 32;
     static constexpr int C = HS * 2 / 16;         // 16-byte words a row
     static constexpr int kRow = HS * 2;
     static constexpr int kStage = 2 * KT * kRow;  // K then V
-    static constexpr int kRings = kWalkWarps * kStages * kStage;
+    static constexpr int kRings = kWalkWarps * kStages * 8192;
+    static constexpr int kDepth = kStages * 8192 * TEAM / kStage;  // stages of a ring
+    static constexpr int kItems = ring_items(TEAM);
     static constexpr int kSmem = kRings + kWalkWarps * kItems * (int)sizeof(WalkItem);
+    static_assert(kDepth < kItems, "a walk's ring of items");
 };
 // Shared memory of either role, before the plan.
-template <int HS, bool TC>
-constexpr int kWork = TC && (int)TcShape<HS>::kSmem > Shape<HS>::kSmem ? (int)TcShape<HS>::kSmem : Shape<HS>::kSmem;
+template <int HS, bool TC, int TEAM>
+constexpr int kWork = TC && (int)TcShape<HS>::kSmem > Shape<HS, TEAM>::kSmem ? (int)TcShape<HS>::kSmem : Shape<HS, TEAM>::kSmem;
 
 // Word c of row r sits at word c ^ swz(r): the eight rows that one ldmatrix phase reads fall into
 // different banks.
@@ -95,16 +99,19 @@ __device__ __forceinline__ int swz(int r) { return r & 7; }
 // TREE: the rows are drafted tokens, and of the sequence's last keys a row sees its own path (see tree_bits).  What a row does not
 // see has no weight, but 0 times an infinity or NaN of V is NaN: tiles with drafted keys are looked through for such values, which then
 // stay out of the product and are added one by one to the rows that see them.
-template <typename T, int HS, bool TREE>
+// TEAM > 1: so many warps are one walker, with a ring together and 16 pairs each.  Where a sequence has more pairs than 16, each warp for itself
+// would bring the keys in anew (32 sequences of 8000 keys, 8 KV heads of 128: 171 us with 16 pairs, 323 with 32, 628 with 64).
+template <typename T, int HS, bool TREE, int TEAM>
 __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, unsigned char *smem, int warp, int block0) {
-    using Sh = Shape<HS>;
+    using Sh = Shape<HS, TEAM>;
     constexpr int KT = Sh::KT, C = Sh::C, NT = KT / 8;  // NT: n8 tiles of keys
-    const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3, wid = walker_id(warp, block0);
-    const uint32_t ring = smem_u32(smem) + warp * (kStages * Sh::kStage);
-    WalkItem *queue = reinterpret_cast<WalkItem *>(smem + Sh::kRings) + warp * kItems;
+    constexpr int kStages = Sh::kDepth;
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3, team = warp / TEAM, member = warp % TEAM, wid = walker_id(team, block0);
+    const uint32_t ring = smem_u32(smem) + team * (kStages * Sh::kStage);
+    WalkItem *queue = reinterpret_cast<WalkItem *>(smem + Sh::kRings) + warp * Sh::kItems;
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const int words = p.head_size / 8;  // 16-byte words of a row that exist
-    Walk<KT, Sh::kRow, TREE> walk;
+    Walk<KT, Sh::kRow, TREE, TEAM> walk;
     walk.start(p, pl, wid);
     float m_run[2], l_run[2], o[HS / 8][4];
     constexpr int QR = HS / 16 * 4;
@@ -115,16 +122,22 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
     // step s copies tile s - 1 and computes tile s - kStages
 #pragma unroll 1
     for (int step = 0;; ++step) {
+        if constexpr (TEAM > 1)
+            if (step >= kStages) {
+                // the next tile is here, and all of the team are done with the one whose stage is copied into
+                cp_wait<kStages - 2>();
+                team_sync<TEAM>(team);
+            }
         {
             const uint32_t st = ring + ((step + kStages - 1) % kStages) * Sh::kStage;
-            walk.step(p, pl, gq, words, queue, st, st + KT * Sh::kRow, swz);
+            walk.step(p, pl, gq, words, queue, st, st + KT * Sh::kRow, swz, member);
         }
         if (step < kStages) continue;
         if (step - kStages >= walk.issued) break;
         if (it == 0) {
             __syncwarp();  // the item was written by lane 0
-            w = queue[items++ % kItems];
-            if constexpr (TREE) tree = tree_item<KT>(p, w, gq);
+            w = queue[items++ % Sh::kItems];
+            if constexpr (TREE) tree = tree_item<KT>(p, w, gq, member);
             const char *qa = walk_query(p, w, g4, gq), *qb = walk_query(p, w, g4 + 8, gq);
             m_run[0] = m_run[1] = -CUDART_INF_F;
             l_run[0] = l_run[1] = 0.f;
@@ -156,8 +169,10 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
                 }
             }
         }
-        cp_wait<kStages - 1>();
-        __syncwarp();
+        if constexpr (TEAM == 1) {
+            cp_wait<kStages - 1>();
+            __syncwarp();
+        }
         const uint32_t ks_base = ring + (step % kStages) * Sh::kStage, vs_base = ks_base + KT * Sh::kRow;
         float s[NT][4];
 #pragma unroll
@@ -293,8 +308,9 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
                 const int mi = g4 + 8 * r;
                 if (mi >= w.pairs || slot >= p.max_parts) continue;
-                if (t4 == 0) reinterpret_cast<float2 *>(p.ws_ml)[(size_t)slot * kM + mi] = make_float2(m_run[r] - T::kLift, l);
-                float *dst = p.ws_acc + ((size_t)slot * kM + mi) * p.head_size;
+                const size_t at = (size_t)slot * (kM * TEAM) + kM * member + mi;
+                if (t4 == 0) reinterpret_cast<float2 *>(p.ws_ml)[at] = make_float2(m_run[r] - T::kLift, l);
+                float *dst = p.ws_acc + at * p.head_size;
 #pragma unroll
                 for (int i = 0; i < HS / 8; ++i) {
                     const int d = 8 * i + 2 * t4;
@@ -302,7 +318,7 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
                 }
             }
         }
-        __syncwarp();  // the stage is read before the next copy into it
+        if constexpr (TEAM == 1) __syncwarp();  // the stage is read before the next copy into it
     }
     cp_wait<0>();
 }
@@ -311,13 +327,13 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
 
 // TC: blocks below the plan's share take the tensor-core role, the others walk.  Calls that have no use for it have a kernel of
 // the walk alone, of fewer threads, which is up sooner.
-template <typename T, int HS, bool BF, bool TC, bool TREE>
+template <typename T, int HS, bool BF, bool TC, bool TREE, int TEAM>
 __global__ void __launch_bounds__(attn_threads(TC), 1) attn_pages_16_kernel(const __grid_constant__ TcAttn ta) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const PagesAttn &p = ta.p;
     pdl_launch_dependents();
     pdl_wait();
-    const Plan pl = plan_here<attn_threads(TC), TREE>(p, smem + kWork<HS, TC>, smem, blockIdx.x == 0);
+    const Plan pl = plan_here<attn_threads(TC), TREE>(p, smem + kWork<HS, TC, TEAM>, smem, blockIdx.x == 0);
     const int n_tc = TC ? pl.hdr[kHdrTcBlocks] : 0, warp = threadIdx.x / 32 - walk_first(TC);
     if constexpr (TC) {
         if ((int)blockIdx.x < n_tc) return tc_role<HS, BF>(ta, pl, smem, blockIdx.x);
@@ -328,7 +344,7 @@ __global__ void __launch_bounds__(attn_threads(TC), 1) attn_pages_16_kernel(cons
         }
         asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     }
-    walk_role<T, HS, TREE>(p, pl, smem, warp, n_tc);
+    walk_role<T, HS, TREE, TEAM>(p, pl, smem, warp, n_tc);
 }
 
 namespace {
@@ -349,10 +365,10 @@ bool encode_pages(CUtensorMap *m, const char *base, const PagesAttn &p, int rows
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int HS, bool BF, bool TC, bool TREE>
+template <typename T, int HS, bool BF, bool TC, bool TREE, int TEAM>
 cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
-    constexpr int bytes = kWork<HS, TC> + (int)kPlanSmem;
-    auto fn = attn_pages_16_kernel<T, HS, BF, TC, TREE>;
+    constexpr int bytes = kWork<HS, TC, TEAM> + (int)kPlanSmem;
+    auto fn = attn_pages_16_kernel<T, HS, BF, TC, TREE, TEAM>;
     static DeviceOnce once;
     cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes, TC ? 168 : 0);
     if (e != cudaSuccess) return e;
@@ -363,7 +379,11 @@ cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
 }
 template <typename T, int HS, bool BF, bool TREE>
 cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
-    return ta.p.tc ? launch<T, HS, BF, true, TREE>(ta, cfg) : launch<T, HS, BF, false, TREE>(ta, cfg);
+    if constexpr (TREE) {
+        if (ta.p.team == 4) return ta.p.tc ? launch<T, HS, BF, true, true, 4>(ta, cfg) : launch<T, HS, BF, false, true, 4>(ta, cfg);
+        if (ta.p.team == 2) return ta.p.tc ? launch<T, HS, BF, true, true, 2>(ta, cfg) : launch<T, HS, BF, false, true, 2>(ta, cfg);
+    }
+    return ta.p.tc ? launch<T, HS, BF, true, TREE, 1>(ta, cfg) : launch<T, HS, BF, false, TREE, 1>(ta, cfg);
 }
 
 template <bool TREE>

@@ -31,22 +31,27 @@ namespace {
 
 constexpr int kStagesF = 2;  // tiles of a warp's ring; shared memory holds the queries of 16 pairs beside it
 
-template <int HS>
+// A team of warps has their rings' memory together, and tiles of twice the keys where heads are large.
+template <int HS, int TEAM>
 struct ShapeF {
-    static constexpr int KT = HS == 128 ? 8 : HS == 64 ? 16 : 32;
+    static constexpr int KT = HS == 128 ? (TEAM > 1 ? 16 : 8) : HS == 64 ? (TEAM > 1 ? 32 : 16) : 32;
     static constexpr int C = HS / 4;              // 16-byte words a row
     static constexpr int kRow = HS * 4;
     static constexpr int kStage = 2 * KT * kRow;  // K then V
+    static constexpr int kRing = kStagesF * 8192; // of a warp
+    static constexpr int kDepth = kRing * TEAM / kStage;
     static constexpr int kQ = kM * kRow;          // queries
     static constexpr int kS = KT * 8 * 4;         // scores, then weights [key][pair]
-    static constexpr int kWarp = kStagesF * kStage + kQ + kS + kM * 4 + kItems * (int)sizeof(WalkItem);
-    static constexpr int kSmem = kWalkWarps * kWarp;
+    static constexpr int kItems = ring_items(TEAM);
+    static constexpr int kOwn = kQ + kS + kM * 4 + kItems * (int)sizeof(WalkItem);
+    static_assert(kDepth < kItems, "a walk's ring of items");
+    static constexpr int kSmem = kWalkWarps * (kRing + kOwn);
 };
 // Head size of the tensor-core role, and the shared memory of either role, before the plan.
 template <int HS>
 constexpr int kTcHead = HS > 64 ? 128 : 64;
-template <int HS, bool TC>
-constexpr int kWorkF = TC && (int)Tc32Shape<kTcHead<HS>>::kSmem > ShapeF<HS>::kSmem ? (int)Tc32Shape<kTcHead<HS>>::kSmem : ShapeF<HS>::kSmem;
+template <int HS, bool TC, int TEAM>
+constexpr int kWorkF = TC && (int)Tc32Shape<kTcHead<HS>>::kSmem > ShapeF<HS, TEAM>::kSmem ? (int)Tc32Shape<kTcHead<HS>>::kSmem : ShapeF<HS, TEAM>::kSmem;
 
 // Word c of row r sits at word c ^ swzf(r): two rows by four words, or one row by eight, fall into different banks.
 __device__ __forceinline__ int swzf(int r) { return ((r & 1) << 2) | ((r >> 1) & 3); }
@@ -96,10 +101,10 @@ struct StateF {
 
 // One tile of an item of at most R pairs: left keys from its first on.  TREE: some of them are drafted, and pair i sees those with a bit in lane
 // i's word.  A weight of -1 then stands for a key that a pair does not see: 0 would not do, its row of V may hold infinities or NaN.
-template <int HS, int R, bool TREE>
+template <int HS, int TEAM, int R, bool TREE>
 __device__ __forceinline__ void tile_f32(StateF<HS> &st, const unsigned char *ks, const unsigned char *qs, float *ss, float *cs, int left,
                                          float scale_log2, unsigned bits) {
-    using Sh = ShapeF<HS>;
+    using Sh = ShapeF<HS, TEAM>;
     constexpr int KT = Sh::KT, C = Sh::C;
     using Sp = Split<KT, R>;
     constexpr int A = Sp::A, Q = Sp::Q, D = Sp::D;
@@ -250,10 +255,10 @@ __device__ __forceinline__ float4 finite_only(float4 x) {
 // One tile of an item of more than 8 pairs, which are the rows of the products.  The sums of rows g4 and g4 + 8 live in
 // st.acc as n8 tiles; m2, l2: their softmax state.
 // TREE: as above; infinities and NaN of V stay out of the products and are added one by one to the rows that see them.
-template <int HS, bool TREE>
+template <int HS, int TEAM, bool TREE>
 __device__ __forceinline__ void tile_mma(StateF<HS> &st, float *m2, float *l2, const unsigned char *ks, const unsigned char *qs, int left,
                                          float scale_log2, unsigned bits) {
-    using Sh = ShapeF<HS>;
+    using Sh = ShapeF<HS, TEAM>;
     constexpr int KT = Sh::KT, NT = KT / 8;
     const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
     const unsigned char *vs = ks + KT * Sh::kRow;
@@ -429,35 +434,41 @@ __device__ __forceinline__ void tile_mma(StateF<HS> &st, float *m2, float *l2, c
 }
 
 // The walk of one warp: number `warp` of its block's, whose first walking one is block0.
-template <int HS, bool TREE>
+template <int HS, bool TREE, int TEAM>
 __device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, unsigned char *smem, int warp, int block0) {
-    using Sh = ShapeF<HS>;
-    constexpr int KT = Sh::KT, C = Sh::C;
-    const int lane = threadIdx.x & 31, wid = walker_id(warp, block0);
-    unsigned char *ring = smem + warp * Sh::kWarp, *qs = ring + kStagesF * Sh::kStage;
+    using Sh = ShapeF<HS, TEAM>;
+    constexpr int KT = Sh::KT, C = Sh::C, kStages = Sh::kDepth;
+    const int lane = threadIdx.x & 31, team = warp / TEAM, member = warp % TEAM, wid = walker_id(team, block0);
+    unsigned char *ring = smem + team * (TEAM * Sh::kRing), *qs = smem + kWalkWarps * Sh::kRing + warp * Sh::kOwn;
     float *ss = reinterpret_cast<float *>(qs + Sh::kQ), *cs = ss + Sh::kS / 4;
     WalkItem *queue = reinterpret_cast<WalkItem *>(cs + kM);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads), words = p.head_size / 4;
-    Walk<KT, Sh::kRow, TREE> walk;
+    Walk<KT, Sh::kRow, TREE, TEAM> walk;
     walk.start(p, pl, wid);
     StateF<HS> st;
     float m2[2], l2[2];
     WalkItem w = {};
     TreeItem tree = {};
     int it = 0, items = 0;  // tile within the item, items taken
-    // step s copies tile s - 1 and computes tile s - kStagesF
+    // step s copies tile s - 1 and computes tile s - kStages
 #pragma unroll 1
     for (int step = 0;; ++step) {
+        if constexpr (TEAM > 1)
+            if (step >= kStages) {
+                // the next tile is here, and all of the team are done with the one whose stage is copied into
+                cp_wait<kStages - 2>();
+                team_sync<TEAM>(team);
+            }
         {
-            const uint32_t to = smem_u32(ring) + ((step + kStagesF - 1) % kStagesF) * Sh::kStage;
-            walk.step(p, pl, gq, words, queue, to, to + KT * Sh::kRow, swzf);
+            const uint32_t to = smem_u32(ring) + ((step + kStages - 1) % kStages) * Sh::kStage;
+            walk.step(p, pl, gq, words, queue, to, to + KT * Sh::kRow, swzf, member);
         }
-        if (step < kStagesF) continue;
-        if (step - kStagesF >= walk.issued) break;
+        if (step < kStages) continue;
+        if (step - kStages >= walk.issued) break;
         if (it == 0) {
             __syncwarp();  // the item was written by lane 0
-            w = queue[items++ % kItems];
-            if constexpr (TREE) tree = tree_item<KT>(p, w, gq);
+            w = queue[items++ % Sh::kItems];
+            if constexpr (TREE) tree = tree_item<KT>(p, w, gq, member);
             const int n = w.pairs <= 8 ? 8 : kM;
 #pragma unroll 1
             for (int e = lane; e < n * C; e += 32) {
@@ -473,22 +484,22 @@ __device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, uns
 #pragma unroll
             for (int r = 0; r < (HS / 8 > 8 ? HS / 8 : 8); ++r) st.acc[r][0] = st.acc[r][1] = make_float2(0.f, 0.f);
         }
-        cp_wait<kStagesF - 1>();
+        if constexpr (TEAM == 1) cp_wait<kStages - 1>();
         __syncwarp();
-        const unsigned char *ks = ring + (step % kStagesF) * Sh::kStage;
+        const unsigned char *ks = ring + (step % kStages) * Sh::kStage;
         const int left = w.left - it * KT;
         auto tile = [&](auto drafted, unsigned bits) {
             constexpr bool D = decltype(drafted)::value;
             if (w.pairs <= 1)
-                tile_f32<HS, 1, D>(st, ks, qs, ss, cs, left, p.scale_log2, bits);
+                tile_f32<HS, TEAM, 1, D>(st, ks, qs, ss, cs, left, p.scale_log2, bits);
             else if (w.pairs <= 2)
-                tile_f32<HS, 2, D>(st, ks, qs, ss, cs, left, p.scale_log2, bits);
+                tile_f32<HS, TEAM, 2, D>(st, ks, qs, ss, cs, left, p.scale_log2, bits);
             else if (w.pairs <= 4)
-                tile_f32<HS, 4, D>(st, ks, qs, ss, cs, left, p.scale_log2, bits);
+                tile_f32<HS, TEAM, 4, D>(st, ks, qs, ss, cs, left, p.scale_log2, bits);
             else if (w.pairs <= 8)
-                tile_f32<HS, 8, D>(st, ks, qs, ss, cs, left, p.scale_log2, bits);
+                tile_f32<HS, TEAM, 8, D>(st, ks, qs, ss, cs, left, p.scale_log2, bits);
             else
-                tile_mma<HS, D>(st, m2, l2, ks, qs, left, p.scale_log2, bits);
+                tile_mma<HS, TEAM, D>(st, m2, l2, ks, qs, left, p.scale_log2, bits);
         };
         if (TREE && left - KT < tree.n)  // the tile reaches drafted keys
             tile(std::integral_constant<bool, TREE>(), tree_bits(tree.sees, tree.n, left));
@@ -498,8 +509,8 @@ __device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, uns
             // the part
             it = 0;
             const int slot = w.slot + wid;
-            float2 *ml = reinterpret_cast<float2 *>(p.ws_ml) + (size_t)slot * kM;
-            float *to = p.ws_acc + (size_t)slot * kM * p.head_size;
+            float2 *ml = reinterpret_cast<float2 *>(p.ws_ml) + (size_t)slot * (kM * TEAM) + kM * member;
+            float *to = p.ws_acc + ((size_t)slot * (kM * TEAM) + kM * member) * p.head_size;
             if (slot >= p.max_parts) {
             } else if (w.pairs <= 8) {
                 const int R = w.pairs <= 1 ? 1 : w.pairs <= 2 ? 2 : w.pairs <= 4 ? 4 : 8, LP = 32 / R;
@@ -549,12 +560,12 @@ __device__ __forceinline__ void walk_f32(const PagesAttn &p, const Plan &pl, uns
 
 // TC: blocks below the plan's share take the tensor-core role, the others walk.  Calls that have no use for it have a kernel of
 // the walk alone, of fewer threads, which is up sooner.
-template <int HS, bool TC, bool TREE>
+template <int HS, bool TC, bool TREE, int TEAM>
 __global__ void __launch_bounds__(attn_threads(TC), 1) attn_pages_f32_kernel(const __grid_constant__ PagesAttn p) {
     extern __shared__ __align__(1024) unsigned char smem[];
     pdl_launch_dependents();
     pdl_wait();
-    const Plan pl = plan_here<attn_threads(TC), TREE>(p, smem + kWorkF<HS, TC>, smem, blockIdx.x == 0);
+    const Plan pl = plan_here<attn_threads(TC), TREE>(p, smem + kWorkF<HS, TC, TEAM>, smem, blockIdx.x == 0);
     const int n_tc = TC ? pl.hdr[kHdrTcBlocks] : 0, warp = threadIdx.x / 32 - walk_first(TC);
     if constexpr (TC) {
         if ((int)blockIdx.x < n_tc) return tc32_role<kTcHead<HS>>(p, pl, smem, blockIdx.x);
@@ -565,14 +576,15 @@ __global__ void __launch_bounds__(attn_threads(TC), 1) attn_pages_f32_kernel(con
         }
         asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     }
-    walk_f32<HS, TREE>(p, pl, smem, warp, n_tc);
+    walk_f32<HS, TREE, TEAM>(p, pl, smem, warp, n_tc);
 }
 
 namespace {
-template <int HS, bool TC, bool TREE>
+template <int HS, bool TC, bool TREE, int TEAM>
 cudaError_t launch(const PagesAttn &p, cudaLaunchConfig_t cfg) {
-    constexpr int bytes = kWorkF<HS, TC> + (int)kPlanSmem;
-    auto fn = attn_pages_f32_kernel<HS, TC, TREE>;
+    constexpr int bytes = kWorkF<HS, TC, TEAM> + (int)kPlanSmem;
+    static_assert(bytes <= 227 * 1024, "shared memory of a block");
+    auto fn = attn_pages_f32_kernel<HS, TC, TREE, TEAM>;
     static DeviceOnce once;
     cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes, TC ? 168 : 0);
     if (e != cudaSuccess) return e;
@@ -583,7 +595,11 @@ cudaError_t launch(const PagesAttn &p, cudaLaunchConfig_t cfg) {
 }
 template <int HS, bool TREE>
 cudaError_t launch(const PagesAttn &p, cudaLaunchConfig_t cfg) {
-    return p.tc ? launch<HS, true, TREE>(p, cfg) : launch<HS, false, TREE>(p, cfg);
+    if constexpr (TREE) {
+        if (p.team == 4) return p.tc ? launch<HS, true, true, 4>(p, cfg) : launch<HS, false, true, 4>(p, cfg);
+        if (p.team == 2) return p.tc ? launch<HS, true, true, 2>(p, cfg) : launch<HS, false, true, 2>(p, cfg);
+    }
+    return p.tc ? launch<HS, true, TREE, 1>(p, cfg) : launch<HS, false, TREE, 1>(p, cfg);
 }
 
 template <bool TREE>

@@ -54,8 +54,9 @@ struct PagesAccept {
     const int *parents;              // [rows] or nullptr (chains)
     const int *tokens, *targets;     // [rows]
     int *path, *counts, *next;       // [rows], [n], [n] or nullptr
+    bool move_here;                  // set by the launch: one block does it all
 };
-cudaError_t launch_pages_accept(const PagesView &p, const PagesAccept &a, cudaStream_t s);
+cudaError_t launch_pages_accept(const PagesView &p, PagesAccept a, cudaStream_t s);
 
 // Raises a kernel's shared-memory limit once per device (the attribute outlives the call).  least_regs: registers a thread it
 // must have been compiled to, where it hands them around between its warps.
@@ -106,6 +107,8 @@ struct PagesAttn {
     int max_parts;            // parts the workspace holds
     int num_sms;              // blocks
     int tile_shift;           // log2 of the keys of a warp's tile
+    int team, tile_units;     // warps that walk together (1 but for trees), 8 KB that their tile is
+    int pair_shift, start;    // log2 of the pairs of an item, cost of its start
     bool tc;                  // prefixes may go to the tensor cores
     bool plan_in_block;       // every block plans for itself (no plan kernel before)
     bool wide;                // sequences as long as their tables would overflow the plan's 32 bits
@@ -115,6 +118,8 @@ struct PagesAttn {
 // Its kernels over 16-bit caches (attn_pages_16.cu) and fp32 caches (attn_pages_f32.cu): the logarithm of the keys of a
 // warp's tile; whether 16-bit pages allow tensor-core tiles (fp32 pages all do).
 int attn_pages_16_shift(int head_size);
+int attn_tree_16_shift(int head_size, int team);
+int attn_tree_f32_shift(int head_size, int team);
 bool attn_pages_tc_supported(const PagesAttn &p);
 cudaError_t launch_attn_pages_16(const PagesAttn &p, cudaLaunchConfig_t cfg);
 int attn_pages_f32_shift(int head_size);

@@ -23,7 +23,7 @@ struct RopeParams {
     // filled in by the launch
     int per_head[2];             // a head's units: pieces of `width` elements (or pairs) that turn, then pieces to copy
     int units;                   // of a row, both sides
-    int rows_per, splits;        // rows of a block, or blocks of a row
+    int splits, part, abreast;   // blocks of a row, units of each, rows side by side in one
     unsigned long long turns[kRopePairs];  // 2^64 times the turns that one position adds to each pair, mod 2^64
 };
 // half: pair i is elements i and i + rot / 2 (else 2 i and 2 i + 1); width: elements an access may take (1, 2, 4 or 8; at most
@@ -51,7 +51,7 @@ struct RulesParams {
     // filled in by the launch
     int slice, rows_per;         // tokens and rows of a block
 };
-// vec: four elements an access, which every row's address allows.
-cudaError_t launch_rules(RulesParams p, int dtype, bool out_f32, bool vec, int num_sms, cudaStream_t s);
+// vec: elements an access (1, 4, or 8 of 16 bits), which every row's address allows.
+cudaError_t launch_rules(RulesParams p, int dtype, bool out_f32, int vec, int num_sms, cudaStream_t s);
 
 }  // namespace l2

@@ -183,8 +183,8 @@ int attn_rows(const char *who, const L2Pages *pool, const PagesView &v, int laye
     return L2_OK;
 }
 
-// Most that an item costs in the plan: as many keys as a table has room for, in tiles of 8 that cost 7.
-long long longest_item(const PagesView &v) { return (((long long)v.max_pages * v.page_size + 7) / 8) * 7 + 128; }
+// Most that an item costs in the plan: as many keys as a table has room for, in tiles of 8 that cost 7 (a team's of 16: 41).
+long long longest_item(const PagesView &v, bool tree) { return (((long long)v.max_pages * v.page_size + 7) / 8) * (tree ? 21 : 7) + 128; }
 
 int attn_launch(const char *who, const PagesAttn &k, int device, void *ws, long long ws_bytes, void *cuda_stream) {
     DeviceGuard guard;
@@ -273,7 +273,7 @@ int l2_pages_attention(const L2Pages *pool, const L2PagesAttention *a, void *ws,
     k.G = a->G;
     // a bound of the plan's costs: own keys and prefixes
     const long long gq = (k.n_heads + k.n_kv_heads - 1) / k.n_kv_heads, items = 2ll * k.B * ((gq + 15) / 16 + 1) * k.n_kv_heads;
-    k.wide = items * longest_item(v) > 1ll << 30;
+    k.wide = items * longest_item(v, false) > 1ll << 30;
     return attn_launch(who, k, device, ws, ws_bytes, cuda_stream);
 }
 
@@ -310,7 +310,7 @@ int l2_pages_tree_attention(const L2Pages *pool, const L2PagesTreeAttention *a, 
     k.G = a->n;
     // as above: all rows' pairs in items of 16, one more for each sequence
     const long long gq = (k.n_heads + k.n_kv_heads - 1) / k.n_kv_heads, items = (k.B * gq / 16 + k.G) * k.n_kv_heads;
-    k.wide = items * longest_item(v) > 1ll << 30;
+    k.wide = items * longest_item(v, true) > 1ll << 30;
     return attn_launch(who, k, device, ws, ws_bytes, cuda_stream);
 }
 

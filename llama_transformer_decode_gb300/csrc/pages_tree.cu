@@ -23,6 +23,8 @@ namespace {
 constexpr int kT = kPagesThreads;
 constexpr int kMoveThreads = 256;
 constexpr int kBatch = 8;
+// Up to so many words of a position, of all sequences, the first kernel moves them itself: a launch less.
+constexpr int kMoveHere = 4096;
 
 __device__ __forceinline__ int ceil_div_d(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ bool page_ok(const PagesView &p, int page) { return page >= 0 && page < p.n_pages; }
@@ -53,11 +55,36 @@ __device__ __forceinline__ u64 walk_path(const TreeParents &t, const int *tokens
     return path;
 }
 
+// Byte offset, in a (layer, K or V, head), of a sequence's row.
+__device__ __forceinline__ long long row_offset(const PagesView &p, int s, int pos) {
+    const int col = (int)((unsigned)pos / (unsigned)p.page_size);
+    return p.table[(size_t)s * p.max_pages + col] * p.page_stride + (pos - col * p.page_size) * p.row_stride;
+}
+
+// Moves word u of all (layer, K or V, head) words along a path of c tokens whose first `stay` are where they were.
+template <class From, class To>
+__device__ __forceinline__ void move_word(const PagesView &p, long long u, int stay, int c, From from, To to) {
+    const int vh = p.row_bytes >> 4, words = vh * p.n_kv_heads;
+    const int w = (int)(u % words), lv = (int)(u / words), h = w / vh;
+    char *pool = (lv & 1 ? p.v : p.k) + (lv >> 1) * p.layer_stride + h * p.head_stride + ((w - h * vh) << 4);
+#pragma unroll 1
+    for (int j0 = stay; j0 < c; j0 += kBatch) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (j0 + j < c) x[j] = *reinterpret_cast<const uint4 *>(pool + from(j0 + j));
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (j0 + j < c) *reinterpret_cast<uint4 *>(pool + to(j0 + j)) = x[j];
+    }
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, const PagesAccept a) {
     __shared__ int sq[kPagesMaxCall], first_s[kPagesMaxCall], n_s[kPagesMaxCall], len_s[kPagesMaxCall], last_s[kPagesMaxCall], why;
     __shared__ u64 path_s[kPagesMaxCall];
+    __shared__ long long from[kTreeNodes], to[kTreeNodes];  // byte offsets of rows, where this block moves them
     const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
     pdl_launch_dependents();
     pdl_wait();
@@ -171,6 +198,19 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
         }
     }
     if (i == 0) p.scratch[kScrRefused] = 0;
+    if (!a.move_here) return;
+    // little to move: this block does it
+    const int words = 2 * p.n_layers * p.n_kv_heads * (p.row_bytes >> 4);
+    for (int e = 0; e < a.n; ++e) {
+        const u64 path = path_s[e];
+        const int n = n_s[e], c = __popcll(path), s0 = sq[e], base = len_s[e] - n, stay = min(c, __ffsll(~path) - 1);
+        if (c == n || stay == c) continue;
+        __syncthreads();  // the offsets before are read
+        if (i < n && (path >> i & 1)) from[__popcll(path & ((1ull << i) - 1))] = row_offset(p, s0, base + i);
+        if (i < c) to[i] = row_offset(p, s0, base + i);
+        __syncthreads();
+        for (int u = i; u < words; u += kT) move_word(p, u, stay, c, [&](int j) { return from[j]; }, [&](int j) { return to[j]; });
+    }
 }
 
 // Block (x, i) moves its share of the words of sequence seqs[i]'s rows.
@@ -188,33 +228,18 @@ __global__ void __launch_bounds__(kMoveThreads) pages_accept_move_kernel(const P
     __syncthreads();
     if (tid < c) {
         const int x = a.path[first + tid];
-        auto offset = [&](int pos) {
-            const int col = pos / p.page_size;
-            return p.table[(size_t)s * p.max_pages + col] * p.page_stride + (pos - col * p.page_size) * p.row_stride;
-        };
-        from[tid] = offset(base + x);
-        to[tid] = offset(base + tid);
+        from[tid] = row_offset(p, s, base + x);
+        to[tid] = row_offset(p, s, base + tid);
         if (x != tid) atomicMin(&stay_s, tid);  // from here on rows move: the path is ascending
     }
     __syncthreads();
-    const int vh = p.row_bytes >> 4, words = vh * p.n_kv_heads;
     const long long u = (long long)blockIdx.x * kMoveThreads + tid;
-    if (u >= 2ll * p.n_layers * words) return;
-    const int w = (int)(u % words), lv = (int)(u / words), h = w / vh;
-    char *pool = (lv & 1 ? p.v : p.k) + (lv >> 1) * p.layer_stride + h * p.head_stride + ((w - h * vh) << 4);
-#pragma unroll 1
-    for (int j0 = stay_s; j0 < c; j0 += kBatch) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (j0 + j < c) x[j] = *reinterpret_cast<const uint4 *>(pool + from[j0 + j]);
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (j0 + j < c) *reinterpret_cast<uint4 *>(pool + to[j0 + j]) = x[j];
-    }
+    if (u < 2ll * p.n_layers * p.n_kv_heads * (p.row_bytes >> 4)) move_word(p, u, stay_s, c, [&](int j) { return from[j]; }, [&](int j) { return to[j]; });
 }
 
-cudaError_t launch_pages_accept(const PagesView &p, const PagesAccept &a, cudaStream_t s) {
+cudaError_t launch_pages_accept(const PagesView &p, PagesAccept a, cudaStream_t s) {
+    const long long words = 2ll * p.n_layers * p.n_kv_heads * (p.row_bytes >> 4);
+    a.move_here = words * a.n <= kMoveHere;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kT);
@@ -225,8 +250,7 @@ cudaError_t launch_pages_accept(const PagesView &p, const PagesAccept &a, cudaSt
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, pages_accept_kernel, p, a);
-    if (e != cudaSuccess || a.rows == 0) return e;
-    const long long words = 2ll * p.n_layers * p.n_kv_heads * (p.row_bytes >> 4);
+    if (e != cudaSuccess || a.rows == 0 || a.move_here) return e;
     cfg.gridDim = dim3((unsigned)((words + kMoveThreads - 1) / kMoveThreads), a.n);
     cfg.blockDim = dim3(kMoveThreads);
     return cudaLaunchKernelEx(&cfg, pages_accept_move_kernel, p, a);

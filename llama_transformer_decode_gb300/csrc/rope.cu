@@ -10,11 +10,12 @@
 // is that part exactly, for positions of either sign, and the fraction's own rounding (2^-53 of f) is all that is lost.
 // The high bits as fp32 half-turns go to sincospif: an angle in [-pi, pi] off by at most 2^-24 of itself.
 //
-// How.  HBM bounds it (every element is read and written once; 16384 rows of 32 + 4 heads of 64 in fp16: see the launch below), at a
-// few rows the latency of one launch.  A unit is one access of 16 bytes (two, half a turning part apart, where pairs are
-// halves), the whole head's, side after side.  A block takes the units of some rows, or a part of one row's; its
-// threads load their units first, then make the rows' cosines and sines, once for all heads, in shared memory, while those
-// loads are on their way.  Where sizes or addresses do not allow 16 bytes, accesses are of 8, 4 or of single elements.
+// How.  HBM bounds it (every element is read and written once), at a few rows the latency of one launch.  A unit is one access of
+// 16 bytes (two, half a turning part apart, where pairs are halves) of a head.  A thread has one unit of the row, side after side, head
+// after head, and takes it in several rows: where it is, is worked out once (unit by unit over rows and heads the divisions took
+// longer than HBM: 16384 rows of 32 + 4 heads of 64 in fp16 took 48 us).  Threads load their units first, then make the rows'
+// cosines and sines, once for all heads, in shared memory, while those loads are on their way.  Where sizes or addresses do
+// not allow 16 bytes, accesses are of 8, 4 or of single elements.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,8 +29,9 @@ namespace l2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;      // most units a thread holds
-constexpr int kMaxRows = 16;   // most rows of a block
+constexpr int kRows = 4;        // rows a thread takes, where there are many
+constexpr int kTable = 2048;    // cosines and sines of a block
+constexpr int kMaxAbreast = 16; // rows that lie side by side in a block
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -49,59 +51,42 @@ struct alignas(sizeof(T) * W) Piece {
     T v[W];
 };
 
-// Where a unit is: its first element in memory (and, in y, where it goes), its first pair, or -1 for one that is copied.
-template <typename T>
-struct Place {
-    const T *x;
-    T *y;
-    int pair, row;  // row of the block's table
-};
-
 }  // namespace
 
 template <typename T, int W, bool HALF, int K>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr bool kTwo = HALF || W == 1;  // a unit that turns is two accesses
-    __shared__ float2 table[kMaxRows * kRopePairs];
-    pdl_launch_dependents();
-    pdl_wait();
+    __shared__ float2 table[kTable];
     const int pairs = p.rot / 2;
     const int block = blockIdx.x / p.splits, part = blockIdx.x - block * p.splits;
-    const int row0 = block * p.rows_per, n_rows = min(p.rows_per, p.rows - row0);
-    // elements from a unit's first access to its second
+    const int row0 = block * (p.abreast * K), n_rows = min(p.abreast * K, p.rows - row0);
+    // the thread's unit, in rows `sub`, sub + abreast, ..
+    const int sub = (int)((unsigned)threadIdx.x / (unsigned)p.part), u = part * p.part + threadIdx.x - sub * p.part;
+    const int first = p.per_head[0] * p.s[0].heads;
+    const bool second = u >= first, on = sub < p.abreast && u < p.units;
+    const RopeSide &s = p.s[second];
+    const int ph = p.per_head[second], v = second ? u - first : u, h = (int)((unsigned)v / (unsigned)ph), c = v - h * ph;
+    // elements from a unit's first access to its second; units of a head that turn: W pairs each of halves, W elements of neighbours, one
+    // pair where W is 1; behind them come the pieces that are copied
     const int apart = HALF ? pairs : 1;
-    // units of a head that turn: W pairs each of halves; W elements of neighbours, one pair where W is 1
     const int turning = HALF ? pairs / W : W == 1 ? pairs : p.rot / W;
-    const int u0 = part * (K * kThreads), total = n_rows * p.units;
-    auto place = [&](int u) {
-        Place<T> a;
-        a.row = (int)((unsigned)u / (unsigned)p.units);
-        int v = u - a.row * p.units;
-        const int first = p.per_head[0] * p.s[0].heads;
-        const bool second = v >= first;
-        if (second) v -= first;
-        const RopeSide &s = p.s[second];
-        const int ph = p.per_head[second], h = (int)((unsigned)v / (unsigned)ph), c = v - h * ph;
-        const bool turns = c < turning;
-        // first element: behind the turning part come the pieces that are copied
-        const int e = turns ? (HALF ? c * W : W == 1 ? 2 * c : c * W) : p.rot + (c - turning) * W;
-        a.x = reinterpret_cast<const T *>(s.x + (long long)(row0 + a.row) * s.x_row + h * s.x_head) + e;
-        a.y = reinterpret_cast<T *>(s.y + (long long)(row0 + a.row) * s.y_row + h * s.y_head) + e;
-        a.pair = !turns ? -1 : HALF ? c * W : W == 1 ? c : c * W / 2;
-        return a;
-    };
+    const bool turns = c < turning;
+    const int e0 = turns ? (HALF ? c * W : W == 1 ? 2 * c : c * W) : p.rot + (c - turning) * W;
+    const int pair = HALF ? c * W : W == 1 ? c : c * W / 2;
+    const T *x = reinterpret_cast<const T *>(s.x + (row0 + sub) * s.x_row + h * s.x_head) + e0;
+    T *y = reinterpret_cast<T *>(s.y + (row0 + sub) * s.y_row + h * s.y_head) + e0;
+    const long long x_step = p.abreast * s.x_row / (long long)sizeof(T), y_step = p.abreast * s.y_row / (long long)sizeof(T);
+    pdl_launch_dependents();
+    pdl_wait();
     Piece<T, W> xa[K], xb[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int u = u0 + k * kThreads + threadIdx.x;
-        if (u >= total) continue;
-        const Place<T> a = place(u);
-        xa[k] = *reinterpret_cast<const Piece<T, W> *>(a.x);
-        if (kTwo && a.pair >= 0) xb[k] = *reinterpret_cast<const Piece<T, W> *>(a.x + apart);
+        if (!on || sub + k * p.abreast >= n_rows) continue;
+        xa[k] = *reinterpret_cast<const Piece<T, W> *>(x + k * x_step);
+        if (kTwo && turns) xb[k] = *reinterpret_cast<const Piece<T, W> *>(x + k * x_step + apart);
     }
-    // the rows' cosines and sines (a block that copies only would not need them: no such block is worth a test)
-    for (int i = threadIdx.x; i < n_rows * pairs; i += kThreads) {
-        const int r = i / pairs;
+    for (int i = threadIdx.x; i < n_rows * pairs; i += blockDim.x) {
+        const int r = (int)((unsigned)i / (unsigned)pairs);
         const unsigned long long turn = (unsigned long long)(long long)p.positions[row0 + r] * p.turns[i - r * pairs];
         float sn, cs;
         sincospif((float)(long long)turn * 0x1p-63f, &sn, &cs);  // half-turns in [-1, 1]
@@ -110,29 +95,28 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const int u = u0 + k * kThreads + threadIdx.x;
-        if (u >= total) continue;
-        const Place<T> a = place(u);
-        if (a.pair >= 0) {
-            const float2 *t = table + a.row * pairs + a.pair;
+        const int r = sub + k * p.abreast;
+        if (!on || r >= n_rows) continue;
+        if (turns) {
+            const float2 *t = table + r * pairs + pair;
             if constexpr (kTwo) {
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
-                    const float x = to_float(xa[k].v[e]), y = to_float(xb[k].v[e]);
-                    xa[k].v[e] = from_float<T>(x * t[e].x - y * t[e].y);
-                    xb[k].v[e] = from_float<T>(x * t[e].y + y * t[e].x);
+                    const float a = to_float(xa[k].v[e]), b = to_float(xb[k].v[e]);
+                    xa[k].v[e] = from_float<T>(a * t[e].x - b * t[e].y);
+                    xb[k].v[e] = from_float<T>(a * t[e].y + b * t[e].x);
                 }
-                *reinterpret_cast<Piece<T, W> *>(a.y + apart) = xb[k];
+                *reinterpret_cast<Piece<T, W> *>(y + k * y_step + apart) = xb[k];
             } else {
 #pragma unroll
                 for (int e = 0; e < W / 2; ++e) {
-                    const float x = to_float(xa[k].v[2 * e]), y = to_float(xa[k].v[2 * e + 1]);
-                    xa[k].v[2 * e] = from_float<T>(x * t[e].x - y * t[e].y);
-                    xa[k].v[2 * e + 1] = from_float<T>(x * t[e].y + y * t[e].x);
+                    const float a = to_float(xa[k].v[2 * e]), b = to_float(xa[k].v[2 * e + 1]);
+                    xa[k].v[2 * e] = from_float<T>(a * t[e].x - b * t[e].y);
+                    xa[k].v[2 * e + 1] = from_float<T>(a * t[e].y + b * t[e].x);
                 }
             }
         }
-        *reinterpret_cast<Piece<T, W> *>(a.y) = xa[k];
+        *reinterpret_cast<Piece<T, W> *>(y + k * y_step) = xa[k];
     }
 }
 
@@ -147,24 +131,27 @@ cudaError_t launch(RopeParams p, int num_sms, cudaStream_t s) {
         p.units += p.per_head[i] * p.s[i].heads;
     }
     if (p.units == 0) return cudaSuccess;
-    // one unit a thread while that leaves SMs without a block, then up to kUnits: more loads in flight, and fewer cosines
-    const long long blocks = ((long long)p.rows * p.units + kThreads - 1) / kThreads;
-    const int k = blocks <= 2ll * num_sms ? 1 : kUnits;
-    const int most = k * kThreads;
-    p.rows_per = p.units >= most ? 1 : most / p.units < kMaxRows ? most / p.units : kMaxRows;
-    p.splits = (p.units + most - 1) / most;
-    const long long grid = ((long long)p.rows + p.rows_per - 1) / p.rows_per * p.splits;
+    // a row's units over as few blocks as hold them, evenly; rows side by side where they are short
+    p.splits = (p.units + kThreads - 1) / kThreads;
+    p.part = (p.units + p.splits - 1) / p.splits;
+    p.abreast = p.splits > 1 ? 1 : kThreads / p.part < kMaxAbreast ? kThreads / p.part : kMaxAbreast;
+    // one row a thread while that leaves SMs without two blocks, then kRows: more loads in flight
+    const long long least = ((long long)p.rows + p.abreast - 1) / p.abreast * p.splits;
+    const int k = least <= 2ll * num_sms ? 1 : kRows;
+    while (p.abreast > 1 && p.abreast * k * pairs > kTable) --p.abreast;
+    static_assert(kRows * kRopePairs <= kTable, "a block's rows have room for their cosines");
+    const long long grid = ((long long)p.rows + p.abreast * k - 1) / (p.abreast * k) * p.splits;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((p.part * p.abreast + 31) / 32 * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return k == 1 ? cudaLaunchKernelEx(&cfg, rope_kernel<T, W, HALF, 1>, p) : cudaLaunchKernelEx(&cfg, rope_kernel<T, W, HALF, kUnits>, p);
+    return k == 1 ? cudaLaunchKernelEx(&cfg, rope_kernel<T, W, HALF, 1>, p) : cudaLaunchKernelEx(&cfg, rope_kernel<T, W, HALF, kRows>, p);
 }
 
 template <typename T>

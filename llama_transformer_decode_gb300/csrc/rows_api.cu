@@ -168,7 +168,7 @@ int l2_token_rules_init(L2TokenRules *r) {
     r->ready = 0;
     if (r->n_seqs < 1) return refuse(L2_EINVAL, "%s: n_seqs = %d", who, r->n_seqs);
     if (r->vocab_size < 1 || r->vocab_size > 1 << 24) return refuse(L2_EINVAL, "%s: vocab_size %d outside 1..2^24", who, r->vocab_size);
-    if (r->max_len < 0 || r->max_len > 0x3fffffff) return refuse(L2_EINVAL, "%s: max_len %d outside 0..2^30 - 1", who, r->max_len);
+    if (r->max_len < 0 || r->max_len > 0xffff00) return refuse(L2_EINVAL, "%s: max_len %d outside 0..2^24 - 256", who, r->max_len);
     if (r->n_bias < 0 || r->n_bias > 0x3fffffff) return refuse(L2_EINVAL, "%s: n_bias %d outside 0..2^30 - 1", who, r->n_bias);
     if (r->n_seqs > 1 && (r->history_stride < r->max_len || r->history_stride > (1ll << 40)))
         return refuse(L2_EINVAL, "%s: history_stride %lld is below max_len or too large", who, r->history_stride);
@@ -253,8 +253,13 @@ int l2_token_rules(const L2TokenRules *r, const L2TokenRows *a, void *cuda_strea
     p.max_len = r->max_len;
     p.n_bias = r->n_bias;
     p.n_masks = a->n_masks;
-    // four elements an access, where every row begins on one
-    const bool vec = !(reinterpret_cast<uintptr_t>(a->logits) % (4 * es)) && !(reinterpret_cast<uintptr_t>(a->out) % (4 * os)) &&
-                     (a->rows < 2 || (a->row_stride % 4 == 0 && a->out_row_stride % 4 == 0));
+    // elements an access, where every row begins on one: 8 bytes read and 16 written, or 16 of each (32 bytes written by a thread would be two
+    // accesses that each leave every other sector half written)
+    int vec = os == 2 ? 8 : 4;
+    auto fits = [&](int w) {
+        return !(reinterpret_cast<uintptr_t>(a->logits) % (w * es)) && !(reinterpret_cast<uintptr_t>(a->out) % (w * os)) &&
+               (a->rows < 2 || (a->row_stride % w == 0 && a->out_row_stride % w == 0));
+    };
+    if (!fits(vec)) vec = fits(4) ? 4 : 1;
     return finish(who, launch_rules(p, a->dtype, a->out_dtype == L2_F32, vec, sms, static_cast<cudaStream_t>(cuda_stream)));
 }

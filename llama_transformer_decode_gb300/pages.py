@@ -239,15 +239,16 @@ class PagePool:
         before them, to itself and to the tokens above it (``l2_pages_tree_attention``).  ``parents``: each row's parent
         within its tree, -1 for none; without it the trees are chains.  ``lse`` and ``out`` as for attention."""
         qp, (B, H, _), q_st = self._rows("q", q, 3)
-        n = len(seqs)
+        n, ints = seqs.shape[0], self._ints
         out, fresh, o_row, o_head, ws, need = self._outputs(True, (n, B, H), q, out, lse, stream)
-        a = L2PagesTreeAttention(int(layer), n, B, H, qp, out.data_ptr(), None if lse is None else lse.data_ptr(), self._ints("seqs", seqs),
-                                 self._ints("starts", starts, n + 1), None if parents is None else self._ints("parents", parents, B),
+        a = L2PagesTreeAttention(int(layer), n, B, H, qp, out.data_ptr(), None if lse is None else lse.data_ptr(), ints("seqs", seqs),
+                                 ints("starts", starts, n + 1), None if parents is None else ints("parents", parents, B),
                                  q_st[0], q_st[1], o_row, o_head, self._scale if scale is None else float(scale))
         rc = self._lib.l2_pages_tree_attention(self._ref, ctypes.byref(a), ws.data_ptr(), need, self._stream(stream))
         if rc:
             _raise(rc)
-        self._used_on(stream, q, seqs, starts, parents, None if fresh else out, lse)
+        if stream is not None:
+            self._used_on(stream, q, seqs, starts, parents, None if fresh else out, lse)
         return out
 
     def accept(self, tokens, targets, seqs, starts, parents=None, stream=None):
@@ -255,17 +256,17 @@ class PagePool:
         token 0, then the first child of each accepted token whose token is what was sampled from that one's logits
         (``targets``).  Returns int32 tensors ``path`` (each tree's accepted places, then -1), ``counts`` and ``next`` (the target
         of the last accepted token)."""
-        rows, n = len(tokens), len(seqs)
+        rows, n, ints = tokens.shape[0], seqs.shape[0], self._ints
         made = self._made(rows + 2 * n, stream)
-        path, counts, following = made[:rows], made[rows:rows + n], made[rows + n:]
-        a = L2PagesAccept(n, rows, self._ints("seqs", seqs), self._ints("starts", starts, n + 1),
-                          None if parents is None else self._ints("parents", parents, rows), self._ints("tokens", tokens),
-                          self._ints("targets", targets, rows), path.data_ptr(), counts.data_ptr(), following.data_ptr())
+        at = made.data_ptr()
+        a = L2PagesAccept(n, rows, ints("seqs", seqs), ints("starts", starts, n + 1), None if parents is None else ints("parents", parents, rows),
+                          ints("tokens", tokens), ints("targets", targets, rows), at, at + 4 * rows, at + 4 * (rows + n))
         rc = self._lib.l2_pages_accept(self._ref, ctypes.byref(a), self._stream(stream))
         if rc:
             _raise(rc)
-        self._used_on(stream, tokens, targets, seqs, starts, parents)
-        return path, counts, following
+        if stream is not None:
+            self._used_on(stream, tokens, targets, seqs, starts, parents)
+        return made.split_with_sizes([rows, n, n])
 
     def keep(self, path, counts, seqs, starts, stream=None):
         """Shortens the sequences to given paths (``l2_pages_keep``): of the last starts[i + 1] - starts[i] rows of seqs[i],

@@ -38,7 +38,7 @@ class Rope:
             raise ValueError("kind must be None, 'linear', 'base' or 'bands'")
         self._lib, self._torch = _native.load(), torch
         self._kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._raw_stream, self._int32 = torch._C._cuda_getCurrentRawStream, torch.int32
         self.rot_dim, self.layout = int(rot_dim), layout
         n = max(self.rot_dim // 2, 1)
         if freqs is None:
@@ -62,50 +62,57 @@ class Rope:
         """Turns ``q`` and ``k`` ([rows][heads][head size], float32, bfloat16 or float16, rows and heads at any strides) by
         ``positions`` (int32 [rows]).  Results go to ``out_q`` and ``out_k`` (in place: the tensor itself), by default new
         tensors.  Returns (out_q, out_k), None for one that is not given."""
-        torch = self._torch
         x = q if q is not None else k
         if x is None or (q is None and out_q is not None) or (k is None and out_k is not None):
             raise ValueError("q, k or both, and an output only for one that is given")
-        dtype, index = x.dtype, x.get_device()
-        if dtype not in self._kinds or index < 0:
-            raise ValueError("expected float32, bfloat16 or float16 CUDA tensors")
-        rows, hs = x.shape[0], x.shape[-1]
-        if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or positions.get_device() != index \
-                or positions.dim() != 1 or positions.numel() != rows or not positions.is_contiguous():
+        kind, index, shape = self._kinds.get(x.dtype), x.get_device(), x.shape
+        if kind is None or index < 0 or len(shape) != 3:
+            raise ValueError("expected float32, bfloat16 or float16 CUDA tensors [rows][heads][head size]")
+        rows, hs = shape[0], shape[2]
+        if not isinstance(positions, self._torch.Tensor) or positions.dtype is not self._int32 or positions.get_device() != index \
+                or positions.shape != (rows,) or not positions.is_contiguous():
             raise ValueError(f"positions must be a contiguous int32 tensor [{rows}] on the device of q and k")
-
-        def side(t, out):
-            if t is None:
-                return None, (0, None, None, 0, 0, 0, 0), True
-            self._check(t, dtype, index, rows, hs)
-            fresh = out is None
-            if fresh:
-                if stream is None:
-                    out = torch.empty(t.shape, dtype=dtype, device=t.device)
-                else:
-                    with torch.cuda.stream(stream):
-                        out = torch.empty(t.shape, dtype=dtype, device=t.device)
-            else:
-                self._check(out, dtype, index, rows, hs)
-                if out.shape != t.shape:
-                    raise ValueError("an output must have its input's shape")
-            a, b = t.stride(), out.stride()
-            return out, (t.shape[1], t.data_ptr(), out.data_ptr(), a[0], a[1], b[0], b[1]), fresh
-
-        q_out, (qh, qp, qo, qr, qs, qor, qos), q_new = side(q, out_q)
-        k_out, (kh, kp, ko, kr, ks, kor, kos), k_new = side(k, out_k)
-        a = L2RopeRows(rows, self._kinds[dtype], hs, qh, kh, positions.data_ptr(), qp, kp, qo, ko, qr, qs, kr, ks, qor, qos, kor, kos)
+        a = L2RopeRows(rows, kind, hs, 0, 0, positions.data_ptr())
+        q_new, k_new = out_q is None, out_k is None
+        if q is not None:
+            s = self._side(q, x)
+            if q_new:
+                out_q = self._new(q, stream)
+            o = self._side(out_q, q)
+            if out_q.shape != q.shape:
+                raise ValueError("an output must have its input's shape")
+            a.n_heads, a.q, a.q_out = q.shape[1], q.data_ptr(), out_q.data_ptr()
+            a.q_row_stride, a.q_head_stride, a.q_out_row_stride, a.q_out_head_stride = s[0], s[1], o[0], o[1]
+        if k is not None:
+            s = self._side(k, x)
+            if k_new:
+                out_k = self._new(k, stream)
+            o = self._side(out_k, k)
+            if out_k.shape != k.shape:
+                raise ValueError("an output must have its input's shape")
+            a.n_kv_heads, a.k, a.k_out = k.shape[1], k.data_ptr(), out_k.data_ptr()
+            a.k_row_stride, a.k_head_stride, a.k_out_row_stride, a.k_out_head_stride = s[0], s[1], o[0], o[1]
         rc = self._lib.l2_rope(self._ref, ctypes.byref(a), self._raw_stream(index) if stream is None else stream.cuda_stream)
         if rc:
             _raise(rc)
         if stream is not None:  # their memory is kept until the call has run
-            for t in (positions, q, k, None if q_new else q_out, None if k_new else k_out):
+            for t in (positions, q, k, None if q_new else out_q, None if k_new else out_k):
                 if t is not None:
                     t.record_stream(stream)
-        return q_out, k_out
+        return out_q, out_k
+
+    def _new(self, t, stream):
+        torch = self._torch
+        if stream is None:
+            return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
     @staticmethod
-    def _check(t, dtype, index, rows, hs):
-        if t.dim() != 3 or t.dtype is not dtype or t.get_device() != index or t.shape[0] != rows or t.shape[2] != hs \
-                or (hs > 1 and t.stride(2) != 1):
+    def _side(t, like):
+        """Strides of q, k or an output, whose rows, head size, type and device are another's."""
+        shape, want, st = t.shape, like.shape, t.stride()
+        if len(shape) != 3 or shape[0] != want[0] or shape[2] != want[2] or t.dtype is not like.dtype or t.get_device() != like.get_device() \
+                or (st[2] != 1 and shape[2] > 1):
             raise ValueError("q, k and outputs must be [rows][heads][head size] of one type and device, the last dimension contiguous")
+        return st

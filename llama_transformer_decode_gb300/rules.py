@@ -31,7 +31,7 @@ class TokenRules:
     def __init__(self, vocab_size: int, history, lens, counted_from=None, repetition=None, presence=None, frequency=None, bias=None):
         import torch
         self._torch, self._lib = torch, _native.load()
-        self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._raw_stream, self._int32 = torch._C._cuda_getCurrentRawStream, torch.int32
         self._kinds = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
         if not isinstance(history, torch.Tensor) or history.dim() != 2 or history.dtype is not torch.int32 or not history.is_cuda \
                 or (history.shape[1] > 1 and history.stride(1) != 1):
@@ -66,11 +66,25 @@ class TokenRules:
 
     def _ints(self, name, t, n=None):
         """Address of an index array; n: its length, where the call fixes it."""
-        torch = self._torch
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != self._index or t.dim() != 1 \
+        if not isinstance(t, self._torch.Tensor) or t.dtype is not self._int32 or t.get_device() != self._index or t.dim() != 1 \
                 or not t.is_contiguous() or (n is not None and t.numel() != n):
             raise ValueError(f"{name} must be a contiguous int32 tensor [{'n' if n is None else n}] on {self.device}")
         return t.data_ptr()
+
+    def _matrix(self, name, t):
+        """Rows and row stride of logits."""
+        shape, st = t.shape, t.stride()
+        if len(shape) != 2 or shape[1] != self.vocab_size or t.dtype not in self._kinds or t.get_device() != self._index \
+                or (st[1] != 1 and shape[1] > 1):
+            raise ValueError(f"{name} must be [rows][{self.vocab_size}], float32, bfloat16 or float16 on {self.device}, its last dimension contiguous")
+        return shape[0], st[0]
+
+    def _new(self, rows, dtype, stream):
+        torch = self._torch
+        if stream is None:
+            return torch.empty((rows, self.vocab_size), dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty((rows, self.vocab_size), dtype=dtype, device=self.device)
 
     def check(self):
         """Waits for the device and raises L2Error if a row could not be done (and clears the status)."""
@@ -89,16 +103,9 @@ class TokenRules:
         penalised for its path, too.  ``masks`` (int32 [masks][ceil(vocab_size / 32)], bit v % 32 of word v / 32 set where token v is
         allowed): row r's is masks[mask_rows[r]] (-1: none), or masks[r].  Returns ``out`` (in place: ``logits``), by default a
         new tensor of ``out_dtype`` (float32 or the logits' type, which is the default; ``sample`` takes float32)."""
-        torch = self._torch
-        kinds = self._kinds
-
-        def matrix(name, t):
-            if not isinstance(t, torch.Tensor) or t.dtype not in kinds or t.dim() != 2 or t.get_device() != self._index \
-                    or t.shape[1] != self.vocab_size or (t.shape[1] > 1 and t.stride(1) != 1):
-                raise ValueError(f"{name} must be [rows][{self.vocab_size}], float32, bfloat16 or float16 on {self.device}, its last dimension contiguous")
-        matrix("logits", logits)
-        rows = logits.shape[0]
-        n = len(starts) - 1 if starts is not None else rows
+        kinds, ints, V = self._kinds, self._ints, self.vocab_size
+        rows, row_stride = self._matrix("logits", logits)
+        n = rows if starts is None else starts.shape[0] - 1
         if parents is not None and starts is None:
             raise ValueError("parents need starts")
         fresh = out is None
@@ -106,30 +113,27 @@ class TokenRules:
             dtype = logits.dtype if out_dtype is None else out_dtype
             if dtype not in kinds:
                 raise ValueError("out_dtype must be float32 or the logits' type")
-            if stream is None:
-                out = torch.empty((rows, self.vocab_size), dtype=dtype, device=self.device)
-            else:
-                with torch.cuda.stream(stream):
-                    out = torch.empty((rows, self.vocab_size), dtype=dtype, device=self.device)
+            out, out_stride = self._new(rows, dtype, stream), V
         else:
-            matrix("out", out)
-            if out.shape[0] != rows or (out_dtype is not None and out.dtype is not out_dtype):
+            dtype = out.dtype
+            out_rows, out_stride = self._matrix("out", out)
+            if out_rows != rows or (out_dtype is not None and dtype is not out_dtype):
                 raise ValueError("out must have the logits' rows, and out_dtype's type")
-        n_masks = 0
+        a = L2TokenRows(n, rows, None if seqs is None else ints("seqs", seqs, n), None if starts is None else ints("starts", starts),
+                        None if parents is None else ints("parents", parents, rows), None if drafted is None else ints("drafted", drafted, rows),
+                        logits.data_ptr(), out.data_ptr(), kinds[logits.dtype], kinds[dtype], row_stride, out_stride)
         if masks is not None:
-            if masks.dtype is not torch.int32 or masks.dim() != 2 or masks.get_device() != self._index \
-                    or masks.shape[1] != -(-self.vocab_size // 32) or (masks.shape[1] > 1 and masks.stride(1) != 1):
-                raise ValueError(f"masks must be int32 [masks][{-(-self.vocab_size // 32)}] on {self.device}, the last dimension contiguous")
-            n_masks = masks.shape[0]
+            shape, words = masks.shape, -(-V // 32)
+            if masks.dtype is not self._int32 or len(shape) != 2 or masks.get_device() != self._index or shape[1] != words \
+                    or (words > 1 and masks.stride(1) != 1):
+                raise ValueError(f"masks must be int32 [masks][{words}] on {self.device}, the last dimension contiguous")
+            a.masks, a.mask_stride, a.n_masks = masks.data_ptr(), masks.stride(0), shape[0]
+            if mask_rows is not None:
+                a.mask_rows = ints("mask_rows", mask_rows, rows)
         elif mask_rows is not None:
             raise ValueError("mask_rows needs masks")
         if rows == 0:
             return out
-        a = L2TokenRows(n, rows, None if seqs is None else self._ints("seqs", seqs, n), None if starts is None else self._ints("starts", starts),
-                        None if parents is None else self._ints("parents", parents, rows),
-                        None if drafted is None else self._ints("drafted", drafted, rows), logits.data_ptr(), out.data_ptr(), kinds[logits.dtype],
-                        kinds[out.dtype], logits.stride(0), out.stride(0), None if masks is None else masks.data_ptr(),
-                        0 if masks is None else masks.stride(0), n_masks, None if mask_rows is None else self._ints("mask_rows", mask_rows, rows))
         rc = self._lib.l2_token_rules(self._ref, ctypes.byref(a), self._raw_stream(self._index) if stream is None else stream.cuda_stream)
         if rc:
             _raise(rc)

@@ -1,7 +1,8 @@
 """Rules on logits on the GPU against the plain statement in 64 bits.
 
-Tolerance (u = 2^-24): a quotient or product, frequency * n + presence, its subtraction and the bias each round once, each by at most u of
-what it rounds, which is at most m = |l| max(r, 1 / r) + |frequency| n + |presence| + |bias|: 4 u m, and half a step of a 16-bit result.
+Tolerance (u = 2^-24, m = |l| max(r, 1 / r) + |frequency| n + |presence| + |bias|): a quotient, as a product with the rounded inverse, rounds twice,
+frequency * n + presence once, their difference and the bias' sum once each, by at most u of what they round: 2 |l / r| + (|frequency| n +
+|presence|) + 2 m is at most 4 m, so 4 u m, and half a step of a 16-bit result.
 """
 import math
 
