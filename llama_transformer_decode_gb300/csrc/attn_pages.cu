@@ -75,14 +75,21 @@ __device__ __forceinline__ void store_out<__half>(char *o, int d, float4 v) {
     reinterpret_cast<__half2 *>(o + 2 * d)[1] = __floats2half2_rn(v.z, v.w);
 }
 
-constexpr int kEarly = 8;  // rounds of parts' sums loaded before their weights are known
+// Rounds of parts' sums loaded before their weights are known; least blocks of an SM.  Where trees have very many pairs they have few parts
+// each, and more warps at once do more than more loads a warp: 31700 pairs of 3 to 5 parts took 31 us, now 21 (1536 pairs: 2 us longer).
+template <bool MANY>
+constexpr int kEarlyOf = MANY ? 3 : 8;
+template <int NW, bool MANY>
+constexpr int kMergeBlocks = MANY ? 10 : NW == 4 ? 5 : 6;
+constexpr int kManyPairs = 8192;
 }  // namespace
 
 // NW warps per (row, query head) take the parts of its prefix and of its own keys in turn.  Lanes take a part each
 // for (m, l), so a warp's weights are known after one round of loads; LP lanes take a part's sums, the first kEarly
 // rounds of which are loaded beside (m, l).  Then the warps' results are joined in order.
-template <typename T, int NW, bool TREE>
-__global__ void __launch_bounds__(kMergeThreads) attn_pages_merge_kernel(const PagesAttn p) {
+template <typename T, int NW, bool TREE, bool MANY>
+__global__ void __launch_bounds__(kMergeThreads, kMergeBlocks<NW, MANY>) attn_pages_merge_kernel(const PagesAttn p) {
+    constexpr int kEarly = kEarlyOf<MANY>;
     constexpr bool f32 = std::is_same<T, float>::value;
     constexpr int kRows = kMergeThreads / 32 / NW;  // (row, head) pairs a block
     __shared__ float sm[NW], sl[NW];
@@ -288,7 +295,9 @@ WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int
 
 template <typename T, bool TREE>
 cudaError_t launch_merge(const PagesAttn &p, bool few, const cudaLaunchConfig_t &cfg) {
-    return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<T, 4, TREE> : attn_pages_merge_kernel<T, 1, TREE>, p);
+    if constexpr (TREE)
+        if (p.B * p.n_heads > kManyPairs) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<T, 1, true, true>, p);
+    return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<T, 4, TREE, false> : attn_pages_merge_kernel<T, 1, TREE, false>, p);
 }
 
 }  // namespace
@@ -317,7 +326,7 @@ cudaError_t launch_pages_attn(PagesAttn p, void *ws, int num_sms, cudaStream_t s
         p.tile_shift = f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size);
     p.tile_units = 1 << (p.tile_shift - (f32 ? attn_pages_f32_shift(p.head_size) : attn_pages_16_shift(p.head_size)));
     p.pair_shift = p.team == 1 ? 4 : p.team == 2 ? 5 : 6;
-    p.start = item_cost(p.team);
+    p.start = item_cost(p.tree, p.team);
     // whether any prefix of such a call could be one for the tensor cores; the plan decides for each
     p.tc = p.G && tc_worth(p, p.B * heads_per_kv(p.n_heads, p.n_kv_heads), p.max_pages * p.page_size) && (f32 || attn_pages_tc_supported(p));
     p.plan_in_block = (p.tree ? p.G <= kTreePlanInBlock : p.B + p.G <= kPlanInBlock) && !p.wide;

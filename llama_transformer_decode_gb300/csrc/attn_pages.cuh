@@ -89,8 +89,9 @@ __host__ __device__ __forceinline__ int tc_head_rows(int n, bool f32) {  // of a
 // 1 GB of suffixes of head size 128 / 64: 168 / 167 us at 1 pair, 174 / 167 at 4, 210 / 220 at 8, 318 / 282 at 16.
 // Starting an item (its queries, its part) takes a warp 1.25 us where a tile takes 1.55.
 constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
-// A team of warps is one walker: while it starts an item, that many are idle.
-__host__ __device__ constexpr int item_cost(int team) { return kItemCost * team; }
+// A tree's item takes longer to start (3 us: its tokens' words, too), and a team of warps is one walker: that many are idle meanwhile.
+constexpr int kTreeItemCost = 7;
+__host__ __device__ constexpr int item_cost(bool tree, int team) { return (tree ? kTreeItemCost : kItemCost) * team; }
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }
 // The same for teams, whose tiles keep their warps busier than HBM, since mma.sync then bounds them.  32 sequences of 8000 keys: bf16, 8 KV
 // heads of 128, 16 / 32 / 64 pairs with 1 / 2 / 4 warps 171 / 232 / 450 us; fp32, 8 of 3000 and 32 heads of 128: 246 / 369 / 720.
@@ -173,7 +174,7 @@ constexpr int ring_items(int team) { return team > 1 ? 16 : 8; }  // a ring of t
 // are the same.
 template <int KT, int ROW, bool TREE, int TEAM = 1>
 struct Walk {
-    static constexpr int kPairs = kM * TEAM, kStart = item_cost(TEAM), kItems = ring_items(TEAM);
+    static constexpr int kPairs = kM * TEAM, kStart = item_cost(TREE, TEAM), kItems = ring_items(TEAM);
     const int *table;
     long long head;       // byte offset of the KV head
     int src, x, x1;       // source, cost up to which tiles are found, end of the range

@@ -60,7 +60,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     const int i = threadIdx.x, S = TREE ? p.G : p.G + p.B, gq = heads_per_kv(p.n_heads, p.n_kv_heads);
     const bool f32 = p.dtype == L2_F32;
     // pairs and start of an item, tiles of 8 KB that one of its tiles is
-    const int pairs = TREE ? kM * p.team : kM, start = TREE ? item_cost(p.team) : kItemCost, units = TREE ? p.tile_units : 1;
+    const int pairs = TREE ? kM * p.team : kM, start = TREE ? item_cost(true, p.team) : kItemCost, units = TREE ? p.tile_units : 1;
     bool bad = false;
     int len = 0, seq = 0, P = 0, a0 = 0;
     constexpr int kOwn = TREE ? (kPagesMaxCall + NT - 1) / NT : 1;  // parents that a thread looks at

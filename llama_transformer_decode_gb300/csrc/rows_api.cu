@@ -115,7 +115,7 @@ int l2_rope_plan(L2RopePlan *plan, int rot_dim, int layout, const double *freqs,
         if (!std::isfinite(freqs[i])) return refuse(L2_EINVAL, "%s: frequency %d is not finite", who, i);
         double t = freqs[i] / kTwoPi;
         t -= std::floor(t);  // whole turns do nothing at whole positions
-        const double x = std::ldexp(t, 64);
+        const double x = std::nearbyint(std::ldexp(t, 64));
         plan->turns[i] = x >= 18446744073709551616.0 ? 0 : (unsigned long long)x;
     }
     plan->rot_dim = rot_dim;
