@@ -37,7 +37,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxSlice = 8192;   // tokens of a block: two tables of 32 KB
 constexpr int kMinSlice = 1024;
-constexpr int kRowsPer = 8;       // rows of a block, where they come in trees
+constexpr int kMostRows = 32;     // rows of a block, where they come in trees
+constexpr float kTableRows = 4.f; // what making the tables takes, in rows
+constexpr int kBlocks = 4;        // blocks of an SM
 constexpr unsigned kSeen = 1u << 31, kCount = (1u << 24) - 1;
 constexpr int kKindShift = 24;    // 7 bits: 1 + the place
 constexpr unsigned kKind = 0x7fu << kKindShift;
@@ -58,7 +60,7 @@ struct alignas(sizeof(T) * W) Piece {
 
 // TI, TO: types of logits and results; W: elements an access; BIAS: the call has biases (a second table).
 template <typename TI, typename TO, int W, bool BIAS>
-__global__ void __launch_bounds__(kThreads, W == 8 ? 3 : 4) rules_kernel(const RulesParams p) {
+__global__ void __launch_bounds__(kThreads, W == 8 ? 3 : kBlocks) rules_kernel(const RulesParams p) {
     extern __shared__ __align__(16) unsigned count[];  // [slice], and [slice] numbers of bias entries
     __shared__ u64 words[kTreeNodes], kinds[kTreeNodes];
     __shared__ int tokens[kTreeNodes], tree_ok;
@@ -284,11 +286,25 @@ cudaError_t launch(const RulesParams &p, int vec, cudaLaunchConfig_t cfg) {
 
 cudaError_t launch_rules(RulesParams p, int dtype, bool out_f32, int vec, int num_sms, cudaStream_t s) {
     if (p.rows == 0) return cudaSuccess;
-    // the largest slice, since each counts the history anew, that still gives every SM four blocks
-    p.rows_per = p.rows >= kRowsPer * p.n ? kRowsPer : p.rows >= 2 * p.n ? 4 : 1;  // trees' rows together
+    // The largest slice, since each counts the history anew, that still gives every SM blocks; rows of trees (on average rows / n) as many to
+    // a block as make rounds of blocks over the SMs times a block's rows least, a table counting as kTableRows of them.
+    const int at_once = kBlocks * num_sms;
+    p.rows_per = 1;
     p.slice = kMaxSlice;
-    auto blocks = [&]() { return (long long)((p.vocab + p.slice - 1) / p.slice) * ((p.rows + p.rows_per - 1) / p.rows_per); };
-    while (blocks() * 2 <= 5ll * num_sms && p.slice > kMinSlice) p.slice /= 2;
+    auto slices = [&]() { return (p.vocab + p.slice - 1) / p.slice; };
+    if (p.rows >= 2 * p.n) {
+        float least = 0.f;
+        const float tree = (float)p.rows / (float)p.n;
+        for (int r = 1; r <= kMostRows; ++r) {
+            const long long blocks = (long long)slices() * ((p.rows + r - 1) / r), rounds = (blocks + at_once - 1) / at_once;
+            const float cost = (float)rounds * ((float)r + kTableRows * (1.f + (float)(r - 1) / tree));
+            if (r == 1 || cost < least) {
+                least = cost;
+                p.rows_per = r;
+            }
+        }
+    }
+    while ((long long)slices() * ((p.rows + p.rows_per - 1) / p.rows_per) * 2 <= 5ll * num_sms && p.slice > kMinSlice) p.slice /= 2;
     cudaLaunchConfig_t cfg = {};
     // slices one after the other: the first ones, whose tokens are as a rule the frequent ones, take longest
     cfg.gridDim = dim3((p.rows + p.rows_per - 1) / p.rows_per, (p.vocab + p.slice - 1) / p.slice);
