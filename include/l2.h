@@ -528,13 +528,14 @@ int l2_pages_tree_attention(const L2Pages *pool, const L2PagesTreeAttention *arg
 /*
  * Acceptance.  l2_pages_accept finds the path of each tree that the model agrees with: token 0 (what was sampled after the
  * committed rows), then from each accepted token u the first child whose token is targets[u], what was sampled from u's logits.
- * path[starts[i] ..] receives the places of the accepted tokens, ascending, then -1; counts[i] how many they are (0 for a tree without
- * tokens); next[i] the target of the last one (-1 without tokens), which is token 0 of the sequence's next tree.
+ * path[starts[i] ..] receives the places of the accepted tokens, ascending, then -1 (as do rows behind the last tree); counts[i] how many
+ * they are (0 for a tree without tokens); next[i] the target of the last one (-1 without tokens), which is token 0 of the sequence's next
+ * tree.
  * Their rows then become the sequence's last ones, side by side, in every layer; the other rows' places are
  * given back, with the pages that become free.  l2_pages_keep does that with a path and counts that are given (0 <= counts[i]; the first
  * counts[i] entries ascending places of the tree), for callers with a rule of their own; tokens, targets, parents and next are NULL.
  * A page that rows move into, or that is left partly filled, must be held by its sequence alone.  A call that cannot be done
- * whole changes nothing and writes nothing (L2_PAGES_BAD_CALL, L2_PAGES_BAD_PAGE).
+ * whole changes nothing (L2_PAGES_BAD_CALL, L2_PAGES_BAD_PAGE): its counts are then 0, path and next -1.
  */
 typedef struct {
     int n;                        /* sequences, 1..1024, each named once */

