@@ -24,6 +24,7 @@ struct RopeParams {
     int per_head[2];             // a head's units: pieces of `width` elements (or pairs) that turn, then pieces to copy
     int units;                   // of a row, both sides
     int splits, part, abreast;   // blocks of a row, units of each, rows side by side in one
+    int steps;                   // times that a thread takes rows
     unsigned long long turns[kRopePairs];  // 2^64 times the turns that one position adds to each pair, mod 2^64
 };
 // half: pair i is elements i and i + rot / 2 (else 2 i and 2 i + 1); width: elements an access may take (1, 2, 4 or 8; at most

@@ -13,9 +13,10 @@
 // How.  HBM bounds it (every element is read and written once), at a few rows the latency of one launch.  A unit is one access of
 // 16 bytes (two, half a turning part apart, where pairs are halves) of a head.  A thread has one unit of the row, side after side, head
 // after head, and takes it in several rows: where it is, is worked out once (unit by unit over rows and heads the divisions took
-// longer than HBM: 16384 rows of 32 + 4 heads of 64 in fp16 took 48 us).  Threads load their units first, then make the rows'
-// cosines and sines, once for all heads, in shared memory, while those loads are on their way.  Where sizes or addresses do
-// not allow 16 bytes, accesses are of 8, 4 or of single elements.
+// longer than HBM: 16384 rows of 32 + 4 heads of 64 in fp16, half of each turning, took 48 us).  Threads load their first units, then make the
+// block's cosines and sines, once for all heads, in shared memory, while those loads are on their way, and then store each two
+// rows after the next two's loads (2 rows a block 32 us, 2 times 4 29.5: 5.1 TB/s; 32 + 8 heads of 128 in bf16 70 us: 4.8 TB/s).  Where sizes or
+// addresses do not allow 16 bytes, accesses are of 8, 4 or of single elements.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -29,7 +30,9 @@ namespace l2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 2;        // rows a thread takes, where there are many (4: 34 us in place of 32 for the call above, 8: 54)
+constexpr int kRows = 2;        // rows a thread takes at a time, where there are many
+constexpr int kMostSteps = 4;   // so many times, the next rows loaded before the last are stored
+constexpr int kBlocks = 6;      // blocks of an SM that more steps leave
 constexpr int kTable = 2048;    // cosines and sines of a block
 constexpr int kMaxAbreast = 16; // rows that lie side by side in a block
 
@@ -59,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     __shared__ float2 table[kTable];
     const int pairs = p.rot / 2;
     const int block = blockIdx.x / p.splits, part = blockIdx.x - block * p.splits;
-    const int row0 = block * (p.abreast * K), n_rows = min(p.abreast * K, p.rows - row0);
+    const int row0 = block * (p.abreast * K * p.steps), n_rows = min(p.abreast * K * p.steps, p.rows - row0);
     // the thread's unit, in rows `sub`, sub + abreast, ..
     const int sub = (int)((unsigned)threadIdx.x / (unsigned)p.part), u = part * p.part + threadIdx.x - sub * p.part;
     const int first = p.per_head[0] * p.s[0].heads;
@@ -78,13 +81,20 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const long long x_step = p.abreast * s.x_row / (long long)sizeof(T), y_step = p.abreast * s.y_row / (long long)sizeof(T);
     pdl_launch_dependents();
     pdl_wait();
-    Piece<T, W> xa[K], xb[K];
+    struct Step {  // K rows' units
+        Piece<T, W> a[K], b[K];
+    };
+    auto load = [&](Step &x_, int step) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        if (!on || sub + k * p.abreast >= n_rows) continue;
-        xa[k] = *reinterpret_cast<const Piece<T, W> *>(x + k * x_step);
-        if (kTwo && turns) xb[k] = *reinterpret_cast<const Piece<T, W> *>(x + k * x_step + apart);
-    }
+        for (int k = 0; k < K; ++k) {
+            const int i = step * K + k;
+            if (!on || sub + i * p.abreast >= n_rows) continue;
+            x_.a[k] = *reinterpret_cast<const Piece<T, W> *>(x + i * x_step);
+            if (kTwo && turns) x_.b[k] = *reinterpret_cast<const Piece<T, W> *>(x + i * x_step + apart);
+        }
+    };
+    Step now;
+    load(now, 0);
     for (int i = threadIdx.x; i < n_rows * pairs; i += blockDim.x) {
         const int r = (int)((unsigned)i / (unsigned)pairs);
         const unsigned long long turn = (unsigned long long)(long long)p.positions[row0 + r] * p.turns[i - r * pairs];
@@ -93,30 +103,37 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         table[i] = make_float2(p.amplitude * cs, p.amplitude * sn);
     }
     __syncthreads();
+#pragma unroll 1
+    for (int step = 0;; ++step) {
+        Step next;
+        if (step + 1 < p.steps) load(next, step + 1);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int r = sub + k * p.abreast;
-        if (!on || r >= n_rows) continue;
-        if (turns) {
-            const float2 *t = table + r * pairs + pair;
-            if constexpr (kTwo) {
+        for (int k = 0; k < K; ++k) {
+            const int i = step * K + k, r = sub + i * p.abreast;
+            if (!on || r >= n_rows) continue;
+            if (turns) {
+                const float2 *t = table + r * pairs + pair;
+                if constexpr (kTwo) {
 #pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    const float a = to_float(xa[k].v[e]), b = to_float(xb[k].v[e]);
-                    xa[k].v[e] = from_float<T>(a * t[e].x - b * t[e].y);
-                    xb[k].v[e] = from_float<T>(a * t[e].y + b * t[e].x);
-                }
-                *reinterpret_cast<Piece<T, W> *>(y + k * y_step + apart) = xb[k];
-            } else {
+                    for (int e = 0; e < W; ++e) {
+                        const float a = to_float(now.a[k].v[e]), b = to_float(now.b[k].v[e]);
+                        now.a[k].v[e] = from_float<T>(a * t[e].x - b * t[e].y);
+                        now.b[k].v[e] = from_float<T>(a * t[e].y + b * t[e].x);
+                    }
+                    *reinterpret_cast<Piece<T, W> *>(y + i * y_step + apart) = now.b[k];
+                } else {
 #pragma unroll
-                for (int e = 0; e < W / 2; ++e) {
-                    const float a = to_float(xa[k].v[2 * e]), b = to_float(xa[k].v[2 * e + 1]);
-                    xa[k].v[2 * e] = from_float<T>(a * t[e].x - b * t[e].y);
-                    xa[k].v[2 * e + 1] = from_float<T>(a * t[e].y + b * t[e].x);
+                    for (int e = 0; e < W / 2; ++e) {
+                        const float a = to_float(now.a[k].v[2 * e]), b = to_float(now.a[k].v[2 * e + 1]);
+                        now.a[k].v[2 * e] = from_float<T>(a * t[e].x - b * t[e].y);
+                        now.a[k].v[2 * e + 1] = from_float<T>(a * t[e].y + b * t[e].x);
+                    }
                 }
             }
+            *reinterpret_cast<Piece<T, W> *>(y + i * y_step) = now.a[k];
         }
-        *reinterpret_cast<Piece<T, W> *>(y + k * y_step) = xa[k];
+        if (step + 1 >= p.steps) break;
+        now = next;
     }
 }
 
@@ -135,12 +152,16 @@ cudaError_t launch(RopeParams p, int num_sms, cudaStream_t s) {
     p.splits = (p.units + kThreads - 1) / kThreads;
     p.part = (p.units + p.splits - 1) / p.splits;
     p.abreast = p.splits > 1 ? 1 : kThreads / p.part < kMaxAbreast ? kThreads / p.part : kMaxAbreast;
-    // one row a thread while that leaves SMs without two blocks, then kRows: more loads in flight
+    // one row a thread while that leaves SMs without two blocks, then kRows at a time, as many times as leaves every SM kBlocks blocks
     const long long least = ((long long)p.rows + p.abreast - 1) / p.abreast * p.splits;
     const int k = least <= 2ll * num_sms ? 1 : kRows;
     while (p.abreast > 1 && p.abreast * k * pairs > kTable) --p.abreast;
     static_assert(kRows * kRopePairs <= kTable, "a block's rows have room for their cosines");
-    const long long grid = ((long long)p.rows + p.abreast * k - 1) / (p.abreast * k) * p.splits;
+    const long long steps = least / ((long long)kBlocks * num_sms * k);
+    p.steps = k == 1 || steps < 1 ? 1 : steps < kMostSteps ? (int)steps : kMostSteps;
+    while (p.steps > 1 && p.abreast * k * p.steps * pairs > kTable) --p.steps;
+    const int per = p.abreast * k * p.steps;
+    const long long grid = ((long long)p.rows + per - 1) / per * p.splits;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
