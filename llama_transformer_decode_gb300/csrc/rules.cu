@@ -15,8 +15,8 @@
 // read once for every slice, from L2.  An entry is the count (24 bits), whether the token is only seen (before counted_from), and, for a
 // token that the tree drafted, the place of the first drafted token of that kind: its word in `kinds` says which of the
 // tree's tokens are of the kind, so that a row adds those that are on its path (its word of the tree) to the count, and no row
-// waits for another.  (With paths added to the table and taken off again, two barriers a row: 480 rows of 128000 in bf16 took
-// 187 us.)  A bias table holds the number of the last entry of each token, by atomicMax.
+// waits for another.  (480 rows of 30-token trees over 128000 tokens, bf16 to fp32: 79 us, 4.7 TB/s; with paths added to the table and
+// taken off again, two barriers a row, 187.)  A bias table holds the number of the last entry of each token, by atomicMax.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
