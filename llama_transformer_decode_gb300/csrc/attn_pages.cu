@@ -23,7 +23,7 @@
 //
 // Trees of drafted tokens (attn_tree_16.cu, attn_tree_f32.cu) are the same kernels compiled for groups that are sequences: a group's rows
 // are its tree's tokens, its keys one source, whose last ones each row sees or not; 2 or 4 warps walk together where a sequence
-// has more than 16 pairs (l2_pages.h: `team`).  64 chains of 5 tokens on 1000 to 8200 keys, 32 heads on 8 of 128 in bf16: 285 us, 4.4 TB/s.
+// has more than 16 pairs (l2_pages.h: `team`).  64 chains of 5 tokens on 1000 to 8200 keys, 32 heads on 8 of 128 in bf16: 256 us, 4.9 TB/s.
 //
 // Here: the plan as a kernel (large calls), the merge, and the launches.
 #include <cuda_bf16.h>
@@ -286,7 +286,7 @@ struct WsLayout {
 WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int num_sms, bool tree) {
     WsLayout w;
     const int team = tree ? team_of(B, G, n_heads, n_kv_heads) : 1;
-    w.parts = ((size_t)max_items(B, G, n_heads, n_kv_heads, tree, kM * team) + (size_t)num_sms * (kWalkWarps / team));
+    w.parts = ((size_t)max_items(B, G, n_heads, n_kv_heads, tree, kM * team) + (size_t)num_sms * (walk_warps(false, team) / team));
     const size_t tc = G ? tc_part_rows(B, n_heads, n_kv_heads, num_sms) : 0;
     w.plan = 0;
     w.ml = w.plan + align256(plan_bytes(B, G) + (size_t)B * sizeof(RowPlan));

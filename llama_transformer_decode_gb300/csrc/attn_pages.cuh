@@ -93,11 +93,13 @@ constexpr int kCostUnit = 4, kItemCost = 3, kMaxTileCost = 7;
 constexpr int kTreeItemCost = 7;
 __host__ __device__ constexpr int item_cost(bool tree, int team) { return (tree ? kTreeItemCost : kItemCost) * team; }
 __host__ __device__ __forceinline__ int tile_cost(int dtype, int n) { return dtype != 0 || n <= 4 ? 4 : n <= 8 ? 5 : kMaxTileCost; }
-// The same for teams, whose tiles keep their warps busier than HBM, since mma.sync then bounds them.  32 sequences of 8000 keys: bf16, 8 KV
-// heads of 128, 16 / 32 / 64 pairs with 1 / 2 / 4 warps 171 / 232 / 450 us; fp32, 8 of 3000 and 32 heads of 128: 246 / 369 / 720.
+// The same for teams, whose tiles (of `units` 8 KB) keep their warps longer than HBM would take.  32 sequences of 8000 keys in bf16, 8 KV heads of
+// 128, 16 / 32 / 64 pairs with 1 / 2 / 4 warps 173 / 217 / 388 us, of 64: 136 with 2, and 4 of 64 132 with 4; fp32, 8 of 3000 and 32 heads of
+// 128: 246 / 369 / 720.
 __host__ __device__ __forceinline__ int tree_tile_cost(int dtype, int n, int team, int units) {
     if (team == 1) return tile_cost(dtype, n);
-    return dtype == 0 ? (team == 2 ? 21 : 41) * units / 2 : (team == 2 ? 11 : 21) * units / 2;
+    if (dtype == 0) return (team == 2 ? 21 : 41) * units / 2;
+    return units == 2 ? (team == 2 ? 10 : 18) : team == 2 ? 7 : 13;
 }
 constexpr int kMaxTreeTileCost = 41;
 // Cost of a tensor-core tile for n pairs of a KV head, in the same unit (a quarter of reading 8 KB, 0.049 us an SM).  A 16-bit tile
@@ -125,11 +127,12 @@ __host__ __device__ inline int team_of(int B, int G, int n_heads, int n_kv_heads
 // rows with prefixes of 16 to 12000, geometric means with no such limit and with this one: bf16 15.4 and 13.1 us, fp16 17.5 and 14.3;
 // with a limit eight times higher, one of 64 rows and five prefixes of up to 16390 took 40 us instead of 32.
 constexpr int kTcLeast16 = 40000, kTcLeast32 = 4000;
-// In a tree's call teams of warps take up to 32 pairs (fp32: 64) faster: 232 us against 278 in the calls above (32 pairs, bf16; 64 pairs: 450, 333),
-// in fp32 369 against 595 (64 pairs: 720, 706).
+// In a tree's call teams of warps take up to 32 pairs (fp32: 64) faster: 217 us against 278 in the calls above (32 pairs, bf16; 64 pairs: 388, 312),
+// in fp32 369 against 595 (64 pairs: 720, 706), and longer ones, too: 32 sequences of 300 to 600 keys, 64 pairs, 49 us against 62.
+constexpr int kTreeTcLeast16 = 100000;
 __host__ __device__ __forceinline__ bool tc_worth(const PagesAttn &p, int n, int keys) {
     return n > (!p.tree ? kM : p.dtype == 0 ? 64 : 32) && (long long)cdiv(n, kM) * p.n_kv_heads * p.G * tile_cost(p.dtype, kM) * (keys >> p.tile_shift) >=
-                         (p.dtype == 0 ? kTcLeast32 : kTcLeast16);
+                         (p.dtype == 0 ? kTcLeast32 : p.tree ? kTreeTcLeast16 : kTcLeast16);
 }
 
 // The last entry i of an ascending list of n (every `stride`-th int of a, the first at most x) that is at most x,

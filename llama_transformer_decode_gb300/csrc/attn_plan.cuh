@@ -234,7 +234,7 @@ __device__ __forceinline__ void plan_build(const PagesAttn &p, const Plan &pl, P
     if (i == 0) {
         const int cost = all.x, tc = tc_all.x;
         const int least = TREE ? max(2 * kCostUnit * units, tree_tile_cost(p.dtype, kM, p.team, units)) : 2 * kCostUnit;
-        const RoleSplit r = split_roles(cost, tc, p.num_sms, kWalkWarps / (TREE ? p.team : 1), max(start + least, sc.spread),
+        const RoleSplit r = split_roles(cost, tc, p.num_sms, TREE ? walk_warps(f32, p.team) / p.team : kWalkWarps, max(start + least, sc.spread),
                                         tc_min_per(p.head_size, f32));
         pl.src[S].t0 = cost;
         pl.hdr[kHdrCost] = cost;

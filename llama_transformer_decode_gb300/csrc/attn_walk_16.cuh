@@ -81,15 +81,21 @@ struct Shape {
     static constexpr int C = HS * 2 / 16;         // 16-byte words a row
     static constexpr int kRow = HS * 2;
     static constexpr int kStage = 2 * KT * kRow;  // K then V
+    static constexpr int kWarps = walk_warps(false, TEAM), kTeams = kWarps / TEAM;
     static constexpr int kRings = kWalkWarps * kStages * 8192;
-    static constexpr int kDepth = kStages * 8192 * TEAM / kStage;  // stages of a ring
+    static constexpr int kDepth = kRings / kTeams / kStage;  // stages of a ring
+    static_assert(kDepth >= 2 && kDepth * kTeams * kStage <= kRings, "the rings' memory");
     static constexpr int kItems = ring_items(TEAM);
-    static constexpr int kSmem = kRings + kWalkWarps * kItems * (int)sizeof(WalkItem);
+    static constexpr int kSmem = kRings + kWarps * kItems * (int)sizeof(WalkItem);
     static_assert(kDepth < kItems, "a walk's ring of items");
 };
 // Shared memory of either role, before the plan.
 template <int HS, bool TC, int TEAM>
 constexpr int kWork = TC && (int)TcShape<HS>::kSmem > Shape<HS, TEAM>::kSmem ? (int)TcShape<HS>::kSmem : Shape<HS, TEAM>::kSmem;
+
+// Threads of a block: teams take all of its warps, with the tensor-core role or without.
+__host__ __device__ constexpr int walk_threads(bool tc, int team) { return team == 1 ? attn_threads(tc) : 32 * kTeamWarps; }
+static_assert(32 * kTeamWarps == attn_threads(true), "the tensor-core role has as many warps");
 
 // Word c of row r sits at word c ^ swz(r): the eight rows that one ldmatrix phase reads fall into
 // different banks.
@@ -100,7 +106,8 @@ __device__ __forceinline__ int swz(int r) { return r & 7; }
 // see has no weight, but 0 times an infinity or NaN of V is NaN: tiles with drafted keys are looked through for such values, which then
 // stay out of the product and are added one by one to the rows that see them.
 // TEAM > 1: so many warps are one walker, with a ring together and 16 pairs each.  Where a sequence has more pairs than 16, each warp for itself
-// would bring the keys in anew (32 sequences of 8000 keys, 8 KV heads of 128: 171 us with 16 pairs, 323 with 32, 628 with 64).
+// would bring the keys in anew (32 sequences of 8000 keys, 8 KV heads of 128: 173 us with 16 pairs, 323 with 32, 628 with 64;
+// teams of two and four take 217 and 388).
 template <typename T, int HS, bool TREE, int TEAM>
 __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, unsigned char *smem, int warp, int block0) {
     using Sh = Shape<HS, TEAM>;
@@ -328,21 +335,23 @@ __device__ __forceinline__ void walk_role(const PagesAttn &p, const Plan &pl, un
 // TC: blocks below the plan's share take the tensor-core role, the others walk.  Calls that have no use for it have a kernel of
 // the walk alone, of fewer threads, which is up sooner.
 template <typename T, int HS, bool BF, bool TC, bool TREE, int TEAM>
-__global__ void __launch_bounds__(attn_threads(TC), 1) attn_pages_16_kernel(const __grid_constant__ TcAttn ta) {
+__global__ void __launch_bounds__(walk_threads(TC, TEAM), 1) attn_pages_16_kernel(const __grid_constant__ TcAttn ta) {
     extern __shared__ __align__(1024) unsigned char smem[];
     const PagesAttn &p = ta.p;
     pdl_launch_dependents();
     pdl_wait();
-    const Plan pl = plan_here<attn_threads(TC), TREE>(p, smem + kWork<HS, TC, TEAM>, smem, blockIdx.x == 0);
-    const int n_tc = TC ? pl.hdr[kHdrTcBlocks] : 0, warp = threadIdx.x / 32 - walk_first(TC);
+    const Plan pl = plan_here<walk_threads(TC, TEAM), TREE>(p, smem + kWork<HS, TC, TEAM>, smem, blockIdx.x == 0);
+    const int n_tc = TC ? pl.hdr[kHdrTcBlocks] : 0, warp = threadIdx.x / 32 - (TEAM == 1 ? walk_first(TC) : 0);
     if constexpr (TC) {
         if ((int)blockIdx.x < n_tc) return tc_role<HS, BF>(ta, pl, smem, blockIdx.x);
-        // the four warps that do not walk leave their registers to the eight that do: 24 + 2 * 240 = 3 * 168
-        if (warp < 0) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
-            return;
+        if constexpr (TEAM == 1) {
+            // the four warps that do not walk leave their registers to the eight that do: 24 + 2 * 240 = 3 * 168
+            if (warp < 0) {
+                asm volatile("setmaxnreg.dec.sync.aligned.u32 24;");
+                return;
+            }
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
         }
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
     }
     walk_role<T, HS, TREE, TEAM>(p, pl, smem, warp, n_tc);
 }
@@ -370,10 +379,10 @@ cudaError_t launch(const TcAttn &ta, cudaLaunchConfig_t cfg) {
     constexpr int bytes = kWork<HS, TC, TEAM> + (int)kPlanSmem;
     auto fn = attn_pages_16_kernel<T, HS, BF, TC, TREE, TEAM>;
     static DeviceOnce once;
-    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes, TC ? 168 : 0);
+    cudaError_t e = once.smem(reinterpret_cast<const void *>(fn), bytes, TC && TEAM == 1 ? 168 : 0);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(ta.p.num_sms);
-    cfg.blockDim = dim3(attn_threads(TC));
+    cfg.blockDim = dim3(walk_threads(TC, TEAM));
     cfg.dynamicSmemBytes = bytes;
     return cudaLaunchKernelEx(&cfg, fn, ta);
 }
