@@ -23,7 +23,7 @@
 //
 // Trees of drafted tokens (attn_tree_16.cu, attn_tree_f32.cu) are the same kernels compiled for groups that are sequences: a group's rows
 // are its tree's tokens, its keys one source, whose last ones each row sees or not; 2 or 4 warps walk together where a sequence
-// has more than 16 pairs (l2_pages.h: `team`).  64 chains of 5 tokens on 1000 to 8200 keys, 32 heads on 8 of 128 in bf16: 256 us, 4.9 TB/s.
+// has more than 16 pairs (l2_pages.h: `team`).  64 chains of 5 tokens on 1000 to 8200 keys, 32 heads on 8 of 128 in bf16: 254 us, 4.9 TB/s.
 //
 // Here: the plan as a kernel (large calls), the merge, and the launches.
 #include <cuda_bf16.h>
@@ -80,12 +80,15 @@ __device__ __forceinline__ void store_out<__half>(char *o, int d, float4 v) {
 }
 
 // Rounds of parts' sums loaded before their weights are known; least blocks of an SM.  Where trees have very many pairs they have few parts
-// each, and more warps at once do more than more loads a warp: 31700 pairs of 3 to 5 parts took 31 us, now 21 (1536 pairs: 2 us longer).
+// each, and more warps at once do more than more loads a warp: 31700 pairs of 3 to 5 parts took 31 us, with 10 blocks 21 (1536 pairs: 2 us longer),
+// with 8 and two pairs a warp, whose parts are found at once, 18.5 (four pairs a warp: the same, but 10240 pairs took 5 us longer).
 template <bool MANY>
 constexpr int kEarlyOf = MANY ? 3 : 8;
 template <int NW, bool MANY>
-constexpr int kMergeBlocks = MANY ? 10 : NW == 4 ? 5 : 6;
+constexpr int kMergeBlocks = MANY ? 8 : NW == 4 ? 5 : 6;
 constexpr int kManyPairs = 8192;
+template <bool MANY>
+constexpr int kPairsOf = MANY ? 2 : 1;
 }  // namespace
 
 // NW warps per (row, query head) take the parts of its prefix and of its own keys in turn.  Lanes take a part each
@@ -95,171 +98,190 @@ template <typename T, int NW, bool TREE, bool MANY>
 __global__ void __launch_bounds__(kMergeThreads, kMergeBlocks<NW, MANY>) attn_pages_merge_kernel(const PagesAttn p) {
     constexpr int kEarly = kEarlyOf<MANY>;
     constexpr bool f32 = std::is_same<T, float>::value;
-    constexpr int kRows = kMergeThreads / 32 / NW;  // (row, head) pairs a block
+    constexpr int kRows = kMergeThreads / 32 / NW, kPairs = kPairsOf<MANY>;  // (row, head) pairs a block at once, a warp one after the other
+    static_assert(NW == 1 || kPairs == 1, "warps that share a pair have one");
     __shared__ float sm[NW], sl[NW];
     __shared__ float4 sa[NW][32];
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % NW;
-    const int bh = blockIdx.x * kRows + (threadIdx.x >> 5) / NW;
-    const int b = (int)((unsigned)bh / (unsigned)p.n_heads), h = bh - b * p.n_heads;
+    const int bh0 = (blockIdx.x * kRows + (threadIdx.x >> 5) / NW) * kPairs;
     const Plan pl = plan_of(p.plan, p.B, p.G);
     const int gq = heads_per_kv(p.n_heads, p.n_kv_heads);
-    const int kvh = (int)((unsigned)(h * p.n_kv_heads) / (unsigned)p.n_heads), j = h - first_head(kvh, p.n_heads, p.n_kv_heads);
     const int LP = p.head_size > 64 ? 32 : p.head_size > 32 ? 16 : 8;  // lanes of a part's sums
     const int sub = lane / LP, d = 4 * (lane % LP), at_once = 32 / LP;
     const bool on = d < p.head_size;
     pdl_launch_dependents();
     pdl_wait();
-    if (b >= p.B) return;
     const int4 h0 = *reinterpret_cast<const int4 *>(pl.hdr);
     const int per_tc = pl.hdr[kHdrTcPer];
-    const int4 *rp = reinterpret_cast<const int4 *>(pl.row + b);
-    const int4 ow = rp[0], re = rp[1], tc = rp[2];
-    const int4 in = rp[3];
-    const int gr = in.x, per = h0.y;
-    if (!h0.z || (TREE && in.y)) return;
+    const int per = h0.y;
+    if (!h0.z) return;
     const int shift = TREE ? p.pair_shift : 4, pairs = 1 << shift, start = TREE ? p.start : kItemCost;
     static_assert(kM == 1 << 4, "pairs of an item");
-    // first walker, parts and first row of the parts of the item that holds pair mi of a source of n pairs
-    struct Range {
-        int w0, n, row;
+    // where a (row, head)'s parts are
+    struct Parts {
+        int b, h;  // b < 0: none, or not to be written
+        int own_n, own_row, rest_n, rest_row, tc_n, tc_row, tc_rows;
     };
-    auto range = [&](const int4 &s, int mi, int n) {
-        Range r = {};
+    // parts and first row of the parts of the item that holds pair mi of a source of n pairs
+    auto range = [&](const int4 &s, int kvh, int mi, int n, int *count, int *row) {
         if (s.z) {
-            const int item = kvh * ((n + pairs - 1) >> shift) + (mi >> shift), u0 = s.x + item * (start + s.z * s.w);
-            r.w0 = walker_of(u0, per);
-            r.n = walker_of(u0 + tile_place(s.z - 1, start, s.w), per) - r.w0 + 1;
-            r.row = ((s.y + item + r.w0) << shift) + (mi & (pairs - 1));
-        }
-        return r;
-    };
-    const Range own = range(ow, j, gq);
-    Range rest = {};
-    int tc_n = 0, tc_row = 0, tc_rows = 0, tc_two = 0;
-    if (p.G) {
-        const int n = tc.w * gq, mi = gr * gq + j;
-        rest = range(re, mi, n);
-        if (tc.y) {
-            const int run = mi / tc_run(f32), cost = tc_cost(n, p.head_size, f32);
-            const int u0 = tc.x + (kvh * tc_runs(n, f32) + run) * (kTcItemCost + tc.y * cost), w0 = walker_of(u0, per_tc);
-            tc_rows = min(tc_run(f32), n - run * tc_run(f32));
-            tc_two = !f32 && tc_rows <= kTcRows;  // two parts of this row a block, tc_rows apart
-            tc_n = (walker_of(u0 + tile_place(tc.y - 1, kTcItemCost, cost), per_tc) - w0 + 1) << tc_two;
-            tc_row = tc.z + kvh * tc_head_rows(n, f32) + mi + tc_run(f32) * w0;
-        }
-    }
-    const int total = tc_n + rest.n + own.n, n = (total + NW - 1 - warp) / NW;  // parts of the row, of this warp
-    // (m, l) and sums of the warp's i-th part
-    auto part = [&](int i, const float2 *&ml, const float *&acc) {
-        int e = i * NW + warp;
-        if (e < tc_n) {
-            const size_t at = (size_t)(tc_row + tc_run(f32) * (e >> tc_two) + (tc_two ? (e & 1) * tc_rows : 0));
-            ml = reinterpret_cast<const float2 *>(p.tc_ml) + at;
-            acc = p.tc_acc + at * p.head_size;
-        } else {
-            e -= tc_n;
-            const size_t at = (size_t)(e < rest.n ? rest.row + (e << shift) : own.row + ((e - rest.n) << shift));
-            ml = reinterpret_cast<const float2 *>(p.ws_ml) + at;
-            acc = p.ws_acc + at * p.head_size;
+            const int item = kvh * ((n + pairs - 1) >> shift) + (mi >> shift), u0 = s.x + item * (start + s.z * s.w), w0 = walker_of(u0, per);
+            *count = walker_of(u0 + tile_place(s.z - 1, start, s.w), per) - w0 + 1;
+            *row = ((s.y + item + w0) << shift) + (mi & (pairs - 1));
         }
     };
-    auto sums = [&](int e) {
-        const float2 *ml;
-        const float *acc;
-        part(e, ml, acc);
-        return *reinterpret_cast<const float4 *>(acc + d);
+    auto two_parts = [&](int tc_rows) { return !f32 && tc_rows <= kTcRows; };  // of a row a tensor-core block, tc_rows apart
+    auto parts_of = [&](int bh) {
+        Parts x = {};
+        x.b = (int)((unsigned)bh / (unsigned)p.n_heads);
+        x.h = bh - x.b * p.n_heads;
+        if (x.b >= p.B) {
+            x.b = -1;
+            return x;
+        }
+        const int kvh = (int)((unsigned)(x.h * p.n_kv_heads) / (unsigned)p.n_heads), j = x.h - first_head(kvh, p.n_heads, p.n_kv_heads);
+        const int4 *rp = reinterpret_cast<const int4 *>(pl.row + x.b);
+        const int4 ow = rp[0], re = rp[1], tc = rp[2], in = rp[3];
+        if (TREE && in.y) {
+            x.b = -1;
+            return x;
+        }
+        if constexpr (!TREE) range(ow, kvh, j, gq, &x.own_n, &x.own_row);
+        if (p.G) {
+            const int n = tc.w * gq, mi = in.x * gq + j;
+            range(re, kvh, mi, n, &x.rest_n, &x.rest_row);
+            if (tc.y) {
+                const int run = mi / tc_run(f32), cost = tc_cost(n, p.head_size, f32);
+                const int u0 = tc.x + (kvh * tc_runs(n, f32) + run) * (kTcItemCost + tc.y * cost), w0 = walker_of(u0, per_tc);
+                x.tc_rows = min(tc_run(f32), n - run * tc_run(f32));
+                x.tc_n = (walker_of(u0 + tile_place(tc.y - 1, kTcItemCost, cost), per_tc) - w0 + 1) << two_parts(x.tc_rows);
+                x.tc_row = tc.z + kvh * tc_head_rows(n, f32) + mi + tc_run(f32) * w0;
+            }
+        }
+        return x;
     };
-    float m = -CUDART_INF_F, l = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    // Where a warp takes several pairs, a lane finds each one's parts (the divisions are most of a merge of few parts).
+    const Parts mine = parts_of(bh0 + (kPairs > 1 ? lane % kPairs : 0));
 #pragma unroll 1
-    for (int e0 = 0; e0 < n; e0 += 32) {
-        const int e = e0 + lane, cnt = min(32, n - e0);
-        float2 ml = make_float2(-CUDART_INF_F, 0.f);
-        if (e < n) {
-            const float2 *pm;
-            const float *acc;
-            part(e, pm, acc);
-            ml = *pm;
-        }
-        float4 v[kEarly];
-#pragma unroll
-        for (int q = 0; q < kEarly; ++q)
-            if (on && q * at_once + sub < cnt) v[q] = sums(e0 + q * at_once + sub);
-        const bool some = !(ml.x == -CUDART_INF_F && ml.y == 0.f);  // a part without keys has sums of no matter
-        float mn = fmaxf(m, ml.x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        const float base = mn == -CUDART_INF_F ? 0.f : mn;
-        const float c0 = exp2f(m - base), wt = exp2f(ml.x - base);
-        float ls = some ? ml.y * wt : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-        l = l * c0 + ls;
-        m = mn;
-        a.x *= c0;
-        a.y *= c0;
-        a.z *= c0;
-        a.w *= c0;
-        const unsigned have = __ballot_sync(0xffffffffu, some);
-        auto add = [&](int q, const float4 &x, float w) {
-            if (on && q < cnt && (have >> q & 1)) {
-                a.x = fmaf(x.x, w, a.x);
-                a.y = fmaf(x.y, w, a.y);
-                a.z = fmaf(x.z, w, a.z);
-                a.w = fmaf(x.w, w, a.w);
+    for (int pair = 0; pair < kPairs; ++pair) {
+        auto at_lane = [&](int x) { return kPairs > 1 ? __shfl_sync(0xffffffffu, x, pair) : x; };
+        const int b = at_lane(mine.b), h = at_lane(mine.h);
+        if (b < 0) continue;
+        const int own_row = TREE ? 0 : at_lane(mine.own_row), rest_n = at_lane(mine.rest_n), rest_row = at_lane(mine.rest_row);
+        const int tc_n = at_lane(mine.tc_n), tc_row = at_lane(mine.tc_row), tc_rows = at_lane(mine.tc_rows), tc_two = two_parts(tc_rows);
+        const int total = tc_n + rest_n + (TREE ? 0 : at_lane(mine.own_n)), n = (total + NW - 1 - warp) / NW;  // parts of the row, of this warp
+        // (m, l) and sums of the warp's i-th part
+        auto part = [&](int i, const float2 *&ml, const float *&acc) {
+            int e = i * NW + warp;
+            if (e < tc_n) {
+                const size_t at = (size_t)(tc_row + tc_run(f32) * (e >> tc_two) + (tc_two ? (e & 1) * tc_rows : 0));
+                ml = reinterpret_cast<const float2 *>(p.tc_ml) + at;
+                acc = p.tc_acc + at * p.head_size;
+            } else {
+                e -= tc_n;
+                const size_t at = (size_t)(e < rest_n ? rest_row + (e << shift) : own_row + ((e - rest_n) << shift));
+                ml = reinterpret_cast<const float2 *>(p.ws_ml) + at;
+                acc = p.ws_acc + at * p.head_size;
             }
         };
+        auto sums = [&](int e) {
+            const float2 *ml;
+            const float *acc;
+            part(e, ml, acc);
+            return *reinterpret_cast<const float4 *>(acc + d);
+        };
+        float m = -CUDART_INF_F, l = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int e0 = 0; e0 < n; e0 += 32) {
+            const int e = e0 + lane, cnt = min(32, n - e0);
+            float2 ml = make_float2(-CUDART_INF_F, 0.f);
+            if (e < n) {
+                const float2 *pm;
+                const float *acc;
+                part(e, pm, acc);
+                ml = *pm;
+            }
+            float4 v[kEarly];
 #pragma unroll
-        for (int q = 0; q < kEarly; ++q) {
-            const int i = q * at_once + sub;
-            add(i, v[q], __shfl_sync(0xffffffffu, wt, i & 31));
-        }
+            for (int q = 0; q < kEarly; ++q)
+                if (on && q * at_once + sub < cnt) v[q] = sums(e0 + q * at_once + sub);
+            const bool some = !(ml.x == -CUDART_INF_F && ml.y == 0.f);  // a part without keys has sums of no matter
+            float mn = fmaxf(m, ml.x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            const float base = mn == -CUDART_INF_F ? 0.f : mn;
+            const float c0 = exp2f(m - base), wt = exp2f(ml.x - base);
+            float ls = some ? ml.y * wt : 0.f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+            l = l * c0 + ls;
+            m = mn;
+            a.x *= c0;
+            a.y *= c0;
+            a.z *= c0;
+            a.w *= c0;
+            const unsigned have = __ballot_sync(0xffffffffu, some);
+            auto add = [&](int q, const float4 &x, float w) {
+                if (on && q < cnt && (have >> q & 1)) {
+                    a.x = fmaf(x.x, w, a.x);
+                    a.y = fmaf(x.y, w, a.y);
+                    a.z = fmaf(x.z, w, a.z);
+                    a.w = fmaf(x.w, w, a.w);
+                }
+            };
+#pragma unroll
+            for (int q = 0; q < kEarly; ++q) {
+                const int i = q * at_once + sub;
+                add(i, v[q], __shfl_sync(0xffffffffu, wt, i & 31));
+            }
 #pragma unroll 4
-        for (int q = kEarly * at_once; q < cnt; q += at_once) {
-            const int i = q + sub;
-            const float w = __shfl_sync(0xffffffffu, wt, i & 31);
-            if (on && i < cnt) add(i, sums(e0 + i), w);
+            for (int q = kEarly * at_once; q < cnt; q += at_once) {
+                const int i = q + sub;
+                const float w = __shfl_sync(0xffffffffu, wt, i & 31);
+                if (on && i < cnt) add(i, sums(e0 + i), w);
+            }
         }
+#pragma unroll
+        for (int o = 16; o >= 8; o >>= 1)
+            if (o >= LP) {
+                a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+                a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+                a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+                a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+            }
+        if constexpr (NW > 1) {
+            if (sub == 0) sa[warp][lane] = a;
+            if (lane == 0) {
+                sm[warp] = m;
+                sl[warp] = l;
+            }
+            __syncthreads();
+            if (warp) return;
+#pragma unroll
+            for (int w = 1; w < NW; ++w) m = fmaxf(m, sm[w]);
+            const float base = m == -CUDART_INF_F ? 0.f : m;
+            l = 0.f;
+            a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                if (w >= total) break;  // a warp without parts
+                const float c = exp2f(sm[w] - base);
+                const float4 v = sa[w][lane % LP];
+                l = fmaf(sl[w], c, l);
+                a.x = fmaf(v.x, c, a.x);
+                a.y = fmaf(v.y, c, a.y);
+                a.z = fmaf(v.z, c, a.z);
+                a.w = fmaf(v.w, c, a.w);
+            }
+        }
+        // no keys at all: zeros, and a sum of nothing; all scores -inf: 0 / 0, as the formula has it
+        const float inv = total ? 1.0f / l : 0.f;
+        if (on && sub == 0)
+            store_out<T>(p.out + (long long)b * p.o_row + (long long)h * p.o_head, d,
+                         total ? make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
+        if (p.lse && lane == 0) p.lse[(size_t)b * p.n_heads + h] = total ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
     }
-#pragma unroll
-    for (int o = 16; o >= 8; o >>= 1)
-        if (o >= LP) {
-            a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
-            a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
-            a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
-            a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
-        }
-    if constexpr (NW > 1) {
-        if (sub == 0) sa[warp][lane] = a;
-        if (lane == 0) {
-            sm[warp] = m;
-            sl[warp] = l;
-        }
-        __syncthreads();
-        if (warp) return;
-#pragma unroll
-        for (int w = 1; w < NW; ++w) m = fmaxf(m, sm[w]);
-        const float base = m == -CUDART_INF_F ? 0.f : m;
-        l = 0.f;
-        a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if (w >= total) break;  // a warp without parts
-            const float c = exp2f(sm[w] - base);
-            const float4 v = sa[w][lane % LP];
-            l = fmaf(sl[w], c, l);
-            a.x = fmaf(v.x, c, a.x);
-            a.y = fmaf(v.y, c, a.y);
-            a.z = fmaf(v.z, c, a.z);
-            a.w = fmaf(v.w, c, a.w);
-        }
-    }
-    // no keys at all: zeros, and a sum of nothing; all scores -inf: 0 / 0, as the formula has it
-    const float inv = total ? 1.0f / l : 0.f;
-    if (on && sub == 0)
-        store_out<T>(p.out + (long long)b * p.o_row + (long long)h * p.o_head, d,
-                     total ? make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f));
-    if (p.lse && lane == 0) p.lse[(size_t)b * p.n_heads + h] = total ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
 }
 
 namespace {
@@ -298,9 +320,13 @@ WsLayout ws_layout(int B, int G, int n_heads, int n_kv_heads, int head_size, int
 }
 
 template <typename T, bool TREE>
-cudaError_t launch_merge(const PagesAttn &p, bool few, const cudaLaunchConfig_t &cfg) {
+cudaError_t launch_merge(const PagesAttn &p, bool few, cudaLaunchConfig_t cfg) {
+    const int pairs = p.B * p.n_heads;
     if constexpr (TREE)
-        if (p.B * p.n_heads > kManyPairs) return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<T, 1, true, true>, p);
+        if (pairs > kManyPairs) {
+            cfg.gridDim = dim3((pairs + 4 * kPairsOf<true> - 1) / (4 * kPairsOf<true>));
+            return cudaLaunchKernelEx(&cfg, attn_pages_merge_kernel<T, 1, true, true>, p);
+        }
     return cudaLaunchKernelEx(&cfg, few ? attn_pages_merge_kernel<T, 4, TREE, false> : attn_pages_merge_kernel<T, 1, TREE, false>, p);
 }
 

@@ -81,7 +81,7 @@ struct DeviceOnce {
 constexpr int kWalkWarps = 8;
 __host__ __device__ constexpr int walk_first(bool tc) { return tc ? 4 : 0; }
 // Blocks of teams over 16-bit caches walk with twelve warps of 168 registers: a walk waits for its own chain of scores, softmax and products more than
-// for HBM (64 chains of 5 tokens on 1000 to 8200 keys, 20 pairs a KV head, 256 us; with eight warps 285).
+// for HBM (64 chains of 5 tokens on 1000 to 8200 keys, 20 pairs a KV head, 254 us; with eight warps 283).
 constexpr int kTeamWarps = 12;
 __host__ __device__ constexpr int walk_warps(bool f32, int team) { return !f32 && team > 1 ? kTeamWarps : kWalkWarps; }
 __host__ __device__ constexpr int attn_threads(bool tc) { return 32 * (walk_first(tc) + kWalkWarps); }
