@@ -43,6 +43,26 @@ def test_teams_of_warps_and_uneven_heads(H, kv, hs, ps, seqs, dtype):
         check_attention(out, lse, q, rows_seen(rows, order, trees), dtype, 1 / math.sqrt(hs))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("hs,committed", [(40, [0, 30, 1, 700]), (128, [2500, 3, 64, 0])])
+def test_an_odd_number_of_very_many_pairs(hs, committed, dtype):
+    """255 rows of 33 heads: the last pair stands alone, and rows behind the last tree lie beside written ones."""
+    H, kv, sizes = 33, 3, [63, 64, 62, 63]
+    pool, rows, _, _ = build(dtype, H, kv, hs, 16, [(0, [p + n]) for p, n in zip(committed, sizes)], seed=hs)
+    trees = trees_of("wide", sizes, hs)
+    index, starts, parents, B = call_of(range(4), trees)
+    room = 255
+    parents = torch.cat([parents, torch.full((room - B,), -7, dtype=torch.int32, device="cuda")])
+    g = torch.Generator(device="cuda").manual_seed(hs)
+    q = torch.randn((room, H, hs), generator=g, device="cuda").to(DT[dtype])
+    out = torch.full((room, H, hs), 7.0, device="cuda").to(DT[dtype])
+    lse = torch.full((room, H), 7.0, device="cuda")
+    pool.tree_attention(q, 0, index, starts, parents=parents, out=out, lse=lse)
+    pool.check()
+    check_attention(out[:B], lse[:B], q[:B], rows_seen(rows, range(4), trees), dtype, 1 / math.sqrt(hs))
+    assert bool((out[B:] == 7.0).all()) and bool((lse[B:] == 7.0).all())
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_tables_with_room_for_very_long_sequences(dtype):
     """Sequences as long as their tables would be too many keys to number in 32 bits, so a kernel plans the call by its lengths."""
