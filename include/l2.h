@@ -615,7 +615,7 @@ typedef struct {
     long long history_stride;        /* ints, at least max_len */
     const int *history;              /* DEVICE [n_seqs][max_len] */
     const int *lens, *counted_from;  /* DEVICE [n_seqs], counted_from or NULL */
-    const float *repetition, *presence, *frequency; /* DEVICE [n_seqs], each or NULL; repetition above 0 */
+    const float *repetition, *presence, *frequency; /* DEVICE [n_seqs], each or NULL; repetition 2^-126 .. 2^126, so that its inverse is a normal number, too */
     const int *bias_starts;          /* DEVICE [n_seqs + 1]: entries of sequence s */
     const int *bias_tokens;          /* DEVICE [n_bias] */
     const float *bias_values;        /* DEVICE [n_bias] */

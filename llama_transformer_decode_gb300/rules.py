@@ -23,7 +23,7 @@ class TokenRules:
     """The rules of ``n_seqs`` sequences over a vocabulary of ``vocab_size`` tokens.
 
     ``history`` [n_seqs][room] and ``lens`` [n_seqs]: int32 CUDA tensors, the tokens each sequence holds; the caller changes them as
-    sequences grow.  ``repetition``, ``presence``, ``frequency``: float32 [n_seqs] or None.  ``counted_from``: int32 [n_seqs] or
+    sequences grow.  ``repetition``, ``presence``, ``frequency``: float32 [n_seqs] or None (``repetition`` above 0).  ``counted_from``: int32 [n_seqs] or
     None, where the latter two begin to count.  ``bias``: (starts int32 [n_seqs + 1], tokens int32, values float32) or None: entries
     starts[s]..starts[s + 1] - 1 are sequence s's.  All are kept, and read by each call when it runs.
     """
