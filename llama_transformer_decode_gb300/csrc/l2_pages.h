@@ -19,7 +19,8 @@ constexpr int kPagesThreads = 1024;  // threads of the one-block bookkeeping ker
 
 // Integers at the head of a pool's scratch: whether the last fork or free was refused (the kernel that copies its rows then does
 // nothing), the pages a compaction moves, and whether the last extension was refused, which holds for the step's other
-// layers too, whatever is called between them.  Then three lists of n_pages entries.
+// layers too, whatever is called between them.  Then three lists of n_pages entries; the second, of the pages that a compaction
+// moves, is at most half full, and its other half is PagesView::missing.
 enum : int { kScrRefused = 0, kScrMoved = 1, kScrExtension = 2, kScrHead = 8 };
 
 // A page pool.  Rows of head_size elements; strides in bytes.  Position p of sequence s is
@@ -30,6 +31,11 @@ struct PagesView {
     long long layer_stride, page_stride, head_stride, row_stride;  // bytes
     int n_layers, n_pages, n_kv_heads, page_size, n_seqs, max_pages;
     int row_bytes;  // head_size * element size, a multiple of 16
+
+    // A byte a page, not 0 where a sequence that ends in the page does not have the rows that its last step meant to give it: its last
+    // extension was refused, or rows of another layer were left out since.  That lasts until an extension of its own
+    // succeeds, whatever others do, so that what it had committed is not taken for such rows.
+    __host__ __device__ unsigned char *missing() const { return reinterpret_cast<unsigned char *>(scratch + kScrHead + n_pages + n_pages / 2); }
 };
 
 struct PagesAppend {

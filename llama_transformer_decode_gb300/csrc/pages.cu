@@ -116,6 +116,12 @@ __device__ __forceinline__ void refuse(const PagesView &p, int bit, int flag = k
 __device__ __forceinline__ bool page_ok(const PagesView &p, int page) { return page >= 0 && page < p.n_pages; }
 __device__ __forceinline__ bool page_held(const PagesView &p, int page) { return page_ok(p, page) && p.refs[page] > 0; }
 
+// The page that a sequence of n rows ends in, -1 where it has none.
+__device__ __forceinline__ int last_page(const PagesView &p, int s, int n) {
+    const int page = n > 0 && n <= (long long)p.max_pages * p.page_size ? p.table[(size_t)s * p.max_pages + (n - 1) / p.page_size] : -1;
+    return page_ok(p, page) ? page : -1;
+}
+
 }  // namespace
 
 // Append, first half: lens[seqs[i]] grows by its rows and takes the pages that needs, the
@@ -128,10 +134,11 @@ __global__ void __launch_bounds__(kT) pages_extend_kernel(const PagesView p, int
     const int s = i < n ? seqs[i] : -1;
     sq[i] = s;
     __syncthreads();
-    bool bad = false;
-    int old = 0, cnt = 0, have = 0, want = 0;
+    bool bad = false, named = false;
+    int old = 0, cnt = 0, have = 0, want = 0, last = -1;
     if (i < n) {
         const int a = starts ? starts[i] : i, b = starts ? starts[i + 1] : i + 1;
+        named = s >= 0 && s < p.n_seqs && a != b;
         bad = s < 0 || s >= p.n_seqs || a < 0 || b < a || b > rows || (i == 0 && a != 0) || (i == n - 1 && b != rows);
         for (int j = 0; j < i; ++j) bad |= sq[j] == s;
         if (!bad) {
@@ -143,19 +150,25 @@ __global__ void __launch_bounds__(kT) pages_extend_kernel(const PagesView p, int
             have = ceil_div_d(old, p.page_size);
             want = ceil_div_d(old + cnt, p.page_size);
             // rows go into a partly filled last page only if no other sequence holds it
-            if (cnt > 0 && old % p.page_size) {
-                const int page = p.table[(size_t)s * p.max_pages + have - 1];
-                bad = !page_ok(p, page) || p.refs[page] != 1;
+            if (cnt > 0 && old > 0) {
+                last = p.table[(size_t)s * p.max_pages + have - 1];
+                if (!page_ok(p, last) || p.refs[last] != 1) last = -1;
+                bad = last < 0 && old % p.page_size;
             }
         }
     }
-    if (__syncthreads_or(bad)) return refuse(p, L2_PAGES_ERR_ARGS, kScrExtension);
+    auto refused = [&](int bit) {
+        if (named)
+            if (const int page = last_page(p, s, p.lens[s]); page >= 0) p.missing()[page] = 1;
+        refuse(p, bit, kScrExtension);
+    };
+    if (__syncthreads_or(bad)) return refused(L2_PAGES_ERR_ARGS);
     int need;
     const int base = block_scan(want - have, &need, buf);
     base_s[i] = base;
     if (i == 0) base_s[kT] = need;
     int *list = p.scratch + kScrHead;
-    if (need > p.n_pages || lowest_free(p, need, list, buf) < need) return refuse(p, L2_PAGES_ERR_FULL, kScrExtension);
+    if (need > p.n_pages || lowest_free(p, need, list, buf) < need) return refused(L2_PAGES_ERR_FULL);
     // page e of the list belongs to the last sequence whose base is at most e and that takes pages
     for (int e = i; e < need; e += kT) {
         int lo = 0, hi = n;  // base_s[lo] <= e < base_s[hi]
@@ -167,9 +180,11 @@ __global__ void __launch_bounds__(kT) pages_extend_kernel(const PagesView p, int
         const int page = list[e];
         p.table[(size_t)t * p.max_pages + h + e - base_s[lo]] = page;
         p.refs[page] = 1;
+        p.missing()[page] = 0;
     }
     __syncthreads();  // the lengths above are read
     if (i < n) p.lens[s] = old + cnt;
+    if (last >= 0) p.missing()[last] = 0;  // (of a page that others end in, too, it stays theirs)
     if (i == 0) p.scratch[kScrExtension] = 0;
 }
 
@@ -185,7 +200,7 @@ __global__ void __launch_bounds__(256) pages_rows_kernel(const PagesView p, cons
     const int groups = ceil_div_d(a.n_layers, layers_per);
     if (warp >= a.rows * groups) return;
     const int r = warp / groups, lg = warp - r * groups;
-    if (!READ && p.scratch[kScrExtension]) return;
+    const bool left_out = !READ && p.scratch[kScrExtension];
     int i = r, start = r, end = r + 1;
     if (a.starts) {
         int lo = 0, hi = a.n;
@@ -199,6 +214,15 @@ __global__ void __launch_bounds__(256) pages_rows_kernel(const PagesView p, cons
     }
     const int s = a.seqs[i];
     const int n = s >= 0 && s < p.n_seqs ? p.lens[s] : -1;
+    if (!READ && a.extended && left_out) return;
+    if (!READ && !a.extended) {
+        const int last = last_page(p, s, n);
+        if (left_out) {
+            if (last >= 0 && lane == 0) p.missing()[last] = 1;
+            return;
+        }
+        if (last >= 0 && p.missing()[last]) return;  // its last rows are not these
+    }
     const int pos = n < 0 ? -1 : READ ? r - start : n - (end - r);
     if (READ && (r < start || r >= end || pos >= n)) {  // no such row
         if (lane == 0) atomicOr(p.err, L2_PAGES_ERR_ARGS);
@@ -298,6 +322,7 @@ __global__ void __launch_bounds__(kT) pages_fork_kernel(const PagesView p, int n
             const int page = list[base];
             p.table[(size_t)d * p.max_pages + full] = page;
             p.refs[page] = 1;
+            p.missing()[page] = p.missing()[p.table[(size_t)s * p.max_pages + full]];
         }
         p.lens[d] = m;
     }
@@ -409,6 +434,7 @@ __global__ void __launch_bounds__(kT) pages_free_kernel(const PagesView p, int n
         to[a] = b;
         p.refs[b] = __ldcg(p.refs + a);
         p.refs[a] = 0;
+        p.missing()[b] = p.missing()[a];
     }
     if (i == 0) p.scratch[kScrMoved] = moved;
 }

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
     if (i == 0) why = 0;
     __syncthreads();
     bool bad = false;
+    int end = -1;  // page that the sequence ends in
     if (i < a.n) {
         const int b0 = a.starts[i], b1 = a.starts[i + 1];
         bad = s < 0 || s >= p.n_seqs || b0 < 0 || b1 < b0 || b1 > a.rows || b1 - b0 > kTreeNodes || (i == 0 && b0 != 0);
@@ -110,12 +111,15 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
         if (!bad) {
             len = p.lens[s];
             bad = len < b1 - b0 || len > (long long)p.max_pages * p.page_size;
+            if (!bad && b1 > b0) end = p.table[(size_t)s * p.max_pages + (len - 1) / p.page_size];
         }
         first_s[i] = b0;
         n_s[i] = b1 - b0;
         len_s[i] = len;
     }
     if (__syncthreads_or(bad)) return refuse(p, a, L2_PAGES_ERR_ARGS);
+    // whether its last rows are others than the tree's (see PagesView::missing), which is known when the paths are
+    const bool without_rows = page_ok(p, end) && p.missing()[end];
     // the paths, a warp each
     for (int e = warp; e < a.n; e += kT / 32) {
         const int n = n_s[e], first = first_s[e];
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kT) pages_accept_kernel(const PagesView p, con
             last_s[e] = last;
         }
     }
-    if (__syncthreads_or(bad)) return refuse(p, a, L2_PAGES_ERR_ARGS);
+    if (__syncthreads_or(bad || without_rows)) return refuse(p, a, L2_PAGES_ERR_ARGS);
     // pages that rows move into, and the partly filled last one, must be the sequence's alone; those that rows come from and those
     // that are given back must exist
     for (int e = warp; e < a.n; e += kT / 32) {

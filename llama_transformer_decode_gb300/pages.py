@@ -255,7 +255,8 @@ class PagePool:
         """Finds the path of each tree that the model agrees with and shortens the sequences to it (``l2_pages_accept``):
         token 0, then the first child of each accepted token whose token is what was sampled from that one's logits
         (``targets``).  Returns int32 tensors ``path`` (each tree's accepted places, then -1), ``counts`` and ``next`` (the target
-        of the last accepted token).  A call that the device refuses (``check``) accepts nothing: counts 0, the others -1."""
+        of the last accepted token).  A call that the device refuses (``check``) accepts nothing: counts 0, the others -1; so do
+        sequences whose append was refused before it."""
         rows, n, ints = tokens.shape[0], seqs.shape[0], self._ints
         made = self._made(rows + 2 * n, stream)
         at = made.data_ptr()
