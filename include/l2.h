@@ -587,7 +587,8 @@ typedef struct {
 int l2_rope_plan(L2RopePlan *plan, int rot_dim, int layout, const double *freqs, double amplitude);
 
 /* q and k (either may be NULL, with no heads) are turned in one launch, in place where q_out = q with q's strides; otherwise the
- * outputs share no memory with the inputs. */
+ * outputs share no memory with the inputs, nor with each other.  They may lie in one piece of memory, side by side in its rows or in each
+ * head, where the row strides are the same; with other row strides one has to lie behind the other. */
 typedef struct {
     int rows;                /* 0..2^24 - 1 */
     int dtype;               /* L2_F32, L2_BF16, L2_F16 */

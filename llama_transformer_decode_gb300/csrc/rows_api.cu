@@ -28,13 +28,34 @@ struct Extent {
     long long columns() const { return (heads - 1) * head + width; }  // from a row's first byte to its last one's end
     long long bytes() const { return (rows - 1) * row + columns(); }
 };
-// Whether two tensors have no byte in common: one lies behind the other, or they are columns of one matrix (parts of a projection's
-// output).  Other layouts that would share none are taken for ones that do.
+// Whether two tensors of as many rows have no byte in common.  Exact where their rows are alike apart (parts of a projection's output,
+// side by side in a row or in each head); others are taken for sharing some unless one lies behind the other.
 bool apart(const Extent &a, const Extent &b) {
     if (a.p + a.bytes() <= b.p || b.p + b.bytes() <= a.p) return true;
-    if (a.rows < 2 || b.rows < 2 || a.row != b.row || a.columns() > a.row || b.columns() > a.row) return false;
-    const long long d = ((b.p - a.p) % a.row + a.row) % a.row;  // b's first column, counted from a's
-    return d >= a.columns() && d + b.columns() <= a.row;
+    if (a.rows != b.rows || (a.rows > 1 && a.row != b.row)) return false;
+    const long long d = b.p - a.p, row = a.rows > 1 ? a.row : 0;
+    if (row >= a.columns() && row >= b.columns()) {  // columns of one matrix
+        const long long c = (d % row + row) % row;
+        if (c >= a.columns() && c + b.columns() <= row) return true;
+    }
+    // A head of b and one of a, x bytes apart in the same row, meet where some difference of rows makes x + r * row less than a head's width
+    // either way.
+    auto meet = [&](long long x) {
+        const long long w = a.width, v = b.width;  // from a's head on, b's begins above -v and below w
+        if (!row) return x > -v && x < w;
+        const long long r = (w - 1 - x) / row - ((w - 1 - x) % row < 0);  // the most rows that leave it below w
+        return r >= 1 - a.rows && x + (r < a.rows ? r : a.rows - 1) * row > -v;
+    };
+    if (a.heads < 2 || b.heads < 2 || a.head == b.head) {  // differences of heads are all that matters
+        const long long head = a.heads > 1 ? a.head : b.head;
+        for (int h = 1 - a.heads; h < b.heads; ++h)
+            if (meet(d + h * head)) return false;
+        return true;
+    }
+    for (int i = 0; i < a.heads; ++i)
+        for (int j = 0; j < b.heads; ++j)
+            if (meet(d + j * b.head - i * a.head)) return false;
+    return true;
 }
 
 int check_dtype(const char *who, const char *name, int dtype) {
