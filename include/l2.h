@@ -564,8 +564,9 @@ int l2_pages_keep(const L2Pages *pool, const L2PagesAccept *args, void *cuda_str
  *   L2_ROPE_BASE     with base * factor^(rot_dim / (rot_dim - 2)) for base: the slowest pair is slowed by factor, the first not;
  *   L2_ROPE_BANDS    by wavelength: with t = original_len * freq / (2 pi) turns over the trained length, freq * (s + (1 - s) / factor),
  *                    s = (t - low) / (high - low) clamped to 0..1: fast pairs stay, slow ones are slowed by factor.
- * l2_rope_plan takes such frequencies, or a caller's own (finite), once; angles are exact to 2^-52 of p * freq
- * and rounded to fp32 within half a turn, so far positions lose nothing.  Positions are int32, of either sign.
+ * l2_rope_plan takes such frequencies, or a caller's own (finite, of either sign), once; a pair's angle at position p is off by at most |p| 2^-65
+ * turns (a frequency is held as a 64-bit fraction of a turn: those below 2^-65 turns a position turn nothing) and 2^-52 of p * freq, and is
+ * rounded to fp32 within half a turn, so far positions lose nothing that fp32 holds.  Positions are int32, of either sign.
  */
 #define L2_ROPE_INTERLEAVED 0
 #define L2_ROPE_HALF 1

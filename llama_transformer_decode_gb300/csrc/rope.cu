@@ -7,7 +7,8 @@
 //
 // Angles.  p f_i in fp32 is off by 0.06 at position 10^6.  What matters of it is the part of a turn that it ends on, so the
 // frequency is held as a 64-bit fraction of a turn (2^64 f / 2 pi, mod 2^64): the product with an integer position, mod 2^64,
-// is that part exactly, for positions of either sign, and the fraction's own rounding (2^-53 of f) is all that is lost.
+// is that part exactly, for positions of either sign, and what is lost is the fraction's own rounding: 2^-65 of a turn a position (2^-34 of
+// one at the farthest), and 2^-52 of f for its quotient in double.
 // The high bits as fp32 half-turns go to sincospif: an angle in [-pi, pi] off by at most 2^-24 of itself.
 //
 // How.  HBM bounds it (every element is read and written once), at a few rows the latency of one launch.  A unit is one access of

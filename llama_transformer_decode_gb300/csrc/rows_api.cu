@@ -134,10 +134,12 @@ int l2_rope_plan(L2RopePlan *plan, int rot_dim, int layout, const double *freqs,
     if (!std::isfinite((float)amplitude)) return refuse(L2_EINVAL, "%s: amplitude must be finite, in fp32 too", who);
     for (int i = 0; i < rot_dim / 2; ++i) {
         if (!std::isfinite(freqs[i])) return refuse(L2_EINVAL, "%s: frequency %d is not finite", who, i);
-        double t = freqs[i] / kTwoPi;
-        t -= std::floor(t);  // whole turns do nothing at whole positions
+        // of the frequency's size, which keeps a slow pair's bits when it turns back, too; whole turns do nothing at whole positions
+        double t = std::fabs(freqs[i]) / kTwoPi;
+        t -= std::floor(t);
         const double x = std::nearbyint(std::ldexp(t, 64));
-        plan->turns[i] = x >= 18446744073709551616.0 ? 0 : (unsigned long long)x;
+        const unsigned long long turns = x >= 18446744073709551616.0 ? 0 : (unsigned long long)x;
+        plan->turns[i] = freqs[i] < 0 ? 0 - turns : turns;
     }
     plan->rot_dim = rot_dim;
     plan->layout = layout;
