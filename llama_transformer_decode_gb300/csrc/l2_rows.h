@@ -52,7 +52,7 @@ struct RulesParams {
     // filled in by the launch
     int slice, rows_per;         // tokens and rows of a block
 };
-// vec: elements an access (1, 4, or 8 of 16 bits), which every row's address allows.
+// vec: elements an access (1 or 4, or 8 from 16 bits to 16 bits), which every row's address allows.
 cudaError_t launch_rules(RulesParams p, int dtype, bool out_f32, int vec, int num_sms, cudaStream_t s);
 
 }  // namespace l2

@@ -276,7 +276,7 @@ cudaError_t launch(const RulesParams &p, cudaLaunchConfig_t cfg) {
 }
 template <typename TI, typename TO>
 cudaError_t launch(const RulesParams &p, int vec, cudaLaunchConfig_t cfg) {
-    if constexpr (sizeof(TI) == 2)
+    if constexpr (sizeof(TI) == 2 && sizeof(TO) == 2)
         if (vec == 8) return p.n_bias > 0 ? launch<TI, TO, 8, true>(p, cfg) : launch<TI, TO, 8, false>(p, cfg);
     if (vec >= 4) return p.n_bias > 0 ? launch<TI, TO, 4, true>(p, cfg) : launch<TI, TO, 4, false>(p, cfg);
     return p.n_bias > 0 ? launch<TI, TO, 1, true>(p, cfg) : launch<TI, TO, 1, false>(p, cfg);
