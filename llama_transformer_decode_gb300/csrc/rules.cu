@@ -39,7 +39,10 @@ constexpr int kMaxSlice = 8192;   // tokens of a block: two tables of 32 KB
 constexpr int kMinSlice = 1024;
 constexpr int kMostRows = 32;     // rows of a block, where they come in trees
 constexpr float kTableRows = 4.f; // what making the tables takes, in rows
-constexpr int kBlocks = 4;        // blocks of an SM
+// Blocks of an SM: as many as registers allow (80 a thread where an access has 8 elements), and with biases no more than two tables of
+// the largest slice leave room for.
+constexpr int reg_blocks(int width) { return width == 8 ? 3 : 4; }
+constexpr int blocks_of(int width, bool bias) { return bias ? 3 : reg_blocks(width); }
 constexpr unsigned kSeen = 1u << 31, kCount = (1u << 24) - 1;
 constexpr int kKindShift = 24;    // 7 bits: 1 + the place
 constexpr unsigned kKind = 0x7fu << kKindShift;
@@ -60,7 +63,7 @@ struct alignas(sizeof(T) * W) Piece {
 
 // TI, TO: types of logits and results; W: elements an access; BIAS: the call has biases (a second table).
 template <typename TI, typename TO, int W, bool BIAS>
-__global__ void __launch_bounds__(kThreads, W == 8 ? 3 : kBlocks) rules_kernel(const RulesParams p) {
+__global__ void __launch_bounds__(kThreads, reg_blocks(W)) rules_kernel(const RulesParams p) {
     extern __shared__ __align__(16) unsigned count[];  // [slice], and [slice] numbers of bias entries
     __shared__ u64 words[kTreeNodes], kinds[kTreeNodes];
     __shared__ int tokens[kTreeNodes], tree_ok;
@@ -287,8 +290,9 @@ cudaError_t launch(const RulesParams &p, int vec, cudaLaunchConfig_t cfg) {
 cudaError_t launch_rules(RulesParams p, int dtype, bool out_f32, int vec, int num_sms, cudaStream_t s) {
     if (p.rows == 0) return cudaSuccess;
     // The largest slice, since each counts the history anew, that still gives every SM blocks; rows of trees (on average rows / n) as many to
-    // a block as make rounds of blocks over the SMs times a block's rows least, a table counting as kTableRows of them.
-    const int at_once = kBlocks * num_sms;
+    // a block as make rounds of blocks over the SMs times a block's rows least, a table counting as kTableRows of them.  (480 rows of 128000, bf16: with
+    // rounds of three blocks an SM, which is what there is room for, 76 us, with biases 104, to fp32 98; with rounds of four 89, 132, 116.)
+    const int at_once = blocks_of(vec, p.n_bias > 0) * num_sms;
     p.rows_per = 1;
     p.slice = kMaxSlice;
     auto slices = [&]() { return (p.vocab + p.slice - 1) / p.slice; };

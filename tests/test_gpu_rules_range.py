@@ -1,0 +1,43 @@
+"""Rules on logits over the whole range of their arguments, and before the sampler."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import llama_transformer_decode_gb300 as pkg  # noqa: E402
+from tests.test_gpu_rules import DT, Made, check, dev, f32  # noqa: E402
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("bias", [0, 6])
+@pytest.mark.parametrize("V,sizes", [(2048, [40] * 30), (16384, [64] * 9), (8192 + 8, [33] * 20), (8192 + 4, [33] * 20)])
+def test_trees_of_every_kernel(V, sizes, bias, dtype, out):
+    """Rows that come in trees, several to a block, with biases and without, 16 and 8 bytes an access."""
+    n = len(sizes)
+    m = Made(V, n, 50, V + n, bias=bias)
+    starts = np.concatenate([[0], np.cumsum(sizes)])
+    rows = int(starts[-1])
+    drafted = m.rng.integers(0, 40, rows)
+    parents = np.concatenate([[-1] + [int(m.rng.integers(0, u)) for u in range(1, k)] for k in sizes])
+    logits = (torch.randn((rows, V), device="cuda") * 3).to(DT[dtype])
+    which = m.rng.integers(-1, 5, rows)
+    got = m.rules.apply(logits, starts=dev(starts), parents=dev(parents), drafted=dev(drafted), masks=m.packed(), mask_rows=dev(which), out_dtype=DT[out])
+    m.rules.check()
+    x = logits.double().cpu().numpy()
+    for i in range(n):
+        for u in sorted({0, sizes[i] - 1, *m.rng.integers(0, sizes[i], 4).tolist()}):
+            r, path, at = int(starts[i]) + u, [], u
+            while at >= 0:
+                path.append(int(drafted[starts[i] + at]))
+                at = int(parents[starts[i] + at])
+            check(got[r], *m.row(x[r], i, path, None if which[r] < 0 else int(which[r])))
+    again = logits.clone()
+    if out == dtype:
+        m.rules.apply(again, starts=dev(starts), parents=dev(parents), drafted=dev(drafted), masks=m.packed(), mask_rows=dev(which), out=again)
+        assert torch.equal(again.view(torch.uint8), got.view(torch.uint8))
