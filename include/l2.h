@@ -606,7 +606,8 @@ int l2_rope(const L2RopePlan *plan, const L2RopeRows *rows, void *cuda_stream);
 /*
  * Rules on logits before l2_sample: penalties for tokens that a sequence already holds, biases, grammar masks.  For logit l of
  * token v in a row of sequence s, in fp32 and in this order:
- *   v in the history of s or on the row's path:     l = l > 0 ? l / repetition[s] : l * repetition[s];
+ *   v in the history of s or on the row's path:     l = l > 0 ? l / repetition[s] : l * repetition[s]
+ *                                                   (the quotient as l times the rounded inverse, within 2^-23 of it);
  *   n times, counted from counted_from[s] on, n > 0: l = l - (frequency[s] * n + presence[s]);
  *   v among the biases of s:                        l = l + its value (of the last entry that names it);
  *   bit v of the row's mask clear:                  l = -inf (whatever it was).

@@ -3,8 +3,8 @@
 // What it computes, for the logit l of token v in a row of sequence s (in fp32):
 //     seen:     v is in the sequence's history, or on the row's own path of drafted tokens;
 //     n:        how often, counting the history from counted_from[s] on;
-//     l -> l / repetition[s] where l > 0, else l * repetition[s], if seen (the quotient as a product with the rounded inverse:
-//          2^-23 of l at most, and a division for each logit that is seen bounds the slices of frequent tokens);
+//     l -> l / repetition[s] where l > 0, else l * repetition[s], if seen (the quotient as a product with the rounded inverse, two
+//          roundings: within 2^-23 of the quotient; a division for each logit that is seen bounds the slices of frequent tokens);
 //     l -> l - (frequency[s] n + presence[s]) if n > 0;
 //     l -> l + the value of the sequence's last bias entry of v, if it has one;
 //     l -> -inf where the row's mask has bit v clear.

@@ -14,6 +14,23 @@ from tests.test_gpu_rules import DT, Made, check, dev, f32  # noqa: E402
 U = 2.0 ** -24
 
 
+@pytest.mark.parametrize("V", [64, 67])
+def test_quotients_at_any_repetition_penalty(V):
+    """l > 0 seen: l times the rounded inverse, two roundings of at most U of the quotient each (and half of the least subnormal); l <= 0: one."""
+    rep = np.array([2.0 ** -126, 2.0 ** -100, 1e-20, 0.3, 0.7, 1.1, 3.0, 7e5, 2.0 ** 100, 1.9 * 2.0 ** 125, 2.0 ** 126], np.float32)
+    n = len(rep)
+    rules = pkg.TokenRules(V, dev(np.tile(np.arange(V), (n, 1))), dev([V] * n), repetition=f32(rep))
+    rng = np.random.default_rng(V)
+    x = (rng.uniform(0.13, 1.99, (n, V)) * rng.choice([-1, 1], (n, V))).astype(np.float32)
+    got = rules.apply(torch.from_numpy(x).cuda())
+    rules.check()
+    r = rep.astype(np.float64)[:, None]
+    want = np.where(x > 0, x / r, x * r)
+    tol = np.where(x > 0, 2.001, 1) * U * np.abs(want) + 2.0 ** -150
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "fp32"), ("fp32", "fp32")])
 @pytest.mark.parametrize("bias", [0, 6])
 @pytest.mark.parametrize("V,sizes", [(2048, [40] * 30), (16384, [64] * 9), (8192 + 8, [33] * 20), (8192 + 4, [33] * 20)])
