@@ -604,7 +604,8 @@ typedef struct {
 int l2_rope(const L2RopePlan *plan, const L2RopeRows *rows, void *cuda_stream);
 
 /*
- * Rules on logits before l2_sample: penalties for tokens that a sequence already holds, biases, grammar masks.  For logit l of
+ * Rules on logits before l2_sample: penalties for tokens that a sequence already holds, biases, grammar masks.  (Vocabularies
+ * may be larger than what l2_sample takes, 49152 tokens: rows of those are for a sampler of the caller's.)  For logit l of
  * token v in a row of sequence s, in fp32 and in this order:
  *   v in the history of s or on the row's path:     l = l > 0 ? l / repetition[s] : l * repetition[s]
  *                                                   (the quotient as l times the rounded inverse, within 2^-23 of it);

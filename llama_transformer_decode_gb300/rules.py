@@ -1,5 +1,6 @@
 """Rules on logits before sampling: penalties for tokens that a sequence already holds, biases, grammar
-masks (``l2_token_rules`` of ``include/l2.h``).  ``sample`` draws from what they leave.
+masks (``l2_token_rules`` of ``include/l2.h``).  ``sample`` draws from what they leave, where the vocabulary has at most
+49152 tokens; rules take up to 2^24.
 
 Arguments are marshalled here; counting and arithmetic are the CUDA kernel's.  Calls enqueue on
 ``stream`` (default: torch's current stream), never wait, and can be captured into a CUDA graph.

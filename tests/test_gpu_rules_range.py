@@ -58,3 +58,22 @@ def test_trees_of_every_kernel(V, sizes, bias, dtype, out):
     if out == dtype:
         m.rules.apply(again, starts=dev(starts), parents=dev(parents), drafted=dev(drafted), masks=m.packed(), mask_rows=dev(which), out=again)
         assert torch.equal(again.view(torch.uint8), got.view(torch.uint8))
+
+
+def test_the_samplers_vocabulary_is_smaller_than_the_rules():
+    """Rules take up to 2^24 tokens, the sampler 49152: more than that it refuses before anything runs."""
+    for V, fits in ((49152, True), (49153, False), (128000, False)):
+        rules = pkg.TokenRules(V, dev(np.zeros((2, 1))), dev([0, 0]))
+        masks = torch.zeros((2, -(-V // 32)), dtype=torch.int32, device="cuda")
+        masks[1, V // 64] = 1
+        logits = rules.apply(torch.randn((2, V), device="cuda"), masks=masks)
+        rng = torch.tensor([5, 6], dtype=torch.int64, device="cuda")
+        tokens = torch.full((2,), -5, dtype=torch.int32, device="cuda")
+        if fits:
+            pkg.sample(logits, 0.8, 0.9, rng, out=tokens)
+            assert tokens.tolist() == [0, V // 64 * 32]
+        else:
+            with pytest.raises(pkg.L2Error, match="49152"):
+                pkg.sample(logits, 0.8, 0.9, rng, out=tokens)
+            assert tokens.tolist() == [-5, -5] and rng.tolist() == [5, 6]
+            assert bool((logits[0] == -float("inf")).all()) and int(logits[1].argmax()) == V // 64 * 32
