@@ -410,11 +410,12 @@ typedef struct {
  * extends with its first layer (or all layers at once) and writes its other
  * layers with extend 0 and the same seqs and starts.  If the last extension
  * was refused, rows are not written until one succeeds.  Of the sequences that it
- * meant to give rows, and of those whose rows were left out meanwhile, none are
- * written and none accepted (l2_pages_accept) until an extension gives the
- * sequence itself rows, whatever succeeds for others.  Rows of an extend 0 call
- * that would go into a page other sequences hold are left out and reported
- * (L2_PAGES_BAD_CALL).
+ * meant to give rows none are written (L2_PAGES_BAD_CALL) and none accepted
+ * (l2_pages_accept) until an extension gives the sequence itself rows, whatever
+ * succeeds for others; of those whose rows were left out meanwhile none are
+ * accepted until then, or until they are written, from the lowest layer left out on.
+ * Rows of an extend 0 call that would go into a page other sequences hold are left
+ * out and reported (L2_PAGES_BAD_CALL).
  */
 int l2_pages_append(const L2Pages *pool, const L2PagesRows *rows, void *cuda_stream);
 
@@ -538,7 +539,7 @@ int l2_pages_tree_attention(const L2Pages *pool, const L2PagesTreeAttention *arg
  * given back, with the pages that become free.  l2_pages_keep does that with a path and counts that are given (0 <= counts[i]; the first
  * counts[i] entries ascending places of the tree), for callers with a rule of their own; tokens, targets, parents and next are NULL.
  * A page that rows move into, or that is left partly filled, must be held by its sequence alone.  A sequence with a tree whose last
- * extension was refused, or whose rows were left out of a layer since, is refused (see l2_pages_append): its last rows are not
+ * extension was refused, or whose rows were left out of a layer, is refused (see l2_pages_append): its last rows are not
  * the tree's, so a step that found no room loses nothing, although nothing waited between its calls.  A call that cannot be done
  * whole changes nothing (L2_PAGES_BAD_CALL, L2_PAGES_BAD_PAGE); counts of l2_pages_accept are then 0, path and next -1.
  */

@@ -22,6 +22,7 @@ constexpr int kPagesThreads = 1024;  // threads of the one-block bookkeeping ker
 // layers too, whatever is called between them.  Then three lists of n_pages entries; the second, of the pages that a compaction
 // moves, is at most half full, and its other half is PagesView::missing.
 enum : int { kScrRefused = 0, kScrMoved = 1, kScrExtension = 2, kScrHead = 8 };
+__host__ __device__ inline int left_out(int layer) { return 2 + (layer < 253 ? layer : 253); }
 
 // A page pool.  Rows of head_size elements; strides in bytes.  Position p of sequence s is
 // row p % page_size of page table[s * max_pages + p / page_size].
@@ -32,9 +33,10 @@ struct PagesView {
     int n_layers, n_pages, n_kv_heads, page_size, n_seqs, max_pages;
     int row_bytes;  // head_size * element size, a multiple of 16
 
-    // A byte a page, not 0 where a sequence that ends in the page does not have the rows that its last step meant to give it: its last
-    // extension was refused, or rows of another layer were left out since.  That lasts until an extension of its own
-    // succeeds, whatever others do, so that what it had committed is not taken for such rows.
+    // A byte a page, not 0 where a sequence that ends in the page does not have the rows that its last step meant to give it: 1 if its
+    // last extension was refused, or left_out(the lowest layer) if rows of it were left out while another's had been.  That lasts until an
+    // extension of its own succeeds, whatever others do, so that what it had committed is not taken for such rows; left-out rows may
+    // also be written again from that layer on.
     __host__ __device__ unsigned char *missing() const { return reinterpret_cast<unsigned char *>(scratch + kScrHead + n_pages + n_pages / 2); }
 };
 

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(256) pages_rows_kernel(const PagesView p, cons
     const int groups = ceil_div_d(a.n_layers, layers_per);
     if (warp >= a.rows * groups) return;
     const int r = warp / groups, lg = warp - r * groups;
-    const bool left_out = !READ && p.scratch[kScrExtension];
+    const bool held_back = !READ && p.scratch[kScrExtension];
     int i = r, start = r, end = r + 1;
     if (a.starts) {
         int lo = 0, hi = a.n;
@@ -214,14 +214,20 @@ __global__ void __launch_bounds__(256) pages_rows_kernel(const PagesView p, cons
     }
     const int s = a.seqs[i];
     const int n = s >= 0 && s < p.n_seqs ? p.lens[s] : -1;
-    if (!READ && a.extended && left_out) return;
+    if (!READ && a.extended && held_back) return;
+    int missing = 0;  // see PagesView::missing
     if (!READ && !a.extended) {
-        const int last = last_page(p, s, n);
-        if (left_out) {
-            if (last >= 0 && lane == 0) p.missing()[last] = 1;
+        const int last = last_page(p, s, n), here = left_out(a.layer0);
+        if (last >= 0) missing = p.missing()[last];
+        if (held_back) {
+            if (last >= 0 && lane == 0 && (!missing || missing > here)) p.missing()[last] = (unsigned char)here;
             return;
         }
-        if (last >= 0 && p.missing()[last]) return;  // its last rows are not these
+        if (missing == 1) {  // its last rows are not these
+            if (lane == 0) atomicOr(p.err, L2_PAGES_ERR_ARGS);
+            return;
+        }
+        if (here > missing) missing = 0;  // an upper layer is not what was left out first
     }
     const int pos = n < 0 ? -1 : READ ? r - start : n - (end - r);
     if (READ && (r < start || r >= end || pos >= n)) {  // no such row
@@ -239,6 +245,7 @@ __global__ void __launch_bounds__(256) pages_rows_kernel(const PagesView p, cons
         if (lane == 0) atomicOr(p.err, L2_PAGES_ERR_ARGS);
         return;
     }
+    if (!READ && missing && r == end - 1 && lane == 0) p.missing()[page] = 0;
     const long long at = page * p.page_stride + (pos % p.page_size) * p.row_stride;
     const int vh = p.row_bytes >> 4, nv = vh * p.n_kv_heads;  // 16-byte words a head, a row
     const int l0 = lg * layers_per, l1 = min(a.n_layers, l0 + layers_per);

@@ -39,8 +39,8 @@ constexpr int kMaxSlice = 8192;   // tokens of a block: two tables of 32 KB
 constexpr int kMinSlice = 1024;
 constexpr int kMostRows = 32;     // rows of a block, where they come in trees
 constexpr float kTableRows = 4.f; // what making the tables takes, in rows
-// Blocks of an SM: as many as registers allow (80 a thread where an access has 8 elements), and with biases no more than two tables of
-// the largest slice leave room for.
+// Blocks of an SM: as many as registers allow (80 a thread where an access has 8 elements, with 40 bytes of spills, 94 with biases), and with
+// biases no more than two tables of the largest slice leave room for.
 constexpr int reg_blocks(int width) { return width == 8 ? 3 : 4; }
 constexpr int blocks_of(int width, bool bias) { return bias ? 3 : reg_blocks(width); }
 constexpr unsigned kSeen = 1u << 31, kCount = (1u << 24) - 1;

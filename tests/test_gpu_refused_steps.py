@@ -186,6 +186,48 @@ def test_rows_that_a_refusal_left_out_are_not_accepted():
     assert torch.equal(held(pool, 1), torch.cat([old[:, :, :21], y], dim=2))
 
 
+@pytest.mark.parametrize("whole", [False, True])
+def test_rows_that_were_left_out_may_be_written_again(whole):
+    """Once there is room: from the lowest layer on that they were left out of, or all layers at once."""
+    pool = pkg.PagePool(4, 12, KV, 8, HS, 4, 16)
+    x = torch.randn((2, 4, 51, KV, HS), device="cuda")
+    pool.append(x[0], x[1], dev([0, 1]), dev([0, 30, 51]))    # 4 and 3 pages, five are free
+    old = held(pool, 1)
+    y, z = torch.randn((2, 4, 4, KV, HS), device="cuda"), torch.randn((2, 4, 40, KV, HS), device="cuda")
+    append(pool, y, [1], [0, 4], layers=[0, 1])
+    append(pool, z, [0], [0, 40], layers=[0])                 # five pages, four are free
+    append(pool, y, [1], [0, 4], layers=[2])                  # left out
+    append(pool, z[:, :, :9], [0], [0, 9], layers=[0, 1, 2, 3])
+    append(pool, y, [1], [0, 4], layers=[3])                  # written, but the one below is not there
+    cleared(pool, "free pages")
+    before = books(pool)
+    nothing(take(pool, "accept", [1], [0, 4]), 4, 1)
+    cleared(pool, "bookkeeping")
+    assert same(before, pool)
+    if whole:
+        pool.append(y[0], y[1], dev([1]), dev([0, 4]), extend=False)
+    else:
+        for layer in (2, 3):
+            pool.append(y[0, layer], y[1, layer], dev([1]), dev([0, 4]), layer=layer)
+    path, counts, following = take(pool, "accept", [1], [0, 4], fits=3)
+    pool.check()
+    assert counts.tolist() == [3] and torch.equal(held(pool, 1), torch.cat([old, y[:, :, :3]], dim=2))
+    path, counts, following = take(pool, "accept", [0], [0, 9], fits=5)
+    pool.check()
+    assert counts.tolist() == [5]
+
+
+def test_rows_of_a_refused_sequence_are_reported_once_others_succeed():
+    pool = pool_of((30, 21), 8, 8)
+    append(pool, rows(12, pool), [0], [0, 12], layers=[0])    # refused
+    append(pool, rows(5, pool), [1], [0, 5])
+    cleared(pool, "free pages")
+    before = books(pool)
+    append(pool, rows(12, pool), [0], [0, 12], layers=[1])
+    cleared(pool, "bookkeeping")
+    assert same(before, pool)
+
+
 def test_a_refusal_goes_with_its_pages():
     """Compaction moves them, a fork copies a partly filled one, and one that was given back and taken again is a new sequence's."""
     pool = pool_of((9, 30, 21), 10, 8)
